@@ -67,6 +67,9 @@ extern "C" {
 #define PA_DEV_BAD_SLOT       2   /* slot_mapping entry outside the pool        */
 #define PA_DEV_BAD_CONTEXT    4   /* context length above the stated maximum    */
 #define PA_DEV_WAIT_TIMEOUT   8   /* a bounded wait for a bulk copy gave up     */
+#define PA_DEV_NO_BLOCKS     16   /* a step's plan needs more blocks than are free */
+#define PA_DEV_BAD_ROW       32   /* a request's row out of range, or named twice */
+#define PA_DEV_BAD_POSITION  64   /* position past the end of the rotation table */
 
 /* ---- output element types ------------------------------------------------- */
 #define PA_DTYPE_BF16 0
@@ -394,6 +397,145 @@ size_t pa_prefill_fp8_workspace_size(int num_seqs, int max_blocks_per_seq,
                                      int d_head);
 
 /* ===========================================================================
+ * Decode attention of several new tokens per sequence
+ * ===========================================================================
+ * Operation ([P1] sections 7 and 13; [P2] sections 8, 10 and 11): sequence s
+ * has context length C = context_lens[s], of which the last n =
+ * query_start[s+1] - query_start[s] positions are new; their keys and values
+ * are already in the cache.  New token i (position C - n + i) is query row
+ * query_start[s] + i, and for each query head g (KV head g / G)
+ *
+ *   out[row][g][:] = sum_j a_j V_j,   a = softmax(scale * q[row][g] . K_j)
+ *
+ * over the positions j that it sees: every j < C - n, and of the new ones
+ * those up to its own (tree_mask NULL: causal) or position C - n + b for
+ * every bit b set in tree_mask[row] (bits from n on are ignored; a token that
+ * should see itself has its own bit set).  A row that sees nothing is zeros.
+ * It is the form of pa_prefill for few new tokens over long contexts (the
+ * drafts of speculative decoding to verify, short chunks): the cache is read
+ * once for up to 32 rows (new tokens times G) and its positions are split
+ * evenly over the device, whatever the lengths.  For long chunks of many
+ * rows pa_prefill is faster.
+ *
+ * Scores, softmax and sums are fp32.  The value products take the softmax
+ * weights as two bf16 terms (a relative 2^-16).  A non-finite value at a new
+ * position that a row does not see may reach that row's sum (0 * inf); at a
+ * position from C on it never does.
+ *
+ * Arguments
+ *   out           device [num_tokens][n_q_heads][d_head], bf16 or fp32 per
+ *                 out_dtype; rows of tokens of no sequence are not written.
+ *   q             device bf16 [num_tokens][n_q_heads][d_head].
+ *   k_cache, v_cache, block_tables, block_size, scale, max_context_len
+ *                 as pa_decode.
+ *   query_start   device int32 [num_seqs + 1], non-decreasing, within
+ *                 [0, num_tokens].
+ *   context_lens  device int32 [num_seqs], each >= its n.
+ *   tree_mask     optional device int64 [num_tokens], 8-byte aligned; then
+ *                 max_query_len is at most 64 (PA_ERR_UNSUPPORTED otherwise).
+ *   max_query_len host upper bound on every n, at least 1.
+ *   workspace     device, 256-byte aligned, at least
+ *                 pa_decode_multi_workspace_size(max_query_len, n_q_heads,
+ *                 n_kv_heads, d_head) bytes on the current device; needs no
+ *                 initialisation and keeps nothing between calls.  Calls that
+ *                 share one must be ordered (one stream).
+ * A sequence whose n is above max_query_len or its C, or whose query_start
+ * entries are out of order or range, is flagged PA_DEV_BAD_CONTEXT and not
+ * computed; a C above max_context_len or the table is flagged and clamped.
+ * Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_MISALIGNED,
+ * PA_ERR_WORKSPACE or PA_ERR_CUDA. */
+int pa_decode_multi(void* out, int out_dtype, const void* q,
+                    const void* k_cache, const void* v_cache,
+                    const int32_t* block_tables, const int32_t* query_start,
+                    const int32_t* context_lens, const int64_t* tree_mask,
+                    int block_size, float scale, int n_q_heads, int n_kv_heads,
+                    int d_head, int num_seqs, int num_tokens,
+                    int max_query_len, int max_blocks_per_seq, int num_blocks,
+                    int max_context_len, void* workspace,
+                    size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/* pa_decode_multi over FP8 caches (E4M3 codes times k_scale or v_scale, as
+ * pa_decode_fp8, and computed as it computes them); d_head 128.  Softmax
+ * weights enter the value products as f16 (a relative 2^-11). */
+int pa_decode_multi_fp8(void* out, int out_dtype, const void* q,
+                        const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables,
+                        const int32_t* query_start,
+                        const int32_t* context_lens, const int64_t* tree_mask,
+                        int block_size, float scale, float k_scale,
+                        float v_scale, int n_q_heads, int n_kv_heads,
+                        int d_head, int num_seqs, int num_tokens,
+                        int max_query_len, int max_blocks_per_seq,
+                        int num_blocks, int max_context_len, void* workspace,
+                        size_t workspace_bytes, int32_t* status_dev,
+                        void* stream);
+
+/* Bytes of workspace either call needs on the current device (0 for a
+ * non-positive argument). */
+size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads,
+                                      int n_kv_heads, int d_head);
+
+/* ===========================================================================
+ * Planning a step on the GPU
+ * ===========================================================================
+ * The metadata of a serving step from device-resident lengths ([P1] sections
+ * 7, 15 and 20): no host work between steps, and nothing that a captured
+ * graph could not replay.  Live requests own rows: row r holds the block
+ * table row_tables[r], of which the first row_blocks[r] entries are its
+ * blocks, and has row_lens[r] positions in the cache.  Batch entry i is the
+ * request in row seq_rows[i] and brings n = new_lens[i] new positions; a
+ * negative row is padding (n = 0, context 0).  With L = row_lens[r]:
+ *
+ *   blocks    ceil((L + n) / B) - row_blocks[r] more if that is positive,
+ *             taken from the end of free_blocks[0 .. *free_count - 1], entry
+ *             by entry in batch order: the order of the host manager's free
+ *             list.  row_tables, row_blocks and *free_count are brought up
+ *             to date.
+ *   context_lens[i] = L + n;   query_start: the running sum of n, [S + 1]
+ *   block_tables[i] = the row's first ceil((L + n) / B) entries, then -1
+ *   positions[t], slot_mapping[t] of new token t: its position p and
+ *             table[p / B] * B + p % B; -1 and -1 from the last token on.
+ *
+ * row_lens is only read: the caller advances it by what it keeps of the step
+ * (all n positions, or the accepted part of a draft).  Blocks stay with the
+ * row, so planning the same step again takes none.
+ * All or nothing: if the free blocks are too few (PA_DEV_NO_BLOCKS), a row is
+ * out of range or named twice (PA_DEV_BAD_ROW), or a length or count is
+ * negative, beyond the table, or the new positions are more than num_tokens
+ * (PA_DEV_BAD_CONTEXT), the step is planned with every n = 0 and no block is
+ * taken.  A table entry outside the pool gives slot -1 and PA_DEV_BAD_BLOCK_ID.
+ *   free_blocks   device int32 [free_capacity], and free_count, device int32
+ *                 [1]; both NULL: the tables hold every block already
+ *                 (reserved by the host manager) and needing one is
+ *                 PA_DEV_NO_BLOCKS.
+ *   row_tables    device int32 [num_rows][max_blocks_per_seq], 16-byte aligned
+ *   block_tables  device int32 [num_seqs][max_blocks_per_seq], 16-byte aligned
+ *   positions     device int32 [num_tokens]; slot_mapping int64 [num_tokens]
+ * At most 8192 sequences and 262144 rows (PA_ERR_UNSUPPORTED).  Outputs must
+ * not overlap the inputs.  Returns PA_OK, PA_ERR_INVALID_ARG,
+ * PA_ERR_UNSUPPORTED, PA_ERR_MISALIGNED or PA_ERR_CUDA. */
+int pa_plan_step(int32_t* block_tables, int32_t* context_lens,
+                 int32_t* query_start, int32_t* positions,
+                 int64_t* slot_mapping, const int32_t* seq_rows,
+                 const int32_t* new_lens, const int32_t* row_lens,
+                 int32_t* row_tables, int32_t* row_blocks,
+                 const int32_t* free_blocks, int32_t* free_count,
+                 int free_capacity, int num_seqs, int num_rows,
+                 int max_blocks_per_seq, int num_tokens, int block_size,
+                 int num_blocks, int32_t* status_dev, void* stream);
+
+/* Give back every block of the named rows: they go onto free_blocks in table
+ * order, row after row ([P1] section 17), row_blocks of the rows become 0 and
+ * *free_count grows.  Negative entries are skipped.  A row out of range or
+ * named twice (PA_DEV_BAD_ROW), or counts that do not fit the table or
+ * free_capacity (PA_DEV_BAD_CONTEXT), leave everything as it was. */
+int pa_release_rows(const int32_t* rows, int num_released,
+                    const int32_t* row_tables, int32_t* row_blocks,
+                    int num_rows, int max_blocks_per_seq, int32_t* free_blocks,
+                    int32_t* free_count, int free_capacity,
+                    int32_t* status_dev, void* stream);
+
+/* ===========================================================================
  * Cache writes
  * ===========================================================================
  * reshape_and_cache ([P1] section 16 item 3 and section 20: each newly
@@ -427,6 +569,63 @@ int pa_reshape_and_cache_fp8(void* k_cache, void* v_cache, const void* k,
                              int num_tokens, int n_kv_heads, int d_head,
                              int block_size, int num_blocks, float k_scale,
                              float v_scale, int32_t* status_dev, void* stream);
+
+/* The projections of a step made ready for attention in one pass: per-head
+ * RMS norm of q and k, rotation by position, q to q_out, and k and v to their
+ * slots ([P1] sections 7 and 16), for every token t with position >= 0:
+ *
+ *   y = x * rsqrt(mean(x^2) + eps) * gain        (q and k; gains NULL: y = x)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)     for the pairs (c, c + R / 2)
+ *            of a head's first R = rot_dim elements, or (2c, 2c + 1) if
+ *            interleaved != 0, by cos_sin[position][c] and [R / 2 + c]
+ *
+ * in fp32 from the bf16 inputs, rounded once (to nearest even) to bf16.  v
+ * goes to the cache as it is.  A negative position is padding: nothing of the
+ * token is touched.  A negative slot keeps the token's k and v out of the
+ * cache.  A position from max_positions on is skipped and flagged
+ * PA_DEV_BAD_POSITION; a slot outside the pool skips the write and is flagged
+ * PA_DEV_BAD_SLOT.
+ *   q_out         device bf16 [num_tokens][n_q_heads][d_head]; it may be q
+ *                 itself if q is contiguous (q_stride n_q_heads * d_head).
+ *   q, k, v       device bf16, heads of a token contiguous, q_stride /
+ *                 k_stride / v_stride elements between tokens (multiples of
+ *                 8, at least a token's heads): views of one projection's
+ *                 rows serve.
+ *   q_weight, k_weight  device f32 [d_head] gains, both or neither; eps >= 0.
+ *   cos_sin       device f32 [max_positions][rot_dim].
+ *   rot_dim       a multiple of 16 in [16, d_head].
+ *   positions     device int32 [num_tokens]; slot_mapping int64 [num_tokens].
+ * Pointers 16-byte aligned (positions 4, slot_mapping 8).  Returns PA_OK,
+ * PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_MISALIGNED or PA_ERR_CUDA. */
+int pa_qk_norm_rope_cache(void* q_out, void* k_cache, void* v_cache,
+                          const void* q, const void* k, const void* v,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          const float* q_weight, const float* k_weight,
+                          float eps, const float* cos_sin, int max_positions,
+                          int rot_dim, int interleaved,
+                          const int32_t* positions,
+                          const int64_t* slot_mapping, int num_tokens,
+                          int n_q_heads, int n_kv_heads, int d_head,
+                          int block_size, int num_blocks, int32_t* status_dev,
+                          void* stream);
+
+/* pa_qk_norm_rope_cache for FP8 caches: k and v are stored as the E4M3 codes
+ * of their fp32 values over k_scale and v_scale (IEEE division, round to
+ * nearest even, saturating, NaN kept; finite scales > 0): k is rounded once,
+ * from fp32 to its code. */
+int pa_qk_norm_rope_cache_fp8(void* q_out, void* k_cache, void* v_cache,
+                              const void* q, const void* k, const void* v,
+                              int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, const float* q_weight,
+                              const float* k_weight, float eps,
+                              const float* cos_sin, int max_positions,
+                              int rot_dim, int interleaved,
+                              const int32_t* positions,
+                              const int64_t* slot_mapping, int num_tokens,
+                              int n_q_heads, int n_kv_heads, int d_head,
+                              int block_size, int num_blocks, float k_scale,
+                              float v_scale, int32_t* status_dev,
+                              void* stream);
 
 /* copy_blocks: the copy-on-write clone of a shared tail block ([P1]
  * sections 15 and 16): for every pair (src, dst) = (block_pairs[2i],

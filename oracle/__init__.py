@@ -15,6 +15,8 @@ cache_ops   slot-mapping scatter (reshape_and_cache) and copy-on-write block
             copy (copy_blocks) on a host copy of the pool.
 allocator   reference block manager: LIFO free list, reference counts, fork,
             append with copy-on-write, release.
+step        a step's plan (tables, slots, positions) and the norm and rotation
+            of its queries and keys.
 sizing      KV-cache sizing arithmetic (bytes per token, blocks, tail waste).
 
 Sources (the three web pages this method is described on):
@@ -27,4 +29,4 @@ Every function is pinned by tests under tests/ to values the pages print,
 closed forms, invariants or brute force; none is marked "parity unpinned".
 """
 
-from . import allocator, attention, cache_ops, sizing  # noqa: F401
+from . import allocator, attention, cache_ops, sizing, step  # noqa: F401

@@ -170,6 +170,35 @@ def paged_prefill(q, k_cache, v_cache, block_tables, query_start, context_lens, 
     return out
 
 
+def paged_multi(q, k_cache, v_cache, block_tables, query_start, context_lens, scale, block_size, tree_mask=None):
+    """Attention of each sequence's few new tokens: as paged_prefill without
+    tree_mask; with it (one integer per row), new token i of sequence s sees
+    every position before the new ones, and new token b for every bit b < n
+    of its row's word.  A row that sees nothing is zeros."""
+    if tree_mask is None:
+        return paged_prefill(q, k_cache, v_cache, block_tables, query_start, context_lens, scale, block_size)
+    if q.dtype == np.uint16:
+        q = bf16_to_f64(q)
+    T, n_q_heads, d_head = q.shape
+    n_kv_heads = k_cache.shape[1]
+    out = np.zeros((T, n_q_heads, d_head), dtype=np.float64)
+    for s in range(len(context_lens)):
+        C = int(context_lens[s])
+        row0, n = int(query_start[s]), int(query_start[s + 1]) - int(query_start[s])
+        if n <= 0:
+            continue
+        K, V = gather_kv(k_cache, v_cache, block_tables[s], C, block_size)
+        for i in range(n):
+            word = int(tree_mask[row0 + i])
+            sees = list(range(C - n)) + [C - n + b for b in range(n) if word >> b & 1]
+            if not sees:
+                continue
+            for g in range(n_q_heads):
+                h = kv_head_of(g, n_q_heads, n_kv_heads)
+                out[row0 + i, g] = softmax_attention(q[row0 + i, g], K[h][sees], V[h][sees], scale)
+    return out
+
+
 # ----------------------------------------------------------------------------
 # Split computation and exact merge ([P2] sections 10 and 11)
 # ----------------------------------------------------------------------------

@@ -31,6 +31,9 @@ PA_DEV_BAD_BLOCK_ID = 1
 PA_DEV_BAD_SLOT = 2
 PA_DEV_BAD_CONTEXT = 4
 PA_DEV_WAIT_TIMEOUT = 8
+PA_DEV_NO_BLOCKS = 16
+PA_DEV_BAD_ROW = 32
+PA_DEV_BAD_POSITION = 64
 
 PA_DTYPE_BF16 = 0
 PA_DTYPE_F32 = 1
@@ -85,6 +88,22 @@ _SIGS = {
                                 _c_int, _c_float, _c_float, _c_float, _c_int, _c_int, _c_int, _vp, _c_size, _vp, _vp,
                                 _vp]),
     "pa_prefill_fp8_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "pa_decode_multi": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_float, _c_int, _c_int,
+                                 _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp, _vp]),
+    "pa_decode_multi_fp8": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_float, _c_float,
+                                     _c_float, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                     _vp, _c_size, _vp, _vp]),
+    "pa_decode_multi_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "pa_plan_step": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                              _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pa_release_rows": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp]),
+    "pa_qk_norm_rope_cache": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                       _vp, _vp, _c_float, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int,
+                                       _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pa_qk_norm_rope_cache_fp8": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64,
+                                           ctypes.c_int64, _vp, _vp, _c_float, _vp, _c_int, _c_int, _c_int, _vp, _vp,
+                                           _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_float, _vp,
+                                           _vp]),
     "pa_check_bounded_wait": (_c_int, [_c_int, _vp, _vp]),
     "pa_lse_merge": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
     "pa_reshape_and_cache": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
@@ -572,6 +591,167 @@ def pa_swap_blocks(dst_k, dst_v, src_k, src_v, block_pairs, status=None, stream=
             _dev_or_pinned(block_pairs, torch.int32, "block_pairs"), int(P), int(Hkv), int(D), int(B),
             int(SNB), int(DNB), _opt_dev(status, torch.int32, "status"), _stream(stream))
     return _check(st, "pa_swap_blocks_fp8" if fp8 else "pa_swap_blocks")
+
+
+# ----------------------------------------------------------------------------
+# a step of new tokens: planning, norm + rotation + cache write, attention
+# ----------------------------------------------------------------------------
+
+def _ptrs(where, **tensors):
+    """Raw pointers of contiguous CUDA tensors, all on the current device;
+    each argument is (tensor or None, dtype, shape or None)."""
+    dev = torch.cuda.current_device()
+    out = []
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s: %s must be a torch.Tensor" % (where, name))
+        if t.dtype is not dtype:
+            raise TypeError("%s: %s must be %s, got %s" % (where, name, dtype, t.dtype))
+        if t.get_device() != dev:
+            raise ValueError("%s: %s must be a CUDA tensor of the current device (%d), got %s" %
+                             (where, name, dev, t.device))
+        if shape is not None and t.shape != shape:
+            raise ValueError("%s: %s must be %s, got %s" % (where, name, list(shape), list(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s: %s must be contiguous" % (where, name))
+        out.append(t.data_ptr())
+    return out
+
+
+def pa_plan_step(block_tables, context_lens, query_start, positions, slot_mapping, seq_rows, new_lens, row_lens,
+                 row_tables, row_blocks, free_blocks, free_count, block_size, num_blocks, status=None, stream=None):
+    """Plan a step on the GPU: batch entry i (the request in row seq_rows[i])
+    brings new_lens[i] positions.  Takes the blocks it needs from the end of
+    free_blocks[:free_count] (both None: the tables hold them already), brings
+    row_tables / row_blocks / free_count up to date, and writes block_tables
+    [S, max_blocks], context_lens [S], query_start [S + 1], positions [T] and
+    slot_mapping [T]; row_lens is only read.  See pa.h."""
+    S, (R, MB), T = seq_rows.shape[0], row_tables.shape, positions.shape[0]
+    i32 = torch.int32
+    p = _ptrs("pa_plan_step", block_tables=(block_tables, i32, (S, MB)), context_lens=(context_lens, i32, (S,)),
+              query_start=(query_start, i32, (S + 1,)), positions=(positions, i32, (T,)),
+              slot_mapping=(slot_mapping, torch.int64, (T,)), seq_rows=(seq_rows, i32, (S,)),
+              new_lens=(new_lens, i32, (S,)), row_lens=(row_lens, i32, (R,)), row_tables=(row_tables, i32, (R, MB)),
+              row_blocks=(row_blocks, i32, (R,)), free_blocks=(free_blocks, i32, None),
+              free_count=(free_count, i32, (1,)), status=(status, i32, None))
+    return _check(_lib.pa_plan_step(*p[:12], 0 if free_blocks is None else free_blocks.numel(), S, R, MB, T,
+                                    int(block_size), int(num_blocks), p[12], _stream(stream)), "pa_plan_step")
+
+
+def pa_release_rows(rows, row_tables, row_blocks, free_blocks, free_count, status=None, stream=None):
+    """Push every block of the named rows (int32; negative: skipped) onto
+    free_blocks and set their row_blocks to 0; see pa.h."""
+    R, MB = row_tables.shape
+    i32 = torch.int32
+    p = _ptrs("pa_release_rows", rows=(rows, i32, (rows.shape[0],)), row_tables=(row_tables, i32, (R, MB)),
+              row_blocks=(row_blocks, i32, (R,)), free_blocks=(free_blocks, i32, None),
+              free_count=(free_count, i32, (1,)), status=(status, i32, None))
+    return _check(_lib.pa_release_rows(p[0], rows.shape[0], p[1], p[2], R, MB, p[3], p[4], free_blocks.numel(), p[5],
+                                       _stream(stream)), "pa_release_rows")
+
+
+def rope_table(max_positions, rot_dim, base=10000.0, device=None):
+    """Cosines and sines of position * base^(-2c / rot_dim), c < rot_dim / 2,
+    for pa_qk_norm_rope_cache: float32 [max_positions, rot_dim], from angles
+    in float64."""
+    c = torch.arange(rot_dim // 2, dtype=torch.float64)
+    angle = torch.arange(max_positions, dtype=torch.float64)[:, None] * float(base) ** (-2.0 * c / rot_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float().to(device or "cuda")
+
+
+def _token_rows(t, heads, d, dev, name):
+    """Pointer and token stride of bf16 [T, heads, d] whose heads are contiguous within a token."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        raise TypeError("pa_qk_norm_rope_cache: %s must be a bfloat16 tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("pa_qk_norm_rope_cache: %s must be a CUDA tensor of the current device" % name)
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
+        raise ValueError("pa_qk_norm_rope_cache: the heads of a token of %s must be contiguous" % name)
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * d)
+
+
+def pa_qk_norm_rope_cache(q_out, k_cache, v_cache, q, k, v, positions, slot_mapping, cos_sin, q_weight=None,
+                          k_weight=None, eps=1e-6, interleaved=False, status=None, stream=None, k_scale=None,
+                          v_scale=None):
+    """One pass over a step's projections q [T, Hq, D], k and v [T, Hkv, D]
+    (bf16; views of one projection's rows serve): RMS norm of each head of q
+    and k (with gains, float32 [D]), rotation by positions [T] (int32) with
+    cos_sin [max_positions, rot_dim] (see rope_table), q to q_out, k and v to
+    the slots slot_mapping [T] (int64) of the caches.  With k_scale / v_scale,
+    the E4M3 form (uint8 caches); see pa.h."""
+    T, Hq, D = q.shape
+    NB, Hkv, B, _ = k_cache.shape
+    f8 = k_scale is not None
+    if f8 != (v_scale is not None):
+        raise ValueError("pa_qk_norm_rope_cache: k_scale and v_scale go together")
+    cache, f32 = torch.uint8 if f8 else torch.bfloat16, torch.float32
+    p = _ptrs("pa_qk_norm_rope_cache", q_out=(q_out, torch.bfloat16, (T, Hq, D)), k_cache=(k_cache, cache, (NB, Hkv, B, D)),
+              v_cache=(v_cache, cache, (NB, Hkv, B, D)), q_weight=(q_weight, f32, (D,)), k_weight=(k_weight, f32, (D,)),
+              cos_sin=(cos_sin, f32, None), positions=(positions, torch.int32, (T,)),
+              slot_mapping=(slot_mapping, torch.int64, (T,)), status=(status, torch.int32, None))
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or cos_sin.dim() != 2:
+        raise ValueError("pa_qk_norm_rope_cache: k/v must be [T, n_kv_heads, d_head], cos_sin [max_positions, rot_dim]")
+    dev = q_out.get_device()
+    qp, qs = _token_rows(q, Hq, D, dev, "q")
+    kp, ks = _token_rows(k, Hkv, D, dev, "k")
+    vp, vs = _token_rows(v, Hkv, D, dev, "v")
+    if T == 0:
+        return PA_OK
+    args = [p[0], p[1], p[2], qp, kp, vp, qs, ks, vs, p[3], p[4], float(eps), p[5], cos_sin.shape[0], cos_sin.shape[1],
+            1 if interleaved else 0, p[6], p[7], T, Hq, Hkv, D, B, NB]
+    if f8:
+        return _check(_lib.pa_qk_norm_rope_cache_fp8(*args, float(k_scale), float(v_scale), p[8], _stream(stream)),
+                      "pa_qk_norm_rope_cache_fp8")
+    return _check(_lib.pa_qk_norm_rope_cache(*args, p[8], _stream(stream)), "pa_qk_norm_rope_cache")
+
+
+def pa_decode_multi_workspace_size(max_query_len, n_q_heads, n_kv_heads, d_head):
+    return int(_lib.pa_decode_multi_workspace_size(int(max_query_len), int(n_q_heads), int(n_kv_heads), int(d_head)))
+
+
+def decode_multi_workspace(max_query_len, n_q_heads, n_kv_heads, d_head, device=None):
+    """A caller-owned workspace tensor (uint8) of the size pa_decode_multi needs."""
+    n = pa_decode_multi_workspace_size(max_query_len, n_q_heads, n_kv_heads, d_head)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len, block_size, scale,
+                    n_q_heads, n_kv_heads, d_head, max_context_len, tree_mask=None, workspace=None, status=None,
+                    stream=None, k_scale=None, v_scale=None):
+    """out [T, Hq, D] (bf16 or f32) <- attention of each sequence's few new
+    tokens (rows query_start[s] .. query_start[s + 1]) over its paged cache:
+    causal, or by tree_mask [T] (int64: bit b, the token sees new token b of
+    its sequence).  workspace: a uint8 tensor from decode_multi_workspace.
+    With k_scale / v_scale, the E4M3 form (uint8 caches); see pa.h."""
+    f8 = k_scale is not None
+    if f8 != (v_scale is not None):
+        raise ValueError("pa_decode_multi: k_scale and v_scale go together")
+    if out.dtype is torch.bfloat16:
+        out_dtype = PA_DTYPE_BF16
+    elif out.dtype is torch.float32:
+        out_dtype = PA_DTYPE_F32
+    else:
+        raise TypeError("out must be bfloat16 or float32")
+    T, (S, MB), NB, i32 = q.shape[0], block_tables.shape, k_cache.shape[0], torch.int32
+    cache, shape = torch.uint8 if f8 else torch.bfloat16, (NB, n_kv_heads, block_size, d_head)
+    p = _ptrs("pa_decode_multi", out=(out, out.dtype, (T, n_q_heads, d_head)),
+              q=(q, torch.bfloat16, (T, n_q_heads, d_head)), k_cache=(k_cache, cache, shape),
+              v_cache=(v_cache, cache, shape), block_tables=(block_tables, i32, (S, MB)),
+              query_start=(query_start, i32, (S + 1,)), context_lens=(context_lens, i32, (S,)),
+              tree_mask=(tree_mask, torch.int64, (T,)), workspace=(workspace, torch.uint8, None),
+              status=(status, i32, None))
+    args = [p[0], out_dtype, *p[1:8], int(block_size), float(scale)]
+    if f8:
+        args += [float(k_scale), float(v_scale)]
+    args += [int(n_q_heads), int(n_kv_heads), int(d_head), S, T, int(max_query_len), MB, NB, int(max_context_len), p[8],
+             0 if workspace is None else workspace.numel(), p[9], _stream(stream)]
+    if f8:
+        return _check(_lib.pa_decode_multi_fp8(*args), "pa_decode_multi_fp8")
+    return _check(_lib.pa_decode_multi(*args), "pa_decode_multi")
 
 
 # ----------------------------------------------------------------------------

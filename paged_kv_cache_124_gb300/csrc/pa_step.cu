@@ -1,0 +1,384 @@
+// A serving step's metadata on the GPU: block tables, slots and positions of
+// the step's new tokens, from the requests' lengths and the pool's free
+// blocks ("PagedAttention: Virtual Memory for the KV Cache", sections 7, 15
+// and 20: translation, append, the free list as a stack).
+//
+// Request i of the batch holds L cached positions in h blocks and brings n
+// new ones:
+//   need_i = max(0, ceil((L + n) / B) - h)          blocks it takes
+//   first_i = need_0 + ... + need_{i-1}             where its blocks start
+//   entry h + k = free[count - 1 - (first_i + k)]   the stack's order
+//   slot(p) = entry[p / B] * B + p % B              of each new position p
+//
+// Two launches: one block scans the batch (the totals decide whether the step
+// fits at all, so nothing may be written before they are known) and takes the
+// blocks; a grid then expands tables, positions and slots, each of them from
+// the first launch's outputs alone.  There is no scratch memory to share or
+// to reset, so two captured graphs never meet in one.
+
+#include "pa_common.cuh"
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanPer = 8;                            // requests per thread, at most
+constexpr int kPlanMaxSeqs = kPlanThreads * kPlanPer;
+constexpr int kPlanMaxRows = 1 << 18;                  // one bit each in shared memory
+constexpr int kExpandThreads = 256;
+
+struct PlanArgs {
+    const int32_t* seq_rows;
+    const int32_t* new_lens;
+    const int32_t* row_lens;
+    int32_t* row_tables;
+    int32_t* row_blocks;
+    const int32_t* free_blocks;
+    int32_t* free_count;
+    int32_t* block_tables;
+    int32_t* context_lens;
+    int32_t* query_start;
+    int32_t* positions;
+    int64_t* slot_mapping;
+    int32_t* status;
+    int num_seqs, num_rows, max_blocks, free_capacity, num_blocks, log2_block, num_tokens;
+};
+
+// Exclusive scan of one pair per thread over the block; the totals go to
+// every thread.
+__device__ __forceinline__ void scan_pair(long long& a, long long& b, long long& total_a, long long& total_b,
+                                          long long (*sh)[2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long a0 = a, b0 = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+            a += x;
+            b += y;
+        }
+    }
+    if (lane == 31) {
+        sh[warp][0] = a;
+        sh[warp][1] = b;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long x = sh[lane][0], y = sh[lane][1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) {
+                x += u;
+                y += v;
+            }
+        }
+        sh[lane][0] = x;
+        sh[lane][1] = y;
+    }
+    __syncthreads();
+    total_a = sh[kPlanThreads / 32 - 1][0];
+    total_b = sh[kPlanThreads / 32 - 1][1];
+    a = a - a0 + (warp ? sh[warp - 1][0] : 0);
+    b = b - b0 + (warp ? sh[warp - 1][1] : 0);
+}
+
+// Largest i with starts[i] <= x, for starts[0] <= x (entries non-decreasing).
+__device__ __forceinline__ int last_start(const int32_t* starts, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (starts[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+    extern __shared__ uint32_t dyn[];                  // first_[num_seqs], then a bit per row
+    __shared__ long long sh[32][2];
+    int32_t* first_ = reinterpret_cast<int32_t*>(dyn);
+    uint32_t* seen = dyn + a.num_seqs;
+    const int S = a.num_seqs, t = threadIdx.x;
+    for (int i = t; i < (a.num_rows + 31) / 32; i += kPlanThreads) seen[i] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncthreads();
+    const int per = (S + kPlanThreads - 1) / kPlanThreads;
+    const long long cap = (long long)a.max_blocks << a.log2_block;
+    int row[kPlanPer], len[kPlanPer], n[kPlanPer], need[kPlanPer];
+    int bad = 0;
+    long long my_n = 0, my_need = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+        const int i = t * per + k;
+        row[k] = -1;
+        len[k] = n[k] = need[k] = 0;
+        if (k >= per || i >= S) continue;
+        const int r = a.seq_rows[i];
+        if (r < 0) continue;                           // padding of the batch
+        if (r >= a.num_rows || (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u)) {
+            bad |= PA_DEV_BAD_ROW;
+            continue;
+        }
+        const int L = a.row_lens[r], h = a.row_blocks[r], m = a.new_lens[i];
+        if (L < 0 || L > cap || h < 0 || h > a.max_blocks || m < 0 || (long long)L + m > cap) {
+            bad |= PA_DEV_BAD_CONTEXT;
+            continue;
+        }
+        row[k] = r;
+        len[k] = L;
+        n[k] = m;
+        const int nb = (int)(((long long)L + m + (1 << a.log2_block) - 1) >> a.log2_block);
+        need[k] = nb > h ? nb - h : 0;
+        my_n += m;
+        my_need += need[k];
+    }
+    long long base_n = my_n, base_need = my_need, total_n, total_need;
+    scan_pair(base_n, base_need, total_n, total_need, sh);
+    const int count = a.free_count ? *a.free_count : 0;
+    if (total_n > a.num_tokens) bad |= PA_DEV_BAD_CONTEXT;
+    if (total_need > 0 && (count > a.free_capacity || total_need > count)) bad |= PA_DEV_NO_BLOCKS;
+    if (__syncthreads_or(bad)) {
+        // all or nothing: every request keeps what it has and brings nothing
+        if (bad) pa::set_status(a.status, bad);
+#pragma unroll
+        for (int k = 0; k < kPlanPer; ++k) {
+            const int i = t * per + k;
+            if (k < per && i < S) {
+                a.context_lens[i] = len[k];
+                a.query_start[i] = 0;
+            }
+        }
+        if (t == 0) a.query_start[S] = 0;
+        return;
+    }
+    long long at_n = base_n, at_need = base_need;
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+        const int i = t * per + k;
+        if (k >= per || i >= S) continue;
+        a.context_lens[i] = len[k] + n[k];
+        a.query_start[i] = (int)at_n;
+        first_[i] = (int)at_need;
+        at_n += n[k];
+        at_need += need[k];
+    }
+    if (t == 0) a.query_start[S] = (int)total_n;
+    if (total_need == 0) return;
+    __syncthreads();
+    // the step's blocks, in the order they are taken, over all threads
+    for (int k = t; k < total_need; k += kPlanThreads) {
+        const int i = last_start(first_, S, k);
+        const int r = a.seq_rows[i];
+        a.row_tables[(size_t)r * a.max_blocks + a.row_blocks[r] + (k - first_[i])] = a.free_blocks[count - 1 - k];
+    }
+    __syncthreads();                                   // every thread has read the counts it needs
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k)
+        if (need[k]) a.row_blocks[row[k]] += need[k];
+    if (t == 0) *a.free_count = count - (int)total_need;
+}
+
+// Blocks [0, table_blocks): one warp per 1024 entries of a batch row's table;
+// the rest: one thread per token.
+constexpr int kSegment = 1024;
+
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const PlanArgs a, int table_blocks, int segments) {
+    extern __shared__ int32_t starts[];                // [num_seqs] (token blocks)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int S = a.num_seqs, B = 1 << a.log2_block;
+    if ((int)blockIdx.x < table_blocks) {
+        const int w = blockIdx.x * (kExpandThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+        const int i = w / segments, j0 = (w - i * segments) * kSegment;
+        if (i >= S) return;
+        const int r = a.seq_rows[i];
+        const int nb = (r < 0 || r >= a.num_rows) ? 0 : (int)(((long long)a.context_lens[i] + B - 1) >> a.log2_block);
+        const int32_t* src = a.row_tables + (size_t)(nb ? r : 0) * a.max_blocks;
+        int32_t* dst = a.block_tables + (size_t)i * a.max_blocks;
+        const int end = min(j0 + kSegment, a.max_blocks);
+        if ((a.max_blocks & 3) == 0) {
+            for (int j = j0 + 4 * lane; j < end; j += 128) {
+                int4 x = make_int4(-1, -1, -1, -1);
+                if (j < nb) {
+                    x = *reinterpret_cast<const int4*>(src + j);
+                    if (j + 1 >= nb) x.y = -1;
+                    if (j + 2 >= nb) x.z = -1;
+                    if (j + 3 >= nb) x.w = -1;
+                }
+                *reinterpret_cast<int4*>(dst + j) = x;
+            }
+        } else {
+            for (int j = j0 + lane; j < end; j += 32) dst[j] = j < nb ? src[j] : -1;
+        }
+        return;
+    }
+    for (int i = threadIdx.x; i < S; i += kExpandThreads) starts[i] = a.query_start[i];
+    const int total = a.query_start[S];
+    __syncthreads();
+    const int t = (blockIdx.x - table_blocks) * kExpandThreads + threadIdx.x;
+    if (t >= a.num_tokens) return;
+    int pos = -1;
+    long long slot = -1;
+    if (t < total) {
+        const int i = last_start(starts, S, t);        // the last request that starts at or before t: it has t
+        const int n = (i + 1 < S ? starts[i + 1] : total) - starts[i];
+        pos = a.context_lens[i] - n + (t - starts[i]);
+        const int blk = a.row_tables[(size_t)a.seq_rows[i] * a.max_blocks + (pos >> a.log2_block)];
+        if (blk < 0 || blk >= a.num_blocks)
+            pa::set_status(a.status, PA_DEV_BAD_BLOCK_ID);
+        else
+            slot = ((long long)blk << a.log2_block) + (pos & (B - 1));
+    }
+    a.positions[t] = pos;
+    a.slot_mapping[t] = slot;
+}
+
+// Rows given back: their blocks go onto the stack in table order, row after
+// row, as the host manager's release does.
+__global__ void __launch_bounds__(kPlanThreads) release_kernel(const int32_t* rows, int num, const int32_t* row_tables,
+                                                               int32_t* row_blocks, int num_rows, int max_blocks,
+                                                               int32_t* free_blocks, int32_t* free_count,
+                                                               int free_capacity, int32_t* status) {
+    extern __shared__ uint32_t dyn[];                  // first_[num], then a bit per row
+    __shared__ long long sh[32][2];
+    int32_t* first_ = reinterpret_cast<int32_t*>(dyn);
+    uint32_t* seen = dyn + num;
+    const int t = threadIdx.x;
+    for (int i = t; i < (num_rows + 31) / 32; i += kPlanThreads) seen[i] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncthreads();
+    const int per = (num + kPlanThreads - 1) / kPlanThreads;
+    int held[kPlanPer];
+    int bad = 0;
+    long long mine = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+        const int i = t * per + k;
+        held[k] = 0;
+        if (k >= per || i >= num) continue;
+        const int r = rows[i];
+        if (r < 0) continue;
+        if (r >= num_rows || (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u)) {
+            bad |= PA_DEV_BAD_ROW;
+            continue;
+        }
+        held[k] = row_blocks[r];
+        if (held[k] < 0 || held[k] > max_blocks) bad |= PA_DEV_BAD_CONTEXT;
+        mine += held[k];
+    }
+    long long base = mine, other = 0, total, unused;
+    scan_pair(base, other, total, unused, sh);
+    const int count = *free_count;
+    if (count < 0 || count + total > free_capacity) bad |= PA_DEV_BAD_CONTEXT;
+    if (__syncthreads_or(bad)) {
+        if (bad) pa::set_status(status, bad);
+        return;
+    }
+    long long at = base;
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k) {
+        const int i = t * per + k;
+        if (k >= per || i >= num) continue;
+        first_[i] = (int)at;
+        at += held[k];
+    }
+    __syncthreads();
+    for (int k = t; k < total; k += kPlanThreads) {
+        const int i = last_start(first_, num, k);
+        free_blocks[count + k] = row_tables[(size_t)rows[i] * max_blocks + (k - first_[i])];
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanPer; ++k)
+        if (held[k]) row_blocks[rows[t * per + k]] = 0;
+    if (t == 0) *free_count = count + (int)total;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int pa_plan_step(int32_t* block_tables, int32_t* context_lens, int32_t* query_start, int32_t* positions,
+                 int64_t* slot_mapping, const int32_t* seq_rows, const int32_t* new_lens, const int32_t* row_lens,
+                 int32_t* row_tables, int32_t* row_blocks, const int32_t* free_blocks, int32_t* free_count,
+                 int free_capacity, int num_seqs, int num_rows, int max_blocks_per_seq, int num_tokens,
+                 int block_size, int num_blocks, int32_t* status_dev, void* stream) {
+    if (num_seqs < 0 || num_rows <= 0 || max_blocks_per_seq <= 0 || num_tokens < 0 || num_blocks <= 0 ||
+        free_capacity < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!pa_host::supported_block_size(block_size)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > kPlanMaxSeqs || num_rows > kPlanMaxRows ||
+        (long long)max_blocks_per_seq * block_size > 0x7fffffffLL)
+        return PA_ERR_UNSUPPORTED;
+    if (!query_start || (num_seqs > 0 && (!block_tables || !context_lens || !seq_rows || !new_lens || !row_lens ||
+                                          !row_tables || !row_blocks)) ||
+        (num_tokens > 0 && (!positions || !slot_mapping)) || ((free_blocks == nullptr) != (free_count == nullptr)))
+        return PA_ERR_INVALID_ARG;
+    if (!pa_host::aligned16(block_tables) || !pa_host::aligned16(row_tables) || !aligned4(context_lens) ||
+        !aligned4(query_start) || !aligned4(positions) || !aligned4(seq_rows) || !aligned4(new_lens) ||
+        !aligned4(row_lens) || !aligned4(row_blocks) || !aligned4(free_blocks) || !aligned4(free_count) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PA_ERR_MISALIGNED;
+    PlanArgs a{};
+    a.seq_rows = seq_rows;
+    a.new_lens = new_lens;
+    a.row_lens = row_lens;
+    a.row_tables = row_tables;
+    a.row_blocks = row_blocks;
+    a.free_blocks = free_blocks;
+    a.free_count = free_count;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.positions = positions;
+    a.slot_mapping = slot_mapping;
+    a.status = status_dev;
+    a.num_seqs = num_seqs;
+    a.num_rows = num_rows;
+    a.max_blocks = max_blocks_per_seq;
+    a.free_capacity = free_capacity;
+    a.num_blocks = num_blocks;
+    a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
+    a.num_tokens = num_tokens;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    static int attr_plan[64] = {0};
+    const int smem = 4 * num_seqs + 4 * ((num_rows + 31) / 32);
+    if (smem > 40 * 1024 && pa_host::ensure_smem_attr(plan_kernel, smem, attr_plan) != cudaSuccess) return PA_ERR_CUDA;
+    if (pa_host::launch_dependent(plan_kernel, dim3(1), dim3(kPlanThreads), smem, st, a) != cudaSuccess)
+        return PA_ERR_CUDA;
+    const int segments = (max_blocks_per_seq + kSegment - 1) / kSegment;
+    const long long warps = (long long)num_seqs * segments;
+    const int table_blocks = (int)((warps + kExpandThreads / 32 - 1) / (kExpandThreads / 32));
+    const int token_blocks = (int)(((long long)num_tokens + kExpandThreads - 1) / kExpandThreads);
+    if (table_blocks + token_blocks == 0) return PA_OK;
+    return pa_host::launch_dependent(expand_kernel, dim3(table_blocks + token_blocks), dim3(kExpandThreads),
+                                     4 * num_seqs, st, a, table_blocks, segments) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+int pa_release_rows(const int32_t* rows, int num_released, const int32_t* row_tables, int32_t* row_blocks,
+                    int num_rows, int max_blocks_per_seq, int32_t* free_blocks, int32_t* free_count,
+                    int free_capacity, int32_t* status_dev, void* stream) {
+    if (num_released < 0 || num_rows <= 0 || max_blocks_per_seq <= 0 || free_capacity < 0) return PA_ERR_INVALID_ARG;
+    if (num_released > kPlanMaxSeqs || num_rows > kPlanMaxRows) return PA_ERR_UNSUPPORTED;
+    if (num_released == 0) return PA_OK;
+    if (!rows || !row_tables || !row_blocks || !free_blocks || !free_count) return PA_ERR_INVALID_ARG;
+    if (!aligned4(rows) || !aligned4(row_tables) || !aligned4(row_blocks) || !aligned4(free_blocks) ||
+        !aligned4(free_count))
+        return PA_ERR_MISALIGNED;
+    static int attr_release[64] = {0};
+    const int smem = 4 * num_released + 4 * ((num_rows + 31) / 32);
+    if (smem > 40 * 1024 && pa_host::ensure_smem_attr(release_kernel, smem, attr_release) != cudaSuccess)
+        return PA_ERR_CUDA;
+    return pa_host::launch_dependent(release_kernel, dim3(1), dim3(kPlanThreads), smem,
+                                     static_cast<cudaStream_t>(stream), rows, num_released, row_tables, row_blocks,
+                                     num_rows, max_blocks_per_seq, free_blocks, free_count, free_capacity,
+                                     status_dev) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,286 @@
+"""pa_decode_multi and pa_decode_multi_fp8 against the float64 oracle, at the
+sizes, masks and lengths where they can go wrong."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as A
+from oracle import quant as Q
+from _gpu_util import from_bits, out_to_f64, to_bits
+
+pytestmark = pytest.mark.gpu
+
+api = pytest.importorskip("paged_kv_cache_124_gb300.api")
+from paged_kv_cache_124_gb300 import inputs as I  # noqa: E402
+
+K_SCALE, V_SCALE = 0.02, 0.03
+
+
+def _problem(seed, Hq, Hkv, D, B, ctxs, news, fp8=False, gap=0):
+    """Filled slots up to each context, NaN in every other; `gap` rows of q
+    and out before, between and behind the sequences' rows belong to none."""
+    rng = np.random.default_rng(seed)
+    nblk = [-(-c // B) for c in ctxs]
+    NB, MB = sum(nblk) + 4, max(nblk + [1]) + 1
+    ids = rng.permutation(NB).astype(np.int32)
+    tables, at = np.full((len(ctxs), MB), -1, dtype=np.int32), 0
+    for s, n in enumerate(nblk):
+        tables[s, :n] = ids[at:at + n]
+        at += n
+    if fp8:
+        draw = lambda: Q.quantize(np.clip(rng.standard_normal((NB, Hkv, B, D)), -4, 4), 0.02)  # noqa: E731
+    else:
+        draw = lambda: to_bits(I.bf16_normal((NB, Hkv, B, D), int(rng.integers(1 << 30))))  # noqa: E731
+    nan = 0x7F if fp8 else 0x7FC0
+    kc, vc = draw(), draw()
+    filled = np.zeros((NB, B), dtype=bool)
+    for s, c in enumerate(ctxs):
+        for j in range(nblk[s]):
+            filled[tables[s, j], :min(B, c - j * B)] = True
+    for c in (kc, vc):
+        blk, off = np.where(~filled)
+        c[blk, :, off] = nan
+    start = np.concatenate([[0], np.cumsum(news)]).astype(np.int32) + gap
+    T = int(start[-1]) + gap
+    q = I.bf16_normal((T, Hq, D), seed + 1)
+    return q, kc, vc, tables, start, np.array(ctxs, dtype=np.int32)
+
+
+def _run(p, Hq, Hkv, D, B, most, out_dtype=torch.float32, mask=None, fp8=False, scale=None, max_ctx=None, ws=None,
+         status=None, stream=None):
+    q, kc, vc, tables, start, ctx = p
+    dev = "cuda"
+    out = torch.full(q.shape, float("nan"), dtype=out_dtype, device=dev)
+    put = (lambda c: torch.from_numpy(c).to(dev)) if fp8 else (lambda c: from_bits(c))
+    m = None if mask is None else torch.from_numpy(np.array(mask, dtype=np.uint64).view(np.int64)).to(dev)
+    api.pa_decode_multi(out, q.to(dev), put(kc), put(vc), torch.from_numpy(tables).to(dev),
+                        torch.from_numpy(start).to(dev), torch.from_numpy(ctx).to(dev), most, B,
+                        1 / math.sqrt(D) if scale is None else scale, Hq, Hkv, D,
+                        int(ctx.max()) if max_ctx is None else max_ctx, tree_mask=m,
+                        workspace=api.decode_multi_workspace(most, Hq, Hkv, D) if ws is None else ws, status=status,
+                        k_scale=K_SCALE if fp8 else None, v_scale=V_SCALE if fp8 else None)
+    return out
+
+
+def _check(p, out, Hq, Hkv, D, B, mask=None, fp8=False, scale=None, skip=()):
+    """|out - ref| within what the roundings inside allow: a weight is off by
+    a relative 2 (E + 128 * 2^-24) * (|q| . |k|) |scale| + W, E and W the
+    operand roundings (bf16: q exact, weights in two terms, W 2^-16; E4M3: q
+    and weights to f16, 2^-11 each), doubled as the normaliser moves too; an
+    output by that times sum a |v|; and half a step of the output's type."""
+    q, kc, vc, tables, start, ctx = p
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    kd, vd = (Q.dequantize(kc, K_SCALE), Q.dequantize(vc, V_SCALE)) if fp8 else (kc, vc)
+    want = A.paged_multi(to_bits(q), kd, vd, tables, start, ctx, scale, B, mask)
+    f64 = (lambda c: c) if fp8 else A.bf16_to_f64
+    weight = A.paged_multi(to_bits(q), f64(kd), np.abs(f64(vd)), tables, start, ctx, scale, B, mask)
+    E, W = (2.0 ** -11, 2.0 ** -11) if fp8 else (0.0, 2.0 ** -16)
+    got = out_to_f64(out)
+    qa = np.abs(A.bf16_to_f64(to_bits(q)))
+    covered = np.zeros(q.shape[0], dtype=bool)
+    for s in range(len(ctx)):
+        if s in skip:
+            continue
+        K, _ = A.gather_kv(np.abs(f64(kd)), np.abs(f64(vd)), tables[s], int(ctx[s]), B)
+        for r in range(start[s], start[s + 1]):
+            covered[r] = True
+            for g in range(Hq):
+                size = (K[g // (Hq // Hkv)] @ qa[r, g]).max() * abs(scale)
+                tol = (2 * (E + 128 * 2.0 ** -24) * size + W + 2.0 ** -18) * weight[r, g] * 2
+                if out.dtype == torch.bfloat16:
+                    tol = tol + 2.0 ** -8 * np.abs(want[r, g])
+                assert (np.abs(got[r, g] - want[r, g]) <= tol).all(), (s, r, g, np.abs(got[r, g] - want[r, g]).max())
+    assert np.isnan(got[~covered]).all()                       # rows of no sequence are left as they were
+
+
+def _trees(news, rng):
+    words = []
+    for n in news:
+        seen = []
+        for i in range(n):
+            up = int(rng.integers(-1, i)) if i else -1
+            seen.append((seen[up] if up >= 0 else 0) | 1 << i)
+        words += seen
+    return words
+
+
+CASES = [
+    # Hq, Hkv, D, B, contexts, new tokens
+    (4, 2, 64, 16, [2, 16, 17, 38], [1, 2, 3, 1]),
+    (32, 8, 128, 16, [1, 65, 300, 1000], [1, 4, 4, 2]),            # 16 rows: two column tiles
+    (8, 8, 128, 8, [8, 9, 70, 513], [8, 1, 5, 7]),                 # G = 1, 8-position blocks
+    (8, 4, 64, 32, [31, 64, 200], [16, 3, 9]),                     # 32 rows
+    (32, 2, 128, 16, [40, 129], [3, 9]),                           # G = 16: 144 rows, five row tiles
+    (16, 2, 64, 8, [61, 12], [20, 12]),                            # a whole prompt of 12
+    (2, 1, 128, 32, [2500], [2]),                                  # one head: the keys over many blocks
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B,ctxs,news", CASES)
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_multi_equals_the_oracle(Hq, Hkv, D, B, ctxs, news, kind, out_dtype):
+    p = _problem(Hq + D + B, Hq, Hkv, D, B, ctxs, news, gap=2)
+    rng = np.random.default_rng(1)
+    mask = None
+    if kind == "tree":
+        mask = [0, 0] + _trees(news, rng) + [0, 0]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = _run(p, Hq, Hkv, D, B, max(news), out_dtype, mask, status=st)
+    assert st.item() == 0
+    _check(p, out, Hq, Hkv, D, B, mask)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B,ctxs,news", [c for c in CASES if c[2] == 128])
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_multi_fp8_equals_the_oracle(Hq, Hkv, D, B, ctxs, news, kind):
+    p = _problem(Hq + B, Hq, Hkv, D, B, ctxs, news, fp8=True, gap=1)
+    mask = [0] + _trees(news, np.random.default_rng(2)) + [0] if kind == "tree" else None
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = _run(p, Hq, Hkv, D, B, max(news), mask=mask, fp8=True, status=st)
+    assert st.item() == 0
+    _check(p, out, Hq, Hkv, D, B, mask, fp8=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_one_token_is_the_decode(fp8):
+    """n = 1 for every sequence: pa_decode's operation."""
+    Hq, Hkv, D, B, ctxs = 32, 8, 128, 16, [1, 30, 700, 2100]
+    p = _problem(3, Hq, Hkv, D, B, ctxs, [1] * 4, fp8=fp8)
+    _check(p, _run(p, Hq, Hkv, D, B, 1, fp8=fp8), Hq, Hkv, D, B, fp8=fp8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_sixty_four_tokens_and_whole_prompts(D):
+    Hq, Hkv, B, ctxs, news = 4, 1, 16, [64, 100, 63], [64, 64, 63]
+    p = _problem(4, Hq, Hkv, D, B, ctxs, news)
+    words = _trees(news, np.random.default_rng(3))
+    words[63] |= 1 << 63
+    _check(p, _run(p, Hq, Hkv, D, B, 64, mask=words), Hq, Hkv, D, B, words)
+    _check(p, _run(p, Hq, Hkv, D, B, 64), Hq, Hkv, D, B)
+
+
+def test_chunks_past_sixty_four_tokens_are_causal():
+    Hq, Hkv, D, B, ctxs, news = 4, 2, 64, 16, [150, 90], [100, 70]
+    p = _problem(5, Hq, Hkv, D, B, ctxs, news)
+    _check(p, _run(p, Hq, Hkv, D, B, 100), Hq, Hkv, D, B)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_rows_that_see_nothing_are_zero(fp8):
+    """Nothing cached and an empty word: zeros; bits from n on say nothing; a
+    row that sees only the last of many new tokens."""
+    Hq, Hkv, D, B, ctxs, news = 8, 2, 128, 16, [5, 40, 33], [5, 40, 3]
+    p = _problem(6, Hq, Hkv, D, B, ctxs, news, fp8=fp8)
+    words = [0, 1, ~0 << 5 & (2 ** 64 - 1), 4, 31] + [0] * 39 + [1 << 39] + [0, 0, 0]
+    words[5] = 1 << 39
+    out = _run(p, Hq, Hkv, D, B, 40, mask=words, fp8=fp8)
+    _check(p, out, Hq, Hkv, D, B, words, fp8=fp8)
+    assert (out[0] == 0).all() and (out[2] == 0).all() and (out[6] == 0).all() and (out[5] != 0).any()
+    assert (out[45:] != 0).any()                             # the context before the new tokens is always seen
+
+
+def test_scores_of_every_size():
+    """Maxima that grow along the sequence by more than the kernel lets pass
+    without a rescale, fall, and differ between rows; a scale of zero."""
+    Hq, Hkv, D, B, C, n = 4, 1, 128, 16, 900, 4
+    q, kc, vc, tables, start, ctx = _problem(7, Hq, Hkv, D, B, [C], [n])
+    k = A.bf16_to_f64(kc)
+    for j in range(C):
+        k[tables[0, j // B], :, j % B] *= 4.0 * (1 + math.sin(j / 70.0)) * (1 if j < 600 else 0.01)
+    kc = to_bits(torch.from_numpy(np.nan_to_num(k, nan=0.0)).to(torch.bfloat16))
+    p = (q, kc, vc, tables, start, ctx)
+    _check(p, _run(p, Hq, Hkv, D, B, n), Hq, Hkv, D, B)
+    _check(p, _run(p, Hq, Hkv, D, B, n, scale=0.0), Hq, Hkv, D, B, scale=0.0)
+    _check(p, _run(p, Hq, Hkv, D, B, n, scale=-0.05), Hq, Hkv, D, B, scale=-0.05)
+
+
+def test_a_nan_key_makes_its_rows_nan_and_no_other():
+    Hq, Hkv, D, B = 8, 2, 64, 16
+    p = _problem(8, Hq, Hkv, D, B, [300, 40], [3, 2])
+    q, kc, vc, tables, start, ctx = p
+    kc[tables[0, 18], 1, 10, 5] = 0x7FC0                     # position 298: the second of the three new tokens
+    out = out_to_f64(_run(p, Hq, Hkv, D, B, 3))
+    assert np.isnan(out[1:3, 4:]).all() and np.isfinite(out[0]).all() and np.isfinite(out[1:3, :4]).all()
+    assert np.isfinite(out[3:]).all()
+
+
+def test_many_ragged_sequences_and_sequences_that_bring_nothing():
+    """More sequences than a block has threads, lengths from one up, some of
+    them without new tokens, all in one launch over all SMs."""
+    Hq, Hkv, D, B = 4, 2, 64, 8
+    rng = np.random.default_rng(9)
+    news = [int(x) for x in rng.integers(0, 4, 300)]
+    ctxs = [int(max(1, n + rng.integers(0, 90))) for n in news]
+    p = _problem(9, Hq, Hkv, D, B, ctxs, news)
+    _check(p, _run(p, Hq, Hkv, D, B, 3, torch.bfloat16), Hq, Hkv, D, B)
+
+
+def test_the_same_call_twice_gives_the_same_bits_and_any_workspace_serves():
+    Hq, Hkv, D, B, ctxs, news = 32, 8, 128, 16, [4000, 10, 1500], [4, 4, 2]
+    p = _problem(10, Hq, Hkv, D, B, ctxs, news)
+    a = _run(p, Hq, Hkv, D, B, 4)
+    ws = api.decode_multi_workspace(4, Hq, Hkv, D)
+    ws.fill_(0xFF)
+    b = _run(p, Hq, Hkv, D, B, 4, ws=ws)
+    assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+    with pytest.raises(api.PAError) as e:
+        _run(p, Hq, Hkv, D, B, 4, ws=ws[:-256])
+    assert e.value.status == api.PA_ERR_WORKSPACE
+
+
+def test_bad_metadata_is_flagged_and_skipped():
+    Hq, Hkv, D, B, ctxs, news = 8, 2, 64, 16, [50, 30, 20, 40], [2, 3, 2, 2]
+    q, kc, vc, tables, start, ctx = _problem(11, Hq, Hkv, D, B, ctxs, news)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad, most, skip in ((dict(ctx=[50, 2, 20, 40]), 3, {1}), (dict(), 2, {1}),
+                            (dict(start=[0, 2, 5, 7, 10]), 3, {3})):
+        p = (q, kc, vc, tables, np.array(bad.get("start", start), dtype=np.int32),
+             np.array(bad.get("ctx", ctx), dtype=np.int32))
+        st.zero_()
+        out = _run(p, Hq, Hkv, D, B, most, status=st)
+        assert st.item() == api.PA_DEV_BAD_CONTEXT
+        good = (q, kc, vc, tables, start, ctx)
+        _check(good, out, Hq, Hkv, D, B, skip=skip)
+    # a table entry outside the pool is flagged; the other sequences are right
+    t = tables.copy()
+    t[2, 0] = 10 ** 6
+    st.zero_()
+    out = _run((q, kc, vc, t, start, ctx), Hq, Hkv, D, B, 3, status=st)
+    assert st.item() == api.PA_DEV_BAD_BLOCK_ID
+    out[start[2]:start[3]] = float("nan")
+    _check((q, kc, vc, tables, start, ctx), out, Hq, Hkv, D, B, skip={2})
+
+
+def test_on_a_stream_of_its_own():
+    Hq, Hkv, D, B, ctxs, news = 8, 2, 128, 16, [500, 70], [4, 3]
+    p = _problem(12, Hq, Hkv, D, B, ctxs, news)
+    a = _run(p, Hq, Hkv, D, B, 4)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        b = _run(p, Hq, Hkv, D, B, 4)
+    side.synchronize()
+    assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+@pytest.mark.parametrize("i", range(24))
+def test_random_configurations(i):
+    rng = np.random.default_rng(100 + i)
+    fp8 = bool(rng.random() < 0.4)
+    D = 128 if fp8 else int(rng.choice([64, 128]))
+    B, Hkv, G = int(rng.choice([8, 16, 32])), int(rng.choice([1, 2, 3, 4])), int(rng.choice([1, 2, 4, 8, 16]))
+    n_seqs, most = int(rng.integers(1, 7)), int(rng.choice([1, 2, 3, 4, 7, 12, 20]))
+    news = [int(x) for x in rng.integers(0, most + 1, n_seqs)]
+    news[0] = most
+    ctxs = [int(n + rng.choice([0, 1, 15, 16, 17, 47, 48, 64, 200, 700])) for n in news]
+    ctxs = [max(1, c) for c in ctxs]
+    p = _problem(200 + i, G * Hkv, Hkv, D, B, ctxs, news, fp8=fp8, gap=int(rng.integers(0, 3)))
+    mask = None
+    if rng.random() < 0.5:
+        gap = int(p[4][0])
+        mask = [0] * gap + _trees(news, rng) + [0] * gap
+    dt = torch.float32 if rng.random() < 0.5 else torch.bfloat16
+    _check(p, _run(p, G * Hkv, Hkv, D, B, most, dt, mask, fp8), G * Hkv, Hkv, D, B, mask, fp8)

@@ -1,0 +1,399 @@
+"""pa_plan_step, pa_release_rows and pa_qk_norm_rope_cache against the oracle
+(oracle/step.py), and a whole step of new tokens: planned, normed, rotated,
+cached and attended to on the GPU.  Plans are whole numbers and must be
+equal; projections carry one rounding."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as A
+from oracle import quant as Q
+from oracle import step as S
+from _gpu_util import to_bits
+
+pytestmark = pytest.mark.gpu
+
+api = pytest.importorskip("paged_kv_cache_124_gb300.api")
+from paged_kv_cache_124_gb300 import inputs as I  # noqa: E402
+
+
+class Plan:
+    """Device state of a planner and the same state for the oracle."""
+
+    def __init__(self, rows, max_blocks, pool, block, rng, status=True):
+        self.B, self.NB, self.MB, self.R = block, pool, max_blocks, rows
+        ids = [int(x) for x in rng.permutation(pool)]
+        self.tables, self.blocks, self.lens = [[-1] * max_blocks for _ in range(rows)], [0] * rows, [0] * rows
+        self.free = ids
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.d_tables = torch.tensor(self.tables, dtype=torch.int32, device="cuda")
+        self.d_blocks = torch.zeros(rows, dtype=torch.int32, device="cuda")
+        self.d_free = torch.tensor(ids, dtype=torch.int32, device="cuda")
+        self.d_count = torch.tensor([len(ids)], dtype=torch.int32, device="cuda")
+
+    def outputs(self, n_seqs, tokens):
+        i = lambda *s: torch.full(s, 77, dtype=torch.int32, device="cuda")  # noqa: E731
+        return i(n_seqs, self.MB), i(n_seqs), i(n_seqs + 1), i(tokens), i(tokens).long()
+
+    def gpu(self, seq_rows, new, tokens, lens=None, free=True):
+        d = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        out = self.outputs(len(seq_rows), tokens)
+        api.pa_plan_step(*out, d(seq_rows), d(new), d(self.lens if lens is None else lens), self.d_tables, self.d_blocks,
+                         self.d_free if free else None, self.d_count if free else None, self.B, self.NB,
+                         status=self.status)
+        return [x.cpu().tolist() for x in out]
+
+    def check_state(self):
+        assert self.d_blocks.cpu().tolist() == self.blocks
+        n = int(self.d_count.item())
+        assert n == len(self.free) and self.d_free.cpu().tolist()[:n] == self.free
+        got = self.d_tables.cpu().tolist()
+        for r in range(self.R):
+            assert got[r][:self.blocks[r]] == self.tables[r][:self.blocks[r]]
+
+    def step(self, seq_rows, new, pad=0):
+        """Plan on both sides and compare everything; row_lens advance."""
+        tokens = sum(n for r, n in zip(seq_rows, new) if r >= 0) + pad
+        want = S.plan_step(seq_rows, new, self.lens, self.tables, self.blocks, self.free, self.B, tokens)
+        got = self.gpu(seq_rows, new, tokens)
+        assert self.status.item() == 0
+        tables, ctx, start, positions, slots = want
+        assert got[0] == [t + [-1] * (self.MB - len(t)) for t in tables]
+        assert got[1:] == [ctx, start, positions, slots]
+        self.check_state()
+        for r, n in zip(seq_rows, new):
+            if r >= 0:
+                self.lens[r] += n
+
+
+@pytest.mark.parametrize("block,max_blocks,seqs,seed", [(16, 8, 1, 0), (8, 33, 7, 1), (32, 20, 40, 2), (16, 64, 300, 3),
+                                                        (8, 5, 1030, 4), (16, 3, 8192, 5)])
+def test_steps_equal_the_oracle(block, max_blocks, seqs, seed):
+    """Mixed batches (nothing cached, one token, chunks, none, padding among
+    and after the requests), several steps on the same state."""
+    rng = np.random.default_rng(seed)
+    p = Plan(seqs + 5, max_blocks, (seqs + 5) * max_blocks, block, rng)
+    room = max_blocks * block
+    for _ in range(4):
+        rows = [int(r) for r in rng.permutation(seqs + 5)[:seqs]]
+        new = [int(min(rng.choice([0, 1, 1, 1, 2, block, 3 * block + 1]), room - p.lens[r])) for r in rows]
+        for i in rng.integers(0, seqs, seqs // 6):
+            rows[i] = -1
+        p.step(rows, new, pad=int(rng.integers(0, 70)))
+
+
+def test_a_long_chunk_and_an_empty_batch():
+    rng = np.random.default_rng(6)
+    p = Plan(3, 2048, 5000, 8, rng)
+    p.step([2, 0], [16384, 1], pad=5)              # fills its row to the last position
+    p.step([], [], pad=3)
+    p.step([-1, -1], [4, 4], pad=0)                # padding brings nothing
+
+
+def test_planning_again_takes_nothing_and_a_rejected_draft_keeps_its_blocks():
+    rng = np.random.default_rng(7)
+    p = Plan(4, 8, 24, 16, rng)
+    p.step([1, 3], [16, 15])
+    a = p.gpu([1, 3], [9, 9], 18)
+    held = int(p.d_count.item())
+    assert p.gpu([1, 3], [9, 9], 18) == a and int(p.d_count.item()) == held
+    S.plan_step([1, 3], [9, 9], p.lens, p.tables, p.blocks, p.free, 16, 18)
+    p.check_state()
+    p.lens[1] += 2                                  # two of the nine were accepted
+    p.lens[3] += 1
+    p.step([3, 1], [3, 20])
+
+
+def test_tables_reserved_by_the_host_manager():
+    """Without a free list the rows' tables hold the blocks: the slots are the
+    host manager's for the same positions."""
+    alloc = api.BlockAllocator(40, 16)
+    assert alloc.allocate(0, 100) == alloc.allocate(1, 33) == api.PA_OK
+    rng = np.random.default_rng(8)
+    p = Plan(2, 8, 40, 16, rng)
+    tables, _ = alloc.build_tables([0, 1], 8)
+    p.d_tables.copy_(torch.from_numpy(tables))
+    p.d_blocks.copy_(torch.tensor([7, 3], dtype=torch.int32))
+    got = p.gpu([1, 0], [3, 10], 13, lens=[90, 30], free=False)
+    assert p.status.item() == 0
+    assert got[4] == alloc.slot_mapping(1, 30, 3).tolist() + alloc.slot_mapping(0, 90, 10).tolist()
+    assert got[0] == [tables[1].tolist(), tables[0].tolist()]
+    p.gpu([1, 0], [19, 0], 19, lens=[90, 30], free=False)       # a fourth block, and none to take
+    assert p.status.item() == api.PA_DEV_NO_BLOCKS
+
+
+@pytest.mark.parametrize("rows,new,tokens,lens,bit", [
+    ([0, 1], [40, 40], 80, None, "NO_BLOCKS"),           # one block short
+    ([0, 4], [1, 1], 2, None, "BAD_ROW"),                # out of range
+    ([2, 1, 2], [1, 1, 1], 3, None, "BAD_ROW"),          # the same row twice
+    ([0, 1], [1, -1], 2, None, "BAD_CONTEXT"),
+    ([0, 1], [1, 65], 66, None, "BAD_CONTEXT"),          # past the table
+    ([0, 1], [3, 2], 4, None, "BAD_CONTEXT"),            # more than num_tokens
+    ([0, 1], [1, 1], 2, [0, -3, 0, 0], "BAD_CONTEXT"),
+    ([0, 1], [2147483647, 2147483647], 9, None, "BAD_CONTEXT"),
+])
+def test_a_refused_plan_changes_nothing(rows, new, tokens, lens, bit):
+    rng = np.random.default_rng(9)
+    p = Plan(4, 4, 7, 16, rng)
+    p.step([3], [20])
+    p.step([0], [1])                                     # four blocks left: 3 + 3 - 1 are needed
+    got = p.gpu(rows, new, tokens, lens)
+    assert p.status.item() == getattr(api, "PA_DEV_" + bit)
+    assert got[2] == [0] * (len(rows) + 1)
+    assert got[3] == [-1] * tokens and got[4] == [-1] * tokens
+    p.check_state()
+
+
+def test_a_free_count_out_of_range_is_refused():
+    p = Plan(2, 4, 8, 16, np.random.default_rng(10))
+    for n in (9, -1):
+        p.d_count.fill_(n)
+        p.status.zero_()
+        p.gpu([0], [5], 5)
+        assert p.status.item() == api.PA_DEV_NO_BLOCKS and p.d_count.item() == n
+    assert p.d_blocks.cpu().tolist() == [0, 0]
+
+
+def test_a_bad_block_id_gives_no_slot():
+    p = Plan(2, 4, 8, 16, np.random.default_rng(11))
+    p.d_free[-1] = 8                                     # outside the pool of 8
+    p.d_free[-2] = -7
+    got = p.gpu([0, 1], [3, 20], 23)
+    assert p.status.item() == api.PA_DEV_BAD_BLOCK_ID
+    assert got[4][:3] == [-1] * 3 and got[4][3:19] == [-1] * 16 and all(s >= 0 for s in got[4][19:])
+
+
+def test_release_equals_the_oracle_and_refuses():
+    rng = np.random.default_rng(12)
+    p = Plan(30, 10, 250, 8, rng)
+    p.step(list(range(30)), [int(n) for n in rng.integers(0, 60, 30)])
+    rel = lambda rows: api.pa_release_rows(torch.tensor(rows, dtype=torch.int32, device="cuda"), p.d_tables,  # noqa: E731
+                                           p.d_blocks, p.d_free, p.d_count, status=p.status)
+    for rows in ([7, -1, 3], [29, 0, 1, 2], [7]):        # a row that holds nothing is fine
+        rel(rows)
+        S.release_rows(rows, p.tables, p.blocks, p.free)
+        for r in rows:
+            p.lens[r] = 0
+        assert p.status.item() == 0
+        p.check_state()
+    p.step([7, 8], [31, 1])
+    for rows, bit in (([5, 5], api.PA_DEV_BAD_ROW), ([30], api.PA_DEV_BAD_ROW)):
+        p.status.zero_()
+        rel(rows)
+        assert p.status.item() == bit
+        p.check_state()
+    p.status.zero_()
+    p.d_count.fill_(250)                                 # the list would overflow
+    rel([6])
+    assert p.status.item() == api.PA_DEV_BAD_CONTEXT and p.d_blocks[6].item() == p.blocks[6]
+
+
+# ---------------------------------------------------------------------------
+# norm + rotation + cache write
+# ---------------------------------------------------------------------------
+
+def _rope_case(T, Hq, Hkv, D, B, rot, norm, seed, longest=5000, packed=True):
+    rng = np.random.default_rng(seed)
+    if packed:
+        qkv = I.bf16_normal((T, (Hq + 2 * Hkv) * D), seed).cuda()
+        q, k, v = (x.unflatten(1, (-1, D)) for x in qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+    else:
+        q, k, v = (I.bf16_normal((T, h, D), seed + i).cuda() for i, h in enumerate((Hq, Hkv, Hkv)))
+    NB = -(-T // B) + 3
+    slots = rng.permutation(NB * B)[:T].astype(np.int64)
+    pos = rng.integers(0, longest, T).astype(np.int32)
+    pos[0] = longest - 1
+    gains = [torch.from_numpy((1 + 0.2 * rng.standard_normal(D)).astype(np.float32)).cuda() for _ in range(2)] if norm \
+        else [None, None]
+    return q, k, v, pos, slots, gains, NB, api.rope_table(longest, rot)
+
+
+def _expected(x, gain, eps, pos, rot, interleaved):
+    """Exact rows and their tolerance before the final rounding, [T, H, D]:
+    32-bit sums and products put a turned element within 2^-19 (|a| + |b|) of
+    its pair (a, b): at most 19 additions and 8 products and factors in a row
+    and the table's own rounding, each 2^-24, and rsqrt's two units."""
+    x64 = A.bf16_to_f64(to_bits(x))
+    y, tol = np.empty_like(x64), np.empty_like(x64)
+    for t in range(x64.shape[0]):
+        for h in range(x64.shape[1]):
+            y[t, h] = S.norm_rope(x64[t, h], gain, eps, int(pos[t]), rot, interleaved)
+            size = np.abs(S.norm_rope(x64[t, h], gain, eps, 0, rot, interleaved))
+            pair = size.copy()
+            c = np.arange(rot // 2)
+            i, j = (2 * c, 2 * c + 1) if interleaved else (c, c + rot // 2)
+            pair[i] = pair[j] = size[i] + size[j]
+            tol[t, h] = pair * 2.0 ** -19
+    return y, tol
+
+
+def _close(got, want, tol, half_step, smallest=0.0):
+    off = np.abs(got - want)
+    assert (off <= tol + half_step * (np.abs(want) + tol) + smallest).all(), off.max()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,B,rot,inter,norm,packed", [
+    (1, 32, 8, 128, 16, 128, False, True, True),
+    (37, 4, 2, 64, 8, 64, False, True, True),
+    (19, 8, 1, 128, 32, 32, False, True, True),          # a quarter of each head turns
+    (23, 2, 2, 64, 16, 16, True, True, False),
+    (11, 16, 4, 128, 16, 128, True, False, True),
+    (9, 6, 3, 64, 16, 48, False, False, False),
+    (130, 1, 1, 128, 16, 112, True, True, True),
+])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_norm_rope_cache_equals_the_oracle(T, Hq, Hkv, D, B, rot, inter, norm, packed, fp8):
+    q, k, v, pos, slots, (qw, kw), NB, table = _rope_case(T, Hq, Hkv, D, B, rot, norm, 5 * T + Hq, packed=packed)
+    scales = (np.float32(0.013), np.float32(0.021))
+    if fp8:
+        kc = torch.full((NB, Hkv, B, D), 0x5A, dtype=torch.uint8, device="cuda")
+    else:
+        kc = torch.full((NB, Hkv, B, D), 7.5, dtype=torch.bfloat16, device="cuda")
+    vc, untouched = kc.clone(), kc.cpu().clone()
+    out = torch.full((T, Hq, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    extra = dict(k_scale=float(scales[0]), v_scale=float(scales[1])) if fp8 else {}
+    api.pa_qk_norm_rope_cache(out, kc, vc, q, k, v, torch.from_numpy(pos).cuda(), torch.from_numpy(slots).cuda(), table,
+                              q_weight=qw, k_weight=kw, eps=1e-5, interleaved=inter, status=st, **extra)
+    assert st.item() == 0
+    host = lambda w: None if w is None else w.double().cpu().numpy()  # noqa: E731
+    want, tol = _expected(q, host(qw), 1e-5, pos, rot, inter)
+    _close(A.bf16_to_f64(to_bits(out)), want, tol, 2.0 ** -8)
+    want, tol = _expected(k, host(kw), 1e-5, pos, rot, inter)
+    rows = lambda c: c.cpu().permute(0, 2, 1, 3).reshape(NB * B, Hkv, D)[torch.from_numpy(slots)]  # noqa: E731
+    if fp8:
+        s = float(scales[0])
+        got = Q.e4m3_to_f64(rows(kc).numpy())
+        want, tol = np.clip(want / s, -448, 448), tol / s + np.abs(want / s) * 2.0 ** -23
+        _close(got, want, tol, 2.0 ** -4, 2.0 ** -10)    # below 2^-6 the codes are 2^-9 apart
+        assert np.array_equal(rows(vc).numpy(), Q.quantize(v.float().cpu().numpy(), scales[1]))
+    else:
+        _close(A.bf16_to_f64(to_bits(rows(kc))), want, tol, 2.0 ** -8)
+        assert np.array_equal(to_bits(rows(vc)), to_bits(v))
+    # every other slot is as it was
+    keep = np.setdiff1d(np.arange(NB * B), slots)
+    flat = lambda c: c.cpu().permute(0, 2, 1, 3).reshape(NB * B, Hkv, D)[torch.from_numpy(keep)]  # noqa: E731
+    for c in (kc, vc):
+        assert torch.equal(flat(c).float() if not fp8 else flat(c), flat(untouched).float() if not fp8 else
+                           flat(untouched))
+
+
+def test_padding_bad_positions_and_bad_slots():
+    T, Hq, Hkv, D, B = 8, 4, 2, 128, 16
+    q, k, v, pos, slots, (qw, kw), NB, table = _rope_case(T, Hq, Hkv, D, B, 128, True, 3, longest=50)
+    pos = np.array([4, -1, 49, 50, 7, 8, -5, 9], dtype=np.int32)
+    slots = np.array([0, 1, 2, 3, -1, NB * B, 5, 6], dtype=np.int64)
+    kc = torch.zeros((NB, Hkv, B, D), dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    out = torch.full((T, Hq, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.pa_qk_norm_rope_cache(out, kc, vc, q, k, v, torch.from_numpy(pos).cuda(), torch.from_numpy(slots).cuda(), table,
+                              q_weight=qw, k_weight=kw, status=st)
+    assert st.item() == api.PA_DEV_BAD_POSITION | api.PA_DEV_BAD_SLOT
+    left = [bool((out[t] == 3.0).all()) for t in range(T)]
+    assert left == [False, True, False, True, False, False, True, False]
+    written = [bool((vc[s // B, :, s % B] != 0).any()) for s in range(8)]
+    assert written == [True, False, True, False, False, False, True, False]
+    assert (vc[1:] == 0).all()
+
+
+def test_q_in_place_extreme_values_and_no_tokens():
+    T, Hq, Hkv, D, B = 5, 8, 2, 64, 16
+    q, k, v, pos, slots, (qw, kw), NB, table = _rope_case(T, Hq, Hkv, D, B, 64, True, 4, packed=False)
+    q[0, 0] = 0.0                                            # a zero head stays zero: eps is inside the root
+    q[1, 1] = 1e30                                           # squares beyond fp32: the mean is infinite
+    kc = torch.zeros((NB, Hkv, B, D), dtype=torch.bfloat16, device="cuda")
+    vc, p, s = kc.clone(), torch.from_numpy(pos).cuda(), torch.from_numpy(slots).cuda()
+    out = torch.empty_like(q)
+    api.pa_qk_norm_rope_cache(out, kc, vc, q, k, v, p, s, table, q_weight=qw, k_weight=kw)
+    assert (out[0, 0] == 0).all() and (out[1, 1] == 0).all()
+    api.pa_qk_norm_rope_cache(q, kc, vc, q, k, v, p, s, table, q_weight=qw, k_weight=kw)
+    assert torch.equal(out.view(torch.int16), q.view(torch.int16))
+    api.pa_qk_norm_rope_cache(out[:0], kc, vc, q[:0], k[:0], v[:0], p[:0], s[:0], table)
+    with pytest.raises(ValueError, match="contiguous"):
+        api.pa_qk_norm_rope_cache(out[:, :4], kc, vc, q[:, ::2], k, v, p, s, table)
+
+
+# ---------------------------------------------------------------------------
+# a whole step
+# ---------------------------------------------------------------------------
+
+def _random_tree(n, rng):
+    seen = []
+    for i in range(n):
+        up = int(rng.integers(0, i)) if i else -1
+        seen.append((seen[up] if up >= 0 else 0) | 1 << i)
+    return seen
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_steps_of_new_tokens_from_projections_to_attention(fp8):
+    """Prompt chunks, then drafts verified under a tree mask of which a part is
+    kept, then single tokens: each step planned, normed, rotated, cached and
+    attended to on the GPU alone, captured as a graph and replayed, and
+    compared with the oracle over the cache as the GPU left it."""
+    Hq, Hkv, D, B, R, MB = 8, 2, 128, 16, 4, 6
+    rng = np.random.default_rng(20)
+    NB, T, scale, dev = R * MB, 64, 1 / math.sqrt(D), "cuda"
+    p = Plan(R, MB, NB, B, rng)
+    cache = lambda: (torch.full((NB, Hkv, B, D), 0x7F, dtype=torch.uint8, device=dev) if fp8 else  # noqa: E731
+                     I.nan_pool((NB, Hkv, B, D), dev))
+    kc, vc = cache(), cache()
+    table = api.rope_table(MB * B, D)
+    scales = dict(k_scale=0.02, v_scale=0.02) if fp8 else {}
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+    rows, new, lens = i32(R), i32(R), i32(R)
+    tables, ctx, start, pos = i32(R, MB), i32(R), i32(R + 1), i32(T)
+    slots, mask = torch.zeros(T, dtype=torch.int64, device=dev), torch.zeros(T, dtype=torch.int64, device=dev)
+    qkv = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16, device=dev)
+    q, k, v = (x.unflatten(1, (-1, D)) for x in qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+    q_rot = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    out = torch.zeros(T, Hq, D, dtype=torch.float32, device=dev)
+    ws = api.decode_multi_workspace(40, Hq, Hkv, D)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def step():
+        api.pa_plan_step(tables, ctx, start, pos, slots, rows, new, lens, p.d_tables, p.d_blocks, p.d_free, p.d_count, B,
+                         NB, status=st)
+        api.pa_qk_norm_rope_cache(q_rot, kc, vc, q, k, v, pos, slots, table, status=st, **scales)
+        api.pa_decode_multi(out, q_rot, kc, vc, tables, start, ctx, 40, B, scale, Hq, Hkv, D, MB * B, tree_mask=mask,
+                            workspace=ws, status=st, **scales)
+
+    # captured once, on a batch that brings nothing
+    rows.fill_(-1)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n_step, (batch, bring) in enumerate([([2, 0, 3, -1], [40, 1, 17, 0]), ([0, 2, -1, 3], [5, 9, 0, 16]),
+                                             ([3, 2, 1, 0], [1, 1, 1, 1])]):
+        words, total = [], 0
+        for r, n in zip(batch, bring):
+            words += _random_tree(n, rng) if n_step else [(2 << i) - 1 for i in range(n)]
+            total += n
+        rows.copy_(torch.tensor(batch))
+        new.copy_(torch.tensor(bring))
+        lens.copy_(torch.tensor(p.lens))
+        mask[:total] = torch.tensor(words)
+        qkv[:] = I.bf16_normal(tuple(qkv.shape), 30 + n_step).to(dev)
+        out.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        want = S.plan_step(batch, bring, p.lens, p.tables, p.blocks, p.free, B, T)
+        assert pos.cpu().tolist() == want[3] and slots.cpu().tolist() == want[4]
+        p.check_state()
+        kd = Q.dequantize(kc.cpu().numpy(), 0.02) if fp8 else to_bits(kc)
+        vd = Q.dequantize(vc.cpu().numpy(), 0.02) if fp8 else to_bits(vc)
+        ref = A.paged_multi(to_bits(q_rot), kd, vd, tables.cpu().numpy(), want[2], want[1], scale, B, words)
+        got = out.cpu().double().numpy()
+        assert np.abs(got[:total] - ref[:total]).max() <= 2e-3
+        assert (got[total:] == 9.0).all()                     # rows behind the last token
+        for r, n in zip(batch, bring):
+            if r >= 0:
+                p.lens[r] += n if n_step != 1 else (n + 1) // 2   # half of a draft is kept
