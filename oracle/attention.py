@@ -184,7 +184,8 @@ def paged_multi(q, k_cache, v_cache, block_tables, query_start, context_lens, sc
     out = np.zeros((T, n_q_heads, d_head), dtype=np.float64)
     for s in range(len(context_lens)):
         C = int(context_lens[s])
-        row0, n = int(query_start[s]), int(query_start[s + 1]) - int(query_start[s])
+        row0 = int(query_start[s])
+        n = int(query_start[s + 1]) - row0
         if n <= 0:
             continue
         K, V = gather_kv(k_cache, v_cache, block_tables[s], C, block_size)
@@ -195,7 +196,7 @@ def paged_multi(q, k_cache, v_cache, block_tables, query_start, context_lens, sc
                 continue
             for g in range(n_q_heads):
                 h = kv_head_of(g, n_q_heads, n_kv_heads)
-                out[row0 + i, g] = softmax_attention(q[row0 + i, g], K[h][sees], V[h][sees], scale)
+                out[row0 + i, g, :] = softmax_attention(q[row0 + i][g], K[h][sees], V[h][sees], scale)
     return out
 
 

@@ -11,22 +11,27 @@
 //
 // What bounds it: each K/V byte is read once for n * G rows, 4 * n * G
 // operations per two bytes, so up to some tens of rows the cache's bytes
-// bound it and the design is the single-token kernel's, with more columns:
-//  * Work is counted in steps of 64 positions of one unit (sequence, KV
-//    head, tile of 8 * NT rows).  The grid's blocks take equal contiguous
-//    shares of all the steps, computed from the lengths by every block for
-//    itself: no partition size to choose, no empty blocks on ragged batches,
-//    and at most two unfinished units per block whatever the batch.
-//  * A block's 4 warps take 16 positions of a step each, from rings of
-//    shared-memory stages that TMA fills through the block table.  Keys are
-//    the rows of the products (S[16 x 8 NT] = K . Q^T, O^T += V^T . P^T), so
-//    a K or V fragment is loaded once for all the tile's rows.
-//  * The running maximum of a column is raised only when a score exceeds it
-//    by 2^8 (one vote instead of the shuffles of a maximum); weights stay
-//    within 2^8 and sums in fp32.
+// bound it; beyond, the warp-level matrix products do.
+//  * A unit is a (sequence, KV head, tile of rows); its work is counted in
+//    steps of 64 positions plus a constant for starting and joining it.  The
+//    grid is the resident blocks, and they take equal contiguous shares of
+//    all the work, computed from the lengths by every block for itself: no
+//    partition size to choose, no empty blocks on ragged batches, and at
+//    most two unfinished units per block whatever the batch.
+//  * Four warps of a block take 16 positions of a step each, from rings of
+//    shared-memory stages that TMA fills through the block table; with more
+//    than 32 rows a second four warps share the stages and take the other
+//    half of the rows.  The next unit's first tiles are in flight while the
+//    warps' states of a unit are joined, in the one stage they leave free.
+//  * Rows are the rows of the products (S[16 x 16] = Q . K^T, then
+//    O[16 x D] += P . V), so the weights are the second product's operand as
+//    they come out of the first.
+//  * The running maximum of a row is raised only when a score exceeds it by
+//    2^8 (one vote instead of a maximum's shuffles); weights stay within 2^8
+//    and sums in fp32.
 //  * A unit that one block covers is written at once.  Pieces of the others
-//    go to the workspace as (m, z, u), and a second kernel, one block per
-//    unit that a block began and did not finish, merges them.
+//    go to the workspace as (m, z, u), and a second kernel, over the units
+//    that a block began and did not finish, merges them.
 
 #include <math.h>
 
@@ -34,15 +39,19 @@
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kKeyWarps = 4;               // warps that split a step's positions
 constexpr int kTile = 16;                  // positions per warp and step
-constexpr int kStep = kWarps * kTile;
+constexpr int kStep = kKeyWarps * kTile;
 constexpr int kMaxProbes = 2000000;        // ~2 s bound on any single wait
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -3.0e38f;          // a row's maximum before it has seen anything
 constexpr float kRaise = 8.0f;             // log2 of the largest weight before the maximum is raised
 constexpr float kWeightScale = 128.f;      // FP8: weights enter f16 products times 2^7 (at most 2^15)
-constexpr int kMinShare = 4;               // steps per block, at least
+#ifndef PA_MULTI_UNIT_COST
+#define PA_MULTI_UNIT_COST 3
+#endif
+constexpr int kUnitCost = PA_MULTI_UNIT_COST;   // steps that starting and joining a unit is worth
+constexpr int kMinShare = 4 + kUnitCost;   // work per block, at least
 constexpr int kMergeThreads = 256;
 constexpr int kMergeSplit = 4;             // blocks per unit to merge
 
@@ -58,42 +67,53 @@ struct MultiArgs {
     float* part_z;
     float* part_u;                         // [2 per block][rows][D]
     int32_t* status;
-    float scale_log2;                      // scale * log2(e), times the K scale
+    float scale_log2;                      // |scale| * log2(e), times the K scale; > 0
+    float q_sign;                          // the scale's sign (0: a scale of zero, scale_log2 is 1)
     float v_scale;                         // factor on the weighted sums
     int out_f32, log2_block, n_q_heads, n_kv_heads, log2_group, max_blocks, num_blocks, ctx_cap, num_seqs, num_tokens,
         max_query_len;
 };
 
-template <int D, bool F8, int NT>
+// MT: 16-row tiles per warp; RG: groups of four warps, each with its own rows.
+template <int D, bool F8, int MT, int RG>
 struct Geo {
-    static constexpr int kRows = 8 * NT;
-    static constexpr int kSlabs = F8 ? 1 : D / 64;               // 128-byte boxes per row
+    static constexpr int kRows = 16 * MT * RG;                   // rows of a unit
+    static constexpr int kThreads = 32 * kKeyWarps * RG;
+    static constexpr int kSlabs = F8 ? 1 : D / 64;               // 128-byte boxes per cache row
     static constexpr int kSlabBytes = kTile * 128;
-    static constexpr int kTileBytes = kSlabs * kSlabBytes;       // K or V of one tile
+    static constexpr int kTileBytes = kSlabs * kSlabBytes;       // K or V of one warp's tile
     static constexpr int kStageBytes = 2 * kTileBytes;
-    // bytes in flight per SM decide: 64 KB per block at three blocks, 96 at two
-    static constexpr int kBlocksPerSm = NT > 2 ? 2 : 3;
-    static constexpr int kStages = (NT > 2 ? 98304 : 65536) / (kWarps * kStageBytes);
-    static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-    static constexpr int kUStride = D + 4;                       // floats per row of the merge: banks differ
-    static constexpr int kMergeBytes = 4 * kWarps * kRows * (kUStride + 2);
-    static constexpr int kMain = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+    static constexpr int kBlocksPerSm = RG == 2 ? 1 : MT == 2 ? 2 : 3;
+    static constexpr int kRingBytes = (RG == 2 ? 160 : MT == 2 ? 96 : 64) * 1024;
+    static constexpr int kStages = kRingBytes / (kKeyWarps * kStageBytes);
+    // The joining of the warps' states takes the fp32 rows of one row tile
+    // per group: one stage of all key warps (bf16), or two (FP8).
+    static constexpr int kJoinParts = F8 ? 2 : 1;
+    static constexpr int kJoinStages = kJoinParts * RG;
+    static constexpr int kAhead = kStages - kJoinStages;         // tiles of the next unit in flight meanwhile
     static constexpr int kQStride = 2 * D + 16;                  // bytes per row of q: ldmatrix rows hit distinct banks
-    static constexpr int kSmem = 1024 + kMain + kRows * (kQStride + 4) + kWarps * kStages * 8;
+    static constexpr int kSmem = 1024 + kRingBytes + kRows * (kQStride + 4) + kKeyWarps * kRows * 8 +
+                                 2 * kKeyWarps * kStages * 8;
     static constexpr int kSteps = D / 16;
+    static_assert(kAhead >= 1, "the ring has to hold a tile of the next unit beside the join");
+    static_assert(kJoinParts * kKeyWarps * kStageBytes == 4 * kKeyWarps * 16 * D, "a row tile's states fill the join stages");
 };
 
-__device__ __forceinline__ void put(void* out, int f32, size_t i, float v) {
+// Four consecutive values of a row.
+__device__ __forceinline__ void put4(void* out, int f32, size_t i, float4 v) {
     if (f32)
-        static_cast<float*>(out)[i] = v;
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = v;
     else
-        static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + i) =
+            make_uint2(pa::pack_bf16x2(v.x, v.y), pa::pack_bf16x2(v.z, v.w));
 }
 
-// A sequence's part of the step: its work in steps is units * steps.
+// A sequence's part of the call.
 struct Seq {
     int q0, n, ctx, steps, tiles;
-    __device__ __forceinline__ long long work(int heads) const { return (long long)heads * tiles * steps; }
+    __device__ __forceinline__ long long work(int heads) const {
+        return (long long)heads * tiles * (steps + kUnitCost);   // tiles is 0 where nothing is to be done
+    }
 };
 
 template <int kRows>
@@ -112,30 +132,59 @@ __device__ __forceinline__ Seq read_seq(const MultiArgs& a, int s, bool flag) {
     if (bad && flag) pa::set_status(a.status, PA_DEV_BAD_CONTEXT);
     r.ctx = ctx;
     r.tiles = (int)((((long long)r.n << a.log2_group) + kRows - 1) / kRows);
-    r.steps = r.n ? (ctx + kStep - 1) / kStep : 0;
+    r.steps = (ctx + kStep - 1) / kStep;
     return r;
 }
 
-template <int D, bool F8, int NT>
-struct Cols {                              // one warp's running state
-    float m[NT][2], l[NT][2];
-    float acc[NT][D / 16][4];
-    __device__ __forceinline__ void reset() {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            m[t][0] = m[t][1] = -INFINITY;
-            l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) acc[t][k][0] = acc[t][k][1] = acc[t][k][2] = acc[t][k][3] = 0.f;
-        }
-    }
+// The stretch of one unit that a block computes: steps st0 .. st0 + len - 1.
+struct Unit {
+    int q0, n, ctx, first, steps;          // first: position of new token 0
+    int kvh, row0, st0, len, seq, tile, last;   // last: the block that ends the unit
+    int valid;                             // 0: the share has ended
+    const uint64_t* words;                 // mask words of the sequence's tokens, or null
+    const int32_t* table;
 };
 
-// What a lane needs to mask a tile: the unit's rows and the sequence's lengths.
-struct Unit {
-    int ctx, first, n, row0;               // first: position of new token 0; row0: the tile's first row
-    const uint64_t* words;                 // mask words of the sequence's tokens, or null
+// Walks a block's share of the work, unit by unit.
+struct Walk {
+    long long pos, end, off, share;        // off: work of the sequence before pos
+    int seq;
+    Seq sq;
 };
+
+template <int kRows>
+__device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
+    u.valid = 0;
+    while (w.pos < w.end) {
+        while (w.off >= w.sq.work(a.n_kv_heads)) {
+            w.off -= w.sq.work(a.n_kv_heads);
+            w.sq = read_seq<kRows>(a, ++w.seq, false);
+        }
+        const int per = w.sq.steps + kUnitCost;
+        const int unit = (int)(w.off / per), o = (int)(w.off - (long long)unit * per);
+        const int take = (int)min((long long)(per - o), w.end - w.pos);
+        const int lo = max(0, o - kUnitCost), hi = max(0, o + take - kUnitCost);
+        u.last = (int)((w.pos - o + per - 1) / w.share);
+        w.pos += take;
+        w.off += take;
+        if (hi == lo) continue;            // the share ends within the unit's constant part
+        u.q0 = w.sq.q0;
+        u.n = w.sq.n;
+        u.ctx = w.sq.ctx;
+        u.first = w.sq.ctx - w.sq.n;
+        u.steps = w.sq.steps;
+        u.kvh = unit / w.sq.tiles;
+        u.tile = unit - u.kvh * w.sq.tiles;
+        u.row0 = u.tile * kRows;
+        u.st0 = lo;
+        u.len = hi - lo;
+        u.seq = w.seq;
+        u.words = a.tree_mask ? a.tree_mask + w.sq.q0 : nullptr;
+        u.table = a.block_tables + (size_t)w.seq * a.max_blocks;
+        u.valid = 1;
+        return;
+    }
+}
 
 __device__ __forceinline__ bool visible(const Unit& u, int log2_group, int row, int pos) {
     if (pos >= u.ctx) return false;
@@ -145,195 +194,210 @@ __device__ __forceinline__ bool visible(const Unit& u, int log2_group, int row, 
     return u.words ? (j < 64 && (u.words[i] >> j & 1ull)) : j <= i;
 }
 
+// One warp's running state: rows g and g + 8 of each row tile.
+template <int D, int MT>
+struct State {
+    float m[MT][2], l[MT][2];
+    float acc[MT][D / 8][4];
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            m[t][0] = m[t][1] = kNone;
+            l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) acc[t][d][0] = acc[t][d][1] = acc[t][d][2] = acc[t][d][3] = 0.f;
+        }
+    }
+};
+
 // Fold one tile (K at shared address ks, V at vs, positions t0 .. t0 + 15)
-// into the warp's state.
-template <int D, bool F8, int NT>
-__device__ __forceinline__ void fold_tile(Cols<D, F8, NT>& st, uint32_t ks, uint32_t vs, uint32_t qs,
-                                          const float* q_scale, int t0, const Unit& u, const MultiArgs& a, int lane,
-                                          const uint32_t (&qr)[NT <= 2 ? D / 16 : 1][NT][2]) {
-    using G = Geo<D, F8, NT>;
-    const int g = lane >> 2, t4 = lane & 3, mi = lane >> 3;
-    const int k_row = ((mi & 1) << 3) + (lane & 7), k_add = mi >> 1;
-    // q fragments of k-step kk: from registers (NT <= 2) or shared memory
-    auto q_frag = [&](int kk, uint32_t (&b)[NT][2]) {
-        if constexpr (NT <= 2) {
+// into the warp's state.  qs: the warp's rows of q; row_base: their place in
+// the unit; c[t][h]: score factor of rows g + 8 h.
+template <int D, bool F8, int MT>
+__device__ __forceinline__ void fold_tile(State<D, MT>& st, uint32_t ks, uint32_t vs, uint32_t qs, int row_base,
+                                          const float (&c)[MT][2], int t0, const Unit& u, int log2_group, int lane,
+                                          const uint32_t (&qr)[MT == 1 ? D / 16 : 1][4]) {
+    constexpr int kSlabBytes = kTile * 128, kQStride = 2 * D + 16, kSteps = D / 16;
+    const int g = lane >> 2, t4 = lane & 3;
+    // ldmatrix addresses.  K as B operand: keys (lane & 7) + 8 (lane >> 4), chunk + (lane >> 3 & 1);
+    // V (transposed) as B, and q as A: rows (lane & 7) + 8 (lane >> 3 & 1), chunk + (lane >> 4)
+    const int k_row = (lane & 7) + ((lane >> 4) << 3), k_add = (lane >> 3) & 1;
+    const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_add = lane >> 4;
+    float s[MT][2][4];                     // [row tile][keys 0-7, 8-15]: (g, 2 t4), (g, 2 t4 + 1), rows g + 8
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                b[t][0] = qr[kk][t][0];
-                b[t][1] = qr[kk][t][1];
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+    auto score = [&](int kk, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            uint32_t qa[4];
+            if constexpr (MT == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) qa[e] = qr[kk][e];
+            } else {
+                pa::ldsm4(qs + (16 * t + v_row) * kQStride + (2 * kk + v_add) * 16, qa);
             }
-        } else {
+            pa::mma16816<F8>(s[t][0], qa, b00, b01);
+            pa::mma16816<F8>(s[t][1], qa, b10, b11);
+        }
+    };
+    if constexpr (F8) {
+        // a chunk of 16 codes is one k-step; lane (g, t4) gets codes 4 t4 .. 4 t4 + 3 of key g
 #pragma unroll
-            for (int t = 0; t < NT; t += 2) {
-                uint32_t r[4];
-                pa::ldsm4(qs + (8 * t + ((mi >> 1) << 3) + (lane & 7)) * G::kQStride + (2 * kk + (mi & 1)) * 16, r);
-                b[t][0] = r[0];
-                b[t][1] = r[1];
-                b[t + 1][0] = r[2];
-                b[t + 1][1] = r[3];
+        for (int j = 0; j < kSteps / 2; ++j) {
+            uint32_t r[4], b[4][2];
+            pa::ldsm4(ks + pa::swz128(k_row, 2 * j + k_add), r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pa::e4m3x4_to_f16x4(r[e], b[e][0], b[e][1]);
+            score(2 * j, b[0][0], b[0][1], b[2][0], b[2][1]);
+            score(2 * j + 1, b[1][0], b[1][1], b[3][0], b[3][1]);
+        }
+    } else {
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) {
+            uint32_t r[4];
+            pa::ldsm4(ks + (kk >> 2) * kSlabBytes + pa::swz128(k_row, 2 * (kk & 3) + k_add), r);
+            score(kk, r[0], r[1], r[2], r[3]);
+        }
+    }
+    const bool tail = t0 + kTile > u.first;            // some row may not see some position
+    if (tail) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!visible(u, log2_group, row_base + 16 * t + g + 8 * (e >> 1), t0 + 8 * n + 2 * t4 + (e & 1)))
+                        s[t][n][e] = -INFINITY;
+    }
+    // how far the tile's scores rise above the running maxima
+    float over = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float top = fmaxf(fmaxf(s[t][0][2 * h], s[t][0][2 * h + 1]), fmaxf(s[t][1][2 * h], s[t][1][2 * h + 1]));
+            over = fmaxf(over, fmaf(top, c[t][h], -st.m[t][h]));
+        }
+    if (__any_sync(0xffffffffu, over > kRaise)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float top = fmaxf(fmaxf(s[t][0][2 * h], s[t][0][2 * h + 1]), fmaxf(s[t][1][2 * h], s[t][1][2 * h + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float m = fmaxf(st.m[t][h], top * c[t][h]);
+                const float f = pa::exp2_approx(st.m[t][h] - m);
+                st.m[t][h] = m;
+                st.l[t][h] *= f;
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                    st.acc[t][d][2 * h] *= f;
+                    st.acc[t][d][2 * h + 1] *= f;
+                }
+            }
+    }
+    // weights as the A operand: bf16 in two terms (a relative 2^-16), f16 times 2^7 (2^-11)
+    uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float p0 = pa::exp2_approx(fmaf(s[t][n][2 * h], c[t][h], -st.m[t][h]));
+                const float p1 = pa::exp2_approx(fmaf(s[t][n][2 * h + 1], c[t][h], -st.m[t][h]));
+                st.l[t][h] += p0 + p1;
+                if constexpr (F8) {
+                    ph[t][2 * n + h] = pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale);
+                } else {
+                    const uint32_t w = pa::pack_bf16x2(p0, p1);
+                    const float2 f = pa::bf16x2_to_float2(w);
+                    ph[t][2 * n + h] = w;
+                    pl[t][2 * n + h] = pa::pack_bf16x2(p0 - f.x, p1 - f.y);
+                }
+            }
+    // O += P . V; V rows past the context are zeroed (0 * NaN)
+    const int nv = u.ctx - t0;
+    auto values = [&](bool masked, uint32_t mlo, uint32_t mhi) {
+#pragma unroll
+        for (int j = 0; j < D / (F8 ? 32 : 16); ++j) {
+            uint32_t r[4];
+            if constexpr (F8) {
+                // r[0], r[1]: keys 2 t4, 2 t4 + 1 and 2 t4 + 8, + 9, codes 2 g and 2 g + 1 of chunk
+                // 2 j; r[2], r[3]: of chunk 2 j + 1.  Paired by code, they are the products of the
+                // chunk's even and odd columns.
+                pa::ldsm4_trans(vs + pa::swz128(v_row, 2 * j + v_add), r);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t b0[2], b1[2];
+                    pa::e4m3x4_to_f16x4(pa::byte_perm(r[2 * x], 0x3120u), b0[0], b0[1]);
+                    pa::e4m3x4_to_f16x4(pa::byte_perm(r[2 * x + 1], 0x3120u), b1[0], b1[1]);
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd) {
+                        if (masked) {
+                            b0[odd] &= mlo;
+                            b1[odd] &= mhi;
+                        }
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+                            pa::mma16816<true>(st.acc[t][2 * (2 * j + x) + odd], ph[t], b0[odd], b1[odd]);
+                    }
+                }
+            } else {
+                pa::ldsm4_trans(vs + (j >> 2) * kSlabBytes + pa::swz128(v_row, 2 * (j & 3) + v_add), r);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t b0 = masked ? r[2 * x] & mlo : r[2 * x];
+                    const uint32_t b1 = masked ? r[2 * x + 1] & mhi : r[2 * x + 1];
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        pa::mma16816<false>(st.acc[t][2 * j + x], ph[t], b0, b1);
+                        pa::mma16816<false>(st.acc[t][2 * j + x], pl[t], b0, b1);
+                    }
+                }
             }
         }
     };
-    float s[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-    if constexpr (F8) {
-#pragma unroll
-        for (int j = 0; j < G::kSteps / 2; ++j) {
-            uint32_t r[4], af[4], b[NT][2];
-            pa::ldsm4(ks + pa::swz128(k_row, 2 * j + k_add), r);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                pa::e4m3x4_to_f16x4(r[2 * h], af[0], af[2]);
-                pa::e4m3x4_to_f16x4(r[2 * h + 1], af[1], af[3]);
-                q_frag(2 * j + h, b);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) pa::mma16816<true>(s[t], af, b[t][0], b[t][1]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int kk = 0; kk < G::kSteps; ++kk) {
-            uint32_t af[4], b[NT][2];
-            pa::ldsm4(ks + (kk >> 2) * G::kSlabBytes + pa::swz128(k_row, 2 * (kk & 3) + k_add), af);
-            q_frag(kk, b);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) pa::mma16816<false>(s[t], af, b[t][0], b[t][1]);
-        }
-    }
-    // s[t][0], [1]: position g, columns 2 t4 and 2 t4 + 1; [2], [3]: position g + 8
-    bool raise = false;
-    const bool tail = t0 + kTile > u.first;            // some row may not see some position
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        float c0 = a.scale_log2, c1 = a.scale_log2;
-        if constexpr (F8) {
-            const float2 c = *reinterpret_cast<const float2*>(q_scale + 8 * t + 2 * t4);
-            c0 = c.x;
-            c1 = c.y;
-        }
-        s[t][0] *= c0;
-        s[t][1] *= c1;
-        s[t][2] *= c0;
-        s[t][3] *= c1;
-        if (tail) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!visible(u, a.log2_group, 8 * t + 2 * t4 + (e & 1), t0 + g + (e >> 1) * 8)) s[t][e] = -INFINITY;
-        }
-        raise |= fmaxf(s[t][0], s[t][2]) > st.m[t][0] + kRaise || fmaxf(s[t][1], s[t][3]) > st.m[t][1] + kRaise;
-    }
-    if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float b0 = fmaxf(s[t][0], s[t][2]), b1 = fmaxf(s[t][1], s[t][3]);
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
-                b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
-            }
-            const float n0 = fmaxf(st.m[t][0], b0), n1 = fmaxf(st.m[t][1], b1);
-            // a column that has seen nothing yet has sums of zero, whatever the factor
-            const float f0 = n0 == -INFINITY ? 1.f : pa::exp2_approx(st.m[t][0] - n0);
-            const float f1 = n1 == -INFINITY ? 1.f : pa::exp2_approx(st.m[t][1] - n1);
-            st.m[t][0] = n0;
-            st.m[t][1] = n1;
-            st.l[t][0] *= f0;
-            st.l[t][1] *= f1;
-#pragma unroll
-            for (int k = 0; k < G::kSteps; ++k) {
-                st.acc[t][k][0] *= f0;
-                st.acc[t][k][1] *= f1;
-                st.acc[t][k][2] *= f0;
-                st.acc[t][k][3] *= f1;
-            }
-        }
-    }
-    // weights as the B operand: bf16 in two terms (a relative 2^-16), f16 times 2^7 (2^-11)
-    uint32_t bh[NT][2], bl[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const float m0 = st.m[t][0] == -INFINITY ? 0.f : st.m[t][0], m1 = st.m[t][1] == -INFINITY ? 0.f : st.m[t][1];
-        const float p0 = pa::exp2_approx(s[t][0] - m0), p1 = pa::exp2_approx(s[t][1] - m1);
-        const float p2 = pa::exp2_approx(s[t][2] - m0), p3 = pa::exp2_approx(s[t][3] - m1);
-        st.l[t][0] += p0 + p2;
-        st.l[t][1] += p1 + p3;
-        if constexpr (F8) {
-            bh[t][0] = pa::transpose8(pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale));
-            bh[t][1] = pa::transpose8(pa::pack_f16x2(p2 * kWeightScale, p3 * kWeightScale));
-        } else {
-            const uint32_t h01 = pa::pack_bf16x2(p0, p1), h23 = pa::pack_bf16x2(p2, p3);
-            const float2 f01 = pa::bf16x2_to_float2(h01), f23 = pa::bf16x2_to_float2(h23);
-            bh[t][0] = pa::transpose8(h01);
-            bh[t][1] = pa::transpose8(h23);
-            bl[t][0] = pa::transpose8(pa::pack_bf16x2(p0 - f01.x, p1 - f01.y));
-            bl[t][1] = pa::transpose8(pa::pack_bf16x2(p2 - f23.x, p3 - f23.y));
-        }
-    }
-    // O^T += V^T . P^T; V rows past the context are zeroed (0 * NaN)
-    const int nv = u.ctx - t0;
-    uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
     if (nv < kTile) {
-        const int t = 2 * t4;
-        mlo = (t < nv ? 0x0000ffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
-        mhi = (t + 8 < nv ? 0x0000ffffu : 0u) | (t + 9 < nv ? 0xffff0000u : 0u);
-    }
-    if constexpr (F8) {
-#pragma unroll
-        for (int j = 0; j < G::kSteps / 2; ++j) {
-            uint32_t r[4];
-            pa::ldsm4_trans(vs + pa::swz128(k_row, 2 * j + k_add), r);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t af[4];
-                pa::e4m3x4_to_f16x4(pa::byte_perm(r[2 * h], 0x3120u), af[0], af[1]);
-                pa::e4m3x4_to_f16x4(pa::byte_perm(r[2 * h + 1], 0x3120u), af[2], af[3]);
-                af[0] &= mlo;
-                af[1] &= mlo;
-                af[2] &= mhi;
-                af[3] &= mhi;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) pa::mma16816<true>(st.acc[t][2 * j + h], af, bh[t][0], bh[t][1]);
-            }
-        }
+        const int k = 2 * t4;
+        values(true, (k < nv ? 0x0000ffffu : 0u) | (k + 1 < nv ? 0xffff0000u : 0u),
+               (k + 8 < nv ? 0x0000ffffu : 0u) | (k + 9 < nv ? 0xffff0000u : 0u));
     } else {
-        const int v_row = ((mi >> 1) << 3) + (lane & 7), v_add = mi & 1;
-#pragma unroll
-        for (int k = 0; k < G::kSteps; ++k) {
-            uint32_t af[4];
-            pa::ldsm4_trans(vs + (k >> 2) * G::kSlabBytes + pa::swz128(v_row, 2 * (k & 3) + v_add), af);
-            af[0] &= mlo;
-            af[1] &= mlo;
-            af[2] &= mhi;
-            af[3] &= mhi;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                pa::mma16816<false>(st.acc[t][k], af, bh[t][0], bh[t][1]);
-                pa::mma16816<false>(st.acc[t][k], af, bl[t][0], bl[t][1]);
-            }
-        }
+        values(false, 0u, 0u);
     }
 }
 
-template <int D, bool F8, int NT>
-__global__ void __launch_bounds__(kThreads, Geo<D, F8, NT>::kBlocksPerSm)
+template <int D, bool F8, int MT, int RG>
+__global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, RG>::kBlocksPerSm)
     multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const MultiArgs a) {
-    using G = Geo<D, F8, NT>;
-    constexpr int kRows = G::kRows, kStages = G::kStages;
+    using G = Geo<D, F8, MT, RG>;
+    constexpr int kRows = G::kRows, kStages = G::kStages, kThreads = G::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* qsm = ring + G::kMain;                               // [kRows][kQStride]
+    uint8_t* qsm = ring + G::kRingBytes;                          // [kRows][kQStride]
     float* q_scale = reinterpret_cast<float*>(qsm + kRows * G::kQStride);   // FP8: score factor per row
-    uint64_t* bars = reinterpret_cast<uint64_t*>(q_scale + kRows);
-    __shared__ long long sums[kWarps];
-    __shared__ long long where_off;
-    __shared__ int where_seq;
+    float2* stats = reinterpret_cast<float2*>(q_scale + kRows);   // [key warp][row]: maximum and sum
+    uint64_t* full = reinterpret_cast<uint64_t*>(stats + kKeyWarps * kRows);   // [key warp][stage]
+    uint64_t* empty = full + kKeyWarps * kStages;                 // RG > 1: both groups are done with it
+    __shared__ long long sums[kKeyWarps * RG];
+    // Thread 0 walks the share two units ahead; a unit's place is free again
+    // two barriers after its join.
+    __shared__ Walk walk;
+    __shared__ Unit units[4];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kw = warp % kKeyWarps, rg = warp / kKeyWarps;
     const int B = 1 << a.log2_block, heads = a.n_kv_heads;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * kStages; ++i) pa::mbar_init(&bars[i], 1);
+        for (int i = 0; i < kKeyWarps * kStages; ++i) {
+            pa::mbar_init(&full[i], 1);
+            pa::mbar_init(&empty[i], RG);
+        }
         pa::fence_mbar_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -353,85 +417,75 @@ __global__ void __launch_bounds__(kThreads, Geo<D, F8, NT>::kBlocksPerSm)
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     long long total = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kKeyWarps * RG; ++w) {
         if (w < warp) upto += sums[w];
         total += sums[w];
     }
     long long share = (total + gridDim.x - 1) / gridDim.x;
     share = share < kMinShare ? kMinShare : share;
     const long long begin = share * blockIdx.x;
-    long long end = begin + share;
-    end = end > total ? total : end;
     if (threadIdx.x == 0) a.pieces[blockIdx.x].x = -1;
     if (begin >= total) return;
-    if (begin >= upto - mine && begin < upto) {                  // one thread's range holds the first step
+    if (begin >= upto - mine && begin < upto) {                  // one thread's range holds the share's start
         long long off = begin - (upto - mine);
-        for (int s = s_lo;; ++s) {
-            const long long w = read_seq<kRows>(a, s, false).work(heads);
-            if (off < w) {
-                where_seq = s;
-                where_off = off;
-                break;
-            }
-            off -= w;
-        }
-    }
-    __syncthreads();
-    int seq = where_seq;
-    long long off = where_off;                                   // steps of the sequence before the current one
-    Seq sq = read_seq<kRows>(a, seq, false);
-
-    const uint64_t policy = pa::l2_evict_first_policy();
-    uint64_t* wbars = bars + warp * kStages;
-    const uint32_t wring = pa::smem_addr(ring) + warp * kStages * G::kStageBytes;
-    const uint32_t qs = pa::smem_addr(qsm);
-    int used = 0;                                                // stages this warp consumed in earlier segments
-    Cols<D, F8, NT> st;
-
-    for (long long cur = begin; cur < end;) {
+        int s = s_lo;
+        Seq sq = read_seq<kRows>(a, s, false);
         while (off >= sq.work(heads)) {
             off -= sq.work(heads);
-            sq = read_seq<kRows>(a, ++seq, false);
+            sq = read_seq<kRows>(a, ++s, false);
         }
-        const int unit = (int)(off / sq.steps), st0 = (int)(off - (long long)unit * sq.steps);
-        const int len = (int)min((long long)(sq.steps - st0), end - cur);
-        const int kvh = unit / sq.tiles, tile = unit - kvh * sq.tiles;
-        Unit u;
-        u.ctx = sq.ctx;
-        u.n = sq.n;
-        u.first = sq.ctx - sq.n;
-        u.row0 = tile * kRows;
-        u.words = a.tree_mask ? a.tree_mask + sq.q0 : nullptr;
-        const int32_t* table = a.block_tables + (size_t)seq * a.max_blocks;
+        walk.pos = begin;
+        walk.end = min(total, begin + share);
+        walk.off = off;
+        walk.share = share;
+        walk.seq = s;
+        walk.sq = sq;
+        next_unit<kRows>(walk, units[0], a);
+        next_unit<kRows>(walk, units[1], a);
+    }
+    __syncthreads();
+    if (!units[0].valid) return;                                 // a share that ends in a unit's constant part
 
-        // ---- this warp's tiles: positions (st0 + k) * 64 + 16 warp, k < mine_k ----
-        const int base = st0 * kStep + warp * kTile;
-        const int mine_k = base >= u.ctx ? 0 : min(len, (u.ctx - base + kStep - 1) / kStep);
-        // table entries of 32 tiles at a time, one per lane, the next 32 fetched ahead
-        auto fetch = [&](int k, int& e0, int& e1) {
-            e0 = e1 = 0;
-            if (k < mine_k) {
-                const int t0 = base + k * kStep;
-                e0 = table[t0 >> a.log2_block];
-                if (B < kTile && t0 + B < u.ctx) e1 = table[(t0 >> a.log2_block) + 1];
-            }
-        };
-        int e0, e1, f0, f1;
-        fetch(lane, e0, e1);
-        fetch(32 + lane, f0, f1);
-        auto issue = [&](int k) {                                // whole warp
-            if (k && (k & 31) == 0) {
-                e0 = f0;
-                e1 = f1;
-                fetch(k + 32 + lane, f0, f1);
-            }
-            int b0 = __shfl_sync(0xffffffffu, e0, k & 31), b1 = __shfl_sync(0xffffffffu, e1, k & 31);
-            if (lane == 0) {
-                const int t0 = base + k * kStep;
+    const uint64_t policy = pa::l2_evict_first_policy();
+    const uint32_t ring0 = pa::smem_addr(ring) + kw * G::kStageBytes;
+    const uint32_t qs = pa::smem_addr(qsm) + rg * (16 * MT) * G::kQStride;
+    uint64_t* wfull = full + kw * kStages;
+    uint64_t* wempty = empty + kw * kStages;
+    auto stage_at = [&](int stage) { return ring0 + stage * (kKeyWarps * G::kStageBytes); };
+
+    // A warp's tile k of a unit holds positions (st0 + k) * 64 + 16 kw on.  Its
+    // table entries come 32 tiles at a time, one per lane, the next 32 ahead.
+    auto fetch = [&](const Unit& u, int k, int& e0, int& e1) {
+        e0 = e1 = 0;
+        const int t0 = (u.st0 + k) * kStep + kw * kTile;
+        if (k < u.len && t0 < u.ctx) {
+            e0 = u.table[t0 >> a.log2_block];
+            if (B < kTile && t0 + B < u.ctx) e1 = u.table[(t0 >> a.log2_block) + 1];
+        }
+    };
+    int e0 = 0, e1 = 0, f0 = 0, f1 = 0;
+    int used = 0;                                                 // tiles of the ring before the current unit's
+    auto issue = [&](const Unit& u, int k) {                      // whole warp of group 0
+        if (k && (k & 31) == 0) {
+            e0 = f0;
+            e1 = f1;
+            fetch(u, k + 32 + lane, f0, f1);
+        }
+        const int b0 = __shfl_sync(0xffffffffu, e0, k & 31), b1 = __shfl_sync(0xffffffffu, e1, k & 31);
+        if (lane == 0) {
+            const int at = used + k, stage = at % kStages;
+            uint64_t* bar = &wfull[stage];
+            bool free = true;
+            if (RG > 1 && at >= kStages)
+                free = pa::mbar_wait_bounded(&wempty[stage], ((at / kStages) - 1) & 1, kMaxProbes);
+            const int t0 = (u.st0 + k) * kStep + kw * kTile;
+            if (!free) {
+                pa::set_status(a.status, PA_DEV_WAIT_TIMEOUT);    // nothing is issued: its readers give up too
+            } else if (t0 >= u.ctx) {
+                pa::mbar_arrive(bar);                             // no such tile: the stage goes by empty
+            } else {
                 const int box = B < kTile ? B : kTile, boxes = (B < kTile && t0 + B < u.ctx) ? 2 : 1;
-                const int stage = (used + k) % kStages;
-                uint64_t* bar = &wbars[stage];
-                const uint32_t dst = wring + stage * G::kStageBytes;
+                const uint32_t dst = stage_at(stage);
                 pa::mbar_arrive_expect_tx(bar, (uint32_t)(2 * G::kSlabs * boxes * box * 128));
                 for (int r = 0; r < boxes; ++r) {
                     int blk = r ? b1 : b0;
@@ -439,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, F8, NT>::kBlocksPerSm)
                         pa::set_status(a.status, PA_DEV_BAD_BLOCK_ID);
                         blk = 0;
                     }
-                    const int row = (blk * heads + kvh) * B + (r ? 0 : t0 & (B - 1));
+                    const int row = (blk * heads + u.kvh) * B + (r ? 0 : t0 & (B - 1));
 #pragma unroll
                     for (int h = 0; h < G::kSlabs; ++h) {
                         const uint32_t d = dst + h * G::kSlabBytes + r * box * 128;
@@ -448,24 +502,30 @@ __global__ void __launch_bounds__(kThreads, Geo<D, F8, NT>::kBlocksPerSm)
                     }
                 }
             }
-        };
-        for (int k = 0; k < kStages; ++k)
-            if (k < mine_k) issue(k);
-
-        // ---- q of the unit's rows to shared memory, 8 elements per thread ----
-        constexpr int kLanesQ = D / 8;
-        for (int x = threadIdx.x; x < kRows * kLanesQ; x += kThreads) {
-            const int r = x / kLanesQ, c = x % kLanesQ;
+        }
+    };
+    // q of a unit's rows, 8 elements per thread and piece: loaded, then stored
+    constexpr int kLanesQ = D / 8, kQPer = kRows * kLanesQ / kThreads;
+    auto load_q = [&](const Unit& u, uint4 (&v)[kQPer]) {
+#pragma unroll
+        for (int x = 0; x < kQPer; ++x) {
+            const int r = (x * kThreads + threadIdx.x) / kLanesQ, c = threadIdx.x % kLanesQ;
             const int row = u.row0 + r, i = row >> a.log2_group;
-            uint4 v = make_uint4(0, 0, 0, 0);
+            v[x] = make_uint4(0, 0, 0, 0);
             if (i < u.n)
-                v = *reinterpret_cast<const uint4*>(
-                    a.q + ((size_t)(sq.q0 + i) * a.n_q_heads + (kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))) * D +
-                    8 * c);
+                v[x] = *reinterpret_cast<const uint4*>(
+                    a.q + ((size_t)(u.q0 + i) * a.n_q_heads + (u.kvh << a.log2_group) +
+                           (row & ((1 << a.log2_group) - 1))) * D + 8 * c);
+        }
+    };
+    auto store_q = [&](const uint4 (&v)[kQPer]) {
+#pragma unroll
+        for (int x = 0; x < kQPer; ++x) {
+            const int r = (x * kThreads + threadIdx.x) / kLanesQ, c = threadIdx.x % kLanesQ;
             uint8_t* dst = qsm + r * G::kQStride;
+            const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
             if constexpr (F8) {
                 // f16 after a power of two per row that brings its largest element into [2^14, 2^15)
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 float f[8], top = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -479,122 +539,181 @@ __global__ void __launch_bounds__(kThreads, Geo<D, F8, NT>::kBlocksPerSm)
                 int eb = (__float_as_int(top) >> 23) & 0xff;
                 eb = eb < 14 ? 14 : (eb > 254 ? 254 : eb);
                 const float up = __int_as_float((268 - eb) << 23);
-                if (c == 0) q_scale[r] = a.scale_log2 / up;
-                // within 16 elements, place 2 j holds d = 4 j and place 2 j + 8 holds
-                // d = 4 j + 2 (pairs): the order in which ldmatrix hands out K's codes
+                if (c == 0) q_scale[r] = fmaxf(a.scale_log2 / up, 1e-37f);   // never 0: masked scores stay -inf
+                const float by = up * a.q_sign;
+                // within 16 elements, word t4 holds d = 4 t4, 4 t4 + 1 and word t4 + 4 the next
+                // two: the order in which ldmatrix hands out K's codes
                 uint32_t* p = reinterpret_cast<uint32_t*>(dst + (c >> 1) * 32);
                 const int j = (c & 1) * 2;
-                p[j] = pa::pack_f16x2(f[0] * up, f[1] * up);
-                p[j + 4] = pa::pack_f16x2(f[2] * up, f[3] * up);
-                p[j + 1] = pa::pack_f16x2(f[4] * up, f[5] * up);
-                p[j + 5] = pa::pack_f16x2(f[6] * up, f[7] * up);
+                p[j] = pa::pack_f16x2(f[0] * by, f[1] * by);
+                p[j + 4] = pa::pack_f16x2(f[2] * by, f[3] * by);
+                p[j + 1] = pa::pack_f16x2(f[4] * by, f[5] * by);
+                p[j + 5] = pa::pack_f16x2(f[6] * by, f[7] * by);
             } else {
-                *reinterpret_cast<uint4*>(dst + 16 * c) = v;
+                const uint32_t flip = a.q_sign < 0.f ? 0x80008000u : 0u, keep = a.q_sign == 0.f ? 0u : 0xffffffffu;
+                *reinterpret_cast<uint4*>(dst + 16 * c) =
+                    make_uint4((w[0] ^ flip) & keep, (w[1] ^ flip) & keep, (w[2] ^ flip) & keep, (w[3] ^ flip) & keep);
             }
         }
+    };
+
+    uint4 qv[kQPer];
+    if (rg == 0) {
+        fetch(units[0], lane, e0, e1);
+        fetch(units[0], 32 + lane, f0, f1);
+        for (int k = 0; k < G::kAhead; ++k)
+            if (k < units[0].len) issue(units[0], k);
+    }
+    load_q(units[0], qv);
+    for (int nth = 0;; ++nth) {
+        const Unit& u = units[nth & 3];
+        const Unit& next = units[(nth + 1) & 3];
+        store_q(qv);
         __syncthreads();
-        uint32_t qr[NT <= 2 ? G::kSteps : 1][NT][2];
-        if constexpr (NT <= 2) {
+        const int len = u.len, ctx = u.ctx, base = u.st0 * kStep + kw * kTile;
+        const bool more = next.valid;
+        if (rg == 0)
+            for (int k = G::kAhead; k < kStages; ++k)
+                if (k < len) issue(u, k);
+        int n0 = 0, n1 = 0;
+        if (more && rg == 0) fetch(next, lane, n0, n1);
+        if (threadIdx.x == 0) next_unit<kRows>(walk, units[(nth + 2) & 3], a);
+        __syncwarp();
+        uint32_t qr[MT == 1 ? G::kSteps : 1][4];
+        if constexpr (MT == 1) {
 #pragma unroll
             for (int kk = 0; kk < G::kSteps; ++kk)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    pa::ldsm2(qs + (8 * t + (lane & 7)) * G::kQStride + (2 * kk + ((lane >> 3) & 1)) * 16, qr[kk][t][0],
-                              qr[kk][t][1]);
+                pa::ldsm4(qs + ((lane & 7) + (((lane >> 3) & 1) << 3)) * G::kQStride + (2 * kk + (lane >> 4)) * 16, qr[kk]);
         }
+        float c[MT][2];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) c[t][h] = F8 ? q_scale[rg * 16 * MT + 16 * t + (lane >> 2) + 8 * h] : a.scale_log2;
 
+        State<D, MT> st;
         st.reset();
         bool landed = true;
-        for (int k = 0; k < mine_k; ++k) {
-            const int stage = (used + k) % kStages;
-            if (!__all_sync(0xffffffffu, pa::mbar_wait_bounded(&wbars[stage], ((used + k) / kStages) & 1, kMaxProbes))) {
+        for (int k = 0; k < len; ++k) {
+            const int at = used + k, stage = at % kStages;
+            if (!__all_sync(0xffffffffu, pa::mbar_wait_bounded(&wfull[stage], (at / kStages) & 1, kMaxProbes))) {
                 // give up: nothing more is issued, and the copies in flight are waited for, each within the limit
                 if (lane == 0) pa::set_status(a.status, PA_DEV_WAIT_TIMEOUT);
-                const int issued = min(mine_k, k + kStages);
+                const int issued = min(len, k + kStages);
                 for (int j = k; j < issued; ++j)
-                    pa::mbar_wait_bounded(&wbars[(used + j) % kStages], ((used + j) / kStages) & 1, kMaxProbes);
+                    pa::mbar_wait_bounded(&wfull[(used + j) % kStages], ((used + j) / kStages) & 1, kMaxProbes);
                 landed = false;
                 break;
             }
-            const uint32_t ks = wring + stage * G::kStageBytes;
-            fold_tile<D, F8, NT>(st, ks, ks + G::kTileBytes, qs, q_scale, base + k * kStep, u, a, lane, qr);
+            const int t0 = base + k * kStep;
+            if (t0 < ctx) {
+                const uint32_t ks = stage_at(stage);
+                fold_tile<D, F8, MT>(st, ks, ks + G::kTileBytes, qs, rg * 16 * MT, c, t0, u, a.log2_group, lane, qr);
+            }
             __syncwarp();
-            if (k + kStages < mine_k) issue(k + kStages);
-        }
-        used += mine_k;
-
-        // ---- join the warps' states (the exact block merge) ----
-        if (!__syncthreads_and(landed)) return;
-        float* um = reinterpret_cast<float*>(ring);              // [warp][row]
-        float* ul = um + kWarps * kRows;
-        float* uu = ul + kWarps * kRows;                         // [warp][row][kUStride]
-        const int g = lane >> 2, t4 = lane & 3;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-                st.l[t][0] += __shfl_xor_sync(0xffffffffu, st.l[t][0], o);
-                st.l[t][1] += __shfl_xor_sync(0xffffffffu, st.l[t][1], o);
-            }
-            const int r0 = warp * kRows + 8 * t + 2 * t4;
-            if (g == 0) {
-                um[r0] = st.m[t][0];
-                um[r0 + 1] = st.m[t][1];
-                ul[r0] = st.l[t][0];
-                ul[r0 + 1] = st.l[t][1];
-            }
-#pragma unroll
-            for (int k = 0; k < G::kSteps; ++k) {
-                float* p = uu + r0 * G::kUStride + 16 * k + (F8 ? 2 * g : g);
-                constexpr int kNext = F8 ? 1 : 8;
-                p[0] = st.acc[t][k][0];
-                p[G::kUStride] = st.acc[t][k][1];
-                p[kNext] = st.acc[t][k][2];
-                p[G::kUStride + kNext] = st.acc[t][k][3];
-            }
-        }
-        __syncthreads();
-        const long long unit_begin = cur - st0;                  // in steps of the whole call
-        const bool whole = len == sq.steps;
-        const int slot = 2 * blockIdx.x + (unit_begin >= begin ? 1 : 0);
-        for (int x = threadIdx.x; x < kRows * D; x += kThreads) {
-            const int r = x / D, d = x % D;
-            const int row = u.row0 + r, i = row >> a.log2_group;
-            if (i >= u.n) break;                                 // rows come in order
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, um[w * kRows + r]);
-            float Z = 0.f, U = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                // a warp that saw nothing adds its zeros as they are (or the NaN of a score)
-                const float f = um[w * kRows + r] == -INFINITY ? 1.f : pa::exp2_approx(um[w * kRows + r] - M);
-                Z += f * ul[w * kRows + r];
-                U += f * uu[(w * kRows + r) * G::kUStride + d];
-            }
-            if (whole) {
-                const size_t o = ((size_t)(sq.q0 + i) * a.n_q_heads + (kvh << a.log2_group) +
-                                  (row & ((1 << a.log2_group) - 1))) * D + d;
-                put(a.out, a.out_f32, o, Z == 0.f ? 0.f : U * a.v_scale / Z);
+            if constexpr (RG == 1) {
+                if (k + kStages < len) issue(u, k + kStages);
             } else {
-                a.part_u[((size_t)slot * kRows + r) * D + d] = U;
-                if (d == 0) {
-                    a.part_m[slot * kRows + r] = M;
-                    a.part_z[slot * kRows + r] = Z;
+                if (lane == 0) pa::mbar_arrive(&wempty[stage]);
+                // the stage before: the other group is done with it by now, or nearly
+                if (rg == 0 && k && k - 1 + kStages < len) issue(u, k - 1 + kStages);
+            }
+        }
+        used += len;
+        if (!__syncthreads_and(landed)) return;                   // every tile of the unit is consumed
+        if (more && rg == 0) {
+            e0 = n0;
+            e1 = n1;
+            fetch(next, 32 + lane, f0, f1);
+            for (int k = 0; k < G::kAhead; ++k)
+                if (k < next.len) issue(next, k);
+        }
+        if (more) load_q(next, qv);
+
+        // ---- join the key warps' states (the exact block merge), a row tile of each group at a time ----
+        const int g = lane >> 2, t4 = lane & 3;
+        auto join_row = [&](int group, int w, int r) {            // fp32 row r (0..15) of key warp w
+            const int part = group * G::kJoinParts + (F8 ? r >> 3 : 0), rows = F8 ? 8 : 16;
+            const int stage = (used + G::kAhead + part) % kStages;
+            return reinterpret_cast<float*>(ring + stage * (kKeyWarps * G::kStageBytes)) + (w * rows + (r & (rows - 1))) * D;
+        };
+        auto spread = [](int r) { return ((r & 1) << 4) | ((r & 2) << 2); };   // rows to distinct banks
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if (t) __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float l = st.l[t][h];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int r = g + 8 * h;
+                if (t4 == 0) stats[kw * kRows + (rg * MT + t) * 16 + r] = make_float2(st.m[t][h], l);
+                float* row = join_row(rg, kw, r);
+                if constexpr (F8) {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x)
+                        *reinterpret_cast<float4*>(row + ((16 * x + 4 * t4) ^ spread(r))) =
+                            make_float4(st.acc[t][2 * x][2 * h], st.acc[t][2 * x + 1][2 * h],
+                                        st.acc[t][2 * x][2 * h + 1], st.acc[t][2 * x + 1][2 * h + 1]);
+                } else {
+#pragma unroll
+                    for (int d = 0; d < D / 8; ++d)
+                        *reinterpret_cast<float2*>(row + ((8 * d + 2 * t4) ^ spread(r))) =
+                            make_float2(st.acc[t][d][2 * h], st.acc[t][d][2 * h + 1]);
                 }
             }
+            __syncthreads();
+            const bool whole = len == u.steps;
+            const int slot = 2 * blockIdx.x + (u.st0 == 0 ? 1 : 0);
+            for (int x = threadIdx.x; x < RG * 16 * (D / 4); x += kThreads) {
+                const int group = x / (16 * (D / 4)), r = x / (D / 4) % 16, d = x % (D / 4) * 4;
+                const int in_unit = (group * MT + t) * 16 + r;
+                const int row = u.row0 + in_unit, i = row >> a.log2_group;
+                if (i >= u.n) continue;
+                float2 ml[kKeyWarps];
+                float M = kNone;
+#pragma unroll
+                for (int w = 0; w < kKeyWarps; ++w) {
+                    ml[w] = stats[w * kRows + in_unit];
+                    M = fmaxf(M, ml[w].x);
+                }
+                float Z = 0.f;
+                float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kKeyWarps; ++w) {
+                    const float f = pa::exp2_approx(ml[w].x - M);
+                    const float4 v = *reinterpret_cast<const float4*>(join_row(group, w, r) + (d ^ spread(r)));
+                    Z += f * ml[w].y;
+                    U.x += f * v.x;
+                    U.y += f * v.y;
+                    U.z += f * v.z;
+                    U.w += f * v.w;
+                }
+                if (whole) {
+                    const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+                    put4(a.out, a.out_f32,
+                         ((size_t)(u.q0 + i) * a.n_q_heads + (u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))) * D + d,
+                         make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
+                } else {
+                    const size_t at = (size_t)slot * kRows + in_unit;
+                    *reinterpret_cast<float4*>(a.part_u + at * D + d) = U;
+                    if (d == 0) {
+                        a.part_m[at] = M;
+                        a.part_z[at] = Z;
+                    }
+                }
+            }
+            if (t == 0 && !whole && u.st0 == 0 && threadIdx.x == 0)   // this block begins the unit
+                a.pieces[blockIdx.x] = make_int4(u.seq, u.kvh, u.tile, u.last);
         }
-        if (!whole && (slot & 1) && threadIdx.x == 0)            // this block began the unit
-            a.pieces[blockIdx.x] = make_int4(seq, kvh, tile, (int)((unit_begin + sq.steps - 1) / share));
-        cur += len;
-        off += len;
-        __syncthreads();
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the ring goes back to TMA
+        if (!more) return;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the join's stages go back to TMA (after the barrier above)
     }
 }
 
-// out of the units that several blocks share: pieces of block b (its second
-// slot) and of blocks b + 1 .. last (their first), in that order.
+// out of the units that several blocks share: the pieces of block b, which
+// begins the unit (its second slot), and of blocks b + 1 .. last (their
+// first), in that order.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a, int rows) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -603,23 +722,28 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
     if (p.x < 0) return;
     const int q0 = a.query_start[p.x], n = a.query_start[p.x + 1] - q0;
     const int G = 1 << a.log2_group;
-    for (int x = blockIdx.y * kMergeThreads + threadIdx.x; x < rows * D; x += kMergeSplit * kMergeThreads) {
-        const int r = x / D, d = x % D;
+    for (int x = blockIdx.y * kMergeThreads + threadIdx.x; x < rows * (D / 4); x += kMergeSplit * kMergeThreads) {
+        const int r = x / (D / 4), d = x % (D / 4) * 4;
         const int row = p.z * rows + r, i = row >> a.log2_group;
         if (i >= n) return;
-        float M = -INFINITY, Z = 0.f, U = 0.f;
+        float M = kNone, Z = 0.f;
+        float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int b = blockIdx.x; b <= p.w; ++b) {
-            const int at = (2 * b + (b == (int)blockIdx.x)) * rows + r;
-            const float m = a.part_m[at];
-            const float z = a.part_z[at], u = a.part_u[(size_t)at * D + d];
+            const size_t at = (size_t)(2 * b + (b == (int)blockIdx.x)) * rows + r;
+            const float m = a.part_m[at], z = a.part_z[at];
+            const float4 v = *reinterpret_cast<const float4*>(a.part_u + at * D + d);
             const float top = fmaxf(M, m);
-            const float f = M == top ? 1.f : pa::exp2_approx(M - top), h = m == top ? 1.f : pa::exp2_approx(m - top);
+            const float f = pa::exp2_approx(M - top), h = pa::exp2_approx(m - top);
             Z = Z * f + z * h;
-            U = U * f + u * h;
+            U.x = U.x * f + v.x * h;
+            U.y = U.y * f + v.y * h;
+            U.z = U.z * f + v.z * h;
+            U.w = U.w * f + v.w * h;
             M = top;
         }
-        put(a.out, a.out_f32, ((size_t)(q0 + i) * a.n_q_heads + p.y * G + (row & (G - 1))) * D + d,
-            Z == 0.f ? 0.f : U * a.v_scale / Z);
+        const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+        put4(a.out, a.out_f32, ((size_t)(q0 + i) * a.n_q_heads + p.y * G + (row & (G - 1))) * D + d,
+             make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
     }
 }
 
@@ -638,32 +762,30 @@ int sms() {
     return n;
 }
 
-// n-tiles of 8 rows: the fewest that hold all rows of a KV head, at most 4.
-int n_tiles(int max_query_len, int group) {
+// Rows of a unit: 16, 32 or 64, the fewest that hold all rows of a KV head.
+int unit_rows(int max_query_len, int group) {
     const long long rows = (long long)max_query_len * group;
-    return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-#ifndef PA_MULTI_WAVES
-#define PA_MULTI_WAVES 1
-#endif
-int max_grid(int nt) { return sms() * (nt > 2 ? 2 : 3) * PA_MULTI_WAVES; }
+// Resident blocks of the device.
+int max_grid(int rows) { return sms() * (rows == 16 ? 3 : rows == 32 ? 2 : 1); }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: the blocks' pieces, then m and z, then u; 256-byte aligned.
-size_t workspace_size(int grid, int nt, int d) {
-    const size_t rows = (size_t)2 * grid * 8 * nt;
+size_t workspace_size(int grid, int unit, int d) {
+    const size_t rows = (size_t)2 * grid * unit;
     return up256(16 * (size_t)grid) + 2 * up256(4 * rows) + 4 * rows * d;
 }
 
-template <int D, bool F8, int NT>
+template <int D, bool F8, int MT, int RG>
 int launch_multi(const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& a, int grid, cudaStream_t st) {
     static int attr[64] = {0};
-    using G = Geo<D, F8, NT>;
-    if (pa_host::ensure_smem_attr(multi_kernel<D, F8, NT>, G::kSmem, attr) != cudaSuccess) return PA_ERR_CUDA;
-    if (pa_host::launch_dependent(multi_kernel<D, F8, NT>, dim3(grid), dim3(kThreads), G::kSmem, st, mk, mv, a) !=
-        cudaSuccess)
+    using G = Geo<D, F8, MT, RG>;
+    if (pa_host::ensure_smem_attr(multi_kernel<D, F8, MT, RG>, G::kSmem, attr) != cudaSuccess) return PA_ERR_CUDA;
+    if (pa_host::launch_dependent(multi_kernel<D, F8, MT, RG>, dim3(grid), dim3(G::kThreads), G::kSmem, st, mk, mv,
+                                  a) != cudaSuccess)
         return PA_ERR_CUDA;
     return pa_host::launch_dependent(merge_kernel<D>, dim3(grid, kMergeSplit), dim3(kMergeThreads), 0, st, a,
                                      G::kRows) == cudaSuccess
@@ -672,10 +794,10 @@ int launch_multi(const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& 
 }
 
 template <int D, bool F8>
-int launch_multi(int nt, const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& a, int grid, cudaStream_t st) {
-    return nt == 1   ? launch_multi<D, F8, 1>(mk, mv, a, grid, st)
-           : nt == 2 ? launch_multi<D, F8, 2>(mk, mv, a, grid, st)
-                     : launch_multi<D, F8, 4>(mk, mv, a, grid, st);
+int launch_rows(int rows, const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& a, int grid, cudaStream_t st) {
+    return rows == 16   ? launch_multi<D, F8, 1, 1>(mk, mv, a, grid, st)
+           : rows == 32 ? launch_multi<D, F8, 2, 1>(mk, mv, a, grid, st)
+                        : launch_multi<D, F8, 2, 2>(mk, mv, a, grid, st);
 }
 
 int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache,
@@ -704,19 +826,19 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
         return PA_ERR_MISALIGNED;
     const long long cache_rows = (long long)num_blocks * n_kv_heads * block_size;
     if (cache_rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-    const int nt = n_tiles(max_query_len, group);
+    const int unit = unit_rows(max_query_len, group);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
-    const int most = max_grid(nt);
+    const int most = max_grid(unit);
     if (most <= 0) return PA_ERR_CUDA;
-    if (workspace_bytes < workspace_size(most, nt, d_head)) return PA_ERR_WORKSPACE;
+    if (workspace_bytes < workspace_size(most, unit, d_head)) return PA_ERR_WORKSPACE;
 
     MultiArgs a{};
     const long long cap = (long long)max_blocks_per_seq * block_size;
     a.ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
     // no more blocks than the largest possible work has shares of kMinShare steps
-    const long long tiles = ((long long)max_query_len * group + 8 * nt - 1) / (8 * nt);
-    const long long seq_steps = ((long long)a.ctx_cap + kStep - 1) / kStep;
-    const double work = (double)num_seqs * n_kv_heads * (double)tiles * (double)seq_steps;
+    const long long tiles = ((long long)max_query_len * group + unit - 1) / unit;
+    const long long seq_work = ((long long)a.ctx_cap + kStep - 1) / kStep + kUnitCost;
+    const double work = (double)num_seqs * n_kv_heads * (double)tiles * (double)seq_work;
     const double shares = work / kMinShare + 1;
     const int grid = shares < most ? (int)shares : most;
 
@@ -726,7 +848,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     a.query_start = query_start;
     a.context_lens = context_lens;
     a.tree_mask = reinterpret_cast<const uint64_t*>(tree_mask);
-    const size_t rows = (size_t)2 * grid * 8 * nt;
+    const size_t rows = (size_t)2 * grid * unit;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     a.pieces = reinterpret_cast<int4*>(w);
     w += up256(16 * (size_t)grid);
@@ -736,7 +858,9 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     w += up256(4 * rows);
     a.part_u = reinterpret_cast<float*>(w);
     a.status = status_dev;
-    a.scale_log2 = scale * kLog2e * (f8 ? k_scale : 1.f);
+    const float factor = fabsf(scale) * kLog2e * (f8 ? k_scale : 1.f);
+    a.scale_log2 = factor == 0.f ? 1.f : factor;                // masked scores are -inf times it
+    a.q_sign = factor == 0.f ? 0.f : scale > 0.f ? 1.f : -1.f;
     a.v_scale = f8 ? v_scale / kWeightScale : 1.f;
     a.out_f32 = out_dtype == PA_DTYPE_F32;
     a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
@@ -754,9 +878,9 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
         !pa_host::cache_view(&mv, v_cache, cache_rows, d_head, f8 ? 1 : 2, box))
         return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return f8 ? launch_multi<128, true>(nt, mk, mv, a, grid, st)
-              : d_head == 128 ? launch_multi<128, false>(nt, mk, mv, a, grid, st)
-                              : launch_multi<64, false>(nt, mk, mv, a, grid, st);
+    return f8 ? launch_rows<128, true>(unit, mk, mv, a, grid, st)
+              : d_head == 128 ? launch_rows<128, false>(unit, mk, mv, a, grid, st)
+                              : launch_rows<64, false>(unit, mk, mv, a, grid, st);
 }
 
 }  // namespace
@@ -765,8 +889,8 @@ extern "C" {
 
 size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads, int n_kv_heads, int d_head) {
     if (max_query_len <= 0 || n_kv_heads <= 0 || n_q_heads < n_kv_heads || d_head <= 0) return 0;
-    const int nt = n_tiles(max_query_len, n_q_heads / n_kv_heads);
-    return workspace_size(max_grid(nt), nt, d_head);
+    const int unit = unit_rows(max_query_len, n_q_heads / n_kv_heads);
+    return workspace_size(max_grid(unit), unit, d_head);
 }
 
 int pa_decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache,
