@@ -35,44 +35,18 @@
 
 #include <math.h>
 
-#include "pa_mma.cuh"
+#include "pa_multi.cuh"
+
+using namespace pa_multi;
 
 namespace {
 
 constexpr int kKeyWarps = 4;               // warps that split a step's positions
 constexpr int kTile = 16;                  // positions per warp and step
 constexpr int kStep = kKeyWarps * kTile;
-constexpr int kMaxProbes = 2000000;        // ~2 s bound on any single wait
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -3.0e38f;          // a row's maximum before it has seen anything
-constexpr float kRaise = 8.0f;             // log2 of the largest weight before the maximum is raised
 constexpr float kWeightScale = 128.f;      // FP8: weights enter f16 products times 2^7 (at most 2^15)
-#ifndef PA_MULTI_UNIT_COST
-#define PA_MULTI_UNIT_COST 3
-#endif
-constexpr int kUnitCost = PA_MULTI_UNIT_COST;   // steps that starting and joining a unit is worth
-constexpr int kMinShare = 4 + kUnitCost;   // work per block, at least
-constexpr int kMergeThreads = 256;
-constexpr int kMergeSplit = 4;             // blocks per unit to merge
-
-struct MultiArgs {
-    void* out;
-    const __nv_bfloat16* q;
-    const int32_t* block_tables;
-    const int32_t* query_start;
-    const int32_t* context_lens;
-    const uint64_t* tree_mask;             // null: causal
-    int4* pieces;                          // per block: {sequence or -1, KV head, row tile, last block}
-    float* part_m;                         // [2 per block][rows]
-    float* part_z;
-    float* part_u;                         // [2 per block][rows][D]
-    int32_t* status;
-    float scale_log2;                      // |scale| * log2(e), times the K scale; > 0
-    float q_sign;                          // the scale's sign (0: a scale of zero, scale_log2 is 1)
-    float v_scale;                         // factor on the weighted sums
-    int out_f32, log2_block, n_q_heads, n_kv_heads, log2_group, max_blocks, num_blocks, ctx_cap, num_seqs, num_tokens,
-        max_query_len;
-};
+constexpr int kUnitCost = 5;               // steps that starting and joining a unit is worth
+constexpr int kMinSteps = 4;               // steps per block, at least
 
 // MT: 16-row tiles per warp; RG: groups of four warps, each with its own rows.
 template <int D, bool F8, int MT, int RG>
@@ -98,93 +72,6 @@ struct Geo {
     static_assert(kAhead >= 1, "the ring has to hold a tile of the next unit beside the join");
     static_assert(kJoinParts * kKeyWarps * kStageBytes == 4 * kKeyWarps * 16 * D, "a row tile's states fill the join stages");
 };
-
-// Four consecutive values of a row.
-__device__ __forceinline__ void put4(void* out, int f32, size_t i, float4 v) {
-    if (f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = v;
-    else
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + i) =
-            make_uint2(pa::pack_bf16x2(v.x, v.y), pa::pack_bf16x2(v.z, v.w));
-}
-
-// A sequence's part of the call.
-struct Seq {
-    int q0, n, ctx, steps, tiles;
-    __device__ __forceinline__ long long work(int heads) const {
-        return (long long)heads * tiles * (steps + kUnitCost);   // tiles is 0 where nothing is to be done
-    }
-};
-
-template <int kRows>
-__device__ __forceinline__ Seq read_seq(const MultiArgs& a, int s, bool flag) {
-    Seq r;
-    r.q0 = a.query_start[s];
-    const int q1 = a.query_start[s + 1];
-    int ctx = a.context_lens[s];
-    bool bad = ctx < 0 || ctx > a.ctx_cap;
-    ctx = ctx < 0 ? 0 : (ctx > a.ctx_cap ? a.ctx_cap : ctx);
-    r.n = q1 - r.q0;
-    if (r.q0 < 0 || q1 > a.num_tokens || q1 < r.q0 || r.n > ctx || r.n > a.max_query_len) {
-        r.n = 0;                                        // nothing of it is computed
-        bad = true;
-    }
-    if (bad && flag) pa::set_status(a.status, PA_DEV_BAD_CONTEXT);
-    r.ctx = ctx;
-    r.tiles = (int)((((long long)r.n << a.log2_group) + kRows - 1) / kRows);
-    r.steps = (ctx + kStep - 1) / kStep;
-    return r;
-}
-
-// The stretch of one unit that a block computes: steps st0 .. st0 + len - 1.
-struct Unit {
-    int q0, n, ctx, first, steps;          // first: position of new token 0
-    int kvh, row0, st0, len, seq, tile, last;   // last: the block that ends the unit
-    int valid;                             // 0: the share has ended
-    const uint64_t* words;                 // mask words of the sequence's tokens, or null
-    const int32_t* table;
-};
-
-// Walks a block's share of the work, unit by unit.
-struct Walk {
-    long long pos, end, off, share;        // off: work of the sequence before pos
-    int seq;
-    Seq sq;
-};
-
-template <int kRows>
-__device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
-    u.valid = 0;
-    while (w.pos < w.end) {
-        while (w.off >= w.sq.work(a.n_kv_heads)) {
-            w.off -= w.sq.work(a.n_kv_heads);
-            w.sq = read_seq<kRows>(a, ++w.seq, false);
-        }
-        const int per = w.sq.steps + kUnitCost;
-        const int unit = (int)(w.off / per), o = (int)(w.off - (long long)unit * per);
-        const int take = (int)min((long long)(per - o), w.end - w.pos);
-        const int lo = max(0, o - kUnitCost), hi = max(0, o + take - kUnitCost);
-        u.last = (int)((w.pos - o + per - 1) / w.share);
-        w.pos += take;
-        w.off += take;
-        if (hi == lo) continue;            // the share ends within the unit's constant part
-        u.q0 = w.sq.q0;
-        u.n = w.sq.n;
-        u.ctx = w.sq.ctx;
-        u.first = w.sq.ctx - w.sq.n;
-        u.steps = w.sq.steps;
-        u.kvh = unit / w.sq.tiles;
-        u.tile = unit - u.kvh * w.sq.tiles;
-        u.row0 = u.tile * kRows;
-        u.st0 = lo;
-        u.len = hi - lo;
-        u.seq = w.seq;
-        u.words = a.tree_mask ? a.tree_mask + w.sq.q0 : nullptr;
-        u.table = a.block_tables + (size_t)w.seq * a.max_blocks;
-        u.valid = 1;
-        return;
-    }
-}
 
 __device__ __forceinline__ bool visible(const Unit& u, int log2_group, int row, int pos) {
     if (pos >= u.ctx) return false;
@@ -403,45 +290,10 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- this block's share: thread t counts sequences [t * per, (t + 1) * per) ----
-    const int per = (a.num_seqs + kThreads - 1) / kThreads;
-    const int s_lo = threadIdx.x * per, s_hi = min(a.num_seqs, s_lo + per);
-    long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) mine += read_seq<kRows>(a, s, blockIdx.x == 0).work(heads);
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-    }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kKeyWarps * RG; ++w) {
-        if (w < warp) upto += sums[w];
-        total += sums[w];
-    }
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    share = share < kMinShare ? kMinShare : share;
-    const long long begin = share * blockIdx.x;
-    if (threadIdx.x == 0) a.pieces[blockIdx.x].x = -1;
-    if (begin >= total) return;
-    if (begin >= upto - mine && begin < upto) {                  // one thread's range holds the share's start
-        long long off = begin - (upto - mine);
-        int s = s_lo;
-        Seq sq = read_seq<kRows>(a, s, false);
-        while (off >= sq.work(heads)) {
-            off -= sq.work(heads);
-            sq = read_seq<kRows>(a, ++s, false);
-        }
-        walk.pos = begin;
-        walk.end = min(total, begin + share);
-        walk.off = off;
-        walk.share = share;
-        walk.seq = s;
-        walk.sq = sq;
-        next_unit<kRows>(walk, units[0], a);
-        next_unit<kRows>(walk, units[1], a);
+    if (!find_share<kRows, kStep, kUnitCost, kMinSteps, kThreads>(a, walk, sums)) return;
+    if (threadIdx.x == 0) {
+        next_unit<kRows, kStep, kUnitCost>(walk, units[0], a);
+        next_unit<kRows, kStep, kUnitCost>(walk, units[1], a);
     }
     __syncthreads();
     if (!units[0].valid) return;                                 // a share that ends in a unit's constant part
@@ -577,7 +429,7 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
                 if (k < len) issue(u, k);
         int n0 = 0, n1 = 0;
         if (more && rg == 0) fetch(next, lane, n0, n1);
-        if (threadIdx.x == 0) next_unit<kRows>(walk, units[(nth + 2) & 3], a);
+        if (threadIdx.x == 0) next_unit<kRows, kStep, kUnitCost>(walk, units[(nth + 2) & 3], a);
         __syncwarp();
         uint32_t qr[MT == 1 ? G::kSteps : 1][4];
         if constexpr (MT == 1) {
@@ -711,42 +563,6 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
     }
 }
 
-// out of the units that several blocks share: the pieces of block b, which
-// begins the unit (its second slot), and of blocks b + 1 .. last (their
-// first), in that order.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a, int rows) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int4 p = a.pieces[blockIdx.x];
-    if (p.x < 0) return;
-    const int q0 = a.query_start[p.x], n = a.query_start[p.x + 1] - q0;
-    const int G = 1 << a.log2_group;
-    for (int x = blockIdx.y * kMergeThreads + threadIdx.x; x < rows * (D / 4); x += kMergeSplit * kMergeThreads) {
-        const int r = x / (D / 4), d = x % (D / 4) * 4;
-        const int row = p.z * rows + r, i = row >> a.log2_group;
-        if (i >= n) return;
-        float M = kNone, Z = 0.f;
-        float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int b = blockIdx.x; b <= p.w; ++b) {
-            const size_t at = (size_t)(2 * b + (b == (int)blockIdx.x)) * rows + r;
-            const float m = a.part_m[at], z = a.part_z[at];
-            const float4 v = *reinterpret_cast<const float4*>(a.part_u + at * D + d);
-            const float top = fmaxf(M, m);
-            const float f = pa::exp2_approx(M - top), h = pa::exp2_approx(m - top);
-            Z = Z * f + z * h;
-            U.x = U.x * f + v.x * h;
-            U.y = U.y * f + v.y * h;
-            U.z = U.z * f + v.z * h;
-            U.w = U.w * f + v.w * h;
-            M = top;
-        }
-        const float f = Z == 0.f ? 0.f : a.v_scale / Z;
-        put4(a.out, a.out_f32, ((size_t)(q0 + i) * a.n_q_heads + p.y * G + (row & (G - 1))) * D + d,
-             make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
-    }
-}
-
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -762,10 +578,11 @@ int sms() {
     return n;
 }
 
-// Rows of a unit: 16, 32 or 64, the fewest that hold all rows of a KV head.
-int unit_rows(int max_query_len, int group) {
+// Rows of a unit: the fewest that hold all rows of a KV head, at most 64, or
+// 128 where the wide kernel runs.
+int unit_rows(int max_query_len, int group, bool wide) {
     const long long rows = (long long)max_query_len * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || !wide ? 64 : 128;
 }
 
 // Resident blocks of the device.
@@ -784,11 +601,8 @@ int launch_multi(const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& 
     static int attr[64] = {0};
     using G = Geo<D, F8, MT, RG>;
     if (pa_host::ensure_smem_attr(multi_kernel<D, F8, MT, RG>, G::kSmem, attr) != cudaSuccess) return PA_ERR_CUDA;
-    if (pa_host::launch_dependent(multi_kernel<D, F8, MT, RG>, dim3(grid), dim3(G::kThreads), G::kSmem, st, mk, mv,
-                                  a) != cudaSuccess)
-        return PA_ERR_CUDA;
-    return pa_host::launch_dependent(merge_kernel<D>, dim3(grid, kMergeSplit), dim3(kMergeThreads), 0, st, a,
-                                     G::kRows) == cudaSuccess
+    return pa_host::launch_dependent(multi_kernel<D, F8, MT, RG>, dim3(grid), dim3(G::kThreads), G::kSmem, st, mk, mv,
+                                     a) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
@@ -826,7 +640,9 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
         return PA_ERR_MISALIGNED;
     const long long cache_rows = (long long)num_blocks * n_kv_heads * block_size;
     if (cache_rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-    const int unit = unit_rows(max_query_len, group);
+    // The wide kernel (bf16 caches, more than 32 rows) takes the scale's sign as positive.
+    const bool wide = !f8 && scale > 0.f && (long long)max_query_len * group > 32;
+    const int unit = unit_rows(max_query_len, group, wide);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
     const int most = max_grid(unit);
     if (most <= 0) return PA_ERR_CUDA;
@@ -835,11 +651,12 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     MultiArgs a{};
     const long long cap = (long long)max_blocks_per_seq * block_size;
     a.ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
-    // no more blocks than the largest possible work has shares of kMinShare steps
+    // no more blocks than the largest possible work has smallest shares
+    const int step = wide ? kWideStep : kStep, cost = wide ? kWideCost : kUnitCost;
     const long long tiles = ((long long)max_query_len * group + unit - 1) / unit;
-    const long long seq_work = ((long long)a.ctx_cap + kStep - 1) / kStep + kUnitCost;
+    const long long seq_work = ((long long)a.ctx_cap + step - 1) / step + cost;
     const double work = (double)num_seqs * n_kv_heads * (double)tiles * (double)seq_work;
-    const double shares = work / kMinShare + 1;
+    const double shares = work / ((wide ? kWideMinSteps : kMinSteps) + cost) + 1;
     const int grid = shares < most ? (int)shares : most;
 
     a.out = out;
@@ -872,15 +689,25 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     a.num_seqs = num_seqs;
     a.num_tokens = num_tokens;
     a.max_query_len = max_query_len;
-    const int box = block_size < kTile ? block_size : kTile;
+    // a box of the wide kernel is a block, of the others at most a warp's tile
+    const int box = wide || block_size < kTile ? block_size : kTile;
     CUtensorMap mk, mv;
     if (!pa_host::cache_view(&mk, k_cache, cache_rows, d_head, f8 ? 1 : 2, box) ||
         !pa_host::cache_view(&mv, v_cache, cache_rows, d_head, f8 ? 1 : 2, box))
         return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return f8 ? launch_rows<128, true>(unit, mk, mv, a, grid, st)
-              : d_head == 128 ? launch_rows<128, false>(unit, mk, mv, a, grid, st)
-                              : launch_rows<64, false>(unit, mk, mv, a, grid, st);
+    int rc;
+    if (wide)
+        rc = launch_wide(unit, d_head, q, block_size, mk, mv, a, grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    else
+        rc = f8 ? launch_rows<128, true>(unit, mk, mv, a, grid, st)
+             : d_head == 128 ? launch_rows<128, false>(unit, mk, mv, a, grid, st)
+                             : launch_rows<64, false>(unit, mk, mv, a, grid, st);
+    if (rc != PA_OK) return rc;
+    return pa_host::launch_dependent(d_head == 128 ? merge_kernel<128> : merge_kernel<64>, dim3(grid, kMergeSplit),
+                                     dim3(kMergeThreads), 0, st, a, unit) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -889,7 +716,7 @@ extern "C" {
 
 size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads, int n_kv_heads, int d_head) {
     if (max_query_len <= 0 || n_kv_heads <= 0 || n_q_heads < n_kv_heads || d_head <= 0) return 0;
-    const int unit = unit_rows(max_query_len, n_q_heads / n_kv_heads);
+    const int unit = unit_rows(max_query_len, n_q_heads / n_kv_heads, true);   // the largest that a call may take
     return workspace_size(max_grid(unit), unit, d_head);
 }
 

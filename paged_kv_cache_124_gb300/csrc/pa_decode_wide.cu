@@ -1,0 +1,645 @@
+// Attention of several new tokens per sequence for more rows (new tokens
+// times query heads of the group) than warp-level products can keep up with
+// the cache's bytes for: units of 64 or 128 rows on the 5th-generation tensor
+// cores.  Same operation, units, shares and pieces as pa_decode_multi.cu.
+//
+// What bounds it: a tile of 128 positions of one KV head (64 KB of K and V at
+// d_head 128) takes an SM about 1.46 us of its share of the memory's rate,
+// and its products, S = Q . K^T and O += P . V at 128 rows, 0.33 us each: the
+// bytes bound it as long as copies, products and softmax overlap.
+//  * One block per SM walks its share.  Three stages each of K and V; a
+//    producer warp each fills them through the block table, one warp issues
+//    the products, and two groups of four warps take the tiles in turn, even
+//    tiles the first and odd ones the second, each with its own scores,
+//    running statistics and output accumulator in tensor memory (S0, S1, O0,
+//    O1: all 512 columns).  So a thread owns a whole row of its tiles and
+//    exchanges nothing until a unit's end, where the two accumulators are
+//    merged exactly.
+//  * V stays bf16, so the weights enter P . V as two bf16 terms (hi + lo, a
+//    relative 2^-16).  Up to 64 rows the 128 lanes of a product hold each
+//    row twice, 16 lanes apart, one with the hi and one with the lo terms: a
+//    single product does both, and the output adds the two lanes.  With 128
+//    rows they are two products.
+//  * V rows past the context are zeroed in shared memory before the last
+//    tile's product (0 * NaN).
+
+#include "pa_multi.cuh"
+
+namespace {
+
+using namespace pa_multi;
+
+constexpr int kKv = kWideStep;             // positions per tile
+constexpr int kSoftmaxWarps = 8;
+constexpr int kKWarp = 8;                  // walks the share, loads K
+constexpr int kVWarp = 9;                  // loads q (free when its unit's last scores are done) and V
+constexpr int kMmaWarp = 10;               // owns the tensor memory
+constexpr int kThreads = 352;
+constexpr int kUnits = 4;                  // units posted ahead
+constexpr int kUnitReaders = 10;           // warps that read a posted unit
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
+
+template <int D, bool kDup>
+struct Wide {
+    static constexpr int kRows = kDup ? 64 : 128;
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = 128 * 128;                 // 128 rows of 64 bf16, 128-byte swizzle
+    static constexpr int kTileBytes = kHalves * kHalfBytes;      // q, or K or V of a tile
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kK0 = kTileBytes;
+    static constexpr int kV0 = kK0 + kStages * kTileBytes;
+    static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][lane] maximum and sum
+    static constexpr int kCtl = kStats + 2 * 128 * 8;
+    static constexpr int kSmem = kCtl + 1024;
+};
+
+constexpr int kMaxStages = 6;
+
+struct Ctl {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+    uint64_t s_full[2];                    // per group: its tile's scores are in tensor memory
+    uint64_t p_full[2];                    // per group: its weights are (and its O is rescaled)
+    uint64_t o_done, o_free;               // a unit's last product has finished; its O has been read
+    uint64_t stats_full, stats_free;       // the groups' statistics are posted, and read
+    uint64_t unit_full[kUnits], unit_empty[kUnits];
+    Unit units[kUnits];
+    Walk walk;
+    long long sums[kThreads / 32];
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block overflows its space");
+
+// --- tcgen05 ------------------------------------------------------------------
+
+// Start address, leading and stride byte offsets (all >> 4), version 1, 128-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)((lbo & 0x3FFFF) >> 4) << 16) |
+           ((uint64_t)((sbo & 0x3FFFF) >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16: fp32 accumulator, A and B bf16, A K-major, B K-major or (b_mn) MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, int b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// A operand from tensor memory: rows in lanes, two bf16 values per column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(pa::smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void ld32(uint32_t t, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void st32(uint32_t t, const float* v) {
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]), "r"(w[17]), "r"(w[18]),
+        "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]),
+        "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31]));
+}
+
+__device__ __forceinline__ void st16(uint32_t t, const uint32_t* w) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]));
+}
+
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int x, int head, int token, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token),
+        "r"(pa::smem_addr(bar)) : "memory");
+}
+
+// --- packed fp32 pairs --------------------------------------------------------
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t r, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// A whole warp's bounded wait; gives up, too, once another role has.
+__device__ __noinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* status) {
+#pragma unroll 1
+    for (int i = 0; i < kMaxProbes; ++i) {
+        if (__all_sync(0xffffffffu, pa::mbar_try_wait(bar, parity))) return true;
+        if ((i & 63) == 63 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&ctl->abort) != 0)) return false;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+        pa::set_status(status, PA_DEV_WAIT_TIMEOUT);
+    }
+    __syncwarp();
+    return false;
+}
+
+template <int D, bool kDup>
+__global__ void __launch_bounds__(kThreads, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v, const MultiArgs a, int oob_row) {
+    using G = Wide<D, kDup>;
+    constexpr int kRows = G::kRows, kStages = G::kStages;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    Ctl* ctl = reinterpret_cast<Ctl*>(sm + G::kCtl);
+    float2* stats = reinterpret_cast<float2*>(sm + G::kStats);
+    const uint32_t s0 = pa::smem_addr(sm);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int B = 1 << a.log2_block, group = 1 << a.log2_group;
+
+    if (threadIdx.x == 0) {
+        pa::mbar_init(&ctl->q_full, 1);
+        pa::mbar_init(&ctl->q_empty, 1);
+        for (int i = 0; i < kStages; ++i) {
+            pa::mbar_init(&ctl->k_full[i], 1);
+            pa::mbar_init(&ctl->k_empty[i], 1);
+            pa::mbar_init(&ctl->v_full[i], 1);
+            pa::mbar_init(&ctl->v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            pa::mbar_init(&ctl->s_full[i], 1);
+            pa::mbar_init(&ctl->p_full[i], 128);
+        }
+        pa::mbar_init(&ctl->o_done, 1);
+        pa::mbar_init(&ctl->o_free, 256);
+        pa::mbar_init(&ctl->stats_full, 256);
+        pa::mbar_init(&ctl->stats_free, 256);
+        for (int i = 0; i < kUnits; ++i) {
+            pa::mbar_init(&ctl->unit_full[i], 1);
+            pa::mbar_init(&ctl->unit_empty[i], kUnitReaders);
+        }
+        ctl->abort = 0;
+        pa::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(pa::smem_addr(&ctl->tmem)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctl->tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const bool busy = find_share<kRows, kKv, kWideCost, kWideMinSteps, kThreads>(a, ctl->walk, ctl->sums);
+    // an address that is not a multiple of 1024 would break the swizzled tiles
+    if (busy && (s0 & 1023)) {
+        if (threadIdx.x == 0) pa::set_status(a.status, PA_DEV_WAIT_TIMEOUT);
+    } else if (!busy) {
+    } else if (warp == kKWarp || warp == kVWarp) {
+        // ------------------------------------------------------------ producers
+        // Lane i copies block i of each tile (its table entry fetched four
+        // tiles ahead); blocks past the context, and bad ids, are read from
+        // outside the tensor, which fills zeros.
+        const bool is_k = warp == kKWarp;
+        const int blocks = kKv >> a.log2_block;
+        uint64_t* full = is_k ? ctl->k_full : ctl->v_full;
+        uint64_t* empty = is_k ? ctl->k_empty : ctl->v_empty;
+        const CUtensorMap* map = is_k ? &map_k : &map_v;
+        const uint64_t policy = pa::l2_evict_first_policy();
+        int done = 0, nth = 0;                                   // tiles and units so far
+        bool ok = true;
+        for (; ok; ++nth) {
+            const int slot = nth % kUnits;
+            Unit* u = &ctl->units[slot];
+            if (is_k) {
+                if (nth >= kUnits && !wait_for(&ctl->unit_empty[slot], (nth / kUnits - 1) & 1, ctl, a.status)) break;
+                if (lane == 0) {
+                    next_unit<kRows, kKv, kWideCost>(ctl->walk, *u, a);
+                    if (u->valid && u->st0 == 0 && u->len != u->steps)       // this block begins a unit that others end
+                        a.pieces[blockIdx.x] = make_int4(u->seq, u->kvh, u->tile, u->last);
+                    pa::mbar_arrive(&ctl->unit_full[slot]);
+                }
+                __syncwarp();
+                if (!u->valid) break;
+            } else {
+                if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
+                if (!u->valid) break;
+                if (nth >= 1 && !(ok = wait_for(&ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
+                if (lane == 0) {
+                    // 16 rows a box: 16 / group tokens of the group's heads
+                    pa::mbar_arrive_expect_tx(&ctl->q_full, G::kTileBytes);
+                    for (int r = 0; r < 128; r += 16) {
+                        const int row = u->row0 + (kDup ? r >> 5 << 4 : r);
+#pragma unroll
+                        for (int h = 0; h < G::kHalves; ++h)
+                            tma_q(s0 + h * G::kHalfBytes + r * 128, &map_q, h * 64, u->kvh << a.log2_group,
+                                  u->q0 + (row >> a.log2_group), &ctl->q_full);
+                    }
+                }
+            }
+            const int len = u->len, ctx = u->ctx, st0 = u->st0, kvh = u->kvh;
+            const int32_t* table = u->table;
+            if (!is_k) {
+                __syncwarp();
+                if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
+            }
+            constexpr int kFetch = 4;
+            constexpr int kNoBlock = -2147483647 - 1;
+            auto fetch = [&](int j) {
+                const int pos = (st0 + j) * kKv + lane * B;
+                return (j < len && lane < blocks && pos < ctx) ? table[pos >> a.log2_block] : kNoBlock;
+            };
+            auto row_of = [&](int blk) {
+                if (blk == kNoBlock) return oob_row;
+                if (blk < 0 || blk >= a.num_blocks) {
+                    pa::set_status(a.status, PA_DEV_BAD_BLOCK_ID);
+                    return oob_row;
+                }
+                return (blk * a.n_kv_heads + kvh) * B;
+            };
+            int ids[kFetch];
+#pragma unroll
+            for (int x = 0; x < kFetch; ++x) ids[x] = fetch(x);
+            for (int j0 = 0; ok && j0 < len; j0 += kFetch) {
+#pragma unroll
+                for (int x = 0; x < kFetch; ++x) {
+                    const int j = j0 + x;
+                    if (j >= len) break;
+                    const int row = row_of(ids[x]), st = done % kStages;
+                    ids[x] = fetch(j + kFetch);
+                    if (done >= kStages && !(ok = wait_for(&empty[st], (done / kStages - 1) & 1, ctl, a.status))) break;
+                    if (lane == 0) pa::mbar_arrive_expect_tx(&full[st], G::kTileBytes);
+                    __syncwarp();
+                    if (lane < blocks) {
+                        const uint32_t dst = s0 + (is_k ? G::kK0 : G::kV0) + st * G::kTileBytes + lane * B * 128;
+#pragma unroll
+                        for (int h = 0; h < G::kHalves; ++h)
+                            pa::tma_box(dst + h * G::kHalfBytes, map, h * 64, row, &full[st], policy);
+                    }
+                    ++done;
+                }
+            }
+        }
+        // the copies this warp started land before the block exits
+        if (lane == 0) {
+            if (!is_k && nth > 0) pa::mbar_wait_bounded(&ctl->q_full, (nth - 1) & 1, kMaxProbes);
+            for (int i = 0; i < kStages && i < done; ++i)
+                pa::mbar_wait_bounded(&full[(done - 1 - i) % kStages], ((done - 1 - i) / kStages) & 1, kMaxProbes);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t id_s = idesc_bf16(128, kKv, 0), id_o = idesc_bf16(128, D, 1);
+        uint64_t* last = nullptr;
+        uint32_t last_parity = 0;
+        int ns = 0, nv = 0, nth = 0;                             // score tiles, value tiles, units so far
+        int npf[2] = {0, 0};                                     // weights of each group so far
+        bool ok = true;
+        for (; ok; ++nth) {
+            const int slot = nth % kUnits;
+            if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
+            const Unit* u = &ctl->units[slot];
+            const int valid = u->valid, len = u->len, ctx = u->ctx, st0 = u->st0;
+            __syncwarp();
+            if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
+            if (!valid) break;
+            if (!(ok = wait_for(&ctl->q_full, nth & 1, ctl, a.status))) break;
+            // scores of tile j (in tensor memory of group j & 1, whose weights of tile j - 2 are used up:
+            // products run in the order of their issue)
+            auto scores = [&](int j) {
+                const int st = ns % kStages;
+                if (!wait_for(&ctl->k_full[st], (ns / kStages) & 1, ctl, a.status)) return false;
+                fence_after();
+                if (lane == 0) {
+                    const uint32_t k0 = s0 + G::kK0 + st * G::kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * G::kHalfBytes + (kk & 3) * 32;
+                        mma_ss(tmem + (j & 1) * 128, smem_desc(s0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024), id_s,
+                               kk > 0);
+                    }
+                    commit(&ctl->s_full[j & 1]);
+                    commit(&ctl->k_empty[st]);
+                    if (j == len - 1) commit(&ctl->q_empty);
+                }
+                __syncwarp();
+                ++ns;
+                return true;
+            };
+            ok = scores(0) && (len < 2 || scores(1));
+            for (int j = 0; ok && j < len; ++j) {
+                const int st = nv % kStages, w = j & 1;
+                if (!(ok = wait_for(&ctl->v_full[st], (nv / kStages) & 1, ctl, a.status))) break;
+                const uint32_t v0 = s0 + G::kV0 + st * G::kTileBytes;
+                const int left = min(kKv, ctx - (st0 + j) * kKv), steps = (left + 15) >> 4;
+                if (left & 15) {
+                    // rows left .. 16 * steps - 1 of the tile are past the context: zeros
+                    for (int x = lane; x < (16 * steps - left) * G::kHalves * 8; x += 32) {
+                        const int r = left + x / (G::kHalves * 8), c = x % (G::kHalves * 8);
+                        *reinterpret_cast<uint4*>(sm + G::kV0 + st * G::kTileBytes + (c >> 3) * G::kHalfBytes + r * 128 +
+                                                  (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                // the unit before has read its O out
+                if (j == 0 && nth >= 1 && !(ok = wait_for(&ctl->o_free, (nth - 1) & 1, ctl, a.status))) break;
+                if (!(ok = wait_for(&ctl->p_full[w], npf[w] & 1, ctl, a.status))) break;
+                ++npf[w];
+                fence_after();
+                if (lane == 0) {
+                    const uint32_t t_p = tmem + w * 128, t_o = tmem + kTmemO + w * 128;
+                    for (int kk = 0; kk < steps; ++kk)
+                        mma_ts(t_o, t_p + kk * 8, smem_desc(v0 + kk * 2048, G::kHalfBytes, 1024), id_o,
+                               (j > 1 || kk > 0) ? 1u : 0u);
+                    if (!kDup)
+                        for (int kk = 0; kk < steps; ++kk)
+                            mma_ts(t_o, t_p + kKv / 2 + kk * 8, smem_desc(v0 + kk * 2048, G::kHalfBytes, 1024), id_o, 1u);
+                    commit(&ctl->v_empty[st]);
+                    last = &ctl->v_empty[st];
+                    last_parity = (nv / kStages) & 1;
+                    if (j == len - 1) commit(&ctl->o_done);
+                }
+                __syncwarp();
+                ++nv;
+                if (j + 2 < len) ok = scores(j + 2);
+            }
+        }
+        // products in flight finish before the tensor memory is freed (a score product that no value
+        // product followed: its tile's commit)
+        if (lane == 0) {
+            if (last) pa::mbar_wait_bounded(last, last_parity, kMaxProbes);
+            if (ns) pa::mbar_wait_bounded(&ctl->k_empty[(ns - 1) % kStages], ((ns - 1) / kStages) & 1, kMaxProbes);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax: group w takes tiles j = w, w + 2, ...
+        const int w = warp >> 2, quarter = warp & 3;
+        const int tl = quarter * 32 + lane;                      // tensor-memory lane
+        const int r = kDup ? quarter * 16 + (lane & 15) : tl;    // row of the unit
+        const bool is_lo = kDup && (lane & 16);
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t t_s = t_lane + w * 128, t_o = t_lane + kTmemO + w * 128;
+        const float c = a.scale_log2;
+        const uint64_t cc = pair(c, c);
+        int tiles = 0;                                           // this group's tiles so far
+        bool ok = true;
+        for (int nth = 0; ok; ++nth) {
+            const int slot = nth % kUnits;
+            if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
+            const Unit u = ctl->units[slot];
+            __syncwarp();
+            if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
+            if (!u.valid) break;
+            const int i = (u.row0 + r) >> a.log2_group;
+            const bool real = i < u.n;
+            // what the row sees of the new tokens: a word (tree), or those below `lim` positions
+            unsigned long long word = ~0ull;
+            if (u.words && real) word = u.words[i];
+            if (u.n < 64) word &= (1ull << u.n) - 1;
+            const int lim = (u.words || !real) ? u.ctx : u.first + i + 1;
+            float m = kNone, l = 0.f;
+            for (int j = w; ok && j < u.len; j += 2, ++tiles) {
+                if (!(ok = wait_for(&ctl->s_full[w], tiles & 1, ctl, a.status))) break;
+                fence_after();
+                float s[kKv];
+#pragma unroll
+                for (int x = 0; x < kKv / 32; ++x) ld32(t_s + 32 * x, s + 32 * x);
+                wait_ld();
+                const int t0 = (u.st0 + j) * kKv;
+                if (t0 + kKv > u.first) {
+                    const int end = lim - t0;
+#pragma unroll
+                    for (int x = 0; x < kKv; ++x) s[x] = x < end ? s[x] : -INFINITY;
+                    if (u.words) {
+                        const int j0 = t0 - u.first;
+#pragma unroll
+                        for (int x = 0; x < kKv; ++x) {
+                            const int b = j0 + x;
+                            if (b >= 0 && (b > 63 || !(word >> b & 1ull))) s[x] = -INFINITY;
+                        }
+                    }
+                }
+                float top = -INFINITY;
+                {
+                    float p[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) p[k] = s[k];
+#pragma unroll
+                    for (int x = 8; x < kKv; x += 8)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) p[k] = fmaxf(p[k], s[x + k]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, p[k]);
+                }
+                if (kDup) top = __shfl_sync(0xffffffffu, top, lane & 15);   // a row's two lanes decide as one
+                const bool raise = fmaf(top, c, -m) > kRaise;
+                const float m_new = raise ? top * c : m;
+                if (j > w && __any_sync(0xffffffffu, raise)) {
+                    // this group's O holds its tiles before j: their products finished before these scores
+                    const float f = pa::exp2_approx(m - m_new);
+                    const uint64_t ff = pair(f, f);
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 16) {
+                        float o[16];
+                        uint32_t t = t_o + x;
+                        asm volatile(
+                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                            : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]),
+                              "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
+                            : "r"(t));
+                        wait_ld();
+                        uint32_t v[16];
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            float y0, y1;
+                            split(fma2(pair(o[k], o[k + 1]), ff, pair(0.f, 0.f)), y0, y1);
+                            v[k] = __float_as_uint(y0);
+                            v[k + 1] = __float_as_uint(y1);
+                        }
+                        st16(t, v);
+                    }
+                    l *= f;
+                }
+                m = m_new;
+                const uint64_t neg = pair(-m, -m);
+                uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+                for (int x = 0; x < kKv / 32; ++x) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float y0, y1;
+                        split(fma2(pair(s[32 * x + 2 * k], s[32 * x + 2 * k + 1]), cc, neg), y0, y1);
+                        const float p0 = pa::exp2_approx(y0), p1 = pa::exp2_approx(y1);
+                        const uint64_t p = pair(p0, p1);
+                        sum[k & 1] = add2(sum[k & 1], p);
+                        hi[k] = pa::pack_bf16x2(p0, p1);
+                        float r0, r1;
+                        split(sub2(p, pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xffff0000u))), r0, r1);
+                        lo[k] = pa::pack_bf16x2(r0, r1);
+                        if (kDup && is_lo) hi[k] = lo[k];
+                    }
+                    st16(t_s + 16 * x, hi);
+                    if (!kDup) st16(t_s + kKv / 2 + 16 * x, lo);
+                }
+                float a0, a1, b0, b1;
+                split(sum[0], a0, a1);
+                split(sum[1], b0, b1);
+                l += (a0 + a1) + (b0 + b1);
+                wait_st();
+                fence_before();
+                pa::mbar_arrive(&ctl->p_full[w]);
+            }
+            if (!ok) break;
+            // ---- the unit's end: both groups' statistics, then half of the columns each ----
+            if (nth >= 1 && !(ok = wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status))) break;
+            stats[w * 128 + tl] = make_float2(m, l);
+            pa::mbar_arrive(&ctl->stats_full);
+            if (!(ok = wait_for(&ctl->stats_full, nth & 1, ctl, a.status))) break;
+            const float2 e = stats[tl], o = stats[128 + tl];
+            pa::mbar_arrive(&ctl->stats_free);
+            const float M = fmaxf(e.x, o.x), fe = pa::exp2_approx(e.x - M), fo = pa::exp2_approx(o.x - M);
+            const float Z = fe * e.y + fo * o.y;
+            const bool whole = u.len == u.steps, odd = u.len > 1;   // one tile: O1 was not written
+            if (!(ok = wait_for(&ctl->o_done, nth & 1, ctl, a.status))) break;
+            fence_after();
+            const float by = whole ? (Z == 0.f ? 0.f : a.v_scale / Z) : 1.f;
+            const size_t at = (size_t)(2 * blockIdx.x + (u.st0 == 0 ? 1 : 0)) * kRows + r;
+            const size_t out_row = ((size_t)(u.q0 + i) * a.n_q_heads + (u.kvh << a.log2_group) +
+                                    ((u.row0 + r) & (group - 1))) * D;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                const int col = w * (D / 2) + 32 * x;
+                float v[32], v1[32];
+                ld32(t_lane + kTmemO + col, v);
+                ld32(t_lane + kTmemO + 128 + col, v1);
+                wait_ld();
+                if (x == D / 64 - 1) {                           // O is in registers: the next unit's products may write it
+                    fence_before();
+                    pa::mbar_arrive(&ctl->o_free);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    v[k] = fe * v[k] + (odd ? fo * v1[k] : 0.f);
+                    if (kDup) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+                    v[k] *= by;
+                }
+                if (real) {
+                    constexpr int kMine = kDup ? 16 : 32;        // of a row's two lanes, each writes half
+                    const int c0 = kDup && is_lo ? 16 : 0;
+#pragma unroll
+                    for (int k = 0; k < kMine; k += 4) {
+                        const float4 f = kDup && is_lo
+                                             ? make_float4(v[(16 + k) & 31], v[(17 + k) & 31], v[(18 + k) & 31], v[(19 + k) & 31])
+                                             : make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                        if (whole)
+                            put4(a.out, a.out_f32, out_row + col + c0 + k, f);
+                        else
+                            *reinterpret_cast<float4*>(a.part_u + at * D + col + c0 + k) = f;
+                    }
+                }
+            }
+            if (!whole && real && w == 0 && !is_lo) {
+                a.part_m[at] = M;
+                a.part_z[at] = Z;
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+}
+
+// 3-D view of q, [num_tokens][n_q_heads][d_head], in boxes of 16 rows of 64
+// columns: 16 / group tokens of one KV head's group.
+bool q_view(CUtensorMap* map, const void* q, int num_tokens, int n_q_heads, int d_head, int group) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d_head, (cuuint64_t)n_q_heads, (cuuint64_t)num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)d_head * 2, (cuuint64_t)d_head * n_q_heads * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)group, (cuuint32_t)(16 / group)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    auto encode = pa_host::tensor_map_encode();
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kDup>
+cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& a, int oob_row,
+                   int grid, cudaStream_t st) {
+    static int attr[64] = {0};
+    const cudaError_t e = pa_host::ensure_smem_attr(wide_kernel<D, kDup>, Wide<D, kDup>::kSmem, attr);
+    if (e != cudaSuccess) return e;
+    return pa_host::launch_dependent(wide_kernel<D, kDup>, dim3(grid), dim3(kThreads), Wide<D, kDup>::kSmem, st, mq, mk,
+                                     mv, a, oob_row);
+}
+
+}  // namespace
+
+namespace pa_multi {
+
+cudaError_t launch_wide(int rows, int d_head, const void* q, int block_size, const CUtensorMap& mk,
+                        const CUtensorMap& mv, const MultiArgs& a, int grid, cudaStream_t st) {
+    CUtensorMap mq;
+    if (!q_view(&mq, q, a.num_tokens, a.n_q_heads, d_head, 1 << a.log2_group)) return cudaErrorInvalidValue;
+    const int oob = a.num_blocks * a.n_kv_heads * block_size;    // one past the view's last row
+    return d_head == 128 ? (rows == 64 ? launch<128, true>(mq, mk, mv, a, oob, grid, st)
+                                       : launch<128, false>(mq, mk, mv, a, oob, grid, st))
+                         : (rows == 64 ? launch<64, true>(mq, mk, mv, a, oob, grid, st)
+                                       : launch<64, false>(mq, mk, mv, a, oob, grid, st));
+}
+
+}  // namespace pa_multi

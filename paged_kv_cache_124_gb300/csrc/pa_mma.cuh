@@ -95,10 +95,8 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 
 namespace pa_host {
 
-// 2-D view of a cache, [num_blocks * n_kv_heads * block_size rows][d_head]
-// elements (bf16, or one byte each), in boxes of 128 bytes x box_rows rows
-// with 128-byte swizzle.
-inline bool cache_view(CUtensorMap* map, const void* base, long long rows, int d_head, int elem_bytes, int box_rows) {
+// cuTensorMapEncodeTiled of the driver, or null.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -108,6 +106,14 @@ inline bool cache_view(CUtensorMap* map, const void* base, long long rows, int d
                 cudaSuccess && q == cudaDriverEntryPointSuccess)
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
+    return encode;
+}
+
+// 2-D view of a cache, [num_blocks * n_kv_heads * block_size rows][d_head]
+// elements (bf16, or one byte each), in boxes of 128 bytes x box_rows rows
+// with 128-byte swizzle.
+inline bool cache_view(CUtensorMap* map, const void* base, long long rows, int d_head, int elem_bytes, int box_rows) {
+    auto encode = tensor_map_encode();
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)d_head, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)d_head * elem_bytes};

@@ -1,0 +1,224 @@
+// Shared by the kernels that attend several new tokens per sequence: their
+// arguments, the even split of the work over the grid's blocks, and the merge
+// of the units that several blocks share.
+//
+// A unit is a (sequence, KV head, tile of rows).  Its work is the steps of
+// its context plus a constant for starting and joining it; block b takes the
+// work from b * share to (b + 1) * share, sequence after sequence, heads and
+// row tiles within them.  A share that begins within a unit's constant part
+// begins with the unit's first step.
+#pragma once
+
+#include "pa_mma.cuh"
+
+namespace pa_multi {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -3.0e38f;          // a row's maximum before it has seen anything
+constexpr float kRaise = 8.0f;             // log2 of the largest weight before the maximum is raised
+constexpr int kMaxProbes = 2000000;        // ~2 s bound on any single wait
+constexpr int kMergeThreads = 256;
+constexpr int kMergeSplit = 4;             // blocks per unit to merge
+
+struct MultiArgs {
+    void* out;
+    const __nv_bfloat16* q;
+    const int32_t* block_tables;
+    const int32_t* query_start;
+    const int32_t* context_lens;
+    const uint64_t* tree_mask;             // null: causal
+    int4* pieces;                          // per block: {sequence or -1, KV head, row tile, last block}
+    float* part_m;                         // [2 per block][rows]
+    float* part_z;
+    float* part_u;                         // [2 per block][rows][D]
+    int32_t* status;
+    float scale_log2;                      // |scale| * log2(e), times the K scale; > 0
+    float q_sign;                          // the scale's sign (0: a scale of zero, scale_log2 is 1)
+    float v_scale;                         // factor on the weighted sums
+    int out_f32, log2_block, n_q_heads, n_kv_heads, log2_group, max_blocks, num_blocks, ctx_cap, num_seqs, num_tokens,
+        max_query_len;
+};
+
+// Four consecutive values of a row.
+__device__ __forceinline__ void put4(void* out, int f32, size_t i, float4 v) {
+    if (f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = v;
+    else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + i) =
+            make_uint2(pa::pack_bf16x2(v.x, v.y), pa::pack_bf16x2(v.z, v.w));
+}
+
+// A sequence's part of the call.
+struct Seq {
+    int q0, n, ctx, steps, tiles;
+    // tiles is 0 where nothing is to be done; cost: steps that starting and joining a unit is worth
+    __device__ __forceinline__ long long work(int heads, int cost) const {
+        return (long long)heads * tiles * (steps + cost);
+    }
+};
+
+template <int kRows, int kStep>
+__device__ __forceinline__ Seq read_seq(const MultiArgs& a, int s, bool flag) {
+    Seq r;
+    r.q0 = a.query_start[s];
+    const int q1 = a.query_start[s + 1];
+    int ctx = a.context_lens[s];
+    bool bad = ctx < 0 || ctx > a.ctx_cap;
+    ctx = ctx < 0 ? 0 : (ctx > a.ctx_cap ? a.ctx_cap : ctx);
+    r.n = q1 - r.q0;
+    if (r.q0 < 0 || q1 > a.num_tokens || q1 < r.q0 || r.n > ctx || r.n > a.max_query_len) {
+        r.n = 0;                                        // nothing of it is computed
+        bad = true;
+    }
+    if (bad && flag) pa::set_status(a.status, PA_DEV_BAD_CONTEXT);
+    r.ctx = ctx;
+    r.tiles = (int)((((long long)r.n << a.log2_group) + kRows - 1) / kRows);
+    r.steps = (ctx + kStep - 1) / kStep;
+    return r;
+}
+
+// The stretch of one unit that a block computes: steps st0 .. st0 + len - 1.
+struct Unit {
+    int q0, n, ctx, first, steps;          // first: position of new token 0
+    int kvh, row0, st0, len, seq, tile, last;   // last: the block that ends the unit
+    int valid;                             // 0: the share has ended
+    const uint64_t* words;                 // mask words of the sequence's tokens, or null
+    const int32_t* table;
+};
+
+// A block's share of the work, walked unit by unit.
+struct Walk {
+    long long pos, end, off, share;        // off: work of the sequence before pos
+    int seq;
+    Seq sq;
+};
+
+// The next stretch of the share; u.valid is 0 at its end.
+template <int kRows, int kStep, int kUnitCost>
+__device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
+    u.valid = 0;
+    while (w.pos < w.end) {
+        while (w.off >= w.sq.work(a.n_kv_heads, kUnitCost)) {
+            w.off -= w.sq.work(a.n_kv_heads, kUnitCost);
+            w.sq = read_seq<kRows, kStep>(a, ++w.seq, false);
+        }
+        const int per = w.sq.steps + kUnitCost;
+        const int unit = (int)(w.off / per), o = (int)(w.off - (long long)unit * per);
+        const int take = (int)min((long long)(per - o), w.end - w.pos);
+        const int lo = max(0, o - kUnitCost), hi = max(0, o + take - kUnitCost);
+        u.last = (int)((w.pos - o + per - 1) / w.share);
+        w.pos += take;
+        w.off += take;
+        if (hi == lo) continue;            // the share ends within the unit's constant part
+        u.q0 = w.sq.q0;
+        u.n = w.sq.n;
+        u.ctx = w.sq.ctx;
+        u.first = w.sq.ctx - w.sq.n;
+        u.steps = w.sq.steps;
+        u.kvh = unit / w.sq.tiles;
+        u.tile = unit - u.kvh * w.sq.tiles;
+        u.row0 = u.tile * kRows;
+        u.st0 = lo;
+        u.len = hi - lo;
+        u.seq = w.seq;
+        u.words = a.tree_mask ? a.tree_mask + w.sq.q0 : nullptr;
+        u.table = a.block_tables + (size_t)w.seq * a.max_blocks;
+        u.valid = 1;
+        return;
+    }
+}
+
+
+// This block's share, found by all its threads: thread t counts sequences
+// [t * per, (t + 1) * per), and the one whose sequences hold the share's
+// start sets `walk` up there.  False: the block has nothing to do.  Ends with
+// a barrier; `sums` holds a value per warp.
+template <int kRows, int kStep, int kUnitCost, int kMinSteps, int kThreads>
+__device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, long long* sums) {
+    constexpr int kMinShare = kMinSteps + kUnitCost;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = a.n_kv_heads;
+    const int per = (a.num_seqs + kThreads - 1) / kThreads;
+    const int s_lo = threadIdx.x * per, s_hi = min(a.num_seqs, s_lo + per);
+    long long mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) mine += read_seq<kRows, kStep>(a, s, blockIdx.x == 0).work(heads, kUnitCost);
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+    }
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    share = share < kMinShare ? kMinShare : share;
+    const long long begin = share * blockIdx.x;
+    if (threadIdx.x == 0) a.pieces[blockIdx.x].x = -1;
+    if (begin >= total) return false;
+    if (begin >= upto - mine && begin < upto) {
+        long long off = begin - (upto - mine);
+        int s = s_lo;
+        Seq sq = read_seq<kRows, kStep>(a, s, false);
+        while (off >= sq.work(heads, kUnitCost)) {
+            off -= sq.work(heads, kUnitCost);
+            sq = read_seq<kRows, kStep>(a, ++s, false);
+        }
+        walk.pos = begin;
+        walk.end = min(total, begin + share);
+        walk.off = off;
+        walk.share = share;
+        walk.seq = s;
+        walk.sq = sq;
+    }
+    __syncthreads();
+    return true;
+}
+
+// out of the units that several blocks share: the pieces of block b, which
+// begins the unit (its second slot), and of blocks b + 1 .. last (their
+// first), in that order.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a, int rows) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int4 p = a.pieces[blockIdx.x];
+    if (p.x < 0) return;
+    const int q0 = a.query_start[p.x], n = a.query_start[p.x + 1] - q0;
+    const int G = 1 << a.log2_group;
+    for (int x = blockIdx.y * kMergeThreads + threadIdx.x; x < rows * (D / 4); x += kMergeSplit * kMergeThreads) {
+        const int r = x / (D / 4), d = x % (D / 4) * 4;
+        const int row = p.z * rows + r, i = row >> a.log2_group;
+        if (i >= n) return;
+        float M = kNone, Z = 0.f;
+        float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = blockIdx.x; b <= p.w; ++b) {
+            const size_t at = (size_t)(2 * b + (b == (int)blockIdx.x)) * rows + r;
+            const float m = a.part_m[at], z = a.part_z[at];
+            const float4 v = *reinterpret_cast<const float4*>(a.part_u + at * D + d);
+            const float top = fmaxf(M, m);
+            const float f = pa::exp2_approx(M - top), h = pa::exp2_approx(m - top);
+            Z = Z * f + z * h;
+            U.x = U.x * f + v.x * h;
+            U.y = U.y * f + v.y * h;
+            U.z = U.z * f + v.z * h;
+            U.w = U.w * f + v.w * h;
+            M = top;
+        }
+        const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+        put4(a.out, a.out_f32, ((size_t)(q0 + i) * a.n_q_heads + p.y * G + (row & (G - 1))) * D + d,
+             make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
+    }
+}
+
+
+// Launches of the 64- and 128-row units on the 5th-generation tensor cores
+// (pa_decode_wide.cu); cudaSuccess or the launch's error.
+cudaError_t launch_wide(int rows, int d_head, const void* q, int block_size, const CUtensorMap& map_k,
+                        const CUtensorMap& map_v, const MultiArgs& a, int grid, cudaStream_t st);
+constexpr int kWideCost = 2, kWideMinSteps = 2, kWideStep = 128;
+
+}  // namespace pa_multi
