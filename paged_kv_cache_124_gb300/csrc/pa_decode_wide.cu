@@ -9,7 +9,7 @@
 // bytes bound it as long as copies, products and softmax overlap.
 //  * One block per SM walks its share.  Three stages each of K and V; a
 //    producer warp each fills them through the block table, one warp issues
-//    the products, and two groups of four warps take the tiles in turn, even
+//    the score products and one the value products, and two groups of four warps take the tiles in turn, even
 //    tiles the first and odd ones the second, each with its own scores,
 //    running statistics and output accumulator in tensor memory (S0, S1, O0,
 //    O1: all 512 columns).  So a thread owns a whole row of its tiles and
@@ -33,10 +33,11 @@ constexpr int kKv = kWideStep;             // positions per tile
 constexpr int kSoftmaxWarps = 8;
 constexpr int kKWarp = 8;                  // walks the share, loads K
 constexpr int kVWarp = 9;                  // loads q (free when its unit's last scores are done) and V
-constexpr int kMmaWarp = 10;               // owns the tensor memory
-constexpr int kThreads = 352;
+constexpr int kScoreWarp = 10;             // issues the score products and owns the tensor memory
+constexpr int kValueWarp = 11;             // issues the value products
+constexpr int kThreads = 384;
 constexpr int kUnits = 4;                  // units posted ahead
-constexpr int kUnitReaders = 10;           // warps that read a posted unit
+constexpr int kUnitReaders = 11;           // warps that read a posted unit
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
 
@@ -61,6 +62,7 @@ struct Ctl {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t s_full[2];                    // per group: its tile's scores are in tensor memory
     uint64_t p_full[2];                    // per group: its weights are (and its O is rescaled)
+    uint64_t p_done[2];                    // per group: the value products on them have finished
     uint64_t o_done, o_free;               // a unit's last product has finished; its O has been read
     uint64_t stats_full, stats_free;       // the groups' statistics are posted, and read
     uint64_t unit_full[kUnits], unit_empty[kUnits];
@@ -74,11 +76,13 @@ static_assert(sizeof(Ctl) <= 1024, "control block overflows its space");
 
 // --- tcgen05 ------------------------------------------------------------------
 
-// Start address, leading and stride byte offsets (all >> 4), version 1, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)((lbo & 0x3FFFF) >> 4) << 16) |
-           ((uint64_t)((sbo & 0x3FFFF) >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory operand descriptors: start address and leading byte offset
+// (>> 4) in the low word; stride 1024 >> 4, version 1 and 128-byte swizzle in
+// the high one.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+    return ((addr & 0x3FFFF) >> 4) | ((lbo >> 4) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // kind::f16: fp32 accumulator, A and B bf16, A K-major, B K-major or (b_mn) MN-major.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, int b_mn) {
@@ -86,17 +90,21 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, int b_mn) {
            ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+        "n"(kDescHi));
 }
 
 // A operand from tensor memory: rows in lanes, two bf16 values per column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+        "n"(kDescHi));
 }
 
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -178,7 +186,7 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
 }
 
 // A whole warp's bounded wait; gives up, too, once another role has.
-__device__ __noinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* status) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* status) {
 #pragma unroll 1
     for (int i = 0; i < kMaxProbes; ++i) {
         if (__all_sync(0xffffffffu, pa::mbar_try_wait(bar, parity))) return true;
@@ -217,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&ctl->s_full[i], 1);
             pa::mbar_init(&ctl->p_full[i], 128);
+            pa::mbar_init(&ctl->p_done[i], 1);
         }
         pa::mbar_init(&ctl->o_done, 1);
         pa::mbar_init(&ctl->o_free, 256);
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ctl->abort = 0;
         pa::fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(pa::smem_addr(&ctl->tmem)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -337,15 +346,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kStages && i < done; ++i)
                 pa::mbar_wait_bounded(&full[(done - 1 - i) % kStages], ((done - 1 - i) / kStages) & 1, kMaxProbes);
         }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ products
-        constexpr uint32_t id_s = idesc_bf16(128, kKv, 0), id_o = idesc_bf16(128, D, 1);
-        uint64_t* last = nullptr;
-        uint32_t last_parity = 0;
-        int ns = 0, nv = 0, nth = 0;                             // score tiles, value tiles, units so far
-        int npf[2] = {0, 0};                                     // weights of each group so far
+    } else if (warp == kScoreWarp) {
+        // ------------------------------------------------------------ score products
+        // One thread takes about 125 cycles to issue a product of 64: the score
+        // and the value products have an issuer each.
+        constexpr uint32_t idesc = idesc_bf16(128, kKv, 0);
+        const uint32_t q_lo = desc_lo(s0, 16);
+        int at = 0;                                              // tiles so far
+        int np[2] = {0, 0};                                      // and each group's
         bool ok = true;
-        for (; ok; ++nth) {
+        for (int nth = 0; ok; ++nth) {
+            const int slot = nth % kUnits;
+            if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
+            const int valid = ctl->units[slot].valid, len = ctl->units[slot].len;
+            __syncwarp();
+            if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
+            if (!valid) break;
+            if (!wait_for(&ctl->q_full, nth & 1, ctl, a.status)) break;
+            for (int j = 0; j < len; ++j, ++at) {
+                const int st = at % kStages, w = j & 1;
+                // the scores go over the group's weights of before: their value products have to be done
+                ok = wait_for(&ctl->k_full[st], (at / kStages) & 1, ctl, a.status) &&
+                     (np[w] == 0 || wait_for(&ctl->p_done[w], (np[w] - 1) & 1, ctl, a.status));
+                if (!ok) break;
+                ++np[w];
+                fence_after();
+                if (lane == 0) {
+                    const uint32_t k_lo = desc_lo(s0 + G::kK0 + st * G::kTileBytes, 16);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * G::kHalfBytes + (kk & 3) * 32) >> 4;
+                        mma_ss(tmem + w * 128, q_lo + off, k_lo + off, idesc, kk > 0);
+                    }
+                    commit(&ctl->s_full[w]);
+                    commit(&ctl->k_empty[st]);
+                    if (j == len - 1) commit(&ctl->q_empty);
+                }
+                __syncwarp();
+            }
+        }
+        // products in flight finish before the tensor memory is freed
+        if (lane == 0 && at > 0)
+            pa::mbar_wait_bounded(&ctl->k_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
+    } else if (warp == kValueWarp) {
+        // ------------------------------------------------------------ value products
+        constexpr uint32_t idesc = idesc_bf16(128, D, 1);
+        int at = 0;                                              // tiles so far
+        int np[2] = {0, 0};                                      // and each group's
+        bool ok = true;
+        for (int nth = 0; ok; ++nth) {
             const int slot = nth % kUnits;
             if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
             const Unit* u = &ctl->units[slot];
@@ -353,34 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
             if (!valid) break;
-            if (!(ok = wait_for(&ctl->q_full, nth & 1, ctl, a.status))) break;
-            // scores of tile j (in tensor memory of group j & 1, whose weights of tile j - 2 are used up:
-            // products run in the order of their issue)
-            auto scores = [&](int j) {
-                const int st = ns % kStages;
-                if (!wait_for(&ctl->k_full[st], (ns / kStages) & 1, ctl, a.status)) return false;
-                fence_after();
-                if (lane == 0) {
-                    const uint32_t k0 = s0 + G::kK0 + st * G::kTileBytes;
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * G::kHalfBytes + (kk & 3) * 32;
-                        mma_ss(tmem + (j & 1) * 128, smem_desc(s0 + off, 16, 1024), smem_desc(k0 + off, 16, 1024), id_s,
-                               kk > 0);
-                    }
-                    commit(&ctl->s_full[j & 1]);
-                    commit(&ctl->k_empty[st]);
-                    if (j == len - 1) commit(&ctl->q_empty);
-                }
-                __syncwarp();
-                ++ns;
-                return true;
-            };
-            ok = scores(0) && (len < 2 || scores(1));
-            for (int j = 0; ok && j < len; ++j) {
-                const int st = nv % kStages, w = j & 1;
-                if (!(ok = wait_for(&ctl->v_full[st], (nv / kStages) & 1, ctl, a.status))) break;
-                const uint32_t v0 = s0 + G::kV0 + st * G::kTileBytes;
+            // the unit before has read its O out
+            if (nth >= 1 && !wait_for(&ctl->o_free, (nth - 1) & 1, ctl, a.status)) break;
+            for (int j = 0; j < len; ++j, ++at) {
+                const int st = at % kStages, w = j & 1;
+                if (!(ok = wait_for(&ctl->v_full[st], (at / kStages) & 1, ctl, a.status))) break;
+                const uint32_t v_lo = desc_lo(s0 + G::kV0 + st * G::kTileBytes, G::kHalfBytes);
                 const int left = min(kKv, ctx - (st0 + j) * kKv), steps = (left + 15) >> 4;
                 if (left & 15) {
                     // rows left .. 16 * steps - 1 of the tile are past the context: zeros
@@ -392,35 +419,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                // the unit before has read its O out
-                if (j == 0 && nth >= 1 && !(ok = wait_for(&ctl->o_free, (nth - 1) & 1, ctl, a.status))) break;
-                if (!(ok = wait_for(&ctl->p_full[w], npf[w] & 1, ctl, a.status))) break;
-                ++npf[w];
+                if (!(ok = wait_for(&ctl->p_full[w], np[w] & 1, ctl, a.status))) break;
+                ++np[w];
                 fence_after();
                 if (lane == 0) {
                     const uint32_t t_p = tmem + w * 128, t_o = tmem + kTmemO + w * 128;
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma_ts(t_o, t_p + kk * 8, smem_desc(v0 + kk * 2048, G::kHalfBytes, 1024), id_o,
-                               (j > 1 || kk > 0) ? 1u : 0u);
-                    if (!kDup)
-                        for (int kk = 0; kk < steps; ++kk)
-                            mma_ts(t_o, t_p + kKv / 2 + kk * 8, smem_desc(v0 + kk * 2048, G::kHalfBytes, 1024), id_o, 1u);
+#pragma unroll
+                    for (int kk = 0; kk < kKv / 16; ++kk)
+                        if (kk < steps) mma_ts(t_o, t_p + kk * 8, v_lo + kk * (2048 >> 4), idesc, (j > 1 || kk > 0) ? 1u : 0u);
+                    if (!kDup) {
+#pragma unroll
+                        for (int kk = 0; kk < kKv / 16; ++kk)
+                            if (kk < steps) mma_ts(t_o, t_p + kKv / 2 + kk * 8, v_lo + kk * (2048 >> 4), idesc, 1u);
+                    }
+                    commit(&ctl->p_done[w]);
                     commit(&ctl->v_empty[st]);
-                    last = &ctl->v_empty[st];
-                    last_parity = (nv / kStages) & 1;
                     if (j == len - 1) commit(&ctl->o_done);
                 }
                 __syncwarp();
-                ++nv;
-                if (j + 2 < len) ok = scores(j + 2);
             }
         }
-        // products in flight finish before the tensor memory is freed (a score product that no value
-        // product followed: its tile's commit)
-        if (lane == 0) {
-            if (last) pa::mbar_wait_bounded(last, last_parity, kMaxProbes);
-            if (ns) pa::mbar_wait_bounded(&ctl->k_empty[(ns - 1) % kStages], ((ns - 1) / kStages) & 1, kMaxProbes);
-        }
+        if (lane == 0 && at > 0)
+            pa::mbar_wait_bounded(&ctl->v_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
     } else {
         // ------------------------------------------------------------ softmax: group w takes tiles j = w, w + 2, ...
         const int w = warp >> 2, quarter = warp & 3;
@@ -597,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
