@@ -13,8 +13,8 @@
 //    tiles the first and odd ones the second, each with its own scores,
 //    running statistics and output accumulator in tensor memory (S0, S1, O0,
 //    O1: all 512 columns).  So a thread owns a whole row of its tiles and
-//    exchanges nothing until a unit's end, where the two accumulators are
-//    merged exactly.
+//    exchanges nothing until a unit's end, where four more warps merge the two
+//    accumulators exactly while the groups go on to the next unit.
 //  * V stays bf16, so the weights enter P . V as two bf16 terms (hi + lo, a
 //    relative 2^-16).  Up to 64 rows the 128 lanes of a product hold each
 //    row twice, 16 lanes apart, one with the hi and one with the lo terms: a
@@ -35,9 +35,10 @@ constexpr int kKWarp = 8;                  // walks the share, loads K
 constexpr int kVWarp = 9;                  // loads q (free when its unit's last scores are done) and V
 constexpr int kScoreWarp = 10;             // issues the score products and owns the tensor memory
 constexpr int kValueWarp = 11;             // issues the value products
-constexpr int kThreads = 384;
+constexpr int kOutWarp = 12;               // 12 .. 15 read the accumulators out at a unit's end
+constexpr int kThreads = 512;
 constexpr int kUnits = 4;                  // units posted ahead
-constexpr int kUnitReaders = 11;           // warps that read a posted unit
+constexpr int kUnitReaders = 15;           // warps that read a posted unit
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
 
@@ -228,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             pa::mbar_init(&ctl->p_done[i], 1);
         }
         pa::mbar_init(&ctl->o_done, 1);
-        pa::mbar_init(&ctl->o_free, 256);
+        pa::mbar_init(&ctl->o_free, 128);
         pa::mbar_init(&ctl->stats_full, 256);
-        pa::mbar_init(&ctl->stats_free, 256);
+        pa::mbar_init(&ctl->stats_free, 128);
         for (int i = 0; i < kUnits; ++i) {
             pa::mbar_init(&ctl->unit_full[i], 1);
             pa::mbar_init(&ctl->unit_empty[i], kUnitReaders);
@@ -426,11 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t t_p = tmem + w * 128, t_o = tmem + kTmemO + w * 128;
 #pragma unroll
                     for (int kk = 0; kk < kKv / 16; ++kk)
-                        if (kk < steps) mma_ts(t_o, t_p + kk * 8, v_lo + kk * (2048 >> 4), idesc, (j > 1 || kk > 0) ? 1u : 0u);
+                        if (kk < steps) mma_ts(t_o, t_p + 32 * (kk >> 1) + 8 * (kk & 1), v_lo + kk * (2048 >> 4), idesc, (j > 1 || kk > 0) ? 1u : 0u);
                     if (!kDup) {
 #pragma unroll
                         for (int kk = 0; kk < kKv / 16; ++kk)
-                            if (kk < steps) mma_ts(t_o, t_p + kKv / 2 + kk * 8, v_lo + kk * (2048 >> 4), idesc, 1u);
+                            if (kk < steps) mma_ts(t_o, t_p + 32 * (kk >> 1) + 16 + 8 * (kk & 1), v_lo + kk * (2048 >> 4), idesc, 1u);
                     }
                     commit(&ctl->p_done[w]);
                     commit(&ctl->v_empty[st]);
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0 && at > 0)
             pa::mbar_wait_bounded(&ctl->v_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
-    } else {
+    } else if (warp < kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax: group w takes tiles j = w, w + 2, ...
         const int w = warp >> 2, quarter = warp & 3;
         const int tl = quarter * 32 + lane;                      // tensor-memory lane
@@ -456,50 +457,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nth = 0; ok; ++nth) {
             const int slot = nth % kUnits;
             if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
-            const Unit u = ctl->units[slot];
+            const Unit* u = &ctl->units[slot];
+            if (!u->valid) break;                                // (the rest of it is not set then)
+            const int len = u->len, t_first = u->st0 * kKv, first = u->first;
+            const int i = (u->row0 + r) >> a.log2_group;
+            const bool real = i < u->n, tree = u->words != nullptr;
+            // what the row sees of the new tokens: a word (tree), or positions below `lim`
+            unsigned long long word = tree && real ? u->words[i] : ~0ull;
+            if (u->n < 64) word &= (1ull << u->n) - 1;
+            const int lim = (tree || !real) ? u->ctx : first + i + 1;
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
-            if (!u.valid) break;
-            const int i = (u.row0 + r) >> a.log2_group;
-            const bool real = i < u.n;
-            // what the row sees of the new tokens: a word (tree), or those below `lim` positions
-            unsigned long long word = ~0ull;
-            if (u.words && real) word = u.words[i];
-            if (u.n < 64) word &= (1ull << u.n) - 1;
-            const int lim = (u.words || !real) ? u.ctx : u.first + i + 1;
+            // the positions from `start` on that the row sees, as 32 bits
+            auto seen = [&](int start) {
+                const int n = lim - start, b = start - first;
+                uint32_t v = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+                if (tree)
+                    v &= b <= -32 ? ~0u
+                         : b < 0  ? (uint32_t)(word << -b) | ((1u << -b) - 1u)
+                         : b < 64 ? (uint32_t)(word >> b)
+                                  : 0u;
+                return v;
+            };
             float m = kNone, l = 0.f;
-            for (int j = w; ok && j < u.len; j += 2, ++tiles) {
+            for (int j = w; j < len; j += 2, ++tiles) {
                 if (!(ok = wait_for(&ctl->s_full[w], tiles & 1, ctl, a.status))) break;
                 fence_after();
-                float s[kKv];
+                const int t0 = t_first + j * kKv;
+                const bool tail = t0 + kKv > first;              // some row may not see some position
+                // 32 columns of scores, masked
+                auto load = [&](int x, float (&s)[32]) {
+                    ld32(t_s + 32 * x, s);
+                    wait_ld();
+                    if (tail) {
+                        const uint32_t v = seen(t0 + 32 * x);
+                        if (__any_sync(0xffffffffu, v != ~0u)) {
 #pragma unroll
-                for (int x = 0; x < kKv / 32; ++x) ld32(t_s + 32 * x, s + 32 * x);
-                wait_ld();
-                const int t0 = (u.st0 + j) * kKv;
-                if (t0 + kKv > u.first) {
-                    const int end = lim - t0;
-#pragma unroll
-                    for (int x = 0; x < kKv; ++x) s[x] = x < end ? s[x] : -INFINITY;
-                    if (u.words) {
-                        const int j0 = t0 - u.first;
-#pragma unroll
-                        for (int x = 0; x < kKv; ++x) {
-                            const int b = j0 + x;
-                            if (b >= 0 && (b > 63 || !(word >> b & 1ull))) s[x] = -INFINITY;
+                            for (int k = 0; k < 32; ++k) s[k] = (v & (1u << k)) ? s[k] : -INFINITY;
                         }
                     }
-                }
+                };
                 float top = -INFINITY;
-                {
-                    float p[8];
+#pragma unroll 2
+                for (int x = 0; x < kKv / 32; ++x) {
+                    float s[32], p[8];
+                    load(x, s);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) p[k] = s[k];
-#pragma unroll
-                    for (int x = 8; x < kKv; x += 8)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) p[k] = fmaxf(p[k], s[x + k]);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) top = fmaxf(top, p[k]);
+                    for (int k = 0; k < 8; ++k) p[k] = fmaxf(fmaxf(s[k], s[k + 8]), fmaxf(s[k + 16], s[k + 24]));
+                    top = fmaxf(top, fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7]))));
                 }
                 if (kDup) top = __shfl_sync(0xffffffffu, top, lane & 15);   // a row's two lanes decide as one
                 const bool raise = fmaf(top, c, -m) > kRaise;
@@ -507,39 +512,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j > w && __any_sync(0xffffffffu, raise)) {
                     // this group's O holds its tiles before j: their products finished before these scores
                     const float f = pa::exp2_approx(m - m_new);
-                    const uint64_t ff = pair(f, f);
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 16) {
-                        float o[16];
-                        uint32_t t = t_o + x;
-                        asm volatile(
-                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                            : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]),
-                              "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
-                            : "r"(t));
+                    for (int x = 0; x < D; x += 32) {
+                        float o[32];
+                        ld32(t_o + x, o);
                         wait_ld();
-                        uint32_t v[16];
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            float y0, y1;
-                            split(fma2(pair(o[k], o[k + 1]), ff, pair(0.f, 0.f)), y0, y1);
-                            v[k] = __float_as_uint(y0);
-                            v[k + 1] = __float_as_uint(y1);
-                        }
-                        st16(t, v);
+                        for (int k = 0; k < 32; ++k) o[k] *= f;
+                        st32(t_o + x, o);
                     }
                     l *= f;
                 }
                 m = m_new;
                 const uint64_t neg = pair(-m, -m);
                 uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
+                // the weights of 32 columns go over their scores: hi terms in 16 columns, lo terms (two
+                // products) in the other 16
+#pragma unroll 2
                 for (int x = 0; x < kKv / 32; ++x) {
+                    float s[32];
+                    load(x, s);
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         float y0, y1;
-                        split(fma2(pair(s[32 * x + 2 * k], s[32 * x + 2 * k + 1]), cc, neg), y0, y1);
+                        split(fma2(pair(s[2 * k], s[2 * k + 1]), cc, neg), y0, y1);
                         const float p0 = pa::exp2_approx(y0), p1 = pa::exp2_approx(y1);
                         const uint64_t p = pair(p0, p1);
                         sum[k & 1] = add2(sum[k & 1], p);
@@ -549,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lo[k] = pa::pack_bf16x2(r0, r1);
                         if (kDup && is_lo) hi[k] = lo[k];
                     }
-                    st16(t_s + 16 * x, hi);
-                    if (!kDup) st16(t_s + kKv / 2 + 16 * x, lo);
+                    st16(t_s + 32 * x, hi);
+                    if (!kDup) st16(t_s + 32 * x + 16, lo);
                 }
                 float a0, a1, b0, b1;
                 split(sum[0], a0, a1);
@@ -561,55 +558,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pa::mbar_arrive(&ctl->p_full[w]);
             }
             if (!ok) break;
-            // ---- the unit's end: both groups' statistics, then half of the columns each ----
-            if (nth >= 1 && !(ok = wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status))) break;
+            if (nth >= 1 && !wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status)) break;
             stats[w * 128 + tl] = make_float2(m, l);
             pa::mbar_arrive(&ctl->stats_full);
-            if (!(ok = wait_for(&ctl->stats_full, nth & 1, ctl, a.status))) break;
+        }
+    } else {
+        // ------------------------------------------------------------ a unit's end: the two accumulators, merged exactly
+        const int quarter = warp & 3, tl = quarter * 32 + lane;
+        const int r = kDup ? quarter * 16 + (lane & 15) : tl;
+        const bool is_lo = kDup && (lane & 16);
+        const uint32_t t_o = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemO;
+        for (int nth = 0;; ++nth) {
+            const int slot = nth % kUnits;
+            if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
+            const Unit* u = &ctl->units[slot];
+            if (!u->valid) break;
+            const int st0 = u->st0;
+            const int row = u->row0 + r, i = row >> a.log2_group;
+            const bool real = i < u->n, whole = u->len == u->steps, odd = u->len > 1;   // one tile: O1 was not written
+            const size_t out_row = ((size_t)(u->q0 + i) * a.n_q_heads + (u->kvh << a.log2_group) + (row & (group - 1))) * D;
+            __syncwarp();
+            if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
+            if (!wait_for(&ctl->stats_full, nth & 1, ctl, a.status)) break;
             const float2 e = stats[tl], o = stats[128 + tl];
             pa::mbar_arrive(&ctl->stats_free);
-            const float M = fmaxf(e.x, o.x), fe = pa::exp2_approx(e.x - M), fo = pa::exp2_approx(o.x - M);
-            const float Z = fe * e.y + fo * o.y;
-            const bool whole = u.len == u.steps, odd = u.len > 1;   // one tile: O1 was not written
-            if (!(ok = wait_for(&ctl->o_done, nth & 1, ctl, a.status))) break;
-            fence_after();
+            const float M = fmaxf(e.x, o.x), Z0 = pa::exp2_approx(e.x - M), Z1 = pa::exp2_approx(o.x - M);
+            const float Z = Z0 * e.y + Z1 * o.y;
             const float by = whole ? (Z == 0.f ? 0.f : a.v_scale / Z) : 1.f;
-            const size_t at = (size_t)(2 * blockIdx.x + (u.st0 == 0 ? 1 : 0)) * kRows + r;
-            const size_t out_row = ((size_t)(u.q0 + i) * a.n_q_heads + (u.kvh << a.log2_group) +
-                                    ((u.row0 + r) & (group - 1))) * D;
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x) {
-                const int col = w * (D / 2) + 32 * x;
+            const float fe = Z0 * by, fo = Z1 * by;
+            const size_t at = (size_t)(2 * blockIdx.x + (st0 == 0 ? 1 : 0)) * kRows + r;
+            if (!wait_for(&ctl->o_done, nth & 1, ctl, a.status)) break;
+            fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
                 float v[32], v1[32];
-                ld32(t_lane + kTmemO + col, v);
-                ld32(t_lane + kTmemO + 128 + col, v1);
+                ld32(t_o + x, v);
+                ld32(t_o + 128 + x, v1);
                 wait_ld();
-                if (x == D / 64 - 1) {                           // O is in registers: the next unit's products may write it
+                if (x == D - 32) {                               // O is in registers: the next unit's products may write it
                     fence_before();
                     pa::mbar_arrive(&ctl->o_free);
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    v[k] = fe * v[k] + (odd ? fo * v1[k] : 0.f);
-                    if (kDup) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
-                    v[k] *= by;
+                for (int k = 0; k < 32; ++k) v[k] = fe * v[k] + (odd ? fo * v1[k] : 0.f);
+                float f[kDup ? 16 : 32];                         // of a row's two lanes, each writes half
+                if constexpr (kDup) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        // the other lane's terms of my half, for mine of its half
+                        const float other = __shfl_xor_sync(0xffffffffu, is_lo ? v[k] : v[k + 16], 16);
+                        f[k] = (is_lo ? v[k + 16] : v[k]) + other;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) f[k] = v[k];
                 }
                 if (real) {
-                    constexpr int kMine = kDup ? 16 : 32;        // of a row's two lanes, each writes half
-                    const int c0 = kDup && is_lo ? 16 : 0;
+                    const int col = x + (is_lo ? 16 : 0);
 #pragma unroll
-                    for (int k = 0; k < kMine; k += 4) {
-                        const float4 f = kDup && is_lo
-                                             ? make_float4(v[(16 + k) & 31], v[(17 + k) & 31], v[(18 + k) & 31], v[(19 + k) & 31])
-                                             : make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    for (int k = 0; k < (kDup ? 16 : 32); k += 4) {
+                        const float4 y = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
                         if (whole)
-                            put4(a.out, a.out_f32, out_row + col + c0 + k, f);
+                            put4(a.out, a.out_f32, out_row + col + k, y);
                         else
-                            *reinterpret_cast<float4*>(a.part_u + at * D + col + c0 + k) = f;
+                            *reinterpret_cast<float4*>(a.part_u + at * D + col + k) = y;
                     }
                 }
             }
-            if (!whole && real && w == 0 && !is_lo) {
+            if (!whole && real && !is_lo) {
                 a.part_m[at] = M;
                 a.part_z[at] = Z;
             }

@@ -219,6 +219,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
 // (pa_decode_wide.cu); cudaSuccess or the launch's error.
 cudaError_t launch_wide(int rows, int d_head, const void* q, int block_size, const CUtensorMap& map_k,
                         const CUtensorMap& map_v, const MultiArgs& a, int grid, cudaStream_t st);
-constexpr int kWideCost = 2, kWideMinSteps = 2, kWideStep = 128;
+constexpr int kWideCost = 4, kWideMinSteps = 2, kWideStep = 128;
 
 }  // namespace pa_multi
