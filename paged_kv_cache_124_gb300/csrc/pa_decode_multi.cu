@@ -578,11 +578,19 @@ int sms() {
     return n;
 }
 
+#ifndef PA_F8_WIDE_FROM
+#define PA_F8_WIDE_FROM 17
+#endif
+// Whether the units of 64 (or 128) rows of pa_decode_wide.cu serve a call.
+// They take a positive scale (bf16) and measured faster from more than 32
+// rows a KV head on for bf16 caches, more than 16 for E4M3.
+bool is_wide(bool f8, float scale, long long rows) { return f8 ? rows >= PA_F8_WIDE_FROM : scale > 0.f && rows > 32; }
+
 // Rows of a unit: the fewest that hold all rows of a KV head, at most 64, or
-// 128 where the wide kernel runs.
-int unit_rows(int max_query_len, int group, bool wide) {
-    const long long rows = (long long)max_query_len * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || !wide ? 64 : 128;
+// 128 for bf16 on the wide kernel.
+int unit_rows(long long rows, bool f8, bool wide) {
+    if (wide) return f8 || rows <= 64 ? 64 : 128;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 // Resident blocks of the device.
@@ -640,11 +648,11 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
         return PA_ERR_MISALIGNED;
     const long long cache_rows = (long long)num_blocks * n_kv_heads * block_size;
     if (cache_rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-    // The wide kernel (bf16 caches, more than 32 rows) takes the scale's sign as positive.
-    const bool wide = !f8 && scale > 0.f && (long long)max_query_len * group > 32;
-    const int unit = unit_rows(max_query_len, group, wide);
+    const long long all_rows = (long long)max_query_len * group;
+    const bool wide = is_wide(f8, scale, all_rows);
+    const int unit = unit_rows(all_rows, f8, wide);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
-    const int most = max_grid(unit);
+    const int most = wide ? sms() : max_grid(unit);
     if (most <= 0) return PA_ERR_CUDA;
     if (workspace_bytes < workspace_size(most, unit, d_head)) return PA_ERR_WORKSPACE;
 
@@ -653,7 +661,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     a.ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
     // no more blocks than the largest possible work has smallest shares
     const int step = wide ? kWideStep : kStep, cost = wide ? kWideCost : kUnitCost;
-    const long long tiles = ((long long)max_query_len * group + unit - 1) / unit;
+    const long long tiles = (all_rows + unit - 1) / unit;
     const long long seq_work = ((long long)a.ctx_cap + step - 1) / step + cost;
     const double work = (double)num_seqs * n_kv_heads * (double)tiles * (double)seq_work;
     const double shares = work / ((wide ? kWideMinSteps : kMinSteps) + cost) + 1;
@@ -678,7 +686,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     const float factor = fabsf(scale) * kLog2e * (f8 ? k_scale : 1.f);
     a.scale_log2 = factor == 0.f ? 1.f : factor;                // masked scores are -inf times it
     a.q_sign = factor == 0.f ? 0.f : scale > 0.f ? 1.f : -1.f;
-    a.v_scale = f8 ? v_scale / kWeightScale : 1.f;
+    a.v_scale = !f8 ? 1.f : wide ? v_scale : v_scale / kWeightScale;   // (the wide kernel's sums carry its weights' factor)
     a.out_f32 = out_dtype == PA_DTYPE_F32;
     a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     a.n_q_heads = n_q_heads;
@@ -698,7 +706,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc;
     if (wide)
-        rc = launch_wide(unit, d_head, q, block_size, mk, mv, a, grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        rc = launch_wide(unit, d_head, f8, q, block_size, mk, mv, a, grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     else
         rc = f8 ? launch_rows<128, true>(unit, mk, mv, a, grid, st)
              : d_head == 128 ? launch_rows<128, false>(unit, mk, mv, a, grid, st)
@@ -716,8 +724,16 @@ extern "C" {
 
 size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads, int n_kv_heads, int d_head) {
     if (max_query_len <= 0 || n_kv_heads <= 0 || n_q_heads < n_kv_heads || d_head <= 0) return 0;
-    const int unit = unit_rows(max_query_len, n_q_heads / n_kv_heads, true);   // the largest that a call may take
-    return workspace_size(max_grid(unit), unit, d_head);
+    // one size for whichever kernel a call of this shape takes
+    const long long rows = (long long)max_query_len * (n_q_heads / n_kv_heads);
+    size_t most = 0;
+    for (int x = 0; x < 4; ++x) {
+        const bool f8 = x & 1, wide = is_wide(f8, x & 2 ? 1.f : -1.f, rows);
+        const int unit = unit_rows(rows, f8, wide);
+        const size_t n = workspace_size(wide ? sms() : max_grid(unit), unit, d_head);
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 int pa_decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache,

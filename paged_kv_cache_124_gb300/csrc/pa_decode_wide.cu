@@ -42,18 +42,23 @@ constexpr int kUnitReaders = 15;           // warps that read a posted unit
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
 
-template <int D, bool kDup>
+// kHalf: units of 64 rows, in lanes 0-15 of each 32 of a product, the other
+// lanes taking a second term of their weights; else 128.  F8: E4M3 caches.
+template <int D, bool kHalf, bool F8>
 struct Wide {
-    static constexpr int kRows = kDup ? 64 : 128;
-    static constexpr int kHalves = D / 64;
-    static constexpr int kHalfBytes = 128 * 128;                 // 128 rows of 64 bf16, 128-byte swizzle
-    static constexpr int kTileBytes = kHalves * kHalfBytes;      // q, or K or V of a tile
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kK0 = kTileBytes;
+    static_assert(!F8 || (kHalf && D == 128), "E4M3 caches: 64 rows, d_head 128");
+    static constexpr int kRows = kHalf ? 64 : 128;
+    static constexpr int kHalves = F8 ? 1 : D / 64;              // 128-byte columns of a cache row
+    static constexpr int kHalfBytes = 128 * 128;                 // 128 rows of 128 bytes, 128-byte swizzle
+    static constexpr int kTileBytes = kHalves * kHalfBytes;      // K or V of a tile
+    static constexpr int kQBytes = F8 ? 2 * kHalfBytes : kTileBytes;   // q; F8: its two E4M3 terms
+    static constexpr int kStages = F8 || D == 64 ? 6 : 3;
+    static constexpr int kK0 = kQBytes;
     static constexpr int kV0 = kK0 + kStages * kTileBytes;
-    static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][lane] maximum and sum
+    static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][row] maximum and sum; F8: then row factors
     static constexpr int kCtl = kStats + 2 * 128 * 8;
     static constexpr int kSmem = kCtl + 1024;
+    static constexpr int kStepKeys = F8 ? 32 : 16;               // positions of one value product
 };
 
 constexpr int kMaxStages = 6;
@@ -85,27 +90,43 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-// kind::f16: fp32 accumulator, A and B bf16, A K-major, B K-major or (b_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+// fp32 accumulator, A K-major, B K-major or (b_mn) MN-major; A and B bf16 (kind::f16) or E4M3 (kind::f8f6f4).
+__host__ __device__ constexpr uint32_t idesc(bool f8, int m, int n, int b_mn) {
+    return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
 
+template <bool F8>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
-        "n"(kDescHi));
+    if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+            "n"(kDescHi));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+            "n"(kDescHi));
 }
 
-// A operand from tensor memory: rows in lanes, two bf16 values per column.
+// A operand from tensor memory: rows in lanes, two bf16 or four E4M3 values per column.
+template <bool F8>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 y, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
-        "n"(kDescHi));
+    if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "mov.b64 y, {%2, %5};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+            "n"(kDescHi));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "mov.b64 y, {%2, %5};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+            "n"(kDescHi));
 }
 
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -151,6 +172,54 @@ __device__ __forceinline__ void st16(uint32_t t, const uint32_t* w) {
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
         "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]));
+}
+
+// Lanes 0-15 of the warp's 32 (or 16-31, with 16 added to the lane of t):
+// thread x < 16 gets 32 columns of lane x from t on, thread x + 16 those 64
+// columns further.
+__device__ __forceinline__ void ld32_split64(uint32_t t, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 64;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The like for stores: 16 columns, the second half 32 columns further, ...
+__device__ __forceinline__ void st16_split32(uint32_t t, const uint32_t* w) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], 32, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]));
+}
+
+// ... and 8 columns, the second half 16 further.
+__device__ __forceinline__ void st8_split16(uint32_t t, const uint32_t* w) {
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], 16, {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]));
+}
+
+// f16 pairs to E4M3 code pairs (round to nearest, saturating) and back (exact).
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int x, int head, int token, uint64_t* bar) {
@@ -201,11 +270,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ct
     return false;
 }
 
-template <int D, bool kDup>
+template <int D, bool kHalf, bool F8>
 __global__ void __launch_bounds__(kThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const MultiArgs a, int oob_row) {
-    using G = Wide<D, kDup>;
+    using G = Wide<D, kHalf, F8>;
     constexpr int kRows = G::kRows, kStages = G::kStages;
     extern __shared__ __align__(1024) uint8_t sm[];
     Ctl* ctl = reinterpret_cast<Ctl*>(sm + G::kCtl);
@@ -215,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int B = 1 << a.log2_block, group = 1 << a.log2_group;
 
     if (threadIdx.x == 0) {
-        pa::mbar_init(&ctl->q_full, 1);
+        pa::mbar_init(&ctl->q_full, F8 ? 128 : 1);
         pa::mbar_init(&ctl->q_empty, 1);
         for (int i = 0; i < kStages; ++i) {
             pa::mbar_init(&ctl->k_full[i], 1);
@@ -243,6 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(pa::smem_addr(&ctl->tmem)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if constexpr (F8) {
+        // rows of q that no lane 0-15 holds: zeros, so that their scores are finite
+        for (int x = threadIdx.x; x < G::kQBytes / 16; x += kThreads) reinterpret_cast<uint4*>(sm)[x] = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     fence_before();
     __syncthreads();
@@ -285,16 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
                 if (!u->valid) break;
-                if (nth >= 1 && !(ok = wait_for(&ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
-                if (lane == 0) {
-                    // 16 rows a box: 16 / group tokens of the group's heads
-                    pa::mbar_arrive_expect_tx(&ctl->q_full, G::kTileBytes);
-                    for (int r = 0; r < 128; r += 16) {
-                        const int row = u->row0 + (kDup ? r >> 5 << 4 : r);
+                if constexpr (!F8) {
+                    if (nth >= 1 && !(ok = wait_for(&ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
+                    if (lane == 0) {
+                        // 16 rows a box: 16 / group tokens of the group's heads
+                        pa::mbar_arrive_expect_tx(&ctl->q_full, kRows * 128 * G::kHalves);
+                        for (int r = 0; r < kRows; r += 16) {
 #pragma unroll
-                        for (int h = 0; h < G::kHalves; ++h)
-                            tma_q(s0 + h * G::kHalfBytes + r * 128, &map_q, h * 64, u->kvh << a.log2_group,
-                                  u->q0 + (row >> a.log2_group), &ctl->q_full);
+                            for (int h = 0; h < G::kHalves; ++h)
+                                tma_q(s0 + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
+                                      u->kvh << a.log2_group, u->q0 + ((u->row0 + r) >> a.log2_group), &ctl->q_full);
+                        }
                     }
                 }
             }
@@ -343,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the copies this warp started land before the block exits
         if (lane == 0) {
-            if (!is_k && nth > 0) pa::mbar_wait_bounded(&ctl->q_full, (nth - 1) & 1, kMaxProbes);
+            if (!F8 && !is_k && nth > 0) pa::mbar_wait_bounded(&ctl->q_full, (nth - 1) & 1, kMaxProbes);
             for (int i = 0; i < kStages && i < done; ++i)
                 pa::mbar_wait_bounded(&full[(done - 1 - i) % kStages], ((done - 1 - i) / kStages) & 1, kMaxProbes);
         }
@@ -351,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ score products
         // One thread takes about 125 cycles to issue a product of 64: the score
         // and the value products have an issuer each.
-        constexpr uint32_t idesc = idesc_bf16(128, kKv, 0);
+        constexpr uint32_t id = idesc(F8, 128, kKv, 0);
         const uint32_t q_lo = desc_lo(s0, 16);
         int at = 0;                                              // tiles so far
         int np[2] = {0, 0};                                      // and each group's
@@ -374,10 +449,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_after();
                 if (lane == 0) {
                     const uint32_t k_lo = desc_lo(s0 + G::kK0 + st * G::kTileBytes, 16);
+                    if constexpr (F8) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * G::kHalfBytes + (kk & 3) * 32) >> 4;
-                        mma_ss(tmem + w * 128, q_lo + off, k_lo + off, idesc, kk > 0);
+                        for (int x = 0; x < 8; ++x)               // both terms of q, 32 of d_head at a time
+                            mma_ss<true>(tmem + w * 128, q_lo + (((x >> 2) * G::kHalfBytes + (x & 3) * 32) >> 4),
+                                         k_lo + (((x & 3) * 32) >> 4), id, x > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * G::kHalfBytes + (kk & 3) * 32) >> 4;
+                            mma_ss<false>(tmem + w * 128, q_lo + off, k_lo + off, id, kk > 0);
+                        }
                     }
                     commit(&ctl->s_full[w]);
                     commit(&ctl->k_empty[st]);
@@ -391,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             pa::mbar_wait_bounded(&ctl->k_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
     } else if (warp == kValueWarp) {
         // ------------------------------------------------------------ value products
-        constexpr uint32_t idesc = idesc_bf16(128, D, 1);
+        constexpr uint32_t id = idesc(F8, 128, D, 1);
+        constexpr int kStepKeys = G::kStepKeys;
         int at = 0;                                              // tiles so far
         int np[2] = {0, 0};                                      // and each group's
         bool ok = true;
@@ -409,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = at % kStages, w = j & 1;
                 if (!(ok = wait_for(&ctl->v_full[st], (at / kStages) & 1, ctl, a.status))) break;
                 const uint32_t v_lo = desc_lo(s0 + G::kV0 + st * G::kTileBytes, G::kHalfBytes);
-                const int left = min(kKv, ctx - (st0 + j) * kKv), steps = (left + 15) >> 4;
-                if (left & 15) {
-                    // rows left .. 16 * steps - 1 of the tile are past the context: zeros
-                    for (int x = lane; x < (16 * steps - left) * G::kHalves * 8; x += 32) {
+                const int left = min(kKv, ctx - (st0 + j) * kKv), steps = (left + kStepKeys - 1) / kStepKeys;
+                if (left % kStepKeys) {
+                    // the tile's rows from `left` to the end of the last product are past the context: zeros
+                    for (int x = lane; x < (kStepKeys * steps - left) * G::kHalves * 8; x += 32) {
                         const int r = left + x / (G::kHalves * 8), c = x % (G::kHalves * 8);
                         *reinterpret_cast<uint4*>(sm + G::kV0 + st * G::kTileBytes + (c >> 3) * G::kHalfBytes + r * 128 +
                                                   (c & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -425,13 +508,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_after();
                 if (lane == 0) {
                     const uint32_t t_p = tmem + w * 128, t_o = tmem + kTmemO + w * 128;
+                    // weights of product kk (x: their second set): see the softmax
+                    auto product = [&](int kk, int x) {
+                        const uint32_t t = F8 ? 8 * kk + 32 * x : kHalf ? 8 * kk : 32 * (kk >> 1) + 8 * (kk & 1) + 16 * x;
+                        mma_ts<F8>(t_o, t_p + t, v_lo + kk * ((kStepKeys * 128) >> 4), id, (j > 1 || kk > 0 || x > 0) ? 1u : 0u);
+                    };
 #pragma unroll
-                    for (int kk = 0; kk < kKv / 16; ++kk)
-                        if (kk < steps) mma_ts(t_o, t_p + 32 * (kk >> 1) + 8 * (kk & 1), v_lo + kk * (2048 >> 4), idesc, (j > 1 || kk > 0) ? 1u : 0u);
-                    if (!kDup) {
+                    for (int kk = 0; kk < kKv / kStepKeys; ++kk)
+                        if (kk < steps) product(kk, 0);
+                    if (F8 || !kHalf) {
 #pragma unroll
-                        for (int kk = 0; kk < kKv / 16; ++kk)
-                            if (kk < steps) mma_ts(t_o, t_p + 32 * (kk >> 1) + 16 + 8 * (kk & 1), v_lo + kk * (2048 >> 4), idesc, 1u);
+                        for (int kk = 0; kk < kKv / kStepKeys; ++kk)
+                            if (kk < steps) product(kk, 1);
                     }
                     commit(&ctl->p_done[w]);
                     commit(&ctl->v_empty[st]);
@@ -445,13 +533,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax: group w takes tiles j = w, w + 2, ...
         const int w = warp >> 2, quarter = warp & 3;
-        const int tl = quarter * 32 + lane;                      // tensor-memory lane
-        const int r = kDup ? quarter * 16 + (lane & 15) : tl;    // row of the unit
-        const bool is_lo = kDup && (lane & 16);
+        const int r = kHalf ? quarter * 16 + (lane & 15) : quarter * 32 + lane;   // row of the unit
+        const int half = kHalf ? lane >> 4 : 0;                  // 64-row units: which 64 of a tile's columns
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t t_s = t_lane + w * 128, t_o = t_lane + kTmemO + w * 128;
-        const float c = a.scale_log2;
-        const uint64_t cc = pair(c, c);
+        const float* factors = reinterpret_cast<const float*>(stats + 128);   // F8: [unit parity][row]
+        constexpr float kSlack = F8 ? 0.5f : kRaise;             // F8: weights of at most 2^8.5 in E4M3's 448
+        constexpr float kUp = F8 ? 8.f : 0.f;                    // log2 of the weights' common factor
         int tiles = 0;                                           // this group's tiles so far
         bool ok = true;
         for (int nth = 0; ok; ++nth) {
@@ -479,35 +567,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   : 0u;
                 return v;
             };
-            float m = kNone, l = 0.f;
+            float m = kNone, l = 0.f, c = a.scale_log2;
+            if constexpr (F8) {
+                if (!wait_for(&ctl->q_full, nth & 1, ctl, a.status)) break;   // the rows' factors come with q
+                c = factors[(nth & 1) * 64 + r];
+            }
             for (int j = w; j < len; j += 2, ++tiles) {
                 if (!(ok = wait_for(&ctl->s_full[w], tiles & 1, ctl, a.status))) break;
                 fence_after();
                 const int t0 = t_first + j * kKv;
                 const bool tail = t0 + kKv > first;              // some row may not see some position
-                // 32 columns of scores, masked
-                auto load = [&](int x, float (&s)[32]) {
-                    ld32(t_s + 32 * x, s);
-                    wait_ld();
+                auto mask = [&](int start, float* s) {
                     if (tail) {
-                        const uint32_t v = seen(t0 + 32 * x);
+                        const uint32_t v = seen(start);
                         if (__any_sync(0xffffffffu, v != ~0u)) {
 #pragma unroll
                             for (int k = 0; k < 32; ++k) s[k] = (v & (1u << k)) ? s[k] : -INFINITY;
                         }
                     }
                 };
-                float top = -INFINITY;
-#pragma unroll 2
-                for (int x = 0; x < kKv / 32; ++x) {
-                    float s[32], p[8];
-                    load(x, s);
+                auto top32 = [&](const float* s) {
+                    float p[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) p[k] = fmaxf(fmaxf(s[k], s[k + 8]), fmaxf(s[k + 16], s[k + 24]));
-                    top = fmaxf(top, fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7]))));
+                    return fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+                };
+                float s64[kHalf ? 64 : 1];                       // 64-row units: the thread's columns
+                float top;
+                if constexpr (kHalf) {
+                    ld32_split64(t_s, s64);
+                    ld32_split64(t_s + 32, s64 + 32);
+                    wait_ld();
+                    mask(t0 + 64 * half, s64);
+                    mask(t0 + 64 * half + 32, s64 + 32);
+                    top = fmaxf(top32(s64), top32(s64 + 32));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                } else {
+                    top = -INFINITY;
+#pragma unroll 2
+                    for (int x = 0; x < kKv / 32; ++x) {
+                        float s[32];
+                        ld32(t_s + 32 * x, s);
+                        wait_ld();
+                        mask(t0 + 32 * x, s);
+                        top = fmaxf(top, top32(s));
+                    }
                 }
-                if (kDup) top = __shfl_sync(0xffffffffu, top, lane & 15);   // a row's two lanes decide as one
-                const bool raise = fmaf(top, c, -m) > kRaise;
+                const bool raise = fmaf(top, c, -m) > kSlack;
                 const float m_new = raise ? top * c : m;
                 if (j > w && __any_sync(0xffffffffu, raise)) {
                     // this group's O holds its tiles before j: their products finished before these scores
@@ -524,30 +630,81 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= f;
                 }
                 m = m_new;
-                const uint64_t neg = pair(-m, -m);
+                const uint64_t cc = pair(c, c), neg = pair(kUp - m, kUp - m);
                 uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-                // the weights of 32 columns go over their scores: hi terms in 16 columns, lo terms (two
-                // products) in the other 16
-#pragma unroll 2
-                for (int x = 0; x < kKv / 32; ++x) {
-                    float s[32];
-                    load(x, s);
-                    uint32_t hi[16], lo[16];
+                // two columns' weights, summed
+                auto weights = [&](float x0, float x1, int k) {
+                    float y0, y1;
+                    split(fma2(pair(x0, x1), cc, neg), y0, y1);
+                    const uint64_t p = pair(pa::exp2_approx(y0), pa::exp2_approx(y1));
+                    sum[k & 1] = add2(sum[k & 1], p);
+                    return p;
+                };
+                // the bf16 terms of two weights
+                auto terms = [&](uint64_t p, uint32_t& hi, uint32_t& lo) {
+                    float p0, p1, r0, r1;
+                    split(p, p0, p1);
+                    hi = pa::pack_bf16x2(p0, p1);
+                    split(sub2(p, pair(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u))), r0, r1);
+                    lo = pa::pack_bf16x2(r0, r1);
+                };
+                constexpr uint32_t kLanes16 = 16u << 16;
+                if constexpr (F8) {
+                    // Weights as f16 (11 significant bits) and then as three E4M3 terms of 4 bits each, which
+                    // hold them exactly down to 2^-10 (2^-18 of the row's largest): the first two in a
+                    // product's two lanes of a row, the third in a second product's, whose other lane is zero.
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float y0, y1;
-                        split(fma2(pair(s[2 * k], s[2 * k + 1]), cc, neg), y0, y1);
-                        const float p0 = pa::exp2_approx(y0), p1 = pa::exp2_approx(y1);
-                        const uint64_t p = pair(p0, p1);
-                        sum[k & 1] = add2(sum[k & 1], p);
-                        hi[k] = pa::pack_bf16x2(p0, p1);
-                        float r0, r1;
-                        split(sub2(p, pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xffff0000u))), r0, r1);
-                        lo[k] = pa::pack_bf16x2(r0, r1);
-                        if (kDup && is_lo) hi[k] = lo[k];
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t t[3][8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t cell[3] = {0, 0, 0};
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float p0, p1;
+                                split(weights(s64[32 * y + 4 * k + 2 * e], s64[32 * y + 4 * k + 2 * e + 1], e), p0, p1);
+                                uint32_t h = pa::pack_f16x2(p0, p1);
+#pragma unroll
+                                for (int x = 0; x < 3; ++x) {
+                                    const uint32_t code = f16x2_to_e4m3x2(h);
+                                    cell[x] |= code << (16 * e);
+                                    if (x < 2) h = sub_f16x2(h, e4m3x2_to_f16x2(code));
+                                }
+                            }
+#pragma unroll
+                            for (int x = 0; x < 3; ++x) t[x][k] = cell[x];
+                        }
+                        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                        st8_split16(t_s + 8 * y, t[0]);
+                        st8_split16(t_s + kLanes16 + 8 * y, t[1]);
+                        st8_split16(t_s + 32 + 8 * y, t[2]);
+                        st8_split16(t_s + kLanes16 + 32 + 8 * y, zero);
                     }
-                    st16(t_s + 32 * x, hi);
-                    if (!kDup) st16(t_s + 32 * x + 16, lo);
+                } else if constexpr (kHalf) {
+                    // hi terms in a row's first lane, lo terms in its second: columns 0-63
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            terms(weights(s64[32 * y + 2 * k], s64[32 * y + 2 * k + 1], k), hi[k], lo[k]);
+                        st16_split32(t_s + 16 * y, hi);
+                        st16_split32(t_s + kLanes16 + 16 * y, lo);
+                    }
+                } else {
+                    // over each 32 columns of scores: the hi terms of their weights in 16, the lo terms in 16
+#pragma unroll 2
+                    for (int x = 0; x < kKv / 32; ++x) {
+                        float s[32];
+                        ld32(t_s + 32 * x, s);
+                        wait_ld();
+                        mask(t0 + 32 * x, s);
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) terms(weights(s[2 * k], s[2 * k + 1], k), hi[k], lo[k]);
+                        st16(t_s + 32 * x, hi);
+                        st16(t_s + 32 * x + 16, lo);
+                    }
                 }
                 float a0, a1, b0, b1;
                 split(sum[0], a0, a1);
@@ -559,14 +716,79 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             if (nth >= 1 && !wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status)) break;
-            stats[w * 128 + tl] = make_float2(m, l);
+            if (kHalf) l += __shfl_xor_sync(0xffffffffu, l, 16);
+            if (!half) stats[w * kRows + r] = make_float2(m, l);
             pa::mbar_arrive(&ctl->stats_full);
         }
     } else {
         // ------------------------------------------------------------ a unit's end: the two accumulators, merged exactly
-        const int quarter = warp & 3, tl = quarter * 32 + lane;
-        const int r = kDup ? quarter * 16 + (lane & 15) : tl;
-        const bool is_lo = kDup && (lane & 16);
+        const int quarter = warp & 3;
+        const int r = kHalf ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
+        const bool second = kHalf && (lane & 16);                // a row's second lane
+        // E4M3 caches: these warps make q's two terms too.  A bf16 value is the sum of two E4M3 values
+        // (8 significant bits, 4 and 4), after a power of two per row that brings its largest into
+        // [2^7, 2^8); below 2^-16 of that, within 2^-18 of it.
+        auto make_q = [&](const Unit* u, int parity) {
+            const int t = threadIdx.x - 32 * kOutWarp, row = t >> 1, part = t & 1, at = u->row0 + row, i = at >> a.log2_group;
+            uint4 v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                v[x] = make_uint4(0, 0, 0, 0);
+                if (i < u->n)
+                    v[x] = *reinterpret_cast<const uint4*>(
+                        a.q + ((size_t)(u->q0 + i) * a.n_q_heads + (u->kvh << a.log2_group) + (at & (group - 1))) * D + 64 * part + 8 * x);
+            }
+            return [=](uint8_t* smem, float* fac) {
+                float top = 0.f;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t wd[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = pa::bf16x2_to_float2(wd[e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                int eb = (__float_as_int(top) >> 23) & 0xff;
+                eb = eb < 7 ? 7 : (eb > 254 ? 254 : eb);
+                const float up = __int_as_float((261 - eb) << 23), by = up * a.q_sign;
+                if (part == 0) fac[parity * 64 + row] = fmaxf(a.scale_log2 / up, 1e-37f);
+                const int line = (row >> 4) * 32 + (row & 15);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {                    // 16 elements: a 16-byte chunk of each term
+                    uint32_t c0[4], c1[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 q = v[2 * x + (e >> 1)];
+                        const uint32_t w0 = e & 1 ? q.z : q.x, w1 = e & 1 ? q.w : q.y;
+                        uint32_t a0[2], a1[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float2 f = pa::bf16x2_to_float2(y ? w1 : w0);
+                            const float f0 = f.x * by, f1 = f.y * by;
+                            a0[y] = pa::e4m3x2(f0, f1);
+                            const uint32_t h = e4m3x2_to_f16x2(a0[y]);
+                            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                            a1[y] = pa::e4m3x2(f0 - g.x, f1 - g.y);
+                        }
+                        c0[e] = a0[0] | (a0[1] << 16);
+                        c1[e] = a1[0] | (a1[1] << 16);
+                    }
+                    uint8_t* dst = smem + line * 128 + (((4 * part + x) ^ (line & 7)) << 4);
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
+                    *reinterpret_cast<uint4*>(dst + G::kHalfBytes) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            };
+        };
+        float* factors = reinterpret_cast<float*>(stats + 128);
+        if constexpr (F8) {
+            if (wait_for(&ctl->unit_full[0], 0, ctl, a.status) && ctl->units[0].valid) {
+                make_q(&ctl->units[0], 0)(sm, factors);
+                pa::mbar_arrive(&ctl->q_full);
+            }
+        }
         const uint32_t t_o = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemO;
         for (int nth = 0;; ++nth) {
             const int slot = nth % kUnits;
@@ -579,8 +801,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t out_row = ((size_t)(u->q0 + i) * a.n_q_heads + (u->kvh << a.log2_group) + (row & (group - 1))) * D;
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
+            if constexpr (F8) {
+                // the next unit's q, once this one's last scores are done
+                const int ahead = (nth + 1) % kUnits;
+                if (!wait_for(&ctl->unit_full[ahead], ((nth + 1) / kUnits) & 1, ctl, a.status)) break;
+                if (ctl->units[ahead].valid) {
+                    auto store = make_q(&ctl->units[ahead], (nth + 1) & 1);
+                    if (!wait_for(&ctl->q_empty, nth & 1, ctl, a.status)) break;
+                    store(sm, factors);
+                    pa::mbar_arrive(&ctl->q_full);
+                }
+            }
             if (!wait_for(&ctl->stats_full, nth & 1, ctl, a.status)) break;
-            const float2 e = stats[tl], o = stats[128 + tl];
+            const float2 e = stats[r], o = stats[kRows + r];
             pa::mbar_arrive(&ctl->stats_free);
             const float M = fmaxf(e.x, o.x), Z0 = pa::exp2_approx(e.x - M), Z1 = pa::exp2_approx(o.x - M);
             const float Z = Z0 * e.y + Z1 * o.y;
@@ -601,22 +834,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = fe * v[k] + (odd ? fo * v1[k] : 0.f);
-                float f[kDup ? 16 : 32];                         // of a row's two lanes, each writes half
-                if constexpr (kDup) {
+                float f[kHalf ? 16 : 32];                         // of a row's two lanes, each writes half
+                if constexpr (kHalf) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        // the other lane's terms of my half, for mine of its half
-                        const float other = __shfl_xor_sync(0xffffffffu, is_lo ? v[k] : v[k + 16], 16);
-                        f[k] = (is_lo ? v[k + 16] : v[k]) + other;
+                        // the other lane's sums of my half of the columns, for mine of its half
+                        const float other = __shfl_xor_sync(0xffffffffu, second ? v[k] : v[k + 16], 16);
+                        f[k] = (second ? v[k + 16] : v[k]) + other;
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) f[k] = v[k];
                 }
                 if (real) {
-                    const int col = x + (is_lo ? 16 : 0);
+                    const int col = x + (second ? 16 : 0);
 #pragma unroll
-                    for (int k = 0; k < (kDup ? 16 : 32); k += 4) {
+                    for (int k = 0; k < (kHalf ? 16 : 32); k += 4) {
                         const float4 y = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
                         if (whole)
                             put4(a.out, a.out_f32, out_row + col + k, y);
@@ -625,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!whole && real && !is_lo) {
+            if (!whole && real && !second) {
                 a.part_m[at] = M;
                 a.part_z[at] = Z;
             }
@@ -653,29 +886,31 @@ bool q_view(CUtensorMap* map, const void* q, int num_tokens, int n_q_heads, int 
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kDup>
+template <int D, bool kHalf, bool F8>
 cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& a, int oob_row,
                    int grid, cudaStream_t st) {
     static int attr[64] = {0};
-    const cudaError_t e = pa_host::ensure_smem_attr(wide_kernel<D, kDup>, Wide<D, kDup>::kSmem, attr);
+    constexpr int kSmem = Wide<D, kHalf, F8>::kSmem;
+    const cudaError_t e = pa_host::ensure_smem_attr(wide_kernel<D, kHalf, F8>, kSmem, attr);
     if (e != cudaSuccess) return e;
-    return pa_host::launch_dependent(wide_kernel<D, kDup>, dim3(grid), dim3(kThreads), Wide<D, kDup>::kSmem, st, mq, mk,
-                                     mv, a, oob_row);
+    return pa_host::launch_dependent(wide_kernel<D, kHalf, F8>, dim3(grid), dim3(kThreads), kSmem, st, mq, mk, mv, a,
+                                     oob_row);
 }
 
 }  // namespace
 
 namespace pa_multi {
 
-cudaError_t launch_wide(int rows, int d_head, const void* q, int block_size, const CUtensorMap& mk,
+cudaError_t launch_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& mk,
                         const CUtensorMap& mv, const MultiArgs& a, int grid, cudaStream_t st) {
+    const int oob = a.num_blocks * a.n_kv_heads * block_size;    // one past the view's last row
+    if (f8) return launch<128, true, true>(mk, mk, mv, a, oob, grid, st);   // (its q is not copied as it is)
     CUtensorMap mq;
     if (!q_view(&mq, q, a.num_tokens, a.n_q_heads, d_head, 1 << a.log2_group)) return cudaErrorInvalidValue;
-    const int oob = a.num_blocks * a.n_kv_heads * block_size;    // one past the view's last row
-    return d_head == 128 ? (rows == 64 ? launch<128, true>(mq, mk, mv, a, oob, grid, st)
-                                       : launch<128, false>(mq, mk, mv, a, oob, grid, st))
-                         : (rows == 64 ? launch<64, true>(mq, mk, mv, a, oob, grid, st)
-                                       : launch<64, false>(mq, mk, mv, a, oob, grid, st));
+    return d_head == 128 ? (rows == 64 ? launch<128, true, false>(mq, mk, mv, a, oob, grid, st)
+                                       : launch<128, false, false>(mq, mk, mv, a, oob, grid, st))
+                         : (rows == 64 ? launch<64, true, false>(mq, mk, mv, a, oob, grid, st)
+                                       : launch<64, false, false>(mq, mk, mv, a, oob, grid, st));
 }
 
 }  // namespace pa_multi

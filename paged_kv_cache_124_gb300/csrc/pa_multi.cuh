@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
 
 // Launches of the 64- and 128-row units on the 5th-generation tensor cores
 // (pa_decode_wide.cu); cudaSuccess or the launch's error.
-cudaError_t launch_wide(int rows, int d_head, const void* q, int block_size, const CUtensorMap& map_k,
+cudaError_t launch_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& map_k,
                         const CUtensorMap& map_v, const MultiArgs& a, int grid, cudaStream_t st);
 constexpr int kWideCost = 4, kWideMinSteps = 2, kWideStep = 128;
 
