@@ -96,38 +96,39 @@ __host__ __device__ constexpr uint32_t idesc(bool f8, int m, int n, int b_mn) {
            ((uint32_t)(m >> 4) << 24);
 }
 
-template <bool F8>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    if constexpr (F8)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
-            "n"(kDescHi));
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
-            "n"(kDescHi));
-}
+// D = A . B (+ D if acc: a constant predicate where the compiler knows it).
+#define PA_MMA(kind, a_op, setup)                                                                     \
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t" setup           \
+                 "mov.b64 y, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::" kind " [%0], " a_op ", y, %3, p;\n\t}" ::"r"(d), \
+                 "r"(a), "r"(b), "r"(id), "r"(acc), "n"(kDescHi))
+#define PA_MMA_ADD(kind, a_op, setup)                                                                 \
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.eq.b32 p, 0, 0;\n\t" setup            \
+                 "mov.b64 y, {%2, %4};\n\ttcgen05.mma.cta_group::1.kind::" kind " [%0], " a_op ", y, %3, p;\n\t}" ::"r"(d), \
+                 "r"(a), "r"(b), "r"(id), "n"(kDescHi))
 
+template <bool F8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    if constexpr (F8) PA_MMA("f8f6f4", "x", "mov.b64 x, {%1, %5};\n\t");
+    else PA_MMA("f16", "x", "mov.b64 x, {%1, %5};\n\t");
+}
+template <bool F8>
+__device__ __forceinline__ void mma_ss_add(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+    if constexpr (F8) PA_MMA_ADD("f8f6f4", "x", "mov.b64 x, {%1, %4};\n\t");
+    else PA_MMA_ADD("f16", "x", "mov.b64 x, {%1, %4};\n\t");
+}
 // A operand from tensor memory: rows in lanes, two bf16 or four E4M3 values per column.
 template <bool F8>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    if constexpr (F8)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "mov.b64 y, {%2, %5};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
-            "n"(kDescHi));
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "mov.b64 y, {%2, %5};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
-            "n"(kDescHi));
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    if constexpr (F8) PA_MMA("f8f6f4", "[%1]", "");
+    else PA_MMA("f16", "[%1]", "");
 }
+template <bool F8>
+__device__ __forceinline__ void mma_ts_add(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+    if constexpr (F8) PA_MMA_ADD("f8f6f4", "[%1]", "");
+    else PA_MMA_ADD("f16", "[%1]", "");
+}
+#undef PA_MMA
+#undef PA_MMA_ADD
 
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(pa::smem_addr(bar))
@@ -267,6 +268,19 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ct
         pa::set_status(status, PA_DEV_WAIT_TIMEOUT);
     }
     __syncwarp();
+    return false;
+}
+
+// One thread's bounded wait for two barriers.
+__device__ __forceinline__ bool wait_both(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, Ctl* ctl, int32_t* status) {
+#pragma unroll 1
+    for (int i = 0; i < kMaxProbes; ++i) {
+        const bool a = pa::mbar_try_wait(x, px), b = pa::mbar_try_wait(y, py);
+        if (a && b) return true;
+        if ((i & 63) == 63 && *reinterpret_cast<volatile int*>(&ctl->abort)) return false;
+    }
+    *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+    pa::set_status(status, PA_DEV_WAIT_TIMEOUT);
     return false;
 }
 
@@ -424,48 +438,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kScoreWarp) {
         // ------------------------------------------------------------ score products
-        // One thread takes about 125 cycles to issue a product of 64: the score
-        // and the value products have an issuer each.
+        // (An issuing thread's time goes into its chain of instructions, about
+        // 100 cycles a product of 64: the score and the value products have an
+        // issuer each, and one thread waits for all that a tile needs at once.)
         constexpr uint32_t id = idesc(F8, 128, kKv, 0);
-        const uint32_t q_lo = desc_lo(s0, 16);
+        const uint32_t q_lo = desc_lo(s0, 16), k_lo0 = desc_lo(s0 + G::kK0, 16);
         int at = 0;                                              // tiles so far
-        int np[2] = {0, 0};                                      // and each group's
-        bool ok = true;
-        for (int nth = 0; ok; ++nth) {
-            const int slot = nth % kUnits;
-            if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
-            const int valid = ctl->units[slot].valid, len = ctl->units[slot].len;
-            __syncwarp();
-            if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
-            if (!valid) break;
-            if (!wait_for(&ctl->q_full, nth & 1, ctl, a.status)) break;
-            for (int j = 0; j < len; ++j, ++at) {
-                const int st = at % kStages, w = j & 1;
-                // the scores go over the group's weights of before: their value products have to be done
-                ok = wait_for(&ctl->k_full[st], (at / kStages) & 1, ctl, a.status) &&
-                     (np[w] == 0 || wait_for(&ctl->p_done[w], (np[w] - 1) & 1, ctl, a.status));
-                if (!ok) break;
-                ++np[w];
-                fence_after();
-                if (lane == 0) {
-                    const uint32_t k_lo = desc_lo(s0 + G::kK0 + st * G::kTileBytes, 16);
+        if (lane == 0) {
+            int np[2] = {0, 0};                                  // and each group's
+            int st = 0, phase = 0;
+            bool ok = true;
+            for (int nth = 0; ok; ++nth) {
+                const int slot = nth % kUnits;
+                uint64_t* posted = &ctl->unit_full[slot];
+                if (!wait_both(posted, (nth / kUnits) & 1, posted, (nth / kUnits) & 1, ctl, a.status)) break;
+                const int valid = ctl->units[slot].valid, len = ctl->units[slot].len;
+                pa::mbar_arrive(&ctl->unit_empty[slot]);
+                if (!valid) break;
+                if (!wait_both(&ctl->q_full, nth & 1, &ctl->k_full[st], phase, ctl, a.status)) break;
+                for (int j = 0; j < len; ++j, ++at) {
+                    const int w = j & 1, n = w ? np[1] : np[0];
+                    // the scores go over the group's weights of before: their value products have to be done
+                    uint64_t* kf = &ctl->k_full[st];
+                    if (!(ok = n ? wait_both(kf, phase, &ctl->p_done[w], (n - 1) & 1, ctl, a.status)
+                                 : wait_both(kf, phase, kf, phase, ctl, a.status)))
+                        break;
+                    np[0] += 1 - w;
+                    np[1] += w;
+                    fence_after();
+                    const uint32_t k_lo = k_lo0 + st * (G::kTileBytes >> 4), d = tmem + w * 128;
                     if constexpr (F8) {
+                        mma_ss<true>(d, q_lo, k_lo, id, 0);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)               // both terms of q, 32 of d_head at a time
-                            mma_ss<true>(tmem + w * 128, q_lo + (((x >> 2) * G::kHalfBytes + (x & 3) * 32) >> 4),
-                                         k_lo + (((x & 3) * 32) >> 4), id, x > 0);
+                        for (int x = 1; x < 8; ++x)               // both terms of q, 32 of d_head at a time
+                            mma_ss_add<true>(d, q_lo + (((x >> 2) * G::kHalfBytes + (x & 3) * 32) >> 4),
+                                             k_lo + (((x & 3) * 32) >> 4), id);
                     } else {
+                        mma_ss<false>(d, q_lo, k_lo, id, 0);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
+                        for (int kk = 1; kk < D / 16; ++kk) {
                             const uint32_t off = ((kk >> 2) * G::kHalfBytes + (kk & 3) * 32) >> 4;
-                            mma_ss<false>(tmem + w * 128, q_lo + off, k_lo + off, id, kk > 0);
+                            mma_ss_add<false>(d, q_lo + off, k_lo + off, id);
                         }
                     }
                     commit(&ctl->s_full[w]);
                     commit(&ctl->k_empty[st]);
                     if (j == len - 1) commit(&ctl->q_empty);
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
-                __syncwarp();
             }
         }
         // products in flight finish before the tensor memory is freed
@@ -475,8 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ value products
         constexpr uint32_t id = idesc(F8, 128, D, 1);
         constexpr int kStepKeys = G::kStepKeys;
+        const uint32_t v_lo0 = desc_lo(s0 + G::kV0, G::kHalfBytes);
         int at = 0;                                              // tiles so far
         int np[2] = {0, 0};                                      // and each group's
+        int st = 0, phase = 0;
         bool ok = true;
         for (int nth = 0; ok; ++nth) {
             const int slot = nth % kUnits;
@@ -489,12 +514,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the unit before has read its O out
             if (nth >= 1 && !wait_for(&ctl->o_free, (nth - 1) & 1, ctl, a.status)) break;
             for (int j = 0; j < len; ++j, ++at) {
-                const int st = at % kStages, w = j & 1;
-                if (!(ok = wait_for(&ctl->v_full[st], (at / kStages) & 1, ctl, a.status))) break;
-                const uint32_t v_lo = desc_lo(s0 + G::kV0 + st * G::kTileBytes, G::kHalfBytes);
+                const int w = j & 1;
+                ok = lane || wait_both(&ctl->v_full[st], phase, &ctl->p_full[w], (w ? np[1] : np[0]) & 1, ctl, a.status);
+                if (!__shfl_sync(0xffffffffu, (int)ok, 0)) {
+                    ok = false;
+                    break;
+                }
+                np[0] += 1 - w;
+                np[1] += w;
                 const int left = min(kKv, ctx - (st0 + j) * kKv), steps = (left + kStepKeys - 1) / kStepKeys;
                 if (left % kStepKeys) {
                     // the tile's rows from `left` to the end of the last product are past the context: zeros
+                    // (lane 0's wait, and the barrier above, order the copies before these writes)
                     for (int x = lane; x < (kStepKeys * steps - left) * G::kHalves * 8; x += 32) {
                         const int r = left + x / (G::kHalves * 8), c = x % (G::kHalves * 8);
                         *reinterpret_cast<uint4*>(sm + G::kV0 + st * G::kTileBytes + (c >> 3) * G::kHalfBytes + r * 128 +
@@ -503,29 +534,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (!(ok = wait_for(&ctl->p_full[w], np[w] & 1, ctl, a.status))) break;
-                ++np[w];
-                fence_after();
                 if (lane == 0) {
-                    const uint32_t t_p = tmem + w * 128, t_o = tmem + kTmemO + w * 128;
+                    fence_after();
+                    const uint32_t t_p = tmem + w * 128, t_o = tmem + kTmemO + w * 128, v_lo = v_lo0 + st * (G::kTileBytes >> 4);
                     // weights of product kk (x: their second set): see the softmax
-                    auto product = [&](int kk, int x) {
-                        const uint32_t t = F8 ? 8 * kk + 32 * x : kHalf ? 8 * kk : 32 * (kk >> 1) + 8 * (kk & 1) + 16 * x;
-                        mma_ts<F8>(t_o, t_p + t, v_lo + kk * ((kStepKeys * 128) >> 4), id, (j > 1 || kk > 0 || x > 0) ? 1u : 0u);
+                    auto at_p = [&](int kk, int x) {
+                        return t_p + (F8 ? 8 * kk + 32 * x : kHalf ? 8 * kk : 32 * (kk >> 1) + 8 * (kk & 1) + 16 * x);
                     };
+                    auto at_v = [&](int kk) { return v_lo + kk * ((kStepKeys * 128) >> 4); };
+                    mma_ts<F8>(t_o, at_p(0, 0), at_v(0), id, j > 1 ? 1u : 0u);
 #pragma unroll
-                    for (int kk = 0; kk < kKv / kStepKeys; ++kk)
-                        if (kk < steps) product(kk, 0);
+                    for (int kk = 1; kk < kKv / kStepKeys; ++kk)
+                        if (kk < steps) mma_ts_add<F8>(t_o, at_p(kk, 0), at_v(kk), id);
                     if (F8 || !kHalf) {
 #pragma unroll
                         for (int kk = 0; kk < kKv / kStepKeys; ++kk)
-                            if (kk < steps) product(kk, 1);
+                            if (kk < steps) mma_ts_add<F8>(t_o, at_p(kk, 1), at_v(kk), id);
                     }
                     commit(&ctl->p_done[w]);
                     commit(&ctl->v_empty[st]);
                     if (j == len - 1) commit(&ctl->o_done);
                 }
-                __syncwarp();
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
         }
         if (lane == 0 && at > 0)
@@ -539,6 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_s = t_lane + w * 128, t_o = t_lane + kTmemO + w * 128;
         const float* factors = reinterpret_cast<const float*>(stats + 128);   // F8: [unit parity][row]
         constexpr float kSlack = F8 ? 0.5f : kRaise;             // F8: weights of at most 2^8.5 in E4M3's 448
+        constexpr float kHeadroom = F8 ? 2.f : 0.f;              // F8: a raise leaves room for the next ones (a raise
+                                                                 // at every growth cost 560 cycles in half the tiles)
         constexpr float kUp = F8 ? 8.f : 0.f;                    // log2 of the weights' common factor
         int tiles = 0;                                           // this group's tiles so far
         bool ok = true;
@@ -614,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const bool raise = fmaf(top, c, -m) > kSlack;
-                const float m_new = raise ? top * c : m;
+                const float m_new = raise ? fmaf(top, c, kHeadroom) : m;
                 if (j > w && __any_sync(0xffffffffu, raise)) {
                     // this group's O holds its tiles before j: their products finished before these scores
                     const float f = pa::exp2_approx(m - m_new);
@@ -651,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t kLanes16 = 16u << 16;
                 if constexpr (F8) {
                     // Weights as f16 (11 significant bits) and then as three E4M3 terms of 4 bits each, which
-                    // hold them exactly down to 2^-10 (2^-18 of the row's largest): the first two in a
+                    // hold them within 2^-10 (at most 2^-15 of the row's largest): the first two in a
                     // product's two lanes of a row, the third in a second product's, whose other lane is zero.
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
