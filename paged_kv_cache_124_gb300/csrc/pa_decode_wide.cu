@@ -7,21 +7,31 @@
 // d_head 128) takes an SM about 1.46 us of its share of the memory's rate,
 // and its products, S = Q . K^T and O += P . V at 128 rows, 0.33 us each: the
 // bytes bound it as long as copies, products and softmax overlap.
-//  * One block per SM walks its share.  Three stages each of K and V; a
-//    producer warp each fills them through the block table, one warp issues
-//    the score products and one the value products, and two groups of four warps take the tiles in turn, even
-//    tiles the first and odd ones the second, each with its own scores,
-//    running statistics and output accumulator in tensor memory (S0, S1, O0,
-//    O1: all 512 columns).  So a thread owns a whole row of its tiles and
-//    exchanges nothing until a unit's end, where four more warps merge the two
-//    accumulators exactly while the groups go on to the next unit.
-//  * V stays bf16, so the weights enter P . V as two bf16 terms (hi + lo, a
-//    relative 2^-16).  Up to 64 rows the 128 lanes of a product hold each
-//    row twice, 16 lanes apart, one with the hi and one with the lo terms: a
-//    single product does both, and the output adds the two lanes.  With 128
-//    rows they are two products.
+//  * One block per SM walks its share.  A producer warp each fills stages of
+//    K and V through the block table; one warp issues the score products of
+//    whole tiles, into two buffers in turn; two groups of four warps take the
+//    first and the second 64 positions of every tile, each with its own
+//    running statistics and, by an issuing warp of its own, its own output
+//    accumulator.  Scores and accumulators (S0, S1, O0, O1) fill the 512
+//    columns of tensor memory; weights are written over their scores.  The
+//    groups exchange nothing until a unit's end, where four more warps merge
+//    the two accumulators exactly while the groups go on to the next unit.
+//    (An issuing thread spends some 60 to 100 cycles on a product of 64 and a
+//    hand-over between warps 100 to 450, so what bounds the rate of tiles is
+//    the chain scores - softmax - values: two buffers and a chain of half a
+//    tile keep it under the memory's 2800 cycles a tile, E4M3's 1400.)
+//  * Every barrier is waited for in every phase, in order, by each of its
+//    waiters, so no wait can take an older phase's parity for its own.
+//  * bf16: V stays bf16, so the weights enter P . V as two bf16 terms (hi +
+//    lo, a relative 2^-16).  Units of 64 rows lie in lanes 0-15 of each 32:
+//    the hi terms there and the lo terms in the other 16 lanes, so a single
+//    product does both and the output adds the two lanes; a row's scores are
+//    read by two threads.  Units of 128 rows take two products.
+//  * E4M3: the codes are operands as they lie in the cache.  q is the exact
+//    sum of two E4M3 terms, in a row's two lanes, whose scores the softmax
+//    adds; weights are three E4M3 terms in two products.
 //  * V rows past the context are zeroed in shared memory before the last
-//    tile's product (0 * NaN).
+//    tile's products (0 * NaN).
 
 #include "pa_multi.cuh"
 
@@ -34,11 +44,13 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kKWarp = 8;                  // walks the share, loads K
 constexpr int kVWarp = 9;                  // loads q (free when its unit's last scores are done) and V
 constexpr int kScoreWarp = 10;             // issues the score products and owns the tensor memory
-constexpr int kValueWarp = 11;             // issues the value products
 constexpr int kOutWarp = 12;               // 12 .. 15 read the accumulators out at a unit's end
-constexpr int kThreads = 512;
+constexpr int kThreads = 544;
+// warps 11 and 16 issue the value products of groups 0 and 1
+__device__ __forceinline__ int value_group(int warp) { return warp == 11 ? 0 : warp == 16 ? 1 : -1; }
+constexpr int kHalfKv = kKv / 2;           // positions of a tile per group
 constexpr int kUnits = 4;                  // units posted ahead
-constexpr int kUnitReaders = 15;           // warps that read a posted unit
+constexpr int kUnitReaders = 16;           // warps that read a posted unit
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
 
@@ -51,7 +63,7 @@ struct Wide {
     static constexpr int kHalves = F8 ? 1 : D / 64;              // 128-byte columns of a cache row
     static constexpr int kHalfBytes = 128 * 128;                 // 128 rows of 128 bytes, 128-byte swizzle
     static constexpr int kTileBytes = kHalves * kHalfBytes;      // K or V of a tile
-    static constexpr int kQBytes = F8 ? 2 * kHalfBytes : kTileBytes;   // q; F8: its two E4M3 terms
+    static constexpr int kQBytes = kTileBytes;                   // F8: a row's two terms in its two lanes
     static constexpr int kStages = F8 || D == 64 ? 6 : 3;
     static constexpr int kK0 = kQBytes;
     static constexpr int kV0 = kK0 + kStages * kTileBytes;
@@ -66,9 +78,9 @@ constexpr int kMaxStages = 6;
 struct Ctl {
     uint64_t q_full, q_empty;
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-    uint64_t s_full[2];                    // per group: its tile's scores are in tensor memory
-    uint64_t p_full[2];                    // per group: its weights are (and its O is rescaled)
-    uint64_t p_done[2];                    // per group: the value products on them have finished
+    uint64_t s_full[2];                    // per buffer: a tile's scores are in tensor memory
+    uint64_t p_full[2][2];                 // per group and buffer: its weights are (and its O is rescaled)
+    uint64_t p_done[2];                    // per buffer: the value products on both groups' weights have finished
     uint64_t o_done, o_free;               // a unit's last product has finished; its O has been read
     uint64_t stats_full, stats_free;       // the groups' statistics are posted, and read
     uint64_t unit_full[kUnits], unit_empty[kUnits];
@@ -155,17 +167,12 @@ __device__ __forceinline__ void ld32(uint32_t t, float* v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void st32(uint32_t t, const float* v) {
-    uint32_t w[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+__device__ __forceinline__ void ld16(uint32_t t, uint32_t* r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
-        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
-        "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]), "r"(w[17]), "r"(w[18]),
-        "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]),
-        "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31]));
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t));
 }
 
 __device__ __forceinline__ void st16(uint32_t t, const uint32_t* w) {
@@ -176,13 +183,13 @@ __device__ __forceinline__ void st16(uint32_t t, const uint32_t* w) {
 }
 
 // Lanes 0-15 of the warp's 32 (or 16-31, with 16 added to the lane of t):
-// thread x < 16 gets 32 columns of lane x from t on, thread x + 16 those 64
+// thread x < 16 gets 32 columns of lane x from t on, thread x + 16 those 32
 // columns further.
-__device__ __forceinline__ void ld32_split64(uint32_t t, float* v) {
+__device__ __forceinline__ void ld32_split32(uint32_t t, float* v) {
     uint32_t r[32];
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 64;"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -192,17 +199,17 @@ __device__ __forceinline__ void ld32_split64(uint32_t t, float* v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The like for stores: 16 columns, the second half 32 columns further, ...
-__device__ __forceinline__ void st16_split32(uint32_t t, const uint32_t* w) {
+// The like for stores: 16 columns, the second half 16 columns further, ...
+__device__ __forceinline__ void st16_split16(uint32_t t, const uint32_t* w) {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], 32, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], 16, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
         "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]));
 }
 
-// ... and 8 columns, the second half 16 further.
-__device__ __forceinline__ void st8_split16(uint32_t t, const uint32_t* w) {
-    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], 16, {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(w[0]),
+// ... and 8 columns, the second half 8 further.
+__device__ __forceinline__ void st8_split8(uint32_t t, const uint32_t* w) {
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], 8, {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]));
 }
 
@@ -271,12 +278,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ct
     return false;
 }
 
-// One thread's bounded wait for two barriers.
-__device__ __forceinline__ bool wait_both(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, Ctl* ctl, int32_t* status) {
+// One thread's.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* status) {
 #pragma unroll 1
     for (int i = 0; i < kMaxProbes; ++i) {
-        const bool a = pa::mbar_try_wait(x, px), b = pa::mbar_try_wait(y, py);
-        if (a && b) return true;
+        if (pa::mbar_try_wait(bar, parity)) return true;
         if ((i & 63) == 63 && *reinterpret_cast<volatile int*>(&ctl->abort)) return false;
     }
     *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
@@ -304,14 +310,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             pa::mbar_init(&ctl->k_full[i], 1);
             pa::mbar_init(&ctl->k_empty[i], 1);
             pa::mbar_init(&ctl->v_full[i], 1);
-            pa::mbar_init(&ctl->v_empty[i], 1);
+            pa::mbar_init(&ctl->v_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&ctl->s_full[i], 1);
-            pa::mbar_init(&ctl->p_full[i], 128);
-            pa::mbar_init(&ctl->p_done[i], 1);
+            pa::mbar_init(&ctl->p_full[0][i], 128);
+            pa::mbar_init(&ctl->p_full[1][i], 128);
+            pa::mbar_init(&ctl->p_done[i], 2);
         }
-        pa::mbar_init(&ctl->o_done, 1);
+        pa::mbar_init(&ctl->o_done, 2);
         pa::mbar_init(&ctl->o_free, 128);
         pa::mbar_init(&ctl->stats_full, 256);
         pa::mbar_init(&ctl->stats_free, 128);
@@ -326,11 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(pa::smem_addr(&ctl->tmem)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    if constexpr (F8) {
-        // rows of q that no lane 0-15 holds: zeros, so that their scores are finite
-        for (int x = threadIdx.x; x < G::kQBytes / 16; x += kThreads) reinterpret_cast<uint4*>(sm)[x] = make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     fence_before();
     __syncthreads();
@@ -437,51 +439,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pa::mbar_wait_bounded(&full[(done - 1 - i) % kStages], ((done - 1 - i) / kStages) & 1, kMaxProbes);
         }
     } else if (warp == kScoreWarp) {
-        // ------------------------------------------------------------ score products
-        // (An issuing thread's time goes into its chain of instructions, about
-        // 100 cycles a product of 64: the score and the value products have an
-        // issuer each, and one thread waits for all that a tile needs at once.)
+        // ------------------------------------------------------------ score products, by one thread
         constexpr uint32_t id = idesc(F8, 128, kKv, 0);
         const uint32_t q_lo = desc_lo(s0, 16), k_lo0 = desc_lo(s0 + G::kK0, 16);
-        int at = 0;                                              // tiles so far
         if (lane == 0) {
-            int np[2] = {0, 0};                                  // and each group's
-            int st = 0, phase = 0;
+            int at = 0, st = 0, phase = 0;                       // tiles so far; K's stage and phase
             bool ok = true;
             for (int nth = 0; ok; ++nth) {
                 const int slot = nth % kUnits;
-                uint64_t* posted = &ctl->unit_full[slot];
-                if (!wait_both(posted, (nth / kUnits) & 1, posted, (nth / kUnits) & 1, ctl, a.status)) break;
+                if (!wait_one(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
                 const int valid = ctl->units[slot].valid, len = ctl->units[slot].len;
                 pa::mbar_arrive(&ctl->unit_empty[slot]);
                 if (!valid) break;
-                if (!wait_both(&ctl->q_full, nth & 1, &ctl->k_full[st], phase, ctl, a.status)) break;
+                if (!wait_one(&ctl->q_full, nth & 1, ctl, a.status)) break;
                 for (int j = 0; j < len; ++j, ++at) {
-                    const int w = j & 1, n = w ? np[1] : np[0];
-                    // the scores go over the group's weights of before: their value products have to be done
-                    uint64_t* kf = &ctl->k_full[st];
-                    if (!(ok = n ? wait_both(kf, phase, &ctl->p_done[w], (n - 1) & 1, ctl, a.status)
-                                 : wait_both(kf, phase, kf, phase, ctl, a.status)))
+                    const int b = at & 1;
+                    // the scores go over weights of two tiles ago: their value products have to be done
+                    if (!(ok = wait_one(&ctl->k_full[st], phase, ctl, a.status) &&
+                               (at < 2 || wait_one(&ctl->p_done[b], ((at >> 1) - 1) & 1, ctl, a.status))))
                         break;
-                    np[0] += 1 - w;
-                    np[1] += w;
                     fence_after();
-                    const uint32_t k_lo = k_lo0 + st * (G::kTileBytes >> 4), d = tmem + w * 128;
-                    if constexpr (F8) {
-                        mma_ss<true>(d, q_lo, k_lo, id, 0);
+                    const uint32_t k_lo = k_lo0 + st * (G::kTileBytes >> 4), d = tmem + b * 128;
+                    mma_ss<F8>(d, q_lo, k_lo, id, 0);
 #pragma unroll
-                        for (int x = 1; x < 8; ++x)               // both terms of q, 32 of d_head at a time
-                            mma_ss_add<true>(d, q_lo + (((x >> 2) * G::kHalfBytes + (x & 3) * 32) >> 4),
-                                             k_lo + (((x & 3) * 32) >> 4), id);
-                    } else {
-                        mma_ss<false>(d, q_lo, k_lo, id, 0);
-#pragma unroll
-                        for (int kk = 1; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk >> 2) * G::kHalfBytes + (kk & 3) * 32) >> 4;
-                            mma_ss_add<false>(d, q_lo + off, k_lo + off, id);
-                        }
+                    for (int kk = 1; kk < D / (F8 ? 32 : 16); ++kk) {
+                        const uint32_t off = ((kk >> 2) * G::kHalfBytes + (kk & 3) * 32) >> 4;
+                        mma_ss_add<F8>(d, q_lo + off, k_lo + off, id);
                     }
-                    commit(&ctl->s_full[w]);
+                    commit(&ctl->s_full[b]);
                     commit(&ctl->k_empty[st]);
                     if (j == len - 1) commit(&ctl->q_empty);
                     if (++st == kStages) {
@@ -490,18 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            // products in flight finish before the tensor memory is freed
+            if (at > 0) pa::mbar_wait_bounded(&ctl->k_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
         }
-        // products in flight finish before the tensor memory is freed
-        if (lane == 0 && at > 0)
-            pa::mbar_wait_bounded(&ctl->k_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
-    } else if (warp == kValueWarp) {
-        // ------------------------------------------------------------ value products
+        __syncwarp();
+    } else if (value_group(warp) >= 0) {
+        // ------------------------------------------------------------ value products of group w
         constexpr uint32_t id = idesc(F8, 128, D, 1);
-        constexpr int kStepKeys = G::kStepKeys;
-        const uint32_t v_lo0 = desc_lo(s0 + G::kV0, G::kHalfBytes);
-        int at = 0;                                              // tiles so far
-        int np[2] = {0, 0};                                      // and each group's
-        int st = 0, phase = 0;
+        constexpr int kStepKeys = G::kStepKeys, kSteps = kHalfKv / kStepKeys, kSets = F8 || !kHalf ? 2 : 1;
+        const int w = value_group(warp);
+        const uint32_t t_o = tmem + kTmemO + w * 128;
+        const uint32_t v_lo0 = desc_lo(s0 + G::kV0 + w * kHalfKv * 128, G::kHalfBytes);
+        int at = 0, st = 0, phase = 0;                           // tiles so far; V's stage and phase
         bool ok = true;
         for (int nth = 0; ok; ++nth) {
             const int slot = nth % kUnits;
@@ -514,20 +499,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the unit before has read its O out
             if (nth >= 1 && !wait_for(&ctl->o_free, (nth - 1) & 1, ctl, a.status)) break;
             for (int j = 0; j < len; ++j, ++at) {
-                const int w = j & 1;
-                ok = lane || wait_both(&ctl->v_full[st], phase, &ctl->p_full[w], (w ? np[1] : np[0]) & 1, ctl, a.status);
-                if (!__shfl_sync(0xffffffffu, (int)ok, 0)) {
-                    ok = false;
-                    break;
-                }
-                np[0] += 1 - w;
-                np[1] += w;
-                const int left = min(kKv, ctx - (st0 + j) * kKv), steps = (left + kStepKeys - 1) / kStepKeys;
-                if (left % kStepKeys) {
-                    // the tile's rows from `left` to the end of the last product are past the context: zeros
-                    // (lane 0's wait, and the barrier above, order the copies before these writes)
+                const int b = at & 1;
+                // the group's positions of the tile within the context, in products
+                const int left = min(kHalfKv, ctx - (st0 + j) * kKv - w * kHalfKv);
+                const int steps = left > 0 ? (left + kStepKeys - 1) / kStepKeys : 0;
+                ok = lane || (wait_one(&ctl->v_full[st], phase, ctl, a.status) &&
+                              wait_one(&ctl->p_full[w][b], (at >> 1) & 1, ctl, a.status));
+                if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0))) break;
+                if (left > 0 && left % kStepKeys) {
+                    // rows from `left` to the end of the last product are past the context: zeros (lane 0's
+                    // wait, and the shuffle, order the copies before these writes)
                     for (int x = lane; x < (kStepKeys * steps - left) * G::kHalves * 8; x += 32) {
-                        const int r = left + x / (G::kHalves * 8), c = x % (G::kHalves * 8);
+                        const int r = w * kHalfKv + left + x / (G::kHalves * 8), c = x % (G::kHalves * 8);
                         *reinterpret_cast<uint4*>(sm + G::kV0 + st * G::kTileBytes + (c >> 3) * G::kHalfBytes + r * 128 +
                                                   (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
@@ -536,22 +519,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     fence_after();
-                    const uint32_t t_p = tmem + w * 128, t_o = tmem + kTmemO + w * 128, v_lo = v_lo0 + st * (G::kTileBytes >> 4);
-                    // weights of product kk (x: their second set): see the softmax
-                    auto at_p = [&](int kk, int x) {
-                        return t_p + (F8 ? 8 * kk + 32 * x : kHalf ? 8 * kk : 32 * (kk >> 1) + 8 * (kk & 1) + 16 * x);
+                    const uint32_t t_p = tmem + b * 128 + w * kHalfKv, v_lo = v_lo0 + st * (G::kTileBytes >> 4);
+                    // weights of product kk: 8 columns each, a second set of them behind the first
+                    auto products = [&](bool all) {
+#pragma unroll
+                        for (int x = 0; x < kSets; ++x)
+#pragma unroll
+                            for (int kk = 0; kk < kSteps; ++kk) {
+                                if (!(all || kk < steps)) continue;
+                                const uint32_t t = t_p + 8 * (x * kSteps + kk), v = v_lo + kk * ((kStepKeys * 128) >> 4);
+                                if (kk == 0 && x == 0)
+                                    mma_ts<F8>(t_o, t, v, id, j > 0 ? 1u : 0u);
+                                else
+                                    mma_ts_add<F8>(t_o, t, v, id);
+                            }
                     };
-                    auto at_v = [&](int kk) { return v_lo + kk * ((kStepKeys * 128) >> 4); };
-                    mma_ts<F8>(t_o, at_p(0, 0), at_v(0), id, j > 1 ? 1u : 0u);
-#pragma unroll
-                    for (int kk = 1; kk < kKv / kStepKeys; ++kk)
-                        if (kk < steps) mma_ts_add<F8>(t_o, at_p(kk, 0), at_v(kk), id);
-                    if (F8 || !kHalf) {
-#pragma unroll
-                        for (int kk = 0; kk < kKv / kStepKeys; ++kk)
-                            if (kk < steps) mma_ts_add<F8>(t_o, at_p(kk, 1), at_v(kk), id);
-                    }
-                    commit(&ctl->p_done[w]);
+                    if (steps == kSteps)
+                        products(true);
+                    else
+                        products(false);
+                    commit(&ctl->p_done[b]);
                     commit(&ctl->v_empty[st]);
                     if (j == len - 1) commit(&ctl->o_done);
                 }
@@ -564,25 +551,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && at > 0)
             pa::mbar_wait_bounded(&ctl->v_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
     } else if (warp < kSoftmaxWarps) {
-        // ------------------------------------------------------------ softmax: group w takes tiles j = w, w + 2, ...
+        // ------------------------------------------------------------ softmax of group w's half of every tile
         const int w = warp >> 2, quarter = warp & 3;
         const int r = kHalf ? quarter * 16 + (lane & 15) : quarter * 32 + lane;   // row of the unit
-        const int half = kHalf ? lane >> 4 : 0;                  // 64-row units: which 64 of a tile's columns
-        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t t_s = t_lane + w * 128, t_o = t_lane + kTmemO + w * 128;
+        const int half = kHalf ? lane >> 4 : 0;                  // 64-row units: which 32 of the group's columns
+        constexpr int kCols = kHalf ? 32 : 64;                   // columns per thread
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16), t_o = t_lane + kTmemO + w * 128;
         const float* factors = reinterpret_cast<const float*>(stats + 128);   // F8: [unit parity][row]
         constexpr float kSlack = F8 ? 0.5f : kRaise;             // F8: weights of at most 2^8.5 in E4M3's 448
         constexpr float kHeadroom = F8 ? 2.f : 0.f;              // F8: a raise leaves room for the next ones (a raise
                                                                  // at every growth cost 560 cycles in half the tiles)
         constexpr float kUp = F8 ? 8.f : 0.f;                    // log2 of the weights' common factor
-        int tiles = 0;                                           // this group's tiles so far
+        constexpr uint32_t kLanes16 = 16u << 16;
+        int at = 0;                                              // tiles so far
         bool ok = true;
         for (int nth = 0; ok; ++nth) {
             const int slot = nth % kUnits;
             if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
             const Unit* u = &ctl->units[slot];
             if (!u->valid) break;                                // (the rest of it is not set then)
-            const int len = u->len, t_first = u->st0 * kKv, first = u->first;
+            const int len = u->len, first = u->first;
+            const int start = u->st0 * kKv + w * kHalfKv + 32 * half;   // the thread's first position in the unit
             const int i = (u->row0 + r) >> a.log2_group;
             const bool real = i < u->n, tree = u->words != nullptr;
             // what the row sees of the new tokens: a word (tree), or positions below `lim`
@@ -607,60 +596,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_for(&ctl->q_full, nth & 1, ctl, a.status)) break;   // the rows' factors come with q
                 c = factors[(nth & 1) * 64 + r];
             }
-            for (int j = w; j < len; j += 2, ++tiles) {
-                if (!(ok = wait_for(&ctl->s_full[w], tiles & 1, ctl, a.status))) break;
+            for (int j = 0; j < len; ++j, ++at) {
+                const int b = at & 1;
+                if (!(ok = wait_for(&ctl->s_full[b], (at >> 1) & 1, ctl, a.status))) break;
                 fence_after();
-                const int t0 = t_first + j * kKv;
-                const bool tail = t0 + kKv > first;              // some row may not see some position
-                auto mask = [&](int start, float* s) {
-                    if (tail) {
-                        const uint32_t v = seen(start);
-                        if (__any_sync(0xffffffffu, v != ~0u)) {
+                const uint32_t t_s = t_lane + b * 128 + w * kHalfKv;
+                float s[kCols];
+                if constexpr (kHalf) {
+                    ld32_split32(t_s, s);
+                    if constexpr (F8) {                          // and the scores of q's second term, in the row's second lane
+                        float s2[32];
+                        ld32_split32(t_s + kLanes16, s2);
+                        wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = (v & (1u << k)) ? s[k] : -INFINITY;
-                        }
+                        for (int k = 0; k < 32; k += 2)
+                            split(add2(pair(s[k], s[k + 1]), pair(s2[k], s2[k + 1])), s[k], s[k + 1]);
                     }
-                };
-                auto top32 = [&](const float* s) {
+                } else {
+                    ld32(t_s, s);
+                    ld32(t_s + 32, s + 32);
+                }
+                wait_ld();
+                const int t0 = start + j * kKv;
+                if (t0 + kCols > first) {                        // some row may not see some position
+#pragma unroll
+                    for (int x = 0; x < kCols; x += 32) {
+                        const uint32_t v = seen(t0 + x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[x + k] = (v & (1u << k)) ? s[x + k] : -INFINITY;
+                    }
+                }
+                float top;
+                {
                     float p[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) p[k] = fmaxf(fmaxf(s[k], s[k + 8]), fmaxf(s[k + 16], s[k + 24]));
-                    return fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-                };
-                float s64[kHalf ? 64 : 1];                       // 64-row units: the thread's columns
-                float top;
-                if constexpr (kHalf) {
-                    ld32_split64(t_s, s64);
-                    ld32_split64(t_s + 32, s64 + 32);
-                    wait_ld();
-                    mask(t0 + 64 * half, s64);
-                    mask(t0 + 64 * half + 32, s64 + 32);
-                    top = fmaxf(top32(s64), top32(s64 + 32));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                } else {
-                    top = -INFINITY;
-#pragma unroll 2
-                    for (int x = 0; x < kKv / 32; ++x) {
-                        float s[32];
-                        ld32(t_s + 32 * x, s);
-                        wait_ld();
-                        mask(t0 + 32 * x, s);
-                        top = fmaxf(top, top32(s));
+                    for (int k = 0; k < 8; ++k) {
+                        p[k] = fmaxf(fmaxf(s[k], s[k + 8]), fmaxf(s[k + 16], s[k + 24]));
+                        if constexpr (!kHalf) p[k] = fmaxf(p[k], fmaxf(fmaxf(s[k + 32], s[k + 40]), fmaxf(s[k + 48], s[k + 56])));
                     }
+                    top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+                    if (kHalf) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 }
                 const bool raise = fmaf(top, c, -m) > kSlack;
                 const float m_new = raise ? fmaf(top, c, kHeadroom) : m;
-                if (j > w && __any_sync(0xffffffffu, raise)) {
-                    // this group's O holds its tiles before j: their products finished before these scores
+                if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                    // this group's O holds its halves of the tiles before, once their products are done
+                    if (!(ok = wait_for(&ctl->p_done[b ^ 1], ((at - 1) >> 1) & 1, ctl, a.status))) break;
+                    fence_after();
                     const float f = pa::exp2_approx(m - m_new);
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        float o[32];
-                        ld32(t_o + x, o);
+                    for (int x = 0; x < D; x += 16) {
+                        uint32_t o[16];
+                        ld16(t_o + x, o);
                         wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= f;
-                        st32(t_o + x, o);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        st16(t_o + x, o);
                     }
                     l *= f;
                 }
@@ -675,70 +666,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum[k & 1] = add2(sum[k & 1], p);
                     return p;
                 };
-                // the bf16 terms of two weights
-                auto terms = [&](uint64_t p, uint32_t& hi, uint32_t& lo) {
-                    float p0, p1, r0, r1;
-                    split(p, p0, p1);
-                    hi = pa::pack_bf16x2(p0, p1);
-                    split(sub2(p, pair(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u))), r0, r1);
-                    lo = pa::pack_bf16x2(r0, r1);
-                };
-                constexpr uint32_t kLanes16 = 16u << 16;
                 if constexpr (F8) {
                     // Weights as f16 (11 significant bits) and then as three E4M3 terms of 4 bits each, which
                     // hold them within 2^-10 (at most 2^-15 of the row's largest): the first two in a
                     // product's two lanes of a row, the third in a second product's, whose other lane is zero.
+                    uint32_t t[3][8];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint32_t t[3][8];
+                    for (int k = 0; k < 8; ++k) {
+                        t[0][k] = t[1][k] = t[2][k] = 0;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint32_t cell[3] = {0, 0, 0};
+                        for (int e = 0; e < 2; ++e) {
+                            float p0, p1;
+                            split(weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], e), p0, p1);
+                            uint32_t h = pa::pack_f16x2(p0, p1);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float p0, p1;
-                                split(weights(s64[32 * y + 4 * k + 2 * e], s64[32 * y + 4 * k + 2 * e + 1], e), p0, p1);
-                                uint32_t h = pa::pack_f16x2(p0, p1);
-#pragma unroll
-                                for (int x = 0; x < 3; ++x) {
-                                    const uint32_t code = f16x2_to_e4m3x2(h);
-                                    cell[x] |= code << (16 * e);
-                                    if (x < 2) h = sub_f16x2(h, e4m3x2_to_f16x2(code));
-                                }
+                            for (int x = 0; x < 3; ++x) {
+                                // the top 4 bits (a NaN keeps being one), then the rest
+                                const uint32_t top4 = x < 2 ? h & 0xff80ff80u : h;
+                                t[x][k] |= f16x2_to_e4m3x2(top4) << (16 * e);
+                                if (x < 2) h = sub_f16x2(h, top4);
                             }
-#pragma unroll
-                            for (int x = 0; x < 3; ++x) t[x][k] = cell[x];
                         }
-                        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                        st8_split16(t_s + 8 * y, t[0]);
-                        st8_split16(t_s + kLanes16 + 8 * y, t[1]);
-                        st8_split16(t_s + 32 + 8 * y, t[2]);
-                        st8_split16(t_s + kLanes16 + 32 + 8 * y, zero);
                     }
-                } else if constexpr (kHalf) {
-                    // hi terms in a row's first lane, lo terms in its second: columns 0-63
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            terms(weights(s64[32 * y + 2 * k], s64[32 * y + 2 * k + 1], k), hi[k], lo[k]);
-                        st16_split32(t_s + 16 * y, hi);
-                        st16_split32(t_s + kLanes16 + 16 * y, lo);
-                    }
+                    const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    st8_split8(t_s, t[0]);
+                    st8_split8(t_s + kLanes16, t[1]);
+                    st8_split8(t_s + 16, t[2]);
+                    st8_split8(t_s + kLanes16 + 16, zero);
                 } else {
-                    // over each 32 columns of scores: the hi terms of their weights in 16, the lo terms in 16
-#pragma unroll 2
-                    for (int x = 0; x < kKv / 32; ++x) {
-                        float s[32];
-                        ld32(t_s + 32 * x, s);
-                        wait_ld();
-                        mask(t0 + 32 * x, s);
+                    // hi terms in the group's first 32 columns; lo terms in a row's second lane (64-row
+                    // units) or in the other 32 columns
+#pragma unroll
+                    for (int x = 0; x < kCols; x += 32) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) terms(weights(s[2 * k], s[2 * k + 1], k), hi[k], lo[k]);
-                        st16(t_s + 32 * x, hi);
-                        st16(t_s + 32 * x + 16, lo);
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t p = weights(s[x + 2 * k], s[x + 2 * k + 1], k);
+                            float p0, p1, r0, r1;
+                            split(p, p0, p1);
+                            hi[k] = pa::pack_bf16x2(p0, p1);
+                            split(sub2(p, pair(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xffff0000u))), r0, r1);
+                            lo[k] = pa::pack_bf16x2(r0, r1);
+                        }
+                        if constexpr (kHalf) {
+                            st16_split16(t_s, hi);
+                            st16_split16(t_s + kLanes16, lo);
+                        } else {
+                            st16(t_s + x / 2, hi);
+                            st16(t_s + 32 + x / 2, lo);
+                        }
                     }
                 }
                 float a0, a1, b0, b1;
@@ -747,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += (a0 + a1) + (b0 + b1);
                 wait_st();
                 fence_before();
-                pa::mbar_arrive(&ctl->p_full[w]);
+                pa::mbar_arrive(&ctl->p_full[w][b]);
             }
             if (!ok) break;
             if (nth >= 1 && !wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status)) break;
@@ -812,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* dst = smem + line * 128 + (((4 * part + x) ^ (line & 7)) << 4);
                     *reinterpret_cast<uint4*>(dst) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
-                    *reinterpret_cast<uint4*>(dst + G::kHalfBytes) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+                    *reinterpret_cast<uint4*>(dst + 16 * 128) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             };
@@ -832,7 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!u->valid) break;
             const int st0 = u->st0;
             const int row = u->row0 + r, i = row >> a.log2_group;
-            const bool real = i < u->n, whole = u->len == u->steps, odd = u->len > 1;   // one tile: O1 was not written
+            const bool real = i < u->n, whole = u->len == u->steps;
+            const bool both = u->len > 1 || u->ctx - st0 * kKv > kHalfKv;   // group 1 had positions: O1 was written
             const size_t out_row = ((size_t)(u->q0 + i) * a.n_q_heads + (u->kvh << a.log2_group) + (row & (group - 1))) * D;
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
@@ -868,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa::mbar_arrive(&ctl->o_free);
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = fe * v[k] + (odd ? fo * v1[k] : 0.f);
+                for (int k = 0; k < 32; ++k) v[k] = fe * v[k] + (both ? fo * v1[k] : 0.f);
                 float f[kHalf ? 16 : 32];                         // of a row's two lanes, each writes half
                 if constexpr (kHalf) {
 #pragma unroll
