@@ -64,8 +64,9 @@ struct Wide {
     static constexpr int kHalfBytes = 128 * 128;                 // 128 rows of 128 bytes, 128-byte swizzle
     static constexpr int kTileBytes = kHalves * kHalfBytes;      // K or V of a tile
     static constexpr int kQBytes = kTileBytes;                   // F8: a row's two terms in its two lanes
+    static constexpr int kQBuffers = F8 ? 2 : 1;
     static constexpr int kStages = F8 || D == 64 ? 6 : 3;
-    static constexpr int kK0 = kQBytes;
+    static constexpr int kK0 = kQBuffers * kQBytes;
     static constexpr int kV0 = kK0 + kStages * kTileBytes;
     static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][row] maximum and sum; F8: then row factors
     static constexpr int kCtl = kStats + 2 * 128 * 8;
@@ -76,7 +77,7 @@ struct Wide {
 constexpr int kMaxStages = 6;
 
 struct Ctl {
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];        // per buffer of q
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t s_full[2];                    // per buffer: a tile's scores are in tensor memory
     uint64_t p_full[2][2];                 // per group and buffer: its weights are (and its O is rescaled)
@@ -304,8 +305,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int B = 1 << a.log2_block, group = 1 << a.log2_group;
 
     if (threadIdx.x == 0) {
-        pa::mbar_init(&ctl->q_full, F8 ? 128 : 1);
-        pa::mbar_init(&ctl->q_empty, 1);
         for (int i = 0; i < kStages; ++i) {
             pa::mbar_init(&ctl->k_full[i], 1);
             pa::mbar_init(&ctl->k_empty[i], 1);
@@ -313,6 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             pa::mbar_init(&ctl->v_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
+            pa::mbar_init(&ctl->q_full[i], F8 ? 128 : 1);
+            pa::mbar_init(&ctl->q_empty[i], 1);
             pa::mbar_init(&ctl->s_full[i], 1);
             pa::mbar_init(&ctl->p_full[0][i], 128);
             pa::mbar_init(&ctl->p_full[1][i], 128);
@@ -376,15 +377,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
                 if (!u->valid) break;
                 if constexpr (!F8) {
-                    if (nth >= 1 && !(ok = wait_for(&ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
+                    if (nth >= 1 && !(ok = wait_for(ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
                     if (lane == 0) {
                         // 16 rows a box: 16 / group tokens of the group's heads
-                        pa::mbar_arrive_expect_tx(&ctl->q_full, kRows * 128 * G::kHalves);
+                        pa::mbar_arrive_expect_tx(ctl->q_full, kRows * 128 * G::kHalves);
                         for (int r = 0; r < kRows; r += 16) {
 #pragma unroll
                             for (int h = 0; h < G::kHalves; ++h)
                                 tma_q(s0 + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
-                                      u->kvh << a.log2_group, u->q0 + ((u->row0 + r) >> a.log2_group), &ctl->q_full);
+                                      u->kvh << a.log2_group, u->q0 + ((u->row0 + r) >> a.log2_group), ctl->q_full);
                         }
                     }
                 }
@@ -434,14 +435,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the copies this warp started land before the block exits
         if (lane == 0) {
-            if (!F8 && !is_k && nth > 0) pa::mbar_wait_bounded(&ctl->q_full, (nth - 1) & 1, kMaxProbes);
+            if (!F8 && !is_k && nth > 0) pa::mbar_wait_bounded(ctl->q_full, (nth - 1) & 1, kMaxProbes);
             for (int i = 0; i < kStages && i < done; ++i)
                 pa::mbar_wait_bounded(&full[(done - 1 - i) % kStages], ((done - 1 - i) / kStages) & 1, kMaxProbes);
         }
     } else if (warp == kScoreWarp) {
         // ------------------------------------------------------------ score products, by one thread
         constexpr uint32_t id = idesc(F8, 128, kKv, 0);
-        const uint32_t q_lo = desc_lo(s0, 16), k_lo0 = desc_lo(s0 + G::kK0, 16);
+        const uint32_t k_lo0 = desc_lo(s0 + G::kK0, 16);
         if (lane == 0) {
             int at = 0, st = 0, phase = 0;                       // tiles so far; K's stage and phase
             bool ok = true;
@@ -451,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int valid = ctl->units[slot].valid, len = ctl->units[slot].len;
                 pa::mbar_arrive(&ctl->unit_empty[slot]);
                 if (!valid) break;
-                if (!wait_one(&ctl->q_full, nth & 1, ctl, a.status)) break;
+                const int qb = nth % G::kQBuffers;
+                if (!wait_one(&ctl->q_full[qb], (nth / G::kQBuffers) & 1, ctl, a.status)) break;
+                const uint32_t q_lo = desc_lo(s0 + qb * G::kQBytes, 16);
                 for (int j = 0; j < len; ++j, ++at) {
                     const int b = at & 1;
                     // the scores go over weights of two tiles ago: their value products have to be done
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     commit(&ctl->s_full[b]);
                     commit(&ctl->k_empty[st]);
-                    if (j == len - 1) commit(&ctl->q_empty);
+                    if (j == len - 1) commit(&ctl->q_empty[qb]);
                     if (++st == kStages) {
                         st = 0;
                         phase ^= 1;
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16), t_o = t_lane + kTmemO + w * 128;
         const float* factors = reinterpret_cast<const float*>(stats + 128);   // F8: [unit parity][row]
         constexpr float kSlack = F8 ? 0.5f : kRaise;             // F8: weights of at most 2^8.5 in E4M3's 448
-        constexpr float kHeadroom = F8 ? 2.f : 0.f;              // F8: a raise leaves room for the next ones (a raise
+        constexpr float kHeadroom = F8 ? 3.f : 0.f;              // F8: a raise leaves room for the next ones (a raise
                                                                  // at every growth cost 560 cycles in half the tiles)
         constexpr float kUp = F8 ? 8.f : 0.f;                    // log2 of the weights' common factor
         constexpr uint32_t kLanes16 = 16u << 16;
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             float m = kNone, l = 0.f, c = a.scale_log2;
             if constexpr (F8) {
-                if (!wait_for(&ctl->q_full, nth & 1, ctl, a.status)) break;   // the rows' factors come with q
+                if (!wait_for(&ctl->q_full[nth & 1], (nth >> 1) & 1, ctl, a.status)) break;   // the rows' factors come with q
                 c = factors[(nth & 1) * 64 + r];
             }
             for (int j = 0; j < len; ++j, ++at) {
@@ -797,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (F8) {
             if (wait_for(&ctl->unit_full[0], 0, ctl, a.status) && ctl->units[0].valid) {
                 make_q(&ctl->units[0], 0)(sm, factors);
-                pa::mbar_arrive(&ctl->q_full);
+                pa::mbar_arrive(&ctl->q_full[0]);
             }
         }
         const uint32_t t_o = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemO;
@@ -814,14 +817,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
             if constexpr (F8) {
-                // the next unit's q, once this one's last scores are done
+                // the next unit's q, ahead of this unit's end (the buffer's last unit was the one before)
                 const int ahead = (nth + 1) % kUnits;
                 if (!wait_for(&ctl->unit_full[ahead], ((nth + 1) / kUnits) & 1, ctl, a.status)) break;
                 if (ctl->units[ahead].valid) {
                     auto store = make_q(&ctl->units[ahead], (nth + 1) & 1);
-                    if (!wait_for(&ctl->q_empty, nth & 1, ctl, a.status)) break;
-                    store(sm, factors);
-                    pa::mbar_arrive(&ctl->q_full);
+                    const int qb = (nth + 1) & 1;
+                    if (nth >= 1 && !wait_for(&ctl->q_empty[qb], ((nth - 1) >> 1) & 1, ctl, a.status)) break;
+                    store(sm + qb * G::kQBytes, factors);
+                    pa::mbar_arrive(&ctl->q_full[qb]);
                 }
             }
             if (!wait_for(&ctl->stats_full, nth & 1, ctl, a.status)) break;

@@ -13,7 +13,12 @@
 // 32-bit.  The pass is bound by memory: each input is read once and each
 // output written once.  A thread holds 16 elements of a head (two 16-byte
 // chunks, chosen so that both halves of every pair are its own), so a head
-// of 128 is 8 threads and the norm's sum is three shuffles.
+// of 128 is 8 threads and the norm's sum is three shuffles.  A warp takes a
+// token (a part of its heads when tokens are few), so that the angles and
+// the gains are loaded once for all its heads, and has several heads in
+// flight; arithmetic is in packed pairs.  (A thread per head and chunk,
+// loading angles and gains for each, was bound by its instructions: 204 us on
+// 32,048 tokens of 32 + 2 x 8 heads against 116 us for their bytes.)
 
 #include "pa_common.cuh"
 
@@ -40,138 +45,265 @@ struct RopeArgs {
     int max_positions, rot_dim, num_tokens, n_q_heads, n_kv_heads, block_size;
 };
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+// Two fp32 values in a register pair, for packed arithmetic.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t r) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+    return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
-__device__ __forceinline__ void unpack8(uint4 x, float* f) {
+// A thread's 16 elements of a head as 8 pairs: f[i] (i < 4) from the first
+// chunk, f[i + 4] from the second.
+struct Part {
+    uint64_t f[8];
+};
+
+__device__ __forceinline__ void unpack8(uint4 x, uint64_t* f) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const uint64_t* f) {
+    uint32_t w[4];
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 p = pa::bf16x2_to_float2(w[i]);
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
+        const float2 v = unpair(f[i]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
-}
-
-__device__ __forceinline__ uint2 codes8(const float* f, float scale) {
+__device__ __forceinline__ uint2 codes8(const uint64_t* f, float scale) {
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = pa::e4m3x2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale));
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = unpair(f[i]);
+        c[i] = pa::e4m3x2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale));
+    }
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-__device__ __forceinline__ void load8(const float* p, float* f) {
+__device__ __forceinline__ void load8(const float* p, uint64_t* f) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    f[0] = pair(a.x, a.y);
+    f[1] = pair(a.z, a.w);
+    f[2] = pair(b.x, b.y);
+    f[3] = pair(b.z, b.w);
 }
 
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kFlight = 4;                 // heads per thread group in flight
+
+// grid: warps over (token, segment); a segment is `per` turns of the token's
+// turns, first q's, then k's, then v's; a turn is 32 / (D / 16) heads.
 template <int D, bool F8, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_cache_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_cache_kernel(const RopeArgs a, int segments, int per) {
     constexpr int kLanes = D / 16;                     // threads per head
+    constexpr int kHeads = 32 / kLanes;                // heads per turn
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int heads = a.n_q_heads + 2 * a.n_kv_heads;
-    const uint32_t at = blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
-    const int l = threadIdx.x % kLanes;
-    const int t = at / heads;
-    if (t >= a.num_tokens) return;                     // whole heads: a head's threads leave together
-    const int row = at - t * heads;
-    const unsigned mask = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
-    const int pos = a.positions[t];
-    if (pos < 0) return;                               // padding: nothing of the token is touched
-    if (pos >= a.max_positions) {
-        if (l == 0 && row == 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
-        return;
-    }
-    const bool is_q = row < a.n_q_heads, is_v = row >= a.n_q_heads + a.n_kv_heads;
-    const int h = is_q ? row : row - a.n_q_heads - (is_v ? a.n_kv_heads : 0);
-    long long slot = 0;
-    if (!is_q) {
-        slot = a.slots[t];
-        if (slot < 0) return;                          // a key and value that stay out of the cache
-        if (slot >= a.num_slots) {
-            if (l == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
-            return;
-        }
-    }
-    // this thread's two chunks of 8: pairs (i, i + rot_dim / 2) take one from
+    const uint32_t at = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    const uint32_t t = at / segments;
+    if (t >= (uint32_t)a.num_tokens) return;
+    const int lane = threadIdx.x & 31, l = lane % kLanes, g = lane / kLanes;
+    const int q_turns = (a.n_q_heads + kHeads - 1) / kHeads, kv_turns = (a.n_kv_heads + kHeads - 1) / kHeads;
+    const int i0 = (at - t * segments) * per, i1 = i0 + per;
+    // this thread's two chunks of 8: pairs (c, c + rot_dim / 2) take one from
     // each half of the rotated part, all else two neighbours
     const int turn_lanes = a.rot_dim >> 4;
     const bool turns = l < turn_lanes;
     const int c0 = !kInterleaved && turns ? l : 2 * l;
     const int c1 = !kInterleaved && turns ? l + turn_lanes : 2 * l + 1;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + h * D);
-    const uint4 x0 = src[c0], x1 = src[c1];
-    float f[16];
-    unpack8(x0, f);
-    unpack8(x1, f + 8);
-    if (!is_v) {
-        const float* gain = is_q ? a.q_weight : a.k_weight;
-        if (gain) {
-            float s = 0.f;
+
+    const int pos = a.positions[t];
+    const long long slot = a.slots[t];
+    struct Raw {
+        uint4 x0[kFlight], x1[kFlight];
+    };
+    // heads first + u * kHeads + g (u < kFlight, in turns below `end`) of a tensor's row
+    auto load = [&](const __nv_bfloat16* rows, int turn, int end, int heads, Raw& r) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s += f[i] * f[i];
+        for (int u = 0; u < kFlight; ++u) {
+            const int h = (turn + u) * kHeads + g;
+            if (turn + u < end && h < heads) {
+                const uint4* src = reinterpret_cast<const uint4*>(rows + h * D);
+                r.x0[u] = src[c0];
+                r.x1[u] = src[c1];
+            }
+        }
+    };
+    const __nv_bfloat16* q = a.q + (long long)t * a.q_stride;
+    const __nv_bfloat16* k = a.k + (long long)t * a.k_stride;
+    const __nv_bfloat16* v = a.v + (long long)t * a.v_stride;
+    // the first heads' loads do not wait for the position
+    Raw raw;
+    const int q_end = min(i1, q_turns);
+    if (i0 < q_end) load(q, i0, q_end, a.n_q_heads, raw);
+    if (pos < 0) return;                               // padding: nothing of the token is touched
+    if (pos >= a.max_positions) {
+        if (lane == 0 && i0 == 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
+        return;
+    }
+    uint64_t cs[4], sn[4];                             // cosines and sines of this thread's 8 pairs
+    const bool rotates = turns && i0 < q_turns + kv_turns;
+    if (rotates) {
+        const float* p = a.cos_sin + (size_t)pos * a.rot_dim + 8 * l;
+        load8(p, cs);
+        load8(p + (a.rot_dim >> 1), sn);
+    }
+    uint64_t gain[8];
+    const bool norm = a.q_weight != nullptr;
+    auto load_gain = [&](const float* w) {
+        if (norm) {
+            load8(w + 8 * c0, gain);
+            load8(w + 8 * c1, gain + 4);
+        }
+    };
+    auto work = [&](uint4 x0, uint4 x1) {              // whole warp
+        Part p;
+        unpack8(x0, p.f);
+        unpack8(x1, p.f + 4);
+        if (norm) {
+            uint64_t sum = mul2(p.f[0], p.f[0]);
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+            for (int i = 1; i < 8; ++i) sum = fma2(p.f[i], p.f[i], sum);
+            const float2 two = unpair(sum);
+            float s = two.x + two.y;
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             const float inv = rsqrtf(s * (1.f / D) + a.eps);
-            float g[16];
-            load8(gain + 8 * c0, g);
-            load8(gain + 8 * c1, g + 8);
+            const uint64_t ii = pair(inv, inv);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = f[i] * inv * g[i];
+            for (int i = 0; i < 8; ++i) p.f[i] = mul2(mul2(p.f[i], ii), gain[i]);
         }
         if (turns) {
-            const float* cs = a.cos_sin + (size_t)pos * a.rot_dim + 8 * l;
-            float c[8], s[8];
-            load8(cs, c);
-            load8(cs + (a.rot_dim >> 1), s);
+            if constexpr (kInterleaved) {
+                // pair c is (f[c].x, f[c].y)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float& x = f[kInterleaved ? 2 * i : i];
-                float& y = f[kInterleaved ? 2 * i + 1 : i + 8];
-                const float xr = x * c[i] - y * s[i];
-                y = y * c[i] + x * s[i];
-                x = xr;
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = unpair(p.f[i]), cc = unpair(cs[i >> 1]), ss = unpair(sn[i >> 1]);
+                    const float c = i & 1 ? cc.y : cc.x, s = i & 1 ? ss.y : ss.x;
+                    p.f[i] = fma2(pair(f.y, f.x), pair(-s, s), mul2(p.f[i], pair(c, c)));
+                }
+            } else {
+                // pairs are (f[i], f[i + 4]), two at a time
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t x = p.f[i], y = p.f[i + 4];
+                    const float2 s = unpair(sn[i]);
+                    p.f[i] = fma2(y, pair(-s.x, -s.y), mul2(x, cs[i]));
+                    p.f[i + 4] = fma2(x, sn[i], mul2(y, cs[i]));
+                }
+            }
+        }
+        return p;
+    };
+    // ---- queries ----
+    load_gain(a.q_weight);
+    for (int turn = i0; turn < q_end; turn += kFlight) {
+        Raw now = raw;
+        if (turn + kFlight < q_end) load(q, turn + kFlight, q_end, a.n_q_heads, raw);
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            if (turn + u >= q_end) break;
+            const int h = (turn + u) * kHeads + g;
+            const Part p = work(now.x0[u], now.x1[u]);
+            if (h < a.n_q_heads) {
+                uint4* dst = a.q_out + ((size_t)t * a.n_q_heads + h) * (D / 8);
+                dst[c0] = pack8(p.f);
+                dst[c1] = pack8(p.f + 4);
             }
         }
     }
-    if (is_q) {
-        uint4* dst = a.q_out + ((size_t)t * a.n_q_heads + h) * (D / 8);
-        dst[c0] = pack8(f);
-        dst[c1] = pack8(f + 8);
+    if (i1 <= q_turns || slot < 0) return;             // no keys here, or they stay out of the cache
+    if (slot >= a.num_slots) {
+        if (lane == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
         return;
     }
     const long long blk = slot / a.block_size;
     const int off = (int)(slot - blk * a.block_size);
-    const size_t elem = (((size_t)blk * a.n_kv_heads + h) * a.block_size + off) * D;
-    uint8_t* cache = is_v ? a.v_cache : a.k_cache;
-    if constexpr (F8) {
-        const float scale = is_v ? a.v_scale : a.k_scale;
-        uint2* dst = reinterpret_cast<uint2*>(cache + elem);
-        dst[c0] = codes8(f, scale);
-        dst[c1] = codes8(f + 8, scale);
-    } else {
-        uint4* dst = reinterpret_cast<uint4*>(cache + 2 * elem);
-        dst[c0] = is_v ? x0 : pack8(f);
-        dst[c1] = is_v ? x1 : pack8(f + 8);
+    const size_t row0 = ((size_t)blk * a.n_kv_heads * a.block_size + off) * D, head = (size_t)a.block_size * D;
+    auto put = [&](uint8_t* cache, int h, const Part& p, float scale) {
+        const size_t elem = row0 + h * head;
+        if constexpr (F8) {
+            uint2* dst = reinterpret_cast<uint2*>(cache + elem);
+            dst[c0] = codes8(p.f, scale);
+            dst[c1] = codes8(p.f + 4, scale);
+        } else {
+            uint4* dst = reinterpret_cast<uint4*>(cache + 2 * elem);
+            dst[c0] = pack8(p.f);
+            dst[c1] = pack8(p.f + 4);
+        }
+    };
+    // ---- keys, then values ----
+    const int k0 = max(0, i0 - q_turns), k_end = min(i1 - q_turns, kv_turns);
+    const int v0 = max(0, i0 - q_turns - kv_turns), v_end = min(i1 - q_turns - kv_turns, kv_turns);
+    Raw vraw;
+    if (k0 < k_end) {
+        load(k, k0, k_end, a.n_kv_heads, raw);
+        load_gain(a.k_weight);
+    }
+    if (v0 < v_end) load(v, v0, v_end, a.n_kv_heads, vraw);
+    for (int turn = k0; turn < k_end; turn += kFlight) {
+        if (turn > k0) load(k, turn, k_end, a.n_kv_heads, raw);
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            if (turn + u >= k_end) break;
+            const int h = (turn + u) * kHeads + g;
+            const Part p = work(raw.x0[u], raw.x1[u]);
+            if (h < a.n_kv_heads) put(a.k_cache, h, p, a.k_scale);
+        }
+    }
+    for (int turn = v0; turn < v_end; turn += kFlight) {
+        if (turn > v0) load(v, turn, v_end, a.n_kv_heads, vraw);
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int h = (turn + u) * kHeads + g;
+            if (turn + u >= v_end || h >= a.n_kv_heads) break;
+            if constexpr (F8) {
+                Part p;
+                unpack8(vraw.x0[u], p.f);
+                unpack8(vraw.x1[u], p.f + 4);
+                put(a.v_cache, h, p, a.v_scale);
+            } else {
+                uint4* dst = reinterpret_cast<uint4*>(a.v_cache + 2 * (row0 + h * head));
+                dst[c0] = vraw.x0[u];
+                dst[c1] = vraw.x1[u];
+            }
+        }
     }
 }
 
 template <int D, bool F8>
 cudaError_t launch_rope(const RopeArgs& a, int interleaved, cudaStream_t st) {
-    const long long rows = (long long)a.num_tokens * (a.n_q_heads + 2 * a.n_kv_heads);
-    const int per = kRopeThreads / (D / 16);
+    // Few tokens: a token's turns over several warps, down to one turn each,
+    // until there are about 16 warps per SM; many: a warp per token.
+    const int heads = 32 / (D / 16);
+    const int turns = (a.n_q_heads + heads - 1) / heads + 2 * ((a.n_kv_heads + heads - 1) / heads);
+    const long long want = 152LL * 16 / a.num_tokens;
+    const int segments = (int)(want < 1 ? 1 : want > turns ? turns : want);
+    const int per = (turns + segments - 1) / segments, used = (turns + per - 1) / per;
+    const long long warps = (long long)a.num_tokens * used;
     return pa_host::launch_dependent(
         interleaved ? norm_rope_cache_kernel<D, F8, true> : norm_rope_cache_kernel<D, F8, false>,
-        dim3((unsigned)((rows + per - 1) / per)), dim3(kRopeThreads), 0, st, a);
+        dim3((unsigned)((warps + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeThreads), 0, st, a, used, per);
 }
 
 int norm_rope_cache(void* q_out, void* k_cache, void* v_cache, const void* q, const void* k, const void* v,
