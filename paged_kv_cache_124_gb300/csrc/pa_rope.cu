@@ -13,12 +13,12 @@
 // 32-bit.  The pass is bound by memory: each input is read once and each
 // output written once.  A thread holds 16 elements of a head (two 16-byte
 // chunks, chosen so that both halves of every pair are its own), so a head
-// of 128 is 8 threads and the norm's sum is three shuffles.  A warp takes a
-// token (a part of its heads when tokens are few), so that the angles and
-// the gains are loaded once for all its heads, and has several heads in
-// flight; arithmetic is in packed pairs.  (A thread per head and chunk,
-// loading angles and gains for each, was bound by its instructions: 204 us on
-// 32,048 tokens of 32 + 2 x 8 heads against 116 us for their bytes.)
+// of 128 is 8 threads and the norm's sum is three shuffles; arithmetic is in
+// packed pairs.  With many tokens the same threads take two heads of a token
+// at a time, one pair of heads after another, so that angles and gains are
+// loaded once for all of them: 32,048 tokens of 32 + 2 x 8 heads in 123 us,
+// 0.95 of the measured copy rate for their 790 MB.  With few, every head has
+// threads of its own: 4 tokens in 2.0 us, 250 of 256 (E4M3) in 3.6 us.
 
 #include "pa_common.cuh"
 
@@ -108,202 +108,282 @@ __device__ __forceinline__ void load8(const float* p, uint64_t* f) {
     f[3] = pair(b.z, b.w);
 }
 
-constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kFlight = 4;                 // heads per thread group in flight
+// Which of a head's 16-byte chunks thread l of it holds: pairs (c, c +
+// rot_dim / 2) take one from each half of the rotated part, all else two
+// neighbours.
+template <bool kInterleaved>
+struct Place {
+    bool turns;
+    int c0, c1;
+    __device__ __forceinline__ Place(int l, int rot_dim) {
+        turns = l < rot_dim >> 4;
+        c0 = !kInterleaved && turns ? l : 2 * l;
+        c1 = !kInterleaved && turns ? l + (rot_dim >> 4) : 2 * l + 1;
+    }
+};
 
-// grid: warps over (token, segment); a segment is `per` turns of the token's
-// turns, first q's, then k's, then v's; a turn is 32 / (D / 16) heads.
+// y = x * rsqrt(mean(x^2) + eps) * gain over a head's kLanes threads (mask).
+template <int kLanes>
+__device__ __forceinline__ void norm_part(Part& p, const uint64_t* gain, float eps, unsigned mask) {
+    uint64_t sum = mul2(p.f[0], p.f[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum = fma2(p.f[i], p.f[i], sum);
+    const float2 two = unpair(sum);
+    float s = two.x + two.y;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+    const float inv = rsqrtf(s * (1.f / (16 * kLanes)) + eps);
+    const uint64_t ii = pair(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p.f[i] = mul2(mul2(p.f[i], ii), gain[i]);
+}
+
+// (a, b) -> (a cos - b sin, b cos + a sin) for the thread's 8 pairs.
+template <bool kInterleaved>
+__device__ __forceinline__ void turn_part(Part& p, const uint64_t* cs, const uint64_t* sn) {
+    if constexpr (kInterleaved) {
+        // pair i is (f[i].x, f[i].y)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = unpair(p.f[i]), cc = unpair(cs[i >> 1]), ss = unpair(sn[i >> 1]);
+            const float c = i & 1 ? cc.y : cc.x, s = i & 1 ? ss.y : ss.x;
+            p.f[i] = fma2(pair(f.y, f.x), pair(-s, s), mul2(p.f[i], pair(c, c)));
+        }
+    } else {
+        // pairs are (f[i], f[i + 4]), two at a time
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t x = p.f[i], y = p.f[i + 4];
+            const float2 s = unpair(sn[i]);
+            p.f[i] = fma2(y, pair(-s.x, -s.y), mul2(x, cs[i]));
+            p.f[i + 4] = fma2(x, sn[i], mul2(y, cs[i]));
+        }
+    }
+}
+
+// A head's place in the caches.
+template <int D>
+__device__ __forceinline__ size_t cache_elem(const RopeArgs& a, long long slot, int h) {
+    const long long blk = slot / a.block_size;
+    return (((size_t)blk * a.n_kv_heads + h) * a.block_size + (size_t)(slot - blk * a.block_size)) * D;
+}
+
+template <bool F8>
+__device__ __forceinline__ void put_part(uint8_t* cache, size_t elem, const Part& p, float scale, int c0, int c1) {
+    if constexpr (F8) {
+        uint2* dst = reinterpret_cast<uint2*>(cache + elem);
+        dst[c0] = codes8(p.f, scale);
+        dst[c1] = codes8(p.f + 4, scale);
+    } else {
+        uint4* dst = reinterpret_cast<uint4*>(cache + 2 * elem);
+        dst[c0] = pack8(p.f);
+        dst[c1] = pack8(p.f + 4);
+    }
+}
+
+// Few heads in all: D / 16 threads per head and nothing shared, so that all
+// loads are in flight from the start.
 template <int D, bool F8, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_cache_kernel(const RopeArgs a, int segments, int per) {
-    constexpr int kLanes = D / 16;                     // threads per head
-    constexpr int kHeads = 32 / kLanes;                // heads per turn
+__global__ void __launch_bounds__(kRopeThreads, 4) heads_kernel(const RopeArgs a) {
+    constexpr int kLanes = D / 16;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t at = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-    const uint32_t t = at / segments;
-    if (t >= (uint32_t)a.num_tokens) return;
-    const int lane = threadIdx.x & 31, l = lane % kLanes, g = lane / kLanes;
-    const int q_turns = (a.n_q_heads + kHeads - 1) / kHeads, kv_turns = (a.n_kv_heads + kHeads - 1) / kHeads;
-    const int i0 = (at - t * segments) * per, i1 = i0 + per;
-    // this thread's two chunks of 8: pairs (c, c + rot_dim / 2) take one from
-    // each half of the rotated part, all else two neighbours
-    const int turn_lanes = a.rot_dim >> 4;
-    const bool turns = l < turn_lanes;
-    const int c0 = !kInterleaved && turns ? l : 2 * l;
-    const int c1 = !kInterleaved && turns ? l + turn_lanes : 2 * l + 1;
+    const uint32_t heads = a.n_q_heads + 2 * a.n_kv_heads;
+    const uint32_t at = blockIdx.x * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
+    const uint32_t t = at / heads;
+    if (t >= (uint32_t)a.num_tokens) return;           // whole heads: a head's threads leave together
+    const int row = at - t * heads, l = threadIdx.x % kLanes;
+    const unsigned mask = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
+    const bool is_q = row < a.n_q_heads, is_v = row >= a.n_q_heads + a.n_kv_heads;
+    const int h = is_q ? row : row - a.n_q_heads - (is_v ? a.n_kv_heads : 0);
+    const Place<kInterleaved> w(l, a.rot_dim);
+    const uint4* src = reinterpret_cast<const uint4*>(
+        (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + h * D);
+    const int pos = a.positions[t];
+    const long long slot = is_q ? 0 : a.slots[t];
+    const uint4 x0 = src[w.c0], x1 = src[w.c1];
+    const float* gains = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+    uint64_t gain[8];
+    if (gains) {
+        load8(gains + 8 * w.c0, gain);
+        load8(gains + 8 * w.c1, gain + 4);
+    }
+    if (pos < 0) return;                               // padding: nothing of the token is touched
+    if (pos >= a.max_positions) {
+        if (l == 0 && row == 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
+        return;
+    }
+    if (slot < 0) return;                              // a key and value that stay out of the cache
+    if (slot >= a.num_slots) {
+        if (l == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
+        return;
+    }
+    Part p;
+    unpack8(x0, p.f);
+    unpack8(x1, p.f + 4);
+    if (!is_v) {
+        uint64_t cs[4], sn[4];
+        if (w.turns) {
+            const float* tab = a.cos_sin + (size_t)pos * a.rot_dim + 8 * l;
+            load8(tab, cs);
+            load8(tab + (a.rot_dim >> 1), sn);
+        }
+        if (gains) norm_part<kLanes>(p, gain, a.eps, mask);
+        if (w.turns) turn_part<kInterleaved>(p, cs, sn);
+    }
+    if (is_q) {
+        uint4* dst = a.q_out + ((size_t)t * a.n_q_heads + h) * (D / 8);
+        dst[w.c0] = pack8(p.f);
+        dst[w.c1] = pack8(p.f + 4);
+    } else {
+        put_part<F8>(is_v ? a.v_cache : a.k_cache, cache_elem<D>(a, slot, h), p, is_v ? a.v_scale : a.k_scale, w.c0, w.c1);
+    }
+}
 
+// Many: kSide heads of a token side by side (32 / (kSide D / 16) tokens per
+// warp), turn after turn, kFlight turns in flight, so that the angles and
+// the gains are loaded once for all of a token's heads.
+constexpr int kFlight = 4;
+
+template <int D, bool F8, bool kInterleaved, int kSide>
+__global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs a) {
+    constexpr int kLanes = D / 16, kHeads = kSide, kGroup = kLanes * kSide;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t t = blockIdx.x * (kRopeThreads / kGroup) + threadIdx.x / kGroup;
+    if (t >= (uint32_t)a.num_tokens) return;           // whole tokens: a token's threads leave together
+    const int lane = threadIdx.x % kGroup, l = lane % kLanes, g = lane / kLanes;
+    const unsigned mask = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
+    const int q_turns = (a.n_q_heads + kHeads - 1) / kHeads, kv_turns = (a.n_kv_heads + kHeads - 1) / kHeads;
+    const Place<kInterleaved> w(l, a.rot_dim);
     const int pos = a.positions[t];
     const long long slot = a.slots[t];
     struct Raw {
         uint4 x0[kFlight], x1[kFlight];
     };
-    // heads first + u * kHeads + g (u < kFlight, in turns below `end`) of a tensor's row
-    auto load = [&](const __nv_bfloat16* rows, int turn, int end, int heads, Raw& r) {
+    // heads (turn + u) * kHeads + g of a tensor's row
+    auto load = [&](const __nv_bfloat16* rows, int turn, int heads, Raw& r) {
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             const int h = (turn + u) * kHeads + g;
-            if (turn + u < end && h < heads) {
+            if (h < heads) {
                 const uint4* src = reinterpret_cast<const uint4*>(rows + h * D);
-                r.x0[u] = src[c0];
-                r.x1[u] = src[c1];
+                r.x0[u] = src[w.c0];
+                r.x1[u] = src[w.c1];
             }
         }
     };
     const __nv_bfloat16* q = a.q + (long long)t * a.q_stride;
     const __nv_bfloat16* k = a.k + (long long)t * a.k_stride;
     const __nv_bfloat16* v = a.v + (long long)t * a.v_stride;
-    // the first heads' loads do not wait for the position
     Raw raw;
-    const int q_end = min(i1, q_turns);
-    if (i0 < q_end) load(q, i0, q_end, a.n_q_heads, raw);
+    load(q, 0, a.n_q_heads, raw);                      // these do not wait for the position
     if (pos < 0) return;                               // padding: nothing of the token is touched
     if (pos >= a.max_positions) {
-        if (lane == 0 && i0 == 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
+        if (lane == 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
         return;
     }
-    uint64_t cs[4], sn[4];                             // cosines and sines of this thread's 8 pairs
-    const bool rotates = turns && i0 < q_turns + kv_turns;
-    if (rotates) {
+    uint64_t cs[4], sn[4], gain[8];
+    if (w.turns) {
         const float* p = a.cos_sin + (size_t)pos * a.rot_dim + 8 * l;
         load8(p, cs);
         load8(p + (a.rot_dim >> 1), sn);
     }
-    uint64_t gain[8];
     const bool norm = a.q_weight != nullptr;
-    auto load_gain = [&](const float* w) {
+    auto load_gain = [&](const float* g_) {
         if (norm) {
-            load8(w + 8 * c0, gain);
-            load8(w + 8 * c1, gain + 4);
+            load8(g_ + 8 * w.c0, gain);
+            load8(g_ + 8 * w.c1, gain + 4);
         }
     };
-    auto work = [&](uint4 x0, uint4 x1) {              // whole warp
+    auto work = [&](uint4 x0, uint4 x1) {              // a head's threads
         Part p;
         unpack8(x0, p.f);
         unpack8(x1, p.f + 4);
-        if (norm) {
-            uint64_t sum = mul2(p.f[0], p.f[0]);
-#pragma unroll
-            for (int i = 1; i < 8; ++i) sum = fma2(p.f[i], p.f[i], sum);
-            const float2 two = unpair(sum);
-            float s = two.x + two.y;
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float inv = rsqrtf(s * (1.f / D) + a.eps);
-            const uint64_t ii = pair(inv, inv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p.f[i] = mul2(mul2(p.f[i], ii), gain[i]);
-        }
-        if (turns) {
-            if constexpr (kInterleaved) {
-                // pair c is (f[c].x, f[c].y)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = unpair(p.f[i]), cc = unpair(cs[i >> 1]), ss = unpair(sn[i >> 1]);
-                    const float c = i & 1 ? cc.y : cc.x, s = i & 1 ? ss.y : ss.x;
-                    p.f[i] = fma2(pair(f.y, f.x), pair(-s, s), mul2(p.f[i], pair(c, c)));
-                }
-            } else {
-                // pairs are (f[i], f[i + 4]), two at a time
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint64_t x = p.f[i], y = p.f[i + 4];
-                    const float2 s = unpair(sn[i]);
-                    p.f[i] = fma2(y, pair(-s.x, -s.y), mul2(x, cs[i]));
-                    p.f[i + 4] = fma2(x, sn[i], mul2(y, cs[i]));
-                }
-            }
-        }
+        if (norm) norm_part<kLanes>(p, gain, a.eps, mask);
+        if (w.turns) turn_part<kInterleaved>(p, cs, sn);
         return p;
     };
-    // ---- queries ----
     load_gain(a.q_weight);
-    for (int turn = i0; turn < q_end; turn += kFlight) {
-        Raw now = raw;
-        if (turn + kFlight < q_end) load(q, turn + kFlight, q_end, a.n_q_heads, raw);
+    for (int turn = 0; turn < q_turns; turn += kFlight) {
+        const Raw now = raw;
+        load(q, turn + kFlight, a.n_q_heads, raw);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            if (turn + u >= q_end) break;
+            if (turn + u >= q_turns) break;
             const int h = (turn + u) * kHeads + g;
             const Part p = work(now.x0[u], now.x1[u]);
             if (h < a.n_q_heads) {
                 uint4* dst = a.q_out + ((size_t)t * a.n_q_heads + h) * (D / 8);
-                dst[c0] = pack8(p.f);
-                dst[c1] = pack8(p.f + 4);
+                dst[w.c0] = pack8(p.f);
+                dst[w.c1] = pack8(p.f + 4);
             }
         }
     }
-    if (i1 <= q_turns || slot < 0) return;             // no keys here, or they stay out of the cache
+    if (slot < 0) return;                              // a key and value that stay out of the cache
     if (slot >= a.num_slots) {
         if (lane == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
         return;
     }
-    const long long blk = slot / a.block_size;
-    const int off = (int)(slot - blk * a.block_size);
-    const size_t row0 = ((size_t)blk * a.n_kv_heads * a.block_size + off) * D, head = (size_t)a.block_size * D;
-    auto put = [&](uint8_t* cache, int h, const Part& p, float scale) {
-        const size_t elem = row0 + h * head;
-        if constexpr (F8) {
-            uint2* dst = reinterpret_cast<uint2*>(cache + elem);
-            dst[c0] = codes8(p.f, scale);
-            dst[c1] = codes8(p.f + 4, scale);
-        } else {
-            uint4* dst = reinterpret_cast<uint4*>(cache + 2 * elem);
-            dst[c0] = pack8(p.f);
-            dst[c1] = pack8(p.f + 4);
-        }
-    };
-    // ---- keys, then values ----
-    const int k0 = max(0, i0 - q_turns), k_end = min(i1 - q_turns, kv_turns);
-    const int v0 = max(0, i0 - q_turns - kv_turns), v_end = min(i1 - q_turns - kv_turns, kv_turns);
+    const size_t row0 = cache_elem<D>(a, slot, 0), head = (size_t)a.block_size * D;
     Raw vraw;
-    if (k0 < k_end) {
-        load(k, k0, k_end, a.n_kv_heads, raw);
-        load_gain(a.k_weight);
-    }
-    if (v0 < v_end) load(v, v0, v_end, a.n_kv_heads, vraw);
-    for (int turn = k0; turn < k_end; turn += kFlight) {
-        if (turn > k0) load(k, turn, k_end, a.n_kv_heads, raw);
+    load(k, 0, a.n_kv_heads, raw);
+    load_gain(a.k_weight);
+    load(v, 0, a.n_kv_heads, vraw);
+    for (int turn = 0; turn < kv_turns; turn += kFlight) {
+        if (turn) load(k, turn, a.n_kv_heads, raw);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            if (turn + u >= k_end) break;
+            if (turn + u >= kv_turns) break;
             const int h = (turn + u) * kHeads + g;
             const Part p = work(raw.x0[u], raw.x1[u]);
-            if (h < a.n_kv_heads) put(a.k_cache, h, p, a.k_scale);
+            if (h < a.n_kv_heads) put_part<F8>(a.k_cache, row0 + h * head, p, a.k_scale, w.c0, w.c1);
         }
     }
-    for (int turn = v0; turn < v_end; turn += kFlight) {
-        if (turn > v0) load(v, turn, v_end, a.n_kv_heads, vraw);
+    for (int turn = 0; turn < kv_turns; turn += kFlight) {
+        if (turn) load(v, turn, a.n_kv_heads, vraw);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             const int h = (turn + u) * kHeads + g;
-            if (turn + u >= v_end || h >= a.n_kv_heads) break;
+            if (h >= a.n_kv_heads) break;
             if constexpr (F8) {
                 Part p;
                 unpack8(vraw.x0[u], p.f);
                 unpack8(vraw.x1[u], p.f + 4);
-                put(a.v_cache, h, p, a.v_scale);
+                put_part<true>(a.v_cache, row0 + h * head, p, a.v_scale, w.c0, w.c1);
             } else {
                 uint4* dst = reinterpret_cast<uint4*>(a.v_cache + 2 * (row0 + h * head));
-                dst[c0] = vraw.x0[u];
-                dst[c1] = vraw.x1[u];
+                dst[w.c0] = vraw.x0[u];
+                dst[w.c1] = vraw.x1[u];
             }
         }
     }
 }
 
+// Which kernel: the one per token is faster from about 12 million elements
+// on (32 + 2 x 8 heads of 128: 1000 tokens 10.5 against 6.8 us, 2000 13.1 /
+// 13.9, 4000 18.2 / 24.5, 32,048 122.7 / 168; 16 + 2 x 2 of 64: 5000 tokens
+// 7.6 / 5.7, 10,000 12.5 / 12.9, 40,000 36.2 / 42.5), if a token has heads
+// enough to share its angles (2 + 2 x 1: 40,000 tokens 38.5 / 21.9).
+template <int D, bool F8, bool kInterleaved>
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
+    constexpr int kLanes = D / 16, kSide = 2;
+    const int heads = a.n_q_heads + 2 * a.n_kv_heads;
+    const long long rows = (long long)a.num_tokens * heads;
+    if (heads >= 16 && rows * D >= 12000000) {
+        const int per = kRopeThreads / (kLanes * kSide);
+        return pa_host::launch_dependent(tokens_kernel<D, F8, kInterleaved, kSide>,
+                                         dim3((unsigned)(((long long)a.num_tokens + per - 1) / per)), dim3(kRopeThreads), 0,
+                                         st, a);
+    }
+    const int per = kRopeThreads / kLanes;
+    return pa_host::launch_dependent(heads_kernel<D, F8, kInterleaved>, dim3((unsigned)((rows + per - 1) / per)),
+                                     dim3(kRopeThreads), 0, st, a);
+}
+
 template <int D, bool F8>
 cudaError_t launch_rope(const RopeArgs& a, int interleaved, cudaStream_t st) {
-    // Few tokens: a token's turns over several warps, down to one turn each,
-    // until there are about 16 warps per SM; many: a warp per token.
-    const int heads = 32 / (D / 16);
-    const int turns = (a.n_q_heads + heads - 1) / heads + 2 * ((a.n_kv_heads + heads - 1) / heads);
-    const long long want = 152LL * 16 / a.num_tokens;
-    const int segments = (int)(want < 1 ? 1 : want > turns ? turns : want);
-    const int per = (turns + segments - 1) / segments, used = (turns + per - 1) / per;
-    const long long warps = (long long)a.num_tokens * used;
-    return pa_host::launch_dependent(
-        interleaved ? norm_rope_cache_kernel<D, F8, true> : norm_rope_cache_kernel<D, F8, false>,
-        dim3((unsigned)((warps + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeThreads), 0, st, a, used, per);
+    return interleaved ? launch_rope<D, F8, true>(a, st) : launch_rope<D, F8, false>(a, st);
 }
 
 int norm_rope_cache(void* q_out, void* k_cache, void* v_cache, const void* q, const void* k, const void* v,

@@ -397,3 +397,33 @@ def test_steps_of_new_tokens_from_projections_to_attention(fp8):
         for r, n in zip(batch, bring):
             if r >= 0:
                 p.lens[r] += n if n_step != 1 else (n + 1) // 2   # half of a draft is kept
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("Hq,Hkv,D,rot,inter,norm", [(32, 8, 128, 128, False, True), (17, 3, 64, 48, True, True),
+                                                     (13, 2, 128, 64, False, False)])
+def test_many_tokens_equal_the_same_tokens_a_few_at_a_time(Hq, Hkv, D, rot, inter, norm, fp8):
+    """The path that large calls take, with padding and bad places among its
+    tokens, gives the bits of the small calls' (which the oracle checks)."""
+    T, B = 12000000 // ((Hq + 2 * Hkv) * D) + 3, 16
+    q, k, v, pos, slots, (qw, kw), NB, table = _rope_case(T, Hq, Hkv, D, B, rot, norm, 50, longest=900)
+    pos[5], pos[6], pos[T - 1] = -1, 900, 17
+    slots[7], slots[8] = -1, NB * B
+    pos, slots = torch.from_numpy(pos).cuda(), torch.from_numpy(slots).cuda()
+    extra = dict(k_scale=0.013, v_scale=0.021) if fp8 else {}
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    got = []
+    for step in (T, 1000):
+        kc = torch.zeros((NB, Hkv, B, D), dtype=dt, device="cuda")
+        vc, out = kc.clone(), torch.zeros((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(0, T, step):
+            part = slice(i, min(T, i + step))
+            api.pa_qk_norm_rope_cache(out[part], kc, vc, q[part], k[part], v[part], pos[part], slots[part], table,
+                                      q_weight=qw, k_weight=kw, interleaved=inter, status=st, **extra)
+        assert st.item() == api.PA_DEV_BAD_POSITION | api.PA_DEV_BAD_SLOT
+        got.append((out, kc, vc))
+    for a, b in zip(*got):
+        a, b = (x.view(torch.int16) if x.dtype == torch.bfloat16 else x for x in (a, b))
+        assert torch.equal(a, b)
+    assert (got[0][0][5] == 0).all() and (got[0][0][6] == 0).all() and (got[0][0][7] != 0).any()
