@@ -10,11 +10,15 @@
 //   entry h + k = free[count - 1 - (first_i + k)]   the stack's order
 //   slot(p) = entry[p / B] * B + p % B              of each new position p
 //
-// Two launches: one block scans the batch (the totals decide whether the step
-// fits at all, so nothing may be written before they are known) and takes the
-// blocks; a grid then expands tables, positions and slots, each of them from
-// the first launch's outputs alone.  There is no scratch memory to share or
-// to reset, so two captured graphs never meet in one.
+// Nothing may be written before the totals say whether the step fits, and no
+// block may change a count that another still has to read.  Up to 2048
+// requests, one cluster of eight thread blocks does it all: each scans the
+// whole batch for itself, a cluster barrier stands between the reads of the
+// state and its change, and then each expands its share of tables, positions
+// and slots.  Larger steps take two launches: one block scans and takes the
+// blocks, and a grid expands from its outputs alone.  Either way there is no
+// scratch memory to share or to reset, so two captured graphs never meet in
+// one.
 
 #include "pa_common.cuh"
 
@@ -92,6 +96,51 @@ __device__ __forceinline__ int last_start(const int32_t* starts, int n, int x) {
     return lo;
 }
 
+// Thread t's kPer requests (entries [t * per, (t + 1) * per) of the batch) and
+// what is wrong with the step; `seen`: a zeroed bit per row in shared memory.
+template <int kPer>
+struct Requests {
+    int row[kPer], len[kPer], n[kPer], held[kPer], need[kPer];   // row -1: padding
+    long long sum_n = 0, sum_need = 0;
+    int bad = 0;
+
+    __device__ __forceinline__ void read(const PlanArgs& a, int per, uint32_t* seen) {
+        const long long cap = (long long)a.max_blocks << a.log2_block;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = threadIdx.x * per + k;
+            row[k] = -1;
+            len[k] = n[k] = held[k] = need[k] = 0;
+            if (k >= per || i >= a.num_seqs) continue;
+            const int r = a.seq_rows[i], m = a.new_lens[i];
+            if (r < 0) continue;                       // padding of the batch
+            if (r >= a.num_rows || (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u)) {
+                bad |= PA_DEV_BAD_ROW;
+                continue;
+            }
+            const int L = a.row_lens[r], h = a.row_blocks[r];
+            if (L < 0 || L > cap || h < 0 || h > a.max_blocks || m < 0 || (long long)L + m > cap) {
+                bad |= PA_DEV_BAD_CONTEXT;
+                continue;
+            }
+            row[k] = r;
+            len[k] = L;
+            n[k] = m;
+            held[k] = h;
+            const int nb = (int)(((long long)L + m + (1 << a.log2_block) - 1) >> a.log2_block);
+            need[k] = nb > h ? nb - h : 0;
+            sum_n += m;
+            sum_need += need[k];
+        }
+    }
+};
+
+// What is wrong with the step's totals.
+__device__ __forceinline__ int bad_totals(const PlanArgs& a, long long n, long long need, int count) {
+    return (n > a.num_tokens ? PA_DEV_BAD_CONTEXT : 0) |
+           (need > 0 && (count > a.free_capacity || need > count) ? PA_DEV_NO_BLOCKS : 0);
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     extern __shared__ uint32_t dyn[];                  // first_[num_seqs], then a bit per row
     __shared__ long long sh[32][2];
@@ -103,64 +152,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
     const int per = (S + kPlanThreads - 1) / kPlanThreads;
-    const long long cap = (long long)a.max_blocks << a.log2_block;
-    int row[kPlanPer], len[kPlanPer], n[kPlanPer], need[kPlanPer];
-    int bad = 0;
-    long long my_n = 0, my_need = 0;
-#pragma unroll
-    for (int k = 0; k < kPlanPer; ++k) {
-        const int i = t * per + k;
-        row[k] = -1;
-        len[k] = n[k] = need[k] = 0;
-        if (k >= per || i >= S) continue;
-        const int r = a.seq_rows[i];
-        if (r < 0) continue;                           // padding of the batch
-        if (r >= a.num_rows || (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u)) {
-            bad |= PA_DEV_BAD_ROW;
-            continue;
-        }
-        const int L = a.row_lens[r], h = a.row_blocks[r], m = a.new_lens[i];
-        if (L < 0 || L > cap || h < 0 || h > a.max_blocks || m < 0 || (long long)L + m > cap) {
-            bad |= PA_DEV_BAD_CONTEXT;
-            continue;
-        }
-        row[k] = r;
-        len[k] = L;
-        n[k] = m;
-        const int nb = (int)(((long long)L + m + (1 << a.log2_block) - 1) >> a.log2_block);
-        need[k] = nb > h ? nb - h : 0;
-        my_n += m;
-        my_need += need[k];
-    }
-    long long base_n = my_n, base_need = my_need, total_n, total_need;
+    Requests<kPlanPer> q;
+    q.read(a, per, seen);
+    long long base_n = q.sum_n, base_need = q.sum_need, total_n, total_need;
     scan_pair(base_n, base_need, total_n, total_need, sh);
     const int count = a.free_count ? *a.free_count : 0;
-    if (total_n > a.num_tokens) bad |= PA_DEV_BAD_CONTEXT;
-    if (total_need > 0 && (count > a.free_capacity || total_need > count)) bad |= PA_DEV_NO_BLOCKS;
-    if (__syncthreads_or(bad)) {
-        // all or nothing: every request keeps what it has and brings nothing
-        if (bad) pa::set_status(a.status, bad);
-#pragma unroll
-        for (int k = 0; k < kPlanPer; ++k) {
-            const int i = t * per + k;
-            if (k < per && i < S) {
-                a.context_lens[i] = len[k];
-                a.query_start[i] = 0;
-            }
-        }
-        if (t == 0) a.query_start[S] = 0;
-        return;
-    }
-    long long at_n = base_n, at_need = base_need;
+    const int bad = q.bad | bad_totals(a, total_n, total_need, count);
+    // all or nothing: every request of a refused step keeps what it has and brings nothing
+    const bool refused = __syncthreads_or(bad);
+    if (bad) pa::set_status(a.status, bad);
 #pragma unroll
     for (int k = 0; k < kPlanPer; ++k) {
         const int i = t * per + k;
         if (k >= per || i >= S) continue;
-        a.context_lens[i] = len[k] + n[k];
-        a.query_start[i] = (int)at_n;
-        first_[i] = (int)at_need;
-        at_n += n[k];
-        at_need += need[k];
+        a.context_lens[i] = q.len[k] + (refused ? 0 : q.n[k]);
+        a.query_start[i] = refused ? 0 : (int)base_n;
+        first_[i] = (int)base_need;
+        base_n += q.n[k];
+        base_need += q.need[k];
+    }
+    if (refused) {
+        if (t == 0) a.query_start[S] = 0;
+        return;
     }
     if (t == 0) a.query_start[S] = (int)total_n;
     if (total_need == 0) return;
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     __syncthreads();                                   // every thread has read the counts it needs
 #pragma unroll
     for (int k = 0; k < kPlanPer; ++k)
-        if (need[k]) a.row_blocks[row[k]] += need[k];
+        if (q.need[k]) a.row_blocks[q.row[k]] += q.need[k];
     if (t == 0) *a.free_count = count - (int)total_need;
 }
 
@@ -231,6 +244,123 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const PlanArgs a
     }
     a.positions[t] = pos;
     a.slot_mapping[t] = slot;
+}
+
+// The whole step in one cluster, for up to kFusedSeqs requests.
+constexpr int kFusedSeqs = 2048;
+constexpr int kFusedPer = kFusedSeqs / kPlanThreads;
+constexpr int kCluster = 8;
+
+struct Planned {
+    int row, ctx, held, first;             // row -1: padding
+};
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1) fused_plan_kernel(const PlanArgs a) {
+    extern __shared__ uint32_t dyn[];      // Planned[S], start[S + 1], a bit per row
+    __shared__ long long sh[32][2];
+    const int S = a.num_seqs, t = threadIdx.x, me = blockIdx.x * kPlanThreads + t;
+    Planned* plan = reinterpret_cast<Planned*>(dyn);
+    int32_t* start = reinterpret_cast<int32_t*>(plan + S);
+    uint32_t* seen = reinterpret_cast<uint32_t*>(start + S + 1);
+    for (int i = t; i < (a.num_rows + 31) / 32; i += kPlanThreads) seen[i] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncthreads();
+    const int per = (S + kPlanThreads - 1) / kPlanThreads, B = 1 << a.log2_block;
+    const int count = a.free_count ? *a.free_count : 0;
+    Requests<kFusedPer> q;
+    q.read(a, per, seen);
+    long long base_n = q.sum_n, base_need = q.sum_need, total_n, total_need;
+    scan_pair(base_n, base_need, total_n, total_need, sh);
+    const int bad = q.bad | bad_totals(a, total_n, total_need, count);
+    // all or nothing: every request of a refused step keeps what it has and brings nothing
+    const bool refused = __syncthreads_or(bad);
+    if (bad && blockIdx.x == 0) pa::set_status(a.status, bad);
+#pragma unroll
+    for (int k = 0; k < kFusedPer; ++k) {
+        const int i = t * per + k;
+        if (k >= per || i >= S) continue;
+        plan[i] = Planned{q.row[k], q.len[k] + (refused ? 0 : q.n[k]), q.held[k], (int)base_need};
+        start[i] = refused ? 0 : (int)base_n;
+        base_n += q.n[k];
+        base_need += q.need[k];
+    }
+    const int total = refused ? 0 : (int)total_n;
+    if (t == 0) start[S] = total;
+    __syncthreads();
+    // every block of the cluster has read the counts
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // block b of a request: one that it holds, or the step's
+    auto entry = [&](const Planned& p, int b) {
+        return b < p.held ? a.row_tables[(size_t)p.row * a.max_blocks + b]
+                          : a.free_blocks[count - 1 - (p.first + b - p.held)];
+    };
+    constexpr int kAll = kCluster * kPlanThreads;
+    for (int i = me; i < S; i += kAll) {
+        const Planned p = plan[i];
+        a.context_lens[i] = p.ctx;
+        a.query_start[i] = start[i];
+        const int nb = (p.ctx + B - 1) >> a.log2_block;
+        if (!refused && p.row >= 0 && nb > p.held) a.row_blocks[p.row] = nb;
+    }
+    if (me == 0) {
+        a.query_start[S] = total;
+        if (!refused && total_need > 0) *a.free_count = count - (int)total_need;
+    }
+    // tables: a warp per 1024 entries of a batch row; the step's blocks go into the request's own table too
+    const int lane = t & 31, segments = (a.max_blocks + kSegment - 1) / kSegment;
+    for (int w = me >> 5; w < S * segments; w += kAll / 32) {
+        const int i = w / segments, j0 = (w - i * segments) * kSegment, end = min(j0 + kSegment, a.max_blocks);
+        const Planned p = plan[i];
+        const int nb = p.row < 0 ? 0 : (p.ctx + B - 1) >> a.log2_block, old = min(nb, p.held);
+        int32_t* dst = a.block_tables + (size_t)i * a.max_blocks;
+        int32_t* own = a.row_tables + (size_t)(p.row < 0 ? 0 : p.row) * a.max_blocks;
+        const bool wide = (a.max_blocks & 3) == 0;
+        if (wide) {
+            for (int j = j0 + 4 * lane; j < end; j += 128) {
+                int4 x = make_int4(-1, -1, -1, -1);
+                if (j < old) {
+                    x = *reinterpret_cast<const int4*>(own + j);
+                    if (j + 1 >= old) x.y = -1;
+                    if (j + 2 >= old) x.z = -1;
+                    if (j + 3 >= old) x.w = -1;
+                }
+                if (j + 3 < p.held || j >= nb) {
+                    *reinterpret_cast<int4*>(dst + j) = x;
+                } else {                   // some of the four are the step's
+                    const int v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        int id = v[e];
+                        if (j + e >= p.held && j + e < nb) own[j + e] = id = entry(p, j + e);
+                        dst[j + e] = id;
+                    }
+                }
+            }
+        } else {
+            for (int j = j0 + lane; j < end; j += 32) {
+                int id = j < old ? own[j] : -1;
+                if (j >= p.held && j < nb) own[j] = id = entry(p, j);
+                dst[j] = id;
+            }
+        }
+    }
+    for (int x = me; x < a.num_tokens; x += kAll) {
+        int pos = -1;
+        long long slot = -1;
+        if (x < total) {
+            const int i = last_start(start, S, x);     // the last request that starts at or before x: it has x
+            const Planned p = plan[i];
+            pos = p.ctx - (start[i + 1] - x);
+            const int blk = entry(p, pos >> a.log2_block);
+            if (blk < 0 || blk >= a.num_blocks)
+                pa::set_status(a.status, PA_DEV_BAD_BLOCK_ID);
+            else
+                slot = ((long long)blk << a.log2_block) + (pos & (B - 1));
+        }
+        a.positions[x] = pos;
+        a.slot_mapping[x] = slot;
+    }
 }
 
 // Rows given back: their blocks go onto the stack in table order, row after
@@ -343,6 +473,19 @@ int pa_plan_step(int32_t* block_tables, int32_t* context_lens, int32_t* query_st
     a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     a.num_tokens = num_tokens;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // One cluster is faster while its eight SMs keep up with the tables and
+    // the tokens: 4 requests 4.7 us against 5.8, 256 of up to 256 blocks 6.0 /
+    // 7.4, of 1024 7.6 / 8.3, 512 of 256 7.2 / 7.9, 1024 of 256 9.9 / 8.4,
+    // 1000 of 2048 24 / 8.7 (each behind a copy of about 1.3 us).
+    if (num_seqs <= kFusedSeqs && (long long)num_seqs * max_blocks_per_seq + 8LL * num_tokens <= 270000) {
+        static int attr_fused[64] = {0};
+        const int smem = (int)sizeof(Planned) * num_seqs + 4 * (num_seqs + 1) + 4 * ((num_rows + 31) / 32);
+        if (smem > 40 * 1024 && pa_host::ensure_smem_attr(fused_plan_kernel, smem, attr_fused) != cudaSuccess)
+            return PA_ERR_CUDA;
+        return pa_host::launch_dependent(fused_plan_kernel, dim3(kCluster), dim3(kPlanThreads), smem, st, a) == cudaSuccess
+                   ? PA_OK
+                   : PA_ERR_CUDA;
+    }
     static int attr_plan[64] = {0};
     const int smem = 4 * num_seqs + 4 * ((num_rows + 31) / 32);
     if (smem > 40 * 1024 && pa_host::ensure_smem_attr(plan_kernel, smem, attr_plan) != cudaSuccess) return PA_ERR_CUDA;

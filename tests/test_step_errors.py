@@ -165,7 +165,7 @@ def test_binding_refuses_host_tensors_before_any_call(monkeypatch):
         api.pa_plan_step(z(2, 4), z(2), z(3), z(5), z(5, dt=torch.int64), z(2), z(2), z(8), z(8, 4), z(8), None, None,
                          16, 64)
     with pytest.raises(TypeError, match="context_lens"):
-        api._ptrs("x", context_lens=(z(2, dt=torch.int64), torch.int32, (2,)))
+        api._arg("x", "context_lens", z(2, dt=torch.int64), torch.int32, (2,), 0)
     b = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     with pytest.raises(ValueError, match="go together"):
         api.pa_qk_norm_rope_cache(b(1, 4, 64), b(2, 2, 16, 64), b(2, 2, 16, 64), b(1, 4, 64), b(1, 2, 64), b(1, 2, 64),
