@@ -9,20 +9,21 @@
 // "PagedAttention in vLLM: scattered memory, exact attention", sections 10
 // and 11: translation, the online softmax, the exact merge).
 //
+// This file serves up to 16 rows a KV head (and any number with a scale that
+// is not positive); pa_decode_wide.cu takes more.
+//
 // What bounds it: each K/V byte is read once for n * G rows, 4 * n * G
-// operations per two bytes, so up to some tens of rows the cache's bytes
-// bound it; beyond, the warp-level matrix products do.
-//  * A unit is a (sequence, KV head, tile of rows); its work is counted in
+// operations per two bytes, so the cache's bytes bound it.
+//  * A unit is a (sequence, KV head, tile of 16 rows); its work is counted in
 //    steps of 64 positions plus a constant for starting and joining it.  The
 //    grid is the resident blocks, and they take equal contiguous shares of
 //    all the work, computed from the lengths by every block for itself: no
 //    partition size to choose, no empty blocks on ragged batches, and at
 //    most two unfinished units per block whatever the batch.
 //  * Four warps of a block take 16 positions of a step each, from rings of
-//    shared-memory stages that TMA fills through the block table; with more
-//    than 32 rows a second four warps share the stages and take the other
-//    half of the rows.  The next unit's first tiles are in flight while the
-//    warps' states of a unit are joined, in the one stage they leave free.
+//    shared-memory stages that TMA fills through the block table.  The next
+//    unit's first tiles are in flight while the warps' states of a unit are
+//    joined, in the stages they leave free.
 //  * Rows are the rows of the products (S[16 x 16] = Q . K^T, then
 //    O[16 x D] += P . V), so the weights are the second product's operand as
 //    they come out of the first.
@@ -44,90 +45,71 @@ namespace {
 constexpr int kKeyWarps = 4;               // warps that split a step's positions
 constexpr int kTile = 16;                  // positions per warp and step
 constexpr int kStep = kKeyWarps * kTile;
+constexpr int kRows = 16;                  // rows of a unit
+constexpr int kThreads = 32 * kKeyWarps;
+constexpr int kBlocksPerSm = 3;
 constexpr float kWeightScale = 128.f;      // FP8: weights enter f16 products times 2^7 (at most 2^15)
 constexpr int kUnitCost = 5;               // steps that starting and joining a unit is worth
 constexpr int kMinSteps = 4;               // steps per block, at least
 
-// MT: 16-row tiles per warp; RG: groups of four warps, each with its own rows.
-template <int D, bool F8, int MT, int RG>
+template <int D, bool F8>
 struct Geo {
-    static constexpr int kRows = 16 * MT * RG;                   // rows of a unit
-    static constexpr int kThreads = 32 * kKeyWarps * RG;
     static constexpr int kSlabs = F8 ? 1 : D / 64;               // 128-byte boxes per cache row
     static constexpr int kSlabBytes = kTile * 128;
     static constexpr int kTileBytes = kSlabs * kSlabBytes;       // K or V of one warp's tile
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kBlocksPerSm = RG == 2 ? 1 : MT == 2 ? 2 : 3;
-    static constexpr int kRingBytes = (RG == 2 ? 160 : MT == 2 ? 96 : 64) * 1024;
+    static constexpr int kRingBytes = 64 * 1024;                 // of three blocks per SM
     static constexpr int kStages = kRingBytes / (kKeyWarps * kStageBytes);
-    // The joining of the warps' states takes the fp32 rows of one row tile
-    // per group: one stage of all key warps (bf16), or two (FP8).
-    static constexpr int kJoinParts = F8 ? 2 : 1;
-    static constexpr int kJoinStages = kJoinParts * RG;
+    // The joining of the warps' states takes the fp32 rows of the unit: one
+    // stage of all key warps (bf16), or two (E4M3).
+    static constexpr int kJoinStages = F8 ? 2 : 1;
     static constexpr int kAhead = kStages - kJoinStages;         // tiles of the next unit in flight meanwhile
     static constexpr int kQStride = 2 * D + 16;                  // bytes per row of q: ldmatrix rows hit distinct banks
     static constexpr int kSmem = 1024 + kRingBytes + kRows * (kQStride + 4) + kKeyWarps * kRows * 8 +
-                                 2 * kKeyWarps * kStages * 8;
+                                 kKeyWarps * kStages * 8;
     static constexpr int kSteps = D / 16;
     static_assert(kAhead >= 1, "the ring has to hold a tile of the next unit beside the join");
-    static_assert(kJoinParts * kKeyWarps * kStageBytes == 4 * kKeyWarps * 16 * D, "a row tile's states fill the join stages");
+    static_assert(kJoinStages * kKeyWarps * kStageBytes == 4 * kKeyWarps * kRows * D, "a unit's states fill the join stages");
 };
 
 __device__ __forceinline__ bool visible(const Unit& u, int log2_group, int row, int pos) {
     if (pos >= u.ctx) return false;
     if (pos < u.first) return true;
-    const int i = (u.row0 + row) >> log2_group, j = pos - u.first;
-    if (i >= u.n) return true;             // a row that is not there: any finite result will do
-    return u.words ? (j < 64 && (u.words[i] >> j & 1ull)) : j <= i;
+    const int i = (u.row0 + row) >> log2_group;
+    return i >= u.n || sees(u.words, i, pos - u.first);      // a row that is not there: any finite result will do
 }
 
-// One warp's running state: rows g and g + 8 of each row tile.
-template <int D, int MT>
+// One warp's running state: rows g and g + 8.
+template <int D>
 struct State {
-    float m[MT][2], l[MT][2];
-    float acc[MT][D / 8][4];
+    float m[2], l[2];
+    float acc[D / 8][4];
     __device__ __forceinline__ void reset() {
+        m[0] = m[1] = kNone;
+        l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            m[t][0] = m[t][1] = kNone;
-            l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) acc[t][d][0] = acc[t][d][1] = acc[t][d][2] = acc[t][d][3] = 0.f;
-        }
+        for (int d = 0; d < D / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
     }
 };
 
 // Fold one tile (K at shared address ks, V at vs, positions t0 .. t0 + 15)
-// into the warp's state.  qs: the warp's rows of q; row_base: their place in
-// the unit; c[t][h]: score factor of rows g + 8 h.
-template <int D, bool F8, int MT>
-__device__ __forceinline__ void fold_tile(State<D, MT>& st, uint32_t ks, uint32_t vs, uint32_t qs, int row_base,
-                                          const float (&c)[MT][2], int t0, const Unit& u, int log2_group, int lane,
-                                          const uint32_t (&qr)[MT == 1 ? D / 16 : 1][4]) {
-    constexpr int kSlabBytes = kTile * 128, kQStride = 2 * D + 16, kSteps = D / 16;
+// into the warp's state.  qr: the rows of q as A operands; c[h]: score factor
+// of rows g + 8 h.
+template <int D, bool F8>
+__device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const Unit& u,
+                                          int log2_group, int lane, const uint32_t (&qr)[D / 16][4]) {
+    constexpr int kSlabBytes = kTile * 128, kSteps = D / 16;
     const int g = lane >> 2, t4 = lane & 3;
     // ldmatrix addresses.  K as B operand: keys (lane & 7) + 8 (lane >> 4), chunk + (lane >> 3 & 1);
-    // V (transposed) as B, and q as A: rows (lane & 7) + 8 (lane >> 3 & 1), chunk + (lane >> 4)
+    // V (transposed) as B: rows (lane & 7) + 8 (lane >> 3 & 1), chunk + (lane >> 4)
     const int k_row = (lane & 7) + ((lane >> 4) << 3), k_add = (lane >> 3) & 1;
     const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_add = lane >> 4;
-    float s[MT][2][4];                     // [row tile][keys 0-7, 8-15]: (g, 2 t4), (g, 2 t4 + 1), rows g + 8
+    float s[2][4];                         // [keys 0-7, 8-15]: (g, 2 t4), (g, 2 t4 + 1), rows g + 8
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+    for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
     auto score = [&](int kk, uint32_t b00, uint32_t b01, uint32_t b10, uint32_t b11) {
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            uint32_t qa[4];
-            if constexpr (MT == 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) qa[e] = qr[kk][e];
-            } else {
-                pa::ldsm4(qs + (16 * t + v_row) * kQStride + (2 * kk + v_add) * 16, qa);
-            }
-            pa::mma16816<F8>(s[t][0], qa, b00, b01);
-            pa::mma16816<F8>(s[t][1], qa, b10, b11);
-        }
+        pa::mma16816<F8>(s[0], qr[kk], b00, b01);
+        pa::mma16816<F8>(s[1], qr[kk], b10, b11);
     };
     if constexpr (F8) {
         // a chunk of 16 codes is one k-step; lane (g, t4) gets codes 4 t4 .. 4 t4 + 3 of key g
@@ -148,65 +130,55 @@ __device__ __forceinline__ void fold_tile(State<D, MT>& st, uint32_t ks, uint32_
             score(kk, r[0], r[1], r[2], r[3]);
         }
     }
-    const bool tail = t0 + kTile > u.first;            // some row may not see some position
-    if (tail) {
+    if (t0 + kTile > u.first) {                        // some row may not see some position
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!visible(u, log2_group, row_base + 16 * t + g + 8 * (e >> 1), t0 + 8 * n + 2 * t4 + (e & 1)))
-                        s[t][n][e] = -INFINITY;
+            for (int e = 0; e < 4; ++e)
+                if (!visible(u, log2_group, g + 8 * (e >> 1), t0 + 8 * n + 2 * t4 + (e & 1))) s[n][e] = -INFINITY;
     }
     // how far the tile's scores rise above the running maxima
     float over = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float top = fmaxf(fmaxf(s[t][0][2 * h], s[t][0][2 * h + 1]), fmaxf(s[t][1][2 * h], s[t][1][2 * h + 1]));
-            over = fmaxf(over, fmaf(top, c[t][h], -st.m[t][h]));
-        }
+    for (int h = 0; h < 2; ++h) {
+        const float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+        over = fmaxf(over, fmaf(top, c[h], -st.m[h]));
+    }
     if (__any_sync(0xffffffffu, over > kRaise)) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int h = 0; h < 2; ++h) {
+            float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float m = fmaxf(st.m[h], top * c[h]);
+            const float f = pa::exp2_approx(st.m[h] - m);
+            st.m[h] = m;
+            st.l[h] *= f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float top = fmaxf(fmaxf(s[t][0][2 * h], s[t][0][2 * h + 1]), fmaxf(s[t][1][2 * h], s[t][1][2 * h + 1]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float m = fmaxf(st.m[t][h], top * c[t][h]);
-                const float f = pa::exp2_approx(st.m[t][h] - m);
-                st.m[t][h] = m;
-                st.l[t][h] *= f;
-#pragma unroll
-                for (int d = 0; d < D / 8; ++d) {
-                    st.acc[t][d][2 * h] *= f;
-                    st.acc[t][d][2 * h + 1] *= f;
-                }
+            for (int d = 0; d < D / 8; ++d) {
+                st.acc[d][2 * h] *= f;
+                st.acc[d][2 * h + 1] *= f;
             }
+        }
     }
     // weights as the A operand: bf16 in two terms (a relative 2^-16), f16 times 2^7 (2^-11)
-    uint32_t ph[MT][4], pl[MT][4];
+    uint32_t ph[4], pl[4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float p0 = pa::exp2_approx(fmaf(s[t][n][2 * h], c[t][h], -st.m[t][h]));
-                const float p1 = pa::exp2_approx(fmaf(s[t][n][2 * h + 1], c[t][h], -st.m[t][h]));
-                st.l[t][h] += p0 + p1;
-                if constexpr (F8) {
-                    ph[t][2 * n + h] = pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale);
-                } else {
-                    const uint32_t w = pa::pack_bf16x2(p0, p1);
-                    const float2 f = pa::bf16x2_to_float2(w);
-                    ph[t][2 * n + h] = w;
-                    pl[t][2 * n + h] = pa::pack_bf16x2(p0 - f.x, p1 - f.y);
-                }
+        for (int n = 0; n < 2; ++n) {
+            const float p0 = pa::exp2_approx(fmaf(s[n][2 * h], c[h], -st.m[h]));
+            const float p1 = pa::exp2_approx(fmaf(s[n][2 * h + 1], c[h], -st.m[h]));
+            st.l[h] += p0 + p1;
+            if constexpr (F8) {
+                ph[2 * n + h] = pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale);
+            } else {
+                const uint32_t w = pa::pack_bf16x2(p0, p1);
+                const float2 f = pa::bf16x2_to_float2(w);
+                ph[2 * n + h] = w;
+                pl[2 * n + h] = pa::pack_bf16x2(p0 - f.x, p1 - f.y);
             }
+        }
     // O += P . V; V rows past the context are zeroed (0 * NaN)
     const int nv = u.ctx - t0;
     auto values = [&](bool masked, uint32_t mlo, uint32_t mhi) {
@@ -229,9 +201,7 @@ __device__ __forceinline__ void fold_tile(State<D, MT>& st, uint32_t ks, uint32_
                             b0[odd] &= mlo;
                             b1[odd] &= mhi;
                         }
-#pragma unroll
-                        for (int t = 0; t < MT; ++t)
-                            pa::mma16816<true>(st.acc[t][2 * (2 * j + x) + odd], ph[t], b0[odd], b1[odd]);
+                        pa::mma16816<true>(st.acc[2 * (2 * j + x) + odd], ph, b0[odd], b1[odd]);
                     }
                 }
             } else {
@@ -240,11 +210,8 @@ __device__ __forceinline__ void fold_tile(State<D, MT>& st, uint32_t ks, uint32_
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t b0 = masked ? r[2 * x] & mlo : r[2 * x];
                     const uint32_t b1 = masked ? r[2 * x + 1] & mhi : r[2 * x + 1];
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        pa::mma16816<false>(st.acc[t][2 * j + x], ph[t], b0, b1);
-                        pa::mma16816<false>(st.acc[t][2 * j + x], pl[t], b0, b1);
-                    }
+                    pa::mma16816<false>(st.acc[2 * j + x], ph, b0, b1);
+                    pa::mma16816<false>(st.acc[2 * j + x], pl, b0, b1);
                 }
             }
         }
@@ -258,33 +225,30 @@ __device__ __forceinline__ void fold_tile(State<D, MT>& st, uint32_t ks, uint32_
     }
 }
 
-template <int D, bool F8, int MT, int RG>
-__global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, RG>::kBlocksPerSm)
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const MultiArgs a) {
-    using G = Geo<D, F8, MT, RG>;
-    constexpr int kRows = G::kRows, kStages = G::kStages, kThreads = G::kThreads;
+    using G = Geo<D, F8>;
+    constexpr int kStages = G::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* qsm = ring + G::kRingBytes;                          // [kRows][kQStride]
     float* q_scale = reinterpret_cast<float*>(qsm + kRows * G::kQStride);   // FP8: score factor per row
     float2* stats = reinterpret_cast<float2*>(q_scale + kRows);   // [key warp][row]: maximum and sum
     uint64_t* full = reinterpret_cast<uint64_t*>(stats + kKeyWarps * kRows);   // [key warp][stage]
-    uint64_t* empty = full + kKeyWarps * kStages;                 // RG > 1: both groups are done with it
-    __shared__ long long sums[kKeyWarps * RG];
+    __shared__ long long sums[kKeyWarps];
+    __shared__ int unfinite[2];                                   // per unit parity: some new value is not finite
     // Thread 0 walks the share two units ahead; a unit's place is free again
     // two barriers after its join.
     __shared__ Walk walk;
     __shared__ Unit units[4];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kw = warp % kKeyWarps, rg = warp / kKeyWarps;
     const int B = 1 << a.log2_block, heads = a.n_kv_heads;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kKeyWarps * kStages; ++i) {
-            pa::mbar_init(&full[i], 1);
-            pa::mbar_init(&empty[i], RG);
-        }
+        for (int i = 0; i < kKeyWarps * kStages; ++i) pa::mbar_init(&full[i], 1);
+        unfinite[0] = unfinite[1] = 0;
         pa::fence_mbar_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -299,17 +263,16 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
     if (!units[0].valid) return;                                 // a share that ends in a unit's constant part
 
     const uint64_t policy = pa::l2_evict_first_policy();
-    const uint32_t ring0 = pa::smem_addr(ring) + kw * G::kStageBytes;
-    const uint32_t qs = pa::smem_addr(qsm) + rg * (16 * MT) * G::kQStride;
-    uint64_t* wfull = full + kw * kStages;
-    uint64_t* wempty = empty + kw * kStages;
+    const uint32_t ring0 = pa::smem_addr(ring) + warp * G::kStageBytes;
+    const uint32_t qs = pa::smem_addr(qsm);
+    uint64_t* wfull = full + warp * kStages;
     auto stage_at = [&](int stage) { return ring0 + stage * (kKeyWarps * G::kStageBytes); };
 
-    // A warp's tile k of a unit holds positions (st0 + k) * 64 + 16 kw on.  Its
+    // A warp's tile k of a unit holds positions (st0 + k) * 64 + 16 warp on.  Its
     // table entries come 32 tiles at a time, one per lane, the next 32 ahead.
     auto fetch = [&](const Unit& u, int k, int& e0, int& e1) {
         e0 = e1 = 0;
-        const int t0 = (u.st0 + k) * kStep + kw * kTile;
+        const int t0 = (u.st0 + k) * kStep + warp * kTile;
         if (k < u.len && t0 < u.ctx) {
             e0 = u.table[t0 >> a.log2_block];
             if (B < kTile && t0 + B < u.ctx) e1 = u.table[(t0 >> a.log2_block) + 1];
@@ -317,7 +280,7 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
     };
     int e0 = 0, e1 = 0, f0 = 0, f1 = 0;
     int used = 0;                                                 // tiles of the ring before the current unit's
-    auto issue = [&](const Unit& u, int k) {                      // whole warp of group 0
+    auto issue = [&](const Unit& u, int k) {                      // whole warp
         if (k && (k & 31) == 0) {
             e0 = f0;
             e1 = f1;
@@ -327,13 +290,8 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
         if (lane == 0) {
             const int at = used + k, stage = at % kStages;
             uint64_t* bar = &wfull[stage];
-            bool free = true;
-            if (RG > 1 && at >= kStages)
-                free = pa::mbar_wait_bounded(&wempty[stage], ((at / kStages) - 1) & 1, kMaxProbes);
-            const int t0 = (u.st0 + k) * kStep + kw * kTile;
-            if (!free) {
-                pa::set_status(a.status, PA_DEV_WAIT_TIMEOUT);    // nothing is issued: its readers give up too
-            } else if (t0 >= u.ctx) {
+            const int t0 = (u.st0 + k) * kStep + warp * kTile;
+            if (t0 >= u.ctx) {
                 pa::mbar_arrive(bar);                             // no such tile: the stage goes by empty
             } else {
                 const int box = B < kTile ? B : kTile, boxes = (B < kTile && t0 + B < u.ctx) ? 2 : 1;
@@ -410,40 +368,36 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
     };
 
     uint4 qv[kQPer];
-    if (rg == 0) {
-        fetch(units[0], lane, e0, e1);
-        fetch(units[0], 32 + lane, f0, f1);
-        for (int k = 0; k < G::kAhead; ++k)
-            if (k < units[0].len) issue(units[0], k);
-    }
+    fetch(units[0], lane, e0, e1);
+    fetch(units[0], 32 + lane, f0, f1);
+    for (int k = 0; k < G::kAhead; ++k)
+        if (k < units[0].len) issue(units[0], k);
     load_q(units[0], qv);
     for (int nth = 0;; ++nth) {
         const Unit& u = units[nth & 3];
         const Unit& next = units[(nth + 1) & 3];
         store_q(qv);
         __syncthreads();
-        const int len = u.len, ctx = u.ctx, base = u.st0 * kStep + kw * kTile;
+        const int len = u.len, ctx = u.ctx, base = u.st0 * kStep + warp * kTile;
         const bool more = next.valid;
-        if (rg == 0)
-            for (int k = G::kAhead; k < kStages; ++k)
-                if (k < len) issue(u, k);
+        for (int k = G::kAhead; k < kStages; ++k)
+            if (k < len) issue(u, k);
         int n0 = 0, n1 = 0;
-        if (more && rg == 0) fetch(next, lane, n0, n1);
-        if (threadIdx.x == 0) next_unit<kRows, kStep, kUnitCost>(walk, units[(nth + 2) & 3], a);
-        __syncwarp();
-        uint32_t qr[MT == 1 ? G::kSteps : 1][4];
-        if constexpr (MT == 1) {
-#pragma unroll
-            for (int kk = 0; kk < G::kSteps; ++kk)
-                pa::ldsm4(qs + ((lane & 7) + (((lane >> 3) & 1) << 3)) * G::kQStride + (2 * kk + (lane >> 4)) * 16, qr[kk]);
+        if (more) fetch(next, lane, n0, n1);
+        if (threadIdx.x == 0) {
+            next_unit<kRows, kStep, kUnitCost>(walk, units[(nth + 2) & 3], a);
+            unfinite[(nth + 1) & 1] = 0;                          // (its last readers are a barrier behind)
         }
-        float c[MT][2];
+        __syncwarp();
+        uint32_t qr[G::kSteps][4];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int kk = 0; kk < G::kSteps; ++kk)
+            pa::ldsm4(qs + ((lane & 7) + (((lane >> 3) & 1) << 3)) * G::kQStride + (2 * kk + (lane >> 4)) * 16, qr[kk]);
+        float c[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) c[t][h] = F8 ? q_scale[rg * 16 * MT + 16 * t + (lane >> 2) + 8 * h] : a.scale_log2;
+        for (int h = 0; h < 2; ++h) c[h] = F8 ? q_scale[(lane >> 2) + 8 * h] : a.scale_log2;
 
-        State<D, MT> st;
+        State<D> st;
         st.reset();
         bool landed = true;
         for (int k = 0; k < len; ++k) {
@@ -460,104 +414,104 @@ __global__ void __launch_bounds__(Geo<D, F8, MT, RG>::kThreads, Geo<D, F8, MT, R
             const int t0 = base + k * kStep;
             if (t0 < ctx) {
                 const uint32_t ks = stage_at(stage);
-                fold_tile<D, F8, MT>(st, ks, ks + G::kTileBytes, qs, rg * 16 * MT, c, t0, u, a.log2_group, lane, qr);
+                if (t0 + kTile > u.first) {
+                    const int from = max(0, u.first - t0);
+                    uint8_t* v = ring + stage * (kKeyWarps * G::kStageBytes) + warp * G::kStageBytes + G::kTileBytes;
+                    if (drop_unfinite<F8, G::kSlabs>(v, G::kSlabBytes, from, min(kTile, ctx - t0), lane, 32))
+                        unfinite[nth & 1] = 1;
+                    __syncwarp();
+                }
+                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, u, a.log2_group, lane, qr);
             }
             __syncwarp();
-            if constexpr (RG == 1) {
-                if (k + kStages < len) issue(u, k + kStages);
-            } else {
-                if (lane == 0) pa::mbar_arrive(&wempty[stage]);
-                // the stage before: the other group is done with it by now, or nearly
-                if (rg == 0 && k && k - 1 + kStages < len) issue(u, k - 1 + kStages);
-            }
+            if (k + kStages < len) issue(u, k + kStages);
         }
         used += len;
         if (!__syncthreads_and(landed)) return;                   // every tile of the unit is consumed
-        if (more && rg == 0) {
+        if (more) {
             e0 = n0;
             e1 = n1;
             fetch(next, 32 + lane, f0, f1);
             for (int k = 0; k < G::kAhead; ++k)
                 if (k < next.len) issue(next, k);
+            load_q(next, qv);
         }
-        if (more) load_q(next, qv);
 
-        // ---- join the key warps' states (the exact block merge), a row tile of each group at a time ----
+        // ---- join the key warps' states (the exact block merge) ----
         const int g = lane >> 2, t4 = lane & 3;
-        auto join_row = [&](int group, int w, int r) {            // fp32 row r (0..15) of key warp w
-            const int part = group * G::kJoinParts + (F8 ? r >> 3 : 0), rows = F8 ? 8 : 16;
-            const int stage = (used + G::kAhead + part) % kStages;
-            return reinterpret_cast<float*>(ring + stage * (kKeyWarps * G::kStageBytes)) + (w * rows + (r & (rows - 1))) * D;
+        auto join_row = [&](int w, int r) {                       // fp32 row r of key warp w
+            const int rows = kRows / G::kJoinStages, stage = (used + G::kAhead + r / rows) % kStages;
+            return reinterpret_cast<float*>(ring + stage * (kKeyWarps * G::kStageBytes)) + (w * rows + r % rows) * D;
         };
         auto spread = [](int r) { return ((r & 1) << 4) | ((r & 2) << 2); };   // rows to distinct banks
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            if (t) __syncthreads();
+        for (int h = 0; h < 2; ++h) {
+            float l = st.l[h];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int r = g + 8 * h;
+            if (t4 == 0) stats[warp * kRows + r] = make_float2(st.m[h], l);
+            float* row = join_row(warp, r);
+            if constexpr (F8) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float l = st.l[t][h];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                const int r = g + 8 * h;
-                if (t4 == 0) stats[kw * kRows + (rg * MT + t) * 16 + r] = make_float2(st.m[t][h], l);
-                float* row = join_row(rg, kw, r);
-                if constexpr (F8) {
+                for (int x = 0; x < D / 16; ++x)
+                    *reinterpret_cast<float4*>(row + ((16 * x + 4 * t4) ^ spread(r))) = make_float4(
+                        st.acc[2 * x][2 * h], st.acc[2 * x + 1][2 * h], st.acc[2 * x][2 * h + 1], st.acc[2 * x + 1][2 * h + 1]);
+            } else {
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x)
-                        *reinterpret_cast<float4*>(row + ((16 * x + 4 * t4) ^ spread(r))) =
-                            make_float4(st.acc[t][2 * x][2 * h], st.acc[t][2 * x + 1][2 * h],
-                                        st.acc[t][2 * x][2 * h + 1], st.acc[t][2 * x + 1][2 * h + 1]);
-                } else {
-#pragma unroll
-                    for (int d = 0; d < D / 8; ++d)
-                        *reinterpret_cast<float2*>(row + ((8 * d + 2 * t4) ^ spread(r))) =
-                            make_float2(st.acc[t][d][2 * h], st.acc[t][d][2 * h + 1]);
-                }
+                for (int d = 0; d < D / 8; ++d)
+                    *reinterpret_cast<float2*>(row + ((8 * d + 2 * t4) ^ spread(r))) =
+                        make_float2(st.acc[d][2 * h], st.acc[d][2 * h + 1]);
             }
-            __syncthreads();
-            const bool whole = len == u.steps;
-            const int slot = 2 * blockIdx.x + (u.st0 == 0 ? 1 : 0);
-            for (int x = threadIdx.x; x < RG * 16 * (D / 4); x += kThreads) {
-                const int group = x / (16 * (D / 4)), r = x / (D / 4) % 16, d = x % (D / 4) * 4;
-                const int in_unit = (group * MT + t) * 16 + r;
-                const int row = u.row0 + in_unit, i = row >> a.log2_group;
-                if (i >= u.n) continue;
-                float2 ml[kKeyWarps];
-                float M = kNone;
-#pragma unroll
-                for (int w = 0; w < kKeyWarps; ++w) {
-                    ml[w] = stats[w * kRows + in_unit];
-                    M = fmaxf(M, ml[w].x);
-                }
-                float Z = 0.f;
-                float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kKeyWarps; ++w) {
-                    const float f = pa::exp2_approx(ml[w].x - M);
-                    const float4 v = *reinterpret_cast<const float4*>(join_row(group, w, r) + (d ^ spread(r)));
-                    Z += f * ml[w].y;
-                    U.x += f * v.x;
-                    U.y += f * v.y;
-                    U.z += f * v.z;
-                    U.w += f * v.w;
-                }
-                if (whole) {
-                    const float f = Z == 0.f ? 0.f : a.v_scale / Z;
-                    put4(a.out, a.out_f32,
-                         ((size_t)(u.q0 + i) * a.n_q_heads + (u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))) * D + d,
-                         make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
-                } else {
-                    const size_t at = (size_t)slot * kRows + in_unit;
-                    *reinterpret_cast<float4*>(a.part_u + at * D + d) = U;
-                    if (d == 0) {
-                        a.part_m[at] = M;
-                        a.part_z[at] = Z;
-                    }
-                }
-            }
-            if (t == 0 && !whole && u.st0 == 0 && threadIdx.x == 0)   // this block begins the unit
-                a.pieces[blockIdx.x] = make_int4(u.seq, u.kvh, u.tile, u.last);
         }
+        __syncthreads();
+        const bool whole = len == u.steps;
+        const int slot = 2 * blockIdx.x + (u.st0 == 0 ? 1 : 0);
+        for (int x = threadIdx.x; x < kRows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), d = x % (D / 4) * 4;
+            const int row = u.row0 + r, i = row >> a.log2_group;
+            if (i >= u.n) continue;
+            float2 ml[kKeyWarps];
+            float M = kNone;
+#pragma unroll
+            for (int w = 0; w < kKeyWarps; ++w) {
+                ml[w] = stats[w * kRows + r];
+                M = fmaxf(M, ml[w].x);
+            }
+            float Z = 0.f;
+            float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kKeyWarps; ++w) {
+                const float f = pa::exp2_approx(ml[w].x - M);
+                const float4 v = *reinterpret_cast<const float4*>(join_row(w, r) + (d ^ spread(r)));
+                Z += f * ml[w].y;
+                U.x += f * v.x;
+                U.y += f * v.y;
+                U.z += f * v.z;
+                U.w += f * v.w;
+            }
+            if (whole) {
+                const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+                put4(a.out, a.out_f32,
+                     ((size_t)(u.q0 + i) * a.n_q_heads + (u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))) * D + d,
+                     make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
+            } else {
+                const size_t at = (size_t)slot * kRows + r;
+                *reinterpret_cast<float4*>(a.part_u + at * D + d) = U;
+                if (d == 0) {
+                    a.part_m[at] = M;
+                    a.part_z[at] = Z;
+                }
+            }
+        }
+        if (__builtin_expect(unfinite[nth & 1], 0))
+            for (int x = threadIdx.x; x < kRows * (D / 4); x += kThreads) {   // (to what the thread itself has written)
+                const int r = x / (D / 4), d = x % (D / 4) * 4;
+                add_unfinite<D, F8>(a, u.seq, u.kvh, u.row0 + r, u.st0 * kStep, (u.st0 + len) * kStep, d,
+                                    whole ? nullptr : a.part_u + ((size_t)slot * kRows + r) * D + d);
+            }
+        if (!whole && u.st0 == 0 && threadIdx.x == 0)             // this block begins the unit
+            a.pieces[blockIdx.x] = make_int4(u.seq, u.kvh, u.tile, u.last);
         if (!more) return;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the join's stages go back to TMA (after the barrier above)
     }
@@ -578,23 +532,24 @@ int sms() {
     return n;
 }
 
-#ifndef PA_F8_WIDE_FROM
-#define PA_F8_WIDE_FROM 17
-#endif
-// Whether the units of 64 (or 128) rows of pa_decode_wide.cu serve a call.
-// They take a positive scale (bf16) and measured faster from more than 32
-// rows a KV head on for bf16 caches, more than 16 for E4M3.
-bool is_wide(bool f8, float scale, long long rows) { return f8 ? rows >= PA_F8_WIDE_FROM : scale > 0.f && rows > 32; }
+// Whether the units of 64 (or 128) rows of pa_decode_wide.cu serve a call:
+// from more than 16 rows a KV head on, where they read the cache once for all
+// of them.  Both sides measured at 8 KV heads of 128:
+//   sequences x context, rows    here      wide
+//   64 x 4096 bf16, 16           172 us    -
+//   64 x 4096 bf16, 20           173       165 us   (32-row units here)
+//   64 x 4096 bf16, 32           175       169
+//   512 x 500 bf16, 32           232       190
+//   64 x 4096 E4M3, 16           102       119
+//   512 x 500 E4M3, 16           131       232
+// Its bf16 products take a positive scale only; others go 16 rows at a time.
+bool is_wide(bool f8, float scale, long long rows) { return rows > kRows && (f8 || scale > 0.f); }
 
-// Rows of a unit: the fewest that hold all rows of a KV head, at most 64, or
-// 128 for bf16 on the wide kernel.
-int unit_rows(long long rows, bool f8, bool wide) {
-    if (wide) return f8 || rows <= 64 ? 64 : 128;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
+// Rows of a unit: on the wide kernel 64, and 128 for bf16 where a KV head has more.
+int unit_rows(long long rows, bool f8, bool wide) { return !wide ? kRows : f8 || rows <= 64 ? 64 : 128; }
 
 // Resident blocks of the device.
-int max_grid(int rows) { return sms() * (rows == 16 ? 3 : rows == 32 ? 2 : 1); }
+int max_grid(bool wide) { return sms() * (wide ? 1 : kBlocksPerSm); }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -604,22 +559,14 @@ size_t workspace_size(int grid, int unit, int d) {
     return up256(16 * (size_t)grid) + 2 * up256(4 * rows) + 4 * rows * d;
 }
 
-template <int D, bool F8, int MT, int RG>
+template <int D, bool F8>
 int launch_multi(const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& a, int grid, cudaStream_t st) {
     static int attr[64] = {0};
-    using G = Geo<D, F8, MT, RG>;
-    if (pa_host::ensure_smem_attr(multi_kernel<D, F8, MT, RG>, G::kSmem, attr) != cudaSuccess) return PA_ERR_CUDA;
-    return pa_host::launch_dependent(multi_kernel<D, F8, MT, RG>, dim3(grid), dim3(G::kThreads), G::kSmem, st, mk, mv,
-                                     a) == cudaSuccess
+    constexpr int kSmem = Geo<D, F8>::kSmem;
+    if (pa_host::ensure_smem_attr(multi_kernel<D, F8>, kSmem, attr) != cudaSuccess) return PA_ERR_CUDA;
+    return pa_host::launch_dependent(multi_kernel<D, F8>, dim3(grid), dim3(kThreads), kSmem, st, mk, mv, a) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
-}
-
-template <int D, bool F8>
-int launch_rows(int rows, const CUtensorMap& mk, const CUtensorMap& mv, const MultiArgs& a, int grid, cudaStream_t st) {
-    return rows == 16   ? launch_multi<D, F8, 1, 1>(mk, mv, a, grid, st)
-           : rows == 32 ? launch_multi<D, F8, 2, 1>(mk, mv, a, grid, st)
-                        : launch_multi<D, F8, 2, 2>(mk, mv, a, grid, st);
 }
 
 int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache,
@@ -652,7 +599,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     const bool wide = is_wide(f8, scale, all_rows);
     const int unit = unit_rows(all_rows, f8, wide);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
-    const int most = wide ? sms() : max_grid(unit);
+    const int most = max_grid(wide);
     if (most <= 0) return PA_ERR_CUDA;
     if (workspace_bytes < workspace_size(most, unit, d_head)) return PA_ERR_WORKSPACE;
 
@@ -669,6 +616,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
 
     a.out = out;
     a.q = static_cast<const __nv_bfloat16*>(q);
+    a.v_cache = v_cache;
     a.block_tables = block_tables;
     a.query_start = query_start;
     a.context_lens = context_lens;
@@ -708,9 +656,9 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     if (wide)
         rc = launch_wide(unit, d_head, f8, q, block_size, mk, mv, a, grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     else
-        rc = f8 ? launch_rows<128, true>(unit, mk, mv, a, grid, st)
-             : d_head == 128 ? launch_rows<128, false>(unit, mk, mv, a, grid, st)
-                             : launch_rows<64, false>(unit, mk, mv, a, grid, st);
+        rc = f8 ? launch_multi<128, true>(mk, mv, a, grid, st)
+             : d_head == 128 ? launch_multi<128, false>(mk, mv, a, grid, st)
+                             : launch_multi<64, false>(mk, mv, a, grid, st);
     if (rc != PA_OK) return rc;
     return pa_host::launch_dependent(d_head == 128 ? merge_kernel<128> : merge_kernel<64>, dim3(grid, kMergeSplit),
                                      dim3(kMergeThreads), 0, st, a, unit) == cudaSuccess
@@ -730,7 +678,7 @@ size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads, int n_kv
     for (int x = 0; x < 4; ++x) {
         const bool f8 = x & 1, wide = is_wide(f8, x & 2 ? 1.f : -1.f, rows);
         const int unit = unit_rows(rows, f8, wide);
-        const size_t n = workspace_size(wide ? sms() : max_grid(unit), unit, d_head);
+        const size_t n = workspace_size(max_grid(wide), unit, d_head);
         most = n > most ? n : most;
     }
     return most;

@@ -30,8 +30,9 @@
 //  * E4M3: the codes are operands as they lie in the cache.  q is the exact
 //    sum of two E4M3 terms, in a row's two lanes, whose scores the softmax
 //    adds; weights are three E4M3 terms in two products.
-//  * V rows past the context are zeroed in shared memory before the last
-//    tile's products (0 * NaN).
+//  * A warp of its own zeroes V rows past the context (0 * NaN) in shared
+//    memory, and new positions' values that are not finite, which the rows
+//    that see them add at the unit's end.
 
 #include "pa_multi.cuh"
 
@@ -45,12 +46,13 @@ constexpr int kKWarp = 8;                  // walks the share, loads K
 constexpr int kVWarp = 9;                  // loads q (free when its unit's last scores are done) and V
 constexpr int kScoreWarp = 10;             // issues the score products and owns the tensor memory
 constexpr int kOutWarp = 12;               // 12 .. 15 read the accumulators out at a unit's end
-constexpr int kThreads = 544;
+constexpr int kCheckWarp = 17;             // makes V's tiles fit for the products
+constexpr int kThreads = 576;
 // warps 11 and 16 issue the value products of groups 0 and 1
 __device__ __forceinline__ int value_group(int warp) { return warp == 11 ? 0 : warp == 16 ? 1 : -1; }
 constexpr int kHalfKv = kKv / 2;           // positions of a tile per group
 constexpr int kUnits = 4;                  // units posted ahead
-constexpr int kUnitReaders = 16;           // warps that read a posted unit
+constexpr int kUnitReaders = 17;           // warps that read a posted unit
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
 
@@ -79,17 +81,19 @@ constexpr int kMaxStages = 6;
 struct Ctl {
     uint64_t q_full[2], q_empty[2];        // per buffer of q
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+    uint64_t v_ok[kMaxStages];             // V's tile may be multiplied
     uint64_t s_full[2];                    // per buffer: a tile's scores are in tensor memory
     uint64_t p_full[2][2];                 // per group and buffer: its weights are (and its O is rescaled)
     uint64_t p_done[2];                    // per buffer: the value products on both groups' weights have finished
     uint64_t o_done, o_free;               // a unit's last product has finished; its O has been read
-    uint64_t stats_full, stats_free;       // the groups' statistics are posted, and read
+    uint64_t stats_full, stats_free;       // the groups' statistics (and `unfinite`) are posted; the statistics are read
     uint64_t unit_full[kUnits], unit_empty[kUnits];
     Unit units[kUnits];
     Walk walk;
     long long sums[kThreads / 32];
     uint32_t tmem;
     int abort;
+    int unfinite[2];                       // per unit parity: some new value is not finite
 };
 static_assert(sizeof(Ctl) <= 1024, "control block overflows its space");
 
@@ -264,6 +268,13 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
     return d;
 }
 
+__device__ __noinline__ void flag(int32_t* status, int bit) { pa::set_status(status, bit); }
+
+__device__ __noinline__ void give_up(Ctl* ctl, int32_t* status) {
+    *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+    pa::set_status(status, PA_DEV_WAIT_TIMEOUT);
+}
+
 // A whole warp's bounded wait; gives up, too, once another role has.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* status) {
 #pragma unroll 1
@@ -271,11 +282,7 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, Ctl* ct
         if (__all_sync(0xffffffffu, pa::mbar_try_wait(bar, parity))) return true;
         if ((i & 63) == 63 && __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&ctl->abort) != 0)) return false;
     }
-    if ((threadIdx.x & 31) == 0) {
-        *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-        pa::set_status(status, PA_DEV_WAIT_TIMEOUT);
-    }
-    __syncwarp();
+    give_up(ctl, status);
     return false;
 }
 
@@ -286,8 +293,7 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Ctl* ct
         if (pa::mbar_try_wait(bar, parity)) return true;
         if ((i & 63) == 63 && *reinterpret_cast<volatile int*>(&ctl->abort)) return false;
     }
-    *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
-    pa::set_status(status, PA_DEV_WAIT_TIMEOUT);
+    give_up(ctl, status);
     return false;
 }
 
@@ -305,12 +311,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int B = 1 << a.log2_block, group = 1 << a.log2_group;
 
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < kStages; ++i) {
             pa::mbar_init(&ctl->k_full[i], 1);
             pa::mbar_init(&ctl->k_empty[i], 1);
             pa::mbar_init(&ctl->v_full[i], 1);
             pa::mbar_init(&ctl->v_empty[i], 2);
+            pa::mbar_init(&ctl->v_ok[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             pa::mbar_init(&ctl->q_full[i], F8 ? 128 : 1);
             pa::mbar_init(&ctl->q_empty[i], 1);
@@ -321,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         pa::mbar_init(&ctl->o_done, 2);
         pa::mbar_init(&ctl->o_free, 128);
-        pa::mbar_init(&ctl->stats_full, 256);
+        pa::mbar_init(&ctl->stats_full, 256 + 1);
         pa::mbar_init(&ctl->stats_free, 128);
+#pragma unroll 1
         for (int i = 0; i < kUnits; ++i) {
             pa::mbar_init(&ctl->unit_full[i], 1);
             pa::mbar_init(&ctl->unit_empty[i], kUnitReaders);
@@ -349,17 +359,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (!busy) {
     } else if (warp == kKWarp || warp == kVWarp) {
         // ------------------------------------------------------------ producers
-        // Lane i copies block i of each tile (its table entry fetched four
-        // tiles ahead); blocks past the context, and bad ids, are read from
+        // Lanes i * blocks on copy the blocks of tile i of the `per` tiles
+        // that one load of table entries serves, the next load's in flight
+        // meanwhile; blocks past the context, and bad ids, are read from
         // outside the tensor, which fills zeros.
         const bool is_k = warp == kKWarp;
-        const int blocks = kKv >> a.log2_block;
+        const int log2_blocks = 7 - a.log2_block, blocks = 1 << log2_blocks, per = 32 >> log2_blocks;
+        static_assert(kKv == 128, "log2_blocks");
         uint64_t* full = is_k ? ctl->k_full : ctl->v_full;
         uint64_t* empty = is_k ? ctl->k_empty : ctl->v_empty;
         const CUtensorMap* map = is_k ? &map_k : &map_v;
         const uint64_t policy = pa::l2_evict_first_policy();
         int done = 0, nth = 0;                                   // tiles and units so far
         bool ok = true;
+#pragma unroll 1
         for (; ok; ++nth) {
             const int slot = nth % kUnits;
             Unit* u = &ctl->units[slot];
@@ -381,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         // 16 rows a box: 16 / group tokens of the group's heads
                         pa::mbar_arrive_expect_tx(ctl->q_full, kRows * 128 * G::kHalves);
+#pragma unroll 1
                         for (int r = 0; r < kRows; r += 16) {
 #pragma unroll
                             for (int h = 0; h < G::kHalves; ++h)
@@ -396,46 +410,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
             }
-            constexpr int kFetch = 4;
+            const int sub = lane >> log2_blocks, place = (lane & (blocks - 1)) * B;
             constexpr int kNoBlock = -2147483647 - 1;
-            auto fetch = [&](int j) {
-                const int pos = (st0 + j) * kKv + lane * B;
-                return (j < len && lane < blocks && pos < ctx) ? table[pos >> a.log2_block] : kNoBlock;
+            auto fetch = [&](int j) {                            // tiles j .. j + per - 1
+                const int pos = (st0 + j + sub) * kKv + place;
+                return (j + sub < len && pos < ctx) ? table[pos >> a.log2_block] : kNoBlock;
             };
-            auto row_of = [&](int blk) {
-                if (blk == kNoBlock) return oob_row;
-                if (blk < 0 || blk >= a.num_blocks) {
-                    pa::set_status(a.status, PA_DEV_BAD_BLOCK_ID);
-                    return oob_row;
+            int row = 0, ahead = fetch(0);
+#pragma unroll 1
+            for (int j = 0; j < len; ++j, ++done) {
+                const int turn = j & (per - 1), st = done % kStages;
+                if (turn == 0) {
+                    row = oob_row;
+                    if (ahead >= 0 && ahead < a.num_blocks) row = (ahead * a.n_kv_heads + kvh) * B;
+                    else if (ahead != kNoBlock) flag(a.status, PA_DEV_BAD_BLOCK_ID);
+                    ahead = fetch(j + per);
                 }
-                return (blk * a.n_kv_heads + kvh) * B;
-            };
-            int ids[kFetch];
+                if (done >= kStages && !(ok = wait_for(&empty[st], (done / kStages - 1) & 1, ctl, a.status))) break;
+                if (lane == 0) pa::mbar_arrive_expect_tx(&full[st], G::kTileBytes);
+                __syncwarp();
+                if (turn == sub) {
+                    const uint32_t dst = s0 + (is_k ? G::kK0 : G::kV0) + st * G::kTileBytes + place * 128;
 #pragma unroll
-            for (int x = 0; x < kFetch; ++x) ids[x] = fetch(x);
-            for (int j0 = 0; ok && j0 < len; j0 += kFetch) {
-#pragma unroll
-                for (int x = 0; x < kFetch; ++x) {
-                    const int j = j0 + x;
-                    if (j >= len) break;
-                    const int row = row_of(ids[x]), st = done % kStages;
-                    ids[x] = fetch(j + kFetch);
-                    if (done >= kStages && !(ok = wait_for(&empty[st], (done / kStages - 1) & 1, ctl, a.status))) break;
-                    if (lane == 0) pa::mbar_arrive_expect_tx(&full[st], G::kTileBytes);
-                    __syncwarp();
-                    if (lane < blocks) {
-                        const uint32_t dst = s0 + (is_k ? G::kK0 : G::kV0) + st * G::kTileBytes + lane * B * 128;
-#pragma unroll
-                        for (int h = 0; h < G::kHalves; ++h)
-                            pa::tma_box(dst + h * G::kHalfBytes, map, h * 64, row, &full[st], policy);
-                    }
-                    ++done;
+                    for (int h = 0; h < G::kHalves; ++h)
+                        pa::tma_box(dst + h * G::kHalfBytes, map, h * 64, row, &full[st], policy);
                 }
             }
         }
         // the copies this warp started land before the block exits
         if (lane == 0) {
             if (!F8 && !is_k && nth > 0) pa::mbar_wait_bounded(ctl->q_full, (nth - 1) & 1, kMaxProbes);
+#pragma unroll 1
             for (int i = 0; i < kStages && i < done; ++i)
                 pa::mbar_wait_bounded(&full[(done - 1 - i) % kStages], ((done - 1 - i) / kStages) & 1, kMaxProbes);
         }
@@ -446,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int at = 0, st = 0, phase = 0;                       // tiles so far; K's stage and phase
             bool ok = true;
+#pragma unroll 1
             for (int nth = 0; ok; ++nth) {
                 const int slot = nth % kUnits;
                 if (!wait_one(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
@@ -455,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int qb = nth % G::kQBuffers;
                 if (!wait_one(&ctl->q_full[qb], (nth / G::kQBuffers) & 1, ctl, a.status)) break;
                 const uint32_t q_lo = desc_lo(s0 + qb * G::kQBytes, 16);
+#pragma unroll 1
                 for (int j = 0; j < len; ++j, ++at) {
                     const int b = at & 1;
                     // the scores go over weights of two tiles ago: their value products have to be done
@@ -489,70 +496,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int w = value_group(warp);
         const uint32_t t_o = tmem + kTmemO + w * 128;
         const uint32_t v_lo0 = desc_lo(s0 + G::kV0 + w * kHalfKv * 128, G::kHalfBytes);
-        int at = 0, st = 0, phase = 0;                           // tiles so far; V's stage and phase
+        if (lane == 0) {
+            int at = 0, st = 0, phase = 0;                       // tiles so far; V's stage and phase
+            bool ok = true;
+#pragma unroll 1
+            for (int nth = 0; ok; ++nth) {
+                const int slot = nth % kUnits;
+                if (!wait_one(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
+                const Unit* u = &ctl->units[slot];
+                const int valid = u->valid, len = u->len, ctx = u->ctx, st0 = u->st0;
+                pa::mbar_arrive(&ctl->unit_empty[slot]);
+                if (!valid) break;
+                // the unit before has read its O out
+                if (nth >= 1 && !wait_one(&ctl->o_free, (nth - 1) & 1, ctl, a.status)) break;
+#pragma unroll 1
+                for (int j = 0; j < len; ++j, ++at) {
+                    const int b = at & 1;
+                    // the group's positions of the tile within the context, in products
+                    const int left = min(kHalfKv, ctx - (st0 + j) * kKv - w * kHalfKv);
+                    const int steps = left > 0 ? (left + kStepKeys - 1) / kStepKeys : 0;
+                    if (!(ok = wait_one(&ctl->v_ok[st], phase, ctl, a.status) &&
+                               wait_one(&ctl->p_full[w][b], (at >> 1) & 1, ctl, a.status)))
+                        break;
+                    fence_after();
+                    const uint32_t t_p = tmem + b * 128 + w * kHalfKv, v_lo = v_lo0 + st * (G::kTileBytes >> 4);
+                    // weights of product kk: 8 columns each, a second set of them behind the first
+#pragma unroll
+                    for (int kk = 0; kk < kSteps; ++kk) {
+                        if (kk >= steps) break;
+#pragma unroll
+                        for (int x = 0; x < kSets; ++x) {
+                            const uint32_t t = t_p + 8 * (x * kSteps + kk), v = v_lo + kk * ((kStepKeys * 128) >> 4);
+                            if (kk == 0 && x == 0)
+                                mma_ts<F8>(t_o, t, v, id, j > 0 ? 1u : 0u);
+                            else
+                                mma_ts_add<F8>(t_o, t, v, id);
+                        }
+                    }
+                    commit(&ctl->p_done[b]);
+                    commit(&ctl->v_empty[st]);
+                    if (j == len - 1) commit(&ctl->o_done);
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (at > 0) pa::mbar_wait_bounded(&ctl->v_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
+        }
+        __syncwarp();
+    } else if (warp == kCheckWarp) {
+        // ------------------------------------------------------------ V's tiles at a context's end
+        // Zeros in place of values that are not finite at new positions, and in the rows from the context's end to
+        // the end of the last product there; beside the softmax, so that the products need not wait.
+        int st = 0, phase = 0;
         bool ok = true;
+#pragma unroll 1
         for (int nth = 0; ok; ++nth) {
             const int slot = nth % kUnits;
             if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
             const Unit* u = &ctl->units[slot];
-            const int valid = u->valid, len = u->len, ctx = u->ctx, st0 = u->st0;
+            const int valid = u->valid, len = u->len, ctx = u->ctx, st0 = u->st0, first = u->first;
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
             if (!valid) break;
-            // the unit before has read its O out
-            if (nth >= 1 && !wait_for(&ctl->o_free, (nth - 1) & 1, ctl, a.status)) break;
-            for (int j = 0; j < len; ++j, ++at) {
-                const int b = at & 1;
-                // the group's positions of the tile within the context, in products
-                const int left = min(kHalfKv, ctx - (st0 + j) * kKv - w * kHalfKv);
-                const int steps = left > 0 ? (left + kStepKeys - 1) / kStepKeys : 0;
-                ok = lane || (wait_one(&ctl->v_full[st], phase, ctl, a.status) &&
-                              wait_one(&ctl->p_full[w][b], (at >> 1) & 1, ctl, a.status));
-                if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0))) break;
-                if (left > 0 && left % kStepKeys) {
-                    // rows from `left` to the end of the last product are past the context: zeros (lane 0's
-                    // wait, and the shuffle, order the copies before these writes)
-                    for (int x = lane; x < (kStepKeys * steps - left) * G::kHalves * 8; x += 32) {
-                        const int r = w * kHalfKv + left + x / (G::kHalves * 8), c = x % (G::kHalves * 8);
-                        *reinterpret_cast<uint4*>(sm + G::kV0 + st * G::kTileBytes + (c >> 3) * G::kHalfBytes + r * 128 +
-                                                  (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            bool unfinite = false;
+#pragma unroll 1
+            for (int j = 0; j < len; ++j) {
+                if (!(ok = wait_for(&ctl->v_full[st], phase, ctl, a.status))) break;
+                const int t0 = (st0 + j) * kKv, left = ctx - t0;
+                uint8_t* tile = sm + G::kV0 + st * G::kTileBytes;
+                if (t0 + kKv > first) {
+                    unfinite |= drop_unfinite<F8, G::kHalves>(tile, G::kHalfBytes, max(0, first - t0), min(kKv, left), lane, 32);
+                    if (left < kKv && left % G::kStepKeys) {
+#pragma unroll 1
+                        for (int x = lane; x < (G::kStepKeys - left % G::kStepKeys) * G::kHalves * 8; x += 32) {
+                            const int r = left + x / (G::kHalves * 8), c = x % (G::kHalves * 8);
+                            *reinterpret_cast<uint4*>(tile + (c >> 3) * G::kHalfBytes + r * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) {
-                    fence_after();
-                    const uint32_t t_p = tmem + b * 128 + w * kHalfKv, v_lo = v_lo0 + st * (G::kTileBytes >> 4);
-                    // weights of product kk: 8 columns each, a second set of them behind the first
-                    auto products = [&](bool all) {
-#pragma unroll
-                        for (int x = 0; x < kSets; ++x)
-#pragma unroll
-                            for (int kk = 0; kk < kSteps; ++kk) {
-                                if (!(all || kk < steps)) continue;
-                                const uint32_t t = t_p + 8 * (x * kSteps + kk), v = v_lo + kk * ((kStepKeys * 128) >> 4);
-                                if (kk == 0 && x == 0)
-                                    mma_ts<F8>(t_o, t, v, id, j > 0 ? 1u : 0u);
-                                else
-                                    mma_ts_add<F8>(t_o, t, v, id);
-                            }
-                    };
-                    if (steps == kSteps)
-                        products(true);
-                    else
-                        products(false);
-                    commit(&ctl->p_done[b]);
-                    commit(&ctl->v_empty[st]);
-                    if (j == len - 1) commit(&ctl->o_done);
-                }
-                if (++st == kStages) {
+                if (lane == 0) pa::mbar_arrive(&ctl->v_ok[st]);
+                if (++st == G::kStages) {
                     st = 0;
                     phase ^= 1;
                 }
             }
+            if (!ok) break;
+            if (nth >= 1 && !wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status)) break;
+            unfinite = __any_sync(0xffffffffu, unfinite);
+            if (lane == 0) {
+                ctl->unfinite[nth & 1] = unfinite;
+                pa::mbar_arrive(&ctl->stats_full);
+            }
         }
-        if (lane == 0 && at > 0)
-            pa::mbar_wait_bounded(&ctl->v_empty[(at - 1) % kStages], ((at - 1) / kStages) & 1, kMaxProbes);
     } else if (warp < kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax of group w's half of every tile
         const int w = warp >> 2, quarter = warp & 3;
@@ -568,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kLanes16 = 16u << 16;
         int at = 0;                                              // tiles so far
         bool ok = true;
+#pragma unroll 1
         for (int nth = 0; ok; ++nth) {
             const int slot = nth % kUnits;
             if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
@@ -599,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_for(&ctl->q_full[nth & 1], (nth >> 1) & 1, ctl, a.status)) break;   // the rows' factors come with q
                 c = factors[(nth & 1) * 64 + r];
             }
+#pragma unroll 1
             for (int j = 0; j < len; ++j, ++at) {
                 const int b = at & 1;
                 if (!(ok = wait_for(&ctl->s_full[b], (at >> 1) & 1, ctl, a.status))) break;
@@ -742,94 +784,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         // E4M3 caches: these warps make q's two terms too.  A bf16 value is the sum of two E4M3 values
         // (8 significant bits, 4 and 4), after a power of two per row that brings its largest into
         // [2^7, 2^8); below 2^-16 of that, within 2^-18 of it.
-        auto make_q = [&](const Unit* u, int parity) {
+        // Returns false to give up.
+        float* factors = reinterpret_cast<float*>(stats + 128);
+        auto make_q = [&](int nth) {
+            const int slot = nth % kUnits, qb = nth & 1;
+            if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) return false;
+            const Unit* u = &ctl->units[slot];
+            if (!u->valid) return true;
             const int t = threadIdx.x - 32 * kOutWarp, row = t >> 1, part = t & 1, at = u->row0 + row, i = at >> a.log2_group;
-            uint4 v[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                v[x] = make_uint4(0, 0, 0, 0);
-                if (i < u->n)
-                    v[x] = *reinterpret_cast<const uint4*>(
-                        a.q + ((size_t)(u->q0 + i) * a.n_q_heads + (u->kvh << a.log2_group) + (at & (group - 1))) * D + 64 * part + 8 * x);
-            }
-            return [=](uint8_t* smem, float* fac) {
-                float top = 0.f;
+            // read twice, for the maximum and then (from L1) for the terms: fewer instructions than keeping it
+            const bool there = i < u->n;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.q + ((size_t)(u->q0 + i) * a.n_q_heads + (u->kvh << a.log2_group) + (at & (group - 1))) * D + 64 * part);
+            float top = 0.f;
+            if (there) {
+                uint32_t most = 0;                               // the largest magnitude of each half
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const uint32_t wd[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = pa::bf16x2_to_float2(wd[e]);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
+                    const uint4 v = src[x];
+                    most = __vmaxu2(__vmaxu2(most, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                                    __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                int eb = (__float_as_int(top) >> 23) & 0xff;
-                eb = eb < 7 ? 7 : (eb > 254 ? 254 : eb);
-                const float up = __int_as_float((261 - eb) << 23), by = up * a.q_sign;
-                if (part == 0) fac[parity * 64 + row] = fmaxf(a.scale_log2 / up, 1e-37f);
-                const int line = (row >> 4) * 32 + (row & 15);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {                    // 16 elements: a 16-byte chunk of each term
-                    uint32_t c0[4], c1[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4 q = v[2 * x + (e >> 1)];
-                        const uint32_t w0 = e & 1 ? q.z : q.x, w1 = e & 1 ? q.w : q.y;
-                        uint32_t a0[2], a1[2];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float2 f = pa::bf16x2_to_float2(y ? w1 : w0);
-                            const float f0 = f.x * by, f1 = f.y * by;
-                            a0[y] = pa::e4m3x2(f0, f1);
-                            const uint32_t h = e4m3x2_to_f16x2(a0[y]);
-                            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                            a1[y] = pa::e4m3x2(f0 - g.x, f1 - g.y);
-                        }
-                        c0[e] = a0[0] | (a0[1] << 16);
-                        c1[e] = a1[0] | (a1[1] << 16);
-                    }
-                    uint8_t* dst = smem + line * 128 + (((4 * part + x) ^ (line & 7)) << 4);
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
-                    *reinterpret_cast<uint4*>(dst + 16 * 128) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            };
-        };
-        float* factors = reinterpret_cast<float*>(stats + 128);
-        if constexpr (F8) {
-            if (wait_for(&ctl->unit_full[0], 0, ctl, a.status) && ctl->units[0].valid) {
-                make_q(&ctl->units[0], 0)(sm, factors);
-                pa::mbar_arrive(&ctl->q_full[0]);
+                const float2 f = pa::bf16x2_to_float2(most);
+                top = fmaxf(f.x, f.y);
             }
-        }
+            // the buffer's last unit was two before
+            if (nth >= 2 && !wait_for(&ctl->q_empty[qb], ((nth >> 1) - 1) & 1, ctl, a.status)) return false;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            int eb = (__float_as_int(top) >> 23) & 0xff;
+            eb = eb < 7 ? 7 : (eb > 254 ? 254 : eb);
+            const float up = __int_as_float((261 - eb) << 23);
+            const float by = top < INFINITY ? up * a.q_sign : __int_as_float(0x7fffffff);   // (E4M3 has no infinity)
+            if (part == 0) factors[qb * 64 + row] = fmaxf(a.scale_log2 / up, 1e-37f);
+            const int line = (row >> 4) * 32 + (row & 15);
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {                        // 16 elements: a 16-byte chunk of each term
+                const uint4 none = make_uint4(0, 0, 0, 0), v0 = there ? src[2 * x] : none, v1 = there ? src[2 * x + 1] : none;
+                uint32_t c0[4], c1[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 q = e < 2 ? v0 : v1;
+                    const uint32_t w0 = e & 1 ? q.z : q.x, w1 = e & 1 ? q.w : q.y;
+                    uint32_t a0[2], a1[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 f = pa::bf16x2_to_float2(y ? w1 : w0);
+                        const float f0 = f.x * by, f1 = f.y * by;
+                        a0[y] = pa::e4m3x2(f0, f1);
+                        const uint32_t h = e4m3x2_to_f16x2(a0[y]);
+                        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                        a1[y] = pa::e4m3x2(f0 - g.x, f1 - g.y);
+                    }
+                    c0[e] = a0[0] | (a0[1] << 16);
+                    c1[e] = a1[0] | (a1[1] << 16);
+                }
+                uint8_t* dst = sm + qb * G::kQBytes + line * 128 + (((4 * part + x) ^ (line & 7)) << 4);
+                *reinterpret_cast<uint4*>(dst) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
+                *reinterpret_cast<uint4*>(dst + 16 * 128) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            pa::mbar_arrive(&ctl->q_full[qb]);
+            return true;
+        };
         const uint32_t t_o = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemO;
-        for (int nth = 0;; ++nth) {
+#pragma unroll 1
+        for (int nth = F8 ? -1 : 0;; ++nth) {
             const int slot = nth % kUnits;
-            if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
             const Unit* u = &ctl->units[slot];
-            if (!u->valid) break;
+            if (nth >= 0 && !(wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status) && u->valid)) break;
+            if constexpr (F8) {                                  // the next unit's q, ahead of this unit's end
+                if (!make_q(nth + 1)) break;
+                if (nth < 0) continue;
+            }
             const int st0 = u->st0;
+            const int seq = u->seq, kvh = u->kvh, end = st0 + u->len;
             const int row = u->row0 + r, i = row >> a.log2_group;
             const bool real = i < u->n, whole = u->len == u->steps;
             const bool both = u->len > 1 || u->ctx - st0 * kKv > kHalfKv;   // group 1 had positions: O1 was written
-            const size_t out_row = ((size_t)(u->q0 + i) * a.n_q_heads + (u->kvh << a.log2_group) + (row & (group - 1))) * D;
+            const size_t out_row = ((size_t)(u->q0 + i) * a.n_q_heads + (kvh << a.log2_group) + (row & (group - 1))) * D;
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
-            if constexpr (F8) {
-                // the next unit's q, ahead of this unit's end (the buffer's last unit was the one before)
-                const int ahead = (nth + 1) % kUnits;
-                if (!wait_for(&ctl->unit_full[ahead], ((nth + 1) / kUnits) & 1, ctl, a.status)) break;
-                if (ctl->units[ahead].valid) {
-                    auto store = make_q(&ctl->units[ahead], (nth + 1) & 1);
-                    const int qb = (nth + 1) & 1;
-                    if (nth >= 1 && !wait_for(&ctl->q_empty[qb], ((nth - 1) >> 1) & 1, ctl, a.status)) break;
-                    store(sm + qb * G::kQBytes, factors);
-                    pa::mbar_arrive(&ctl->q_full[qb]);
-                }
-            }
             if (!wait_for(&ctl->stats_full, nth & 1, ctl, a.status)) break;
             const float2 e = stats[r], o = stats[kRows + r];
+            const bool unfinite = ctl->unfinite[nth & 1];
             pa::mbar_arrive(&ctl->stats_free);
             const float M = fmaxf(e.x, o.x), Z0 = pa::exp2_approx(e.x - M), Z1 = pa::exp2_approx(o.x - M);
             const float Z = Z0 * e.y + Z1 * o.y;
@@ -878,6 +915,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a.part_m[at] = M;
                 a.part_z[at] = Z;
             }
+            if (__builtin_expect(unfinite, 0))
+#pragma unroll 1
+                for (int d = 0; d < D; d += 4)                   // (to what the thread itself has written)
+                    if (!kHalf || (d & 16) == (lane & 16))
+                        add_unfinite<D, F8>(a, seq, kvh, row, st0 * kKv, end * kKv, d, whole ? nullptr : a.part_u + at * D + d);
         }
     }
     fence_before();

@@ -23,6 +23,7 @@ constexpr int kMergeSplit = 4;             // blocks per unit to merge
 struct MultiArgs {
     void* out;
     const __nv_bfloat16* q;
+    const void* v_cache;
     const int32_t* block_tables;
     const int32_t* query_start;
     const int32_t* context_lens;
@@ -128,7 +129,6 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
     }
 }
 
-
 // This block's share, found by all its threads: thread t counts sequences
 // [t * per, (t + 1) * per), and the one whose sequences hold the share's
 // start sets `walk` up there.  False: the block has nothing to do.  Ends with
@@ -140,6 +140,7 @@ __device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, long 
     const int per = (a.num_seqs + kThreads - 1) / kThreads;
     const int s_lo = threadIdx.x * per, s_hi = min(a.num_seqs, s_lo + per);
     long long mine = 0;
+#pragma unroll 1
     for (int s = s_lo; s < s_hi; ++s) mine += read_seq<kRows, kStep>(a, s, blockIdx.x == 0).work(heads, kUnitCost);
     long long upto = mine;
 #pragma unroll
@@ -150,6 +151,7 @@ __device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, long 
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     long long total = 0;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) upto += sums[w];
         total += sums[w];
@@ -176,6 +178,86 @@ __device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, long 
     }
     __syncthreads();
     return true;
+}
+
+// Whether new token i of a sequence sees its new token j.
+__device__ __forceinline__ bool sees(const uint64_t* words, int i, int j) {
+    return words ? (j < 64 && (words[i] >> j & 1ull)) : j <= i;
+}
+
+// A value that is not finite reaches the rows that see it only.  In a product
+// it would reach all (0 * inf = NaN), so at the new positions, which are all
+// that a row may not see, the products run with zeros in its place, and the
+// rows of such a unit add what they see of it when they are written.
+
+// The elements of w (two bf16, or four E4M3 codes) that are not finite, as a mask.
+template <bool F8>
+__device__ __forceinline__ uint32_t unfinite_mask(uint32_t w) {
+    return F8 ? ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu
+              : ((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
+}
+
+// Zeros in their place in rows from .. to - 1 of a tile (slabs of 128-byte
+// rows, their chunks in any order), by `threads` threads of which this is
+// `thread`; whether it found any.
+template <bool F8, int kSlabs>
+__device__ __forceinline__ bool drop_unfinite(uint8_t* tile, int slab_bytes, int from, int to, int thread, int threads) {
+    uint32_t any = 0;
+#pragma unroll 1
+    for (int x = from * 8 * kSlabs + thread; x < to * 8 * kSlabs; x += threads) {
+        const int row = x / (8 * kSlabs), c = x % (8 * kSlabs);
+        uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * slab_bytes + row * 128 + (c & 7) * 16);
+        uint4 v = *p;
+        const uint32_t m[4] = {unfinite_mask<F8>(v.x), unfinite_mask<F8>(v.y), unfinite_mask<F8>(v.z), unfinite_mask<F8>(v.w)};
+        const uint32_t bad = m[0] | m[1] | m[2] | m[3];
+        if (bad) {
+            *p = make_uint4(v.x & ~m[0], v.y & ~m[1], v.z & ~m[2], v.w & ~m[3]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // for tensor cores, and copies to come
+        }
+        any |= bad;
+    }
+    return any != 0;
+}
+
+// Add the values that are not finite, at d .. d + 3 of the positions of
+// [lo, hi) that a row of sequence s sees, to the row's result: its sums at
+// `part`, or `out` where that is null.
+template <int D, bool F8>
+__device__ __noinline__ void add_unfinite(const MultiArgs& a, int s, int kvh, int row, int lo, int hi, int d, float* part) {
+    const Seq q = read_seq<1, 1>(a, s, false);
+    const int i = row >> a.log2_group, B = 1 << a.log2_block, first = q.ctx - q.n;
+    if (i >= q.n) return;
+    const uint64_t* words = a.tree_mask ? a.tree_mask + q.q0 : nullptr;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int pos = max(lo, first); pos < min(hi, q.ctx); ++pos) {
+        const int blk = a.block_tables[(size_t)s * a.max_blocks + (pos >> a.log2_block)];
+        if (!sees(words, i, pos - first) || blk < 0 || blk >= a.num_blocks) continue;
+        const size_t at = ((size_t)(blk * a.n_kv_heads + kvh) * B + (pos & (B - 1))) * D + d;
+        if constexpr (F8) {                                       // E4M3 has NaN only
+            const uint32_t m = unfinite_mask<true>(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v_cache) + at));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m >> (8 * e) & 1u) sum[e] = __int_as_float(0x7fffffff);
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.v_cache) + at);
+            const float2 x = pa::bf16x2_to_float2(w.x & unfinite_mask<false>(w.x));
+            const float2 y = pa::bf16x2_to_float2(w.y & unfinite_mask<false>(w.y));
+            sum[0] += x.x;
+            sum[1] += x.y;
+            sum[2] += y.x;
+            sum[3] += y.y;
+        }
+    }
+    const size_t at = ((size_t)(q.q0 + i) * a.n_q_heads + (kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))) * D + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (sum[e] == 0.f) continue;
+        float* f = part ? part + e : static_cast<float*>(a.out) + at + e;
+        __nv_bfloat16* b = static_cast<__nv_bfloat16*>(a.out) + at + e;
+        if (part || a.out_f32) *f += sum[e];
+        else *b = __float2bfloat16(__bfloat162float(*b) + sum[e]);
+    }
 }
 
 // out of the units that several blocks share: the pieces of block b, which
@@ -213,7 +295,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
              make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
     }
 }
-
 
 // Launches of the 64- and 128-row units on the 5th-generation tensor cores
 // (pa_decode_wide.cu); cudaSuccess or the launch's error.

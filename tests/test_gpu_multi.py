@@ -284,3 +284,221 @@ def test_random_configurations(i):
         mask = [0] * gap + _trees(news, rng) + [0] * gap
     dt = torch.float32 if rng.random() < 0.5 else torch.bfloat16
     _check(p, _run(p, G * Hkv, Hkv, D, B, most, dt, mask, fp8), G * Hkv, Hkv, D, B, mask, fp8)
+
+
+# More than 16 rows a KV head: units of 64 rows, or 128 for bf16 caches.
+WIDE = [
+    (32, 8, 128, 16, [64, 65, 128, 129, 700, 16], [5, 16, 16, 9, 12, 16]),   # 64 rows; contexts of half a tile
+    (16, 2, 64, 8, [64, 63, 200, 8, 193], [8, 5, 6, 8, 1]),                  # 64 rows, 8-position blocks
+    (16, 1, 128, 32, [30, 128, 257, 520, 8], [5, 8, 7, 8, 8]),               # 128 rows
+    (16, 2, 64, 16, [40, 300, 64], [12, 16, 16]),                            # 128 rows, d_head 64
+    (8, 1, 128, 16, [9000, 33], [8, 3]),                                     # one head over many blocks
+    (4, 1, 128, 8, [300, 260], [64, 40]),                                    # tree words over tile boundaries
+    (1, 1, 128, 16, [100, 90, 64], [40, 17, 64]),                            # G = 1
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B,ctxs,news", WIDE)
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_units_of_many_rows_equal_the_oracle(Hq, Hkv, D, B, ctxs, news, kind, fp8):
+    if fp8 and D != 128:
+        pytest.skip("E4M3 caches have d_head 128")
+    p = _problem(Hq + D + B, Hq, Hkv, D, B, ctxs, news, fp8=fp8, gap=3)
+    mask = [0] * 3 + _trees(news, np.random.default_rng(4)) + [0] * 3 if kind == "tree" else None
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = _run(p, Hq, Hkv, D, B, max(news), torch.bfloat16, mask, fp8, status=st)
+    assert st.item() == 0
+    _check(p, out, Hq, Hkv, D, B, mask, fp8)
+
+
+@pytest.mark.parametrize("n", [4, 16, 32])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_growing_scores_and_scales_of_either_sign(n, fp8):
+    """Maxima that rise by far more than a raise's threshold, again and again,
+    and fall; scales of zero and below."""
+    Hq, Hkv, D, B, C = 4, 1, 128, 16, 900
+    q, kc, vc, tables, start, ctx = _problem(13, Hq, Hkv, D, B, [C], [n], fp8=fp8)
+    k = np.nan_to_num(Q.dequantize(kc, 0.02) if fp8 else A.bf16_to_f64(kc), nan=0.0)
+    for j in range(C):
+        k[tables[0, j // B], :, j % B] *= 4.0 * (1 + math.sin(j / 70.0)) * (1 if j < 600 else 0.01)
+    kc = Q.quantize(np.clip(k, -8.5, 8.5), K_SCALE) if fp8 else to_bits(torch.from_numpy(k).to(torch.bfloat16))
+    p = (q, kc, vc, tables, start, ctx)
+    for scale in (1 / math.sqrt(D), 0.0, -0.05):
+        _check(p, _run(p, Hq, Hkv, D, B, n, scale=scale, fp8=fp8), Hq, Hkv, D, B, scale=scale, fp8=fp8)
+
+
+# (new tokens, G, fp8): units of 16, 64 and 128 rows
+UNITS = [(4, 4, False), (4, 4, True), (9, 4, False), (9, 4, True), (20, 4, False)]
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+@pytest.mark.parametrize("C", [40, 70, 3000])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them_alone(n, G, fp8, kind, C):
+    Hkv, D, B = 2, 128, 16
+    p = _problem(14, G * Hkv, Hkv, D, B, [C, 50], [n, 3], fp8=fp8)
+    q, kc, vc, tables, start, ctx = p
+    words = _trees([n, 3], np.random.default_rng(5)) if kind == "tree" else None
+    bad = [0x7F, 0xFF, 0x7F] if fp8 else [0x7F80, 0xFF80, 0x7FC0]
+    clean = vc.copy()
+    for i, (j, d) in enumerate(((1, 5), (n // 2, 64), (n // 2, 5), (n - 1, 127), (n - 1, 5))):
+        at = tables[0, (C - n + j) // B], i % Hkv, (C - n + j) % B, d
+        vc[at], clean[at] = bad[i % 3], 0
+    at = tables[0, (C - n + 2) // B], 0, (C - n + 2) % B, 7       # and a key that is not
+    kc[at] = bad[2]
+    f64 = (lambda c: Q.dequantize(c, V_SCALE)) if fp8 else A.bf16_to_f64
+    scale = 1 / math.sqrt(D)
+    args = (tables, start, ctx, scale, B, words)
+    k64 = Q.dequantize(kc, K_SCALE) if fp8 else A.bf16_to_f64(kc)
+    with np.errstate(invalid="ignore"):
+        want = A.paged_multi(A.bf16_to_f64(to_bits(q)), k64, f64(vc), *args)
+        out = _run(p, G * Hkv, Hkv, D, B, n, mask=words, fp8=fp8)
+        got = out_to_f64(out)
+        odd = ~np.isfinite(want)
+        assert odd.any() and not odd.all()
+        assert (np.isnan(got[odd]) == np.isnan(want[odd])).all()
+        inf = odd & ~np.isnan(want)
+        assert (got[inf] == want[inf]).all()
+    # everything else is what finite values give
+    k_clean = kc.copy()
+    k_clean[at] = 0
+    rest = out.clone()
+    fine = A.paged_multi(A.bf16_to_f64(to_bits(q)), Q.dequantize(k_clean, K_SCALE) if fp8 else A.bf16_to_f64(k_clean),
+                         f64(clean), *args)
+    rest[torch.from_numpy(odd).cuda()] = torch.from_numpy(fine[odd]).float().cuda()
+    _check((q, k_clean, clean, tables, start, ctx), rest, G * Hkv, Hkv, D, B, words, fp8)
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+def test_bad_blocks_and_lengths_of_one_sequence_leave_the_others(n, G, fp8):
+    Hkv, D, B = 2, 128, 16
+    ctxs, news = [50, 300, 150, 40], [2, n, n, 3]
+    p = _problem(15, G * Hkv, Hkv, D, B, ctxs, news, fp8=fp8)
+    q, kc, vc, tables, start, ctx = p
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for entry in (-1, 10 ** 6):
+        t = tables.copy()
+        t[2, 3] = entry
+        st.zero_()
+        out = _run((q, kc, vc, t, start, ctx), G * Hkv, Hkv, D, B, n, fp8=fp8, status=st)
+        assert st.item() == api.PA_DEV_BAD_BLOCK_ID
+        out[start[2]:start[3]] = float("nan")
+        _check(p, out, G * Hkv, Hkv, D, B, fp8=fp8, skip={2})
+    for bad in (np.array([50, n - 1, 150, 40]), np.array([50, -7, 150, 40])):
+        st.zero_()
+        out = _run((q, kc, vc, tables, start, bad.astype(np.int32)), G * Hkv, Hkv, D, B, n, fp8=fp8, status=st)
+        assert st.item() == api.PA_DEV_BAD_CONTEXT
+        assert torch.isnan(out[start[1]:start[2]]).all()          # not computed, left as it was
+        _check(p, out, G * Hkv, Hkv, D, B, fp8=fp8, skip={1})
+    # a context above max_context_len is cut there
+    st.zero_()
+    out = _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8, status=st, max_ctx=150)
+    assert st.item() == api.PA_DEV_BAD_CONTEXT
+    _check((q, kc, vc, tables, start, np.minimum(ctx, 150).astype(np.int32)), out, G * Hkv, Hkv, D, B, fp8=fp8)
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+def test_no_new_tokens_and_empty_batches(n, G, fp8):
+    Hkv, D, B = 2, 128, 16
+    p = _problem(16, G * Hkv, Hkv, D, B, [40, 70], [0, 0], fp8=fp8, gap=2)
+    assert torch.isnan(_run(p, G * Hkv, Hkv, D, B, n, fp8=fp8)).all()
+    q, kc, vc, tables, start, ctx = p
+    zero = (q, kc, vc, tables, np.zeros(3, dtype=np.int32), np.zeros(2, dtype=np.int32))
+    assert torch.isnan(_run(zero, G * Hkv, Hkv, D, B, n, fp8=fp8, max_ctx=0)).all()
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+def test_captured_calls_that_share_a_workspace_and_calls_on_two_streams(n, G, fp8):
+    Hkv, D, B = 2, 128, 16
+    Hq = G * Hkv
+    probs = [_problem(17 + x, Hq, Hkv, D, B, ctxs, news, fp8=fp8)
+             for x, (ctxs, news) in enumerate((([1500, 40, 700], [n, 3, n]), ([90, 2500], [n, 2])))]
+    want = [_run(p, Hq, Hkv, D, B, n, fp8=fp8) for p in probs]
+    put = (lambda c: torch.from_numpy(c).cuda()) if fp8 else from_bits
+
+    def call(p, ws):
+        q, kc, vc, tables, start, ctx = p
+        a = [q.cuda(), put(kc), put(vc)] + [torch.from_numpy(x).cuda() for x in (tables, start, ctx)]
+        out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+        return out, lambda: api.pa_decode_multi(out, *a, n, B, 1 / math.sqrt(D), Hq, Hkv, D, int(ctx.max()), workspace=ws,
+                                                k_scale=K_SCALE if fp8 else None, v_scale=V_SCALE if fp8 else None)
+
+    shared = api.decode_multi_workspace(n, Hq, Hkv, D)
+    calls = [call(p, shared) for p in probs]
+    graphs = []
+    for _, run in calls:
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    for _ in range(3):
+        for out, _ in calls:
+            out.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for (out, _), w in zip(calls, want):
+            assert torch.equal(out.view(torch.int32), w.view(torch.int32))
+    # at once, each with a workspace of its own
+    calls = [call(p, api.decode_multi_workspace(n, Hq, Hkv, D)) for p in probs]
+    streams = [torch.cuda.Stream() for _ in probs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (_, run), s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                run()
+    torch.cuda.synchronize()
+    for (out, _), w in zip(calls, want):
+        assert torch.equal(out.view(torch.int32), w.view(torch.int32))
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+def test_long_contexts_in_the_last_blocks_of_a_large_cache(n, G, fp8):
+    """Byte offsets past 32 bits and contexts of many steps, against the
+    formula in float64."""
+    Hkv, D, B = 8, 128, 16
+    Hq, NB = G * Hkv, (1 << 18) + 7 if not fp8 else (1 << 19) + 7       # 2^32 bytes of cache is 2^17 (2^18) blocks
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    ctxs, news = [20011, 7], [n, min(n, 7)]
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    kc, vc = (torch.empty(NB, Hkv, B, D, dtype=dt, device="cuda") for _ in range(2))
+    used = sum(-(-c // B) for c in ctxs)
+    tables = torch.full((2, -(-ctxs[0] // B)), -1, dtype=torch.int32)
+    ids = torch.randperm(used, generator=torch.Generator().manual_seed(1)).to(torch.int32) + NB - used
+    tables[0] = ids[:-1]
+    tables[1, 0] = ids[-1]
+    for c in (kc, vc):
+        x = torch.randn(used, Hkv, B, D, generator=gen, device="cuda")
+        c[NB - used:] = (x * 40).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x.to(dt)
+    T = sum(news)
+    q = torch.randn(T, Hq, D, generator=gen, device="cuda").to(torch.bfloat16)
+    start = torch.tensor([0, news[0], T], dtype=torch.int32, device="cuda")
+    out = torch.empty(T, Hq, D, dtype=torch.float32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.pa_decode_multi(out, q, kc, vc, tables.cuda(), start, torch.tensor(ctxs, dtype=torch.int32, device="cuda"), n, B,
+                        1 / math.sqrt(D), Hq, Hkv, D, ctxs[0], workspace=api.decode_multi_workspace(n, Hq, Hkv, D),
+                        status=st, k_scale=K_SCALE if fp8 else None, v_scale=V_SCALE if fp8 else None)
+    assert st.item() == 0
+    E, W = (2.0 ** -11, 2.0 ** -11) if fp8 else (0.0, 2.0 ** -16)
+    for s, C in enumerate(ctxs):
+        def rows(c, scale):
+            x = c[tables[s, :-(-C // B)].long().cuda()]
+            x = x.view(torch.float8_e4m3fn).double() * scale if fp8 else x.double()
+            return x.permute(1, 0, 2, 3).reshape(Hkv, -1, D)[:, :C]
+        K, V = rows(kc, K_SCALE), rows(vc, V_SCALE)
+        lo, m = int(start[s]), news[s]
+        x = q[lo:lo + m].double().view(m, Hkv, G, D)
+        z = torch.einsum("nhgd,hcd->hgnc", x, K) / math.sqrt(D)
+        size = torch.einsum("nhgd,hcd->hgnc", x.abs(), K.abs()).amax(-1) / math.sqrt(D)   # [h, g, n]
+        see = torch.ones(m, C, dtype=torch.bool, device="cuda").tril(C - m)
+        a = torch.softmax(z.masked_fill(~see, -math.inf), -1)
+        want = torch.einsum("hgnc,hcd->nhgd", a, V)
+        weight = torch.einsum("hgnc,hcd->nhgd", a, V.abs())
+        tol = (2 * (E + 128 * 2.0 ** -24) * size + W + 2.0 ** -18).permute(2, 0, 1)[..., None] * weight * 2
+        got = out[lo:lo + m].double().view(m, Hkv, G, D)
+        assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max().item()
