@@ -51,6 +51,11 @@ constexpr int kBlocksPerSm = 3;
 constexpr float kWeightScale = 128.f;      // FP8: weights enter f16 products times 2^7 (at most 2^15)
 constexpr int kUnitCost = 5;               // steps that starting and joining a unit is worth
 constexpr int kMinSteps = 4;               // steps per block, at least
+// Units of at most this many steps are not split where each has a block: 4
+// requests of 4 tokens, 8 KV heads, GPU time of whole units against shares
+// and their merge: 256 positions 9.3 / 11.0 us, 768 16.8 / 16.8, 1024 20.6 /
+// 16.9 (64-row units: 1024 13.7 / 15.4, 1536 17.5 / 16.1, so 8 steps of 128).
+constexpr int kDirectSteps = 12;
 
 template <int D, bool F8>
 struct Geo {
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     float* q_scale = reinterpret_cast<float*>(qsm + kRows * G::kQStride);   // FP8: score factor per row
     float2* stats = reinterpret_cast<float2*>(q_scale + kRows);   // [key warp][row]: maximum and sum
     uint64_t* full = reinterpret_cast<uint64_t*>(stats + kKeyWarps * kRows);   // [key warp][stage]
-    __shared__ long long sums[kKeyWarps];
+    __shared__ Part parts[kKeyWarps];
     __shared__ int unfinite[2];                                   // per unit parity: some new value is not finite
     // Thread 0 walks the share two units ahead; a unit's place is free again
     // two barriers after its join.
@@ -247,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = 1 << a.log2_block, heads = a.n_kv_heads;
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < kKeyWarps * kStages; ++i) pa::mbar_init(&full[i], 1);
         unfinite[0] = unfinite[1] = 0;
         pa::fence_mbar_init();
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (!find_share<kRows, kStep, kUnitCost, kMinSteps, kThreads>(a, walk, sums)) return;
+    if (!find_share<kRows, kStep, kUnitCost, kMinSteps, kDirectSteps, kThreads>(a, walk, parts)) return;
     if (threadIdx.x == 0) {
         next_unit<kRows, kStep, kUnitCost>(walk, units[0], a);
         next_unit<kRows, kStep, kUnitCost>(walk, units[1], a);
@@ -297,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 const int box = B < kTile ? B : kTile, boxes = (B < kTile && t0 + B < u.ctx) ? 2 : 1;
                 const uint32_t dst = stage_at(stage);
                 pa::mbar_arrive_expect_tx(bar, (uint32_t)(2 * G::kSlabs * boxes * box * 128));
+#pragma unroll 1
                 for (int r = 0; r < boxes; ++r) {
                     int blk = r ? b1 : b0;
                     if (blk < 0 || blk >= a.num_blocks) {
@@ -370,9 +377,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     uint4 qv[kQPer];
     fetch(units[0], lane, e0, e1);
     fetch(units[0], 32 + lane, f0, f1);
+#pragma unroll 1
     for (int k = 0; k < G::kAhead; ++k)
         if (k < units[0].len) issue(units[0], k);
     load_q(units[0], qv);
+#pragma unroll 1
     for (int nth = 0;; ++nth) {
         const Unit& u = units[nth & 3];
         const Unit& next = units[(nth + 1) & 3];
@@ -380,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         __syncthreads();
         const int len = u.len, ctx = u.ctx, base = u.st0 * kStep + warp * kTile;
         const bool more = next.valid;
+#pragma unroll 1
         for (int k = G::kAhead; k < kStages; ++k)
             if (k < len) issue(u, k);
         int n0 = 0, n1 = 0;
@@ -400,12 +410,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         State<D> st;
         st.reset();
         bool landed = true;
+#pragma unroll 1
         for (int k = 0; k < len; ++k) {
             const int at = used + k, stage = at % kStages;
             if (!__all_sync(0xffffffffu, pa::mbar_wait_bounded(&wfull[stage], (at / kStages) & 1, kMaxProbes))) {
                 // give up: nothing more is issued, and the copies in flight are waited for, each within the limit
                 if (lane == 0) pa::set_status(a.status, PA_DEV_WAIT_TIMEOUT);
                 const int issued = min(len, k + kStages);
+#pragma unroll 1
                 for (int j = k; j < issued; ++j)
                     pa::mbar_wait_bounded(&wfull[(used + j) % kStages], ((used + j) / kStages) & 1, kMaxProbes);
                 landed = false;
@@ -432,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             e0 = n0;
             e1 = n1;
             fetch(next, 32 + lane, f0, f1);
+#pragma unroll 1
             for (int k = 0; k < G::kAhead; ++k)
                 if (k < next.len) issue(next, k);
             load_q(next, qv);
@@ -467,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         __syncthreads();
         const bool whole = len == u.steps;
         const int slot = 2 * blockIdx.x + (u.st0 == 0 ? 1 : 0);
+#pragma unroll 1
         for (int x = threadIdx.x; x < kRows * (D / 4); x += kThreads) {
             const int r = x / (D / 4), d = x % (D / 4) * 4;
             const int row = u.row0 + r, i = row >> a.log2_group;
@@ -505,13 +519,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             }
         }
         if (__builtin_expect(unfinite[nth & 1], 0))
+#pragma unroll 1
             for (int x = threadIdx.x; x < kRows * (D / 4); x += kThreads) {   // (to what the thread itself has written)
                 const int r = x / (D / 4), d = x % (D / 4) * 4;
                 add_unfinite<D, F8>(a, u.seq, u.kvh, u.row0 + r, u.st0 * kStep, (u.st0 + len) * kStep, d,
                                     whole ? nullptr : a.part_u + ((size_t)slot * kRows + r) * D + d);
             }
         if (!whole && u.st0 == 0 && threadIdx.x == 0)             // this block begins the unit
-            a.pieces[blockIdx.x] = make_int4(u.seq, u.kvh, u.tile, u.last);
+            a.pieces[blockIdx.x] = begun_unit(u, a.log2_group);
         if (!more) return;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the join's stages go back to TMA (after the barrier above)
     }
@@ -612,7 +627,10 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     const long long seq_work = ((long long)a.ctx_cap + step - 1) / step + cost;
     const double work = (double)num_seqs * n_kv_heads * (double)tiles * (double)seq_work;
     const double shares = work / ((wide ? kWideMinSteps : kMinSteps) + cost) + 1;
-    const int grid = shares < most ? (int)shares : most;
+    const double units = (double)num_seqs * n_kv_heads * (double)tiles;
+    const bool direct = a.ctx_cap <= step * (wide ? kWideDirectSteps : kDirectSteps) && units <= most;
+    const int grid = direct ? (int)units : shares < most ? (int)shares : most;
+    a.direct = direct ? (int)tiles : 0;
 
     a.out = out;
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -659,7 +677,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
         rc = f8 ? launch_multi<128, true>(mk, mv, a, grid, st)
              : d_head == 128 ? launch_multi<128, false>(mk, mv, a, grid, st)
                              : launch_multi<64, false>(mk, mv, a, grid, st);
-    if (rc != PA_OK) return rc;
+    if (rc != PA_OK || direct) return rc;                        // (no unit is shared: nothing to merge)
     return pa_host::launch_dependent(d_head == 128 ? merge_kernel<128> : merge_kernel<64>, dim3(grid, kMergeSplit),
                                      dim3(kMergeThreads), 0, st, a, unit) == cudaSuccess
                ? PA_OK

@@ -88,9 +88,11 @@ struct Ctl {
     uint64_t o_done, o_free;               // a unit's last product has finished; its O has been read
     uint64_t stats_full, stats_free;       // the groups' statistics (and `unfinite`) are posted; the statistics are read
     uint64_t unit_full[kUnits], unit_empty[kUnits];
-    Unit units[kUnits];
+    union {
+        Unit units[kUnits];
+        Part parts[kThreads / 32];         // before the roles begin
+    };
     Walk walk;
-    long long sums[kThreads / 32];
     uint32_t tmem;
     int abort;
     int unfinite[2];                       // per unit parity: some new value is not finite
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const bool busy = find_share<kRows, kKv, kWideCost, kWideMinSteps, kThreads>(a, ctl->walk, ctl->sums);
+    const bool busy = find_share<kRows, kKv, kWideCost, kWideMinSteps, kWideDirectSteps, kThreads>(a, ctl->walk, ctl->parts);
     // an address that is not a multiple of 1024 would break the swizzled tiles
     if (busy && (s0 & 1023)) {
         if (threadIdx.x == 0) pa::set_status(a.status, PA_DEV_WAIT_TIMEOUT);
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     next_unit<kRows, kKv, kWideCost>(ctl->walk, *u, a);
                     if (u->valid && u->st0 == 0 && u->len != u->steps)       // this block begins a unit that others end
-                        a.pieces[blockIdx.x] = make_int4(u->seq, u->kvh, u->tile, u->last);
+                        a.pieces[blockIdx.x] = begun_unit(*u, a.log2_group);
                     pa::mbar_arrive(&ctl->unit_full[slot]);
                 }
                 __syncwarp();

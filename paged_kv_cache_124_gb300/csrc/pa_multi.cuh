@@ -6,7 +6,8 @@
 // its context plus a constant for starting and joining it; block b takes the
 // work from b * share to (b + 1) * share, sequence after sequence, heads and
 // row tiles within them.  A share that begins within a unit's constant part
-// begins with the unit's first step.
+// begins with the unit's first step.  Where few units of short contexts leave
+// blocks to spare, each block takes one unit instead and nothing is merged.
 #pragma once
 
 #include "pa_mma.cuh"
@@ -28,7 +29,7 @@ struct MultiArgs {
     const int32_t* query_start;
     const int32_t* context_lens;
     const uint64_t* tree_mask;             // null: causal
-    int4* pieces;                          // per block: {sequence or -1, KV head, row tile, last block}
+    int4* pieces;                          // per block: the unit that it begins and others end, or x of -1 (begun_unit)
     float* part_m;                         // [2 per block][rows]
     float* part_z;
     float* part_u;                         // [2 per block][rows][D]
@@ -38,6 +39,7 @@ struct MultiArgs {
     float v_scale;                         // factor on the weighted sums
     int out_f32, log2_block, n_q_heads, n_kv_heads, log2_group, max_blocks, num_blocks, ctx_cap, num_seqs, num_tokens,
         max_query_len;
+    int direct;                            // not 0: a block takes one whole unit, of `direct` row tiles a KV head
 };
 
 // Four consecutive values of a row.
@@ -81,11 +83,19 @@ __device__ __forceinline__ Seq read_seq(const MultiArgs& a, int s, bool flag) {
 // The stretch of one unit that a block computes: steps st0 .. st0 + len - 1.
 struct Unit {
     int q0, n, ctx, first, steps;          // first: position of new token 0
-    int kvh, row0, st0, len, seq, tile, last;   // last: the block that ends the unit
+    int kvh, row0, st0, len, seq, last;    // last: the block that ends the unit
     int valid;                             // 0: the share has ended
     const uint64_t* words;                 // mask words of the sequence's tokens, or null
     const int32_t* table;
 };
+
+// What the merge needs of a unit: its first token, its tokens (the last tile's
+// may be fewer than its rows hold), KV head and last block.  (A unit's rows
+// are a multiple of the group.)
+__device__ __forceinline__ int4 begun_unit(const Unit& u, int log2_group) {
+    const int skipped = u.row0 >> log2_group;
+    return make_int4(u.q0 + skipped, u.n - skipped, u.kvh, u.last);
+}
 
 // A block's share of the work, walked unit by unit.
 struct Walk {
@@ -117,8 +127,7 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
         u.first = w.sq.ctx - w.sq.n;
         u.steps = w.sq.steps;
         u.kvh = unit / w.sq.tiles;
-        u.tile = unit - u.kvh * w.sq.tiles;
-        u.row0 = u.tile * kRows;
+        u.row0 = (unit - u.kvh * w.sq.tiles) * kRows;
         u.st0 = lo;
         u.len = hi - lo;
         u.seq = w.seq;
@@ -129,48 +138,112 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
     }
 }
 
+// The walk of one whole unit: `unit` of sequence s.
+template <int kUnitCost>
+__device__ __forceinline__ void one_unit(Walk& walk, const Seq& sq, int s, int unit) {
+    walk.pos = 0;
+    walk.end = sq.steps + kUnitCost;
+    walk.off = unit * walk.end;
+    walk.share = walk.end;
+    walk.seq = s;
+    walk.sq = sq;
+}
+
+// A warp's part of the batch: its work, its units and the most steps of one.
+struct Part {
+    long long work;
+    int units, longest;
+};
+
 // This block's share, found by all its threads: thread t counts sequences
 // [t * per, (t + 1) * per), and the one whose sequences hold the share's
 // start sets `walk` up there.  False: the block has nothing to do.  Ends with
-// a barrier; `sums` holds a value per warp.
-template <int kRows, int kStep, int kUnitCost, int kMinSteps, int kThreads>
-__device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, long long* sums) {
+// a barrier; `parts` holds a value per warp until then.  The shares are whole units, one
+// per block, where the grid has a block for each and none is longer than
+// kDirectSteps.
+template <int kRows, int kStep, int kUnitCost, int kMinSteps, int kDirectSteps, int kThreads>
+__device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, Part* parts) {
     constexpr int kMinShare = kMinSteps + kUnitCost;
+    if (a.direct) {
+        int there = 0;
+        if (threadIdx.x == 0) {
+            const int per = a.n_kv_heads * a.direct, s = blockIdx.x / per, unit = blockIdx.x - s * per;
+            const int kvh = unit / a.direct, tile = unit - kvh * a.direct;
+            const Seq sq = read_seq<kRows, kStep>(a, s, unit == 0);
+            one_unit<kUnitCost>(walk, sq, s, kvh * sq.tiles + tile);
+            there = tile < sq.tiles;
+        }
+        return __syncthreads_or(there);
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = a.n_kv_heads;
     const int per = (a.num_seqs + kThreads - 1) / kThreads;
     const int s_lo = threadIdx.x * per, s_hi = min(a.num_seqs, s_lo + per);
-    long long mine = 0;
+    Part mine{0, 0, 0};
 #pragma unroll 1
-    for (int s = s_lo; s < s_hi; ++s) mine += read_seq<kRows, kStep>(a, s, blockIdx.x == 0).work(heads, kUnitCost);
-    long long upto = mine;
+    for (int s = s_lo; s < s_hi; ++s) {
+        const Seq sq = read_seq<kRows, kStep>(a, s, blockIdx.x == 0);
+        mine.work += sq.work(heads, kUnitCost);
+        mine.units = min(mine.units + min(heads * sq.tiles, 1 << 20), 1 << 20);   // (more than any grid is enough to know)
+        if (sq.tiles) mine.longest = max(mine.longest, sq.steps);
+    }
+    Part upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+        const long long w = __shfl_up_sync(0xffffffffu, upto.work, o);
+        const int u = __shfl_up_sync(0xffffffffu, upto.units, o);
+        if (lane >= o) {
+            upto.work += w;
+            upto.units += u;
+        }
+        upto.longest = max(upto.longest, __shfl_xor_sync(0xffffffffu, upto.longest, o));
     }
-    if (lane == 31) sums[warp] = upto;
+    if (lane == 31) parts[warp] = upto;
     __syncthreads();
-    long long total = 0;
+    Part all{0, 0, 0};
 #pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) upto += sums[w];
-        total += sums[w];
+        const Part p = parts[w];
+        if (w < warp) {
+            upto.work += p.work;
+            upto.units += p.units;
+        }
+        all.work += p.work;
+        all.units += p.units;
+        all.longest = max(all.longest, p.longest);
     }
-    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (threadIdx.x == 0) a.pieces[blockIdx.x].x = -1;
+    if (all.longest <= kDirectSteps && all.units <= (int)gridDim.x) {
+        int unit = blockIdx.x;
+        if (unit >= all.units) return false;
+        if (unit < upto.units && unit >= upto.units - mine.units) {
+            unit -= upto.units - mine.units;
+            int s = s_lo;
+            Seq sq = read_seq<kRows, kStep>(a, s, false);
+#pragma unroll 1
+            while (unit >= heads * sq.tiles) {
+                unit -= heads * sq.tiles;
+                sq = read_seq<kRows, kStep>(a, ++s, false);
+            }
+            one_unit<kUnitCost>(walk, sq, s, unit);
+        }
+        __syncthreads();
+        return true;
+    }
+    long long share = (all.work + gridDim.x - 1) / gridDim.x;
     share = share < kMinShare ? kMinShare : share;
     const long long begin = share * blockIdx.x;
-    if (threadIdx.x == 0) a.pieces[blockIdx.x].x = -1;
-    if (begin >= total) return false;
-    if (begin >= upto - mine && begin < upto) {
-        long long off = begin - (upto - mine);
+    if (begin >= all.work) return false;
+    if (begin >= upto.work - mine.work && begin < upto.work) {
+        long long off = begin - (upto.work - mine.work);
         int s = s_lo;
         Seq sq = read_seq<kRows, kStep>(a, s, false);
+#pragma unroll 1
         while (off >= sq.work(heads, kUnitCost)) {
             off -= sq.work(heads, kUnitCost);
             sq = read_seq<kRows, kStep>(a, ++s, false);
         }
         walk.pos = begin;
-        walk.end = min(total, begin + share);
+        walk.end = min(all.work, begin + share);
         walk.off = off;
         walk.share = share;
         walk.seq = s;
@@ -269,14 +342,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int4 p = a.pieces[blockIdx.x];
     if (p.x < 0) return;
-    const int q0 = a.query_start[p.x], n = a.query_start[p.x + 1] - q0;
     const int G = 1 << a.log2_group;
+#pragma unroll 1
     for (int x = blockIdx.y * kMergeThreads + threadIdx.x; x < rows * (D / 4); x += kMergeSplit * kMergeThreads) {
         const int r = x / (D / 4), d = x % (D / 4) * 4;
-        const int row = p.z * rows + r, i = row >> a.log2_group;
-        if (i >= n) return;
+        const int i = r >> a.log2_group;
+        if (i >= p.y) return;
         float M = kNone, Z = 0.f;
         float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
         for (int b = blockIdx.x; b <= p.w; ++b) {
             const size_t at = (size_t)(2 * b + (b == (int)blockIdx.x)) * rows + r;
             const float m = a.part_m[at], z = a.part_z[at];
@@ -291,7 +365,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
             M = top;
         }
         const float f = Z == 0.f ? 0.f : a.v_scale / Z;
-        put4(a.out, a.out_f32, ((size_t)(q0 + i) * a.n_q_heads + p.y * G + (row & (G - 1))) * D + d,
+        put4(a.out, a.out_f32, ((size_t)(p.x + i) * a.n_q_heads + p.z * G + (r & (G - 1))) * D + d,
              make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
     }
 }
@@ -300,6 +374,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
 // (pa_decode_wide.cu); cudaSuccess or the launch's error.
 cudaError_t launch_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& map_k,
                         const CUtensorMap& map_v, const MultiArgs& a, int grid, cudaStream_t st);
-constexpr int kWideCost = 4, kWideMinSteps = 2, kWideStep = 128;
+constexpr int kWideCost = 4, kWideMinSteps = 2, kWideStep = 128, kWideDirectSteps = 8;
 
 }  // namespace pa_multi

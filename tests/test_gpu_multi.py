@@ -502,3 +502,19 @@ def test_long_contexts_in_the_last_blocks_of_a_large_cache(n, G, fp8):
         tol = (2 * (E + 128 * 2.0 ** -24) * size + W + 2.0 ** -18).permute(2, 0, 1)[..., None] * weight * 2
         got = out[lo:lo + m].double().view(m, Hkv, G, D)
         assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max().item()
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+def test_whole_units_per_block_whether_the_bound_or_the_lengths_tell(n, G, fp8):
+    """Short contexts take a block per unit: known from max_context_len, or
+    only from the lengths; one context too long for that among them."""
+    Hkv, D, B = 2, 128, 16
+    ctxs, news = [60, 700, 33, 1, 64], [n, 2, n - 1, 1, 0]
+    q, kc, vc, tables, start, ctx = p = _problem(21, G * Hkv, Hkv, D, B, ctxs, news, fp8=fp8, gap=1)
+    near = _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8)
+    _check(p, near, G * Hkv, Hkv, D, B, fp8=fp8)
+    wide = np.concatenate([tables, np.full((len(ctxs), 300), -1, dtype=np.int32)], 1)
+    far = _run((q, kc, vc, wide, start, ctx), G * Hkv, Hkv, D, B, n, fp8=fp8, max_ctx=5000)
+    assert torch.equal(near.view(torch.int32), far.view(torch.int32))
+    p = _problem(22, G * Hkv, Hkv, D, B, [60, 1400, 33, 1, 64], news, fp8=fp8, gap=1)
+    _check(p, _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
