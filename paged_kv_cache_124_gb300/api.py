@@ -742,8 +742,9 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context
     """out [T, Hq, D] (bf16 or f32) <- attention of each sequence's few new
     tokens (rows query_start[s] .. query_start[s + 1]) over its paged cache:
     causal, or by tree_mask [T] (int64: bit b, the token sees new token b of
-    its sequence).  workspace: a uint8 tensor from decode_multi_workspace.
-    With k_scale / v_scale, the E4M3 form (uint8 caches); see pa.h."""
+    its sequence).  workspace: a uint8 tensor from decode_multi_workspace
+    (default: one allocated for this call through PyTorch's caching
+    allocator).  With k_scale / v_scale, the E4M3 form (uint8 caches); see pa.h."""
     w, dev, i32 = "pa_decode_multi", torch.cuda.current_device(), torch.int32
     f8 = k_scale is not None
     if f8 != (v_scale is not None):
@@ -756,6 +757,10 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context
         raise TypeError("out must be bfloat16 or float32")
     T, (S, MB), NB = q.shape[0], block_tables.shape, k_cache.shape[0]
     cache, shape = torch.uint8 if f8 else torch.bfloat16, (NB, n_kv_heads, block_size, d_head)
+    if workspace is None:
+        workspace = decode_multi_workspace(max_query_len, n_q_heads, n_kv_heads, d_head, q.device)
+        if stream is not None:                         # not to be handed out again while that stream uses it
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
     args = (_arg(w, "out", out, out.dtype, (T, n_q_heads, d_head), dev), out_dtype,
             _arg(w, "q", q, torch.bfloat16, (T, n_q_heads, d_head), dev), _arg(w, "k_cache", k_cache, cache, shape, dev),
             _arg(w, "v_cache", v_cache, cache, shape, dev), _arg(w, "block_tables", block_tables, i32, (S, MB), dev),
@@ -763,7 +768,7 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context
             _arg(w, "context_lens", context_lens, i32, (S,), dev),
             _opt_arg(w, "tree_mask", tree_mask, torch.int64, (T,), dev), int(block_size), float(scale))
     tail = (int(n_q_heads), int(n_kv_heads), int(d_head), S, T, int(max_query_len), MB, NB, int(max_context_len),
-            _opt_arg(w, "workspace", workspace, torch.uint8, None, dev), 0 if workspace is None else workspace.numel(),
+            _arg(w, "workspace", workspace, torch.uint8, None, dev), workspace.numel(),
             _opt_arg(w, "status", status, i32, None, dev), _raw_stream(stream, dev))
     if f8:
         return _check(_lib.pa_decode_multi_fp8(*args, float(k_scale), float(v_scale), *tail), "pa_decode_multi_fp8")

@@ -252,7 +252,7 @@ constexpr int kFusedPer = kFusedSeqs / kPlanThreads;
 constexpr int kCluster = 8;
 
 struct Planned {
-    int row, ctx, held, first;             // row -1: padding
+    int row, ctx, held, first;             // row -1: padding; entries from `held` on are the step's
 };
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1) fused_plan_kernel(const PlanArgs a) {
@@ -280,7 +280,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     for (int k = 0; k < kFusedPer; ++k) {
         const int i = t * per + k;
         if (k >= per || i >= S) continue;
-        plan[i] = Planned{q.row[k], q.len[k] + (refused ? 0 : q.n[k]), q.held[k], (int)base_need};
+        // (a refused step's tables are what the rows have, even where that is too little for their lengths)
+        plan[i] = Planned{q.row[k], q.len[k] + (refused ? 0 : q.n[k]), refused ? a.max_blocks : q.held[k], (int)base_need};
         start[i] = refused ? 0 : (int)base_n;
         base_n += q.n[k];
         base_need += q.need[k];

@@ -518,3 +518,19 @@ def test_whole_units_per_block_whether_the_bound_or_the_lengths_tell(n, G, fp8):
     assert torch.equal(near.view(torch.int32), far.view(torch.int32))
     p = _problem(22, G * Hkv, Hkv, D, B, [60, 1400, 33, 1, 64], news, fp8=fp8, gap=1)
     _check(p, _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
+
+
+def test_a_call_without_a_workspace_takes_one_of_its_own():
+    Hq, Hkv, D, B = 8, 2, 128, 16
+    p = q, kc, vc, tables, start, ctx = _problem(23, Hq, Hkv, D, B, [2000, 70], [4, 3])
+    want = _run(p, Hq, Hkv, D, B, 4)
+    a = [q.cuda(), from_bits(kc), from_bits(vc)] + [torch.from_numpy(x).cuda() for x in (tables, start, ctx)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream):
+        out = torch.zeros(q.shape, dtype=torch.float32, device="cuda")
+        torch.cuda.synchronize()
+        api.pa_decode_multi(out, *a, 4, B, 1 / math.sqrt(D), Hq, Hkv, D, 2000, stream=stream)
+        torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(0xFF)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int32), want.view(torch.int32))

@@ -427,3 +427,88 @@ def test_many_tokens_equal_the_same_tokens_a_few_at_a_time(Hq, Hkv, D, rot, inte
         a, b = (x.view(torch.int16) if x.dtype == torch.bfloat16 else x for x in (a, b))
         assert torch.equal(a, b)
     assert (got[0][0][5] == 0).all() and (got[0][0][6] == 0).all() and (got[0][0][7] != 0).any()
+
+
+@pytest.mark.parametrize("seqs,max_blocks,rows", [
+    (2, 8, 3),                       # one cluster
+    (4, 1 << 17, 5),                 # two launches: tables past what the cluster takes
+])
+@pytest.mark.parametrize("bad", ["blocks", "row"])
+def test_a_refused_plan_with_less_blocks_than_its_lengths_need(seqs, max_blocks, rows, bad):
+    """Rows that hold fewer blocks than their positions fill (they would take
+    the rest): a refused step shows what the rows have and takes nothing."""
+    p = Plan(rows, max_blocks, 9, 16, np.random.default_rng(13))
+    p.d_tables.fill_(-1)
+    lens = [100] + [0] * (rows - 1)
+    if bad == "blocks":
+        p.d_count.fill_(3)
+    seq_rows = [0, 1 if bad == "blocks" else rows] + [-1] * (seqs - 2)
+    before = p.d_tables.clone(), p.d_blocks.clone(), p.d_count.clone()
+    got = p.gpu(seq_rows, [20, 1] + [0] * (seqs - 2), 30, lens)
+    assert p.status.item() == (api.PA_DEV_NO_BLOCKS if bad == "blocks" else api.PA_DEV_BAD_ROW)
+    assert got[1][0] == 100 and got[2] == [0] * (seqs + 1) and got[3] == [-1] * 30 and got[4] == [-1] * 30
+    assert all(x == -1 for t in got[0] for x in t)
+    for a, b in zip(before, (p.d_tables, p.d_blocks, p.d_count)):
+        assert torch.equal(a, b)
+    p.d_count.fill_(9)
+    p.status.zero_()
+    if bad == "blocks":                                  # enough of them: the rest of the row's is taken with the step's
+        got = p.gpu(seq_rows, [20, 1] + [0] * (seqs - 2), 30, lens)
+        assert p.status.item() == 0 and p.d_blocks.cpu().tolist()[:2] == [8, 1] and p.d_count.item() == 0
+        assert got[0][0][:8] == p.free[:0:-1] and got[0][1][0] == p.free[0]
+        assert got[3][:21] == list(range(100, 120)) + [0]
+
+
+@pytest.mark.parametrize("seqs,max_blocks,rows,tokens", [
+    (2048, 4, 2050, 0), (2049, 4, 2050, 0),              # the most requests of one cluster, and one more
+    (100, 2000, 101, 8750), (100, 2000, 101, 8751),      # its most table entries and tokens
+    (3, 4, 262144, 5),                                   # the most rows
+])
+def test_steps_at_the_bounds_of_the_single_launch(seqs, max_blocks, rows, tokens):
+    rng = np.random.default_rng(14)
+    p = Plan(rows, max_blocks, 5000, 8, rng)
+    which = [int(r) for r in rng.permutation(rows)[:seqs]]
+    for _ in range(2):
+        new = [int(n) for n in rng.integers(0, 3, seqs)]
+        p.step(which, new, pad=max(0, tokens - sum(new)))
+        p.step(which, [0] * (seqs - 1) + [1], pad=tokens)
+
+
+def test_plans_of_two_pools_at_once_and_replayed():
+    """Two planners on two streams, and both captured: each keeps to its own
+    state."""
+    rng = np.random.default_rng(15)
+    plans = [Plan(40, 64, 900, 16, rng) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in plans]
+    d = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    news = [[int(n) for n in rng.integers(0, 4, 40)] for _ in plans]
+    outs = [p.outputs(40, 130) for p in plans]
+    args = [(d(list(range(40))), d(n), d([0] * 40)) for n in news]
+    run = lambda i: api.pa_plan_step(*outs[i], *args[i], plans[i].d_tables, plans[i].d_blocks, plans[i].d_free,  # noqa: E731
+                                     plans[i].d_count, 16, 900, status=plans[i].status)
+    lens = [a[2] for a in args]
+    torch.cuda.synchronize()
+    for step in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                run(i)
+                lens[i].add_(args[i][1])
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(i)
+            lens[i].add_(args[i][1])
+        graphs.append(g)
+    for step in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for p, n, o in zip(plans, news, outs):
+        for step in range(9):
+            want = S.plan_step(list(range(40)), n, p.lens, p.tables, p.blocks, p.free, 16, 130)
+            p.lens = [a + b for a, b in zip(p.lens, n)]
+        assert p.status.item() == 0
+        p.check_state()
+        assert [x.cpu().tolist() for x in o[1:]] == list(want[1:])
