@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in include/pa.h (ctypes; marshalling only).
+"""Python binding of the C ABI in include/pa.h (ctypes, and for the operators of
+every step the native module _step_calls; marshalling only).
 
 Every function here checks tensor placement, dtype and shape, turns tensors
 into raw pointers and sizes, and calls the library entry point of the same
@@ -50,6 +51,8 @@ if not os.path.exists(_LIB_PATH):
                       "there is no fallback implementation")
 
 _lib = ctypes.CDLL(_LIB_PATH)
+
+from . import _step_calls  # noqa: E402  (the step operators' calls; linked to the library)
 
 _c_int, _c_size, _c_float = ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _vp, _i32p, _i64p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64)
@@ -597,27 +600,6 @@ def pa_swap_blocks(dst_k, dst_v, src_k, src_v, block_pairs, status=None, stream=
 # a step of new tokens: planning, norm + rotation + cache write, attention
 # ----------------------------------------------------------------------------
 
-def _arg(where, name, t, dtype, shape, dev):
-    """Raw pointer of a contiguous CUDA tensor of the current device `dev`;
-    shape None: any."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and \
-            (shape is None or t.shape == shape) and t.is_contiguous():
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s: %s must be a torch.Tensor" % (where, name))
-    if t.dtype is not dtype:
-        raise TypeError("%s: %s must be %s, got %s" % (where, name, dtype, t.dtype))
-    if t.get_device() != dev:
-        raise ValueError("%s: %s must be a CUDA tensor of the current device (%d), got %s" % (where, name, dev, t.device))
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s: %s must be %s, got %s" % (where, name, list(shape), list(t.shape)))
-    raise ValueError("%s: %s must be contiguous" % (where, name))
-
-
-def _opt_arg(where, name, t, dtype, shape, dev):
-    return None if t is None else _arg(where, name, t, dtype, shape, dev)
-
-
 # torch.cuda.current_stream makes a Stream object; its handle alone is quicker
 _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -638,31 +620,18 @@ def pa_plan_step(block_tables, context_lens, query_start, positions, slot_mappin
     row_tables / row_blocks / free_count up to date, and writes block_tables
     [S, max_blocks], context_lens [S], query_start [S + 1], positions [T] and
     slot_mapping [T]; row_lens is only read.  See pa.h."""
-    w, dev, i32 = "pa_plan_step", torch.cuda.current_device(), torch.int32
-    S, (R, MB), T = seq_rows.shape[0], row_tables.shape, positions.shape[0]
-    st = _lib.pa_plan_step(
-        _arg(w, "block_tables", block_tables, i32, (S, MB), dev), _arg(w, "context_lens", context_lens, i32, (S,), dev),
-        _arg(w, "query_start", query_start, i32, (S + 1,), dev), _arg(w, "positions", positions, i32, (T,), dev),
-        _arg(w, "slot_mapping", slot_mapping, torch.int64, (T,), dev), _arg(w, "seq_rows", seq_rows, i32, (S,), dev),
-        _arg(w, "new_lens", new_lens, i32, (S,), dev), _arg(w, "row_lens", row_lens, i32, (R,), dev),
-        _arg(w, "row_tables", row_tables, i32, (R, MB), dev), _arg(w, "row_blocks", row_blocks, i32, (R,), dev),
-        _opt_arg(w, "free_blocks", free_blocks, i32, None, dev), _opt_arg(w, "free_count", free_count, i32, (1,), dev),
-        0 if free_blocks is None else free_blocks.numel(), S, R, MB, T, int(block_size), int(num_blocks),
-        _opt_arg(w, "status", status, i32, None, dev), _raw_stream(stream, dev))
-    return _check(st, w)
+    dev = torch.cuda.current_device()
+    return _check(_step_calls.plan_step(block_tables, context_lens, query_start, positions, slot_mapping, seq_rows, new_lens,
+                                        row_lens, row_tables, row_blocks, free_blocks, free_count, block_size, num_blocks,
+                                        status, dev, _raw_stream(stream, dev)), "pa_plan_step")
 
 
 def pa_release_rows(rows, row_tables, row_blocks, free_blocks, free_count, status=None, stream=None):
     """Push every block of the named rows (int32; negative: skipped) onto
     free_blocks and set their row_blocks to 0; see pa.h."""
-    w, dev, i32 = "pa_release_rows", torch.cuda.current_device(), torch.int32
-    R, MB = row_tables.shape
-    st = _lib.pa_release_rows(
-        _arg(w, "rows", rows, i32, (rows.shape[0],), dev), rows.shape[0],
-        _arg(w, "row_tables", row_tables, i32, (R, MB), dev), _arg(w, "row_blocks", row_blocks, i32, (R,), dev), R, MB,
-        _arg(w, "free_blocks", free_blocks, i32, None, dev), _arg(w, "free_count", free_count, i32, (1,), dev),
-        free_blocks.numel(), _opt_arg(w, "status", status, i32, None, dev), _raw_stream(stream, dev))
-    return _check(st, w)
+    dev = torch.cuda.current_device()
+    return _check(_step_calls.release_rows(rows, row_tables, row_blocks, free_blocks, free_count, status, dev,
+                                           _raw_stream(stream, dev)), "pa_release_rows")
 
 
 def rope_table(max_positions, rot_dim, base=10000.0, device=None):
@@ -674,22 +643,6 @@ def rope_table(max_positions, rot_dim, base=10000.0, device=None):
     return torch.cat([angle.cos(), angle.sin()], 1).float().to(device or "cuda")
 
 
-def _token_rows(where, name, t, shape, dev):
-    """Pointer and token stride of a bf16 tensor [T, heads, d] whose heads are
-    contiguous within a token."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
-        raise TypeError("%s: %s must be a bfloat16 tensor" % (where, name))
-    if t.get_device() != dev:
-        raise ValueError("%s: %s must be a CUDA tensor of the current device (%d), got %s" % (where, name, dev, t.device))
-    if t.shape != shape:
-        raise ValueError("%s: %s must be %s, got %s" % (where, name, list(shape), list(t.shape)))
-    T, heads, d = shape
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != d):
-        raise ValueError("%s: the heads of a token of %s must be contiguous" % (where, name))
-    return t.data_ptr(), (s[0] if T > 1 else heads * d)
-
-
 def pa_qk_norm_rope_cache(q_out, k_cache, v_cache, q, k, v, positions, slot_mapping, cos_sin, q_weight=None,
                           k_weight=None, eps=1e-6, interleaved=False, status=None, stream=None, k_scale=None,
                           v_scale=None):
@@ -699,31 +652,13 @@ def pa_qk_norm_rope_cache(q_out, k_cache, v_cache, q, k, v, positions, slot_mapp
     cos_sin [max_positions, rot_dim] (see rope_table), q to q_out, k and v to
     the slots slot_mapping [T] (int64) of the caches.  With k_scale / v_scale,
     the E4M3 form (uint8 caches); see pa.h."""
-    w, dev, f32 = "pa_qk_norm_rope_cache", torch.cuda.current_device(), torch.float32
-    T, Hq, D = q.shape
-    NB, Hkv, B, _ = k_cache.shape
-    f8 = k_scale is not None
-    if f8 != (v_scale is not None):
+    dev = torch.cuda.current_device()
+    if (k_scale is None) != (v_scale is None):
         raise ValueError("pa_qk_norm_rope_cache: k_scale and v_scale go together")
-    if cos_sin.dim() != 2:
-        raise ValueError("pa_qk_norm_rope_cache: cos_sin must be [max_positions, rot_dim]")
-    cache, shape = torch.uint8 if f8 else torch.bfloat16, (NB, Hkv, B, D)
-    qp, qs = _token_rows(w, "q", q, (T, Hq, D), dev)
-    kp, ks = _token_rows(w, "k", k, (T, Hkv, D), dev)
-    vp, vs = _token_rows(w, "v", v, (T, Hkv, D), dev)
-    args = (_arg(w, "q_out", q_out, torch.bfloat16, (T, Hq, D), dev), _arg(w, "k_cache", k_cache, cache, shape, dev),
-            _arg(w, "v_cache", v_cache, cache, shape, dev), qp, kp, vp, qs, ks, vs,
-            _opt_arg(w, "q_weight", q_weight, f32, (D,), dev), _opt_arg(w, "k_weight", k_weight, f32, (D,), dev),
-            float(eps), _arg(w, "cos_sin", cos_sin, f32, None, dev), cos_sin.shape[0], cos_sin.shape[1],
-            1 if interleaved else 0, _arg(w, "positions", positions, torch.int32, (T,), dev),
-            _arg(w, "slot_mapping", slot_mapping, torch.int64, (T,), dev), T, Hq, Hkv, D, B, NB)
-    tail = (_opt_arg(w, "status", status, torch.int32, None, dev), _raw_stream(stream, dev))
-    if T == 0:
-        return PA_OK                                   # (empty tensors have no address)
-    if f8:
-        return _check(_lib.pa_qk_norm_rope_cache_fp8(*args, float(k_scale), float(v_scale), *tail),
-                      "pa_qk_norm_rope_cache_fp8")
-    return _check(_lib.pa_qk_norm_rope_cache(*args, *tail), w)
+    return _check(_step_calls.qk_norm_rope_cache(q_out, k_cache, v_cache, q, k, v, positions, slot_mapping, cos_sin, q_weight,
+                                                 k_weight, eps, bool(interleaved), status, k_scale, v_scale, dev,
+                                                 _raw_stream(stream, dev)),
+                  "pa_qk_norm_rope_cache" if k_scale is None else "pa_qk_norm_rope_cache_fp8")
 
 
 def pa_decode_multi_workspace_size(max_query_len, n_q_heads, n_kv_heads, d_head):
@@ -745,34 +680,17 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context
     its sequence).  workspace: a uint8 tensor from decode_multi_workspace
     (default: one allocated for this call through PyTorch's caching
     allocator).  With k_scale / v_scale, the E4M3 form (uint8 caches); see pa.h."""
-    w, dev, i32 = "pa_decode_multi", torch.cuda.current_device(), torch.int32
-    f8 = k_scale is not None
-    if f8 != (v_scale is not None):
+    dev = torch.cuda.current_device()
+    if (k_scale is None) != (v_scale is None):
         raise ValueError("pa_decode_multi: k_scale and v_scale go together")
-    if out.dtype is torch.bfloat16:
-        out_dtype = PA_DTYPE_BF16
-    elif out.dtype is torch.float32:
-        out_dtype = PA_DTYPE_F32
-    else:
-        raise TypeError("out must be bfloat16 or float32")
-    T, (S, MB), NB = q.shape[0], block_tables.shape, k_cache.shape[0]
-    cache, shape = torch.uint8 if f8 else torch.bfloat16, (NB, n_kv_heads, block_size, d_head)
     if workspace is None:
         workspace = decode_multi_workspace(max_query_len, n_q_heads, n_kv_heads, d_head, q.device)
         if stream is not None:                         # not to be handed out again while that stream uses it
             workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
-    args = (_arg(w, "out", out, out.dtype, (T, n_q_heads, d_head), dev), out_dtype,
-            _arg(w, "q", q, torch.bfloat16, (T, n_q_heads, d_head), dev), _arg(w, "k_cache", k_cache, cache, shape, dev),
-            _arg(w, "v_cache", v_cache, cache, shape, dev), _arg(w, "block_tables", block_tables, i32, (S, MB), dev),
-            _arg(w, "query_start", query_start, i32, (S + 1,), dev),
-            _arg(w, "context_lens", context_lens, i32, (S,), dev),
-            _opt_arg(w, "tree_mask", tree_mask, torch.int64, (T,), dev), int(block_size), float(scale))
-    tail = (int(n_q_heads), int(n_kv_heads), int(d_head), S, T, int(max_query_len), MB, NB, int(max_context_len),
-            _arg(w, "workspace", workspace, torch.uint8, None, dev), workspace.numel(),
-            _opt_arg(w, "status", status, i32, None, dev), _raw_stream(stream, dev))
-    if f8:
-        return _check(_lib.pa_decode_multi_fp8(*args, float(k_scale), float(v_scale), *tail), "pa_decode_multi_fp8")
-    return _check(_lib.pa_decode_multi(*args, *tail), w)
+    return _check(_step_calls.decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len,
+                                           block_size, scale, n_q_heads, n_kv_heads, d_head, max_context_len, tree_mask,
+                                           workspace, status, k_scale, v_scale, dev, _raw_stream(stream, dev)),
+                  "pa_decode_multi" if k_scale is None else "pa_decode_multi_fp8")
 
 
 # ----------------------------------------------------------------------------

@@ -1,8 +1,11 @@
-"""Build the C-ABI library libpa_gb300.so for sm_103a, in tree.
+"""Build the C-ABI library libpa_gb300.so for sm_103a, and the binding's native
+module _step_calls.so, in tree.
 
 Each translation unit under csrc/ is compiled by nvcc in parallel and the
-objects are linked into paged_kv_cache_124_gb300/libpa_gb300.so.  Nothing is
-rebuilt when the library is newer than every source and header.
+objects are linked into paged_kv_cache_124_gb300/libpa_gb300.so.  The module,
+csrc/binding/, is compiled beside them by the host's C++ compiler against
+PyTorch's headers and linked to the library.  Nothing is rebuilt when both are
+newer than every source and header.
 
     python -m paged_kv_cache_124_gb300.build [--force]
 """
@@ -13,6 +16,7 @@ import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libpa_gb300.so")
+BINDING = os.path.join(CSRC, "binding", "step_calls.cpp")
+MODULE = os.path.join(PKG, "_step_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -38,7 +44,7 @@ def sources():
 def _inputs():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     hdrs += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    return sources() + hdrs + [os.path.abspath(__file__)]
+    return sources() + hdrs + [BINDING, os.path.abspath(__file__)]
 
 
 # ELF e_machine of a shared object built for this host (x86-64 or AArch64)
@@ -54,14 +60,15 @@ def elf_matches_host(header, machine=None):
 
 
 def up_to_date():
-    """The library exists, was built for this host's machine, and is newer
-    than every source and header."""
-    if not os.path.exists(LIB):
-        return False
-    with open(LIB, "rb") as f:
-        if not elf_matches_host(f.read(20)):
+    """The library and the module exist, were built for this host's machine,
+    and are newer than every source and header."""
+    for built in (LIB, MODULE):
+        if not os.path.exists(built):
             return False
-    t = os.path.getmtime(LIB)
+        with open(built, "rb") as f:
+            if not elf_matches_host(f.read(20)):
+                return False
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -76,23 +83,58 @@ def _compile(src, verbose):
     return obj, r.stderr
 
 
+def _run(what, cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, " ".join(cmd), r.stderr))
+
+
+def _cxx():
+    cand = shutil.which("g++") or shutil.which("c++")
+    if cand is None:
+        raise RuntimeError("no C++ compiler found; g++ is required to build _step_calls.so")
+    return cand
+
+
+def _compile_binding():
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJ_DIR, os.path.basename(BINDING) + ".o")
+    _run("the binding's compilation",
+         [_cxx(), "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+          "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-c", BINDING, "-o", obj])
+    return obj
+
+
+def _link_binding(obj):
+    import torch
+
+    _run("the binding's link",
+         [_cxx(), "-shared", "-o", MODULE + ".tmp", obj, LIB, "-Wl,-rpath,$ORIGIN", "-L",
+          os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(MODULE + ".tmp", MODULE)
+
+
 def build(force=False, verbose=False):
-    """Compile csrc/ into libpa_gb300.so (sm_103a).  Returns the library path."""
+    """Compile csrc/ into libpa_gb300.so (sm_103a) and _step_calls.so.  Returns the library path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose), sources()))
+        binding = binding.result()
     if verbose:
         for _, log in results:
             if log:
                 sys.stderr.write(log)
     tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    _run("link", [_nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp] +
+         [o for o, _ in results])
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

@@ -512,3 +512,41 @@ def test_plans_of_two_pools_at_once_and_replayed():
         assert p.status.item() == 0
         p.check_state()
         assert [x.cpu().tolist() for x in o[1:]] == list(want[1:])
+
+
+def test_tensors_of_wrong_type_shape_place_or_layout_are_refused():
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    b = lambda *s: z(*s, dt=torch.bfloat16)  # noqa: E731
+    plan = dict(block_tables=z(2, 4), context_lens=z(2), query_start=z(3), positions=z(5), slot_mapping=z(5).long(),
+                seq_rows=z(2), new_lens=z(2), row_lens=z(8), row_tables=z(8, 4), row_blocks=z(8), free_blocks=z(64),
+                free_count=z(1), block_size=16, num_blocks=64)
+    rope = dict(q_out=b(3, 4, 64), k_cache=b(2, 2, 16, 64), v_cache=b(2, 2, 16, 64), q=b(3, 4, 64), k=b(3, 2, 64),
+                v=b(3, 2, 64), positions=z(3), slot_mapping=z(3).long(), cos_sin=z(9, 64, dt=torch.float32))
+    multi = dict(out=b(3, 4, 64), q=b(3, 4, 64), k_cache=b(2, 2, 16, 64), v_cache=b(2, 2, 16, 64), block_tables=z(1, 2),
+                 query_start=z(2), context_lens=z(1), max_query_len=3, block_size=16, scale=0.125, n_q_heads=4,
+                 n_kv_heads=2, d_head=64, max_context_len=32)
+    for fn, good, cases in (
+            (api.pa_plan_step, plan, [
+                (dict(context_lens=z(3)), ValueError, "context_lens must be"), (dict(positions=z(6)), ValueError, "slot_mapping must be"),
+                (dict(row_tables=z(4, 8).t()), ValueError, "row_tables must be contiguous"),
+                (dict(new_lens=z(2).cpu()), ValueError, "new_lens must be a CUDA tensor"),
+                (dict(row_blocks=z(8).long()), TypeError, "row_blocks must be torch.int32"),
+                (dict(free_count=z(2)), ValueError, "free_count must be"), (dict(seq_rows=None), TypeError, "seq_rows must be a torch"),
+                (dict(block_size=1 << 40), ValueError, "outside 32 bits"), (dict(block_size="16"), TypeError, None)]),
+            (api.pa_qk_norm_rope_cache, rope, [
+                (dict(q=b(3, 64, 4).transpose(1, 2)), ValueError, "q must have the heads"),
+                (dict(k=b(3, 4, 64)), ValueError, "k must be"), (dict(v=b(4, 2, 64)), ValueError, "v must be"),
+                (dict(cos_sin=z(9, 64)), TypeError, "cos_sin must be torch.float32"),
+                (dict(q_out=b(6, 4, 64)[::2]), ValueError, "q_out must be contiguous"),
+                (dict(k_scale=0.1, v_scale=0.1), TypeError, "k_cache must be torch.uint8"),
+                (dict(q_weight=z(63, dt=torch.float32), k_weight=z(64, dt=torch.float32)), ValueError, "q_weight must be")]),
+            (api.pa_decode_multi, multi, [
+                (dict(out=z(3, 4, 64)), TypeError, "out must be bfloat16"), (dict(q=b(3, 2, 64)), ValueError, "q must be"),
+                (dict(v_cache=b(2, 2, 8, 64)), ValueError, "v_cache must be"), (dict(query_start=z(1)), ValueError, "query_start must be"),
+                (dict(tree_mask=z(2).long()), ValueError, "tree_mask must be"), (dict(k_scale=0.1), ValueError, "go together"),
+                (dict(workspace=z(16)), TypeError, "workspace must be torch.uint8"), (dict(scale="x"), TypeError, None)])):
+        assert fn(**good) == api.PA_OK
+        for change, error, text in cases:
+            with pytest.raises(error, match=text):
+                fn(**dict(good, **change))
+    torch.cuda.synchronize()

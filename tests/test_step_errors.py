@@ -163,16 +163,22 @@ def test_binding_refuses_host_tensors_before_any_call(monkeypatch):
     z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)  # noqa: E731
     with pytest.raises(ValueError, match="CUDA tensor"):
         api.pa_plan_step(z(2, 4), z(2), z(3), z(5), z(5, dt=torch.int64), z(2), z(2), z(8), z(8, 4), z(8), None, None,
-                         16, 64)
-    with pytest.raises(TypeError, match="context_lens"):
-        api._arg("x", "context_lens", z(2, dt=torch.int64), torch.int32, (2,), 0)
+                         16, 64, stream=0)
+    with pytest.raises(TypeError, match="block_tables must be torch.int32, got torch.int64"):
+        api.pa_plan_step(z(2, 4, dt=torch.int64), z(2), z(3), z(5), z(5, dt=torch.int64), z(2), z(2), z(8), z(8, 4), z(8),
+                         None, None, 16, 64, stream=0)
+    with pytest.raises(TypeError, match="seq_rows must be a torch.Tensor"):
+        api.pa_plan_step(z(2, 4), z(2), z(3), z(5), z(5, dt=torch.int64), [0, 1], z(2), z(8), z(8, 4), z(8), None, None,
+                         16, 64, stream=0)
+    with pytest.raises(ValueError, match="row_tables must have 2 dimensions"):
+        api.pa_release_rows(z(2), z(8), z(8), z(9), z(1), stream=0)
     b = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     with pytest.raises(ValueError, match="go together"):
         api.pa_qk_norm_rope_cache(b(1, 4, 64), b(2, 2, 16, 64), b(2, 2, 16, 64), b(1, 4, 64), b(1, 2, 64), b(1, 2, 64),
                                   z(1), z(1, dt=torch.int64), z(9, 64, dt=torch.float32), k_scale=0.1)
     with pytest.raises(ValueError, match="CUDA tensor"):
         api.pa_decode_multi(b(1, 4, 64), b(1, 4, 64), b(2, 2, 16, 64), b(2, 2, 16, 64), z(1, 3), z(2), z(1), 1, 16,
-                            0.125, 4, 2, 64, 48)
+                            0.125, 4, 2, 64, 48, workspace=z(16, dt=torch.uint8), stream=0)
 
 
 def test_rope_table_is_the_angles_cosines_and_sines():
