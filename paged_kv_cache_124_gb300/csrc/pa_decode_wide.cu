@@ -156,7 +156,16 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for this warp's loads; `v` (their results) is not used before.
+template <int N, class T>
+__device__ __forceinline__ void wait_ld(T* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr (T(0.5f) == T(0)) asm volatile("" : "+r"(v[i]));
+        else asm volatile("" : "+f"(v[i]));
+    }
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of this thread's lane.
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* empty = is_k ? ctl->k_empty : ctl->v_empty;
         const CUtensorMap* map = is_k ? &map_k : &map_v;
         const uint64_t policy = pa::l2_evict_first_policy();
-        int done = 0, nth = 0;                                   // tiles and units so far
+        int loaded = 0, nth = 0;                                 // tiles and units so far
         bool ok = true;
 #pragma unroll 1
         for (; ok; ++nth) {
@@ -420,15 +429,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int row = 0, ahead = fetch(0);
 #pragma unroll 1
-            for (int j = 0; j < len; ++j, ++done) {
-                const int turn = j & (per - 1), st = done % kStages;
+            for (int j = 0; j < len; ++j, ++loaded) {
+                const int turn = j & (per - 1), st = loaded % kStages;
                 if (turn == 0) {
                     row = oob_row;
                     if (ahead >= 0 && ahead < a.num_blocks) row = (ahead * a.n_kv_heads + kvh) * B;
                     else if (ahead != kNoBlock) flag(a.status, PA_DEV_BAD_BLOCK_ID);
                     ahead = fetch(j + per);
                 }
-                if (done >= kStages && !(ok = wait_for(&empty[st], (done / kStages - 1) & 1, ctl, a.status))) break;
+                if (loaded >= kStages && !(ok = wait_for(&empty[st], (loaded / kStages - 1) & 1, ctl, a.status))) break;
                 if (lane == 0) pa::mbar_arrive_expect_tx(&full[st], G::kTileBytes);
                 __syncwarp();
                 if (turn == sub) {
@@ -443,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             if (!F8 && !is_k && nth > 0) pa::mbar_wait_bounded(ctl->q_full, (nth - 1) & 1, kMaxProbes);
 #pragma unroll 1
-            for (int i = 0; i < kStages && i < done; ++i)
-                pa::mbar_wait_bounded(&full[(done - 1 - i) % kStages], ((done - 1 - i) / kStages) & 1, kMaxProbes);
+            for (int i = 0; i < kStages && i < loaded; ++i)
+                pa::mbar_wait_bounded(&full[(loaded - 1 - i) % kStages], ((loaded - 1 - i) / kStages) & 1, kMaxProbes);
         }
     } else if (warp == kScoreWarp) {
         // ------------------------------------------------------------ score products, by one thread
@@ -645,16 +654,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < len; ++j, ++at) {
                 const int b = at & 1;
+                const uint32_t t_s = t_lane + b * 128 + w * kHalfKv;
                 if (!(ok = wait_for(&ctl->s_full[b], (at >> 1) & 1, ctl, a.status))) break;
                 fence_after();
-                const uint32_t t_s = t_lane + b * 128 + w * kHalfKv;
                 float s[kCols];
                 if constexpr (kHalf) {
                     ld32_split32(t_s, s);
                     if constexpr (F8) {                          // and the scores of q's second term, in the row's second lane
                         float s2[32];
                         ld32_split32(t_s + kLanes16, s2);
-                        wait_ld();
+                        wait_ld<32>(s2);
+                        wait_ld<32>(s);
 #pragma unroll
                         for (int k = 0; k < 32; k += 2)
                             split(add2(pair(s[k], s[k + 1]), pair(s2[k], s2[k + 1])), s[k], s[k + 1]);
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ld32(t_s, s);
                     ld32(t_s + 32, s + 32);
                 }
-                wait_ld();
+                wait_ld<kCols>(s);
                 const int t0 = start + j * kKv;
                 if (t0 + kCols > first) {                        // some row may not see some position
 #pragma unroll
@@ -695,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < D; x += 16) {
                         uint32_t o[16];
                         ld16(t_o + x, o);
-                        wait_ld();
+                        wait_ld<16>(o);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                         st16(t_o + x, o);
@@ -882,7 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float v[32], v1[32];
                 ld32(t_o + x, v);
                 ld32(t_o + 128 + x, v1);
-                wait_ld();
+                wait_ld<32>(v);
+                wait_ld<32>(v1);
                 if (x == D - 32) {                               // O is in registers: the next unit's products may write it
                     fence_before();
                     pa::mbar_arrive(&ctl->o_free);
