@@ -13,7 +13,11 @@
 // is not positive); pa_decode_wide.cu takes more.
 //
 // What bounds it: each K/V byte is read once for n * G rows, 4 * n * G
-// operations per two bytes, so the cache's bytes bound it.
+// operations per two bytes, so the cache's bytes bound it.  64 sequences of
+// 4096 positions, 8 KV heads of 128, 16 rows: 167 us, 0.95 of the measured
+// copy rate; E4M3 98 us, 0.81 (there the unpacking of codes to f16 for
+// warp-level products takes 44 % of the ALU's cycles).  The smallest steps
+// are a chain of latencies: 4 sequences of up to 37 positions take 5.3 us.
 //  * A unit is a (sequence, KV head, tile of 16 rows); its work is counted in
 //    steps of 64 positions plus a constant for starting and joining it.  The
 //    grid is the resident blocks, and they take equal contiguous shares of
@@ -32,7 +36,8 @@
 //    and sums in fp32.
 //  * A unit that one block covers is written at once.  Pieces of the others
 //    go to the workspace as (m, z, u), and a second kernel, over the units
-//    that a block began and did not finish, merges them.
+//    that a block began and did not finish, merges them.  Short contexts with
+//    a block for every unit are not split, and then nothing is merged.
 
 #include <math.h>
 
@@ -548,15 +553,13 @@ int sms() {
 }
 
 // Whether the units of 64 (or 128) rows of pa_decode_wide.cu serve a call:
-// from more than 16 rows a KV head on, where they read the cache once for all
-// of them.  Both sides measured at 8 KV heads of 128:
-//   sequences x context, rows    here      wide
-//   64 x 4096 bf16, 16           172 us    -
-//   64 x 4096 bf16, 20           173       165 us   (32-row units here)
-//   64 x 4096 bf16, 32           175       169
-//   512 x 500 bf16, 32           232       190
-//   64 x 4096 E4M3, 16           102       119
-//   512 x 500 E4M3, 16           131       232
+// from more than 16 rows a KV head on, where they read the cache once and
+// units of 16 twice.  8 KV heads of 128, us here against there:
+//   sequences x positions   bf16, 16 rows   20 or 32      E4M3, 16     20 or 32
+//   64 x 4096               167 / 161       317 / 161     98 / 104     179 / 104
+//   512 x 500               172 / 168       349 / 176     127 / 152    242 / 154
+//   2048 x 60               202 / 353       @@
+// (At 16 rows short contexts decide: a unit there costs some 3 to 4 us.)
 // Its bf16 products take a positive scale only; others go 16 rows at a time.
 bool is_wide(bool f8, float scale, long long rows) { return rows > kRows && (f8 || scale > 0.f); }
 

@@ -6,7 +6,12 @@
 // What bounds it: a tile of 128 positions of one KV head (64 KB of K and V at
 // d_head 128) takes an SM about 1.46 us of its share of the memory's rate,
 // and its products, S = Q . K^T and O += P . V at 128 rows, 0.33 us each: the
-// bytes bound it as long as copies, products and softmax overlap.
+// bytes bound it as long as copies, products and softmax overlap.  64
+// sequences of 4096 positions, 8 KV heads of 128: 32 rows 163 us (0.98 of the
+// measured copy rate), 64 rows 168 (0.96), 128 rows 182 (0.90; 750 TFLOP/s).
+// E4M3: 32 rows 104 us (0.77), bound by the softmax, whose conversions to
+// three E4M3 terms take half of the ALU's cycles and some 1650 of a tile's.
+// (Two terms, a relative 2^-9, were 97 us: not worth the weights' precision.)
 //  * One block per SM walks its share.  A producer warp each fills stages of
 //    K and V through the block table; one warp issues the score products of
 //    whole tiles, into two buffers in turn; two groups of four warps take the
@@ -19,7 +24,11 @@
 //    (An issuing thread spends some 60 to 100 cycles on a product of 64 and a
 //    hand-over between warps 100 to 450, so what bounds the rate of tiles is
 //    the chain scores - softmax - values: two buffers and a chain of half a
-//    tile keep it under the memory's 2800 cycles a tile, E4M3's 1400.)
+//    tile keep it under the memory's 2800 cycles a tile.)
+//  * Roles are many and their code together is larger than the instruction
+//    cache, so what is not a tile's work is kept out of it or rolled up
+//    (unroll 1): with one miss for five fetches instead of 25, 64 requests of
+//    8 tokens over E4M3 took 100 us instead of 68.
 //  * Every barrier is waited for in every phase, in order, by each of its
 //    waiters, so no wait can take an older phase's parity for its own.
 //  * bf16: V stays bf16, so the weights enter P . V as two bf16 terms (hi +

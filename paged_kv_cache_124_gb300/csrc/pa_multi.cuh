@@ -348,13 +348,17 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
         const int r = x / (D / 4), d = x % (D / 4) * 4;
         const int i = r >> a.log2_group;
         if (i >= p.y) return;
-        float M = kNone, Z = 0.f;
-        float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int b = blockIdx.x; b <= p.w; ++b) {
-            const size_t at = (size_t)(2 * b + (b == (int)blockIdx.x)) * rows + r;
-            const float m = a.part_m[at], z = a.part_z[at];
-            const float4 v = *reinterpret_cast<const float4*>(a.part_u + at * D + d);
+        // a unit has two pieces at least: the first two are loaded together
+        int at = (2 * blockIdx.x + 1) * rows + r;
+        const float* u = a.part_u + (size_t)at * D + d;
+        float M = a.part_m[at], Z = a.part_z[at];
+        float4 U = *reinterpret_cast<const float4*>(u);
+        at += rows;
+        u += (size_t)rows * D;
+        float m = a.part_m[at], z = a.part_z[at];
+        float4 v = *reinterpret_cast<const float4*>(u);
+#pragma unroll 1
+        for (int b = blockIdx.x + 1;;) {
             const float top = fmaxf(M, m);
             const float f = pa::exp2_approx(M - top), h = pa::exp2_approx(m - top);
             Z = Z * f + z * h;
@@ -363,6 +367,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
             U.z = U.z * f + v.z * h;
             U.w = U.w * f + v.w * h;
             M = top;
+            if (++b > p.w) break;
+            at += 2 * rows;                                      // (the first slot of the next block)
+            u += (size_t)2 * rows * D;
+            m = a.part_m[at];
+            z = a.part_z[at];
+            v = *reinterpret_cast<const float4*>(u);
         }
         const float f = Z == 0.f ? 0.f : a.v_scale / Z;
         put4(a.out, a.out_f32, ((size_t)(p.x + i) * a.n_q_heads + p.z * G + (r & (G - 1))) * D + d,
