@@ -54,7 +54,10 @@ constexpr int kRows = 16;                  // rows of a unit
 constexpr int kThreads = 32 * kKeyWarps;
 constexpr int kBlocksPerSm = 3;
 constexpr float kWeightScale = 128.f;      // FP8: weights enter f16 products times 2^7 (at most 2^15)
-constexpr int kUnitCost = 5;               // steps that starting and joining a unit is worth
+// Steps that starting and joining a unit is worth (64 requests of 512 to 4096
+// positions, 16 rows: 2, 5, 9 bf16 102.5, 103.9, 105.6 us; E4M3 68.5, 64.1,
+// 66.9 on lengths of 500 to 4096).
+__host__ __device__ constexpr int unit_cost(bool f8) { return f8 ? 5 : 3; }
 constexpr int kMinSteps = 4;               // steps per block, at least
 // Units of at most this many steps are not split where each has a block: 4
 // requests of 4 tokens, 8 KV heads, GPU time of whole units against shares
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const MultiArgs a) {
     using G = Geo<D, F8>;
-    constexpr int kStages = G::kStages;
+    constexpr int kStages = G::kStages, kUnitCost = unit_cost(F8);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* qsm = ring + G::kRingBytes;                          // [kRows][kQStride]
@@ -555,10 +558,10 @@ int sms() {
 // Whether the units of 64 (or 128) rows of pa_decode_wide.cu serve a call:
 // from more than 16 rows a KV head on, where they read the cache once and
 // units of 16 twice.  8 KV heads of 128, us here against there:
-//   sequences x positions   bf16, 16 rows   20 or 32      E4M3, 16     20 or 32
-//   64 x 4096               167 / 161       317 / 161     98 / 104     179 / 104
+//   sequences x positions   bf16, 16 rows   32 rows       E4M3, 16     32 rows
+//   64 x 4096               167 / 161       319 / 163     98 / 104     180 / 104
 //   512 x 500               172 / 168       349 / 176     127 / 152    242 / 154
-//   2048 x 60               202 / 353       @@
+//   2048 x 60               200 / 341       -             210 / 469    -
 // (At 16 rows short contexts decide: a unit there costs some 3 to 4 us.)
 // Its bf16 products take a positive scale only; others go 16 rows at a time.
 bool is_wide(bool f8, float scale, long long rows) { return rows > kRows && (f8 || scale > 0.f); }
@@ -625,7 +628,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     const long long cap = (long long)max_blocks_per_seq * block_size;
     a.ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
     // no more blocks than the largest possible work has smallest shares
-    const int step = wide ? kWideStep : kStep, cost = wide ? kWideCost : kUnitCost;
+    const int step = wide ? kWideStep : kStep, cost = wide ? kWideCost : unit_cost(f8);
     const long long tiles = (all_rows + unit - 1) / unit;
     const long long seq_work = ((long long)a.ctx_cap + step - 1) / step + cost;
     const double work = (double)num_seqs * n_kv_heads * (double)tiles * (double)seq_work;
