@@ -19,7 +19,6 @@ constexpr float kNone = -3.0e38f;          // a row's maximum before it has seen
 constexpr float kRaise = 8.0f;             // log2 of the largest weight before the maximum is raised
 constexpr int kMaxProbes = 2000000;        // ~2 s bound on any single wait
 constexpr int kMergeThreads = 256;
-constexpr int kMergeSplit = 4;             // blocks per unit to merge
 
 struct MultiArgs {
     void* out;
@@ -335,30 +334,24 @@ __device__ __noinline__ void add_unfinite(const MultiArgs& a, int s, int kvh, in
 
 // out of the units that several blocks share: the pieces of block b, which
 // begins the unit (its second slot), and of blocks b + 1 .. last (their
-// first), in that order.
-template <int D>
+// first).  kMergeThreads / kItems threads take four columns of a row and share
+// its pieces.
+template <int D, int kItems>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a, int rows) {
+    constexpr int kStep = kMergeThreads / kItems;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int4 p = a.pieces[blockIdx.x];
     if (p.x < 0) return;
-    const int G = 1 << a.log2_group;
+    const int G = 1 << a.log2_group, mine = kStep > 1 ? threadIdx.x / kItems : 0;
+    const int pieces = p.w - blockIdx.x + 1;                     // two at least
 #pragma unroll 1
-    for (int x = blockIdx.y * kMergeThreads + threadIdx.x; x < rows * (D / 4); x += kMergeSplit * kMergeThreads) {
-        const int r = x / (D / 4), d = x % (D / 4) * 4;
-        const int i = r >> a.log2_group;
-        if (i >= p.y) return;
-        // a unit has two pieces at least: the first two are loaded together
-        int at = (2 * blockIdx.x + 1) * rows + r;
-        const float* u = a.part_u + (size_t)at * D + d;
-        float M = a.part_m[at], Z = a.part_z[at];
-        float4 U = *reinterpret_cast<const float4*>(u);
-        at += rows;
-        u += (size_t)rows * D;
-        float m = a.part_m[at], z = a.part_z[at];
-        float4 v = *reinterpret_cast<const float4*>(u);
-#pragma unroll 1
-        for (int b = blockIdx.x + 1;;) {
+    for (int x = blockIdx.y * kItems + threadIdx.x % kItems; x < rows * (D / 4); x += gridDim.y * kItems) {
+        const int r = x / (D / 4), d = x % (D / 4) * 4, i = r >> a.log2_group;
+        const bool there = i < p.y;
+        float M = kNone, Z = 0.f;
+        float4 U = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float m, float z, float4 v) {
             const float top = fmaxf(M, m);
             const float f = pa::exp2_approx(M - top), h = pa::exp2_approx(m - top);
             Z = Z * f + z * h;
@@ -367,16 +360,40 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
             U.z = U.z * f + v.z * h;
             U.w = U.w * f + v.w * h;
             M = top;
-            if (++b > p.w) break;
-            at += 2 * rows;                                      // (the first slot of the next block)
-            u += (size_t)2 * rows * D;
-            m = a.part_m[at];
-            z = a.part_z[at];
-            v = *reinterpret_cast<const float4*>(u);
+        };
+        if (there) {
+            // two pieces' loads together; a piece's slot is the first of its block's two but for the first piece
+#pragma unroll 1
+            for (int k = mine; k < pieces; k += 2 * kStep) {
+                const int then = min(k + kStep, pieces - 1);
+                const int at = (2 * ((int)blockIdx.x + k) + (k == 0)) * rows + r;
+                const int next = (2 * ((int)blockIdx.x + then) + (then == 0)) * rows + r;
+                const float m0 = a.part_m[at], m1 = a.part_m[next], z0 = a.part_z[at], z1 = a.part_z[next];
+                const float4 v0 = *reinterpret_cast<const float4*>(a.part_u + (size_t)at * D + d);
+                const float4 v1 = *reinterpret_cast<const float4*>(a.part_u + (size_t)next * D + d);
+                add(m0, z0, v0);
+                if (k + kStep < pieces) add(m1, z1, v1);
+            }
         }
-        const float f = Z == 0.f ? 0.f : a.v_scale / Z;
-        put4(a.out, a.out_f32, ((size_t)(p.x + i) * a.n_q_heads + p.z * G + (r & (G - 1))) * D + d,
-             make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
+        if constexpr (kStep > 1) {
+            __shared__ float4 sums[kMergeThreads];
+            __shared__ float2 stats[kMergeThreads];
+            sums[threadIdx.x] = U;
+            stats[threadIdx.x] = make_float2(M, Z);
+            __syncthreads();
+            if (mine == 0)
+#pragma unroll
+                for (int k = 1; k < kStep; ++k) {
+                    const float2 e = stats[k * kItems + threadIdx.x];
+                    add(e.x, e.y, sums[k * kItems + threadIdx.x]);
+                }
+            __syncthreads();
+        }
+        if (mine == 0 && there) {
+            const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+            put4(a.out, a.out_f32, ((size_t)(p.x + i) * a.n_q_heads + p.z * G + (r & (G - 1))) * D + d,
+                 make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
+        }
     }
 }
 

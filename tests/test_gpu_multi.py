@@ -534,3 +534,19 @@ def test_a_call_without_a_workspace_takes_one_of_its_own():
         torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(0xFF)
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int32), want.view(torch.int32))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("Hkv,G,D,B,ctxs,news", [
+    (1, 4, 128, 16, [30001], [4]),                            # one head's keys over every SM: hundreds of pieces
+    (1, 8, 128, 16, [20005], [9]),                            # the same in units of 64 rows
+    (1, 16, 128, 32, [20001], [9]),                           # and of 128 (E4M3: three of 64)
+    (2, 4, 128, 8, [1150, 193, 16], [4, 3, 1]),               # twelve warps, whole units
+    (2, 2, 64, 16, [1500, 129, 700], [3, 1, 8]),              # twelve warps, shares
+    (3, 2, 128, 32, [1153, 1152, 200], [2, 2, 2]),            # a step past what is not split
+])
+def test_few_units_of_long_contexts(Hkv, G, D, B, ctxs, news, fp8):
+    if fp8 and D != 128:
+        D = 128
+    p = _problem(24, G * Hkv, Hkv, D, B, ctxs, news, fp8=fp8, gap=1)
+    _check(p, _run(p, G * Hkv, Hkv, D, B, max(news), fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
