@@ -390,61 +390,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* empty = is_k ? ctl->k_empty : ctl->v_empty;
         const CUtensorMap* map = is_k ? &map_k : &map_v;
         const uint64_t policy = pa::l2_evict_first_policy();
-        int loaded = 0, nth = 0;                                 // tiles and units so far
-        bool ok = true;
-#pragma unroll 1
-        for (; ok; ++nth) {
+        const int sub = lane >> log2_blocks, place = (lane & (blocks - 1)) * B;
+        constexpr int kNoBlock = -2147483647 - 1;
+        // A unit, and the table entries of its first tiles on their way.
+        struct Next {
+            int valid, len, ctx, st0, kvh, token, first;
+            const int32_t* table;
+        };
+        auto fetch = [&](const Next& x, int j) {                 // tiles j .. j + per - 1
+            const int pos = (x.st0 + j + sub) * kKv + place;
+            return (j + sub < x.len && pos < x.ctx) ? x.table[pos >> a.log2_block] : kNoBlock;
+        };
+        auto take = [&](int nth, Next& x) {                      // K's warp posts it, V's waits for it
             const int slot = nth % kUnits;
             Unit* u = &ctl->units[slot];
             if (is_k) {
-                if (nth >= kUnits && !wait_for(&ctl->unit_empty[slot], (nth / kUnits - 1) & 1, ctl, a.status)) break;
+                if (nth >= kUnits && !wait_for(&ctl->unit_empty[slot], (nth / kUnits - 1) & 1, ctl, a.status)) return false;
                 if (lane == 0) {
                     next_unit<kRows, kKv, kWideCost>(ctl->walk, *u, a);
                     if (u->valid && u->st0 == 0 && u->len != u->steps)       // this block begins a unit that others end
                         a.pieces[blockIdx.x] = begun_unit(*u, a.log2_group);
-                    pa::mbar_arrive(&ctl->unit_full[slot]);
                 }
                 __syncwarp();
-                if (!u->valid) break;
-            } else {
-                if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) break;
-                if (!u->valid) break;
-                if constexpr (!F8) {
-                    if (nth >= 1 && !(ok = wait_for(ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
-                    if (lane == 0) {
-                        // 16 rows a box: 16 / group tokens of the group's heads
-                        pa::mbar_arrive_expect_tx(ctl->q_full, kRows * 128 * G::kHalves);
+            } else if (!wait_for(&ctl->unit_full[slot], (nth / kUnits) & 1, ctl, a.status)) {
+                return false;
+            }
+            x.valid = u->valid;
+            x.len = u->len;
+            x.ctx = u->ctx;
+            x.st0 = u->st0;
+            x.kvh = u->kvh;
+            x.table = u->table;
+            x.token = u->q0 + (u->row0 >> a.log2_group);
+            __syncwarp();
+            if (lane == 0) pa::mbar_arrive(is_k ? &ctl->unit_full[slot] : &ctl->unit_empty[slot]);
+            if (x.valid) x.first = fetch(x, 0);
+            return true;
+        };
+        int loaded = 0, nth = 0;                                 // tiles and units so far
+        Next now, next;
+        bool ok = take(0, now);
 #pragma unroll 1
-                        for (int r = 0; r < kRows; r += 16) {
+        for (; ok && now.valid; ++nth) {
+            if (!F8 && !is_k) {
+                if (nth >= 1 && !(ok = wait_for(ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
+                if (lane == 0) {
+                    // 16 rows a box: 16 / group tokens of the group's heads
+                    pa::mbar_arrive_expect_tx(ctl->q_full, kRows * 128 * G::kHalves);
+#pragma unroll 1
+                    for (int r = 0; r < kRows; r += 16) {
 #pragma unroll
-                            for (int h = 0; h < G::kHalves; ++h)
-                                tma_q(s0 + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
-                                      u->kvh << a.log2_group, u->q0 + ((u->row0 + r) >> a.log2_group), ctl->q_full);
-                        }
+                        for (int h = 0; h < G::kHalves; ++h)
+                            tma_q(s0 + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
+                                  now.kvh << a.log2_group, now.token + (r >> a.log2_group), ctl->q_full);
                     }
                 }
             }
-            const int len = u->len, ctx = u->ctx, st0 = u->st0, kvh = u->kvh;
-            const int32_t* table = u->table;
-            if (!is_k) {
-                __syncwarp();
-                if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
-            }
-            const int sub = lane >> log2_blocks, place = (lane & (blocks - 1)) * B;
-            constexpr int kNoBlock = -2147483647 - 1;
-            auto fetch = [&](int j) {                            // tiles j .. j + per - 1
-                const int pos = (st0 + j + sub) * kKv + place;
-                return (j + sub < len && pos < ctx) ? table[pos >> a.log2_block] : kNoBlock;
-            };
-            int row = 0, ahead = fetch(0);
+            // the unit after it, so that its first table entries come beside this one's tiles
+            ok = take(nth + 1, next);
+            int row = 0, ahead = now.first;
 #pragma unroll 1
-            for (int j = 0; j < len; ++j, ++loaded) {
+            for (int j = 0; ok && j < now.len; ++j, ++loaded) {
                 const int turn = j & (per - 1), st = loaded % kStages;
                 if (turn == 0) {
                     row = oob_row;
-                    if (ahead >= 0 && ahead < a.num_blocks) row = (ahead * a.n_kv_heads + kvh) * B;
+                    if (ahead >= 0 && ahead < a.num_blocks) row = (ahead * a.n_kv_heads + now.kvh) * B;
                     else if (ahead != kNoBlock) flag(a.status, PA_DEV_BAD_BLOCK_ID);
-                    ahead = fetch(j + per);
+                    ahead = fetch(now, j + per);
                 }
                 if (loaded >= kStages && !(ok = wait_for(&empty[st], (loaded / kStages - 1) & 1, ctl, a.status))) break;
                 if (lane == 0) pa::mbar_arrive_expect_tx(&full[st], G::kTileBytes);
@@ -456,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pa::tma_box(dst + h * G::kHalfBytes, map, h * 64, row, &full[st], policy);
                 }
             }
+            now = next;
         }
         // the copies this warp started land before the block exits
         if (lane == 0) {

@@ -98,8 +98,8 @@ __device__ __forceinline__ int4 begun_unit(const Unit& u, int log2_group) {
 
 // A block's share of the work, walked unit by unit.
 struct Walk {
-    long long pos, end, off, share;        // off: work of the sequence before pos
-    int seq;
+    long long pos, left, share;            // work of the batch before here, and of this share from here on
+    int seq, unit, gone;                   // the sequence's unit, and how much of its work is before here
     Seq sq;
 };
 
@@ -107,25 +107,28 @@ struct Walk {
 template <int kRows, int kStep, int kUnitCost>
 __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
     u.valid = 0;
-    while (w.pos < w.end) {
-        while (w.off >= w.sq.work(a.n_kv_heads, kUnitCost)) {
-            w.off -= w.sq.work(a.n_kv_heads, kUnitCost);
+    while (w.left > 0) {
+        if (w.unit >= a.n_kv_heads * w.sq.tiles) {
+            w.unit = 0;
             w.sq = read_seq<kRows, kStep>(a, ++w.seq, false);
+            continue;
         }
-        const int per = w.sq.steps + kUnitCost;
-        const int unit = (int)(w.off / per), o = (int)(w.off - (long long)unit * per);
-        const int take = (int)min((long long)(per - o), w.end - w.pos);
+        const int per = w.sq.steps + kUnitCost, o = w.gone, unit = w.unit;
+        const int take = (int)min((long long)(per - o), w.left);
         const int lo = max(0, o - kUnitCost), hi = max(0, o + take - kUnitCost);
-        u.last = (int)((w.pos - o + per - 1) / w.share);
+        const bool ends = o + take == per;
+        u.last = ends ? 0 : (int)((w.pos - o + per - 1) / w.share);   // (of a unit that another block ends)
         w.pos += take;
-        w.off += take;
+        w.left -= take;
+        w.gone = ends ? 0 : o + take;
+        w.unit += ends;
         if (hi == lo) continue;            // the share ends within the unit's constant part
         u.q0 = w.sq.q0;
         u.n = w.sq.n;
         u.ctx = w.sq.ctx;
         u.first = w.sq.ctx - w.sq.n;
         u.steps = w.sq.steps;
-        u.kvh = unit / w.sq.tiles;
+        u.kvh = w.sq.tiles == 1 ? unit : unit / w.sq.tiles;
         u.row0 = (unit - u.kvh * w.sq.tiles) * kRows;
         u.st0 = lo;
         u.len = hi - lo;
@@ -141,10 +144,10 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
 template <int kUnitCost>
 __device__ __forceinline__ void one_unit(Walk& walk, const Seq& sq, int s, int unit) {
     walk.pos = 0;
-    walk.end = sq.steps + kUnitCost;
-    walk.off = unit * walk.end;
-    walk.share = walk.end;
+    walk.left = walk.share = sq.steps + kUnitCost;
     walk.seq = s;
+    walk.unit = unit;
+    walk.gone = 0;
     walk.sq = sq;
 }
 
@@ -241,11 +244,13 @@ __device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, Part*
             off -= sq.work(heads, kUnitCost);
             sq = read_seq<kRows, kStep>(a, ++s, false);
         }
+        const int per = sq.steps + kUnitCost;
         walk.pos = begin;
-        walk.end = min(all.work, begin + share);
-        walk.off = off;
+        walk.left = min(all.work, begin + share) - begin;
         walk.share = share;
         walk.seq = s;
+        walk.unit = (int)(off / per);
+        walk.gone = (int)(off - (long long)walk.unit * per);
         walk.sq = sq;
     }
     __syncthreads();
