@@ -89,11 +89,11 @@ struct Geo {
     static_assert(kJoinStages * kStageBytes == 4 * kRows * D, "a unit's states fill the join stages");
 };
 
-__device__ __forceinline__ bool visible(const Unit& u, int log2_group, int row, int pos) {
+__device__ __forceinline__ bool visible(const MultiArgs& a, const Unit& u, int row, int pos) {
     if (pos >= u.ctx) return false;
     if (pos < u.first) return true;
-    const int i = (u.row0 + row) >> log2_group;
-    return i >= u.n || sees(u.words, i, pos - u.first);      // a row that is not there: any finite result will do
+    const int i = (u.row0 + row) >> a.log2_group;
+    return i >= u.n || sees(words_of(a, u), i, pos - u.first);      // a row that is not there: any finite result will do
 }
 
 // One warp's running state: rows g and g + 8.
@@ -113,8 +113,8 @@ struct State {
 // into the warp's state.  qr: the rows of q as A operands; c[h]: score factor
 // of rows g + 8 h.
 template <int D, bool F8>
-__device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const Unit& u,
-                                          int log2_group, int lane, const uint32_t (&qr)[D / 16][4]) {
+__device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const MultiArgs& a,
+                                          const Unit& u, int lane, const uint32_t (&qr)[D / 16][4]) {
     constexpr int kSlabBytes = kTile * 128, kSteps = D / 16;
     const int g = lane >> 2, t4 = lane & 3;
     // ldmatrix addresses.  K as B operand: keys (lane & 7) + 8 (lane >> 4), chunk + (lane >> 3 & 1);
@@ -152,7 +152,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (!visible(u, log2_group, g + 8 * (e >> 1), t0 + 8 * n + 2 * t4 + (e & 1))) s[n][e] = -INFINITY;
+                if (!visible(a, u, g + 8 * (e >> 1), t0 + 8 * n + 2 * t4 + (e & 1))) s[n][e] = -INFINITY;
     }
     // how far the tile's scores rise above the running maxima
     float over = -INFINITY;
@@ -293,8 +293,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
         e0 = e1 = 0;
         const int t0 = (u.st0 + k) * kStep + warp * kTile;
         if (k < u.len && t0 < u.ctx) {
-            e0 = u.table[t0 >> a.log2_block];
-            if (B < kTile && t0 + B < u.ctx) e1 = u.table[(t0 >> a.log2_block) + 1];
+            const int32_t* table = table_of(a, u);
+            e0 = table[t0 >> a.log2_block];
+            if (B < kTile && t0 + B < u.ctx) e1 = table[(t0 >> a.log2_block) + 1];
         }
     };
     int e0 = 0, e1 = 0, f0 = 0, f1 = 0;
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
                         unfinite[nth & 1] = 1;
                     __syncwarp();
                 }
-                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, u, a.log2_group, lane, qr);
+                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, a, u, lane, qr);
             }
             __syncwarp();
             if (k + kStages < len) issue(u, k + kStages);
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
             }
         }
         __syncthreads();
-        const bool whole = len == u.steps;
+        const bool whole = u.whole;
         const int slot = 2 * blockIdx.x + (u.st0 == 0 ? 1 : 0);
 #pragma unroll 1
         for (int x = threadIdx.x; x < kRows * (D / 4); x += kThreads) {

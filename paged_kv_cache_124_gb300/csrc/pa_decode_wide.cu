@@ -60,7 +60,7 @@ constexpr int kThreads = 576;
 // warps 11 and 16 issue the value products of groups 0 and 1
 __device__ __forceinline__ int value_group(int warp) { return warp == 11 ? 0 : warp == 16 ? 1 : -1; }
 constexpr int kHalfKv = kKv / 2;           // positions of a tile per group
-constexpr int kUnits = 4;                  // units posted ahead
+constexpr int kUnits = 8;                  // units posted ahead
 constexpr int kUnitReaders = 17;           // warps that read a posted unit
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
@@ -75,9 +75,11 @@ struct Wide {
     static constexpr int kHalfBytes = 128 * 128;                 // 128 rows of 128 bytes, 128-byte swizzle
     static constexpr int kTileBytes = kHalves * kHalfBytes;      // K or V of a tile
     static constexpr int kQBytes = kTileBytes;                   // F8: a row's two terms in its two lanes
-    static constexpr int kQBuffers = F8 ? 2 : 1;
+    // Buffers of q, and from one to the next; 64-row units of bf16: in the other 16 lines of each 32.
+    static constexpr int kQBuffers = kHalf ? 2 : 1;
+    static constexpr int kQNext = F8 ? kQBytes : 16 * 128;
     static constexpr int kStages = F8 || D == 64 ? 6 : 3;
-    static constexpr int kK0 = kQBuffers * kQBytes;
+    static constexpr int kK0 = F8 ? 2 * kQBytes : kQBytes;
     static constexpr int kV0 = kK0 + kStages * kTileBytes;
     static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][row] maximum and sum; F8: then row factors
     static constexpr int kCtl = kStats + 2 * 128 * 8;
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nth >= kUnits && !wait_for(&ctl->unit_empty[slot], (nth / kUnits - 1) & 1, ctl, a.status)) return false;
                 if (lane == 0) {
                     next_unit<kRows, kKv, kWideCost>(ctl->walk, *u, a);
-                    if (u->valid && u->st0 == 0 && u->len != u->steps)       // this block begins a unit that others end
+                    if (u->valid && u->st0 == 0 && !u->whole)       // this block begins a unit that others end
                         a.pieces[blockIdx.x] = begun_unit(*u, a.log2_group);
                 }
                 __syncwarp();
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.ctx = u->ctx;
             x.st0 = u->st0;
             x.kvh = u->kvh;
-            x.table = u->table;
+            x.table = table_of(a, *u);
             x.token = u->q0 + (u->row0 >> a.log2_group);
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(is_k ? &ctl->unit_full[slot] : &ctl->unit_empty[slot]);
@@ -433,16 +435,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (; ok && now.valid; ++nth) {
             if (!F8 && !is_k) {
-                if (nth >= 1 && !(ok = wait_for(ctl->q_empty, (nth - 1) & 1, ctl, a.status))) break;
+                constexpr int kQ = G::kQBuffers;
+                const int qb = nth % kQ;
+                if (nth >= kQ && !(ok = wait_for(&ctl->q_empty[qb], (nth / kQ - 1) & 1, ctl, a.status))) break;
                 if (lane == 0) {
                     // 16 rows a box: 16 / group tokens of the group's heads
-                    pa::mbar_arrive_expect_tx(ctl->q_full, kRows * 128 * G::kHalves);
+                    pa::mbar_arrive_expect_tx(&ctl->q_full[qb], kRows * 128 * G::kHalves);
 #pragma unroll 1
                     for (int r = 0; r < kRows; r += 16) {
 #pragma unroll
                         for (int h = 0; h < G::kHalves; ++h)
-                            tma_q(s0 + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
-                                  now.kvh << a.log2_group, now.token + (r >> a.log2_group), ctl->q_full);
+                            tma_q(s0 + qb * G::kQNext + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
+                                  now.kvh << a.log2_group, now.token + (r >> a.log2_group), &ctl->q_full[qb]);
                     }
                 }
             }
@@ -472,7 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the copies this warp started land before the block exits
         if (lane == 0) {
-            if (!F8 && !is_k && nth > 0) pa::mbar_wait_bounded(ctl->q_full, (nth - 1) & 1, kMaxProbes);
+            if (!F8 && !is_k)
+#pragma unroll 1
+                for (int i = max(0, nth - G::kQBuffers); i < nth; ++i)
+                    pa::mbar_wait_bounded(&ctl->q_full[i % G::kQBuffers], (i / G::kQBuffers) & 1, kMaxProbes);
 #pragma unroll 1
             for (int i = 0; i < kStages && i < loaded; ++i)
                 pa::mbar_wait_bounded(&full[(loaded - 1 - i) % kStages], ((loaded - 1 - i) / kStages) & 1, kMaxProbes);
@@ -493,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!valid) break;
                 const int qb = nth % G::kQBuffers;
                 if (!wait_one(&ctl->q_full[qb], (nth / G::kQBuffers) & 1, ctl, a.status)) break;
-                const uint32_t q_lo = desc_lo(s0 + qb * G::kQBytes, 16);
+                const uint32_t q_lo = desc_lo(s0 + qb * G::kQNext, 16);
 #pragma unroll 1
                 for (int j = 0; j < len; ++j, ++at) {
                     const int b = at & 1;
@@ -650,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int len = u->len, first = u->first;
             const int start = u->st0 * kKv + w * kHalfKv + 32 * half;   // the thread's first position in the unit
             const int i = (u->row0 + r) >> a.log2_group;
-            const bool real = i < u->n, tree = u->words != nullptr;
+            const bool real = i < u->n, tree = a.tree_mask != nullptr;
             // what the row sees of the new tokens: a word (tree), or positions below `lim`
-            unsigned long long word = tree && real ? u->words[i] : ~0ull;
+            unsigned long long word = tree && real ? words_of(a, *u)[i] : ~0ull;
             if (u->n < 64) word &= (1ull << u->n) - 1;
             const int lim = (tree || !real) ? u->ctx : first + i + 1;
             __syncwarp();
@@ -893,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st0 = u->st0;
             const int seq = u->seq, kvh = u->kvh, end = st0 + u->len;
             const int row = u->row0 + r, i = row >> a.log2_group;
-            const bool real = i < u->n, whole = u->len == u->steps;
+            const bool real = i < u->n, whole = u->whole;
             const bool both = u->len > 1 || u->ctx - st0 * kKv > kHalfKv;   // group 1 had positions: O1 was written
             const size_t out_row = ((size_t)(u->q0 + i) * a.n_q_heads + (kvh << a.log2_group) + (row & (group - 1))) * D;
             __syncwarp();

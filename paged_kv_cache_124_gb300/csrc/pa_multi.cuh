@@ -81,12 +81,18 @@ __device__ __forceinline__ Seq read_seq(const MultiArgs& a, int s, bool flag) {
 
 // The stretch of one unit that a block computes: steps st0 .. st0 + len - 1.
 struct Unit {
-    int q0, n, ctx, first, steps;          // first: position of new token 0
-    int kvh, row0, st0, len, seq, last;    // last: the block that ends the unit
-    int valid;                             // 0: the share has ended
-    const uint64_t* words;                 // mask words of the sequence's tokens, or null
-    const int32_t* table;
+    int q0, n, ctx, first;                 // first: position of new token 0
+    int kvh, row0, st0, len, seq, last;    // last: the block that ends the unit, if this one does not
+    int whole, valid;                      // valid 0: the share has ended
 };
+
+// The mask words of a unit's tokens, or null, and its table.
+__device__ __forceinline__ const uint64_t* words_of(const MultiArgs& a, const Unit& u) {
+    return a.tree_mask ? a.tree_mask + u.q0 : nullptr;
+}
+__device__ __forceinline__ const int32_t* table_of(const MultiArgs& a, const Unit& u) {
+    return a.block_tables + (size_t)u.seq * a.max_blocks;
+}
 
 // What the merge needs of a unit: its first token, its tokens (the last tile's
 // may be fewer than its rows hold), KV head and last block.  (A unit's rows
@@ -127,14 +133,12 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
         u.n = w.sq.n;
         u.ctx = w.sq.ctx;
         u.first = w.sq.ctx - w.sq.n;
-        u.steps = w.sq.steps;
         u.kvh = w.sq.tiles == 1 ? unit : unit / w.sq.tiles;
         u.row0 = (unit - u.kvh * w.sq.tiles) * kRows;
         u.st0 = lo;
         u.len = hi - lo;
         u.seq = w.seq;
-        u.words = a.tree_mask ? a.tree_mask + w.sq.q0 : nullptr;
-        u.table = a.block_tables + (size_t)w.seq * a.max_blocks;
+        u.whole = u.len == w.sq.steps;
         u.valid = 1;
         return;
     }
