@@ -14,10 +14,10 @@
 //
 // What bounds it: each K/V byte is read once for n * G rows, 4 * n * G
 // operations per two bytes, so the cache's bytes bound it.  64 sequences of
-// 4096 positions, 8 KV heads of 128, 16 rows: 167 us, 0.95 of the measured
-// copy rate; E4M3 98 us, 0.81 (there the unpacking of codes to f16 for
+// 4096 positions, 8 KV heads of 128, 16 rows: 168 us, 0.94 of the measured
+// copy rate; E4M3 97 us, 0.82 (there the unpacking of codes to f16 for
 // warp-level products takes 44 % of the ALU's cycles).  The smallest steps
-// are a chain of latencies: 4 sequences of up to 37 positions take 5.3 us.
+// are a chain of latencies: 4 sequences of up to 37 positions take 4.7 us.
 //  * A unit is a (sequence, KV head, tile of 16 rows); its work is counted in
 //    steps of a block's positions plus a constant for starting and joining
 //    it.  The grid is the resident blocks, and they take equal contiguous

@@ -7,9 +7,9 @@
 // d_head 128) takes an SM about 1.46 us of its share of the memory's rate,
 // and its products, S = Q . K^T and O += P . V at 128 rows, 0.33 us each: the
 // bytes bound it as long as copies, products and softmax overlap.  64
-// sequences of 4096 positions, 8 KV heads of 128: 32 rows 163 us (0.98 of the
-// measured copy rate), 64 rows 168 (0.96), 128 rows 182 (0.90; 750 TFLOP/s).
-// E4M3: 32 rows 104 us (0.77), bound by the softmax, whose conversions to
+// sequences of 4096 positions, 8 KV heads of 128: 32 rows 166 us (0.96 of the
+// measured copy rate), 64 rows 171 (0.94), 128 rows 178 (0.91; 767 TFLOP/s).
+// E4M3: 32 rows 105 us (0.76), bound by the softmax, whose conversions to
 // three E4M3 terms take half of the ALU's cycles and some 1650 of a tile's.
 // (Two terms, a relative 2^-9, were 97 us: not worth the weights' precision.)
 //  * One block per SM walks its share.  A producer warp each fills stages of
@@ -60,7 +60,7 @@ constexpr int kThreads = 576;
 // warps 11 and 16 issue the value products of groups 0 and 1
 __device__ __forceinline__ int value_group(int warp) { return warp == 11 ? 0 : warp == 16 ? 1 : -1; }
 constexpr int kHalfKv = kKv / 2;           // positions of a tile per group
-constexpr int kUnits = 8;                  // units posted ahead
+constexpr int kUnits = 4;                  // units posted ahead
 constexpr int kUnitReaders = 17;           // warps that read a posted unit
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;           // S0 at 0, S1 at 128, O0 and O1 from here
@@ -75,11 +75,9 @@ struct Wide {
     static constexpr int kHalfBytes = 128 * 128;                 // 128 rows of 128 bytes, 128-byte swizzle
     static constexpr int kTileBytes = kHalves * kHalfBytes;      // K or V of a tile
     static constexpr int kQBytes = kTileBytes;                   // F8: a row's two terms in its two lanes
-    // Buffers of q, and from one to the next; 64-row units of bf16: in the other 16 lines of each 32.
-    static constexpr int kQBuffers = kHalf ? 2 : 1;
-    static constexpr int kQNext = F8 ? kQBytes : 16 * 128;
+    static constexpr int kQBuffers = F8 ? 2 : 1;
     static constexpr int kStages = F8 || D == 64 ? 6 : 3;
-    static constexpr int kK0 = F8 ? 2 * kQBytes : kQBytes;
+    static constexpr int kK0 = kQBuffers * kQBytes;
     static constexpr int kV0 = kK0 + kStages * kTileBytes;
     static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][row] maximum and sum; F8: then row factors
     static constexpr int kCtl = kStats + 2 * 128 * 8;
@@ -429,29 +427,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.valid) x.first = fetch(x, 0);
             return true;
         };
-        int loaded = 0, nth = 0;                                 // tiles and units so far
+        int loaded = 0, asked = 0;                               // tiles so far, and units' q
         Next now, next;
-        bool ok = take(0, now);
+        bool ok = true;
 #pragma unroll 1
-        for (; ok && now.valid; ++nth) {
-            if (!F8 && !is_k) {
-                constexpr int kQ = G::kQBuffers;
-                const int qb = nth % kQ;
-                if (nth >= kQ && !(ok = wait_for(&ctl->q_empty[qb], (nth / kQ - 1) & 1, ctl, a.status))) break;
+        for (int nth = -1; ok; ++nth) {
+            if (nth >= 0 && !now.valid) break;
+            if (!F8 && !is_k && nth >= 0) {
+                if (nth >= 1 && !wait_for(ctl->q_empty, (nth - 1) & 1, ctl, a.status)) break;
                 if (lane == 0) {
                     // 16 rows a box: 16 / group tokens of the group's heads
-                    pa::mbar_arrive_expect_tx(&ctl->q_full[qb], kRows * 128 * G::kHalves);
+                    pa::mbar_arrive_expect_tx(ctl->q_full, kRows * 128 * G::kHalves);
 #pragma unroll 1
                     for (int r = 0; r < kRows; r += 16) {
 #pragma unroll
                         for (int h = 0; h < G::kHalves; ++h)
-                            tma_q(s0 + qb * G::kQNext + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
-                                  now.kvh << a.log2_group, now.token + (r >> a.log2_group), &ctl->q_full[qb]);
+                            tma_q(s0 + h * G::kHalfBytes + (kHalf ? 2 * r : r) * 128, &map_q, h * 64,
+                                  now.kvh << a.log2_group, now.token + (r >> a.log2_group), ctl->q_full);
                     }
                 }
+                ++asked;
             }
             // the unit after it, so that its first table entries come beside this one's tiles
-            ok = take(nth + 1, next);
+            if (!take(nth + 1, next)) break;
+            if (nth < 0) {
+                now = next;
+                continue;
+            }
             int row = 0, ahead = now.first;
 #pragma unroll 1
             for (int j = 0; ok && j < now.len; ++j, ++loaded) {
@@ -476,10 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the copies this warp started land before the block exits
         if (lane == 0) {
-            if (!F8 && !is_k)
-#pragma unroll 1
-                for (int i = max(0, nth - G::kQBuffers); i < nth; ++i)
-                    pa::mbar_wait_bounded(&ctl->q_full[i % G::kQBuffers], (i / G::kQBuffers) & 1, kMaxProbes);
+            if (asked > 0) pa::mbar_wait_bounded(ctl->q_full, (asked - 1) & 1, kMaxProbes);
 #pragma unroll 1
             for (int i = 0; i < kStages && i < loaded; ++i)
                 pa::mbar_wait_bounded(&full[(loaded - 1 - i) % kStages], ((loaded - 1 - i) / kStages) & 1, kMaxProbes);
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!valid) break;
                 const int qb = nth % G::kQBuffers;
                 if (!wait_one(&ctl->q_full[qb], (nth / G::kQBuffers) & 1, ctl, a.status)) break;
-                const uint32_t q_lo = desc_lo(s0 + qb * G::kQNext, 16);
+                const uint32_t q_lo = desc_lo(s0 + qb * G::kQBytes, 16);
 #pragma unroll 1
                 for (int j = 0; j < len; ++j, ++at) {
                     const int b = at & 1;

@@ -104,7 +104,7 @@ __device__ __forceinline__ int4 begun_unit(const Unit& u, int log2_group) {
 
 // A block's share of the work, walked unit by unit.
 struct Walk {
-    long long pos, left, share;            // work of the batch before here, and of this share from here on
+    long long left, share;                 // work of this share from here on, and of a whole one
     int seq, unit, gone;                   // the sequence's unit, and how much of its work is before here
     Seq sq;
 };
@@ -123,8 +123,9 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
         const int take = (int)min((long long)(per - o), w.left);
         const int lo = max(0, o - kUnitCost), hi = max(0, o + take - kUnitCost);
         const bool ends = o + take == per;
-        u.last = ends ? 0 : (int)((w.pos - o + per - 1) / w.share);   // (of a unit that another block ends)
-        w.pos += take;
+        // a unit that goes on behind this share: the blocks from here to its end
+        const unsigned rest = per - o - take, share = (unsigned)min(w.share, 1ll << 30);
+        u.last = blockIdx.x + (rest ? (rest + share - 1) / share : 0);
         w.left -= take;
         w.gone = ends ? 0 : o + take;
         w.unit += ends;
@@ -147,7 +148,6 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
 // The walk of one whole unit: `unit` of sequence s.
 template <int kUnitCost>
 __device__ __forceinline__ void one_unit(Walk& walk, const Seq& sq, int s, int unit) {
-    walk.pos = 0;
     walk.left = walk.share = sq.steps + kUnitCost;
     walk.seq = s;
     walk.unit = unit;
@@ -249,7 +249,6 @@ __device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, Part*
             sq = read_seq<kRows, kStep>(a, ++s, false);
         }
         const int per = sq.steps + kUnitCost;
-        walk.pos = begin;
         walk.left = min(all.work, begin + share) - begin;
         walk.share = share;
         walk.seq = s;
