@@ -9,9 +9,8 @@
 // bytes bound it as long as copies, products and softmax overlap.  64
 // sequences of 4096 positions, 8 KV heads of 128: 32 rows 166 us (0.96 of the
 // measured copy rate), 64 rows 171 (0.94), 128 rows 178 (0.91; 767 TFLOP/s).
-// E4M3: 32 rows 105 us (0.76), bound by the softmax, whose conversions to
-// three E4M3 terms take half of the ALU's cycles and some 1650 of a tile's.
-// (Two terms, a relative 2^-9, were 97 us: not worth the weights' precision.)
+// E4M3: 32 rows @@ us (@@), bound by the softmax, whose conversions to four
+// terms take half of the ALU's cycles and some @@ of a tile's.
 //  * One block per SM walks its share.  A producer warp each fills stages of
 //    K and V through the block table; one warp issues the score products of
 //    whole tiles, into two buffers in turn; two groups of four warps take the
@@ -38,7 +37,7 @@
 //    read by two threads.  Units of 128 rows take two products.
 //  * E4M3: the codes are operands as they lie in the cache.  q is the exact
 //    sum of two E4M3 terms, in a row's two lanes, whose scores the softmax
-//    adds; weights are three E4M3 terms in two products.
+//    adds; weights are four E5M2 terms in two products.
 //  * A warp of its own zeroes V rows past the context (0 * NaN) in shared
 //    memory, and new positions' values that are not finite, which the rows
 //    that see them add at the unit's end.
@@ -118,9 +117,10 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-// fp32 accumulator, A K-major, B K-major or (b_mn) MN-major; A and B bf16 (kind::f16) or E4M3 (kind::f8f6f4).
-__host__ __device__ constexpr uint32_t idesc(bool f8, int m, int n, int b_mn) {
-    return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+// fp32 accumulator, A K-major, B K-major or (b_mn) MN-major; A and B bf16 (kind::f16), or B E4M3 and A E4M3 or
+// (a_e5m2) E5M2 (kind::f8f6f4, whose operands may differ).
+__host__ __device__ constexpr uint32_t idesc(bool f8, int m, int n, int b_mn, bool a_e5m2 = false) {
+    return (1u << 4) | (f8 ? (a_e5m2 ? 1u << 7 : 0u) : (1u << 7) | (1u << 10)) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
 
@@ -144,7 +144,7 @@ __device__ __forceinline__ void mma_ss_add(uint32_t d, uint32_t a, uint32_t b, u
     if constexpr (F8) PA_MMA_ADD("f8f6f4", "x", "mov.b64 x, {%1, %4};\n\t");
     else PA_MMA_ADD("f16", "x", "mov.b64 x, {%1, %4};\n\t");
 }
-// A operand from tensor memory: rows in lanes, two bf16 or four E4M3 values per column.
+// A operand from tensor memory: rows in lanes, two bf16 or four E5M2 values per column.
 template <bool F8>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     if constexpr (F8) PA_MMA("f8f6f4", "[%1]", "");
@@ -238,12 +238,7 @@ __device__ __forceinline__ void st8_split8(uint32_t t, const uint32_t* w) {
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]));
 }
 
-// f16 pairs to E4M3 code pairs (round to nearest, saturating) and back (exact).
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-    return r;
-}
+// E4M3 code pairs as f16 pairs, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
@@ -530,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (value_group(warp) >= 0) {
         // ------------------------------------------------------------ value products of group w
-        constexpr uint32_t id = idesc(F8, 128, D, 1);
+        constexpr uint32_t id = idesc(F8, 128, D, 1, F8);
         constexpr int kStepKeys = G::kStepKeys, kSteps = kHalfKv / kStepKeys, kSets = F8 || !kHalf ? 2 : 1;
         const int w = value_group(warp);
         const uint32_t t_o = tmem + kTmemO + w * 128;
@@ -640,10 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kCols = kHalf ? 32 : 64;                   // columns per thread
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16), t_o = t_lane + kTmemO + w * 128;
         const float* factors = reinterpret_cast<const float*>(stats + 128);   // F8: [unit parity][row]
-        constexpr float kSlack = F8 ? 0.5f : kRaise;             // F8: weights of at most 2^8.5 in E4M3's 448
+        constexpr float kSlack = F8 ? 0.5f : kRaise;             // F8: weights of at most 2^15.5 in E5M2's 57344
         constexpr float kHeadroom = F8 ? 3.f : 0.f;              // F8: a raise leaves room for the next ones (a raise
                                                                  // at every growth cost 560 cycles in half the tiles)
-        constexpr float kUp = F8 ? 8.f : 0.f;                    // log2 of the weights' common factor
+        constexpr float kUp = F8 ? 15.f : 0.f;                   // log2 of the weights' common factor
         constexpr uint32_t kLanes16 = 16u << 16;
         int at = 0;                                              // tiles so far
         bool ok = true;
@@ -752,32 +747,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return p;
                 };
                 if constexpr (F8) {
-                    // Weights as f16 (11 significant bits) and then as three E4M3 terms of 4 bits each, which
-                    // hold them within 2^-10 (at most 2^-15 of the row's largest): the first two in a
-                    // product's two lanes of a row, the third in a second product's, whose other lane is zero.
-                    uint32_t t[3][8];
+                    // Weights as f16 (a relative 2^-11), exactly the sum of four E5M2 terms: an f16's upper byte is
+                    // its E5M2 value cut off, and so is what that leaves, down to 2^-16 (2^-28 of the row's
+                    // largest).  (E4M3 ends at 2^-9, which would lose weights below 2^-14, and a long tail of such
+                    // can be most of a row's sum.)  Two and two terms in a product's two lanes of a row.
+                    uint32_t t[4][8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        t[0][k] = t[1][k] = t[2][k] = 0;
+                        uint32_t h[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float p0, p1;
                             split(weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], e), p0, p1);
-                            uint32_t h = pa::pack_f16x2(p0, p1);
+                            h[e] = pa::pack_f16x2(p0, p1);
+                        }
 #pragma unroll
-                            for (int x = 0; x < 3; ++x) {
-                                // the top 4 bits (a NaN keeps being one), then the rest
-                                const uint32_t top4 = x < 2 ? h & 0xff80ff80u : h;
-                                t[x][k] |= f16x2_to_e4m3x2(top4) << (16 * e);
-                                if (x < 2) h = sub_f16x2(h, top4);
+                        for (int x = 0; x < 4; ++x) {
+                            t[x][k] = __byte_perm(h[0], h[1], 0x7531);
+                            if (x < 3) {
+                                h[0] = sub_f16x2(h[0], h[0] & 0xff00ff00u);
+                                h[1] = sub_f16x2(h[1], h[1] & 0xff00ff00u);
                             }
                         }
                     }
-                    const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     st8_split8(t_s, t[0]);
                     st8_split8(t_s + kLanes16, t[1]);
                     st8_split8(t_s + 16, t[2]);
-                    st8_split8(t_s + kLanes16 + 16, zero);
+                    st8_split8(t_s + kLanes16 + 16, t[3]);
                 } else {
                     // hi terms in the group's first 32 columns; lo terms in a row's second lane (64-row
                     // units) or in the other 32 columns

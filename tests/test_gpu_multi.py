@@ -69,7 +69,13 @@ def _check(p, out, Hq, Hkv, D, B, mask=None, fp8=False, scale=None, skip=()):
     a relative 2 (E + 128 * 2^-24) * (|q| . |k|) |scale| + W, E and W the
     operand roundings (bf16: q exact, weights in two terms, W 2^-16; E4M3: q
     and weights to f16, 2^-11 each), doubled as the normaliser moves too; an
-    output by that times sum a |v|; and half a step of the output's type."""
+    output by that times sum a |v|; and half a step of the output's type.
+    E4M3, besides: more than 16 rows take weights as E5M2 terms, scaled so that
+    a row's largest is 2^12 at least (2^15 with a headroom of 2^3) and cut off
+    at E5M2's smallest step, 2^-16: a weight may lose 2^-28 of the largest,
+    and, the normaliser being at least the largest, an output 2^-28 sum |v|.
+    (f16, up to 16 rows: the largest is 2^7 at least, half a step 2^-25:
+    2^-32.)"""
     q, kc, vc, tables, start, ctx = p
     scale = 1 / math.sqrt(D) if scale is None else scale
     kd, vd = (Q.dequantize(kc, K_SCALE), Q.dequantize(vc, V_SCALE)) if fp8 else (kc, vc)
@@ -83,12 +89,14 @@ def _check(p, out, Hq, Hkv, D, B, mask=None, fp8=False, scale=None, skip=()):
     for s in range(len(ctx)):
         if s in skip:
             continue
-        K, _ = A.gather_kv(np.abs(f64(kd)), np.abs(f64(vd)), tables[s], int(ctx[s]), B)
+        K, V = A.gather_kv(np.abs(f64(kd)), np.abs(f64(vd)), tables[s], int(ctx[s]), B)
         for r in range(start[s], start[s + 1]):
             covered[r] = True
             for g in range(Hq):
                 size = (K[g // (Hq // Hkv)] @ qa[r, g]).max() * abs(scale)
                 tol = (2 * (E + 128 * 2.0 ** -24) * size + W + 2.0 ** -18) * weight[r, g] * 2
+                if fp8:
+                    tol = tol + 2.0 ** -28 * V[g // (Hq // Hkv)].sum(0)
                 if out.dtype == torch.bfloat16:
                     tol = tol + 2.0 ** -8 * np.abs(want[r, g])
                 assert (np.abs(got[r, g] - want[r, g]) <= tol).all(), (s, r, g, np.abs(got[r, g] - want[r, g]).max())
@@ -550,3 +558,22 @@ def test_few_units_of_long_contexts(Hkv, G, D, B, ctxs, news, fp8):
         D = 128
     p = _problem(24, G * Hkv, Hkv, D, B, ctxs, news, fp8=fp8, gap=1)
     _check(p, _run(p, G * Hkv, Hkv, D, B, max(news), fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+@pytest.mark.parametrize("C", [1000, 6000])                 # in one block, and in many
+@pytest.mark.parametrize("above", [6.0, 9.0, 11.0, 20.0])
+def test_one_large_weight_and_a_long_tail_of_small_ones(n, G, fp8, above, C):
+    """A key whose score is `above` over thousands of others': their weights,
+    2^-9 to 2^-29 of the largest, are what the output is made of."""
+    Hkv, D, B = 1, 128, 16
+    q, kc, vc, tables, start, ctx = _problem(25, G * Hkv, Hkv, D, B, [C], [n], fp8=fp8)
+    q = (0.25 * torch.sign(q.float()[:1, :1].expand_as(q))).to(torch.bfloat16)
+    rng = np.random.default_rng(26)
+    k = 0.02 * rng.standard_normal(kc.shape)
+    v = 1.0 + 0.1 * rng.standard_normal(vc.shape)
+    k[tables[0, 3], :, 5] = above / (0.25 * math.sqrt(D)) * np.sign(q.float()[0, 0].numpy())
+    v[tables[0, 3], :, 5] = 0.0
+    put = (lambda x, s: Q.quantize(x, s)) if fp8 else (lambda x, s: to_bits(torch.from_numpy(x).to(torch.bfloat16)))
+    p = (q, put(k, K_SCALE), put(v, V_SCALE), tables, start, ctx)
+    _check(p, _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
