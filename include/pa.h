@@ -461,9 +461,9 @@ int pa_decode_multi(void* out, int out_dtype, const void* q,
  * pa_decode_fp8); d_head 128.  With up to 16 rows (new tokens times G) codes
  * are taken as f16, exactly, and q and the softmax weights rounded to f16 (a
  * relative 2^-11).  With more, q is split into two E4M3 terms, exactly for
- * what is within 2^-16 of the head's largest element, and the weights into
- * four E5M2 terms of their f16 values (a relative 2^-11, or 2^-28 of the
- * row's largest weight). */
+ * what is within 2^-14 of the head's largest element (else to within 2^-22 of
+ * it), and the weights into four E5M2 terms of their f16 values (a relative
+ * 2^-11, or 2^-28 of the row's largest weight). */
 int pa_decode_multi_fp8(void* out, int out_dtype, const void* q,
                         const void* k_cache, const void* v_cache,
                         const int32_t* block_tables,

@@ -577,3 +577,15 @@ def test_one_large_weight_and_a_long_tail_of_small_ones(n, G, fp8, above, C):
     put = (lambda x, s: Q.quantize(x, s)) if fp8 else (lambda x, s: to_bits(torch.from_numpy(x).to(torch.bfloat16)))
     p = (q, put(k, K_SCALE), put(v, V_SCALE), tables, start, ctx)
     _check(p, _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+def test_a_head_with_one_element_far_above_the_others(n, G, fp8):
+    """An element of q some 16384 times the others, which meets keys that are zero
+    there: the scores are the others' alone."""
+    Hkv, D, B, C = 2, 128, 16, 700
+    q, kc, vc, tables, start, ctx = _problem(27, G * Hkv, Hkv, D, B, [C], [n], fp8=fp8)
+    q[:, :, 17] = 16384.0
+    kc[..., 17] = 0
+    p = (q, kc, vc, tables, start, ctx)
+    _check(p, _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
