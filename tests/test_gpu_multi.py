@@ -589,3 +589,52 @@ def test_a_head_with_one_element_far_above_the_others(n, G, fp8):
     kc[..., 17] = 0
     p = (q, kc, vc, tables, start, ctx)
     _check(p, _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8), G * Hkv, Hkv, D, B, fp8=fp8)
+
+
+@pytest.mark.parametrize("fp8,D,G", [(False, 64, 8), (False, 128, 16), (True, 128, 8)])
+def test_units_of_many_rows_over_more_sequences_than_threads(fp8, D, G):
+    Hkv, B = 1, 8
+    rng = np.random.default_rng(28)
+    news = [int(x) for x in rng.integers(0, 2, 700)]
+    news[3] = 4 if G == 8 else 8
+    ctxs = [int(max(1, n + rng.integers(0, 150))) for n in news]
+    p = _problem(28, G * Hkv, Hkv, D, B, ctxs, news, fp8=fp8)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = _run(p, G * Hkv, Hkv, D, B, max(news), torch.bfloat16, fp8=fp8, status=st)
+    assert st.item() == 0
+    _check(p, out, G * Hkv, Hkv, D, B, fp8=fp8)
+
+
+def test_calls_from_two_threads_at_once():
+    """The library is entered by both: the binding lets go of the interpreter
+    during a call."""
+    import threading
+    Hkv, D, B = 2, 128, 16
+    work = []
+    for n, G, fp8 in UNITS[:4]:
+        p = _problem(29, G * Hkv, Hkv, D, B, [900, 40], [n, 2], fp8=fp8)
+        q, kc, vc, tables, start, ctx = p
+        put = (lambda c: torch.from_numpy(c).cuda()) if fp8 else from_bits
+        work.append((n, G, fp8, [q.cuda(), put(kc), put(vc)] + [torch.from_numpy(x).cuda() for x in (tables, start, ctx)],
+                     _run(p, G * Hkv, Hkv, D, B, n, fp8=fp8)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def calls(order):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(25):
+                for n, G, fp8, a, want in order:
+                    out = torch.empty_like(want)
+                    api.pa_decode_multi(out, *a, n, B, 1 / math.sqrt(D), G * Hkv, Hkv, D, 900,
+                                        k_scale=K_SCALE if fp8 else None, v_scale=V_SCALE if fp8 else None)
+                    stream.synchronize()
+                    if not torch.equal(out.view(torch.int32), want.view(torch.int32)):
+                        wrong.append((n, G, fp8))
+
+    threads = [threading.Thread(target=calls, args=(o,)) for o in (work, work[::-1])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
