@@ -458,9 +458,10 @@ int pa_decode_multi(void* out, int out_dtype, const void* q,
                     size_t workspace_bytes, int32_t* status_dev, void* stream);
 
 /* pa_decode_multi over FP8 caches (E4M3 codes times k_scale or v_scale, as
- * pa_decode_fp8); d_head 128.  With up to 16 rows (new tokens times G) codes
- * are taken as f16, exactly, and q and the softmax weights rounded to f16 (a
- * relative 2^-11).  With more, q is split into two E4M3 terms, exactly for
+ * pa_decode_fp8); d_head 128.  With up to 16 rows (new tokens times G), or
+ * contexts of up to 128 positions in few sequences, codes are taken as f16,
+ * exactly, and q and the softmax weights rounded to f16 (a relative 2^-11).
+ * Else q is split into two E4M3 terms, exactly for
  * what is within 2^-14 of the head's largest element (else to within 2^-22 of
  * it), and the weights into four E5M2 terms of their f16 values (a relative
  * 2^-11, or 2^-28 of the row's largest weight). */

@@ -573,6 +573,17 @@ int sms() {
 // Its bf16 products take a positive scale only; others go 16 rows at a time.
 bool is_wide(bool f8, float scale, long long rows) { return rows > kRows && (f8 || scale > 0.f); }
 
+// Whether a call that the wide kernel could take goes 16 rows at a time all
+// the same: contexts of one tile, and an SM for each unit of 16 (a third of
+// one where the units there would be of 128).  8 KV heads of 128, 64
+// positions, us here against there: 4 sequences of 32 rows 6.2 / 7.2, of 64
+// 6.5 / 7.9, of 128 7.9 / 9.8, 9 of 96 7.9 / 9.2, 1 of 256 6.7 / 10.8; 18 of
+// 32 at 128 positions 8.7 / 7.7; E4M3 4 of 128 at 128 9.1 / 8.3.
+bool in_small_tiles(bool f8, long long rows, double heads, int ctx) {
+    const double units = heads * (double)((rows + kRows - 1) / kRows);
+    return ctx <= 128 && units <= (f8 || rows <= 64 ? 1 : 3) * sms();
+}
+
 // Rows of a unit: on the wide kernel 64, and 128 for bf16 where a KV head has more.
 int unit_rows(long long rows, bool f8, bool wide) { return !wide ? kRows : f8 || rows <= 64 ? 64 : 128; }
 
@@ -638,7 +649,9 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     const long long cache_rows = (long long)num_blocks * n_kv_heads * block_size;
     if (cache_rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
     const long long all_rows = (long long)max_query_len * group;
-    const bool wide = is_wide(f8, scale, all_rows);
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    const int ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
+    const bool wide = is_wide(f8, scale, all_rows) && !in_small_tiles(f8, all_rows, (double)num_seqs * n_kv_heads, ctx_cap);
     const int unit = unit_rows(all_rows, f8, wide);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
     const int most = max_grid(wide);
@@ -646,8 +659,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     if (workspace_bytes < workspace_size(most, unit, d_head)) return PA_ERR_WORKSPACE;
 
     MultiArgs a{};
-    const long long cap = (long long)max_blocks_per_seq * block_size;
-    a.ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
+    a.ctx_cap = ctx_cap;
     // no more blocks than the largest possible work has smallest shares
     const double units = (double)num_seqs * n_kv_heads * (double)((all_rows + unit - 1) / unit);
     const int warps = wide ? 0 : block_warps(units, a.ctx_cap);

@@ -345,7 +345,7 @@ UNITS = [(4, 4, False), (4, 4, True), (9, 4, False), (9, 4, True), (20, 4, False
 @pytest.mark.parametrize("C", [40, 70, 3000])
 def test_values_that_are_not_finite_reach_the_rows_that_see_them_alone(n, G, fp8, kind, C):
     Hkv, D, B = 2, 128, 16
-    p = _problem(14, G * Hkv, Hkv, D, B, [C, 50], [n, 3], fp8=fp8)
+    p = _problem(14, G * Hkv, Hkv, D, B, [C, 200], [n, 3], fp8=fp8)
     q, kc, vc, tables, start, ctx = p
     words = _trees([n, 3], np.random.default_rng(5)) if kind == "tree" else None
     bad = [0x7F, 0xFF, 0x7F] if fp8 else [0x7F80, 0xFF80, 0x7FC0]
@@ -638,3 +638,13 @@ def test_calls_from_two_threads_at_once():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_many_rows_over_contexts_of_one_tile(fp8, kind):
+    """Prompts and chunks of up to 128 positions in few sequences: 16 rows at a time."""
+    Hq, Hkv, D, B, ctxs, news = 16, 4, 128, 16, [64, 128, 33, 7], [64, 20, 33, 1]
+    p = _problem(30, Hq, Hkv, D, B, ctxs, news, fp8=fp8, gap=2)
+    mask = [0] * 2 + _trees(news, np.random.default_rng(31)) + [0] * 2 if kind == "tree" else None
+    _check(p, _run(p, Hq, Hkv, D, B, 64, torch.bfloat16, mask, fp8, max_ctx=128), Hq, Hkv, D, B, mask, fp8)
