@@ -436,7 +436,7 @@ size_t pa_prefill_fp8_workspace_size(int num_seqs, int max_blocks_per_seq,
  *   tree_mask     optional device int64 [num_tokens], 8-byte aligned; then
  *                 max_query_len is at most 64 (PA_ERR_UNSUPPORTED otherwise).
  *   max_query_len host upper bound on every n, at least 1.
- *   out must not overlap the inputs.
+ *   out must not overlap the inputs (out == q: PA_ERR_INVALID_ARG).
  *   workspace     device, 256-byte aligned, at least
  *                 pa_decode_multi_workspace_size(max_query_len, n_q_heads,
  *                 n_kv_heads, d_head) bytes on the current device; needs no
@@ -461,10 +461,10 @@ int pa_decode_multi(void* out, int out_dtype, const void* q,
  * pa_decode_fp8); d_head 128.  With up to 16 rows (new tokens times G), or
  * contexts of up to 128 positions in few sequences, codes are taken as f16,
  * exactly, and q and the softmax weights rounded to f16 (a relative 2^-11).
- * Else q is split into two E4M3 terms, exactly for
- * what is within 2^-14 of the head's largest element (else to within 2^-22 of
- * it), and the weights into four E5M2 terms of their f16 values (a relative
- * 2^-11, or 2^-28 of the row's largest weight). */
+ * Otherwise q is split into two E4M3 terms, exactly for what is within 2^-14
+ * of the head's largest element (else to within 2^-22 of it), and the weights
+ * into four E5M2 terms of their f16 values (a relative 2^-11, or 2^-28 of the
+ * row's largest weight). */
 int pa_decode_multi_fp8(void* out, int out_dtype, const void* q,
                         const void* k_cache, const void* v_cache,
                         const int32_t* block_tables,

@@ -10,7 +10,8 @@
 // and 11: translation, the online softmax, the exact merge).
 //
 // This file serves up to 16 rows a KV head (and any number with a scale that
-// is not positive); pa_decode_wide.cu takes more.
+// is not positive, or over a few contexts of one tile); pa_decode_wide.cu
+// takes more.
 //
 // What bounds it: each K/V byte is read once for n * G rows, 4 * n * G
 // operations per two bytes, so the cache's bytes bound it.  64 sequences of
@@ -641,7 +642,7 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     if (group != 1 && group != 2 && group != 4 && group != 8 && group != 16) return PA_ERR_UNSUPPORTED;
     if (tree_mask && max_query_len > 64) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_tokens == 0) return PA_OK;
-    if (!out || !q || !k_cache || !v_cache || !block_tables || !query_start || !context_lens)
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !query_start || !context_lens || out == q)
         return PA_ERR_INVALID_ARG;
     if (!pa_host::aligned16(out) || !pa_host::aligned16(q) || !pa_host::aligned16(k_cache) ||
         !pa_host::aligned16(v_cache) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
