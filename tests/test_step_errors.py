@@ -13,7 +13,7 @@ A = 0x100000            # a 256-byte-aligned stand-in address (never dereference
 
 
 def multi(fp8=False, **kw):
-    a = dict(out=A, out_dtype=api.PA_DTYPE_BF16, q=A, k=A, v=A, tables=A, start=A, ctx=A, mask=None, block_size=16,
+    a = dict(out=2 * A, out_dtype=api.PA_DTYPE_BF16, q=A, k=A, v=A, tables=A, start=A, ctx=A, mask=None, block_size=16,
              scale=0.088, k_scale=0.01, v_scale=0.01, hq=32, hkv=8, d=128, num_seqs=4, tokens=16, most=4, max_blocks=8,
              num_blocks=64, max_ctx=128, ws=A, ws_bytes=1 << 40)
     a.update(kw)
@@ -36,6 +36,7 @@ def multi(fp8=False, **kw):
     (dict(out_dtype=5), api.PA_ERR_INVALID_ARG),
     (dict(out=None), api.PA_ERR_INVALID_ARG),
     (dict(start=None), api.PA_ERR_INVALID_ARG),
+    (dict(out=A), api.PA_ERR_INVALID_ARG),                        # in place of q
     (dict(block_size=64), api.PA_ERR_UNSUPPORTED),
     (dict(d=96), api.PA_ERR_UNSUPPORTED),
     (dict(hq=12), api.PA_ERR_UNSUPPORTED),
