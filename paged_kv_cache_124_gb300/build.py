@@ -26,6 +26,7 @@ OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libpa_gb300.so")
 BINDING = os.path.join(CSRC, "binding", "step_calls.cpp")
 MODULE = os.path.join(PKG, "_step_calls.so")
+TORCH_STAMP = os.path.join(OBJ_DIR, "torch_version")      # PyTorch's version that the module was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -60,14 +61,18 @@ def elf_matches_host(header, machine=None):
 
 
 def up_to_date():
-    """The library and the module exist, were built for this host's machine,
-    and are newer than every source and header."""
+    """The library and the module exist, were built for this host's machine
+    and PyTorch, and are newer than every source and header."""
     for built in (LIB, MODULE):
         if not os.path.exists(built):
             return False
         with open(built, "rb") as f:
             if not elf_matches_host(f.read(20)):
                 return False
+    import torch
+
+    if not os.path.exists(TORCH_STAMP) or open(TORCH_STAMP).read() != torch.__version__:
+        return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
@@ -115,6 +120,8 @@ def _link_binding(obj):
          [_cxx(), "-shared", "-o", MODULE + ".tmp", obj, LIB, "-Wl,-rpath,$ORIGIN", "-L",
           os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
     os.replace(MODULE + ".tmp", MODULE)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(torch.__version__)
 
 
 def build(force=False, verbose=False):
