@@ -7,6 +7,7 @@ name.  All computation happens in libpa_gb300.so; if the library is missing
 this module raises at import time rather than computing anything itself.
 """
 
+import contextlib
 import ctypes
 import os
 import re
@@ -612,6 +613,20 @@ def _raw_stream(stream, dev):
     return _current_handle(dev)
 
 
+def _allocating_for(stream):
+    """A context in which PyTorch's allocator serves the stream that a call runs on, so that memory taken for the
+    call comes from that stream's own pool: what used it before, and what gets it next, is ordered with the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle == 2:                                # cudaStreamPerThread: one handle, as many streams as threads
+            raise ValueError("a call on the per-thread default stream takes a workspace of the caller's")
+        # 0 and 1 (cudaStreamLegacy) are the default stream, which ExternalStream does not wrap
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    return torch.cuda.stream(stream)
+
+
 def pa_plan_step(block_tables, context_lens, query_start, positions, slot_mapping, seq_rows, new_lens, row_lens,
                  row_tables, row_blocks, free_blocks, free_count, block_size, num_blocks, status=None, stream=None):
     """Plan a step on the GPU: batch entry i (the request in row seq_rows[i])
@@ -679,14 +694,14 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context
     causal, or by tree_mask [T] (int64: bit b, the token sees new token b of
     its sequence).  workspace: a uint8 tensor from decode_multi_workspace
     (default: one allocated for this call through PyTorch's caching
-    allocator).  With k_scale / v_scale, the E4M3 form (uint8 caches); see pa.h."""
+    allocator, on the stream of the call).  With k_scale / v_scale, the E4M3
+    form (uint8 caches); see pa.h."""
     dev = torch.cuda.current_device()
     if (k_scale is None) != (v_scale is None):
         raise ValueError("pa_decode_multi: k_scale and v_scale go together")
     if workspace is None:
-        workspace = decode_multi_workspace(max_query_len, n_q_heads, n_kv_heads, d_head, q.device)
-        if stream is not None:                         # not to be handed out again while that stream uses it
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+        with _allocating_for(stream):
+            workspace = decode_multi_workspace(max_query_len, n_q_heads, n_kv_heads, d_head)
     return _check(_step_calls.decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len,
                                            block_size, scale, n_q_heads, n_kv_heads, d_head, max_context_len, tree_mask,
                                            workspace, status, k_scale, v_scale, dev, _raw_stream(stream, dev)),

@@ -648,3 +648,29 @@ def test_many_rows_over_contexts_of_one_tile(fp8, kind):
     p = _problem(30, Hq, Hkv, D, B, ctxs, news, fp8=fp8, gap=2)
     mask = [0] * 2 + _trees(news, np.random.default_rng(31)) + [0] * 2 if kind == "tree" else None
     _check(p, _run(p, Hq, Hkv, D, B, 64, torch.bfloat16, mask, fp8, max_ctx=128), Hq, Hkv, D, B, mask, fp8)
+
+
+def test_a_workspace_of_its_own_is_ordered_with_what_the_memory_was_before():
+    """Memory freed on the current stream with work on it still to run does not become the workspace of a call on
+    another stream; the default stream by its handle, too."""
+    Hq, Hkv, D, B = 8, 2, 128, 16
+    p = q, kc, vc, tables, start, ctx = _problem(32, Hq, Hkv, D, B, [2000, 70], [4, 3])
+    want = _run(p, Hq, Hkv, D, B, 4)
+    a = [q.cuda(), from_bits(kc), from_bits(vc)] + [torch.from_numpy(x).cuda() for x in (tables, start, ctx)]
+    size = api.pa_decode_multi_workspace_size(4, Hq, Hkv, D)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    out = torch.zeros(q.shape, dtype=torch.float32, device="cuda")
+    for current, stream in ((torch.cuda.current_stream(), side), (torch.cuda.current_stream(), side.cuda_stream), (other, 0)):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(current):
+            before = torch.empty(size, dtype=torch.uint8, device="cuda")
+            torch.cuda._sleep(4_000_000)                     # about 2 ms
+            before.fill_(0x5A)
+            torch.cuda._sleep(4_000_000)
+            kept = before.clone()
+            del before
+            api.pa_decode_multi(out, *a, 4, B, 1 / math.sqrt(D), Hq, Hkv, D, 2000, stream=stream)
+        torch.cuda.synchronize()
+        assert (kept == 0x5A).all()
+        assert torch.equal(out.view(torch.int32), want.view(torch.int32))

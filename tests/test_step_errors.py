@@ -187,3 +187,47 @@ def test_rope_table_is_the_angles_cosines_and_sines():
     assert t.shape == (1000, 64) and t.dtype == torch.float32
     angle = torch.tensor(999.0, dtype=torch.float64) * 500000.0 ** (-2 * 31 / 64.0)
     assert t[999, 31] == angle.cos().float() and t[999, 63] == angle.sin().float()
+
+
+class _Handle:
+    """A stream object of another library: its handle alone."""
+
+    def __init__(self, cuda_stream):
+        self.cuda_stream = cuda_stream
+
+
+@pytest.mark.parametrize("given,used", [
+    (None, "current"), (0x5000, 0x5000), (_Handle(0x6000), 0x6000), (0, "default"), (1, "default"), (_Handle(0), "default"),
+])
+def test_a_workspace_of_the_calls_own_comes_from_the_streams_pool(monkeypatch, given, used):
+    """Memory of another stream's pool could still be in use there when the call writes it."""
+    current, seen = ["current"], []
+
+    class use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: handle)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    monkeypatch.setattr(api, "_current_handle", lambda dev: 77)
+    monkeypatch.setattr(api, "decode_multi_workspace", lambda *a: seen.append(current[-1]) or torch.zeros(16))
+    monkeypatch.setattr(api._step_calls, "decode_multi", lambda *a: seen.append(a[-1]) or api.PA_OK)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    assert api.pa_decode_multi(q, q, q, q, q, q, q, 1, 16, 0.125, 4, 2, 64, 48, stream=given) == api.PA_OK
+    handle = 77 if given is None else getattr(given, "cuda_stream", given)
+    assert seen == [used, handle] and current == ["current"]
+
+
+def test_a_workspace_of_its_own_is_refused_on_the_per_thread_stream(monkeypatch):
+    """One handle for a stream of every thread: no pool is ordered with it."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="per-thread"):
+        api.pa_decode_multi(*[None] * 7, 1, 16, 0.125, 4, 2, 64, 48, stream=2)
