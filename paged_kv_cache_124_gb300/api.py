@@ -208,6 +208,20 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _allocating_for(stream):
+    """A context in which PyTorch's allocator serves the stream that a call runs on, so that memory taken for the
+    call comes from that stream's own pool: what used it before, and what gets it next, is ordered with the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle == 2:                                # cudaStreamPerThread: one handle, as many streams as threads
+            raise ValueError("on the per-thread default stream a call takes a workspace (and counters) of the caller's")
+        # 0 and 1 (cudaStreamLegacy) are the default stream, which ExternalStream does not wrap
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    return torch.cuda.stream(stream)
+
+
 # ----------------------------------------------------------------------------
 # kernels
 # ----------------------------------------------------------------------------
@@ -314,7 +328,8 @@ def prefill_counters(device, stream=None):
     key = (dev.index if dev.index is not None else torch.cuda.current_device(), handle)
     t = _prefill_counters.get(key)
     if t is None:
-        t = torch.zeros(2, dtype=torch.int32, device=dev)
+        with _allocating_for(stream):                  # zeroed ahead of the call
+            t = torch.zeros(2, dtype=torch.int32, device=dev)
         _prefill_counters[key] = t
     return t
 
@@ -337,7 +352,8 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, query_start, context_lens
     work-claim pair (default: this stream's, from prefill_counters; False:
     none, a fixed round-robin assignment of work).  `workspace`: a uint8
     device tensor of at least pa_prefill_workspace_size bytes (default: one
-    allocated for this call through PyTorch's caching allocator)."""
+    allocated for this call through PyTorch's caching allocator, on the stream
+    of the call)."""
     if out.dtype == torch.bfloat16:
         out_dtype = PA_DTYPE_BF16
     elif out.dtype == torch.float32:
@@ -358,7 +374,8 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, query_start, context_lens
     if block_tables.dim() != 2 or context_lens.shape != (num_seqs,) or query_start.shape != (num_seqs + 1,):
         raise ValueError("block_tables [S, max_blocks], query_start [S + 1], context_lens [S]")
     if workspace is None:
-        workspace = prefill_workspace(num_seqs, block_tables.shape[1], block_size, n_kv_heads, d_head, q.device)
+        with _allocating_for(stream):
+            workspace = prefill_workspace(num_seqs, block_tables.shape[1], block_size, n_kv_heads, d_head, q.device)
     st = _lib.pa_prefill(_opt_dev(out, out.dtype, "out"), out_dtype, _dev(q, torch.bfloat16, "q"),
                          _dev(k_cache, torch.bfloat16, "k_cache"), _dev(v_cache, torch.bfloat16, "v_cache"),
                          _dev(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
@@ -407,7 +424,9 @@ def pa_prefill_fp8(out, q, k_cache, v_cache, block_tables, query_start, context_
     if block_tables.dim() != 2 or context_lens.shape != (num_seqs,) or query_start.shape != (num_seqs + 1,):
         raise ValueError("block_tables [S, max_blocks], query_start [S + 1], context_lens [S]")
     if workspace is None:
-        workspace = prefill_fp8_workspace(num_seqs, block_tables.shape[1], block_size, n_kv_heads, d_head, q.device)
+        with _allocating_for(stream):
+            workspace = prefill_fp8_workspace(num_seqs, block_tables.shape[1], block_size, n_kv_heads, d_head,
+                                              q.device)
     st = _lib.pa_prefill_fp8(_opt_dev(out, out.dtype, "out"), out_dtype, _dev(q, torch.bfloat16, "q"),
                              _dev(k_cache, torch.uint8, "k_cache"), _dev(v_cache, torch.uint8, "v_cache"),
                              _dev(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
@@ -611,20 +630,6 @@ def _raw_stream(stream, dev):
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     return _current_handle(dev)
-
-
-def _allocating_for(stream):
-    """A context in which PyTorch's allocator serves the stream that a call runs on, so that memory taken for the
-    call comes from that stream's own pool: what used it before, and what gets it next, is ordered with the call."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if handle == 2:                                # cudaStreamPerThread: one handle, as many streams as threads
-            raise ValueError("a call on the per-thread default stream takes a workspace of the caller's")
-        # 0 and 1 (cudaStreamLegacy) are the default stream, which ExternalStream does not wrap
-        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
-    return torch.cuda.stream(stream)
 
 
 def pa_plan_step(block_tables, context_lens, query_start, positions, slot_mapping, seq_rows, new_lens, row_lens,

@@ -473,3 +473,33 @@ def test_prefill_captured_in_a_cuda_graph_equals_eager():
         assert torch.equal(out.view(torch.int32), eager.view(torch.int32))
         out.fill_(float("nan"))
     assert int(cnt.abs().sum().item()) == 0
+
+
+def test_memory_of_the_calls_own_is_ordered_with_what_it_was_before():
+    """Without a workspace and counters of the caller's, on a stream that is not the current one: memory freed on the
+    current stream with work on it still to run is not taken, and the counters are zero before the call reads them."""
+    Hq, Hkv, D, B = 8, 2, 128, 16
+    ctxs, news = [700, 300], [500, 300]
+    qb, kb, vb, tab, qs, ctx = _problem(43, Hq, Hkv, D, B, ctxs, news)
+    dev = lambda a: torch.from_numpy(a).cuda()
+    args = (from_bits(qb), from_bits(kb), from_bits(vb), dev(tab), dev(qs), dev(ctx), max(news), B,
+            1 / math.sqrt(D), Hq, Hkv, D)
+    want = torch.empty((qb.shape[0], Hq, D), dtype=torch.float32, device="cuda")
+    api.pa_prefill(want, *args)
+    size = api.pa_prefill_workspace_size(len(ctxs), tab.shape[1], B, Hkv, D)
+    side, other, out = torch.cuda.Stream(), torch.cuda.Stream(), torch.empty_like(want)
+    for current, stream in ((torch.cuda.current_stream(), side), (torch.cuda.current_stream(), side.cuda_stream),
+                            (other, 0)):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(current):
+            before = torch.empty(size, dtype=torch.uint8, device="cuda")
+            torch.cuda._sleep(4_000_000)                     # about 2 ms
+            before.fill_(0x5A)
+            torch.cuda._sleep(4_000_000)
+            kept = before.clone()
+            del before
+            api.pa_prefill(out, *args, stream=stream)
+        torch.cuda.synchronize()
+        assert (kept == 0x5A).all()
+        assert torch.equal(out.view(torch.int32), want.view(torch.int32))
