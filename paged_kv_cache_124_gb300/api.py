@@ -322,16 +322,19 @@ _prefill_counters = {}
 def prefill_counters(device, stream=None):
     """The two zeroed int32 work-claim counters pa_prefill uses on this device
     and stream (each call leaves them zero again); one pair per stream, since
-    calls sharing a pair must not overlap."""
+    calls sharing a pair must not overlap.  While the stream is captured, a
+    pair of the graph's own, zeroed by the graph: a graph may be replayed
+    beside others and beside the stream's calls."""
     dev = torch.device(device)
     handle = _stream(stream).value or 0
-    key = (dev.index if dev.index is not None else torch.cuda.current_device(), handle)
-    t = _prefill_counters.get(key)
-    if t is None:
-        with _allocating_for(stream):                  # zeroed ahead of the call
-            t = torch.zeros(2, dtype=torch.int32, device=dev)
-        _prefill_counters[key] = t
-    return t
+    with _allocating_for(stream):                      # zeroed ahead of the call
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(2, dtype=torch.int32, device=dev)
+        key = (dev.index if dev.index is not None else torch.cuda.current_device(), handle)
+        t = _prefill_counters.get(key)
+        if t is None:
+            t = _prefill_counters[key] = torch.zeros(2, dtype=torch.int32, device=dev)
+        return t
 
 
 def pa_prefill_workspace_size(num_seqs, max_blocks_per_seq, block_size, n_kv_heads, d_head):

@@ -20,7 +20,7 @@ class Handle:
 @pytest.fixture
 def taken(monkeypatch):
     """What was allocated, and on which stream; `current`: the stack of current streams."""
-    log = types.SimpleNamespace(current=["current"], took=[], called=[])
+    log = types.SimpleNamespace(current=["current"], took=[], called=[], captured=[])
 
     class use:
         def __init__(self, stream):
@@ -43,6 +43,7 @@ def taken(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", use)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: handle)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: log.current[-1] in log.captured)
     monkeypatch.setattr(api, "prefill_workspace", took("workspace"))
     monkeypatch.setattr(api, "prefill_fp8_workspace", took("workspace"))
     monkeypatch.setattr(api, "_prefill_counters", {})
@@ -80,3 +81,20 @@ def test_the_per_thread_stream_takes_the_callers_memory(taken):
     with pytest.raises(ValueError, match="per-thread"):
         prefill(False, stream=2, counters=False)
     assert prefill(False, stream=2, counters=False, workspace=torch.empty(16)) == api.PA_OK
+
+
+@pytest.mark.parametrize("given,used", [(None, "current"), (0x5000, 0x5000)])
+def test_a_captured_call_has_counters_of_its_own(taken, given, used):
+    """Those of the stream's calls would be zeroed in the graph alone, or shared by graphs that are replayed at once."""
+    count = lambda: [s for what, s in taken.took if what == "counters"]  # noqa: E731
+    taken.captured.append(used)
+    prefill(False, stream=given)
+    prefill(False, stream=given)
+    assert count() == [used, used]
+    taken.captured.clear()
+    for _ in range(2):
+        prefill(False, stream=given)
+        assert count() == [used] * 3                     # then one pair for the stream, kept
+    taken.captured.append(used)
+    prefill(False, stream=given)
+    assert count() == [used] * 4

@@ -503,3 +503,40 @@ def test_memory_of_the_calls_own_is_ordered_with_what_it_was_before():
         torch.cuda.synchronize()
         assert (kept == 0x5A).all()
         assert torch.equal(out.view(torch.int32), want.view(torch.int32))
+
+
+def test_captured_calls_with_counters_of_their_own_replayed_at_once():
+    """Two graphs captured on one stream without counters of the caller's, replayed on two streams beside an eager
+    call of the capture's stream: none waits for the others, and each gives the eager output."""
+    Hq, Hkv, D, B = 16, 4, 64, 16
+    probs = [_problem(44 + i, Hq, Hkv, D, B, [900, 300 + i], [700, 300]) for i in range(3)]
+    dev = lambda a: torch.from_numpy(a).cuda()
+    calls, want = [], []
+    for qb, kb, vb, tab, qs, ctx in probs:
+        args = (from_bits(qb), from_bits(kb), from_bits(vb), dev(tab), dev(qs), dev(ctx), 700, B, 1 / math.sqrt(D), Hq,
+                Hkv, D)
+        out = torch.zeros((qb.shape[0], Hq, D), dtype=torch.float32, device="cuda")
+        ws = api.prefill_workspace(2, tab.shape[1], B, Hkv, D)
+        run = lambda out=out, args=args, ws=ws: api.pa_prefill(out, *args, workspace=ws)  # noqa: E731
+        run()
+        want.append(out.clone())
+        calls.append((out, run))
+    capture, streams = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for _, run in calls[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=capture):
+            run()
+        graphs.append(g)
+    for _ in range(5):
+        for out, _ in calls:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(capture):
+            calls[2][1]()
+        torch.cuda.synchronize()
+        for (out, _), w in zip(calls, want):
+            assert torch.equal(out.view(torch.int32), w.view(torch.int32))
