@@ -513,7 +513,9 @@ size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads,
  * out of range or named twice (PA_DEV_BAD_ROW), or a length or count is
  * negative, beyond the table, or the new positions are more than num_tokens
  * (PA_DEV_BAD_CONTEXT), the step is planned with every n = 0 and no block is
- * taken.  A table entry outside the pool gives slot -1 and PA_DEV_BAD_BLOCK_ID.
+ * taken (an entry whose row, or whose row's L, is out of range is planned as
+ * padding).  A table entry outside the pool gives slot -1 and
+ * PA_DEV_BAD_BLOCK_ID.
  *   free_blocks   device int32 [free_capacity], and free_count, device int32
  *                 [1]; both NULL: the tables hold every block already
  *                 (reserved by the host manager) and needing one is

@@ -114,17 +114,24 @@ struct Requests {
             if (k >= per || i >= a.num_seqs) continue;
             const int r = a.seq_rows[i], m = a.new_lens[i];
             if (r < 0) continue;                       // padding of the batch
-            if (r >= a.num_rows || (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u)) {
+            if (r >= a.num_rows) {
                 bad |= PA_DEV_BAD_ROW;
                 continue;
             }
+            if (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u) bad |= PA_DEV_BAD_ROW;
             const int L = a.row_lens[r], h = a.row_blocks[r];
-            if (L < 0 || L > cap || h < 0 || h > a.max_blocks || m < 0 || (long long)L + m > cap) {
+            if (L < 0 || L > cap) {
                 bad |= PA_DEV_BAD_CONTEXT;
                 continue;
             }
+            // whatever else is wrong refuses the step, and a refused step shows what the row has: the same for every
+            // entry that names it, whichever of them is the first to mark it
             row[k] = r;
             len[k] = L;
+            if (h < 0 || h > a.max_blocks || m < 0 || (long long)L + m > cap) {
+                bad |= PA_DEV_BAD_CONTEXT;
+                continue;
+            }
             n[k] = m;
             held[k] = h;
             const int nb = (int)(((long long)L + m + (1 << a.log2_block) - 1) >> a.log2_block);

@@ -550,3 +550,37 @@ def test_tensors_of_wrong_type_shape_place_or_layout_are_refused():
             with pytest.raises(error, match=text):
                 fn(**dict(good, **change))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("max_blocks", [8, 1 << 17], ids=["one cluster", "two launches"])
+@pytest.mark.parametrize("rows,new,held,bit", [
+    ([2, 1, 2, 0], [1, 1, 4, 1], None, "BAD_ROW"),       # the same row twice, with different lengths
+    ([2, 2, 2, 2], [0, 0, 0, 0], None, "BAD_ROW"),
+    ([1, 2, 0, -1], [-1, 1, 2, 5], None, "BAD_CONTEXT"),
+    ([1, 2, 0, 7], [2147483647, 1, 2, 5], None, "BAD_CONTEXT|BAD_ROW"),
+    ([1, 2, 0, -1], [1, 1, 1, 1], -1, "BAD_CONTEXT"),    # a row that holds fewer blocks than none
+    ([1, 2, 0, -1], [1, 1, 1, 1], 1 << 30, "BAD_CONTEXT"),
+])
+def test_a_refused_plan_shows_what_every_named_row_has(max_blocks, rows, new, held, bit):
+    """Every n is 0, of the entries that are at fault as well, and of both that name one row whichever comes first."""
+    p = Plan(5, max_blocks, 30, 8, np.random.default_rng(16))
+    p.step([2, 0, 1], [20, 7, 33])
+    if held is not None:
+        p.d_blocks[1] = held
+    before = p.d_tables.clone(), p.d_blocks.clone(), p.d_count.clone()
+    want = 0
+    for name in bit.split("|"):
+        want |= getattr(api, "PA_DEV_" + name)
+    for _ in range(20):
+        p.status.zero_()
+        got = p.gpu(rows, new, 12)
+        assert p.status.item() == want
+        there = [r if 0 <= r < 5 else None for r in rows]
+        assert got[1] == [0 if r is None else p.lens[r] for r in there]
+        for t, r in zip(got[0], there):
+            nb = 0 if r is None else -(-p.lens[r] // 8)
+            assert t[:nb] == p.tables[r][:nb] if nb else True
+            assert all(x == -1 for x in t[nb:])
+        assert got[2] == [0] * 5 and got[3] == [-1] * 12 and got[4] == [-1] * 12
+    for a, b in zip(before, (p.d_tables, p.d_blocks, p.d_count)):
+        assert torch.equal(a, b)
