@@ -600,7 +600,8 @@ int pa_reshape_and_cache_fp8(void* k_cache, void* v_cache, const void* k,
  * PA_DEV_BAD_POSITION; a slot outside the pool skips the write and is flagged
  * PA_DEV_BAD_SLOT.
  *   q_out         device bf16 [num_tokens][n_q_heads][d_head]; it may be q
- *                 itself if q is contiguous (q_stride n_q_heads * d_head).
+ *                 itself if q is contiguous (q_stride n_q_heads * d_head;
+ *                 PA_ERR_INVALID_ARG otherwise).
  *   q, k, v       device bf16, heads of a token contiguous, q_stride /
  *                 k_stride / v_stride elements between tokens (multiples of
  *                 8, at least a token's heads): views of one projection's

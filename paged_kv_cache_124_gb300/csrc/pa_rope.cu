@@ -413,6 +413,8 @@ int norm_rope_cache(void* q_out, void* k_cache, void* v_cache, const void* q, co
         !pa_host::aligned16(q_weight) || !pa_host::aligned16(k_weight) || ((q_stride | k_stride | v_stride) & 7) ||
         (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
         return PA_ERR_MISALIGNED;
+    // in place of a strided q, rows would be written over rows still to be read
+    if (q_out == q && num_tokens > 1 && q_stride != (int64_t)n_q_heads * d_head) return PA_ERR_INVALID_ARG;
     RopeArgs a{};
     a.q_out = static_cast<uint4*>(q_out);
     a.k_cache = static_cast<uint8_t*>(k_cache);

@@ -231,3 +231,9 @@ def test_a_workspace_of_its_own_is_refused_on_the_per_thread_stream(monkeypatch)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="per-thread"):
         api.pa_decode_multi(*[None] * 7, 1, 16, 0.125, 4, 2, 64, 48, stream=2)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_rope_in_place_of_a_strided_q_is_refused(fp8):
+    assert rope(fp8, qs=6144) == api.PA_ERR_INVALID_ARG
+    assert rope(fp8, qs=6144, tokens=0) == api.PA_OK
