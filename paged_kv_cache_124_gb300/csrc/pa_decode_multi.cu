@@ -645,7 +645,9 @@ int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, c
     if (!out || !q || !k_cache || !v_cache || !block_tables || !query_start || !context_lens || out == q)
         return PA_ERR_INVALID_ARG;
     if (!pa_host::aligned16(out) || !pa_host::aligned16(q) || !pa_host::aligned16(k_cache) ||
-        !pa_host::aligned16(v_cache) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+        !pa_host::aligned16(v_cache) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+        (reinterpret_cast<uintptr_t>(query_start) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
         return PA_ERR_MISALIGNED;
     const long long cache_rows = (long long)num_blocks * n_kv_heads * block_size;
     if (cache_rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;

@@ -237,3 +237,9 @@ def test_a_workspace_of_its_own_is_refused_on_the_per_thread_stream(monkeypatch)
 def test_rope_in_place_of_a_strided_q_is_refused(fp8):
     assert rope(fp8, qs=6144) == api.PA_ERR_INVALID_ARG
     assert rope(fp8, qs=6144, tokens=0) == api.PA_OK
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("name", ["tables", "start", "ctx"])
+def test_multi_takes_aligned_lengths_and_tables_only(fp8, name):
+    assert multi(fp8, **{name: A + 2}) == api.PA_ERR_MISALIGNED
