@@ -432,6 +432,17 @@ __global__ void __launch_bounds__(kPlanThreads) release_kernel(const int32_t* ro
     if (t == 0) *free_count = count + (int)total;
 }
 
+// Shared memory of the kernels for a call's sizes.  Past 40 KiB a kernel is
+// given what its largest call needs, whatever this one does: threads that call
+// with different sizes then never set a limit below one that another relies on.
+constexpr int fused_smem(int seqs, int rows) { return (int)sizeof(Planned) * seqs + 4 * (seqs + 1) + 4 * ((rows + 31) / 32); }
+constexpr int list_smem(int seqs, int rows) { return 4 * seqs + 4 * ((rows + 31) / 32); }
+
+template <typename K>
+bool has_smem(K kernel, int bytes, int most, int* granted) {
+    return bytes <= 40 * 1024 || pa_host::ensure_smem_attr(kernel, most, granted) == cudaSuccess;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -487,16 +498,15 @@ int pa_plan_step(int32_t* block_tables, int32_t* context_lens, int32_t* query_st
     // 1000 of 2048 24 / 8.7 (each behind a copy of about 1.3 us).
     if (num_seqs <= kFusedSeqs && (long long)num_seqs * max_blocks_per_seq + 8LL * num_tokens <= 270000) {
         static int attr_fused[64] = {0};
-        const int smem = (int)sizeof(Planned) * num_seqs + 4 * (num_seqs + 1) + 4 * ((num_rows + 31) / 32);
-        if (smem > 40 * 1024 && pa_host::ensure_smem_attr(fused_plan_kernel, smem, attr_fused) != cudaSuccess)
-            return PA_ERR_CUDA;
+        const int smem = fused_smem(num_seqs, num_rows);
+        if (!has_smem(fused_plan_kernel, smem, fused_smem(kFusedSeqs, kPlanMaxRows), attr_fused)) return PA_ERR_CUDA;
         return pa_host::launch_dependent(fused_plan_kernel, dim3(kCluster), dim3(kPlanThreads), smem, st, a) == cudaSuccess
                    ? PA_OK
                    : PA_ERR_CUDA;
     }
     static int attr_plan[64] = {0};
-    const int smem = 4 * num_seqs + 4 * ((num_rows + 31) / 32);
-    if (smem > 40 * 1024 && pa_host::ensure_smem_attr(plan_kernel, smem, attr_plan) != cudaSuccess) return PA_ERR_CUDA;
+    const int smem = list_smem(num_seqs, num_rows);
+    if (!has_smem(plan_kernel, smem, list_smem(kPlanMaxSeqs, kPlanMaxRows), attr_plan)) return PA_ERR_CUDA;
     if (pa_host::launch_dependent(plan_kernel, dim3(1), dim3(kPlanThreads), smem, st, a) != cudaSuccess)
         return PA_ERR_CUDA;
     const int segments = (max_blocks_per_seq + kSegment - 1) / kSegment;
@@ -521,9 +531,8 @@ int pa_release_rows(const int32_t* rows, int num_released, const int32_t* row_ta
         !aligned4(free_count))
         return PA_ERR_MISALIGNED;
     static int attr_release[64] = {0};
-    const int smem = 4 * num_released + 4 * ((num_rows + 31) / 32);
-    if (smem > 40 * 1024 && pa_host::ensure_smem_attr(release_kernel, smem, attr_release) != cudaSuccess)
-        return PA_ERR_CUDA;
+    const int smem = list_smem(num_released, num_rows);
+    if (!has_smem(release_kernel, smem, list_smem(kPlanMaxSeqs, kPlanMaxRows), attr_release)) return PA_ERR_CUDA;
     return pa_host::launch_dependent(release_kernel, dim3(1), dim3(kPlanThreads), smem,
                                      static_cast<cudaStream_t>(stream), rows, num_released, row_tables, row_blocks,
                                      num_rows, max_blocks_per_seq, free_blocks, free_count, free_capacity,
