@@ -53,7 +53,11 @@ if not os.path.exists(_LIB_PATH):
 
 _lib = ctypes.CDLL(_LIB_PATH)
 
-from . import _step_calls  # noqa: E402  (the step operators' calls; linked to the library)
+try:
+    from . import _step_calls  # noqa: E402  (the step operators' calls; linked to the library)
+except ImportError as e:
+    raise ImportError("_step_calls.so has not been built for this Python and PyTorch "
+                      "(python -m paged_kv_cache_124_gb300.build): %s" % e) from e
 
 _c_int, _c_size, _c_float = ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _vp, _i32p, _i64p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64)

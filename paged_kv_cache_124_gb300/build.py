@@ -1,13 +1,16 @@
 """Build the C-ABI library libpa_gb300.so for sm_103a, and the binding's native
 module _step_calls.so, in tree.
 
-Each translation unit under csrc/ is compiled by nvcc in parallel and the
-objects are linked into paged_kv_cache_124_gb300/libpa_gb300.so.  The module,
-csrc/binding/, is compiled beside them by the host's C++ compiler against
-PyTorch's headers and linked to the library.  Nothing is rebuilt when both are
-newer than every source and header.
+The library needs nvcc alone: each translation unit under csrc/ is compiled in
+parallel and the objects are linked into paged_kv_cache_124_gb300/libpa_gb300.so.
+The module, csrc/binding/, is compiled beside them by the host's C++ compiler
+against PyTorch's headers and linked to the library.  Each is built again when
+one of its own sources or headers is newer, the module also for another
+PyTorch.
 
-    python -m paged_kv_cache_124_gb300.build [--force]
+    python -m paged_kv_cache_124_gb300.build [--force] [--library]
+
+--library: the library alone, for clients of the C ABI (no PyTorch).
 """
 
 import concurrent.futures
@@ -42,10 +45,17 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
-def _inputs():
+def _public_headers():
+    return [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+
+
+def _library_inputs():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hdrs += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    return sources() + hdrs + [BINDING, os.path.abspath(__file__)]
+    return sources() + hdrs + _public_headers() + [os.path.abspath(__file__)]
+
+
+def _module_inputs():
+    return [BINDING] + _public_headers() + [os.path.abspath(__file__)]
 
 
 # ELF e_machine of a shared object built for this host (x86-64 or AArch64)
@@ -60,21 +70,30 @@ def elf_matches_host(header, machine=None):
             want is not None and int.from_bytes(header[18:20], "little") == want)
 
 
-def up_to_date():
-    """The library and the module exist, were built for this host's machine
-    and PyTorch, and are newer than every source and header."""
-    for built in (LIB, MODULE):
-        if not os.path.exists(built):
+def _current(built, inputs):
+    """The file exists, was built for this host's machine, and is newer than
+    its inputs."""
+    if not os.path.exists(built):
+        return False
+    with open(built, "rb") as f:
+        if not elf_matches_host(f.read(20)):
             return False
-        with open(built, "rb") as f:
-            if not elf_matches_host(f.read(20)):
-                return False
+    t = os.path.getmtime(built)
+    return all(os.path.getmtime(p) <= t for p in inputs)
+
+
+def library_up_to_date():
+    return _current(LIB, _library_inputs())
+
+
+def module_up_to_date():
+    """As the library, and built for this PyTorch."""
+    if not _current(MODULE, _module_inputs()) or not os.path.exists(TORCH_STAMP):
+        return False
     import torch
 
-    if not os.path.exists(TORCH_STAMP) or open(TORCH_STAMP).read() != torch.__version__:
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    with open(TORCH_STAMP) as f:
+        return f.read() == torch.__version__
 
 
 def _compile(src, verbose):
@@ -124,15 +143,13 @@ def _link_binding(obj):
         f.write(torch.__version__)
 
 
-def build(force=False, verbose=False):
-    """Compile csrc/ into libpa_gb300.so (sm_103a) and _step_calls.so.  Returns the library path."""
-    if not force and up_to_date():
+def build_library(force=False, verbose=False):
+    """Compile csrc/ into libpa_gb300.so (sm_103a).  Returns its path."""
+    if not force and library_up_to_date():
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose), sources()))
-        binding = binding.result()
     if verbose:
         for _, log in results:
             if log:
@@ -141,9 +158,20 @@ def build(force=False, verbose=False):
     _run("link", [_nvcc(), *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp] +
          [o for o, _ in results])
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    return LIB
+
+
+def build(force=False, verbose=False):
+    """The library, and the binding's module beside it.  Returns the library's path."""
+    if not force and module_up_to_date():
+        return build_library(verbose=verbose)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_binding)
+        build_library(force, verbose)
+        _link_binding(binding.result())
     return LIB
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print((build_library if "--library" in sys.argv else build)(force="--force" in sys.argv, verbose="-v" in sys.argv))
