@@ -86,3 +86,13 @@ def test_a_newer_source_builds_what_it_belongs_to(tree, monkeypatch):
     assert b.library_up_to_date() and not b.module_up_to_date()
     os.utime(os.path.join(b.CSRC, "one.cu"), (later, later))
     assert not b.library_up_to_date()
+
+
+def test_the_entry_points_can_be_run_as_a_script():
+    """python __graft_entry__.py --smoke calls what the whole file defines."""
+    import ast
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "__graft_entry__.py")
+    with open(path) as f:
+        body = ast.parse(f.read()).body
+    main = [isinstance(n, ast.If) and "__name__" in ast.unparse(n.test) for n in body]
+    assert main.count(True) == 1 and main[-1]
