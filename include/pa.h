@@ -96,7 +96,9 @@ const char* pa_status_string(int status);
  * softmax is computed online in fp32 with a running maximum and sum
  * ([P1] section 13; [P2] section 11).  A context length of 0 gives a zero
  * row.  The token this step appended is part of the context: context_lens
- * counts it.
+ * counts it.  An infinite value makes its column of the row infinite or NaN
+ * (a weight enters the products as two terms, of which the second may be zero
+ * or negative).
  *
  * Each sequence is split into partitions of partition_size positions, one
  * thread block per (sequence, group of up to 8 query heads, partition).  A
@@ -422,7 +424,11 @@ size_t pa_prefill_fp8_workspace_size(int num_seqs, int max_blocks_per_seq,
  *
  * Scores, softmax and sums are fp32.  The value products take the softmax
  * weights as two bf16 terms (a relative 2^-16).  Keys and values that a row
- * does not see, non-finite ones among them, do not touch its result.
+ * does not see, non-finite ones among them, do not touch its result.  A value
+ * that a row sees and that is not finite makes the row's element of its column
+ * not finite: what the sum above gives if it is at a new position, and else
+ * possibly NaN in place of an infinity (a weight's second term may be zero or
+ * negative).
  *
  * Arguments
  *   out           device [num_tokens][n_q_heads][d_head], bf16 or fp32 per

@@ -674,3 +674,23 @@ def test_a_workspace_of_its_own_is_ordered_with_what_the_memory_was_before():
         torch.cuda.synchronize()
         assert (kept == 0x5A).all()
         assert torch.equal(out.view(torch.int32), want.view(torch.int32))
+
+
+@pytest.mark.parametrize("n,G,fp8", [u for u in UNITS if not u[2]])
+@pytest.mark.parametrize("C", [70, 3000])
+def test_infinite_values_of_the_context_reach_their_column_alone(n, G, fp8, C):
+    """Positions before the new ones, which every row sees: the column of their KV head's rows is not finite (an
+    infinity may become NaN), and everything else is what finite values give."""
+    Hkv, D, B = 2, 128, 16
+    p = _problem(33, G * Hkv, Hkv, D, B, [C, 200], [n, 3])
+    q, kc, vc, tables, start, ctx = p
+    clean = vc.copy()
+    for j, h, d, bits in ((0, 0, 5, 0x7F80), (C - n - 1, 0, 64, 0xFF80), (C // 2, 1, 127, 0x7F80)):
+        at = tables[0, j // B], h, j % B, d
+        vc[at], clean[at] = bits, 0
+    out = _run(p, G * Hkv, Hkv, D, B, n)
+    odd = torch.zeros_like(out, dtype=torch.bool)
+    odd[:n, :G, 5] = odd[:n, :G, 64] = odd[:n, G:, 127] = True
+    assert torch.equal(~torch.isfinite(out), odd)
+    fine = _run((q, kc, clean, tables, start, ctx), G * Hkv, Hkv, D, B, n)
+    _check((q, kc, clean, tables, start, ctx), torch.where(odd, fine, out), G * Hkv, Hkv, D, B)
