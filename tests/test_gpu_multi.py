@@ -694,3 +694,50 @@ def test_infinite_values_of_the_context_reach_their_column_alone(n, G, fp8, C):
     assert torch.equal(~torch.isfinite(out), odd)
     fine = _run((q, kc, clean, tables, start, ctx), G * Hkv, Hkv, D, B, n)
     _check((q, kc, clean, tables, start, ctx), torch.where(odd, fine, out), G * Hkv, Hkv, D, B)
+
+
+@pytest.mark.parametrize("n,G,fp8", UNITS)
+@pytest.mark.parametrize("Hkv,B,ctxs", [
+    (1, 16, [30001]),                                        # one head's keys over every SM: hundreds of pieces
+    (2, 32, [20011, 7, 193, 2048]),
+    (2, 8, [1150, 1, 640, 129, 4097, 768]),                  # whole units, and shares that end anywhere
+    (8, 16, [500 + 411 * i for i in range(9)]),              # an even split of ragged contexts
+])
+def test_every_position_of_long_contexts_counts_once(n, G, fp8, Hkv, B, ctxs):
+    """q of zero, so that every weight is the same, and a position's value 1 in one column of 128 drawn for it: an
+    output is the share of its column among the positions that the row sees.  Value sums are whole numbers times the
+    weights' power of two, and exact.  So are the sums of weights where a weight is 2^0; E4M3 caches and more than 16
+    rows take it as 2^12 from an approximation good to 2^-22, and the chain of a thread's additions is C / 4 at most,
+    each good to 2^-24; factor and division take 2^-22.  A stretch of 16 positions lost or taken twice is several
+    times that, which is tested on the formula's side."""
+    D, news = 128, [min(n, c) for c in ctxs]
+    q, kc, vc, tables, start, ctx = _problem(34, G * Hkv, Hkv, D, B, ctxs, news, fp8=fp8)
+    q.zero_()
+    rng = np.random.default_rng(35)
+    column = [rng.integers(0, D, (c, Hkv)) for c in ctxs]
+    for s, c in enumerate(ctxs):
+        j = np.arange(c)
+        at = tables[s, j // B], slice(None), j % B
+        vc[at] = 0
+        for h in range(Hkv):
+            vc[tables[s, j // B], h, j % B, column[s][:, h]] = 0x38 if fp8 else 0x3F80
+    got = out_to_f64(_run((q, kc, vc, tables, start, ctx), G * Hkv, Hkv, D, B, n, fp8=fp8))
+    by = V_SCALE if fp8 else 1.0
+    by = float(np.float32(by))
+    for s, c in enumerate(ctxs):
+        for h in range(Hkv):
+            hits = np.zeros((c, D))
+            hits[np.arange(c), column[s][:, h]] = 1.0
+            total = hits.cumsum(0)
+            off = 2.0 ** -21 + c / 4 * 2.0 ** -24
+            for i in range(news[s]):
+                see = c - news[s] + i + 1
+                want = by * total[see - 1] / see
+                rows = got[start[s] + i, h * G:(h + 1) * G]
+                assert (np.abs(rows - want) <= off * want).all(), (s, h, i, np.abs(rows / want - 1).max())
+            if c > 2000:
+                part = np.add.reduceat(hits, np.arange(0, c, 16))
+                length = np.minimum(16, c - np.arange(0, c, 16))[:, None]
+                for sign in (-1, 1):
+                    moved = np.abs((total[-1] + sign * part) / (c + sign * length) * c / total[-1] - 1).max(1)
+                    assert moved[:-1].min() > 4 * off
