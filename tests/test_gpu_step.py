@@ -584,3 +584,30 @@ def test_a_refused_plan_shows_what_every_named_row_has(max_blocks, rows, new, he
         assert got[2] == [0] * 5 and got[3] == [-1] * 12 and got[4] == [-1] * 12
     for a, b in zip(before, (p.d_tables, p.d_blocks, p.d_count)):
         assert torch.equal(a, b)
+
+
+def test_the_readmes_example_runs_over_a_state_that_holds_together():
+    """The steps planned on the GPU keep to blocks of their own, attend to positions that they have written, and give
+    what the oracle gives over the cache as it is left."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    with open(path) as f:
+        (code,) = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    x = {}
+    exec(compile(code, "README.md", "exec"), x)
+    torch.cuda.synchronize()
+    B, NB, ctx, tables = x["B"], x["NB"], x["context_lens"].tolist(), x["block_tables"].cpu().numpy()
+    owned = set(x["alloc"].free_list())
+    assert ctx == [1004, 44] and x["row_lens"].tolist() == [1002, 44] and x["row_blocks"].tolist() == [0, 0]
+    assert sorted(x["free_blocks"].tolist()) == sorted(set(range(NB)) - owned) and x["free_count"].item() == NB - len(owned)
+    for t, c in zip(tables, ctx):
+        ids = t[:-(-c // B)]
+        assert not owned & set(ids.tolist())
+        slots = torch.from_numpy(ids[np.arange(c) // B]).long().cuda(), torch.from_numpy(np.arange(c) % B).cuda()
+        for cache in (x["k_cache"], x["v_cache"]):
+            assert (cache[slots[0], :, slots[1]] != 0).any(-1).all()
+    want = A.paged_multi(to_bits(x["q_out"]), to_bits(x["k_cache"]), to_bits(x["v_cache"]), tables,
+                         x["query_start"].tolist(), ctx, x["scale"], B)
+    off = np.abs(x["out"].double().cpu().numpy() - want)
+    assert (off <= 2.0 ** -8 * np.abs(want) + 2e-3).all()
