@@ -29,7 +29,9 @@
 //    (unroll 1): with one miss for five fetches instead of 25, 64 requests of
 //    8 tokens over E4M3 took 100 us instead of 68.
 //  * Every barrier is waited for in every phase, in order, by each of its
-//    waiters, so no wait can take an older phase's parity for its own.
+//    waiters, so no wait can take an older phase's parity for its own.  One
+//    exception: the softmax groups wait for p_done only when they rescale;
+//    why that wait can meet one phase alone stands there.
 //  * bf16: V stays bf16, so the weights enter P . V as two bf16 terms (hi +
 //    lo, a relative 2^-16).  Units of 64 rows lie in lanes 0-15 of each 32:
 //    the hi terms there and the lo terms in the other 16 lanes, so a single
@@ -721,7 +723,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool raise = fmaf(top, c, -m) > kSlack;
                 const float m_new = raise ? fmaf(top, c, kHeadroom) : m;
                 if (j > 0 && __any_sync(0xffffffffu, raise)) {
-                    // this group's O holds its halves of the tiles before, once their products are done
+                    // This group's O holds its halves of the tiles before, once their products are done.  The wait
+                    // is for tile at - 1's phase of its buffer's barrier, whatever was skipped: the phase before it,
+                    // tile at - 3's, is over, since the scores of tile at - 1 were issued after it and have been
+                    // read; and the one after it, tile at + 1's, takes weights that this warp has yet to give.
+                    // (Both hold for two score buffers; a third would need a wait in every phase.)
                     if (!(ok = wait_for(&ctl->p_done[b ^ 1], ((at - 1) >> 1) & 1, ctl, a.status))) break;
                     fence_after();
                     const float f = pa::exp2_approx(m - m_new);
