@@ -243,29 +243,29 @@ __global__ void __launch_bounds__(kRopeThreads, 4) heads_kernel(const RopeArgs a
 // Many: kSide heads of a token side by side (32 / (kSide D / 16) tokens per
 // warp), turn after turn, kFlight turns in flight, so that the angles and
 // the gains are loaded once for all of a token's heads.
-constexpr int kFlight = 4;
+constexpr int kFlight = 4, kSide = 2;
 
-template <int D, bool F8, bool kInterleaved, int kSide>
+template <int D, bool F8, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs a) {
-    constexpr int kLanes = D / 16, kHeads = kSide, kGroup = kLanes * kSide;
+    constexpr int kLanes = D / 16, kGroup = kLanes * kSide;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t t = blockIdx.x * (kRopeThreads / kGroup) + threadIdx.x / kGroup;
     if (t >= (uint32_t)a.num_tokens) return;           // whole tokens: a token's threads leave together
     const int lane = threadIdx.x % kGroup, l = lane % kLanes, g = lane / kLanes;
     const unsigned mask = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
-    const int q_turns = (a.n_q_heads + kHeads - 1) / kHeads, kv_turns = (a.n_kv_heads + kHeads - 1) / kHeads;
+    const int q_turns = (a.n_q_heads + kSide - 1) / kSide, kv_turns = (a.n_kv_heads + kSide - 1) / kSide;
     const Place<kInterleaved> w(l, a.rot_dim);
     const int pos = a.positions[t];
     const long long slot = a.slots[t];
     struct Raw {
         uint4 x0[kFlight], x1[kFlight];
     };
-    // heads (turn + u) * kHeads + g of a tensor's row
+    // heads (turn + u) * kSide + g of a tensor's row
     auto load = [&](const __nv_bfloat16* rows, int turn, int heads, Raw& r) {
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const int h = (turn + u) * kHeads + g;
+            const int h = (turn + u) * kSide + g;
             if (h < heads) {
                 const uint4* src = reinterpret_cast<const uint4*>(rows + h * D);
                 r.x0[u] = src[w.c0];
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs 
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             if (turn + u >= q_turns) break;
-            const int h = (turn + u) * kHeads + g;
+            const int h = (turn + u) * kSide + g;
             const Part p = work(now.x0[u], now.x1[u]);
             if (h < a.n_q_heads) {
                 uint4* dst = a.q_out + ((size_t)t * a.n_q_heads + h) * (D / 8);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs 
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             if (turn + u >= kv_turns) break;
-            const int h = (turn + u) * kHeads + g;
+            const int h = (turn + u) * kSide + g;
             const Part p = work(raw.x0[u], raw.x1[u]);
             if (h < a.n_kv_heads) put_part<F8>(a.k_cache, row0 + h * head, p, a.k_scale, w.c0, w.c1);
         }
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs 
         if (turn) load(v, turn, a.n_kv_heads, vraw);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const int h = (turn + u) * kHeads + g;
+            const int h = (turn + u) * kSide + g;
             if (h >= a.n_kv_heads) break;
             if constexpr (F8) {
                 Part p;
@@ -367,12 +367,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs 
 // enough to share its angles (2 + 2 x 1: 40,000 tokens 38.5 / 21.9).
 template <int D, bool F8, bool kInterleaved>
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
-    constexpr int kLanes = D / 16, kSide = 2;
+    constexpr int kLanes = D / 16;
     const int heads = a.n_q_heads + 2 * a.n_kv_heads;
     const long long rows = (long long)a.num_tokens * heads;
     if (heads >= 16 && rows * D >= 12000000) {
         const int per = kRopeThreads / (kLanes * kSide);
-        return pa_host::launch_dependent(tokens_kernel<D, F8, kInterleaved, kSide>,
+        return pa_host::launch_dependent(tokens_kernel<D, F8, kInterleaved>,
                                          dim3((unsigned)(((long long)a.num_tokens + per - 1) / per)), dim3(kRopeThreads), 0,
                                          st, a);
     }
