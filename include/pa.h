@@ -604,7 +604,8 @@ int pa_reshape_and_cache_fp8(void* k_cache, void* v_cache, const void* k,
  * token is touched.  A negative slot keeps the token's k and v out of the
  * cache.  A position from max_positions on is skipped and flagged
  * PA_DEV_BAD_POSITION; a slot outside the pool skips the write and is flagged
- * PA_DEV_BAD_SLOT.
+ * PA_DEV_BAD_SLOT.  Two tokens with the same slot in one call race, and their
+ * rows may mix.
  *   q_out         device bf16 [num_tokens][n_q_heads][d_head]; it may be q
  *                 itself if q is contiguous (q_stride n_q_heads * d_head;
  *                 PA_ERR_INVALID_ARG otherwise).

@@ -16,7 +16,7 @@
 // What bounds it: each K/V byte is read once for n * G rows, 4 * n * G
 // operations per two bytes, so the cache's bytes bound it.  64 sequences of
 // 4096 positions, 8 KV heads of 128, 16 rows: 168 us, 0.94 of the measured
-// copy rate; E4M3 97 us, 0.82 (there the unpacking of codes to f16 for
+// copy rate; E4M3 94 us, 0.85 (there the unpacking of codes to f16 for
 // warp-level products takes 44 % of the ALU's cycles).  The smallest steps
 // are a chain of latencies: 4 sequences of up to 37 positions take 4.7 us.
 //  * A unit is a (sequence, KV head, tile of 16 rows); its work is counted in
@@ -565,12 +565,20 @@ int sms() {
 
 // Whether the units of 64 (or 128) rows of pa_decode_wide.cu serve a call:
 // from more than 16 rows a KV head on, where they read the cache once and
-// units of 16 twice.  8 KV heads of 128, us here against there:
-//   sequences x positions   bf16, 16 rows   32 rows       E4M3, 16     32 rows
-//   64 x 4096               167 / 161       319 / 163     98 / 104     180 / 104
-//   512 x 500               172 / 168       349 / 176     127 / 152    242 / 154
-//   2048 x 60               200 / 341       -             210 / 469    -
-// (At 16 rows short contexts decide: a unit there costs some 3 to 4 us.)
+// units of 16 twice or more.  8 KV heads of 128, us here / there (batches in
+// turn, so that nothing stays in L2):
+//   sequences x positions   16 rows       20 rows       32 rows       64 rows
+//   bf16  64 x 4096         168 / 162     322 / 163     327 / 164     635 / 168
+//         512 x 500         166 / 167     329 / 169     342 / 174     710 / 192
+//         512 x 128          62 / 90      110 / 92      117 / 94      237 / 100
+//         2048 x 60         184 / 316     331 / 318     373 / 327     740 / 364
+//   E4M3  64 x 4096          94 / 100     174 / 100     175 / 101     338 / 108
+//         512 x 500         122 / 166     233 / 166     237 / 165     470 / 167
+//         512 x 128          64 / 125     117 / 133     119 / 140     237 / 157
+//         2048 x 60         197 / 459     373 / 499     392 / 511     767 / 585
+// (At 16 rows short contexts decide: a unit there costs some 3 to 5 us.  At 17
+// to 32 rows the rule is wrong for E4M3 contexts of a tile or less in many
+// sequences, which lose 14 to 30 % by it.)
 // Its bf16 products take a positive scale only; others go 16 rows at a time.
 bool is_wide(bool f8, float scale, long long rows) { return rows > kRows && (f8 || scale > 0.f); }
 

@@ -7,10 +7,15 @@
 // d_head 128) takes an SM about 1.46 us of its share of the memory's rate,
 // and its products, S = Q . K^T and O += P . V at 128 rows, 0.33 us each: the
 // bytes bound it as long as copies, products and softmax overlap.  64
-// sequences of 4096 positions, 8 KV heads of 128: 32 rows 166 us (0.96 of the
-// measured copy rate), 64 rows 171 (0.94), 128 rows 178 (0.91; 767 TFLOP/s).
-// E4M3: 32 rows 103 us (0.78), bound by the softmax of a tile, whose splitting
-// of the weights into four terms takes much of the ALU's cycles.
+// sequences of 4096 positions, 8 KV heads of 128: 32 rows 165 us (0.96 of the
+// measured copy rate), 64 rows 170 (0.94), 128 rows 174 (0.94; 789 TFLOP/s).
+// E4M3: 32 rows 101 us (0.80), 64 rows 107 (0.77); 128 rows, as two units that
+// read the cache each, 196 (0.43).  No unit of the SM is full there (ALU 44 %,
+// issue slots 51 %, tensor cores 39 %, DRAM 56 % on a ragged batch of 32 rows),
+// and a tile costs nearly the same with 20, 32 or 64 of its rows there: what
+// bounds it is a tile's chain of hand-overs, in which the softmax, with four
+// terms of each weight, is longer than bf16's.  How much of that is work on
+// rows that are not there, no counter tells.
 //  * One block per SM walks its share.  A producer warp each fills stages of
 //    K and V through the block table; one warp issues the score products of
 //    whole tiles, into two buffers in turn; two groups of four warps take the

@@ -17,8 +17,10 @@
 // packed pairs.  With many tokens the same threads take two heads of a token
 // at a time, one pair of heads after another, so that angles and gains are
 // loaded once for all of them: 32,048 tokens of 32 + 2 x 8 heads in 123 us,
-// 0.95 of the measured copy rate for their 790 MB.  With few, every head has
-// threads of its own: 4 tokens in 2.0 us, 250 of 256 (E4M3) in 3.6 us.
+// 0.95 of the measured copy rate for their 790 MB; into E4M3 caches, with an
+// IEEE division for each of their elements, in 145 us, 0.74 for 724 MB.  With
+// few, every head has threads of its own: 4 tokens in 2.0 us, 250 of 256 (E4M3)
+// in 3.5 us.
 
 #include "pa_common.cuh"
 
@@ -361,10 +363,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs 
 }
 
 // Which kernel: the one per token is faster from about 12 million elements
-// on (32 + 2 x 8 heads of 128: 1000 tokens 10.5 against 6.8 us, 2000 13.1 /
-// 13.9, 4000 18.2 / 24.5, 32,048 122.7 / 168; 16 + 2 x 2 of 64: 5000 tokens
-// 7.6 / 5.7, 10,000 12.5 / 12.9, 40,000 36.2 / 42.5), if a token has heads
-// enough to share its angles (2 + 2 x 1: 40,000 tokens 38.5 / 21.9).
+// on (32 + 2 x 8 heads of 128: 1000 tokens 10.0 against 6.5 us, 2000 13.1 /
+// 13.6, 4000 18.3 / 24.2, 32,048 122.9 / 168; E4M3 1000 13.9 / 7.0, 2000 16.8 /
+// 14.6, 4000 21.8 / 25.7, 32,048 144 / 180; 16 + 2 x 2 of 64: 5000 tokens 7.6 /
+// 5.7, 10,000 12.5 / 12.9, 40,000 36.2 / 42.5), if a token has heads enough to
+// share its angles (2 + 2 x 1: 40,000 tokens 38.5 / 21.9).
 template <int D, bool F8, bool kInterleaved>
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
     constexpr int kLanes = D / 16;
