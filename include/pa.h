@@ -490,6 +490,68 @@ size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads,
                                       int n_kv_heads, int d_head);
 
 /* ===========================================================================
+ * Attention of new tokens with shaped scores
+ * ===========================================================================
+ * The attention of pa_decode_multi, from one new token a sequence to whole
+ * prompts, for models that shape their scores.  With C = context_lens[s], n
+ * new tokens (rows query_start[s] .. query_start[s + 1] - 1 of q and out) and
+ * p = C - n + i the position of new token i, for each query head h:
+ *
+ *   s_j = scale * q . k_j
+ *   s_j = softcap * tanh(s_j / softcap)            (softcap 0: as it is)
+ *   s_j = s_j - slopes[h] * |p - j|                (slopes NULL: as it is)
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j)      over the positions j < C
+ *         with visible[t][0] <= j < visible[t][1]  (visible NULL: j <= p)
+ *
+ * The interval of a token gives a sliding window (p - W + 1, p + 1), the
+ * document it belongs to (begin, p + 1), a prefix or an image whose positions
+ * see one another (.., end); it is clipped to [0, C).  A token whose interval
+ * is empty gets zeros.  Positions outside it do not reach the token's row,
+ * whatever they hold.  Sums and statistics are fp32, outputs rounded once.
+ *   visible       device int32 [num_tokens][2], 8-byte aligned, or NULL.
+ *   slopes        device f32 [n_q_heads], finite, or NULL.
+ *   softcap       finite, >= 0; scale finite (PA_ERR_INVALID_ARG otherwise).
+ *   workspace     as for pa_decode_multi, of pa_attend_workspace_size bytes
+ *                 for the same arguments.
+ * Everything else (shapes, alignment, sequences that are flagged and not
+ * computed) is as for pa_decode_multi. */
+int pa_attend(void* out, int out_dtype, const void* q, const void* k_cache,
+              const void* v_cache, const int32_t* block_tables,
+              const int32_t* query_start, const int32_t* context_lens,
+              const int32_t* visible, const float* slopes, float softcap,
+              int block_size, float scale, int n_q_heads, int n_kv_heads,
+              int d_head, int num_seqs, int num_tokens, int max_query_len,
+              int max_blocks_per_seq, int num_blocks, int max_context_len,
+              void* workspace, size_t workspace_bytes, int32_t* status_dev,
+              void* stream);
+
+/* pa_attend over a block-scaled cache: E4M3 codes with a power-of-two scale
+ * for each block and KV head, the element being
+ *   code * 2^(k_scales[block][h] - 127)            (v_scales for values)
+ * as pa_qk_norm_rope_cache_scaled and pa_reshape_and_cache_scaled write them
+ * (bytes 0 .. 254; 255 is no scale).  d_head 128.
+ *   k_scales, v_scales  device uint8 [num_blocks][n_kv_heads]. */
+int pa_attend_scaled(void* out, int out_dtype, const void* q,
+                     const void* k_cache, const void* v_cache,
+                     const uint8_t* k_scales, const uint8_t* v_scales,
+                     const int32_t* block_tables, const int32_t* query_start,
+                     const int32_t* context_lens, const int32_t* visible,
+                     const float* slopes, float softcap, int block_size,
+                     float scale, int n_q_heads, int n_kv_heads, int d_head,
+                     int num_seqs, int num_tokens, int max_query_len,
+                     int max_blocks_per_seq, int num_blocks,
+                     int max_context_len, void* workspace,
+                     size_t workspace_bytes, int32_t* status_dev,
+                     void* stream);
+
+/* Bytes of workspace pa_attend, or (scaled != 0) pa_attend_scaled, needs on
+ * the current device (0 for a non-positive argument). */
+size_t pa_attend_workspace_size(int num_seqs, int max_query_len,
+                                int max_blocks_per_seq, int block_size,
+                                int n_q_heads, int n_kv_heads, int d_head,
+                                int scaled);
+
+/* ===========================================================================
  * Planning a step on the GPU
  * ===========================================================================
  * The metadata of a serving step from device-resident lengths ([P1] sections
@@ -648,6 +710,92 @@ int pa_qk_norm_rope_cache_fp8(void* q_out, void* k_cache, void* v_cache,
                               int block_size, int num_blocks, float k_scale,
                               float v_scale, int32_t* status_dev,
                               void* stream);
+
+/* pa_qk_norm_rope_cache for positions of several axes (time, height and width
+ * of images and video): pair c turns by
+ *   cos_sin[positions[axis_of_pair[c]][t]][c] and [R / 2 + c].
+ * A token with a negative position on any axis is padding; one from
+ * max_positions on, on any, is skipped and flagged.
+ *   positions     device int32 [num_axes][num_tokens], num_axes 1 .. 4.
+ *   axis_of_pair  HOST int8 [rot_dim / 2], each in [0, num_axes)
+ *                 (PA_ERR_INVALID_ARG otherwise); read during the call. */
+int pa_qk_norm_mrope_cache(void* q_out, void* k_cache, void* v_cache,
+                           const void* q, const void* k, const void* v,
+                           int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const float* q_weight,
+                           const float* k_weight, float eps,
+                           const float* cos_sin, int max_positions,
+                           int rot_dim, int interleaved,
+                           const int32_t* positions, int num_axes,
+                           const int8_t* axis_of_pair,
+                           const int64_t* slot_mapping, int num_tokens,
+                           int n_q_heads, int n_kv_heads, int d_head,
+                           int block_size, int num_blocks,
+                           int32_t* status_dev, void* stream);
+
+/* The like for FP8 caches, as pa_qk_norm_rope_cache_fp8. */
+int pa_qk_norm_mrope_cache_fp8(void* q_out, void* k_cache, void* v_cache,
+                               const void* q, const void* k, const void* v,
+                               int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, const float* q_weight,
+                               const float* k_weight, float eps,
+                               const float* cos_sin, int max_positions,
+                               int rot_dim, int interleaved,
+                               const int32_t* positions, int num_axes,
+                               const int8_t* axis_of_pair,
+                               const int64_t* slot_mapping, int num_tokens,
+                               int n_q_heads, int n_kv_heads, int d_head,
+                               int block_size, int num_blocks, float k_scale,
+                               float v_scale, int32_t* status_dev,
+                               void* stream);
+
+/* pa_qk_norm_rope_cache (num_axes 0, positions [num_tokens]) or
+ * pa_qk_norm_mrope_cache into a block-scaled cache: E4M3 codes with a scale
+ * 2^(byte - 127) for each block and KV head, of keys and of values.  For each
+ * block and head that the call writes to,
+ *
+ *   e = the least with |y| <= 448 * 2^e for all (finite) fp32 values y that
+ *       the call writes there, at least -127; and at least the block's e
+ *       before, unless the call writes the block's offset 0, which begins it
+ *       anew;
+ *   code = E4M3(y * 2^-e), rounded once to nearest even, infinities to +-448,
+ *       NaN kept; the block's codes at other offsets, where e has grown by k,
+ *       become E4M3(code * 2^-k).
+ *
+ * So the positions of a block are written from offset 0 on, in one call or in
+ * several, as they come; rewriting the last ones (a draft's) is writing on.
+ * The tokens of one block must follow one another in the call, in the order
+ * of their slots, as pa_plan_step and pa_alloc_slot_mapping give them (of one
+ * that the call takes up twice, the scale is that of one of the two, and codes
+ * may be of the other).
+ *   k_scales, v_scales  device uint8 [num_blocks][n_kv_heads]; those of blocks
+ *                 not begun yet are not read.  A block's copy takes its two
+ *                 rows of them along. */
+int pa_qk_norm_rope_cache_scaled(void* q_out, void* k_cache, void* v_cache,
+                                 uint8_t* k_scales, uint8_t* v_scales,
+                                 const void* q, const void* k, const void* v,
+                                 int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, const float* q_weight,
+                                 const float* k_weight, float eps,
+                                 const float* cos_sin, int max_positions,
+                                 int rot_dim, int interleaved,
+                                 const int32_t* positions, int num_axes,
+                                 const int8_t* axis_of_pair,
+                                 const int64_t* slot_mapping, int num_tokens,
+                                 int n_q_heads, int n_kv_heads, int d_head,
+                                 int block_size, int num_blocks,
+                                 int32_t* status_dev, void* stream);
+
+/* The append alone, of bf16 keys and values as they are (models without
+ * rotation): k, v as for pa_qk_norm_rope_cache, with their strides. */
+int pa_reshape_and_cache_scaled(void* k_cache, void* v_cache,
+                                uint8_t* k_scales, uint8_t* v_scales,
+                                const void* k, const void* v,
+                                int64_t k_stride, int64_t v_stride,
+                                const int64_t* slot_mapping, int num_tokens,
+                                int n_kv_heads, int d_head, int block_size,
+                                int num_blocks, int32_t* status_dev,
+                                void* stream);
 
 /* copy_blocks: the copy-on-write clone of a shared tail block ([P1]
  * sections 15 and 16): for every pair (src, dst) = (block_pairs[2i],

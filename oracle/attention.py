@@ -200,6 +200,44 @@ def paged_multi(q, k_cache, v_cache, block_tables, query_start, context_lens, sc
     return out
 
 
+def shaped_scores(q, K, scale, position, softcap=0.0, slope=0.0):
+    """One row's scores over the positions of K, shaped: s = scale q . k_j, then
+    softcap tanh(s / softcap) if softcap is not 0, less slope |position - j|."""
+    s = scale * (np.asarray(K, dtype=np.float64) @ np.asarray(q, dtype=np.float64))
+    if softcap:
+        s = softcap * np.tanh(s / softcap)
+    return s - slope * np.abs(position - np.arange(len(s)))
+
+
+def paged_shaped(q, k_cache, v_cache, block_tables, query_start, context_lens, scale, block_size, visible=None,
+                 softcap=0.0, slopes=None):
+    """Attention of each sequence's n new tokens (its last positions) with
+    shaped scores: row t sees the positions visible[t][0] <= j < visible[t][1]
+    of its context (None: up to its own).  A row that sees nothing is zeros."""
+    if q.dtype == np.uint16:
+        q = bf16_to_f64(q)
+    T, n_q_heads, d_head = q.shape
+    n_kv_heads = k_cache.shape[1]
+    out = np.zeros((T, n_q_heads, d_head), dtype=np.float64)
+    for s in range(len(context_lens)):
+        C, row0 = int(context_lens[s]), int(query_start[s])
+        n = int(query_start[s + 1]) - row0
+        if n <= 0:
+            continue
+        K, V = gather_kv(k_cache, v_cache, block_tables[s], C, block_size)
+        for i in range(n):
+            p = C + i - n
+            lo, hi = (0, p + 1) if visible is None else (max(0, int(visible[row0 + i][0])), min(C, int(visible[row0 + i][1])))
+            if lo >= hi:
+                continue
+            for g in range(n_q_heads):
+                h = kv_head_of(g, n_q_heads, n_kv_heads)
+                x = shaped_scores(q[row0 + i][g], K[h][:hi], scale, p, softcap, 0.0 if slopes is None else float(slopes[g]))[lo:]
+                e = np.exp(x - x.max())
+                out[row0 + i, g, :] = e @ V[h][lo:hi] / e.sum()
+    return out
+
+
 # ----------------------------------------------------------------------------
 # Split computation and exact merge ([P2] sections 10 and 11)
 # ----------------------------------------------------------------------------

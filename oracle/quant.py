@@ -76,3 +76,49 @@ def quantize(x, scale):
 def dequantize(codes, scale):
     """float64 values of codes at one float32 scale."""
     return e4m3_to_f64(codes) * float(np.float32(scale))
+
+
+# ----------------------------------------------------------------------------
+# Block-scaled caches: codes times a power of two for each block and head
+# ----------------------------------------------------------------------------
+
+def least_exponent(top):
+    """The least e >= -127 with top <= 448 * 2^e."""
+    e = -127
+    while top > 448.0 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def append_scaled(codes, scales, x, slots, block_size):
+    """Append x [T, H, D] (float64) at slots, token by token of each block's
+    run: codes [NB, H, B, D] and scales [NB, H] (bytes: e + 127) are changed in
+    place.  The tokens of a block follow one another; negative slots are none."""
+    t = 0
+    while t < len(slots):
+        if slots[t] < 0:
+            t += 1
+            continue
+        block, first = slots[t] // block_size, slots[t] % block_size
+        run = [t]
+        while t + 1 < len(slots) and slots[t + 1] == slots[t] + 1 and slots[t + 1] // block_size == block:
+            t += 1
+            run.append(t)
+        t += 1
+        for h in range(codes.shape[1]):
+            y = np.asarray(x, dtype=np.float64)[run, h]
+            sizes = np.abs(y[np.isfinite(y)])
+            e = least_exponent(sizes.max() if sizes.size else 0.0)
+            if first:
+                old = int(scales[block, h]) - 127
+                e = max(e, old)
+                if e > old:
+                    others = [o for o in range(block_size) if not first <= o < first + len(run)]
+                    codes[block, h, others] = f64_to_e4m3(e4m3_to_f64(codes[block, h, others]) * 2.0 ** (old - e))
+            codes[block, h, first:first + len(run)] = f64_to_e4m3(y * 2.0 ** -e)
+            scales[block, h] = e + 127
+
+
+def dequantize_scaled(codes, scales):
+    """The elements of a block-scaled cache, float64."""
+    return e4m3_to_f64(codes) * 2.0 ** (scales.astype(np.float64) - 127)[..., None, None]

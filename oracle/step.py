@@ -55,14 +55,15 @@ def release_rows(rows, row_tables, row_blocks, free_list):
 
 
 def norm_rope(x, gain, eps, position, rot_dim, interleaved, base=10000.0):
-    """One head's row x [d] (float64) normed and turned; gain None: no norm."""
+    """One head's row x [d] (float64) normed and turned; gain None: no norm.
+    position: one for all pairs, or a sequence with one for each (of its axis)."""
     y = np.asarray(x, dtype=np.float64)
     if gain is not None:
         y = y / np.sqrt(np.sum(y * y) / len(y) + eps) * np.asarray(gain, dtype=np.float64)
     y = y.copy()
     half = rot_dim // 2
     for c in range(half):
-        angle = position * base ** (-2.0 * c / rot_dim)
+        angle = (position if np.ndim(position) == 0 else position[c]) * base ** (-2.0 * c / rot_dim)
         i, j = (2 * c, 2 * c + 1) if interleaved else (c, c + half)
         a, b = y[i], y[j]
         y[i] = a * np.cos(angle) - b * np.sin(angle)

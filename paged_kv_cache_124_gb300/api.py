@@ -112,6 +112,25 @@ _SIGS = {
                                            ctypes.c_int64, _vp, _vp, _c_float, _vp, _c_int, _c_int, _c_int, _vp, _vp,
                                            _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_float, _vp,
                                            _vp]),
+    "pa_qk_norm_mrope_cache": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                        _vp, _vp, _c_float, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _c_int,
+                                        _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pa_qk_norm_mrope_cache_fp8": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_int64, _vp, _vp, _c_float, _vp, _c_int, _c_int, _c_int, _vp,
+                                            _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
+                                            _c_float, _vp, _vp]),
+    "pa_qk_norm_rope_cache_scaled": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64,
+                                              ctypes.c_int64, _vp, _vp, _c_float, _vp, _c_int, _c_int, _c_int, _vp,
+                                              _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
+                                              _vp]),
+    "pa_reshape_and_cache_scaled": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _c_int,
+                                             _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pa_attend": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_float, _c_int, _c_float, _c_int, _c_int,
+                           _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp, _vp]),
+    "pa_attend_scaled": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_float, _c_int, _c_float,
+                                  _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_size,
+                                  _vp, _vp]),
+    "pa_attend_workspace_size": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "pa_check_bounded_wait": (_c_int, [_c_int, _vp, _vp]),
     "pa_lse_merge": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
     "pa_reshape_and_cache": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
@@ -688,6 +707,65 @@ def pa_qk_norm_rope_cache(q_out, k_cache, v_cache, q, k, v, positions, slot_mapp
                   "pa_qk_norm_rope_cache" if k_scale is None else "pa_qk_norm_rope_cache_fp8")
 
 
+def rope_axes(sections, interleaved=False):
+    """The axis of each rotated pair, for pa_qk_norm_mrope_cache: sections[a]
+    pairs of axis a, axis after axis, or (interleaved) the axes in turn while
+    they have pairs left."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0:
+        raise ValueError("sections must be counts of pairs, one an axis")
+    if not interleaved:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    axes = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                axes.append(a)
+                left[a] -= 1
+    return bytes(axes)
+
+
+def pa_qk_norm_mrope_cache(q_out, k_cache, v_cache, q, k, v, positions, axes, slot_mapping, cos_sin, q_weight=None,
+                           k_weight=None, eps=1e-6, interleaved=False, status=None, stream=None, k_scale=None,
+                           v_scale=None):
+    """pa_qk_norm_rope_cache for positions of several axes: positions [A, T]
+    (int32), and pair c turned by the position on axis axes[c] (a sequence of
+    rot_dim / 2 integers; see rope_axes); see pa.h."""
+    dev = torch.cuda.current_device()
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("pa_qk_norm_mrope_cache: k_scale and v_scale go together")
+    if axes is None:
+        raise TypeError("pa_qk_norm_mrope_cache: axes must be a sequence of integers")
+    return _check(_step_calls.qk_norm_mrope_cache(q_out, k_cache, v_cache, q, k, v, positions, axes, slot_mapping, cos_sin,
+                                                  q_weight, k_weight, eps, bool(interleaved), status, k_scale, v_scale,
+                                                  None, None, dev, _raw_stream(stream, dev)),
+                  "pa_qk_norm_mrope_cache" if k_scale is None else "pa_qk_norm_mrope_cache_fp8")
+
+
+def pa_qk_norm_rope_cache_scaled(q_out, k_cache, v_cache, k_scales, v_scales, q, k, v, positions, slot_mapping, cos_sin,
+                                 axes=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, status=None,
+                                 stream=None):
+    """pa_qk_norm_rope_cache into a block-scaled cache: E4M3 codes (uint8
+    [num_blocks, Hkv, B, D]) with scales (uint8 [num_blocks, Hkv], biased
+    powers of two) that cover each block's values and grow with what is
+    appended; with axes, positions [A, T] as pa_qk_norm_mrope_cache.  The
+    tokens of a block follow one another, from its offset 0 on; see pa.h."""
+    dev = torch.cuda.current_device()
+    if k_scales is None or v_scales is None:
+        raise TypeError("pa_qk_norm_rope_cache_scaled: k_scales and v_scales must be torch.Tensors")
+    return _check(_step_calls.qk_norm_mrope_cache(q_out, k_cache, v_cache, q, k, v, positions, axes, slot_mapping, cos_sin,
+                                                  q_weight, k_weight, eps, bool(interleaved), status, None, None, k_scales,
+                                                  v_scales, dev, _raw_stream(stream, dev)),
+                  "pa_qk_norm_rope_cache_scaled")
+
+
+def pa_reshape_and_cache_scaled(k_cache, v_cache, k_scales, v_scales, k, v, slot_mapping, status=None, stream=None):
+    """Append k[t], v[t] ([T, Hkv, D] bf16) at the slots slot_mapping[t] of a block-scaled cache; see pa.h."""
+    dev = torch.cuda.current_device()
+    return _check(_step_calls.reshape_and_cache_scaled(k_cache, v_cache, k_scales, v_scales, k, v, slot_mapping, status, dev,
+                                                       _raw_stream(stream, dev)), "pa_reshape_and_cache_scaled")
+
+
 def pa_decode_multi_workspace_size(max_query_len, n_q_heads, n_kv_heads, d_head):
     return int(_lib.pa_decode_multi_workspace_size(int(max_query_len), int(n_q_heads), int(n_kv_heads), int(d_head)))
 
@@ -718,6 +796,45 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, query_start, context
                                            block_size, scale, n_q_heads, n_kv_heads, d_head, max_context_len, tree_mask,
                                            workspace, status, k_scale, v_scale, dev, _raw_stream(stream, dev)),
                   "pa_decode_multi" if k_scale is None else "pa_decode_multi_fp8")
+
+
+def pa_attend_workspace_size(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads, n_kv_heads, d_head,
+                             scaled=False):
+    return int(_lib.pa_attend_workspace_size(int(num_seqs), int(max_query_len), int(max_blocks_per_seq), int(block_size),
+                                             int(n_q_heads), int(n_kv_heads), int(d_head), int(bool(scaled))))
+
+
+def attend_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads, n_kv_heads, d_head, scaled=False,
+                     device=None):
+    """A caller-owned workspace tensor (uint8) of the size pa_attend needs (scaled: over a block-scaled cache)."""
+    n = pa_attend_workspace_size(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads, n_kv_heads, d_head,
+                                 scaled)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_attend(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len, block_size, scale,
+              n_q_heads, n_kv_heads, d_head, max_context_len, visible=None, softcap=0.0, slopes=None, k_scales=None,
+              v_scales=None, workspace=None, status=None, stream=None):
+    """out [T, Hq, D] (bf16 or f32) <- attention of each sequence's new tokens
+    (rows query_start[s] .. query_start[s + 1], one or a whole prompt) over its
+    paged cache, with scores softcap * tanh(s / softcap) (softcap 0: s) less
+    slopes[h] * distance (slopes: float32 [Hq]), over the positions
+    visible[t, 0] <= j < visible[t, 1] of each token (int32 [T, 2]; default:
+    causal).  With k_scales / v_scales (uint8 [num_blocks, Hkv]), over a
+    block-scaled cache (uint8 codes).  workspace: a uint8 tensor from
+    attend_workspace (default: one allocated for this call through PyTorch's
+    caching allocator, on the stream of the call); see pa.h."""
+    dev = torch.cuda.current_device()
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("pa_attend: k_scales and v_scales go together")
+    if workspace is None:
+        with _allocating_for(stream):
+            workspace = attend_workspace(block_tables.shape[0], max_query_len, block_tables.shape[1], block_size, n_q_heads,
+                                         n_kv_heads, d_head, k_scales is not None)
+    return _check(_step_calls.attend(out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len,
+                                     block_size, scale, n_q_heads, n_kv_heads, d_head, max_context_len, visible, softcap,
+                                     slopes, k_scales, v_scales, workspace, status, dev, _raw_stream(stream, dev)),
+                  "pa_attend" if k_scales is None else "pa_attend_scaled")
 
 
 # ----------------------------------------------------------------------------

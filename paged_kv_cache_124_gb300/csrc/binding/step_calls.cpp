@@ -1,5 +1,5 @@
 // The binding's calls of the step operators (planning, norm + rotation + cache
-// write, attention of new tokens): tensors checked, turned into pointers and
+// write, attention of new tokens, plain and shaped): tensors checked, turned into pointers and
 // passed to the library's entry points in one native call.
 //
 // A step's kernels take 2 to 10 us on small batches; checking a dozen tensors
@@ -107,6 +107,26 @@ class Call {
             refuse(PyExc_ValueError, name, "must have the heads of a token contiguous");
         stride = tokens > 1 ? t.stride(0) : heads * d;
         return const_cast<void*>(t.const_data_ptr());
+    }
+
+    // A sequence of at most 64 small integers (bytes serve), its length in `n`.
+    void small_ints(int i, const char* name, int8_t (&to)[64], int& n) const {
+        PyObject* fast = PySequence_Fast(args_[i], "");
+        if (!fast) {
+            PyErr_Clear();
+            refuse(PyExc_TypeError, name, "must be a sequence of integers");
+        }
+        const Py_ssize_t size = PySequence_Fast_GET_SIZE(fast);
+        bool fits = size <= 64;
+        for (Py_ssize_t k = 0; fits && k < size; ++k) {
+            const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(fast, k));
+            fits = !(v == -1 && PyErr_Occurred()) && v >= -128 && v < 128;
+            if (fits) to[k] = static_cast<int8_t>(v);
+        }
+        Py_DECREF(fast);
+        PyErr_Clear();
+        if (!fits) refuse(PyExc_ValueError, name, "must be at most 64 small integers");
+        n = static_cast<int>(size);
     }
 
   private:
@@ -293,9 +313,147 @@ PyObject* decode_multi(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// The axes of a rotation: positions [T] (axes None) or [A, T], and the axis of each pair.
+struct Axes {
+    const void* positions;
+    int8_t of_pair[64];
+    int num = 0;
+    Axes(const Call& c, int at, int axes_at, int64_t T, int rot) {
+        if (c.none(axes_at)) {
+            positions = c.at_(at, "positions", at::kInt, {T});
+            return;
+        }
+        num = c.size(c.tensor(at, "positions", 2).size(0));
+        positions = c.at_(at, "positions", at::kInt, {num, T});
+        int pairs;
+        c.small_ints(axes_at, "axes", of_pair, pairs);
+        if (2 * pairs != rot) throw Refused{PyExc_ValueError, "axes must have one entry for each pair that cos_sin turns"};
+        if (num == 0) throw Refused{PyExc_ValueError, "positions must have an axis"};
+    }
+};
+
+// (q_out, k_cache, v_cache, q, k, v, positions, axes, slot_mapping, cos_sin, q_weight, k_weight, eps, interleaved, status,
+//  k_scale, v_scale, k_scales, v_scales, device, stream)
+PyObject* qk_norm_mrope_cache(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded("pa_qk_norm_mrope_cache", args, n, 21, [](const Call& c) {
+        const at::Tensor& queries = c.tensor(3, "q", 3);
+        const at::Tensor& cache = c.tensor(1, "k_cache", 4);
+        const int64_t T = queries.size(0), Hq = queries.size(1), D = queries.size(2);
+        const int64_t NB = cache.size(0), Hkv = cache.size(1), B = cache.size(2);
+        const bool scaled = !c.none(17), f8 = !c.none(15);
+        const at::ScalarType type = f8 || scaled ? at::kByte : at::kBFloat16;
+        int64_t qs, ks, vs;
+        void* q = c.token_rows(3, "q", T, Hq, D, qs);
+        void* k = c.token_rows(4, "k", T, Hkv, D, ks);
+        void* v = c.token_rows(5, "v", T, Hkv, D, vs);
+        void* q_out = c.at_(0, "q_out", at::kBFloat16, {T, Hq, D});
+        void* k_cache = c.at_(1, "k_cache", type, {NB, Hkv, B, D});
+        void* v_cache = c.at_(2, "v_cache", type, {NB, Hkv, B, D});
+        const at::Tensor& table = c.tensor(9, "cos_sin", 2);
+        const int max_positions = c.size(table.size(0)), rot = c.size(table.size(1));
+        const Axes axes(c, 6, 7, T, rot);
+        void* slots = c.at_(8, "slot_mapping", at::kLong, {T});
+        void* cos_sin = c.any(9, "cos_sin", at::kFloat);
+        void* q_weight = c.optional(10, "q_weight", at::kFloat, {D});
+        void* k_weight = c.optional(11, "k_weight", at::kFloat, {D});
+        const float eps = c.number(12);
+        const int inter = c.integer(13) != 0;
+        void* status = c.optional(14, "status", at::kInt);
+        const float k_scale = f8 ? c.number(15) : 0.f, v_scale = f8 ? c.number(16) : 0.f;
+        void* k_scales = c.optional(17, "k_scales", at::kByte, {NB, Hkv});
+        void* v_scales = scaled ? c.at_(18, "v_scales", at::kByte, {NB, Hkv}) : nullptr;
+        const int tokens = c.size(T), hq = c.size(Hq), hkv = c.size(Hkv), d = c.size(D), b = c.size(B), nb = c.size(NB);
+        if (tokens == 0) return (int)PA_OK;                      // (empty tensors have no address)
+        const int32_t* at = static_cast<const int32_t*>(axes.positions);
+        return unlocked([&] {
+            if (scaled)
+                return pa_qk_norm_rope_cache_scaled(q_out, k_cache, v_cache, as<uint8_t>(k_scales), as<uint8_t>(v_scales), q, k, v,
+                                                    qs, ks, vs, as<float>(q_weight), as<float>(k_weight), eps, as<float>(cos_sin),
+                                                    max_positions, rot, inter, at, axes.num, axes.of_pair, as<int64_t>(slots),
+                                                    tokens, hq, hkv, d, b, nb, as<int32_t>(status), c.stream());
+            if (f8)
+                return pa_qk_norm_mrope_cache_fp8(q_out, k_cache, v_cache, q, k, v, qs, ks, vs, as<float>(q_weight),
+                                                  as<float>(k_weight), eps, as<float>(cos_sin), max_positions, rot, inter, at,
+                                                  axes.num, axes.of_pair, as<int64_t>(slots), tokens, hq, hkv, d, b, nb, k_scale,
+                                                  v_scale, as<int32_t>(status), c.stream());
+            return pa_qk_norm_mrope_cache(q_out, k_cache, v_cache, q, k, v, qs, ks, vs, as<float>(q_weight), as<float>(k_weight),
+                                          eps, as<float>(cos_sin), max_positions, rot, inter, at, axes.num, axes.of_pair,
+                                          as<int64_t>(slots), tokens, hq, hkv, d, b, nb, as<int32_t>(status), c.stream());
+        });
+    });
+}
+
+// (k_cache, v_cache, k_scales, v_scales, k, v, slot_mapping, status, device, stream)
+PyObject* reshape_and_cache_scaled(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded("pa_reshape_and_cache_scaled", args, n, 10, [](const Call& c) {
+        const at::Tensor& cache = c.tensor(0, "k_cache", 4);
+        const int64_t NB = cache.size(0), Hkv = cache.size(1), B = cache.size(2), D = cache.size(3);
+        const int64_t T = c.tensor(6, "slot_mapping", 1).size(0);
+        int64_t ks, vs;
+        void* k_cache = c.at_(0, "k_cache", at::kByte, {NB, Hkv, B, D});
+        void* v_cache = c.at_(1, "v_cache", at::kByte, {NB, Hkv, B, D});
+        void* k_scales = c.at_(2, "k_scales", at::kByte, {NB, Hkv});
+        void* v_scales = c.at_(3, "v_scales", at::kByte, {NB, Hkv});
+        void* k = c.token_rows(4, "k", T, Hkv, D, ks);
+        void* v = c.token_rows(5, "v", T, Hkv, D, vs);
+        void* slots = c.at_(6, "slot_mapping", at::kLong, {T});
+        void* status = c.optional(7, "status", at::kInt);
+        const int tokens = c.size(T), hkv = c.size(Hkv), d = c.size(D), b = c.size(B), nb = c.size(NB);
+        if (tokens == 0) return (int)PA_OK;
+        return unlocked([&] {
+            return pa_reshape_and_cache_scaled(k_cache, v_cache, as<uint8_t>(k_scales), as<uint8_t>(v_scales), k, v, ks, vs,
+                                               as<int64_t>(slots), tokens, hkv, d, b, nb, as<int32_t>(status), c.stream());
+        });
+    });
+}
+
+// (out, q, k_cache, v_cache, block_tables, query_start, context_lens, max_query_len, block_size, scale, n_q_heads,
+//  n_kv_heads, d_head, max_context_len, visible, softcap, slopes, k_scales, v_scales, workspace, status, device, stream)
+PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded("pa_attend", args, n, 23, [](const Call& c) {
+        const at::Tensor& result = c.tensor(0, "out");
+        if (result.scalar_type() != at::kBFloat16 && result.scalar_type() != at::kFloat)
+            throw Refused{PyExc_TypeError, "pa_attend: out must be bfloat16 or float32"};
+        const int64_t T = c.tensor(1, "q", 3).size(0), NB = c.tensor(2, "k_cache", 4).size(0);
+        const at::Tensor& entries = c.tensor(4, "block_tables", 2);
+        const int64_t S = entries.size(0), MB = entries.size(1);
+        const int most = c.integer(7), B = c.integer(8), Hq = c.integer(10), Hkv = c.integer(11), D = c.integer(12),
+                  max_ctx = c.integer(13);
+        const float scale = c.number(9), cap = c.number(15);
+        const bool scaled = !c.none(17);
+        const at::ScalarType type = scaled ? at::kByte : at::kBFloat16;
+        void* out = c.at_(0, "out", result.scalar_type(), {T, Hq, D});
+        void* q = c.at_(1, "q", at::kBFloat16, {T, Hq, D});
+        void* k = c.at_(2, "k_cache", type, {NB, Hkv, B, D});
+        void* v = c.at_(3, "v_cache", type, {NB, Hkv, B, D});
+        void* tables = c.at_(4, "block_tables", at::kInt, {S, MB});
+        void* start = c.at_(5, "query_start", at::kInt, {S + 1});
+        void* ctx = c.at_(6, "context_lens", at::kInt, {S});
+        void* visible = c.optional(14, "visible", at::kInt, {T, 2});
+        void* slopes = c.optional(16, "slopes", at::kFloat, {Hq});
+        void* k_scales = c.optional(17, "k_scales", at::kByte, {NB, Hkv});
+        void* v_scales = scaled ? c.at_(18, "v_scales", at::kByte, {NB, Hkv}) : nullptr;
+        void* ws = c.any(19, "workspace", at::kByte);
+        const size_t ws_bytes = static_cast<size_t>(c.tensor(19, "workspace").numel());
+        void* status = c.optional(20, "status", at::kInt);
+        const int dtype = result.scalar_type() == at::kFloat ? PA_DTYPE_F32 : PA_DTYPE_BF16;
+        const int seqs = c.size(S), width = c.size(MB), tokens = c.size(T), nb = c.size(NB);
+        return unlocked([&] {
+            return scaled ? pa_attend_scaled(out, dtype, q, k, v, as<uint8_t>(k_scales), as<uint8_t>(v_scales), as<int32_t>(tables),
+                                             as<int32_t>(start), as<int32_t>(ctx), as<int32_t>(visible), as<float>(slopes), cap, B,
+                                             scale, Hq, Hkv, D, seqs, tokens, most, width, nb, max_ctx, ws, ws_bytes,
+                                             as<int32_t>(status), c.stream())
+                          : pa_attend(out, dtype, q, k, v, as<int32_t>(tables), as<int32_t>(start), as<int32_t>(ctx),
+                                      as<int32_t>(visible), as<float>(slopes), cap, B, scale, Hq, Hkv, D, seqs, tokens, most, width,
+                                      nb, max_ctx, ws, ws_bytes, as<int32_t>(status), c.stream());
+        });
+    });
+}
+
 #define PA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_METHOD(plan_step), PA_METHOD(release_rows), PA_METHOD(qk_norm_rope_cache),
-                         PA_METHOD(decode_multi), {nullptr, nullptr, 0, nullptr}};
+                         PA_METHOD(decode_multi), PA_METHOD(qk_norm_mrope_cache), PA_METHOD(reshape_and_cache_scaled),
+                         PA_METHOD(attend), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

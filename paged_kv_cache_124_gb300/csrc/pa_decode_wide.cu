@@ -969,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int d = 0; d < D; d += 4)                   // (to what the thread itself has written)
                     if (!kHalf || (d & 16) == (lane & 16))
-                        add_unfinite<D, F8>(a, seq, kvh, row, st0 * kKv, end * kKv, d, whole ? nullptr : a.part_u + at * D + d);
+                        add_unfinite<D, F8, kKv>(a, seq, kvh, row, st0 * kKv, end * kKv, d, whole ? nullptr : a.part_u + at * D + d);
         }
     }
     fence_before();

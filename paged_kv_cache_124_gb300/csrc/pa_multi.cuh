@@ -20,7 +20,38 @@ constexpr float kRaise = 8.0f;             // log2 of the largest weight before 
 constexpr int kMaxProbes = 2000000;        // ~2 s bound on any single wait
 constexpr int kMergeThreads = 256;
 
+// A sequence's part of the call.
+struct Seq {
+    int q0, n, ctx, steps, tiles;
+    // tiles is 0 where nothing is to be done; cost: steps that starting and joining a unit is worth
+    __device__ __forceinline__ long long work(int heads, int cost) const {
+        return (long long)heads * tiles * (steps + cost);
+    }
+};
+
+// The stretch of one unit that a block computes: steps st0 .. st0 + len - 1.
+struct Unit {
+    int q0, n, ctx, first;                 // first: position of new token 0
+    int kvh, row0, st0, len, seq, last;    // last: the block that ends the unit, if this one does not
+    int whole, valid;                      // valid 0: the share has ended
+};
+
+// The like where each token sees an interval of positions: ctx is the end of
+// the positions that some token of the sequence sees, base (a multiple of 16)
+// their begin, where step 0 starts; all tokens see seen_lo .. seen_hi - 1.
+struct ShapedSeq : Seq {
+    int base, first, seen_lo, seen_hi;
+};
+struct ShapedUnit : Unit {
+    int base, seen_lo, seen_hi;
+    // whether every row sees positions lo .. hi - 1
+    __device__ __forceinline__ bool all_see(int lo, int hi) const { return lo >= seen_lo && hi <= seen_hi; }
+};
+
 struct MultiArgs {
+    using Seq = pa_multi::Seq;
+    using Unit = pa_multi::Unit;
+    static constexpr bool kShaped = false;
     void* out;
     const __nv_bfloat16* q;
     const void* v_cache;
@@ -41,6 +72,33 @@ struct MultiArgs {
     int direct;                            // not 0: a block takes one whole unit, of `direct` row tiles a KV head
 };
 
+// Scores s become cap tanh(s / cap), less slope |p - j| (pa_attend); E4M3
+// caches have a scale per block and head.
+struct ShapedArgs : MultiArgs {
+    using Seq = ShapedSeq;
+    using Unit = ShapedUnit;
+    static constexpr bool kShaped = true;
+    const int2* visible;                   // [tokens] positions x .. y - 1 are seen; null: causal
+    const float* slopes;                   // [query heads], or null
+    const uint8_t* k_scales;               // [blocks][KV heads] biased exponents, or null
+    const uint8_t* v_scales;
+    float cap_log2, cap_inv;               // cap * log2(e) and 1 over it; 0: none
+};
+
+// 2^(e - 127) of a scale's byte.
+__device__ __forceinline__ float scale_of(uint32_t e) { return __int_as_float(e ? (int)(e << 23) : 0x00400000); }
+
+// cap tanh(x / cap) in units of log2: x and the result times log2(e).  Around
+// zero by tanh's series, up to x^9 (the next term is 5e-8 of it at 0.3), beyond
+// by 1 - 2 / (e^2x + 1), which would cancel there: relative errors below 1e-6.
+__device__ __forceinline__ float capped(float x, float cap_log2, float cap_inv) {
+    const float u = x * cap_inv, v = u * u;
+    const float p = fmaf(fmaf(fmaf(fmaf(v, 62.f / 2835.f, -17.f / 315.f), v, 2.f / 15.f), v, -1.f / 3.f), v, 1.f);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(pa::exp2_approx(u * (2.f * kLog2e)) + 1.f));
+    return cap_log2 * (fabsf(u) < 0.3f ? u * p : fmaf(-2.f, r, 1.f));
+}
+
 // Four consecutive values of a row.
 __device__ __forceinline__ void put4(void* out, int f32, size_t i, float4 v) {
     if (f32)
@@ -50,18 +108,9 @@ __device__ __forceinline__ void put4(void* out, int f32, size_t i, float4 v) {
             make_uint2(pa::pack_bf16x2(v.x, v.y), pa::pack_bf16x2(v.z, v.w));
 }
 
-// A sequence's part of the call.
-struct Seq {
-    int q0, n, ctx, steps, tiles;
-    // tiles is 0 where nothing is to be done; cost: steps that starting and joining a unit is worth
-    __device__ __forceinline__ long long work(int heads, int cost) const {
-        return (long long)heads * tiles * (steps + cost);
-    }
-};
-
-template <int kRows, int kStep>
-__device__ __forceinline__ Seq read_seq(const MultiArgs& a, int s, bool flag) {
-    Seq r;
+template <int kRows, int kStep, class Args>
+__device__ __forceinline__ typename Args::Seq read_seq(const Args& a, int s, bool flag) {
+    typename Args::Seq r;
     r.q0 = a.query_start[s];
     const int q1 = a.query_start[s + 1];
     int ctx = a.context_lens[s];
@@ -75,16 +124,35 @@ __device__ __forceinline__ Seq read_seq(const MultiArgs& a, int s, bool flag) {
     if (bad && flag) pa::set_status(a.status, PA_DEV_BAD_CONTEXT);
     r.ctx = ctx;
     r.tiles = (int)((((long long)r.n << a.log2_group) + kRows - 1) / kRows);
-    r.steps = (ctx + kStep - 1) / kStep;
+    if constexpr (Args::kShaped) {
+        r.first = ctx - r.n;
+        int lo = 0, hi = ctx;
+        r.seen_lo = 0;
+        r.seen_hi = r.first + 1;
+        if (a.visible) {
+            lo = r.seen_hi = 0x7fffffff;
+            hi = 0;
+#pragma unroll 4
+            for (int i = 0; i < r.n; ++i) {
+                const int2 v = a.visible[r.q0 + i];
+                const int x = max(v.x, 0), y = min(v.y, ctx);
+                if (x < y) {
+                    lo = min(lo, x);
+                    hi = max(hi, y);
+                }
+                r.seen_lo = max(r.seen_lo, x);
+                r.seen_hi = min(r.seen_hi, y);
+            }
+            if (lo >= hi) lo = hi = 0;                  // nothing is seen: a step of no positions, and zeros
+        }
+        r.base = lo & ~15;
+        r.ctx = hi;
+        r.steps = max(1, (hi - r.base + kStep - 1) / kStep);
+    } else {
+        r.steps = (ctx + kStep - 1) / kStep;
+    }
     return r;
 }
-
-// The stretch of one unit that a block computes: steps st0 .. st0 + len - 1.
-struct Unit {
-    int q0, n, ctx, first;                 // first: position of new token 0
-    int kvh, row0, st0, len, seq, last;    // last: the block that ends the unit, if this one does not
-    int whole, valid;                      // valid 0: the share has ended
-};
 
 // The mask words of a unit's tokens, or null, and its table.
 __device__ __forceinline__ const uint64_t* words_of(const MultiArgs& a, const Unit& u) {
@@ -103,15 +171,17 @@ __device__ __forceinline__ int4 begun_unit(const Unit& u, int log2_group) {
 }
 
 // A block's share of the work, walked unit by unit.
-struct Walk {
+template <class Seq>
+struct WalkOf {
     long long left, share;                 // work of this share from here on, and of a whole one
     int seq, unit, gone;                   // the sequence's unit, and how much of its work is before here
     Seq sq;
 };
+using Walk = WalkOf<Seq>;
 
 // The next stretch of the share; u.valid is 0 at its end.
-template <int kRows, int kStep, int kUnitCost>
-__device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
+template <int kRows, int kStep, int kUnitCost, class Args>
+__device__ __noinline__ void next_unit(WalkOf<typename Args::Seq>& w, typename Args::Unit& u, const Args& a) {
     u.valid = 0;
     while (w.left > 0) {
         if (w.unit >= a.n_kv_heads * w.sq.tiles) {
@@ -133,7 +203,14 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
         u.q0 = w.sq.q0;
         u.n = w.sq.n;
         u.ctx = w.sq.ctx;
-        u.first = w.sq.ctx - w.sq.n;
+        if constexpr (Args::kShaped) {
+            u.first = w.sq.first;
+            u.base = w.sq.base;
+            u.seen_lo = w.sq.seen_lo;
+            u.seen_hi = w.sq.seen_hi;
+        } else {
+            u.first = w.sq.ctx - w.sq.n;
+        }
         u.kvh = w.sq.tiles == 1 ? unit : unit / w.sq.tiles;
         u.row0 = (unit - u.kvh * w.sq.tiles) * kRows;
         u.st0 = lo;
@@ -146,8 +223,8 @@ __device__ __noinline__ void next_unit(Walk& w, Unit& u, const MultiArgs& a) {
 }
 
 // The walk of one whole unit: `unit` of sequence s.
-template <int kUnitCost>
-__device__ __forceinline__ void one_unit(Walk& walk, const Seq& sq, int s, int unit) {
+template <int kUnitCost, class Seq>
+__device__ __forceinline__ void one_unit(WalkOf<Seq>& walk, const Seq& sq, int s, int unit) {
     walk.left = walk.share = sq.steps + kUnitCost;
     walk.seq = s;
     walk.unit = unit;
@@ -167,8 +244,9 @@ struct Part {
 // a barrier; `parts` holds a value per warp until then.  The shares are whole units, one
 // per block, where the grid has a block for each and none is longer than
 // kDirectSteps.
-template <int kRows, int kStep, int kUnitCost, int kMinSteps, int kDirectSteps, int kThreads>
-__device__ __forceinline__ bool find_share(const MultiArgs& a, Walk& walk, Part* parts) {
+template <int kRows, int kStep, int kUnitCost, int kMinSteps, int kDirectSteps, int kThreads, class Args>
+__device__ __forceinline__ bool find_share(const Args& a, WalkOf<typename Args::Seq>& walk, Part* parts) {
+    using Seq = typename Args::Seq;
     constexpr int kMinShare = kMinSteps + kUnitCost;
     if (a.direct) {
         int there = 0;
@@ -302,17 +380,41 @@ __device__ __forceinline__ bool drop_unfinite(uint8_t* tile, int slab_bytes, int
 // Add the values that are not finite, at d .. d + 3 of the positions of
 // [lo, hi) that a row of sequence s sees, to the row's result: its sums at
 // `part`, or `out` where that is null.
-template <int D, bool F8>
-__device__ __noinline__ void add_unfinite(const MultiArgs& a, int s, int kvh, int row, int lo, int hi, int d, float* part) {
-    const Seq q = read_seq<1, 1>(a, s, false);
-    const int i = row >> a.log2_group, B = 1 << a.log2_block, first = q.ctx - q.n;
+// Shaped: the tiles of kTile positions that every row sees keep theirs.
+template <int D, bool F8, int kTile, class Args>
+__device__ __noinline__ void add_unfinite(const Args& a, int s, int kvh, int row, int lo, int hi, int d, float* part) {
+    const auto q = read_seq<1, 1>(a, s, false);
+    const int i = row >> a.log2_group, B = 1 << a.log2_block;
     if (i >= q.n) return;
-    const uint64_t* words = a.tree_mask ? a.tree_mask + q.q0 : nullptr;
+    int first, end = min(hi, q.ctx);
+    const uint64_t* words = nullptr;
+    if constexpr (Args::kShaped) {
+        first = lo;
+        if (a.visible) {
+            const int2 v = a.visible[q.q0 + i];
+            first = max(lo, v.x);
+            end = min(end, v.y);
+        } else {
+            end = min(end, q.first + i + 1);
+        }
+    } else {
+        first = q.ctx - q.n;
+        words = a.tree_mask ? a.tree_mask + q.q0 : nullptr;
+    }
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int pos = max(lo, first); pos < min(hi, q.ctx); ++pos) {
+    for (int pos = max(lo, first); pos < end; ++pos) {
+        if constexpr (Args::kShaped) {
+            const int t0 = lo + (pos - lo) / kTile * kTile;
+            if (t0 >= q.seen_lo && t0 + kTile <= q.seen_hi) {
+                pos = t0 + kTile - 1;
+                continue;
+            }
+        } else if (!sees(words, i, pos - first)) {
+            continue;
+        }
         const int blk = a.block_tables[(size_t)s * a.max_blocks + (pos >> a.log2_block)];
-        if (!sees(words, i, pos - first) || blk < 0 || blk >= a.num_blocks) continue;
+        if (blk < 0 || blk >= a.num_blocks) continue;
         const size_t at = ((size_t)(blk * a.n_kv_heads + kvh) * B + (pos & (B - 1))) * D + d;
         if constexpr (F8) {                                       // E4M3 has NaN only
             const uint32_t m = unfinite_mask<true>(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v_cache) + at));
@@ -404,6 +506,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
         }
     }
 }
+
+// The merge of the units that blocks share (pa_decode_multi.cu).
+cudaError_t launch_merge(const MultiArgs& a, int unit, int d_head, double units, int grid, cudaStream_t st);
 
 // Launches of the 64- and 128-row units on the 5th-generation tensor cores
 // (pa_decode_wide.cu); cudaSuccess or the launch's error.
