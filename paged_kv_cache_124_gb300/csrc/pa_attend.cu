@@ -10,9 +10,15 @@
 // begins at the first position that some token of it sees and ends behind
 // the last, so a window costs its own bytes.
 
+#include "pa_attend.cuh"
 #include "pa_multi_rows.cuh"
 
 namespace {
+
+// Whether a call goes in tiles of 128 rows (pa_attend_prompt.cu), with a scale above 0.
+bool is_prompt(long long rows) { return rows > 64; }
+
+size_t rows_workspace(int d_head) { return workspace_size(max_grid(false), kRows, d_head); }
 
 int attend(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scales,
            const uint8_t* v_scales, const int32_t* block_tables, const int32_t* query_start,
@@ -44,12 +50,24 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
     const long long all_rows = (long long)max_query_len * group;
     const long long cap = (long long)max_blocks_per_seq * block_size;
     const int ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
+    if (is_prompt(all_rows) && scale > 0.f) {
+        const size_t n = pa_attend_calls::prompt_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads,
+                                                           n_kv_heads, d_head, f8);
+        if (n) {
+            if (workspace_bytes < n) return PA_ERR_WORKSPACE;
+            return pa_attend_calls::launch_prompt({out, out_dtype == PA_DTYPE_F32, q, k_cache, v_cache, k_scales, v_scales,
+                                                   block_tables, query_start, context_lens, visible, slopes, softcap, scale,
+                                                   block_size, n_q_heads, n_kv_heads, d_head, num_seqs, num_tokens,
+                                                   max_query_len, max_blocks_per_seq, num_blocks, ctx_cap, workspace,
+                                                   status_dev, static_cast<cudaStream_t>(stream)});
+        }
+    }
     const bool wide = false;
     const int unit = kRows;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
     const int most = max_grid(wide);
     if (most <= 0) return PA_ERR_CUDA;
-    if (workspace_bytes < workspace_size(most, unit, d_head)) return PA_ERR_WORKSPACE;
+    if (workspace_bytes < rows_workspace(d_head)) return PA_ERR_WORKSPACE;
 
     ShapedArgs a{};
     a.ctx_cap = ctx_cap;
@@ -108,7 +126,11 @@ size_t pa_attend_workspace_size(int num_seqs, int max_query_len, int max_blocks_
     if (num_seqs <= 0 || max_query_len <= 0 || max_blocks_per_seq <= 0 || block_size <= 0 || n_kv_heads <= 0 ||
         n_q_heads < n_kv_heads || d_head <= 0)
         return 0;
-    return workspace_size(max_grid(false), kRows, d_head);
+    const size_t rows = rows_workspace(d_head);
+    if (!is_prompt((long long)max_query_len * (n_q_heads / n_kv_heads))) return rows;
+    const size_t prompt = pa_attend_calls::prompt_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads,
+                                                            n_kv_heads, d_head, scaled != 0);
+    return prompt > rows ? prompt : rows;
 }
 
 int pa_attend(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache,

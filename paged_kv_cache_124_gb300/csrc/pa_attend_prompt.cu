@@ -1,0 +1,266 @@
+// Prompts and long chunks of pa_attend and pa_attend_scaled: the prefill
+// kernel (pa_prefill.cuh) with shaped scores, and its staging passes.
+//
+// What the shape changes: an item's tiles run from the first position that
+// one of its rows sees to the last, rather than from 0 to its own; scores are
+// capped and biased in registers before the softmax; rows mask by an interval.
+// The staging leaves out values that are not finite, since the weights of
+// rows that do not see them are zeros and 0 * inf is not; the rows that see
+// them add them when they are written.  From a block-scaled cache it makes
+// bf16 keys and fp16 values that hold every element exactly (a tile whose
+// blocks' scales are outside fp16's range keeps bf16 values, as pa_prefill's
+// do).
+
+#include "pa_attend.cuh"
+#include "pa_prefill.cuh"
+
+namespace {
+
+struct ShapedStageArgs : StageArgs {
+    const uint8_t* k_scales;
+    const uint8_t* v_scales;
+    const int32_t* query_start;
+    const int2* visible;
+    int num_tokens, ctx_cap;
+    int* sched;           // zeroed for the prefill kernel's claims
+};
+
+// Whether tile j of the sequence is seen by some row (by a whole block).
+__device__ __forceinline__ bool tile_is_seen(const ShapedStageArgs& a, int s, int j, int ctx) {
+    if (!a.visible) return true;
+    const int q0 = a.query_start[s], q1 = min(a.query_start[s + 1], a.num_tokens);   // (of a flagged sequence, anything)
+    int lo = INT_MAX, hi = 0;
+    for (int t = max(q0, 0) + threadIdx.x; t < q1; t += 256) {
+        const int2 v = a.visible[t];
+        const int from = max(v.x, 0), to = min(v.y, ctx);
+        if (from < to) {
+            lo = min(lo, from);
+            hi = max(hi, to);
+        }
+    }
+    // (ranges that only together reach over the tile count as seen: every tile between the first and the last is read)
+    const int before = __syncthreads_or(lo < (j + 1) * kKv), behind = __syncthreads_or(hi > j * kKv);
+    return before && behind;
+}
+
+__device__ __forceinline__ bool tile_there(const ShapedStageArgs& a, int s, int j, int& ctx) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x < 2 && blockIdx.x + blockIdx.y + blockIdx.z == 0) a.sched[threadIdx.x] = 0;
+    ctx = a.context_lens[s];
+    ctx = min(max(ctx, 0), a.ctx_cap);                           // the prefill kernel flags and clamps the same
+    return j * kKv < ctx && tile_is_seen(a, s, j, ctx);
+}
+
+// Two bf16 that are not finite, as a mask.
+__device__ __forceinline__ uint32_t unfinite2(uint32_t w) {
+    return ((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
+}
+
+// stage_v_kernel without the values that are not finite (format bit 1: there are some).
+template <int D>
+__global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __restrict__ v_cache, const ShapedStageArgs a) {
+    constexpr int kChunksPerRow = D / 8, kPer = kKv * kChunksPerRow / 256;
+    const int j = blockIdx.x, s = blockIdx.y, h = blockIdx.z;
+    int ctx;
+    if (!tile_there(a, s, j, ctx)) return;
+    const int32_t* table = a.block_tables + (size_t)s * a.max_blocks;
+    uint4 v[kPer];
+    uint32_t amax = 0, bad = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int c = threadIdx.x + 256 * i, pos = j * kKv + c / kChunksPerRow;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (pos < ctx) {
+            const int blk = __ldg(table + pos / a.block_size);
+            if (blk >= 0 && blk < a.num_blocks)
+                v[i] = __ldg(v_cache + (((size_t)blk * a.n_kv_heads + h) * a.block_size + pos % a.block_size) * kChunksPerRow +
+                             c % kChunksPerRow);
+            // a bad entry reads zeros; the prefill kernel's K loads flag it
+        }
+        const uint4 m = make_uint4(unfinite2(v[i].x), unfinite2(v[i].y), unfinite2(v[i].z), unfinite2(v[i].w));
+        bad |= m.x | m.y | m.z | m.w;
+        v[i] = make_uint4(v[i].x & ~m.x, v[i].y & ~m.y, v[i].z & ~m.z, v[i].w & ~m.w);
+        amax = max_u16x2(amax, max_u16x2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
+        amax = max_u16x2(amax, max_u16x2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+    }
+    const bool wide = __syncthreads_or((amax & 0xffffu) >= kF16Wide || (amax >> 16) >= kF16Wide) != 0;
+    const bool some = __syncthreads_or(bad != 0) != 0;
+    uint4* dst = reinterpret_cast<uint4*>(a.v_stage + ((size_t)(h * a.num_seqs + s) * a.l_slot + (size_t)j * kKv) * D);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        dst[threadIdx.x + 256 * i] = wide ? v[i]
+                                          : make_uint4(bf16x2_to_f16x2(v[i].x), bf16x2_to_f16x2(v[i].y),
+                                                       bf16x2_to_f16x2(v[i].z), bf16x2_to_f16x2(v[i].w));
+    if (threadIdx.x == 0) a.v_fmt[(size_t)(h * a.num_seqs + s) * a.t_slot + j] = (wide ? 1 : 0) | (some ? 2 : 0);
+}
+
+// A block-scaled cache's tile: K as bf16, V as fp16 where the blocks' scales are 2^-15 .. 2^7 (the values are
+// multiples of 2^-24 below 2^16 then), else as bf16; all exact.
+template <int D>
+__global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restrict__ k_cache, const uint4* __restrict__ v_cache,
+                                                           uint16_t* k_stage, const ShapedStageArgs a) {
+    constexpr int kChunksPerRow = D / 16, kPer = kKv * kChunksPerRow / 256;
+    const int j = blockIdx.x, s = blockIdx.y, h = blockIdx.z;
+    int ctx;
+    if (!tile_there(a, s, j, ctx)) return;
+    const int32_t* table = a.block_tables + (size_t)s * a.max_blocks;
+    const size_t row0 = ((size_t)(h * a.num_seqs + s) * a.l_slot + (size_t)j * kKv) * D;
+    uint4 code[2][kPer];
+    float scale[2][kPer];
+    uint32_t bad = 0;
+    bool narrow = true;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int c = threadIdx.x + 256 * i, pos = j * kKv + c / kChunksPerRow;
+        code[0][i] = code[1][i] = make_uint4(0, 0, 0, 0);
+        scale[0][i] = scale[1][i] = 0.f;
+        if (pos < ctx) {
+            const int blk = __ldg(table + pos / a.block_size);
+            if (blk >= 0 && blk < a.num_blocks) {
+                const size_t at = (((size_t)blk * a.n_kv_heads + h) * a.block_size + pos % a.block_size) * kChunksPerRow + c % kChunksPerRow;
+                code[0][i] = __ldg(k_cache + at);
+                code[1][i] = __ldg(v_cache + at);
+                const int ke = a.k_scales[(size_t)blk * a.n_kv_heads + h], ve = a.v_scales[(size_t)blk * a.n_kv_heads + h];
+                scale[0][i] = __int_as_float(ke ? ke << 23 : 0x00400000);
+                scale[1][i] = __int_as_float(ve ? ve << 23 : 0x00400000);
+                if (ve && (ve < 112 || ve > 134)) narrow = false;   // (what 2^-127 scales is nothing to any sum)
+            } else {
+                pa::set_status(a.status, PA_DEV_BAD_BLOCK_ID);
+            }
+        }
+        uint4& v = code[1][i];                                   // NaN, E4M3's only one that is not finite
+        auto nan4 = [](uint32_t w) { return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu; };
+        const uint4 m = make_uint4(nan4(v.x), nan4(v.y), nan4(v.z), nan4(v.w));
+        bad |= m.x | m.y | m.z | m.w;
+        v = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
+    }
+    const bool wide = __syncthreads_or(!narrow) != 0, some = __syncthreads_or(bad != 0) != 0;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        uint4* dst = reinterpret_cast<uint4*>((kv ? a.v_stage : k_stage) + row0);
+        const bool as_bf16 = kv == 0 || wide;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t w[4] = {code[kv][i].x, code[kv][i].y, code[kv][i].z, code[kv][i].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                const float lo = x.x * scale[kv][i], hi = x.y * scale[kv][i];
+                f[e] = as_bf16 ? pack_bf16_rn(lo, hi) : pack_f16_rn(lo, hi);
+            }
+            const int c = threadIdx.x + 256 * i;
+            dst[2 * c] = make_uint4(f[0], f[1], f[2], f[3]);
+            dst[2 * c + 1] = make_uint4(f[4], f[5], f[6], f[7]);
+        }
+    }
+    if (threadIdx.x == 0) a.v_fmt[(size_t)(h * a.num_seqs + s) * a.t_slot + j] = (wide ? 1 : 0) | (some ? 2 : 0);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D, bool kScaled>
+int launch_shaped(const ShapedPrefillArgs& a, const ShapedStageArgs& sa, const pa_attend_calls::Call& c, uint16_t* k_stage, int grid) {
+    CUtensorMap mq, mk, mv;
+    const long long cache_rows = (long long)c.num_blocks * c.n_kv_heads * c.block_size;
+    if (!make_maps<D>(mq, mk, mv, a, sa, c.q, c.k_cache, kScaled ? k_stage : nullptr, c.num_tokens, cache_rows)) return PA_ERR_CUDA;
+    const auto kernel = prefill_kernel<D, kScaled, ShapedPrefillArgs>;
+    if (pa_host::ensure_smem_attr(kernel, PGeo<D>::kSmem, g_smem_done<D, kScaled, ShapedPrefillArgs>) != cudaSuccess)
+        return PA_ERR_CUDA;
+    const dim3 sgrid((unsigned)sa.t_slot, (unsigned)sa.num_seqs, (unsigned)sa.n_kv_heads);
+    cudaError_t e;
+    if constexpr (kScaled)
+        e = pa_host::launch_dependent(stage_scaled_kernel<D>, sgrid, dim3(256), 0, c.stream, static_cast<const uint4*>(c.k_cache),
+                                      static_cast<const uint4*>(c.v_cache), k_stage, sa);
+    else
+        e = pa_host::launch_dependent(stage_shaped_v_kernel<D>, sgrid, dim3(256), 0, c.stream, static_cast<const uint4*>(c.v_cache), sa);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    return pa_host::launch_dependent(kernel, dim3(grid), dim3(kThreads), PGeo<D>::kSmem, c.stream, mq, mk, mv, a) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+namespace pa_attend_calls {
+
+size_t prompt_workspace(int num_seqs, int max_query_len, int max_blocks, int block_size, int n_q_heads, int n_kv_heads,
+                        int d_head, bool scaled) {
+    const int group = n_q_heads / n_kv_heads;
+    const double tiles = ((double)max_query_len * group + 2 * kRows - 1) / (2 * kRows);
+    const double slots = ((double)max_blocks * block_size + kKv) * num_seqs * n_kv_heads;
+    if (num_seqs > 65535 || n_kv_heads > 65535 || group > kRows || slots > INT_MAX - kKv ||
+        tiles * num_seqs * n_kv_heads > INT_MAX - 4096.0)
+        return 0;
+    return workspace_layout(num_seqs, max_blocks, block_size, n_kv_heads, d_head, scaled).total + 256;
+}
+
+int launch_prompt(const Call& c) {
+    const bool scaled = c.k_scales != nullptr;
+    const Workspace ws = workspace_layout(c.num_seqs, c.max_blocks, c.block_size, c.n_kv_heads, c.d_head, scaled);
+    uint8_t* w8 = static_cast<uint8_t*>(c.workspace);
+    int* sched = reinterpret_cast<int*>(w8 + ws.total);
+    const int group = c.n_q_heads / c.n_kv_heads, tq = kRows / group;
+    const long long tiles = ((long long)c.max_query_len + 2 * tq - 1) / (2 * tq), items = tiles * c.num_seqs * c.n_kv_heads;
+    ShapedPrefillArgs a{};
+    a.out = c.out;
+    a.out_f32 = c.out_f32;
+    a.out_al32 = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;
+    a.block_tables = c.block_tables;
+    a.max_blocks = c.max_blocks;
+    a.query_start = c.query_start;
+    a.context_lens = c.context_lens;
+    a.num_seqs = c.num_seqs;
+    a.num_tokens = c.num_tokens;
+    a.tiles_per_seq = (int)tiles;
+    a.block_size = c.block_size;
+    a.n_kv_heads = c.n_kv_heads;
+    a.group = group;
+    a.tq = tq;
+    a.n_q_heads = c.n_q_heads;
+    a.num_blocks = c.num_blocks;
+    a.oob_row = c.num_blocks * c.n_kv_heads * c.block_size;
+    a.scale_log2 = c.scale * kLog2e;
+    a.v_fmt = w8 + ws.fmt_off;
+    a.l_slot = ws.l_slot;
+    a.t_slot = ws.t_slot;
+    a.k_scale = a.v_scale = 1.f;
+    a.status = c.status;
+    a.sched = sched;
+    a.visible = reinterpret_cast<const int2*>(c.visible);
+    a.slopes = c.slopes;
+    a.cap_log2 = c.softcap * kLog2e;
+    a.cap_inv = c.softcap > 0.f ? 1.f / a.cap_log2 : 0.f;
+    a.v_cache = c.v_cache;
+    a.ctx_cap = c.ctx_cap;
+    a.max_query_len = c.max_query_len;
+    const int sms = num_sms(), grid = (int)(items < sms ? items : sms);
+    const long long per_head = tiles * c.num_seqs, hpg = (2LL * grid + per_head - 1) / per_head;
+    a.heads_per_group = (int)(hpg < 1 ? 1 : hpg > c.n_kv_heads ? c.n_kv_heads : hpg);
+    ShapedStageArgs sa{};
+    sa.block_tables = c.block_tables;
+    sa.max_blocks = c.max_blocks;
+    sa.context_lens = c.context_lens;
+    sa.num_seqs = c.num_seqs;
+    sa.block_size = c.block_size;
+    sa.n_kv_heads = c.n_kv_heads;
+    sa.num_blocks = c.num_blocks;
+    sa.l_slot = ws.l_slot;
+    sa.t_slot = ws.t_slot;
+    sa.v_stage = reinterpret_cast<uint16_t*>(w8);
+    sa.v_fmt = w8 + ws.fmt_off;
+    sa.status = c.status;
+    sa.k_scales = c.k_scales;
+    sa.v_scales = c.v_scales;
+    sa.query_start = c.query_start;
+    sa.visible = a.visible;
+    sa.num_tokens = c.num_tokens;
+    sa.sched = sched;
+    sa.ctx_cap = c.ctx_cap;
+    if (scaled) return launch_shaped<128, true>(a, sa, c, reinterpret_cast<uint16_t*>(w8 + ws.k_off), grid);
+    return c.d_head == 128 ? launch_shaped<128, false>(a, sa, c, nullptr, grid) : launch_shaped<64, false>(a, sa, c, nullptr, grid);
+}
+
+}  // namespace pa_attend_calls

@@ -88,6 +88,7 @@ struct ShapedPrefillArgs : PrefillArgs {
     const float* slopes;  // [query heads], or null
     float cap_log2, cap_inv;   // cap * log2(e) and 1 over it; 0: none
     const void* v_cache;  // for values that are not finite
+    int ctx_cap, max_query_len;
 };
 
 // One work item: query rows [t0, t0 + 2 tq) of sequence seq's n new tokens
@@ -436,6 +437,14 @@ __device__ __forceinline__ bool decode_item(int i, const Args& a, Item& it, bool
     it.n = a.query_start[it.seq + 1] - it.q0;
     it.ctx = a.context_lens[it.seq];
     it.t0 = tile * 2 * a.tq;
+    if constexpr (Args::kShaped) {                        // sequences that are flagged, as pa_decode_multi does
+        bool bad = it.ctx < 0 || it.ctx > a.ctx_cap;
+        it.ctx = max(0, min(it.ctx, a.ctx_cap));
+        const bool none = it.q0 < 0 || it.n < 0 || it.q0 + it.n > a.num_tokens || it.n > it.ctx || it.n > a.max_query_len;
+        bad |= none;
+        if (bad && flag) pa::set_status(a.status, PA_DEV_BAD_CONTEXT);
+        if (none) return false;
+    }
     if (it.t0 >= it.n || it.q0 < 0) return false;
     if (it.ctx > a.max_blocks * a.block_size) {
         if (flag) pa::set_status(a.status, PA_DEV_BAD_CONTEXT);
@@ -1080,9 +1089,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pa::mbar_arrive(&bars->o_free[x]);
                 if (valid_row[x]) {
                     scale_f32x2<kOCols>(o, inv);
-                    if constexpr (kShaped)
+                    if constexpr (kShaped) {
+                        if (l_all == 0.f) {                       // a row that sees nothing, perhaps of tiles that nothing staged
+#pragma unroll
+                            for (int k = 0; k < kOCols; ++k) o[k] = 0.f;
+                        }
                         if (__builtin_expect(it.wide & 2, 0))
                             add_unfinite_values<D, kF8, kOCols>(a, it, row_lo[x], row_lim[x], hc * kOCols, fmt, x ? it.nt1 : it.nt0, o);
+                    }
                     // a thread writes its half row: whole 32-byte sectors when
                     // out allows it (16-byte stores fill half a sector each and
                     // cost as much as a whole one)

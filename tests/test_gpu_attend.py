@@ -282,7 +282,13 @@ def test_bad_inputs_are_flagged(scaled, news):
     assert st.item() == api.PA_DEV_BAD_CONTEXT
     a, b = p.start[1], p.start[2]
     assert torch.equal(out[:a], want[:a]) and torch.equal(out[b:], want[b:]) and torch.isnan(out[a:b]).all()
-    p.ctx[1] = 60
+    p.ctx[1], st[0] = 60, 0
+    most, p.most = p.most, max(n for n in news if n < p.most)      # more new tokens than the call allows: not computed
+    out = p.run(status=st)
+    p.most = most
+    left = torch.isnan(out).all(-1).all(-1)
+    assert st.item() == api.PA_DEV_BAD_CONTEXT
+    assert left.tolist() == [n == most for n in news for _ in range(n)] and torch.equal(out[~left], want[~left])
     p.tables[0, 1] = 1 << 20                                       # outside the pool: flagged, the others as they were
     st.zero_()
     out = p.run(status=st)
