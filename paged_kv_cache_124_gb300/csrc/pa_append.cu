@@ -29,7 +29,8 @@ struct AppendArgs : RopeArgs {
     uint8_t* k_scales;
     uint8_t* v_scales;
     int span;                                          // tokens of a warp
-    int kv_blocks;                                     // thread blocks of keys and values; the others take queries
+    int kv_blocks;                                     // thread blocks of keys and values: every (every + 1)th of the grid's
+    int every;                                         // first; the others take queries
     int q_heads_per;                                   // query heads one after another in the same lanes
     int log2_block;
 };
@@ -84,7 +85,7 @@ __device__ __forceinline__ uint32_t code_again(uint32_t w, float by) {
 }
 
 template <int D, int kBlock, bool kInterleaved, bool kAxes>
-__global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArgs a) {
     constexpr int kLanes = D / 16, kRowsAt = 32 / kLanes;      // tokens side by side in a warp
     constexpr int kRounds = (kBlock + kRowsAt - 1) / kRowsAt;  // of a run
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -92,11 +93,13 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
     const int lane = threadIdx.x & 31, l = lane % kLanes, g = lane / kLanes;
     const unsigned mask = ((1u << kLanes) - 1u) << (lane / kLanes * kLanes);
     const Place<kInterleaved> w(l, a.rot_dim);
-    if ((int)blockIdx.x >= a.kv_blocks) {
+    // Blocks of both kinds run side by side: queries stream, keys and values wait for their largest.
+    const int turn = blockIdx.x / (a.every + 1), kv_before = min((int)(turn + (blockIdx.x % (a.every + 1) != 0)), a.kv_blocks);
+    if (blockIdx.x % (a.every + 1) || turn >= a.kv_blocks) {
         // ------------------------------------------------------------ queries
         constexpr int kFlight = 4;
         const uint32_t parts = (a.n_q_heads + a.q_heads_per - 1) / a.q_heads_per;
-        const uint32_t nth = (blockIdx.x - a.kv_blocks) * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
+        const uint32_t nth = (blockIdx.x - kv_before) * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
         const uint32_t t = nth / parts;
         if (t >= (uint32_t)a.num_tokens) return;               // whole heads: a head's threads leave together
         const int h0 = (nth - t * parts) * a.q_heads_per, h1 = min(h0 + a.q_heads_per, a.n_q_heads);
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
         return;
     }
     // ---------------------------------------------------------------- keys and values
-    const uint32_t per = 2 * a.n_kv_heads, item = blockIdx.x * kWarps + (threadIdx.x >> 5), first = item / per * a.span;
+    const uint32_t per = 2 * a.n_kv_heads, item = turn * kWarps + (threadIdx.x >> 5), first = item / per * a.span;
     if (first >= (uint32_t)a.num_tokens) return;
     const int which = item % per, h = which >> 1;
     const bool is_v = which & 1;
@@ -214,17 +217,17 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
             }
         }
         const int old = off ? *scales : 0;
-        uint64_t gain[8];
-        if (norm) {
-            load8(a.k_weight + 8 * w.c0, gain);
-            load8(a.k_weight + 8 * w.c1, gain + 4);
-        }
         // round r's part of the rows, ready for the cache
         auto part = [&](int r) {
             Part p;
             unpack8(x0[r], p.f);
             unpack8(x1[r], p.f + 4);
-            if (norm) norm_part<kLanes>(p, gain, a.eps, mask);
+            if (norm) {
+                uint64_t gain[8];                                // (from L1: registers are short)
+                load8(a.k_weight + 8 * w.c0, gain);
+                load8(a.k_weight + 8 * w.c1, gain + 4);
+                norm_part<kLanes>(p, gain, a.eps, mask);
+            }
             const int i = r * kRowsAt + g;
             if (turns && i < n) {
                 Where<kAxes> at;
@@ -289,7 +292,9 @@ cudaError_t launch_append(const AppendArgs& a, int interleaved, cudaStream_t st)
     const long long q = a.n_q_heads ? (long long)a.num_tokens * ((a.n_q_heads + a.q_heads_per - 1) / a.q_heads_per) : 0;
     AppendArgs b = a;
     b.kv_blocks = (int)((kv + kWarps - 1) / kWarps);
-    const unsigned grid = (unsigned)(b.kv_blocks + (q + kRopeThreads / kLanes - 1) / (kRopeThreads / kLanes));
+    const int q_blocks = (int)((q + kRopeThreads / kLanes - 1) / (kRopeThreads / kLanes));
+    b.every = q_blocks / b.kv_blocks;
+    const unsigned grid = (unsigned)(b.kv_blocks + q_blocks);
     const auto kernel = a.num_axes ? (interleaved ? append_kernel<D, kBlock, true, true> : append_kernel<D, kBlock, false, true>)
                                    : (interleaved ? append_kernel<D, kBlock, true, false> : append_kernel<D, kBlock, false, false>);
     return pa_host::launch_dependent(kernel, dim3(grid), dim3(kRopeThreads), 0, st, b);
