@@ -10,13 +10,13 @@
 // subnormals, which lose bits).
 //
 // The tokens of one block follow one another (a run: consecutive slots within
-// a block).  A warp takes a run's keys or values of one head: D / 16 lanes a
-// token, all of the run's tokens in registers as they came, twice through the
-// arithmetic: for the largest value, then for the codes (which is cheaper
-// than 32-bit values of a run in registers, and both passes are far below the
-// time of its bytes).  A run belongs to the warp that has its first token
-// among its own `span`; so decode batches go a token a warp, and prompts
-// about a block a warp.  Queries go beside, in blocks of their own.
+// a block).  A thread block takes the runs that begin among its own tokens,
+// for up to eight heads: D / 16 lanes hold a token's part of a head, as
+// pa_rope.cu's do, and a token's angles are loaded once for all of its heads.
+// The rows stay in registers as they came while the largest values of each
+// run and head meet in shared memory, and go through the arithmetic again for
+// the codes (a run of 32-bit values would not fit).  Queries go beside, in
+// blocks of their own.
 
 #include <cuda_fp16.h>
 #include <math.h>
@@ -28,7 +28,6 @@ namespace {
 struct AppendArgs : RopeArgs {
     uint8_t* k_scales;
     uint8_t* v_scales;
-    int span;                                          // tokens of a warp
     int kv_blocks;                                     // thread blocks of keys and values: every (every + 1)th of the grid's
     int every;                                         // first; the others take queries
     int q_heads_per;                                   // query heads one after another in the same lanes
@@ -84,20 +83,54 @@ __device__ __forceinline__ uint32_t code_again(uint32_t w, float by) {
     return pa::e4m3x2(x.x * by, x.y * by) | (pa::e4m3x2(y.x * by, y.y * by) << 16);
 }
 
-template <int D, int kBlock, bool kInterleaved, bool kAxes>
+// Rows on their way to a warp, in shared memory rather than in registers: a
+// slot holds the two chunks of each lane, which alone reads them back.
+__device__ __forceinline__ void copy_in(uint32_t slot, int lane, const uint4* src, int c0, int c1) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n\tcp.async.cg.shared.global [%2], [%3], 16;" ::"r"(slot + 16 * lane),
+                 "l"(src + c0), "r"(slot + 512 + 16 * lane), "l"(src + c1) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+__device__ __forceinline__ void read_slot(uint32_t slot, int lane, uint64_t* f) {
+    uint4 x;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(slot + 512 * k + 16 * lane) : "memory");
+        unpack8(x, f + 4 * k);
+    }
+}
+
+constexpr int kFlight = 8;                             // heads of a query on their way
+constexpr int kTileHeads = 8;                          // KV heads of a thread block
+constexpr int kWindow = 64;                            // tokens that a thread block looks at: its own, one before, kBlock - 1 behind
+
+// Tokens of a thread block, and how its D / 16 lanes per head's part go over
+// them: kMany: 16 tokens, the heads in turn (4 of D 128); else 16 parts side by
+// side, a key or a value of a head each, and the tokens that leaves (2 of D 128).
+template <int D, bool kMany>
+struct Share {
+    static constexpr int kLanes = D / 16, kGroups = kRopeThreads / kLanes;
+    static constexpr int kTokens = kMany ? 16 : kGroups / 16, kSides = kGroups / kTokens;
+    static constexpr int kHeads = kMany ? kTileHeads / kSides : 1;
+};
+
+template <int D, int kBlock, bool kInterleaved, bool kAxes, bool kMany>
 __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArgs a) {
-    constexpr int kLanes = D / 16, kRowsAt = 32 / kLanes;      // tokens side by side in a warp
-    constexpr int kRounds = (kBlock + kRowsAt - 1) / kRowsAt;  // of a run
+    using S = Share<D, kMany>;
+    constexpr int kLanes = S::kLanes, kTokens = S::kTokens, kHeads = S::kHeads;
+    extern __shared__ __align__(16) uint8_t smem[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, l = lane % kLanes, g = lane / kLanes;
+    const int lane = threadIdx.x & 31, l = lane % kLanes;
     const unsigned mask = ((1u << kLanes) - 1u) << (lane / kLanes * kLanes);
     const Place<kInterleaved> w(l, a.rot_dim);
     // Blocks of both kinds run side by side: queries stream, keys and values wait for their largest.
     const int turn = blockIdx.x / (a.every + 1), kv_before = min((int)(turn + (blockIdx.x % (a.every + 1) != 0)), a.kv_blocks);
     if (blockIdx.x % (a.every + 1) || turn >= a.kv_blocks) {
         // ------------------------------------------------------------ queries
-        constexpr int kFlight = 4;
+        const uint32_t slots = pa::smem_addr(smem) + (threadIdx.x >> 5) * (kFlight * 1024);
         const uint32_t parts = (a.n_q_heads + a.q_heads_per - 1) / a.q_heads_per;
         const uint32_t nth = (blockIdx.x - kv_before) * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
         const uint32_t t = nth / parts;
@@ -105,79 +138,79 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArg
         const int h0 = (nth - t * parts) * a.q_heads_per, h1 = min(h0 + a.q_heads_per, a.n_q_heads);
         Where<kAxes> at;
         at.load(a, t);
-        const __nv_bfloat16* rows = a.q + (long long)t * a.q_stride;
-        uint4 x0[kFlight], x1[kFlight];
-        auto load = [&](int h) {
+        const uint4* rows = reinterpret_cast<const uint4*>(a.q + (long long)t * a.q_stride);
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u)
-                if (h + u < h1) {
-                    const uint4* src = reinterpret_cast<const uint4*>(rows + (h + u) * D);
-                    x0[u] = src[w.c0];
-                    x1[u] = src[w.c1];
-                }
-        };
-        load(h0);
-        uint64_t gain[8];
-        if (a.q_weight) {
-            load8(a.q_weight + 8 * w.c0, gain);
-            load8(a.q_weight + 8 * w.c1, gain + 4);
+        for (int u = 0; u < kFlight; ++u) {
+            if (h0 + u < h1) copy_in(slots + 1024 * u, lane, rows + (h0 + u) * (D / 8), w.c0, w.c1);
+            copies_end();
         }
-        if (at.lowest() < 0 || at.highest() >= a.max_positions) return;   // (flagged by the keys' warps)
-        uint64_t cs[4], sn[4];
-        if (w.turns) load_angles<kAxes>(a, at, l, cs, sn);
-#pragma unroll 1
-        for (int h = h0; h < h1; h += kFlight) {
-            uint4 y0[kFlight], y1[kFlight];
-#pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                y0[u] = x0[u];
-                y1[u] = x1[u];
+        if (at.lowest() >= 0 && at.highest() < a.max_positions) {   // (else flagged by the keys' warps)
+            uint64_t cs[4], sn[4];
+            if (w.turns) load_angles<kAxes>(a, at, l, cs, sn);
+            uint64_t gain[8];
+            if (a.q_weight) {
+                load8(a.q_weight + 8 * w.c0, gain);
+                load8(a.q_weight + 8 * w.c1, gain + 4);
             }
-            load(h + kFlight);
-#pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                if (h + u >= h1) break;
+            int u = 0;
+#pragma unroll 1
+            for (int h = h0; h < h1; ++h) {
+                wait_copies<kFlight - 1>();
+                const uint32_t slot = slots + 1024 * u;
                 Part p;
-                unpack8(y0[u], p.f);
-                unpack8(y1[u], p.f + 4);
+                read_slot(slot, lane, p.f);
                 if (a.q_weight) norm_part<kLanes>(p, gain, a.eps, mask);
                 if (w.turns) turn_part<kInterleaved>(p, cs, sn);
-                uint4* dst = a.q_out + ((size_t)t * a.n_q_heads + h + u) * (D / 8);
-                dst[w.c0] = pack8(p.f);
-                dst[w.c1] = pack8(p.f + 4);
+                const uint4 y0 = pack8(p.f), y1 = pack8(p.f + 4);
+                if (h + kFlight < h1) copy_in(slot, lane, rows + (h + kFlight) * (D / 8), w.c0, w.c1);
+                copies_end();
+                uint4* dst = a.q_out + ((size_t)t * a.n_q_heads + h) * (D / 8);
+                dst[w.c0] = y0;
+                dst[w.c1] = y1;
+                u = (u + 1) % kFlight;
             }
         }
+        wait_copies<0>();
         return;
     }
     // ---------------------------------------------------------------- keys and values
-    const uint32_t per = 2 * a.n_kv_heads, item = turn * kWarps + (threadIdx.x >> 5), first = item / per * a.span;
-    if (first >= (uint32_t)a.num_tokens) return;
-    const int which = item % per, h = which >> 1;
-    const bool is_v = which & 1;
-    // Tokens first - 1 .. first + 62, two a lane: their slots, negative where nothing is written.
-    long long slot[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const long long t = (long long)first - 1 + lane + 32 * x;
-        slot[x] = -1;
-        if (t >= 0 && t < a.num_tokens && lane + 32 * x < a.span + kBlock) {
-            slot[x] = a.slots[t];
-            bool there = true;
-            if (a.positions) {
-                Where<kAxes> at;
-                at.load(a, t);
-                there = at.lowest() >= 0 && at.highest() < a.max_positions;
-                if (which == 0 && at.lowest() >= 0 && !there) pa::set_status(a.status, PA_DEV_BAD_POSITION);
-            }
-            if (!there) slot[x] = -1;
-            if (slot[x] >= a.num_slots) {
-                if (which == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
-                slot[x] = -1;
-            }
-        }
-    }
+    struct Shared {
+        long long slot[kWindow];                                 // of tokens first - 1 on; negative where nothing is written
+        int4 where[kWindow];                                     // their positions
+        uint32_t top[16][2 * kTileHeads];                        // largest magnitudes of each run's keys, then values; then scales
+    };
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
+    const int tiles = (a.n_kv_heads + kTileHeads - 1) / kTileHeads, tile = turn % tiles;
+    const long long first = (long long)(turn / tiles) * kTokens;
+    const int head0 = tile * kTileHeads, heads = min(kTileHeads, a.n_kv_heads - head0);
     unsigned long long there, follows;                           // bit j: token first - 1 + j is written; and goes on with the run
     {
+        long long slot[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {                            // (every warp for itself; the first for all to read)
+            const int j = lane + 32 * x;
+            const long long t = first - 1 + j;
+            slot[x] = -1;
+            if (t >= 0 && t < a.num_tokens && j < kTokens + kBlock) {
+                slot[x] = a.slots[t];
+                if (a.positions) {
+                    Where<kAxes> at;
+                    at.load(a, t);
+                    if (at.lowest() < 0 || at.highest() >= a.max_positions) {
+                        if (threadIdx.x < 32 && tile == 0 && at.lowest() >= 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
+                        slot[x] = -1;
+                    }
+                    if (threadIdx.x < 32) sh.where[j] = make_int4(at.of(0), at.of(1), at.of(2), at.of(3));
+                }
+                if (slot[x] >= a.num_slots) {
+                    if (threadIdx.x < 32 && tile == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
+                    slot[x] = -1;
+                }
+            }
+            if (threadIdx.x < 32) sh.slot[j] = slot[x];
+        }
+        sh.top[threadIdx.x / 16][threadIdx.x % 16] = 0;
+        static_assert(kRopeThreads == 16 * 2 * kTileHeads, "a thread for each run, head and kind");
         const long long p0 = __shfl_up_sync(0xffffffffu, slot[0], 1), p1 = __shfl_up_sync(0xffffffffu, slot[1], 1);
         const long long last = __shfl_sync(0xffffffffu, slot[0], 31);
         const long long before[2] = {lane ? p0 : -1, lane ? p1 : last};
@@ -190,114 +223,187 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArg
         there = b[0] | (unsigned long long)b[1] << 32;
         follows = f[0] | (unsigned long long)f[1] << 32;
     }
-    unsigned long long heads = there & ~follows & (((1ull << a.span) - 1) << 1);   // the runs' first tokens (span <= 32)
-    const __nv_bfloat16* src = is_v ? a.v : a.k;
-    const long long stride = is_v ? a.v_stride : a.k_stride;
-    uint8_t* cache = is_v ? a.v_cache : a.k_cache;
-    uint8_t* all_scales = is_v ? a.v_scales : a.k_scales;
-    const bool norm = !is_v && a.k_weight, turns = !is_v && w.turns;
+    // The runs' first tokens, and the tokens from the first run's begin to the last one's end: theirs, but for ones that are not written.
+    const unsigned long long starts = there & ~follows & (((1ull << kTokens) - 1) << 1);
+    if (!starts) return;
+    const int begin = __ffsll((long long)starts) - 1, last_run = 63 - __clzll((long long)starts);
+    const int end = last_run + __ffsll((long long)~(follows >> (last_run + 1)));
+    const int group = threadIdx.x / kLanes, side = group / kTokens, mine = begin + group % kTokens;
+    const bool one_pass = end - begin <= kTokens;                // the rows stay in registers
+    __syncthreads();
+
+    // Item x of this thread: K (x < kHeads) or V of head head_of(x); few tokens: one of either.
+    auto head_of = [&](int x) { return kMany ? (x % kHeads) * S::kSides + side : side % kTileHeads; };
+    auto is_v = [&](int x) { return kMany ? x >= kHeads : side >= kTileHeads; };
+    constexpr int kItems = kMany ? 2 * kHeads : 1;
+    uint4 x0[kItems], x1[kItems];
+    auto load = [&](int j) {                                     // token j of the window
+        const bool in = j < end && (there >> j & 1);
+#pragma unroll
+        for (int x = 0; x < kItems; ++x) {
+            x0[x] = x1[x] = make_uint4(0, 0, 0, 0);
+            if (in && head_of(x) < heads) {
+                const uint4* src = reinterpret_cast<const uint4*>((is_v(x) ? a.v + (first - 1 + j) * a.v_stride : a.k + (first - 1 + j) * a.k_stride) +
+                                                                  (head0 + head_of(x)) * D);
+                x0[x] = src[w.c0];
+                x1[x] = src[w.c1];
+            }
+        }
+        return in;
+    };
+    uint64_t cs[4], sn[4];
+    auto angles = [&](int j) {
+        if (!w.turns || (!kMany && is_v(0))) return;
+        const int4 p = sh.where[j];
+        Where<kAxes> at;
+        at.p[0] = p.x;
+        if constexpr (kAxes) {
+            at.p[1] = p.y;
+            at.p[2] = p.z;
+            at.p[3] = p.w;
+        }
+        load_angles<kAxes>(a, at, l, cs, sn);
+    };
+    auto key = [&](int x) {                                      // item x ready for the cache
+        Part p;
+        unpack8(x0[x], p.f);
+        unpack8(x1[x], p.f + 4);
+        if (a.k_weight) {
+            uint64_t gain[8];                                    // (from L1: registers are short)
+            load8(a.k_weight + 8 * w.c0, gain);
+            load8(a.k_weight + 8 * w.c1, gain + 4);
+            norm_part<kLanes>(p, gain, a.eps, mask);
+        }
+        if (w.turns) turn_part<kInterleaved>(p, cs, sn);
+        return p;
+    };
+    auto run_of = [&](int j) { return __popcll(starts & ((2ull << j) - 1)) - 1; };
 #pragma unroll 1
-    for (; heads; heads &= heads - 1) {
-        const int j = __ffsll((long long)heads) - 1;
-        const int n = __ffsll((long long)~(follows >> (j + 1)));  // tokens of the run, kBlock at most
-        const long long s0 = __shfl_sync(0xffffffffu, j < 32 ? slot[0] : slot[1], j & 31);
-        const int blk = (int)(s0 >> a.log2_block), off = (int)s0 & (kBlock - 1);
-        const size_t t0 = (size_t)first - 1 + j;
-        uint8_t* scales = all_scales + (size_t)blk * a.n_kv_heads + h;
-        uint8_t* rows = cache + ((size_t)blk * a.n_kv_heads + h) * (kBlock * D);
-        uint4 x0[kRounds], x1[kRounds];
+    for (int j = mine; j < begin + (end - begin + kTokens - 1) / kTokens * kTokens; j += kTokens) {
+        const bool in = load(j);
+        if (in) angles(j);
+        const int run = in ? run_of(j) : 0;
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const int i = r * kRowsAt + g;
-            x0[r] = x1[r] = make_uint4(0, 0, 0, 0);
-            if (i < n) {
-                const uint4* p = reinterpret_cast<const uint4*>(src + (long long)(t0 + i) * stride + h * D);
-                x0[r] = p[w.c0];
-                x1[r] = p[w.c1];
+        for (int x = 0; x < kItems; ++x) {
+            uint32_t top;
+            if (is_v(x)) {
+                uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(x0[x].x & 0x7fff7fffu, x0[x].y & 0x7fff7fffu),
+                                               __vmaxu2(x0[x].z & 0x7fff7fffu, x0[x].w & 0x7fff7fffu)),
+                                      __vmaxu2(__vmaxu2(x1[x].x & 0x7fff7fffu, x1[x].y & 0x7fff7fffu),
+                                               __vmaxu2(x1[x].z & 0x7fff7fffu, x1[x].w & 0x7fff7fffu)));
+                m = max(m & 0xffffu, m >> 16);
+                top = m << 16;
+                if (m >= 0x7f80u) {                              // NaN is no value, and infinities saturate
+                    Part p;
+                    unpack8(x0[x], p.f);
+                    unpack8(x1[x], p.f + 4);
+                    top = __float_as_uint(finite_top_of(p, 0.f));
+                }
+            } else {
+                const Part p = key(x);
+                float f = top_of(p, 0.f);
+                if (!(f < INFINITY)) f = finite_top_of(p, 0.f);
+                top = __float_as_uint(f);
             }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+            if (in && l == 0 && head_of(x) < heads) atomicMax(&sh.top[run][(is_v(x) ? kTileHeads : 0) + head_of(x)], top);
         }
-        const int old = off ? *scales : 0;
-        // round r's part of the rows, ready for the cache
-        auto part = [&](int r) {
-            Part p;
-            unpack8(x0[r], p.f);
-            unpack8(x1[r], p.f + 4);
-            if (norm) {
-                uint64_t gain[8];                                // (from L1: registers are short)
-                load8(a.k_weight + 8 * w.c0, gain);
-                load8(a.k_weight + 8 * w.c1, gain + 4);
-                norm_part<kLanes>(p, gain, a.eps, mask);
-            }
-            const int i = r * kRowsAt + g;
-            if (turns && i < n) {
-                Where<kAxes> at;
-                at.load(a, t0 + i);
-                uint64_t cs[4], sn[4];
-                load_angles<kAxes>(a, at, l, cs, sn);
-                turn_part<kInterleaved>(p, cs, sn);
-            }
-            return p;
-        };
-        float top = 0.f;
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            if (r * kRowsAt < n) top = top_of(part(r), top);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (!(top < INFINITY)) {                                 // infinities saturate, at the scale of the others
-            top = 0.f;
-#pragma unroll
-            for (int r = 0; r < kRounds; ++r)
-                if (r * kRowsAt < n) top = finite_top_of(part(r), top);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    __syncthreads();
+    {
+        // a thread for each run, head and kind: the scale, and where it has grown the block's other codes again, by its warp
+        const int run = threadIdx.x / 16, kind = threadIdx.x % 16 / kTileHeads, h = threadIdx.x % kTileHeads;
+        int old = 0, now = 0, off = 0, n = 0;
+        size_t place = 0;                                        // of the block's head
+        if (run < __popcll(starts) && h < heads) {
+            unsigned long long rest = starts;
+            for (int i = 0; i < run; ++i) rest &= rest - 1;
+            const int j = __ffsll((long long)rest) - 1;
+            const long long slot = sh.slot[j];
+            off = (int)slot & (kBlock - 1);
+            n = __ffsll((long long)~(follows >> (j + 1)));
+            place = (size_t)(slot >> a.log2_block) * a.n_kv_heads + head0 + h;
+            uint8_t* scale = (kind ? a.v_scales : a.k_scales) + place;
+            old = off ? *scale : 0;
+            now = max(old, scale_byte(__uint_as_float(sh.top[run][threadIdx.x % 16])));
+            if (now != old || !off) *scale = (uint8_t)now;
+            sh.top[run][threadIdx.x % 16] = now;
         }
-        const int now = max(old, scale_byte(top));
-        const float up = scale_of(254 - now);
-        const uint64_t by = pair(up, up);
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const int i = r * kRowsAt + g;
-            if (r * kRowsAt >= n) break;
-            const Part p = part(r);
-            if (i < n) {
-                uint2* dst = reinterpret_cast<uint2*>(rows + (off + i) * D);
-                dst[w.c0] = codes_by(p.f, by);
-                dst[w.c1] = codes_by(p.f + 4, by);
-            }
-        }
-        if (off && now > old) {                                  // the scale has grown: the block's other codes again
-            const float down = now - old > 126 ? 0.f : scale_of(127 - (now - old));
+        for (unsigned grown = __ballot_sync(0xffffffffu, off && now > old); grown; grown &= grown - 1) {
+            const int from = __ffs(grown) - 1;
+            const int by = __shfl_sync(0xffffffffu, now - old, from), o = __shfl_sync(0xffffffffu, off, from);
+            const int tokens = __shfl_sync(0xffffffffu, n, from), v = __shfl_sync(0xffffffffu, kind, from);
+            const unsigned long long at = __shfl_sync(0xffffffffu, (unsigned long long)place, from);
+            const float down = by > 126 ? 0.f : scale_of(127 - by);
+            uint4* codes = reinterpret_cast<uint4*>((v ? a.v_cache : a.k_cache) + at * (kBlock * D));
 #pragma unroll 1
             for (int x = lane; x < kBlock * (D / 16); x += 32) {
                 const int row = x / (D / 16);
-                if (row >= off && row < off + n) continue;
-                uint4* p = reinterpret_cast<uint4*>(rows) + x;
-                uint4 v = *p;
-                v.x = code_again(v.x, down);
-                v.y = code_again(v.y, down);
-                v.z = code_again(v.z, down);
-                v.w = code_again(v.w, down);
-                *p = v;
+                if (row >= o && row < o + tokens) continue;
+                uint4 c = codes[x];
+                c.x = code_again(c.x, down);
+                c.y = code_again(c.y, down);
+                c.z = code_again(c.z, down);
+                c.w = code_again(c.w, down);
+                codes[x] = c;
             }
         }
-        if (lane == 0 && (now != old || !off)) *scales = (uint8_t)now;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int j = mine; j < begin + (end - begin + kTokens - 1) / kTokens * kTokens; j += kTokens) {
+        bool in = j < end && (there >> j & 1);
+        if (!one_pass) {
+            in = load(j);
+            if (in) angles(j);
+        }
+        const int run = in ? run_of(j) : 0;
+        const long long slot = in ? sh.slot[j] : 0;
+        const size_t place = (size_t)(slot >> a.log2_block) * a.n_kv_heads + head0;
+        const int row = (int)slot & (kBlock - 1);
+#pragma unroll
+        for (int x = 0; x < kItems; ++x) {
+            const int h = head_of(x);
+            Part p;
+            if (is_v(x)) {
+                unpack8(x0[x], p.f);
+                unpack8(x1[x], p.f + 4);
+            } else {
+                p = key(x);
+            }
+            if (in && h < heads) {
+                const float up = scale_of(254 - (int)sh.top[run][(is_v(x) ? kTileHeads : 0) + h]);
+                uint2* dst = reinterpret_cast<uint2*>((is_v(x) ? a.v_cache : a.k_cache) + ((place + h) * kBlock + row) * D);
+                dst[w.c0] = codes_by(p.f, pair(up, up));
+                dst[w.c1] = codes_by(p.f + 4, pair(up, up));
+            }
+        }
     }
 }
 
-template <int D, int kBlock>
+template <int D, int kBlock, bool kMany>
 cudaError_t launch_append(const AppendArgs& a, int interleaved, cudaStream_t st) {
-    constexpr int kLanes = D / 16;
-    const long long kv = ((long long)a.num_tokens + a.span - 1) / a.span * 2 * a.n_kv_heads;
+    using S = Share<D, kMany>;
+    constexpr int kParts = kRopeThreads / S::kLanes;
+    const long long kv = ((long long)a.num_tokens + S::kTokens - 1) / S::kTokens * ((a.n_kv_heads + kTileHeads - 1) / kTileHeads);
     const long long q = a.n_q_heads ? (long long)a.num_tokens * ((a.n_q_heads + a.q_heads_per - 1) / a.q_heads_per) : 0;
     AppendArgs b = a;
-    b.kv_blocks = (int)((kv + kWarps - 1) / kWarps);
-    const int q_blocks = (int)((q + kRopeThreads / kLanes - 1) / (kRopeThreads / kLanes));
+    b.kv_blocks = (int)kv;
+    const int q_blocks = (int)((q + kParts - 1) / kParts);
     b.every = q_blocks / b.kv_blocks;
-    const unsigned grid = (unsigned)(b.kv_blocks + q_blocks);
-    const auto kernel = a.num_axes ? (interleaved ? append_kernel<D, kBlock, true, true> : append_kernel<D, kBlock, false, true>)
-                                   : (interleaved ? append_kernel<D, kBlock, true, false> : append_kernel<D, kBlock, false, false>);
-    return pa_host::launch_dependent(kernel, dim3(grid), dim3(kRopeThreads), 0, st, b);
+    const auto kernel = a.num_axes ? (interleaved ? append_kernel<D, kBlock, true, true, kMany> : append_kernel<D, kBlock, false, true, kMany>)
+                                   : (interleaved ? append_kernel<D, kBlock, true, false, kMany> : append_kernel<D, kBlock, false, false, kMany>);
+    constexpr int kSmem = kWarps * kFlight * 1024;
+    static int attr[4][64] = {{0}};
+    const cudaError_t e = pa_host::ensure_smem_attr(kernel, kSmem, attr[2 * (a.num_axes != 0) + (interleaved != 0)]);
+    if (e != cudaSuccess) return e;
+    return pa_host::launch_dependent(kernel, dim3((unsigned)(b.kv_blocks + q_blocks)), dim3(kRopeThreads), kSmem, st, b);
+}
+
+template <int D, int kBlock>
+cudaError_t launch_append(const AppendArgs& a, bool many, int interleaved, cudaStream_t st) {
+    return many ? launch_append<D, kBlock, true>(a, interleaved, st) : launch_append<D, kBlock, false>(a, interleaved, st);
 }
 
 int append(void* q_out, void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales, const void* q, const void* k,
@@ -357,17 +463,17 @@ int append(void* q_out, void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t
     a.n_kv_heads = n_kv_heads;
     a.block_size = block_size;
     a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
-    a.span = num_tokens <= 2048 ? 1 : block_size;
     const bool many = n_q_heads >= 8 && (long long)num_tokens * (n_q_heads + 2 * n_kv_heads) * d_head >= 12000000;
+    const bool many_tokens = num_tokens >= 1024;
     a.q_heads_per = many ? (n_q_heads + 1) / 2 : 1;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        d_head == 128 ? (block_size == 8    ? launch_append<128, 8>(a, interleaved, st)
-                         : block_size == 16 ? launch_append<128, 16>(a, interleaved, st)
-                                            : launch_append<128, 32>(a, interleaved, st))
-                      : (block_size == 8    ? launch_append<64, 8>(a, interleaved, st)
-                         : block_size == 16 ? launch_append<64, 16>(a, interleaved, st)
-                                            : launch_append<64, 32>(a, interleaved, st));
+        d_head == 128 ? (block_size == 8    ? launch_append<128, 8>(a, many_tokens, interleaved, st)
+                         : block_size == 16 ? launch_append<128, 16>(a, many_tokens, interleaved, st)
+                                            : launch_append<128, 32>(a, many_tokens, interleaved, st))
+                      : (block_size == 8    ? launch_append<64, 8>(a, many_tokens, interleaved, st)
+                         : block_size == 16 ? launch_append<64, 16>(a, many_tokens, interleaved, st)
+                                            : launch_append<64, 32>(a, many_tokens, interleaved, st));
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
