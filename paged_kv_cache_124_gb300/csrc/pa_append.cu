@@ -13,9 +13,8 @@
 // a block).  A thread block takes the runs that begin among its own tokens,
 // for up to eight heads: D / 16 lanes hold a token's part of a head, as
 // pa_rope.cu's do, and a token's angles are loaded once for all of its heads.
-// The rows stay in registers as they came while the largest values of each
-// run and head meet in shared memory, and go through the arithmetic again for
-// the codes (a run of 32-bit values would not fit).  Queries go beside, in
+// Turned keys wait in shared memory, in 32 bits, and values in registers, as
+// they came, while the largest of each run and head meet.  Queries go beside, in
 // blocks of their own.
 
 #include <cuda_fp16.h>
@@ -73,6 +72,12 @@ __device__ __forceinline__ uint2 codes_by(const uint64_t* f, uint64_t by) {
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
+    return d;
+}
+
 // Four codes times `by`, rounded again.
 __device__ __forceinline__ uint32_t code_again(uint32_t w, float by) {
     uint32_t lo, hi;
@@ -104,6 +109,7 @@ __device__ __forceinline__ void read_slot(uint32_t slot, int lane, uint64_t* f) 
 
 constexpr int kFlight = 8;                             // heads of a query on their way
 constexpr int kTileHeads = 8;                          // KV heads of a thread block
+constexpr int kSharedBytes = 64 * 8 + 64 * 16 + 16 * 16 * 4;
 constexpr int kWindow = 64;                            // tokens that a thread block looks at: its own, one before, kBlock - 1 behind
 
 // Tokens of a thread block, and how its D / 16 lanes per head's part go over
@@ -117,7 +123,7 @@ struct Share {
 };
 
 template <int D, int kBlock, bool kInterleaved, bool kAxes, bool kMany>
-__global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArgs a) {
     using S = Share<D, kMany>;
     constexpr int kLanes = S::kLanes, kTokens = S::kTokens, kHeads = S::kHeads;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -179,6 +185,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArg
         int4 where[kWindow];                                     // their positions
         uint32_t top[16][2 * kTileHeads];                        // largest magnitudes of each run's keys, then values; then scales
     };
+    static_assert(sizeof(Shared) == kSharedBytes, "kSharedBytes");
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     const int tiles = (a.n_kv_heads + kTileHeads - 1) / kTileHeads, tile = turn % tiles;
     const long long first = (long long)(turn / tiles) * kTokens;
@@ -232,28 +239,24 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArg
     const bool one_pass = end - begin <= kTokens;                // the rows stay in registers
     __syncthreads();
 
-    // Item x of this thread: K (x < kHeads) or V of head head_of(x); few tokens: one of either.
-    auto head_of = [&](int x) { return kMany ? (x % kHeads) * S::kSides + side : side % kTileHeads; };
-    auto is_v = [&](int x) { return kMany ? x >= kHeads : side >= kTileHeads; };
-    constexpr int kItems = kMany ? 2 * kHeads : 1;
-    uint4 x0[kItems], x1[kItems];
-    auto load = [&](int j) {                                     // token j of the window
-        const bool in = j < end && (there >> j & 1);
+    // This thread's parts: of heads side, side + kSides, .. both keys and values; few tokens: one of either.
+    auto head_of = [&](int x) { return kMany ? x * S::kSides + side : side % kTileHeads; };
+    const bool keys = kMany || side < kTileHeads, values = kMany || side >= kTileHeads;
+    uint4 x0[kHeads], x1[kHeads];
+    auto load = [&](const __nv_bfloat16* rows, long long stride, int j, bool in) {   // token j of the window
 #pragma unroll
-        for (int x = 0; x < kItems; ++x) {
+        for (int x = 0; x < kHeads; ++x) {
             x0[x] = x1[x] = make_uint4(0, 0, 0, 0);
             if (in && head_of(x) < heads) {
-                const uint4* src = reinterpret_cast<const uint4*>((is_v(x) ? a.v + (first - 1 + j) * a.v_stride : a.k + (first - 1 + j) * a.k_stride) +
-                                                                  (head0 + head_of(x)) * D);
+                const uint4* src = reinterpret_cast<const uint4*>(rows + (first - 1 + j) * stride + (head0 + head_of(x)) * D);
                 x0[x] = src[w.c0];
                 x1[x] = src[w.c1];
             }
         }
-        return in;
     };
     uint64_t cs[4], sn[4];
-    auto angles = [&](int j) {
-        if (!w.turns || (!kMany && is_v(0))) return;
+    auto angles = [&](int j, bool in) {
+        if (!w.turns || !in) return;
         const int4 p = sh.where[j];
         Where<kAxes> at;
         at.p[0] = p.x;
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArg
         }
         load_angles<kAxes>(a, at, l, cs, sn);
     };
-    auto key = [&](int x) {                                      // item x ready for the cache
+    auto key = [&](int x) {                                      // part x of the keys ready for the cache
         Part p;
         unpack8(x0[x], p.f);
         unpack8(x1[x], p.f + 4);
@@ -277,37 +280,59 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArg
         if (w.turns) turn_part<kInterleaved>(p, cs, sn);
         return p;
     };
-    auto run_of = [&](int j) { return __popcll(starts & ((2ull << j) - 1)) - 1; };
-#pragma unroll 1
-    for (int j = mine; j < begin + (end - begin + kTokens - 1) / kTokens * kTokens; j += kTokens) {
-        const bool in = load(j);
-        if (in) angles(j);
-        const int run = in ? run_of(j) : 0;
+    // where they wait for their scale
+    uint32_t kept = pa::smem_addr(smem + sizeof(Shared)) + 16 * threadIdx.x;
+    auto keep = [&](int x, const Part& p) {
 #pragma unroll
-        for (int x = 0; x < kItems; ++x) {
-            uint32_t top;
-            if (is_v(x)) {
-                uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(x0[x].x & 0x7fff7fffu, x0[x].y & 0x7fff7fffu),
-                                               __vmaxu2(x0[x].z & 0x7fff7fffu, x0[x].w & 0x7fff7fffu)),
-                                      __vmaxu2(__vmaxu2(x1[x].x & 0x7fff7fffu, x1[x].y & 0x7fff7fffu),
-                                               __vmaxu2(x1[x].z & 0x7fff7fffu, x1[x].w & 0x7fff7fffu)));
+        for (int q = 0; q < 4; ++q)
+            asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(kept + (4 * x + q) * (16 * kRopeThreads)), "l"(p.f[2 * q]), "l"(p.f[2 * q + 1]) : "memory");
+    };
+    auto get = [&](int x) {
+        Part p;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(p.f[2 * q]), "=l"(p.f[2 * q + 1]) : "r"(kept + (4 * x + q) * (16 * kRopeThreads)) : "memory");
+        return p;
+    };
+    auto meet = [&](int kind, int x, bool in, int run, uint32_t top) {
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+        if (in && l == 0 && head_of(x) < heads) atomicMax(&sh.top[run][kind * kTileHeads + head_of(x)], top);
+    };
+    auto run_of = [&](int j) { return __popcll(starts & ((2ull << j) - 1)) - 1; };
+    const int stop = begin + (end - begin + kTokens - 1) / kTokens * kTokens;
+#pragma unroll 1
+    for (int j = mine; j < stop; j += kTokens) {
+        const bool in = j < end && (there >> j & 1);
+        const int run = in ? run_of(j) : 0;
+        if (keys) {
+            load(a.k, a.k_stride, j, in);
+            angles(j, in);
+#pragma unroll
+            for (int x = 0; x < kHeads; ++x) {
+                const Part p = key(x);
+                float f = top_of(p, 0.f);
+                if (!(f < INFINITY)) f = finite_top_of(p, 0.f);
+                if (one_pass) keep(x, p);
+                meet(0, x, in, run, __float_as_uint(f));
+            }
+        }
+        if (values) {
+            load(a.v, a.v_stride, j, in);
+#pragma unroll
+            for (int x = 0; x < kHeads; ++x) {
+                uint32_t m = max2(max2(max2(x0[x].x & 0x7fff7fffu, x0[x].y & 0x7fff7fffu), max2(x0[x].z & 0x7fff7fffu, x0[x].w & 0x7fff7fffu)),
+                                  max2(max2(x1[x].x & 0x7fff7fffu, x1[x].y & 0x7fff7fffu), max2(x1[x].z & 0x7fff7fffu, x1[x].w & 0x7fff7fffu)));
                 m = max(m & 0xffffu, m >> 16);
-                top = m << 16;
+                uint32_t top = m << 16;
                 if (m >= 0x7f80u) {                              // NaN is no value, and infinities saturate
                     Part p;
                     unpack8(x0[x], p.f);
                     unpack8(x1[x], p.f + 4);
                     top = __float_as_uint(finite_top_of(p, 0.f));
                 }
-            } else {
-                const Part p = key(x);
-                float f = top_of(p, 0.f);
-                if (!(f < INFINITY)) f = finite_top_of(p, 0.f);
-                top = __float_as_uint(f);
+                meet(1, x, in, run, top);
             }
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
-            if (in && l == 0 && head_of(x) < heads) atomicMax(&sh.top[run][(is_v(x) ? kTileHeads : 0) + head_of(x)], top);
         }
     }
     __syncthreads();
@@ -352,31 +377,43 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const AppendArg
     }
     __syncthreads();
 #pragma unroll 1
-    for (int j = mine; j < begin + (end - begin + kTokens - 1) / kTokens * kTokens; j += kTokens) {
-        bool in = j < end && (there >> j & 1);
-        if (!one_pass) {
-            in = load(j);
-            if (in) angles(j);
-        }
+    for (int j = mine; j < stop; j += kTokens) {
+        const bool in = j < end && (there >> j & 1);
         const int run = in ? run_of(j) : 0;
         const long long slot = in ? sh.slot[j] : 0;
-        const size_t place = (size_t)(slot >> a.log2_block) * a.n_kv_heads + head0;
-        const int row = (int)slot & (kBlock - 1);
-#pragma unroll
-        for (int x = 0; x < kItems; ++x) {
+        const size_t place = ((size_t)(slot >> a.log2_block) * a.n_kv_heads + head0) * kBlock + ((int)slot & (kBlock - 1));
+        auto put = [&](int kind, int x, const Part& p) {
             const int h = head_of(x);
+            if (!in || h >= heads) return;
+            const float up = scale_of(254 - (int)sh.top[run][kind * kTileHeads + h]);
+            uint2* dst = reinterpret_cast<uint2*>((kind ? a.v_cache : a.k_cache) + (place + (size_t)h * kBlock) * D);
+            dst[w.c0] = codes_by(p.f, pair(up, up));
+            dst[w.c1] = codes_by(p.f + 4, pair(up, up));
+        };
+        auto value = [&](int x) {
             Part p;
-            if (is_v(x)) {
-                unpack8(x0[x], p.f);
-                unpack8(x1[x], p.f + 4);
-            } else {
-                p = key(x);
+            unpack8(x0[x], p.f);
+            unpack8(x1[x], p.f + 4);
+            return p;
+        };
+        if (one_pass) {
+            if (values)
+#pragma unroll
+                for (int x = 0; x < kHeads; ++x) put(1, x, value(x));
+            if (keys)
+#pragma unroll
+                for (int x = 0; x < kHeads; ++x) put(0, x, get(x));
+        } else {
+            if (keys) {
+                load(a.k, a.k_stride, j, in);
+                angles(j, in);
+#pragma unroll
+                for (int x = 0; x < kHeads; ++x) put(0, x, key(x));
             }
-            if (in && h < heads) {
-                const float up = scale_of(254 - (int)sh.top[run][(is_v(x) ? kTileHeads : 0) + h]);
-                uint2* dst = reinterpret_cast<uint2*>((is_v(x) ? a.v_cache : a.k_cache) + ((place + h) * kBlock + row) * D);
-                dst[w.c0] = codes_by(p.f, pair(up, up));
-                dst[w.c1] = codes_by(p.f + 4, pair(up, up));
+            if (values) {
+                load(a.v, a.v_stride, j, in);
+#pragma unroll
+                for (int x = 0; x < kHeads; ++x) put(1, x, value(x));
             }
         }
     }
@@ -394,7 +431,9 @@ cudaError_t launch_append(const AppendArgs& a, int interleaved, cudaStream_t st)
     b.every = q_blocks / b.kv_blocks;
     const auto kernel = a.num_axes ? (interleaved ? append_kernel<D, kBlock, true, true, kMany> : append_kernel<D, kBlock, false, true, kMany>)
                                    : (interleaved ? append_kernel<D, kBlock, true, false, kMany> : append_kernel<D, kBlock, false, false, kMany>);
-    constexpr int kSmem = kWarps * kFlight * 1024;
+    // queries' rows on their way; keys that wait for their scale, in 32 bits, and what a thread block shares of its tokens
+    constexpr int kKept = 64 * kRopeThreads * S::kHeads + kSharedBytes;
+    constexpr int kSmem = kWarps * kFlight * 1024 > kKept ? kWarps * kFlight * 1024 : kKept;
     static int attr[4][64] = {{0}};
     const cudaError_t e = pa_host::ensure_smem_attr(kernel, kSmem, attr[2 * (a.num_axes != 0) + (interleaved != 0)]);
     if (e != cudaSuccess) return e;
