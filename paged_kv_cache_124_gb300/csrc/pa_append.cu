@@ -11,7 +11,7 @@
 //
 // The tokens of one block follow one another (a run: consecutive slots within
 // a block).  A thread block takes the runs that begin among its own tokens,
-// for up to eight heads: D / 16 lanes hold a token's part of a head, as
+// for four or eight heads: D / 16 lanes hold a token's part of a head, as
 // pa_rope.cu's do, and a token's angles are loaded once for all of its heads.
 // Turned keys wait in shared memory, in 32 bits, and values in registers, as
 // they came, while the largest of each run and head meet.  Queries go beside, in
@@ -108,24 +108,38 @@ __device__ __forceinline__ void read_slot(uint32_t slot, int lane, uint64_t* f) 
 }
 
 constexpr int kFlight = 8;                             // heads of a query on their way
-constexpr int kTileHeads = 8;                          // KV heads of a thread block
-constexpr int kSharedBytes = 64 * 8 + 64 * 16 + 16 * 16 * 4;
+constexpr int kRuns = 16;                              // of a thread block at most: a run a token
 constexpr int kWindow = 64;                            // tokens that a thread block looks at: its own, one before, kBlock - 1 behind
 
-// Tokens of a thread block, and how its D / 16 lanes per head's part go over
-// them: kMany: 16 tokens, the heads in turn (4 of D 128); else 16 parts side by
-// side, a key or a value of a head each, and the tokens that leaves (2 of D 128).
-template <int D, bool kMany>
-struct Share {
-    static constexpr int kLanes = D / 16, kGroups = kRopeThreads / kLanes;
-    static constexpr int kTokens = kMany ? 16 : kGroups / 16, kSides = kGroups / kTokens;
-    static constexpr int kHeads = kMany ? kTileHeads / kSides : 1;
+struct Shared {                                        // what a thread block of keys and values shares
+    long long slot[kWindow];                           // of tokens first - 1 on; negative where nothing is written
+    int4 where[kWindow];                               // their positions
+    unsigned long long there, follows;                 // bit j: token first - 1 + j is written; and goes on with the run
+    uint32_t top[kRuns][16];                           // largest magnitudes of each run's keys, then values; then scales
+    int grown[kRuns][16];                              // log2 of what the block's other codes are to be divided by
 };
 
-template <int D, int kBlock, bool kInterleaved, bool kAxes, bool kMany>
-__global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArgs a) {
-    using S = Share<D, kMany>;
-    constexpr int kLanes = S::kLanes, kTokens = S::kTokens, kHeads = S::kHeads;
+// How a thread block goes over keys and values, D / 16 lanes a token and head.
+//   kFew   4 heads' keys and values side by side, a part a thread, of the
+//          tokens that leaves (4 of D 128): the least latency.
+//   kSome  16 tokens, 4 heads, 2 of them in turn (D 128).
+//   kMany  16 tokens, 8 heads, 4 in turn: a token's angles serve the most.
+enum Mode { kFew, kSome, kMany };
+template <int D, int kMode>
+struct Share {
+    static constexpr int kLanes = D / 16, kGroups = kRopeThreads / kLanes, kTile = kMode == kMany ? 8 : 4;
+    static constexpr int kTokens = kMode == kFew ? kGroups / (2 * kTile) : kRuns, kSides = kGroups / kTokens;
+    static constexpr int kHeads = kMode == kFew ? 1 : kTile / kSides;
+    static constexpr int kTogether = kMode == kSome;           // keys and values loaded together (kMany has no registers for both)
+};
+
+// (Thread blocks an SM: 2 against 3 with many tokens, whose registers then hold the gains, 32,048 tokens 137 / 141 us; 3
+// against 2 with fewer, 250 of 256 4.6 / 5.3.)
+template <int D, bool kInterleaved, bool kAxes, int kMode>
+__global__ void __launch_bounds__(kRopeThreads, kMode == kMany ? 2 : 3) append_kernel(const AppendArgs a) {
+    using S = Share<D, kMode>;
+    constexpr int kLanes = S::kLanes, kTokens = S::kTokens, kHeads = S::kHeads, kTileHeads = S::kTile;
+    const int kBlock = 1 << a.log2_block;
     extern __shared__ __align__(16) uint8_t smem[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -159,7 +173,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
                 load8(a.q_weight + 8 * w.c1, gain + 4);
             }
             int u = 0;
-#pragma unroll 1
+#pragma unroll 2
             for (int h = h0; h < h1; ++h) {
                 wait_copies<kFlight - 1>();
                 const uint32_t slot = slots + 1024 * u;
@@ -180,21 +194,16 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
         return;
     }
     // ---------------------------------------------------------------- keys and values
-    struct Shared {
-        long long slot[kWindow];                                 // of tokens first - 1 on; negative where nothing is written
-        int4 where[kWindow];                                     // their positions
-        uint32_t top[16][2 * kTileHeads];                        // largest magnitudes of each run's keys, then values; then scales
-    };
-    static_assert(sizeof(Shared) == kSharedBytes, "kSharedBytes");
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     const int tiles = (a.n_kv_heads + kTileHeads - 1) / kTileHeads, tile = turn % tiles;
     const long long first = (long long)(turn / tiles) * kTokens;
     const int head0 = tile * kTileHeads, heads = min(kTileHeads, a.n_kv_heads - head0);
-    unsigned long long there, follows;                           // bit j: token first - 1 + j is written; and goes on with the run
-    {
+    sh.top[threadIdx.x / 16][threadIdx.x % 16] = 0;
+    static_assert(kRopeThreads == 16 * kRuns, "a thread for each");
+    if (threadIdx.x < 32) {                                      // a warp finds the runs
         long long slot[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {                            // (every warp for itself; the first for all to read)
+        for (int x = 0; x < 2; ++x) {
             const int j = lane + 32 * x;
             const long long t = first - 1 + j;
             slot[x] = -1;
@@ -204,20 +213,18 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
                     Where<kAxes> at;
                     at.load(a, t);
                     if (at.lowest() < 0 || at.highest() >= a.max_positions) {
-                        if (threadIdx.x < 32 && tile == 0 && at.lowest() >= 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
+                        if (tile == 0 && at.lowest() >= 0) pa::set_status(a.status, PA_DEV_BAD_POSITION);
                         slot[x] = -1;
                     }
-                    if (threadIdx.x < 32) sh.where[j] = make_int4(at.of(0), at.of(1), at.of(2), at.of(3));
+                    sh.where[j] = make_int4(at.of(0), at.of(1), at.of(2), at.of(3));
                 }
                 if (slot[x] >= a.num_slots) {
-                    if (threadIdx.x < 32 && tile == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
+                    if (tile == 0) pa::set_status(a.status, PA_DEV_BAD_SLOT);
                     slot[x] = -1;
                 }
             }
-            if (threadIdx.x < 32) sh.slot[j] = slot[x];
+            sh.slot[j] = slot[x];
         }
-        sh.top[threadIdx.x / 16][threadIdx.x % 16] = 0;
-        static_assert(kRopeThreads == 16 * 2 * kTileHeads, "a thread for each run, head and kind");
         const long long p0 = __shfl_up_sync(0xffffffffu, slot[0], 1), p1 = __shfl_up_sync(0xffffffffu, slot[1], 1);
         const long long last = __shfl_sync(0xffffffffu, slot[0], 31);
         const long long before[2] = {lane ? p0 : -1, lane ? p1 : last};
@@ -227,9 +234,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
             b[x] = __ballot_sync(0xffffffffu, slot[x] >= 0);
             f[x] = __ballot_sync(0xffffffffu, slot[x] >= 0 && before[x] >= 0 && slot[x] == before[x] + 1 && (slot[x] & (kBlock - 1)));
         }
-        there = b[0] | (unsigned long long)b[1] << 32;
-        follows = f[0] | (unsigned long long)f[1] << 32;
+        if (lane == 0) {
+            sh.there = b[0] | (unsigned long long)b[1] << 32;
+            sh.follows = f[0] | (unsigned long long)f[1] << 32;
+        }
     }
+    __syncthreads();
+    const unsigned long long there = sh.there, follows = sh.follows;
     // The runs' first tokens, and the tokens from the first run's begin to the last one's end: theirs, but for ones that are not written.
     const unsigned long long starts = there & ~follows & (((1ull << kTokens) - 1) << 1);
     if (!starts) return;
@@ -237,20 +248,22 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
     const int end = last_run + __ffsll((long long)~(follows >> (last_run + 1)));
     const int group = threadIdx.x / kLanes, side = group / kTokens, mine = begin + group % kTokens;
     const bool one_pass = end - begin <= kTokens;                // the rows stay in registers
-    __syncthreads();
 
     // This thread's parts: of heads side, side + kSides, .. both keys and values; few tokens: one of either.
-    auto head_of = [&](int x) { return kMany ? x * S::kSides + side : side % kTileHeads; };
-    const bool keys = kMany || side < kTileHeads, values = kMany || side >= kTileHeads;
-    uint4 x0[kHeads], x1[kHeads];
-    auto load = [&](const __nv_bfloat16* rows, long long stride, int j, bool in) {   // token j of the window
+    auto head_of = [&](int x) { return kMode != kFew ? x * S::kSides + side : side % kTileHeads; };
+    const bool keys = kMode != kFew || side < kTileHeads, values = kMode != kFew || side >= kTileHeads;
+    struct Raw {
+        uint4 x0[kHeads], x1[kHeads];
+    };
+    Raw k, v;
+    auto load = [&](const __nv_bfloat16* rows, long long stride, int j, bool in, Raw& r) {   // token j of the window
 #pragma unroll
         for (int x = 0; x < kHeads; ++x) {
-            x0[x] = x1[x] = make_uint4(0, 0, 0, 0);
+            r.x0[x] = r.x1[x] = make_uint4(0, 0, 0, 0);
             if (in && head_of(x) < heads) {
                 const uint4* src = reinterpret_cast<const uint4*>(rows + (first - 1 + j) * stride + (head0 + head_of(x)) * D);
-                x0[x] = src[w.c0];
-                x1[x] = src[w.c1];
+                r.x0[x] = src[w.c0];
+                r.x1[x] = src[w.c1];
             }
         }
     };
@@ -267,14 +280,20 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
         }
         load_angles<kAxes>(a, at, l, cs, sn);
     };
+    uint64_t gain[8];
+    if (a.k_weight && kMode == kMany) {
+        load8(a.k_weight + 8 * w.c0, gain);
+        load8(a.k_weight + 8 * w.c1, gain + 4);
+    }
     auto key = [&](int x) {                                      // part x of the keys ready for the cache
         Part p;
-        unpack8(x0[x], p.f);
-        unpack8(x1[x], p.f + 4);
+        unpack8(k.x0[x], p.f);
+        unpack8(k.x1[x], p.f + 4);
         if (a.k_weight) {
-            uint64_t gain[8];                                    // (from L1: registers are short)
-            load8(a.k_weight + 8 * w.c0, gain);
-            load8(a.k_weight + 8 * w.c1, gain + 4);
+            if (kMode != kMany) {                                // (from L1: registers are short)
+                load8(a.k_weight + 8 * w.c0, gain);
+                load8(a.k_weight + 8 * w.c1, gain + 4);
+            }
             norm_part<kLanes>(p, gain, a.eps, mask);
         }
         if (w.turns) turn_part<kInterleaved>(p, cs, sn);
@@ -305,8 +324,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
     for (int j = mine; j < stop; j += kTokens) {
         const bool in = j < end && (there >> j & 1);
         const int run = in ? run_of(j) : 0;
+        if (keys) load(a.k, a.k_stride, j, in, k);
+        if (values && S::kTogether) load(a.v, a.v_stride, j, in, v);
         if (keys) {
-            load(a.k, a.k_stride, j, in);
             angles(j, in);
 #pragma unroll
             for (int x = 0; x < kHeads; ++x) {
@@ -318,17 +338,18 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
             }
         }
         if (values) {
-            load(a.v, a.v_stride, j, in);
+            if (!S::kTogether) load(a.v, a.v_stride, j, in, v);
 #pragma unroll
             for (int x = 0; x < kHeads; ++x) {
-                uint32_t m = max2(max2(max2(x0[x].x & 0x7fff7fffu, x0[x].y & 0x7fff7fffu), max2(x0[x].z & 0x7fff7fffu, x0[x].w & 0x7fff7fffu)),
-                                  max2(max2(x1[x].x & 0x7fff7fffu, x1[x].y & 0x7fff7fffu), max2(x1[x].z & 0x7fff7fffu, x1[x].w & 0x7fff7fffu)));
+                const uint4 y = v.x0[x], z = v.x1[x];
+                uint32_t m = max2(max2(max2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), max2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)),
+                                  max2(max2(z.x & 0x7fff7fffu, z.y & 0x7fff7fffu), max2(z.z & 0x7fff7fffu, z.w & 0x7fff7fffu)));
                 m = max(m & 0xffffu, m >> 16);
                 uint32_t top = m << 16;
                 if (m >= 0x7f80u) {                              // NaN is no value, and infinities saturate
                     Part p;
-                    unpack8(x0[x], p.f);
-                    unpack8(x1[x], p.f + 4);
+                    unpack8(y, p.f);
+                    unpack8(z, p.f + 4);
                     top = __float_as_uint(finite_top_of(p, 0.f));
                 }
                 meet(1, x, in, run, top);
@@ -336,46 +357,51 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
         }
     }
     __syncthreads();
-    {
-        // a thread for each run, head and kind: the scale, and where it has grown the block's other codes again, by its warp
-        const int run = threadIdx.x / 16, kind = threadIdx.x % 16 / kTileHeads, h = threadIdx.x % kTileHeads;
-        int old = 0, now = 0, off = 0, n = 0;
-        size_t place = 0;                                        // of the block's head
-        if (run < __popcll(starts) && h < heads) {
-            unsigned long long rest = starts;
-            for (int i = 0; i < run; ++i) rest &= rest - 1;
-            const int j = __ffsll((long long)rest) - 1;
-            const long long slot = sh.slot[j];
-            off = (int)slot & (kBlock - 1);
-            n = __ffsll((long long)~(follows >> (j + 1)));
-            place = (size_t)(slot >> a.log2_block) * a.n_kv_heads + head0 + h;
-            uint8_t* scale = (kind ? a.v_scales : a.k_scales) + place;
-            old = off ? *scale : 0;
-            now = max(old, scale_byte(__uint_as_float(sh.top[run][threadIdx.x % 16])));
+    const int runs = __popcll(starts);
+    // the block that run's tokens go to, from `off` on, and its head (an index of scales)
+    auto block_of = [&](int run, int h, int& off, int& n) {
+        unsigned long long rest = starts;
+        for (int i = 0; i < run; ++i) rest &= rest - 1;
+        const int j = __ffsll((long long)rest) - 1;
+        off = (int)sh.slot[j] & (kBlock - 1);
+        n = __ffsll((long long)~(follows >> (j + 1)));
+        return (size_t)(sh.slot[j] >> a.log2_block) * a.n_kv_heads + head0 + h;
+    };
+    if (threadIdx.x < runs * 2 * kTileHeads) {                   // a thread for each run, kind and head: its scale
+        const int run = threadIdx.x / (2 * kTileHeads), kh = threadIdx.x % (2 * kTileHeads), h = kh % kTileHeads;
+        if (h < heads) {
+            int off, n;
+            uint8_t* scale = (kh < kTileHeads ? a.k_scales : a.v_scales) + block_of(run, h, off, n);
+            const int old = off ? *scale : 0, now = max(old, scale_byte(__uint_as_float(sh.top[run][kh])));
             if (now != old || !off) *scale = (uint8_t)now;
-            sh.top[run][threadIdx.x % 16] = now;
-        }
-        for (unsigned grown = __ballot_sync(0xffffffffu, off && now > old); grown; grown &= grown - 1) {
-            const int from = __ffs(grown) - 1;
-            const int by = __shfl_sync(0xffffffffu, now - old, from), o = __shfl_sync(0xffffffffu, off, from);
-            const int tokens = __shfl_sync(0xffffffffu, n, from), v = __shfl_sync(0xffffffffu, kind, from);
-            const unsigned long long at = __shfl_sync(0xffffffffu, (unsigned long long)place, from);
-            const float down = by > 126 ? 0.f : scale_of(127 - by);
-            uint4* codes = reinterpret_cast<uint4*>((v ? a.v_cache : a.k_cache) + at * (kBlock * D));
-#pragma unroll 1
-            for (int x = lane; x < kBlock * (D / 16); x += 32) {
-                const int row = x / (D / 16);
-                if (row >= o && row < o + tokens) continue;
-                uint4 c = codes[x];
-                c.x = code_again(c.x, down);
-                c.y = code_again(c.y, down);
-                c.z = code_again(c.z, down);
-                c.w = code_again(c.w, down);
-                codes[x] = c;
-            }
+            sh.top[run][kh] = now;
+            sh.grown[run][kh] = off ? now - old : 0;
+        } else {
+            sh.grown[run][kh] = 0;
         }
     }
     __syncthreads();
+    // where a scale has grown, the block's other codes again
+#pragma unroll 1
+    for (int x = threadIdx.x / 32; x < runs * 2 * kTileHeads; x += kWarps) {
+        const int run = x / (2 * kTileHeads), kh = x % (2 * kTileHeads), by = sh.grown[run][kh];
+        if (!by) continue;
+        int off, n;
+        const size_t place = block_of(run, kh % kTileHeads, off, n);
+        const float down = by > 126 ? 0.f : scale_of(127 - by);
+        uint4* codes = reinterpret_cast<uint4*>((kh < kTileHeads ? a.k_cache : a.v_cache) + place * (kBlock * D));
+#pragma unroll 2
+        for (int y = lane; y < kBlock * (D / 16); y += 32) {
+            const int row = y / (D / 16);
+            if (row >= off && row < off + n) continue;
+            uint4 c = codes[y];
+            c.x = code_again(c.x, down);
+            c.y = code_again(c.y, down);
+            c.z = code_again(c.z, down);
+            c.w = code_again(c.w, down);
+            codes[y] = c;
+        }
+    }
 #pragma unroll 1
     for (int j = mine; j < stop; j += kTokens) {
         const bool in = j < end && (there >> j & 1);
@@ -392,8 +418,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
         };
         auto value = [&](int x) {
             Part p;
-            unpack8(x0[x], p.f);
-            unpack8(x1[x], p.f + 4);
+            unpack8(v.x0[x], p.f);
+            unpack8(v.x1[x], p.f + 4);
             return p;
         };
         if (one_pass) {
@@ -405,13 +431,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
                 for (int x = 0; x < kHeads; ++x) put(0, x, get(x));
         } else {
             if (keys) {
-                load(a.k, a.k_stride, j, in);
+                load(a.k, a.k_stride, j, in, k);
                 angles(j, in);
 #pragma unroll
                 for (int x = 0; x < kHeads; ++x) put(0, x, key(x));
             }
             if (values) {
-                load(a.v, a.v_stride, j, in);
+                load(a.v, a.v_stride, j, in, v);
 #pragma unroll
                 for (int x = 0; x < kHeads; ++x) put(1, x, value(x));
             }
@@ -419,20 +445,20 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_kernel(const AppendArg
     }
 }
 
-template <int D, int kBlock, bool kMany>
+template <int D, int kMode>
 cudaError_t launch_append(const AppendArgs& a, int interleaved, cudaStream_t st) {
-    using S = Share<D, kMany>;
+    using S = Share<D, kMode>;
     constexpr int kParts = kRopeThreads / S::kLanes;
-    const long long kv = ((long long)a.num_tokens + S::kTokens - 1) / S::kTokens * ((a.n_kv_heads + kTileHeads - 1) / kTileHeads);
+    const long long kv = ((long long)a.num_tokens + S::kTokens - 1) / S::kTokens * ((a.n_kv_heads + S::kTile - 1) / S::kTile);
     const long long q = a.n_q_heads ? (long long)a.num_tokens * ((a.n_q_heads + a.q_heads_per - 1) / a.q_heads_per) : 0;
     AppendArgs b = a;
     b.kv_blocks = (int)kv;
     const int q_blocks = (int)((q + kParts - 1) / kParts);
     b.every = q_blocks / b.kv_blocks;
-    const auto kernel = a.num_axes ? (interleaved ? append_kernel<D, kBlock, true, true, kMany> : append_kernel<D, kBlock, false, true, kMany>)
-                                   : (interleaved ? append_kernel<D, kBlock, true, false, kMany> : append_kernel<D, kBlock, false, false, kMany>);
+    const auto kernel = a.num_axes ? (interleaved ? append_kernel<D, true, true, kMode> : append_kernel<D, false, true, kMode>)
+                                   : (interleaved ? append_kernel<D, true, false, kMode> : append_kernel<D, false, false, kMode>);
     // queries' rows on their way; keys that wait for their scale, in 32 bits, and what a thread block shares of its tokens
-    constexpr int kKept = 64 * kRopeThreads * S::kHeads + kSharedBytes;
+    constexpr int kKept = 64 * kRopeThreads * S::kHeads + sizeof(Shared);
     constexpr int kSmem = kWarps * kFlight * 1024 > kKept ? kWarps * kFlight * 1024 : kKept;
     static int attr[4][64] = {{0}};
     const cudaError_t e = pa_host::ensure_smem_attr(kernel, kSmem, attr[2 * (a.num_axes != 0) + (interleaved != 0)]);
@@ -440,9 +466,10 @@ cudaError_t launch_append(const AppendArgs& a, int interleaved, cudaStream_t st)
     return pa_host::launch_dependent(kernel, dim3((unsigned)(b.kv_blocks + q_blocks)), dim3(kRopeThreads), kSmem, st, b);
 }
 
-template <int D, int kBlock>
-cudaError_t launch_append(const AppendArgs& a, bool many, int interleaved, cudaStream_t st) {
-    return many ? launch_append<D, kBlock, true>(a, interleaved, st) : launch_append<D, kBlock, false>(a, interleaved, st);
+template <int D>
+cudaError_t launch_append(const AppendArgs& a, int mode, int interleaved, cudaStream_t st) {
+    return mode == kFew ? launch_append<D, kFew>(a, interleaved, st) : mode == kSome ? launch_append<D, kSome>(a, interleaved, st)
+                                                                     : launch_append<D, kMany>(a, interleaved, st);
 }
 
 int append(void* q_out, void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales, const void* q, const void* k,
@@ -503,16 +530,14 @@ int append(void* q_out, void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t
     a.block_size = block_size;
     a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     const bool many = n_q_heads >= 8 && (long long)num_tokens * (n_q_heads + 2 * n_kv_heads) * d_head >= 12000000;
-    const bool many_tokens = num_tokens >= 1024;
+    // 32 + 2 x 8 heads of 128, us of kFew / kSome / kMany: prompts of 300 tokens 10.6 / 11.5 / 13.7, 700 13.9 / 12.1 / 14.4, 2003
+    // 19.4 / 17.4 / 19.5, 4006 31.5 / 26.5 / 23.0, 8012 58.6 / 47.9 / 41.5; a token each of 256 requests 5.0 / 8.2 / 9.7, 1024
+    // 12.8 / 13.7 / 16.4, 4096 36.5 / 28.6 / 27.1
+    const int mode = num_tokens < 600 ? kFew : num_tokens < 3000 ? kSome : kMany;
     a.q_heads_per = many ? (n_q_heads + 1) / 2 : 1;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        d_head == 128 ? (block_size == 8    ? launch_append<128, 8>(a, many_tokens, interleaved, st)
-                         : block_size == 16 ? launch_append<128, 16>(a, many_tokens, interleaved, st)
-                                            : launch_append<128, 32>(a, many_tokens, interleaved, st))
-                      : (block_size == 8    ? launch_append<64, 8>(a, many_tokens, interleaved, st)
-                         : block_size == 16 ? launch_append<64, 16>(a, many_tokens, interleaved, st)
-                                            : launch_append<64, 32>(a, many_tokens, interleaved, st));
+        d_head == 128 ? launch_append<128>(a, mode, interleaved, st) : launch_append<64>(a, mode, interleaved, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

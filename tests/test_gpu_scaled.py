@@ -252,9 +252,10 @@ def test_norm_rope_append_equals_the_oracle(T, Hq, Hkv, D, B, sections, inter, n
     assert np.array_equal(rows(kc.cpu().numpy())[keep], rows(codes[0])[keep])   # the blocks' other codes, coded again or as they were
 
 
-def test_many_tokens_are_the_same_in_calls_of_few():
-    """Prompts past the size from which warps take a block's tokens at a time, against calls of a few hundred tokens."""
-    T, Hq, Hkv, D, B = 5003, 32, 4, 128, 16
+@pytest.mark.parametrize("T,Hkv,D,B", [(5003, 9, 128, 16), (5003, 4, 64, 32), (2003, 9, 128, 32), (900, 5, 64, 8)])
+def test_many_tokens_are_the_same_in_calls_of_few(T, Hkv, D, B):
+    """Calls of sizes that divide the work in other ways, over heads that fill no whole share, against calls of a few hundred tokens."""
+    Hq = 2 * Hkv
     q, k, v = _qkv(T, Hq, Hkv, D, 1)
     pos = torch.arange(T, dtype=torch.int32, device="cuda")
     NB = T // B + 9
