@@ -15,10 +15,13 @@
 
 namespace {
 
-// Whether a call goes in tiles of 128 rows (pa_attend_prompt.cu), with a scale above 0.
-bool is_prompt(long long rows) { return rows > 64; }
+// Which kernel takes a call.  Up to 16 rows a KV head: units of 16.  More:
+// with a scale above 0, units of 64 or 128 rows (wide), or, for long chunks and
+// prompts, the prefill kernel.  (Scales of 0 or below: units of 16 rows.)
+enum Route { kUnits16, kWide, kPrompt };
+Route route_of(long long rows, float scale) { return rows <= kRows || !(scale > 0.f) ? kUnits16 : rows <= 256 ? kWide : kPrompt; }
 
-size_t rows_workspace(int d_head) { return workspace_size(max_grid(false), kRows, d_head); }
+int unit_of(Route route, long long rows, bool f8) { return unit_rows(rows, f8, route == kWide); }
 
 int attend(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scales,
            const uint8_t* v_scales, const int32_t* block_tables, const int32_t* query_start,
@@ -51,7 +54,8 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
     const long long cap = (long long)max_blocks_per_seq * block_size;
     const int ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
-    if (is_prompt(all_rows) && scale > 0.f) {
+    Route route = route_of(all_rows, scale);
+    if (route == kPrompt) {
         const size_t n = pa_attend_calls::prompt_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads,
                                                            n_kv_heads, d_head, f8);
         if (n) {
@@ -62,19 +66,17 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
                                                    max_query_len, max_blocks_per_seq, num_blocks, ctx_cap, workspace,
                                                    status_dev, static_cast<cudaStream_t>(stream)});
         }
+        route = kWide;
     }
-    const bool wide = false;
-    const int unit = kRows;
-    const int most = max_grid(wide);
+    const bool wide = route == kWide;
+    const int unit = unit_of(route, all_rows, f8), most = max_grid(wide);
     if (most <= 0) return PA_ERR_CUDA;
-    if (workspace_bytes < rows_workspace(d_head)) return PA_ERR_WORKSPACE;
+    if (workspace_bytes < workspace_size(most, unit, d_head)) return PA_ERR_WORKSPACE;
 
     ShapedArgs a{};
     a.ctx_cap = ctx_cap;
-    const long long tiles = (all_rows + unit - 1) / unit;
-    if (tiles * num_seqs * n_kv_heads > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;
-    Split split = split_work(f8, wide, all_rows <= kRows ? all_rows : kRows, num_seqs, n_kv_heads * (int)tiles, ctx_cap);
-    if (split.direct) split.direct = (int)tiles;
+    if ((double)((all_rows + unit - 1) / unit) * num_seqs * n_kv_heads > 1 << 30) return PA_ERR_UNSUPPORTED;
+    const Split split = split_work(f8, wide, all_rows, num_seqs, n_kv_heads, ctx_cap);
     a.direct = split.direct;
     a.out = out;
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -87,7 +89,7 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
     const float factor = fabsf(scale) * kLog2e;
     a.scale_log2 = factor == 0.f ? 1.f : factor;
     a.q_sign = factor == 0.f ? 0.f : scale > 0.f ? 1.f : -1.f;
-    a.v_scale = f8 ? 1.f / kWeightScale : 1.f;
+    a.v_scale = f8 && !wide ? 1.f / kWeightScale : 1.f;         // (the wide kernel's sums carry its weights' factor)
     a.out_f32 = out_dtype == PA_DTYPE_F32;
     a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     a.n_q_heads = n_q_heads;
@@ -104,15 +106,19 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
     a.v_scales = v_scales;
     a.cap_log2 = softcap * kLog2e;
     a.cap_inv = softcap > 0.f ? 1.f / a.cap_log2 : 0.f;
-    const int box = block_size < kTile ? block_size : kTile;
+    const int box = wide || block_size < kTile ? block_size : kTile;
     CUtensorMap mk, mv;
     if (!pa_host::cache_view(&mk, k_cache, cache_rows, d_head, f8 ? 1 : 2, box) ||
         !pa_host::cache_view(&mv, v_cache, cache_rows, d_head, f8 ? 1 : 2, box))
         return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int rc = f8 ? launch_multi<128, true>(split.warps, mk, mv, a, split.grid, st)
-                 : d_head == 128 ? launch_multi<128, false>(split.warps, mk, mv, a, split.grid, st)
-                                 : launch_multi<64, false>(split.warps, mk, mv, a, split.grid, st);
+    int rc;
+    if (wide)
+        rc = launch_shaped_wide(unit, d_head, f8, q, block_size, mk, mv, a, split.grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    else
+        rc = f8 ? launch_multi<128, true>(split.warps, mk, mv, a, split.grid, st)
+             : d_head == 128 ? launch_multi<128, false>(split.warps, mk, mv, a, split.grid, st)
+                             : launch_multi<64, false>(split.warps, mk, mv, a, split.grid, st);
     if (rc != PA_OK || split.direct) return rc;
     return launch_merge(a, unit, d_head, split.units, split.grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -126,11 +132,20 @@ size_t pa_attend_workspace_size(int num_seqs, int max_query_len, int max_blocks_
     if (num_seqs <= 0 || max_query_len <= 0 || max_blocks_per_seq <= 0 || block_size <= 0 || n_kv_heads <= 0 ||
         n_q_heads < n_kv_heads || d_head <= 0)
         return 0;
-    const size_t rows = rows_workspace(d_head);
-    if (!is_prompt((long long)max_query_len * (n_q_heads / n_kv_heads))) return rows;
-    const size_t prompt = pa_attend_calls::prompt_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads,
-                                                            n_kv_heads, d_head, scaled != 0);
-    return prompt > rows ? prompt : rows;
+    // one size for whichever kernel a call of this shape takes
+    const long long rows = (long long)max_query_len * (n_q_heads / n_kv_heads);
+    size_t most = 0;
+    for (const Route route : {kUnits16, kWide}) {
+        if (route == kWide && rows <= kRows) break;
+        const size_t n = workspace_size(max_grid(route == kWide), unit_of(route, rows, scaled != 0), d_head);
+        most = n > most ? n : most;
+    }
+    if (route_of(rows, 1.f) == kPrompt) {
+        const size_t n = pa_attend_calls::prompt_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads,
+                                                           n_kv_heads, d_head, scaled != 0);
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 int pa_attend(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache,

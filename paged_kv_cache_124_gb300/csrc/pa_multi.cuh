@@ -10,6 +10,7 @@
 // blocks to spare, each block takes one unit instead and nothing is merged.
 #pragma once
 
+#include "pa_cap.cuh"
 #include "pa_mma.cuh"
 
 namespace pa_multi {
@@ -37,8 +38,8 @@ struct Unit {
 };
 
 // The like where each token sees an interval of positions: ctx is the end of
-// the positions that some token of the sequence sees, base (a multiple of 16)
-// their begin, where step 0 starts; all tokens see seen_lo .. seen_hi - 1.
+// the positions that some token of the sequence sees, base (a multiple of 16,
+// or of 32) their begin, where step 0 starts; all tokens see seen_lo .. seen_hi - 1.
 struct ShapedSeq : Seq {
     int base, first, seen_lo, seen_hi;
 };
@@ -88,17 +89,6 @@ struct ShapedArgs : MultiArgs {
 // 2^(e - 127) of a scale's byte.
 __device__ __forceinline__ float scale_of(uint32_t e) { return __int_as_float(e ? (int)(e << 23) : 0x00400000); }
 
-// cap tanh(x / cap) in units of log2: x and the result times log2(e).  Around
-// zero by tanh's series, up to x^9 (the next term is 5e-8 of it at 0.3), beyond
-// by 1 - 2 / (e^2x + 1), which would cancel there: relative errors below 1e-6.
-__device__ __forceinline__ float capped(float x, float cap_log2, float cap_inv) {
-    const float u = x * cap_inv, v = u * u;
-    const float p = fmaf(fmaf(fmaf(fmaf(v, 62.f / 2835.f, -17.f / 315.f), v, 2.f / 15.f), v, -1.f / 3.f), v, 1.f);
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(pa::exp2_approx(u * (2.f * kLog2e)) + 1.f));
-    return cap_log2 * (fabsf(u) < 0.3f ? u * p : fmaf(-2.f, r, 1.f));
-}
-
 // Four consecutive values of a row.
 __device__ __forceinline__ void put4(void* out, int f32, size_t i, float4 v) {
     if (f32)
@@ -145,7 +135,7 @@ __device__ __forceinline__ typename Args::Seq read_seq(const Args& a, int s, boo
             }
             if (lo >= hi) lo = hi = 0;                  // nothing is seen: a step of no positions, and zeros
         }
-        r.base = lo & ~15;
+        r.base = lo & ~(kRows == 16 ? 15 : 31);             // (a tile of the wide kernel begins with a block)
         r.ctx = hi;
         r.steps = max(1, (hi - r.base + kStep - 1) / kStep);
     } else {
@@ -511,7 +501,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
 cudaError_t launch_merge(const MultiArgs& a, int unit, int d_head, double units, int grid, cudaStream_t st);
 
 // Launches of the 64- and 128-row units on the 5th-generation tensor cores
-// (pa_decode_wide.cu); cudaSuccess or the launch's error.
+// (pa_decode_wide.cu, pa_attend_wide.cu); cudaSuccess or the launch's error.
+cudaError_t launch_shaped_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& map_k,
+                               const CUtensorMap& map_v, const ShapedArgs& a, int grid, cudaStream_t st);
 cudaError_t launch_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& map_k,
                         const CUtensorMap& map_v, const MultiArgs& a, int grid, cudaStream_t st);
 // (Unit cost of 2, 3, 4, 6 steps: 64 requests of 8 tokens, E4M3 68.6, 67.3, 67.6, 69.5 us; 48 trees of 16, bf16

@@ -157,7 +157,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = capped(s[n][e], a.cap_log2, a.cap_inv);
+                for (int e = 0; e < 4; ++e) s[n][e] = pa::capped(s[n][e], a.cap_log2, a.cap_inv);
         }
         if (a.slopes) {
 #pragma unroll

@@ -10,7 +10,7 @@
 #include <type_traits>
 #include <mutex>
 
-#include "pa_common.cuh"
+#include "pa_cap.cuh"
 
 namespace {
 
@@ -335,41 +335,6 @@ __device__ __forceinline__ void write_weights(float (&s)[kHalfCols], uint64_t c2
             w[qq] = kBf16 ? pack_bf16_rn(s[2 * q], s[2 * q + 1]) : pack_f16_rn(s[2 * q], s[2 * q + 1]);
         }
         tmem_st16u(t_p + h2 * (kHalfCols / 4), w);
-    }
-}
-
-// cap tanh(s c2 / cap) of n scores, times log2(e) (c2 and cap_log2 are; cap_inv
-// is 1 / cap_log2).  Where all of a warp's are within 0.3 of the cap, by the
-// series up to x^9 (the next term is 5e-8 of it) in packed pairs; else by
-// 1 - 2 / (e^2x + 1), which cancels around 0, beyond.
-template <int n>
-__device__ __forceinline__ void cap_scores(float (&s)[n], float c2, float cap_log2, float cap_inv) {
-    float top[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < n; ++i) top[i & 3] = fmaxf(top[i & 3], fabsf(s[i]));
-    const float by = c2 * cap_inv;
-    const bool far = !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(by) < 0.3f);
-    const auto both = [](float x) { return f32x2(x, x); };
-    const uint64_t by2 = both(by), cap2 = both(cap_log2);
-    if (!__any_sync(0xffffffffu, far)) {
-#pragma unroll
-        for (int i = 0; i < n; i += 2) {
-            const uint64_t u = mul_f32x2(f32x2(s[i], s[i + 1]), by2), v = mul_f32x2(u, u);
-            uint64_t p = fma_f32x2(v, both(62.f / 2835.f), both(-17.f / 315.f));
-            p = fma_f32x2(p, v, both(2.f / 15.f));
-            p = fma_f32x2(p, v, both(-1.f / 3.f));
-            p = fma_f32x2(p, v, both(1.f));
-            f32x2_split(mul_f32x2(mul_f32x2(u, cap2), p), s[i], s[i + 1]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-        const float u = s[i] * by, v = u * u;
-        const float p = fmaf(fmaf(fmaf(fmaf(v, 62.f / 2835.f, -17.f / 315.f), v, 2.f / 15.f), v, -1.f / 3.f), v, 1.f);
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(u * 2.8853900817779268f) + 1.f));
-        s[i] = cap_log2 * (fabsf(u) < 0.3f ? u * p : fmaf(-2.f, r, 1.f));
     }
 }
 
@@ -960,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float c2 = c2x[x];
                         if constexpr (kShaped) {
                             if (a.cap_inv != 0.f) {
-                                cap_scores<kHalfCols>(s, c2, a.cap_log2, a.cap_inv);
+                                pa::cap_scores<kHalfCols>(s, c2, a.cap_log2, a.cap_inv);
                                 c2 = 1.f;
                             }
                             if (a.slopes) {

@@ -288,7 +288,10 @@ def test_bad_inputs_are_flagged(scaled, news):
     p.most = most
     left = torch.isnan(out).all(-1).all(-1)
     assert st.item() == api.PA_DEV_BAD_CONTEXT
-    assert left.tolist() == [n == most for n in news for _ in range(n)] and torch.equal(out[~left], want[~left])
+    assert left.tolist() == [n == most for n in news for _ in range(n)]
+    # (another kernel may take the smaller call: each within 2 (2^-11 + 2^-11) of sums of a |v|, by the roundings of weights and q)
+    top = float(np.nanmax(np.abs(Q.dequantize_scaled(p.vc, p.vs) if scaled else A.bf16_to_f64(p.vc))))
+    assert (out[~left] - want[~left]).abs().max() <= 2 * 4 * 2.0 ** -11 * top
     p.tables[0, 1] = 1 << 20                                       # outside the pool: flagged, the others as they were
     st.zero_()
     out = p.run(status=st)
