@@ -39,7 +39,8 @@ struct Unit {
 
 // The like where each token sees an interval of positions: ctx is the end of
 // the positions that some token of the sequence sees, base (a multiple of 16,
-// or of 32) their begin, where step 0 starts; all tokens see seen_lo .. seen_hi - 1.
+// or of 32) their begin, where step 0 starts; all tokens that see any see
+// seen_lo .. seen_hi - 1.
 struct ShapedSeq : Seq {
     int base, first, seen_lo, seen_hi;
 };
@@ -86,8 +87,8 @@ struct ShapedArgs : MultiArgs {
     float cap_log2, cap_inv;               // cap * log2(e) and 1 over it; 0: none
 };
 
-// 2^(e - 127) of a scale's byte.
-__device__ __forceinline__ float scale_of(uint32_t e) { return __int_as_float(e ? (int)(e << 23) : 0x00400000); }
+// 2^(e - 127) of a scale's byte (of byte 0, 0: what 2^-127 scales is nothing beside any sum).
+__device__ __forceinline__ float scale_of(uint32_t e) { return __int_as_float((int)(e << 23)); }
 
 // Four consecutive values of a row.
 __device__ __forceinline__ void put4(void* out, int f32, size_t i, float4 v) {
@@ -126,12 +127,12 @@ __device__ __forceinline__ typename Args::Seq read_seq(const Args& a, int s, boo
             for (int i = 0; i < r.n; ++i) {
                 const int2 v = a.visible[r.q0 + i];
                 const int x = max(v.x, 0), y = min(v.y, ctx);
-                if (x < y) {
+                if (x < y) {                            // (what a row that sees nothing comes to is not looked at)
                     lo = min(lo, x);
                     hi = max(hi, y);
+                    r.seen_lo = max(r.seen_lo, x);
+                    r.seen_hi = min(r.seen_hi, y);
                 }
-                r.seen_lo = max(r.seen_lo, x);
-                r.seen_hi = min(r.seen_hi, y);
             }
             if (lo >= hi) lo = hi = 0;                  // nothing is seen: a step of no positions, and zeros
         }
@@ -335,8 +336,9 @@ __device__ __forceinline__ bool sees(const uint64_t* words, int i, int j) {
 
 // A value that is not finite reaches the rows that see it only.  In a product
 // it would reach all (0 * inf = NaN), so at the new positions, which are all
-// that a row may not see, the products run with zeros in its place, and the
-// rows of such a unit add what they see of it when they are written.
+// that a row may not see (shaped: those that some row does not see), the
+// products run with zeros in its place, and the rows of such a unit add what
+// they see of it when they are written.
 
 // The elements of w (two bf16, or four E4M3 codes) that are not finite, as a mask.
 template <bool F8>
@@ -367,11 +369,23 @@ __device__ __forceinline__ bool drop_unfinite(uint8_t* tile, int slab_bytes, int
     return any != 0;
 }
 
+// The like outside positions seen_lo .. seen_hi - 1 of a tile that begins at
+// t0, of its first `rows` rows.
+template <bool F8, int kSlabs>
+__device__ __forceinline__ bool drop_unfinite_outside(uint8_t* tile, int slab_bytes, int t0, int seen_lo, int seen_hi, int rows,
+                                                      int thread, int threads) {
+    const int lo = min(max(seen_lo - t0, 0), rows), hi = max(min(seen_hi - t0, rows), lo);
+    bool any = false;
+    if (lo > 0) any |= drop_unfinite<F8, kSlabs>(tile, slab_bytes, 0, lo, thread, threads);
+    if (hi < rows) any |= drop_unfinite<F8, kSlabs>(tile, slab_bytes, hi, rows, thread, threads);
+    return any;
+}
+
 // Add the values that are not finite, at d .. d + 3 of the positions of
 // [lo, hi) that a row of sequence s sees, to the row's result: its sums at
 // `part`, or `out` where that is null.
-// Shaped: the tiles of kTile positions that every row sees keep theirs.
-template <int D, bool F8, int kTile, class Args>
+// (Shaped: positions that every row sees, within seen_lo .. seen_hi, keep theirs.)
+template <int D, bool F8, class Args>
 __device__ __noinline__ void add_unfinite(const Args& a, int s, int kvh, int row, int lo, int hi, int d, float* part) {
     const auto q = read_seq<1, 1>(a, s, false);
     const int i = row >> a.log2_group, B = 1 << a.log2_block;
@@ -395,9 +409,8 @@ __device__ __noinline__ void add_unfinite(const Args& a, int s, int kvh, int row
 #pragma unroll 1
     for (int pos = max(lo, first); pos < end; ++pos) {
         if constexpr (Args::kShaped) {
-            const int t0 = lo + (pos - lo) / kTile * kTile;
-            if (t0 >= q.seen_lo && t0 + kTile <= q.seen_hi) {
-                pos = t0 + kTile - 1;
+            if (pos >= q.seen_lo && pos < q.seen_hi) {
+                pos = q.seen_hi - 1;
                 continue;
             }
         } else if (!sees(words, i, pos - first)) {
@@ -490,9 +503,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MultiArgs a,
             __syncthreads();
         }
         if (mine == 0 && there) {
-            const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+            const float f = a.v_scale / Z;
             put4(a.out, a.out_f32, ((size_t)(p.x + i) * a.n_q_heads + p.z * G + (r & (G - 1))) * D + d,
-                 make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
+                 Z == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
         }
     }
 }

@@ -90,7 +90,7 @@ __device__ __forceinline__ bool visible(const MultiArgs& a, const Unit& u, int r
 template <int D>
 struct State {
     float m[2], l[2];
-    float top, inv;                        // block-scaled values: the largest scale so far, which acc is in units of, and 1 over it
+    float top, inv;                        // block-scaled values: the largest scale so far, which acc is in units of, and kWeightScale over it
     float acc[D / 8][4];
     __device__ __forceinline__ void reset() {
         top = inv = 0.f;
@@ -108,7 +108,7 @@ struct State {
 template <int D, bool F8, class Args, class Rows>
 __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const Args& a,
                                           const typename Args::Unit& u, int lane, const uint32_t (&qr)[D / 16][4],
-                                          const Rows& shape, uint32_t scales) {
+                                          const Rows& shape, uint32_t scales, bool some) {
     constexpr bool kShaped = Args::kShaped;
     constexpr int kSlabBytes = kTile * 128, kSteps = D / 16;
     const int g = lane >> 2, t4 = lane & 3;
@@ -142,31 +142,25 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
             score(kk, r[0], r[1], r[2], r[3]);
         }
     }
-    float by[2] = {1.f, 1.f};                          // block-scaled values: factors of the weights
+    float by[2] = {1.f, 1.f};                          // block-scaled values: factors of the weights, of 8 positions each
+    float f[2][2];                                     // factors of the scores: of positions 8 n on, and row g + 8 h
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) f[n][h] = kShaped && F8 ? fmaxf(c[h] * scale_of(scales >> (16 * n) & 0xff), 1e-37f) : c[h];   // never 0: masked scores stay -inf
     if constexpr (kShaped) {
-        // scores in units of log2, capped and biased: their factor is 1 from here on
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const float k_scale = F8 ? scale_of(scales >> (16 * n) & 0xff) : 1.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) s[n][2 * h + e] *= c[h] * k_scale;
-        }
-        if (a.cap_inv != 0.f) {
+        if (a.cap_inv != 0.f || a.slopes) {            // scores in units of log2 from here on
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = pa::capped(s[n][e], a.cap_log2, a.cap_inv);
+                for (int e = 0; e < 4; ++e) {
+                    s[n][e] *= f[n][e >> 1];
+                    if (a.cap_inv != 0.f) s[n][e] = pa::capped(s[n][e], a.cap_log2, a.cap_inv);
+                    if (a.slopes) s[n][e] -= shape.slope[e >> 1] * (float)abs(shape.pos[e >> 1] - (t0 + 8 * n + 2 * t4 + (e & 1)));
+                }
+            f[0][0] = f[0][1] = f[1][0] = f[1][1] = 1.f;
         }
-        if (a.slopes) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[n][e] -= shape.slope[e >> 1] * (float)abs(shape.pos[e >> 1] - (t0 + 8 * n + 2 * t4 + (e & 1)));
-        }
-        if (!u.all_see(t0, t0 + kTile)) {
+        if (some) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -176,18 +170,20 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
                 }
         }
         if constexpr (F8) {
-            const float v0 = scale_of(scales >> 8 & 0xff), v1 = scale_of(scales >> 24), top = fmaxf(st.top, fmaxf(v0, v1));
+            by[0] = scale_of(scales >> 8 & 0xff);
+            by[1] = scale_of(scales >> 24);
+            const float top = fmaxf(by[0], by[1]);
             if (top > st.top) {                        // (the whole warp)
-                const float f = st.top / top;          // (powers of two: exact)
+                const float less = st.top / top;       // (powers of two: exact)
                 st.top = top;
-                st.inv = 1.f / top;
+                st.inv = kWeightScale / top;
 #pragma unroll
                 for (int d = 0; d < D / 8; ++d)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st.acc[d][e] *= f;
+                    for (int e = 0; e < 4; ++e) st.acc[d][e] *= less;
             }
-            by[0] = v0 * st.inv;
-            by[1] = v1 * st.inv;
+            by[0] *= st.inv;
+            by[1] *= st.inv;
         }
     } else if (t0 + kTile > u.first) {                 // some row may not see some position
 #pragma unroll
@@ -196,28 +192,33 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
             for (int e = 0; e < 4; ++e)
                 if (!visible(a, u, g + 8 * (e >> 1), t0 + 8 * n + 2 * t4 + (e & 1))) s[n][e] = -INFINITY;
     }
-    const float cs[2] = {kShaped ? 1.f : c[0], kShaped ? 1.f : c[1]};
     // how far the tile's scores rise above the running maxima
     float over = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-        over = fmaxf(over, fmaf(top, cs[h], -st.m[h]));
+        if constexpr (kShaped && F8) {
+            over = fmaxf(over, fmaxf(fmaf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), f[0][h], -st.m[h]),
+                                     fmaf(fmaxf(s[1][2 * h], s[1][2 * h + 1]), f[1][h], -st.m[h])));
+        } else {
+            const float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            over = fmaxf(over, fmaf(top, f[0][h], -st.m[h]));
+        }
     }
     if (__any_sync(0xffffffffu, over > kRaise)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            float top = kShaped && F8 ? fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]) * f[0][h], fmaxf(s[1][2 * h], s[1][2 * h + 1]) * f[1][h])
+                                      : fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float m = fmaxf(st.m[h], top * cs[h]);
-            const float f = pa::exp2_approx(st.m[h] - m);
+            const float m = fmaxf(st.m[h], kShaped && F8 ? top : top * f[0][h]);
+            const float less = pa::exp2_approx(st.m[h] - m);
             st.m[h] = m;
-            st.l[h] *= f;
+            st.l[h] *= less;
 #pragma unroll
             for (int d = 0; d < D / 8; ++d) {
-                st.acc[d][2 * h] *= f;
-                st.acc[d][2 * h + 1] *= f;
+                st.acc[d][2 * h] *= less;
+                st.acc[d][2 * h + 1] *= less;
             }
         }
     }
@@ -227,17 +228,16 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            const float p0 = pa::exp2_approx(fmaf(s[n][2 * h], cs[h], -st.m[h]));
-            const float p1 = pa::exp2_approx(fmaf(s[n][2 * h + 1], cs[h], -st.m[h]));
+            const float p0 = pa::exp2_approx(fmaf(s[n][2 * h], f[n][h], -st.m[h]));
+            const float p1 = pa::exp2_approx(fmaf(s[n][2 * h + 1], f[n][h], -st.m[h]));
             st.l[h] += p0 + p1;
             if constexpr (F8) {
-                ph[2 * n + h] = kShaped ? pa::pack_f16x2(p0 * (kWeightScale * by[n]), p1 * (kWeightScale * by[n]))
-                                         : pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale);
+                ph[2 * n + h] = kShaped ? pa::pack_f16x2(p0 * by[n], p1 * by[n]) : pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale);
             } else {
                 const uint32_t w = pa::pack_bf16x2(p0, p1);
-                const float2 f = pa::bf16x2_to_float2(w);
+                const float2 hi = pa::bf16x2_to_float2(w);
                 ph[2 * n + h] = w;
-                pl[2 * n + h] = pa::pack_bf16x2(p0 - f.x, p1 - f.y);
+                pl[2 * n + h] = pa::pack_bf16x2(p0 - hi.x, p1 - hi.y);
             }
         }
     // O += P . V; V rows past the context are zeroed (0 * NaN)
@@ -486,6 +486,11 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
         for (int h = 0; h < 2; ++h) c[h] = F8 ? q_scale[(lane >> 2) + 8 * h] : a.scale_log2;
 
         const Rows shape(a, u, lane >> 2);
+        int seen_lo = 0, seen_hi = 0;
+        if constexpr (kShaped) {
+            seen_lo = u.seen_lo;
+            seen_hi = u.seen_hi;
+        }
         State<D> st;
         st.reset();
         bool landed = true;
@@ -510,17 +515,15 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
             }
             if (t0 < ctx) {
                 const uint32_t ks = stage_at(stage);
-                bool some;                                        // some row may not see some position
-                if constexpr (kShaped) some = !u.all_see(t0, t0 + kTile);
-                else some = t0 + kTile > u.first;
-                if (some) {
-                    const int from = kShaped ? 0 : max(0, u.first - t0);
+                const bool some = kShaped ? t0 < seen_lo || t0 + kTile > seen_hi : t0 + kTile > u.first;
+                if (some) {                                       // some row may not see some position
                     uint8_t* v = ring + stage * (kWarps * G::kStageBytes) + warp * G::kStageBytes + G::kTileBytes;
-                    if (drop_unfinite<F8, G::kSlabs>(v, G::kSlabBytes, from, min(kTile, ctx - t0), lane, 32))
+                    if (kShaped ? drop_unfinite_outside<F8, G::kSlabs>(v, G::kSlabBytes, t0, seen_lo, seen_hi, min(kTile, ctx - t0), lane, 32)
+                                : drop_unfinite<F8, G::kSlabs>(v, G::kSlabBytes, max(0, u.first - t0), min(kTile, ctx - t0), lane, 32))
                         unfinite[nth & 1] = 1;
                     __syncwarp();
                 }
-                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, a, u, lane, qr, shape, tile_scales);
+                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, a, u, lane, qr, shape, tile_scales, some);
             }
             __syncwarp();
             if (k + kStages < len) issue(u, k + kStages);
@@ -598,10 +601,10 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
                 U.w += f * v.w;
             }
             if (whole) {
-                const float f = Z == 0.f ? 0.f : a.v_scale / Z;
+                const float f = a.v_scale / Z;
                 put4(a.out, a.out_f32,
                      ((size_t)(u.q0 + i) * a.n_q_heads + (u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))) * D + d,
-                     make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
+                     Z == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(U.x * f, U.y * f, U.z * f, U.w * f));
             } else {
                 const size_t at = (size_t)slot * kRows + r;
                 *reinterpret_cast<float4*>(a.part_u + at * D + d) = U;
@@ -615,7 +618,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
 #pragma unroll 1
             for (int x = threadIdx.x; x < kRows * (D / 4); x += kThreads) {   // (to what the thread itself has written)
                 const int r = x / (D / 4), d = x % (D / 4) * 4;
-                add_unfinite<D, F8, kTile>(a, u.seq, u.kvh, u.row0 + r, base_of(u) + u.st0 * kStep, base_of(u) + (u.st0 + len) * kStep, d,
+                add_unfinite<D, F8>(a, u.seq, u.kvh, u.row0 + r, base_of(u) + u.st0 * kStep, base_of(u) + (u.st0 + len) * kStep, d,
                                     whole ? nullptr : a.part_u + ((size_t)slot * kRows + r) * D + d);
             }
         if (!whole && u.st0 == 0 && threadIdx.x == 0)             // this block begins the unit

@@ -584,7 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t0 = base + (st0 + j) * kKv, left = ctx - t0;
                 uint8_t* tile = sm + G::kV0 + st * G::kTileBytes;
                 if (kShaped ? t0 < seen_lo || t0 + kKv > seen_hi : t0 + kKv > first) {
-                    unfinite |= drop_unfinite<F8, G::kHalves>(tile, G::kHalfBytes, kShaped ? 0 : max(0, first - t0), min(kKv, left), lane, 32);
+                    unfinite |= kShaped ? drop_unfinite_outside<F8, G::kHalves>(tile, G::kHalfBytes, t0, seen_lo, seen_hi, min(kKv, left), lane, 32)
+                                        : drop_unfinite<F8, G::kHalves>(tile, G::kHalfBytes, max(0, first - t0), min(kKv, left), lane, 32);
                     if (left < kKv && left % G::kStepKeys) {
 #pragma unroll 1
                         for (int x = lane; x < (G::kStepKeys - left % G::kStepKeys) * G::kHalves * 8; x += 32) {
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // Block-scaled: the scales of the group's 64 positions of a tile, lane i's of block i (K's byte, and V's above it),
             // asked for a tile ahead and their table entries two.
-            float v_top = 0.f, v_inv = 0.f;                      // the largest of V so far, which O is in units of; and 1 over it
+            float v_top = 0.f;                                   // the largest of V so far, 2^(this - 127), which O is in units of
             int entry = -1;
             uint32_t scales = 0, scales_next = 0;
             auto entry_of = [&](int j) {
@@ -727,37 +728,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 wait_ld<kCols>(s);
                 const int t0 = start + j * kKv;
-                float cs = c;                                    // the scores' factor
-                float by[4] = {1.f, 1.f, 1.f, 1.f};              // block-scaled values: the weights' factors, of 8 positions each
-                bool grows = false;                              // and whether V's scale does
+                float cs[4] = {c, c, c, c};                      // the scores' factors, of 8 positions each (all the same but where block-scaled)
+                float by[4] = {0.f, 0.f, 0.f, 0.f};              // block-scaled values: log2 of the weights' factors
+                bool grows = false;                              // and whether V's largest scale does
                 float v_new = v_top;
                 if constexpr (kShaped) {
                     if constexpr (kScaled) {
-                        float most = 0.f;
+                        int most = 0;
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint32_t e = __shfl_sync(0xffffffffu, scales, (32 * half + 8 * x) >> a.log2_block);
-                            const float f = c * scale_of(e & 0xff);
-                            by[x] = scale_of(e >> 8);
-                            most = fmaxf(most, by[x]);
-#pragma unroll
-                            for (int k = 8 * x; k < 8 * x + 8; k += 2) split(mul2(pair(s[k], s[k + 1]), pair(f, f)), s[k], s[k + 1]);
+                            const int e = __shfl_sync(0xffffffffu, scales, (32 * half + 8 * x) >> a.log2_block);
+                            cs[x] = fmaxf(c * scale_of(e & 0xff), 1e-37f);   // never 0: masked scores stay -inf
+                            by[x] = (float)(e >> 8);
+                            most = max(most, e >> 8);
                         }
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
-                        grows = most > v_top;
-                        v_new = fmaxf(most, v_top);
+                        most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+                        v_new = fmaxf((float)most, v_top);
+                        grows = v_new > v_top;
                         scales = scales_next;
-                        cs = 1.f;
                     }
-                    if (a.cap_inv != 0.f) {
-                        pa::cap_scores<kCols>(s, cs, a.cap_log2, a.cap_inv);
-                        cs = 1.f;
-                    }
-                    if (a.slopes) {
-                        const float d0 = (float)(pos - t0);
+                    if (a.cap_inv != 0.f || a.slopes) {          // scores in units of log2 from here on
+                        if constexpr (kScaled) {
 #pragma unroll
-                        for (int k = 0; k < kCols; ++k) s[k] = fmaf(-slope, fabsf(d0 - (float)k), s[k] * cs);
-                        cs = 1.f;
+                            for (int k = 0; k < kCols; k += 2) split(mul2(pair(s[k], s[k + 1]), pair(cs[k >> 3], cs[k >> 3])), s[k], s[k + 1]);
+                        }
+                        float all = kScaled ? 1.f : c;
+                        if (a.cap_inv != 0.f) {
+                            pa::cap_scores<kCols>(s, all, a.cap_log2, a.cap_inv);
+                            all = 1.f;
+                        }
+                        if (a.slopes) {
+                            const float d0 = (float)(pos - t0);
+#pragma unroll
+                            for (int k = 0; k < kCols; ++k) s[k] = fmaf(-slope, fabsf(d0 - (float)k), s[k] * all);
+                        }
+                        cs[0] = cs[1] = cs[2] = cs[3] = 1.f;
                     }
                 }
                 if (kShaped ? t0 < seen_lo || t0 + kCols > seen_hi : t0 + kCols > first) {   // some row may not see some position
@@ -769,7 +774,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 float top;
-                {
+                if constexpr (kScaled) {
+                    float p[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float* v = s + 8 * x;
+                        p[x] = cs[x] * fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+                    }
+                    top = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                } else {
                     float p[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -779,8 +793,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
                     if (kHalf) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 }
-                const bool raise = fmaf(top, cs, -m) > kSlack;
-                const float m_new = raise ? fmaf(top, cs, kHeadroom) : m;
+                const float c1 = kScaled ? 1.f : cs[0];          // (scaled: the maximum has its factors)
+                const bool raise = fmaf(top, c1, -m) > kSlack;
+                const float m_new = raise ? fmaf(top, c1, kHeadroom) : m;
                 if (j > 0 && __any_sync(0xffffffffu, raise || (kScaled && grows))) {
                     // This group's O holds its halves of the tiles before, once their products are done.  The wait
                     // is for tile at - 1's phase of its buffer's barrier, whatever was skipped: the phase before it,
@@ -791,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_after();
                     float f = pa::exp2_approx(m - m_new);
                     l *= f;
-                    if (kScaled && grows) f *= v_top / v_new;    // (powers of two: exact)
+                    if (kScaled && grows) f *= pa::exp2_approx(v_top - v_new);
 #pragma unroll 1
                     for (int x = 0; x < D; x += 16) {
                         uint32_t o[16];
@@ -804,16 +819,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 m = m_new;
                 if constexpr (kScaled) {
-                    if (grows) {
-                        v_top = v_new;
-                        v_inv = 1.f / v_new;
-                    }
+                    v_top = v_new;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) by[x] *= v_inv;
+                    for (int x = 0; x < 4; ++x) by[x] = fmaxf(by[x] - v_top, -60.f);   // (weights of less are nothing)
                 }
-                const uint64_t cc = pair(cs, cs), neg = pair(kUp - m, kUp - m);
                 uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
                 // two columns' weights, summed
+                const uint64_t cc = pair(cs[0], cs[0]), neg = pair(kUp - m, kUp - m);
                 auto weights = [&](float x0, float x1, int k) {
                     float y0, y1;
                     split(fma2(pair(x0, x1), cc, neg), y0, y1);
@@ -821,23 +833,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum[k & 1] = add2(sum[k & 1], p);
                     return p;
                 };
+                // the like of block x, times 2^by[x]
+                auto scaled_weights = [&](float x0, float x1, int x) {
+                    const float n = kUp - m + by[x];
+                    float y0, y1;
+                    split(fma2(pair(x0, x1), pair(cs[x], cs[x]), pair(n, n)), y0, y1);
+                    return pair(pa::exp2_approx(y0), pa::exp2_approx(y1));
+                };
                 if constexpr (F8) {
                     // Weights as f16 (a relative 2^-11), exactly the sum of four E5M2 terms: an f16's upper byte is
                     // its E5M2 value cut off, and so is what that leaves, down to 2^-16 (2^-28 of the row's
                     // largest).  (E4M3 ends at 2^-9, which would lose weights below 2^-14, and a long tail of such
                     // can be most of a row's sum.)  Two and two terms in a product's two lanes of a row.
                     uint32_t t[4][8];
+                    uint64_t block = 0;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         uint32_t h[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float p0, p1;
-                            uint64_t p = weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], e);
-                            if constexpr (kScaled) p = mul2(p, pair(by[k >> 1], by[k >> 1]));
+                            uint64_t p;
+                            if constexpr (kScaled) {
+                                p = scaled_weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], k >> 1);
+                                block = (k & 1) + e == 0 ? p : add2(block, p);
+                            } else {
+                                p = weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], e);
+                            }
                             split(p, p0, p1);
                             h[e] = pa::pack_f16x2(p0, p1);
                         }
+                        if constexpr (kScaled)
+                            if (k & 1) {                         // a block's sum, without its factor
+                                const float back = pa::exp2_approx(-by[k >> 1]);
+                                sum[0] = fma2(block, pair(back, back), sum[0]);
+                            }
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             t[x][k] = __byte_perm(h[0], h[1], 0x7531);
@@ -887,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nth >= 1 && !wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status)) break;
             if (kHalf) l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (!half) stats[w * kRows + r] = make_float2(m, l);
-            if (kScaled && quarter == 0 && lane == 0) ctl->tops[w] = v_top;
+            if (kScaled && quarter == 0 && lane == 0) ctl->tops[w] = __int_as_float((int)v_top << 23);
             pa::mbar_arrive(&ctl->stats_full);
         }
     } else {
@@ -973,7 +1003,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int st0 = u->st0;
             const int seq = u->seq, kvh = u->kvh, end = st0 + u->len, base = base_of(*u);
-            const bool some = !kShaped || u->ctx > base;         // (a unit whose rows see nothing has no products)
             const int row = u->row0 + r, i = row >> a.log2_group;
             const bool real = i < u->n, whole = u->whole;
             const bool both = u->len > 1 || u->ctx - base - st0 * kKv > kHalfKv;   // group 1 had positions: O1 was written
@@ -992,6 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float M = fmaxf(e.x, o.x), Z0 = pa::exp2_approx(e.x - M), Z1 = pa::exp2_approx(o.x - M);
             const float Z = Z0 * e.y + Z1 * o.y;
             const float by = whole ? (Z == 0.f ? 0.f : a.v_scale / Z) : 1.f;
+            const bool none = kShaped && Z == 0.f;               // a row that sees nothing (and perhaps had no products)
             const float fe = Z0 * by * top0, fo = Z1 * by * top1;
             const size_t at = (size_t)(2 * blockIdx.x + (st0 == 0 ? 1 : 0)) * kRows + r;
             if (!wait_for(&ctl->o_done, nth & 1, ctl, a.status)) break;
@@ -1008,7 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa::mbar_arrive(&ctl->o_free);
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = (some ? fe * v[k] : 0.f) + (both ? fo * v1[k] : 0.f);
+                for (int k = 0; k < 32; ++k) v[k] = none ? 0.f : fe * v[k] + (both ? fo * v1[k] : 0.f);
                 float f[kHalf ? 16 : 32];                         // of a row's two lanes, each writes half
                 if constexpr (kHalf) {
 #pragma unroll
@@ -1041,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int d = 0; d < D; d += 4)                   // (to what the thread itself has written)
                     if (!kHalf || (d & 16) == (lane & 16))
-                        add_unfinite<D, F8, kKv>(a, seq, kvh, row, base + st0 * kKv, base + end * kKv, d, whole ? nullptr : a.part_u + at * D + d);
+                        add_unfinite<D, F8>(a, seq, kvh, row, base + st0 * kKv, base + end * kKv, d, whole ? nullptr : a.part_u + at * D + d);
         }
     }
     fence_before();
