@@ -54,30 +54,27 @@ struct Geo {
     static_assert(kJoinStages * kStageBytes == 4 * kRows * D, "a unit's states fill the join stages");
 };
 
-// Shaped units: what a thread's two rows (g and g + 8) see, and their bias.
+// Shaped units: what a row sees, its position, and its bias' slope times
+// log2(e).  In shared memory: few tiles need it, and registers are short.
 struct Shape {
-    int lo[2], hi[2], pos[2];
-    float slope[2];                        // times log2(e)
-    __device__ __forceinline__ Shape(const ShapedArgs& a, const ShapedUnit& u, int g) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = u.row0 + g + 8 * h, i = row >> a.log2_group;
-            const bool real = i < u.n;
-            pos[h] = u.first + i;
-            lo[h] = 0;
-            hi[h] = real ? min(pos[h] + 1, u.ctx) : u.ctx;       // a row that is not there: any finite result will do
-            if (a.visible && real) {
-                const int2 v = a.visible[u.q0 + i];
-                lo[h] = v.x;
-                hi[h] = min(v.y, u.ctx);
-            }
-            slope[h] = a.slopes ? kLog2e * a.slopes[(u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))] : 0.f;
-        }
+    int lo, hi, pos;
+    float slope;
+};
+__device__ __forceinline__ Shape shape_of(const ShapedArgs& a, const ShapedUnit& u, int r) {
+    Shape s;
+    const int row = u.row0 + r, i = row >> a.log2_group;
+    const bool real = i < u.n;
+    s.pos = u.first + i;
+    s.lo = 0;
+    s.hi = real ? min(s.pos + 1, u.ctx) : u.ctx;                 // a row that is not there: any finite result will do
+    if (a.visible && real) {
+        const int2 v = a.visible[u.q0 + i];
+        s.lo = v.x;
+        s.hi = min(v.y, u.ctx);
     }
-};
-struct NoShape {
-    __device__ __forceinline__ NoShape(const MultiArgs&, const Unit&, int) {}
-};
+    s.slope = a.slopes ? kLog2e * a.slopes[(u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))] : 0.f;
+    return s;
+}
 
 __device__ __forceinline__ bool visible(const MultiArgs& a, const Unit& u, int row, int pos) {
     if (pos >= u.ctx) return false;
@@ -105,10 +102,10 @@ struct State {
 // into the warp's state.  qr: the rows of q as A operands; c[h]: score factor
 // of rows g + 8 h.  scales (shaped, E4M3): the scale bytes of K and V of the
 // tile's first 8 positions, then of the others.
-template <int D, bool F8, class Args, class Rows>
+template <int D, bool F8, class Args>
 __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const Args& a,
                                           const typename Args::Unit& u, int lane, const uint32_t (&qr)[D / 16][4],
-                                          const Rows& shape, uint32_t scales, bool some) {
+                                          const Shape* shape, uint32_t scales, bool some) {
     constexpr bool kShaped = Args::kShaped;
     constexpr int kSlabBytes = kTile * 128, kSteps = D / 16;
     const int g = lane >> 2, t4 = lane & 3;
@@ -150,23 +147,26 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
         for (int h = 0; h < 2; ++h) f[n][h] = kShaped && F8 ? fmaxf(c[h] * scale_of(scales >> (16 * n) & 0xff), 1e-37f) : c[h];   // never 0: masked scores stay -inf
     if constexpr (kShaped) {
         if (a.cap_inv != 0.f || a.slopes) {            // scores in units of log2 from here on
+            const float slope[2] = {shape[g].slope, shape[g + 8].slope};
+            const int at[2] = {shape[g].pos, shape[g + 8].pos};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[n][e] *= f[n][e >> 1];
                     if (a.cap_inv != 0.f) s[n][e] = pa::capped(s[n][e], a.cap_log2, a.cap_inv);
-                    if (a.slopes) s[n][e] -= shape.slope[e >> 1] * (float)abs(shape.pos[e >> 1] - (t0 + 8 * n + 2 * t4 + (e & 1)));
+                    if (a.slopes) s[n][e] -= slope[e >> 1] * (float)abs(at[e >> 1] - (t0 + 8 * n + 2 * t4 + (e & 1)));
                 }
             f[0][0] = f[0][1] = f[1][0] = f[1][1] = 1.f;
         }
         if (some) {
+            const int lo[2] = {shape[g].lo, shape[g + 8].lo}, hi[2] = {shape[g].hi, shape[g + 8].hi};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int pos = t0 + 8 * n + 2 * t4 + (e & 1);
-                    if (pos < shape.lo[e >> 1] || pos >= shape.hi[e >> 1]) s[n][e] = -INFINITY;
+                    if (pos < lo[e >> 1] || pos >= hi[e >> 1]) s[n][e] = -INFINITY;
                 }
         }
         if constexpr (F8) {
@@ -292,7 +292,6 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
     using G = Geo<D, F8, kWarps>;
     using Unit = typename Args::Unit;
     constexpr bool kShaped = Args::kShaped, kScaled = kShaped && F8;
-    using Rows = std::conditional_t<kShaped, Shape, NoShape>;
     constexpr int kStages = G::kStages, kThreads = G::kThreads;
     constexpr int kStep = step_of(kWarps), kUnitCost = cost_of(kWarps, F8), kMinSteps = least_of(kWarps), kDirectSteps = direct_of(kWarps);
     extern __shared__ uint8_t smem_raw[];
@@ -307,6 +306,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
     // two barriers after its join.
     __shared__ WalkOf<typename Args::Seq> walk;
     __shared__ Unit units[4];
+    __shared__ Shape shape[kShaped ? kRows : 1];                  // of the unit's rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = 1 << a.log2_block, heads = a.n_kv_heads;
@@ -464,6 +464,8 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
         const Unit& u = units[nth & 3];
         const Unit& next = units[(nth + 1) & 3];
         store_q(qv);
+        if constexpr (kShaped)
+            if (threadIdx.x < kRows) shape[threadIdx.x] = shape_of(a, u, threadIdx.x);
         __syncthreads();
         const int len = u.len, ctx = u.ctx, base = base_of(u) + u.st0 * kStep + warp * kTile;
         const bool more = next.valid;
@@ -485,7 +487,6 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
 #pragma unroll
         for (int h = 0; h < 2; ++h) c[h] = F8 ? q_scale[(lane >> 2) + 8 * h] : a.scale_log2;
 
-        const Rows shape(a, u, lane >> 2);
         int seen_lo = 0, seen_hi = 0;
         if constexpr (kShaped) {
             seen_lo = u.seen_lo;
