@@ -507,7 +507,8 @@ size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads,
  * document it belongs to (begin, p + 1), a prefix or an image whose positions
  * see one another (.., end); it is clipped to [0, C).  A token whose interval
  * is empty gets zeros.  Positions outside it do not reach the token's row,
- * whatever they hold.  Sums and statistics are fp32, outputs rounded once.
+ * whatever they hold.  Sums and statistics are fp32 (a capped score is within
+ * 2^-20 of itself and 2^-21 of the cap), outputs rounded once.
  *   visible       device int32 [num_tokens][2], 8-byte aligned, or NULL.
  *   slopes        device f32 [n_q_heads], finite, or NULL.
  *   softcap       finite, >= 0; scale finite (PA_ERR_INVALID_ARG otherwise).

@@ -73,7 +73,7 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
     if (most <= 0) return PA_ERR_CUDA;
     if (workspace_bytes < workspace_size(most, unit, d_head)) return PA_ERR_WORKSPACE;
 
-    ShapedArgs a{};
+    CurvedArgs a{};
     a.ctx_cap = ctx_cap;
     if ((double)((all_rows + unit - 1) / unit) * num_seqs * n_kv_heads > 1 << 30) return PA_ERR_UNSUPPORTED;
     const Split split = split_work(f8, wide, all_rows, num_seqs, n_kv_heads, ctx_cap);
@@ -112,13 +112,14 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
         !pa_host::cache_view(&mv, v_cache, cache_rows, d_head, f8 ? 1 : 2, box))
         return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const ShapedArgs& shaped = a;
     int rc;
     if (wide)
         rc = launch_shaped_wide(unit, d_head, f8, q, block_size, mk, mv, a, split.grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     else
-        rc = f8 ? launch_multi<128, true>(split.warps, mk, mv, a, split.grid, st)
-             : d_head == 128 ? launch_multi<128, false>(split.warps, mk, mv, a, split.grid, st)
-                             : launch_multi<64, false>(split.warps, mk, mv, a, split.grid, st);
+        rc = f8 ? launch_multi<128, true>(split.warps, mk, mv, shaped, split.grid, st)
+             : d_head == 128 ? launch_multi<128, false>(split.warps, mk, mv, shaped, split.grid, st)
+                             : launch_multi<64, false>(split.warps, mk, mv, shaped, split.grid, st);
     if (rc != PA_OK || split.direct) return rc;
     return launch_merge(a, unit, d_head, split.units, split.grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -161,13 +161,13 @@ __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restri
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D, bool kScaled>
-int launch_shaped(const ShapedPrefillArgs& a, const ShapedStageArgs& sa, const pa_attend_calls::Call& c, uint16_t* k_stage, int grid) {
+template <int D, bool kScaled, class Args>
+int launch_shaped(const Args& a, const ShapedStageArgs& sa, const pa_attend_calls::Call& c, uint16_t* k_stage, int grid) {
     CUtensorMap mq, mk, mv;
     const long long cache_rows = (long long)c.num_blocks * c.n_kv_heads * c.block_size;
     if (!make_maps<D>(mq, mk, mv, a, sa, c.q, c.k_cache, kScaled ? k_stage : nullptr, c.num_tokens, cache_rows)) return PA_ERR_CUDA;
-    const auto kernel = prefill_kernel<D, kScaled, ShapedPrefillArgs>;
-    if (pa_host::ensure_smem_attr(kernel, PGeo<D>::kSmem, g_smem_done<D, kScaled, ShapedPrefillArgs>) != cudaSuccess)
+    const auto kernel = prefill_kernel<D, kScaled, Args>;
+    if (pa_host::ensure_smem_attr(kernel, PGeo<D>::kSmem, g_smem_done<D, kScaled, Args>) != cudaSuccess)
         return PA_ERR_CUDA;
     const dim3 sgrid((unsigned)sa.t_slot, (unsigned)sa.num_seqs, (unsigned)sa.n_kv_heads);
     cudaError_t e;
@@ -204,7 +204,7 @@ int launch_prompt(const Call& c) {
     int* sched = reinterpret_cast<int*>(w8 + ws.total);
     const int group = c.n_q_heads / c.n_kv_heads, tq = kRows / group;
     const long long tiles = ((long long)c.max_query_len + 2 * tq - 1) / (2 * tq), items = tiles * c.num_seqs * c.n_kv_heads;
-    ShapedPrefillArgs a{};
+    CurvedPrefillArgs a{};
     a.out = c.out;
     a.out_f32 = c.out_f32;
     a.out_al32 = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;
@@ -259,8 +259,11 @@ int launch_prompt(const Call& c) {
     sa.num_tokens = c.num_tokens;
     sa.sched = sched;
     sa.ctx_cap = c.ctx_cap;
-    if (scaled) return launch_shaped<128, true>(a, sa, c, reinterpret_cast<uint16_t*>(w8 + ws.k_off), grid);
-    return c.d_head == 128 ? launch_shaped<128, false>(a, sa, c, nullptr, grid) : launch_shaped<64, false>(a, sa, c, nullptr, grid);
+    const auto launch = [&](const auto& args) {
+        if (scaled) return launch_shaped<128, true>(args, sa, c, reinterpret_cast<uint16_t*>(w8 + ws.k_off), grid);
+        return c.d_head == 128 ? launch_shaped<128, false>(args, sa, c, nullptr, grid) : launch_shaped<64, false>(args, sa, c, nullptr, grid);
+    };
+    return c.softcap > 0.f || c.slopes ? launch(a) : launch(static_cast<const ShapedPrefillArgs&>(a));
 }
 
 }  // namespace pa_attend_calls

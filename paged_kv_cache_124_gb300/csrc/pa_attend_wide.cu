@@ -12,8 +12,9 @@
 namespace pa_multi {
 
 cudaError_t launch_shaped_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& mk,
-                               const CUtensorMap& mv, const ShapedArgs& a, int grid, cudaStream_t st) {
-    return launch_units(rows, d_head, f8, q, block_size, mk, mv, a, grid, st);
+                               const CUtensorMap& mv, const CurvedArgs& a, int grid, cudaStream_t st) {
+    return a.cap_inv != 0.f || a.slopes ? launch_units(rows, d_head, f8, q, block_size, mk, mv, a, grid, st)
+                                        : launch_units(rows, d_head, f8, q, block_size, mk, mv, static_cast<const ShapedArgs&>(a), grid, st);
 }
 
 }  // namespace pa_multi

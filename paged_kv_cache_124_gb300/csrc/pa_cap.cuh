@@ -1,7 +1,7 @@
 // Scores capped by a tanh: cap tanh(x / cap), in units of log2 (x, cap and the
 // result times log2(e)).  Around zero by tanh's series, up to x^9 (the next
 // term is 5e-8 of it at 0.3), beyond by 1 - 2 / (e^2x + 1), which would cancel
-// there: relative errors below 1e-6.  (The hardware's tanh is off by 2^-11,
+// there: relative errors below 1e-6 (cap_scores: also 2^-22 of the cap).  (The hardware's tanh is off by 2^-11,
 // which a cap of 50 makes 0.02 of a score.)
 #pragma once
 
@@ -18,19 +18,21 @@ __device__ __forceinline__ float capped(float x, float cap_log2, float cap_inv) 
     return cap_log2 * (fabsf(u) < 0.3f ? u * p : fmaf(-2.f, r, 1.f));
 }
 
-// n scores (times c2; cap_inv is 1 / cap_log2).  Where all of a warp's are
-// within 0.3 of the cap, as nearly always, by the series alone, in packed pairs.
+// n scores s (times c2; cap_inv is 1 / cap_log2).  Where all of a warp's are
+// within half of the cap, as nearly always, by a polynomial in s^2 alone, in
+// packed pairs: tanh(u) / u fitted on [0, 0.5] with even ripple (relative
+// 6e-7), the scales of u folded into its coefficients.
 template <int n>
 __device__ __forceinline__ void cap_scores(float (&s)[n], float c2, float cap_log2, float cap_inv) {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < n; ++i) top[i & 3] = fmaxf(top[i & 3], fabsf(s[i]));
-    const float by = c2 * cap_inv;
-    const bool far = !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(by) < 0.3f);
+    for (int i = 0; i < n; i += 2) asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %1;\n\tabs.f32 y, %2;\n\tmax.f32 %0, %0, x, y;\n\t}" : "+f"(top[i / 2 & 3]) : "f"(s[i]), "f"(s[i + 1]));
+    const float by = c2 * cap_inv, w = by * by;
+    const bool far = !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(by) < 0.5f);
     if (!__any_sync(0xffffffffu, far)) {
-        const auto both = [](float lo, float hi) {
+        const auto both = [](float x) {
             uint64_t r;
-            asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+            asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
             return r;
         };
         const auto mul = [](uint64_t a, uint64_t b) {
@@ -38,25 +40,31 @@ __device__ __forceinline__ void cap_scores(float (&s)[n], float c2, float cap_lo
             asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
             return d;
         };
-        const auto fma = [](uint64_t a, uint64_t b, float c) {
+        const auto fma = [](uint64_t a, uint64_t b, uint64_t c) {
             uint64_t d;
-            asm("{\n\t.reg .b64 c;\n\tmov.b64 c, {%3, %3};\n\tfma.rn.f32x2 %0, %1, %2, c;\n\t}" : "=l"(d) : "l"(a), "l"(b), "f"(c));
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
             return d;
         };
+        const uint64_t q0 = both(c2 * 0.999999456f), q1 = both(c2 * w * -0.3332632f), q2 = both(c2 * w * w * 0.131903234f),
+                       q3 = both(c2 * w * w * w * -0.0444030606f);
 #pragma unroll
         for (int i = 0; i < n; i += 2) {
-            const uint64_t u = mul(both(s[i], s[i + 1]), both(by, by)), v = mul(u, u);
-            uint64_t p = fma(v, both(62.f / 2835.f, 62.f / 2835.f), -17.f / 315.f);
-            p = fma(p, v, 2.f / 15.f);
-            p = fma(p, v, -1.f / 3.f);
-            p = fma(p, v, 1.f);
-            p = mul(mul(u, both(cap_log2, cap_log2)), p);
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(s[i]), "=f"(s[i + 1]) : "l"(p));
+            uint64_t x;
+            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(s[i]), "f"(s[i + 1]));
+            const uint64_t v = mul(x, x), y = mul(x, fma(fma(fma(q3, v, q2), v, q1), v, q0));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(s[i]), "=f"(s[i + 1]) : "l"(y));
         }
         return;
     }
+    // else by the second form of `capped` alone, which is within 2^-22 of the cap
+    const float to = by * 2.8853900817779268f;
 #pragma unroll
-    for (int i = 0; i < n; ++i) s[i] = capped(s[i] * c2, cap_log2, cap_inv);
+    for (int i = 0; i < n; ++i) {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s[i] * to));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+        s[i] = fmaf(-2.f * cap_log2, r, cap_log2);
+    }
 }
 
 }  // namespace pa

@@ -53,7 +53,7 @@ struct ShapedUnit : Unit {
 struct MultiArgs {
     using Seq = pa_multi::Seq;
     using Unit = pa_multi::Unit;
-    static constexpr bool kShaped = false;
+    static constexpr bool kShaped = false, kCurved = false;
     void* out;
     const __nv_bfloat16* q;
     const void* v_cache;
@@ -79,12 +79,16 @@ struct MultiArgs {
 struct ShapedArgs : MultiArgs {
     using Seq = ShapedSeq;
     using Unit = ShapedUnit;
-    static constexpr bool kShaped = true;
+    static constexpr bool kShaped = true, kCurved = false;
     const int2* visible;                   // [tokens] positions x .. y - 1 are seen; null: causal
     const float* slopes;                   // [query heads], or null
     const uint8_t* k_scales;               // [blocks][KV heads] biased exponents, or null
     const uint8_t* v_scales;
     float cap_log2, cap_inv;               // cap * log2(e) and 1 over it; 0: none
+};
+// With a cap or a bias: a form of the wide kernel of its own.
+struct CurvedArgs : ShapedArgs {
+    static constexpr bool kCurved = true;
 };
 
 // 2^(e - 127) of a scale's byte (of byte 0, 0: what 2^-127 scales is nothing beside any sum).
@@ -516,7 +520,7 @@ cudaError_t launch_merge(const MultiArgs& a, int unit, int d_head, double units,
 // Launches of the 64- and 128-row units on the 5th-generation tensor cores
 // (pa_decode_wide.cu, pa_attend_wide.cu); cudaSuccess or the launch's error.
 cudaError_t launch_shaped_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& map_k,
-                               const CUtensorMap& map_v, const ShapedArgs& a, int grid, cudaStream_t st);
+                               const CUtensorMap& map_v, const CurvedArgs& a, int grid, cudaStream_t st);
 cudaError_t launch_wide(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& map_k,
                         const CUtensorMap& map_v, const MultiArgs& a, int grid, cudaStream_t st);
 // (Unit cost of 2, 3, 4, 6 steps: 64 requests of 8 tokens, E4M3 68.6, 67.3, 67.6, 69.5 us; 48 trees of 16, bf16

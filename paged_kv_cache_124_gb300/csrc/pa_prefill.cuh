@@ -51,7 +51,7 @@ struct PGeo {
 };
 
 struct PrefillArgs {
-    static constexpr bool kShaped = false;
+    static constexpr bool kShaped = false, kCurved = false;
     void* out;
     int out_f32;
     int out_al32;         // out is 32-byte aligned: 256-bit stores
@@ -83,12 +83,16 @@ struct PrefillArgs {
 // Scores s become cap tanh(s / cap), less slope |p - j|, over an interval of
 // positions per token (pa_attend).
 struct ShapedPrefillArgs : PrefillArgs {
-    static constexpr bool kShaped = true;
+    static constexpr bool kShaped = true, kCurved = false;
     const int2* visible;  // [tokens] positions x .. y - 1 are seen; null: causal
     const float* slopes;  // [query heads], or null
     float cap_log2, cap_inv;   // cap * log2(e) and 1 over it; 0: none
     const void* v_cache;  // for values that are not finite
     int ctx_cap, max_query_len;
+};
+// With a cap or a bias (forms of their own: their code beside the masks' alone cost 15 %).
+struct CurvedPrefillArgs : ShapedPrefillArgs {
+    static constexpr bool kCurved = true;
 };
 
 // One work item: query rows [t0, t0 + 2 tq) of sequence seq's n new tokens
@@ -461,28 +465,34 @@ __device__ __forceinline__ Item read_item(const Item* src) {
 }
 
 // The staging leaves out values that are not finite (0 * inf is not 0); a row
-// adds those that it sees, positions [lo, lim) from the item's first, here:
-// columns c0 .. c0 + n - 1 of the row.
+// adds those that it sees, positions [lo, lim) from the item's first, to what
+// its thread has written: columns c0 .. c0 + n - 1, from element `at` of out.
 template <int D, bool kF8, int n>
-__device__ __noinline__ void add_unfinite_values(const ShapedPrefillArgs& a, const Item& it, int lo, int lim, int c0,
-                                                 const uint8_t* fmt, int n_tiles, float* o) {
-    const int32_t* table = a.block_tables + (size_t)it.seq * a.max_blocks;
+__device__ __noinline__ void add_unfinite_values(const ShapedPrefillArgs& a, int seq, int h, int base, int lo, int lim, int c0,
+                                                 const uint8_t* fmt, int n_tiles, size_t out_at) {
+    const int32_t* table = a.block_tables + (size_t)seq * a.max_blocks;
 #pragma unroll 1
     for (int pos = lo; pos < min(lim, n_tiles * kKv); ++pos) {
         if (!(fmt[pos / kKv] & 2)) {
             pos |= kKv - 1;
             continue;
         }
-        const int at = it.base + pos, blk = table[at / a.block_size];
+        const int at = base + pos, blk = table[at / a.block_size];
         if (blk < 0 || blk >= a.num_blocks) continue;
-        const size_t row = (((size_t)blk * a.n_kv_heads + it.h) * a.block_size + at % a.block_size) * D + c0;
+        const size_t row = (((size_t)blk * a.n_kv_heads + h) * a.block_size + at % a.block_size) * D + c0;
 #pragma unroll 1
         for (int c = 0; c < n; ++c) {
-            if constexpr (kF8) {
-                if ((static_cast<const uint8_t*>(a.v_cache)[row + c] & 0x7f) == 0x7f) o[c] = __int_as_float(0x7fffffff);
+            float v;
+            if constexpr (kF8)
+                v = (static_cast<const uint8_t*>(a.v_cache)[row + c] & 0x7f) == 0x7f ? __int_as_float(0x7fffffff) : 0.f;
+            else
+                v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v_cache)[row + c]);
+            if (fabsf(v) < INFINITY) continue;
+            if (a.out_f32) {
+                static_cast<float*>(a.out)[out_at + c] += v;
             } else {
-                const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v_cache)[row + c]);
-                if (!(fabsf(v) < INFINITY)) o[c] += v;
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + out_at + c;
+                *o = __float2bfloat16(__bfloat162float(*o) + v);
             }
         }
     }
@@ -885,9 +895,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_used[2] = {kNothing, kNothing}, l[2] = {0.f, 0.f};
             int row_lim[2], row_lo[2] = {0, 0};
             float slope = 0.f;                            // times log2(e)
-            if constexpr (kShaped)
+            if constexpr (Args::kCurved)
                 if (a.slopes) slope = 1.4426950408889634f * a.slopes[it.h * a.group + gq];
             bool valid_row[2];
+#pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int tok = it.t0 + x * a.tq + t;
                 valid_row[x] = tok < it.n && it.q0 + tok < a.num_tokens;
@@ -909,6 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr bool kMayBeWide = decltype(may_be_wide)::value;
                 for (int j = 0; ok && j < it.n_tiles; ++j) {
                     const int wide = kMayBeWide ? (kShaped ? fmt[j] & 1 : fmt[j]) : 0;   // V tile j staged as fp16 (0) or bf16 (1)
+#pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (j >= nt[x]) continue;
                         ok = wait_warp(&bars->s_full[x], ns[x] & 1, bars, a.status);
@@ -923,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         const int lim = row_lim[x] - j * kKv - hc * kHalfCols;     // valid columns of this half
                         float c2 = c2x[x];
-                        if constexpr (kShaped) {
+                        if constexpr (Args::kCurved) {
                             if (a.cap_inv != 0.f) {
                                 pa::cap_scores<kHalfCols>(s, c2, a.cap_log2, a.cap_inv);
                                 c2 = 1.f;
@@ -931,10 +943,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (a.slopes) {
                                 // the token's distance to the half's first column
                                 const float d0 = (float)(it.ctx - it.n + it.t0 + x * a.tq + t - it.base - j * kKv - hc * kHalfCols);
+                                if (__all_sync(0xffffffffu, (float)lim <= d0 + 1.f)) {   // no row sees ahead: distances without their sign
+                                    uint64_t bias[4];
 #pragma unroll
-                                for (int cc = 0; cc < kHalfCols; ++cc) s[cc] = fmaf(-slope, fabsf(d0 - (float)cc), s[cc] * c2);
+                                    for (int k = 0; k < 4; ++k) bias[k] = f32x2(slope * (2 * k - d0), slope * (2 * k + 1 - d0));
+                                    const uint64_t c = f32x2(c2, c2), step = f32x2(8.f * slope, 8.f * slope);
+#pragma unroll
+                                    for (int cc = 0; cc < kHalfCols; cc += 2) {
+                                        uint64_t& b = bias[cc / 2 & 3];
+                                        f32x2_split(fma_f32x2(f32x2(s[cc], s[cc + 1]), c, b), s[cc], s[cc + 1]);
+                                        b = add_f32x2(b, step);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int cc = 0; cc < kHalfCols; ++cc) s[cc] = fmaf(-slope, fabsf(d0 - (float)cc), s[cc] * c2);
+                                }
                                 c2 = 1.f;
                             }
+                        }
+                        if constexpr (kShaped) {
                             const int from = row_lo[x] - j * kKv - hc * kHalfCols;
                             if (from > 0 || lim < kHalfCols) {
 #pragma unroll
@@ -1034,6 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 run_tiles(std::true_type{});
             else
                 run_tiles(std::false_type{});
+#pragma unroll
             for (int x = 0; x < 2 && ok; ++x) {
                 if (nt[x] == 0) continue;
                 const float l_all = l[x] + exchange(x, l[x], ok);
@@ -1059,8 +1087,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < kOCols; ++k) o[k] = 0.f;
                         }
-                        if (__builtin_expect(it.wide & 2, 0))
-                            add_unfinite_values<D, kF8, kOCols>(a, it, row_lo[x], row_lim[x], hc * kOCols, fmt, x ? it.nt1 : it.nt0, o);
                     }
                     // a thread writes its half row: whole 32-byte sectors when
                     // out allows it (16-byte stores fill half a sector each and
@@ -1095,6 +1121,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             dst[q] = make_uint4(pack_bf16_rn(o[8 * q], o[8 * q + 1]), pack_bf16_rn(o[8 * q + 2], o[8 * q + 3]),
                                                 pack_bf16_rn(o[8 * q + 4], o[8 * q + 5]), pack_bf16_rn(o[8 * q + 6], o[8 * q + 7]));
                     }
+                    if constexpr (kShaped)
+                        if (__builtin_expect(it.wide & 2, 0))
+                            add_unfinite_values<D, kF8, kOCols>(a, it.seq, it.h, it.base, row_lo[x], row_lim[x], hc * kOCols, fmt, x ? it.nt1 : it.nt0, orow);
                 }
             }
         }

@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     lim = v.y;
                 }
                 lim = min(lim, u->ctx);
-                if (a.slopes) slope = kLog2e * a.slopes[(u->kvh << a.log2_group) + ((u->row0 + r) & ((1 << a.log2_group) - 1))];
+                if (Args::kCurved && a.slopes) slope = kLog2e * a.slopes[(u->kvh << a.log2_group) + ((u->row0 + r) & ((1 << a.log2_group) - 1))];
                 seen_lo = u->seen_lo;
                 seen_hi = u->seen_hi;
                 table = table_of(a, *u);
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         grows = v_new > v_top;
                         scales = scales_next;
                     }
-                    if (a.cap_inv != 0.f || a.slopes) {          // scores in units of log2 from here on
+                    if (Args::kCurved) {                         // scores in units of log2 from here on
                         if constexpr (kScaled) {
 #pragma unroll
                             for (int k = 0; k < kCols; k += 2) split(mul2(pair(s[k], s[k + 1]), pair(cs[k >> 3], cs[k >> 3])), s[k], s[k + 1]);

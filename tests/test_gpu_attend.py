@@ -86,7 +86,9 @@ class Problem:
         """|out - ref| within what the roundings inside allow.  A score is off
         by the operand roundings and the products' 32 bits, (E + 128 2^-24)
         (|q| . |k|) |scale| (bf16: q exact; E4M3 codes: q to f16, 2^-11), by the
-        cap's evaluation, 2^-19 of it, and by a bias's roundings, 2^-22 of it;
+        cap's evaluation, 2^-20 of the score (a polynomial's 6e-7 and roundings)
+        and 2^-21 of the cap (1 - 2 / (e + 1), whose quotient's 2^-22.5 of e and
+        half steps come to 2^-23 of 1), and by a bias's roundings, 2^-22 of it;
         a weight by that and its own rounding W (bf16: two terms, 2^-16; else
         f16, 2^-11); all doubled, as the normaliser moves too; an output by
         that times sum a |v|, and half a step of its type.  Values that f16
@@ -110,7 +112,7 @@ class Problem:
                 for g in range(self.Hq):
                     size = (K[g // G] @ qa[r, g]).max() * abs(self.scale) if len(K[0]) else 0.0
                     bias = 0.0 if self.slopes is None else float(self.slopes[g]) * int(self.ctx[s])
-                    off = (E + 128 * 2.0 ** -24) * size + 2.0 ** -19 * min(size, self.cap or 0.0) + 2.0 ** -22 * (bias + size)
+                    off = (E + 128 * 2.0 ** -24) * size + 2.0 ** -20 * min(size, self.cap) + 2.0 ** -21 * self.cap + 2.0 ** -22 * (bias + size)
                     tol = 2 * (off + W) * weight[r, g] * 2 + 2.0 ** -24 * (V[g // G].max() if len(V[0]) else 0.0)
                     if out.dtype == torch.bfloat16:
                         tol = tol + 2.0 ** -8 * np.abs(want[r, g])
