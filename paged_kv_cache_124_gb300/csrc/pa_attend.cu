@@ -4,22 +4,59 @@
 // E4M3 codes with a power-of-two scale per block and head (pa_attend,
 // pa_attend_scaled; the formulas stand in pa.h).
 //
-// Up to 16 rows a KV head (new tokens times query heads of the group) take
-// the units of pa_multi_rows.cuh.  What the shape costs them is arithmetic on
-// 16 scores a tile and lane beside the cache's bytes.  A sequence's work
-// begins at the first position that some token of it sees and ends behind
-// the last, so a window costs its own bytes.
+// Three kernels take them (route_of): units of 16 rows a KV head, on warp-level
+// products (pa_multi_rows.cuh), units of 64 and 128 rows on the tensor cores
+// (pa_wide.cuh), and whole prompts (pa_prefill.cuh).  In the first two a
+// sequence's work begins at the first position that some token of it sees and
+// ends behind the last; in the third that goes by items of 256 rows: so a
+// window costs its own bytes.
+//
+// What the shape costs beside the plain kernels: with few rows, arithmetic
+// that the cache's bytes hide (64 decodes of 4096 positions, capped, 169 us,
+// 0.94 of the measured copy rate; block-scaled 107, where a weight and a score
+// take a factor more).  With many, the softmax's instructions bind: 8 prompts
+// of 2003 tokens 300 us causal (285 plain), 373 with a bias, 418 with a cap.
 
 #include "pa_attend.cuh"
 #include "pa_multi_rows.cuh"
 
 namespace {
 
-// Which kernel takes a call.  Up to 16 rows a KV head: units of 16.  More:
-// with a scale above 0, units of 64 or 128 rows (wide), or, for long chunks and
-// prompts, the prefill kernel.  (Scales of 0 or below: units of 16 rows.)
 enum Route { kUnits16, kWide, kPrompt };
-Route route_of(long long rows, float scale) { return rows <= kRows || !(scale > 0.f) ? kUnits16 : rows <= 256 ? kWide : kPrompt; }
+
+// From this many rows a KV head on (new tokens times the group's heads) a call may go to the prefill kernel.
+constexpr long long kPromptRows = 192;
+
+// Which kernel takes a call.  Up to 16 rows a KV head, with a scale that is
+// not positive, and over few short contexts (in_small_tiles), or many that are
+// block-scaled, of up to 256 positions with up to 32 rows: units of 16 rows.  More rows:
+// units of 64 or 128 (wide), whose contexts are split over the device, or the
+// prefill kernel, whose items of 256 rows read their keys once, up to their
+// own last one.  The estimates (us, on 152 SMs) count wide units, at 1.75 us
+// of an SM a tile of 128 positions (block-scaled, 64 rows: 1.25) and 6 (4.5)
+// to begin and end, and items, at 2.6 a tile of two and 6.5.  32 query and 8
+// KV heads, us of wide / prefill:
+//   contexts x new tokens   bf16        block-scaled
+//   8 x 8192, 64            105 / 178   144 / 219
+//   8 x 8192, 128           183 / 181   266 / 221
+//   8 x 1024, 128            51 / 38     63 / 44
+//   64 x 2048, 64           196 / 253   311 / 319
+//   64 x 512, 128           190 / 124   241 / 146
+//   1 x 16384, 512          170 / 252   261 / 266
+//   8 x 64, 64               12 / 16     18 / 16
+//   64 x 64, 64              52 / 46     87 / 51
+// and of units of 16 rows / wide: 512 x 60, 8 tokens 99 / 99 and 118 / 144; 512 x 300 217 / 144 and 212 / 217.
+Route route_of(long long rows, float scale, bool f8, int num_seqs, int n_kv_heads, int group, int ctx) {
+    const double heads = (double)num_seqs * n_kv_heads;
+    if (rows <= kRows || !(scale > 0.f) || in_small_tiles(f8, rows, heads, ctx)) return kUnits16;
+    if (f8 && rows <= 32 && ctx <= 256 && heads >= 1024) return kUnits16;
+    if (rows < kPromptRows) return kWide;
+    const double units = heads * (double)((rows + (f8 ? 63 : 127)) / (f8 ? 64 : 128)), tiles = (ctx + 127) / 128;
+    const double wide = 5 + units * tiles * (f8 ? 1.25 : 1.75) / 152 + ceil(units / 152) * (f8 ? 4.5 : 6) + (units > 152 ? 4 : 0);
+    const double items = heads * (double)((rows + 255) / 256), seen = (ctx - 0.5 * (double)(rows / group)) / 128 + 0.5;
+    const double prompt = 8 + fmax(1.0, items / 152) * (2.6 * seen + 6.5) + heads * ctx * (f8 ? 0.9e-4 : 0.7e-4);
+    return wide <= prompt ? kWide : kPrompt;
+}
 
 int unit_of(Route route, long long rows, bool f8) { return unit_rows(rows, f8, route == kWide); }
 
@@ -54,7 +91,7 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
     const long long cap = (long long)max_blocks_per_seq * block_size;
     const int ctx_cap = (int)(cap < max_context_len ? cap : max_context_len);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return PA_ERR_WORKSPACE;
-    Route route = route_of(all_rows, scale);
+    Route route = route_of(all_rows, scale, f8, num_seqs, n_kv_heads, group, ctx_cap);
     if (route == kPrompt) {
         const size_t n = pa_attend_calls::prompt_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads,
                                                            n_kv_heads, d_head, f8);
@@ -141,7 +178,7 @@ size_t pa_attend_workspace_size(int num_seqs, int max_query_len, int max_blocks_
         const size_t n = workspace_size(max_grid(route == kWide), unit_of(route, rows, scaled != 0), d_head);
         most = n > most ? n : most;
     }
-    if (route_of(rows, 1.f) == kPrompt) {
+    if (rows >= kPromptRows) {
         const size_t n = pa_attend_calls::prompt_workspace(num_seqs, max_query_len, max_blocks_per_seq, block_size, n_q_heads,
                                                            n_kv_heads, d_head, scaled != 0);
         most = n > most ? n : most;

@@ -67,17 +67,6 @@ namespace {
 // Its bf16 products take a positive scale only; others go 16 rows at a time.
 bool is_wide(bool f8, float scale, long long rows) { return rows > kRows && (f8 || scale > 0.f); }
 
-// Whether a call that the wide kernel could take goes 16 rows at a time all
-// the same: contexts of one tile, and an SM for each unit of 16 (a third of
-// one where the units there would be of 128).  8 KV heads of 128, 64
-// positions, us here against there: 4 sequences of 32 rows 6.2 / 7.2, of 64
-// 6.5 / 7.9, of 128 7.9 / 9.8, 9 of 96 7.9 / 9.2, 1 of 256 6.7 / 10.8; 18 of
-// 32 at 128 positions 8.7 / 7.7; E4M3 4 of 128 at 128 9.1 / 8.3.
-bool in_small_tiles(bool f8, long long rows, double heads, int ctx) {
-    const double units = heads * (double)((rows + kRows - 1) / kRows);
-    return ctx <= 128 && units <= (f8 || rows <= 64 ? 1 : 3) * sms();
-}
-
 int decode_multi(void* out, int out_dtype, const void* q, const void* k_cache, const void* v_cache,
                  const int32_t* block_tables, const int32_t* query_start, const int32_t* context_lens,
                  const int64_t* tree_mask, int block_size, float scale, int n_q_heads, int n_kv_heads, int d_head,

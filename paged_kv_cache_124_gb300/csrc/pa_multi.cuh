@@ -42,12 +42,10 @@ struct Unit {
 // or of 32) their begin, where step 0 starts; all tokens that see any see
 // seen_lo .. seen_hi - 1.
 struct ShapedSeq : Seq {
-    int base, first, seen_lo, seen_hi;
+    int base, first, seen_lo, seen_hi, blind;                     // blind: some token sees nothing
 };
 struct ShapedUnit : Unit {
-    int base, seen_lo, seen_hi;
-    // whether every row sees positions lo .. hi - 1
-    __device__ __forceinline__ bool all_see(int lo, int hi) const { return lo >= seen_lo && hi <= seen_hi; }
+    int base, seen_lo, seen_hi, blind;
 };
 
 struct MultiArgs {
@@ -124,6 +122,7 @@ __device__ __forceinline__ typename Args::Seq read_seq(const Args& a, int s, boo
         int lo = 0, hi = ctx;
         r.seen_lo = 0;
         r.seen_hi = r.first + 1;
+        r.blind = 0;
         if (a.visible) {
             lo = r.seen_hi = 0x7fffffff;
             hi = 0;
@@ -136,6 +135,8 @@ __device__ __forceinline__ typename Args::Seq read_seq(const Args& a, int s, boo
                     hi = max(hi, y);
                     r.seen_lo = max(r.seen_lo, x);
                     r.seen_hi = min(r.seen_hi, y);
+                } else {
+                    r.blind = 1;
                 }
             }
             if (lo >= hi) lo = hi = 0;                  // nothing is seen: a step of no positions, and zeros
@@ -203,6 +204,7 @@ __device__ __noinline__ void next_unit(WalkOf<typename Args::Seq>& w, typename A
             u.base = w.sq.base;
             u.seen_lo = w.sq.seen_lo;
             u.seen_hi = w.sq.seen_hi;
+            u.blind = w.sq.blind;
         } else {
             u.first = w.sq.ctx - w.sq.n;
         }

@@ -105,7 +105,7 @@ struct State {
 template <int D, bool F8, class Args>
 __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const Args& a,
                                           const typename Args::Unit& u, int lane, const uint32_t (&qr)[D / 16][4],
-                                          const Shape* shape, uint32_t scales, bool some) {
+                                          const Shape* shape, uint32_t scales, bool masked) {
     constexpr bool kShaped = Args::kShaped;
     constexpr int kSlabBytes = kTile * 128, kSteps = D / 16;
     const int g = lane >> 2, t4 = lane & 3;
@@ -159,7 +159,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
                 }
             f[0][0] = f[0][1] = f[1][0] = f[1][1] = 1.f;
         }
-        if (some) {
+        if (masked) {
             const int lo[2] = {shape[g].lo, shape[g + 8].lo}, hi[2] = {shape[g].hi, shape[g + 8].hi};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -487,10 +487,11 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
 #pragma unroll
         for (int h = 0; h < 2; ++h) c[h] = F8 ? q_scale[(lane >> 2) + 8 * h] : a.scale_log2;
 
-        int seen_lo = 0, seen_hi = 0;
+        int seen_lo = 0, seen_hi = 0, blind = 0;
         if constexpr (kShaped) {
             seen_lo = u.seen_lo;
             seen_hi = u.seen_hi;
+            blind = u.blind;
         }
         State<D> st;
         st.reset();
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
                         unfinite[nth & 1] = 1;
                     __syncwarp();
                 }
-                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, a, u, lane, qr, shape, tile_scales, some);
+                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, a, u, lane, qr, shape, tile_scales, some || blind);
             }
             __syncwarp();
             if (k + kStages < len) issue(u, k + kStages);
@@ -656,6 +657,17 @@ inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 inline size_t workspace_size(int grid, int unit, int d) {
     const size_t rows = (size_t)2 * grid * unit;
     return up256(16 * (size_t)grid) + 2 * up256(4 * rows) + 4 * rows * d;
+}
+
+// Whether a call that the wide kernel could take goes 16 rows at a time all
+// the same: contexts of one tile, and an SM for each unit of 16 (a third of
+// one where the units there would be of 128).  8 KV heads of 128, 64
+// positions, us here against there: 4 sequences of 32 rows 6.2 / 7.2, of 64
+// 6.5 / 7.9, of 128 7.9 / 9.8, 9 of 96 7.9 / 9.2, 1 of 256 6.7 / 10.8; 18 of
+// 32 at 128 positions 8.7 / 7.7; E4M3 4 of 128 at 128 9.1 / 8.3.
+inline bool in_small_tiles(bool f8, long long rows, double heads, int ctx) {
+    const double units = heads * (double)((rows + kRows - 1) / kRows);
+    return ctx <= 128 && units <= (f8 || rows <= 64 ? 1 : 3) * sms();
 }
 
 inline void set_workspace(MultiArgs& a, void* workspace, int grid, int unit) {

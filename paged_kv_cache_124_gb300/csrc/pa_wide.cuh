@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // what the row sees of the new tokens: a word (tree), or positions below `lim`
             unsigned long long word = tree && real ? words_of(a, *u)[i] : ~0ull;
             if (u->n < 64) word &= (1ull << u->n) - 1;
-            int lim = (tree || !real) ? u->ctx : first + i + 1, from = 0, seen_lo = 0, seen_hi = 0;
+            int lim = (tree || !real) ? u->ctx : first + i + 1, from = 0;
             const int pos = first + i;
             float slope = 0.f;                                   // times log2(e)
             const int32_t* table = nullptr;
@@ -653,8 +653,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 lim = min(lim, u->ctx);
                 if (Args::kCurved && a.slopes) slope = kLog2e * a.slopes[(u->kvh << a.log2_group) + ((u->row0 + r) & ((1 << a.log2_group) - 1))];
-                seen_lo = u->seen_lo;
-                seen_hi = u->seen_hi;
                 table = table_of(a, *u);
                 kvh = u->kvh;
                 end = u->ctx;
@@ -765,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         cs[0] = cs[1] = cs[2] = cs[3] = 1.f;
                     }
                 }
-                if (kShaped ? t0 < seen_lo || t0 + kCols > seen_hi : t0 + kCols > first) {   // some row may not see some position
+                if (kShaped ? t0 < from || t0 + kCols > lim : t0 + kCols > first) {   // some row (shaped: this one) may not see some position
 #pragma unroll
                     for (int x = 0; x < kCols; x += 32) {
                         const uint32_t v = seen(t0 + x);

@@ -110,10 +110,10 @@ class Problem:
             for r in range(self.start[s], self.start[s + 1]):
                 covered[r] = True
                 for g in range(self.Hq):
-                    size = (K[g // G] @ qa[r, g]).max() * abs(self.scale) if len(K[0]) else 0.0
+                    size = np.nanmax(K[g // G] @ qa[r, g]) * abs(self.scale) if len(K[0]) else 0.0   # (NaN: where nobody looks)
                     bias = 0.0 if self.slopes is None else float(self.slopes[g]) * int(self.ctx[s])
                     off = (E + 128 * 2.0 ** -24) * size + 2.0 ** -20 * min(size, self.cap) + 2.0 ** -21 * self.cap + 2.0 ** -22 * (bias + size)
-                    tol = 2 * (off + W) * weight[r, g] * 2 + 2.0 ** -24 * (V[g // G].max() if len(V[0]) else 0.0)
+                    tol = 2 * (off + W) * weight[r, g] * 2 + 2.0 ** -24 * (np.nanmax(V[g // G]) if len(V[0]) else 0.0)
                     if out.dtype == torch.bfloat16:
                         tol = tol + 2.0 ** -8 * np.abs(want[r, g])
                     assert (np.abs(got[r, g] - want[r, g]) <= tol).all(), (s, r, g, np.abs(got[r, g] - want[r, g]).max(), tol.max())
@@ -186,6 +186,25 @@ def test_rows_that_see_nothing_are_zeros(scaled, news):
     out = p.run()
     p.check(out)
     assert (out[1:3] == 0).all() and (out[news[0]:] == 0).all()
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("news", [[3], [8], [90], [150]], ids=["3", "8", "90", "150"])
+@pytest.mark.parametrize("empty", [(400, 400), (0, 0), (9, 3), (2000, 3000)])
+def test_rows_that_see_nothing_beside_rows_that_see_all(scaled, news, empty):
+    """Tiles that need no mask for the others."""
+    p = Problem(4, 4, 1, 128, 16, [900], news, "window", scaled=scaled)
+    p.visible[:, 0], p.visible[:, 1] = 0, 900
+    p.visible[1] = empty
+    p.visible[-1] = empty
+    if empty == (2000, 3000):                                      # and NaN where nobody looks
+        p.visible[::3, 0] = 20
+        for c in (p.kc, p.vc):
+            c[p.tables[0, 0], :, 3] = 0x7F if scaled else 0x7FC0
+        p.visible[:, 0] = np.maximum(p.visible[:, 0], 4)
+    out = p.run()
+    p.check(out)
+    assert (out[1] == 0).all() and (out[-1] == 0).all()
 
 
 @pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
