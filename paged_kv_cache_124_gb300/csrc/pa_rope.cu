@@ -105,9 +105,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) heads_kernel(const RopeArgs a
 // Many: kSide heads of a token side by side (32 / (kSide D / 16) tokens per
 // warp), turn after turn, kFlight turns in flight, so that the angles and
 // the gains are loaded once for all of a token's heads.
-constexpr int kFlight = 4, kSide = 2;
+constexpr int kFlight = 4;
 
-template <int D, bool F8, bool kInterleaved, bool kAxes>
+template <int D, bool F8, bool kInterleaved, bool kAxes, int kSide>
 __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs a) {
     constexpr int kLanes = D / 16, kGroup = kLanes * kSide;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -225,17 +225,31 @@ __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs 
 // 14.6, 4000 21.8 / 25.7, 32,048 144 / 180; 16 + 2 x 2 of 64: 5000 tokens 7.6 /
 // 5.7, 10,000 12.5 / 12.9, 40,000 36.2 / 42.5), if a token has heads enough to
 // share its angles (2 + 2 x 1: 40,000 tokens 38.5 / 21.9).
+template <int D, bool F8, bool kInterleaved, bool kAxes, int kSide>
+cudaError_t launch_tokens(const RopeArgs& a, cudaStream_t st) {
+    const int per = kRopeThreads / (D / 16 * kSide);
+    return pa_host::launch_dependent(tokens_kernel<D, F8, kInterleaved, kAxes, kSide>,
+                                     dim3((unsigned)(((long long)a.num_tokens + per - 1) / per)), dim3(kRopeThreads), 0, st, a);
+}
+
+// Several axes: the kernel per token with four heads side by side, in blocks
+// of half the time, where its waves of resident blocks (two an SM) are at most
+// 1.5 times those of two heads.  32 + 2 x 4 heads of 128, us by head / four /
+// two: 500 tokens 4.0 / 4.2 / 6.0, 800 4.8 / 4.2 / 6.0, 2003 13.6 / 9.6 / 11.0,
+// 4006 (one wave of two) 21.0 / 17.2 / 16.0, 5003 (three of four, two of two)
+// 28.9 / 21.7 / 22.8, 8012 - / 31.5 / 29.2.
 template <int D, bool F8, bool kInterleaved, bool kAxes>
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
     constexpr int kLanes = D / 16;
     const int heads = a.n_q_heads + 2 * a.n_kv_heads;
     const long long rows = (long long)a.num_tokens * heads;
-    if (heads >= 16 && rows * D >= 12000000) {
-        const int per = kRopeThreads / (kLanes * kSide);
-        return pa_host::launch_dependent(tokens_kernel<D, F8, kInterleaved, kAxes>,
-                                         dim3((unsigned)(((long long)a.num_tokens + per - 1) / per)), dim3(kRopeThreads), 0,
-                                         st, a);
+    if constexpr (kAxes) {
+        const long long resident = 2 * 152, four = kRopeThreads / (4 * kLanes), two = kRopeThreads / (2 * kLanes);
+        const auto waves = [&](long long tokens) { return (a.num_tokens + tokens * resident - 1) / (tokens * resident); };
+        if (heads >= 16 && rows * D >= 3000000 && 2 * waves(four) <= 3 * waves(two))
+            return launch_tokens<D, F8, kInterleaved, kAxes, 4>(a, st);
     }
+    if (heads >= 16 && rows * D >= 12000000) return launch_tokens<D, F8, kInterleaved, kAxes, 2>(a, st);
     const int per = kRopeThreads / kLanes;
     return pa_host::launch_dependent(heads_kernel<D, F8, kInterleaved, kAxes>, dim3((unsigned)((rows + per - 1) / per)),
                                      dim3(kRopeThreads), 0, st, a);
