@@ -126,7 +126,7 @@ __device__ __forceinline__ typename Args::Seq read_seq(const Args& a, int s, boo
         if (a.visible) {
             lo = r.seen_hi = 0x7fffffff;
             hi = 0;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < r.n; ++i) {
                 const int2 v = a.visible[r.q0 + i];
                 const int x = max(v.x, 0), y = min(v.y, ctx);

@@ -88,7 +88,8 @@ class Problem:
         (|q| . |k|) |scale| (bf16: q exact; E4M3 codes: q to f16, 2^-11), by the
         cap's evaluation, 2^-20 of the score (a polynomial's 6e-7 and roundings)
         and 2^-21 of the cap (1 - 2 / (e + 1), whose quotient's 2^-22.5 of e and
-        half steps come to 2^-23 of 1), and by a bias's roundings, 2^-22 of it;
+        half steps come to 2^-23 of 1), and by a bias's roundings, 2^-20 of it
+        (prompts count distances up in at most 16 additions, 2^-24 each);
         a weight by that and its own rounding W (bf16: two terms, 2^-16; else
         f16, 2^-11); all doubled, as the normaliser moves too; an output by
         that times sum a |v|, and half a step of its type.  Values that f16
@@ -112,7 +113,7 @@ class Problem:
                 for g in range(self.Hq):
                     size = np.nanmax(K[g // G] @ qa[r, g]) * abs(self.scale) if len(K[0]) else 0.0   # (NaN: where nobody looks)
                     bias = 0.0 if self.slopes is None else float(self.slopes[g]) * int(self.ctx[s])
-                    off = (E + 128 * 2.0 ** -24) * size + 2.0 ** -20 * min(size, self.cap) + 2.0 ** -21 * self.cap + 2.0 ** -22 * (bias + size)
+                    off = (E + 128 * 2.0 ** -24) * size + 2.0 ** -20 * min(size, self.cap) + 2.0 ** -21 * self.cap + 2.0 ** -20 * bias + 2.0 ** -22 * size
                     tol = 2 * (off + W) * weight[r, g] * 2 + 2.0 ** -24 * (np.nanmax(V[g // G]) if len(V[0]) else 0.0)
                     if out.dtype == torch.bfloat16:
                         tol = tol + 2.0 ** -8 * np.abs(want[r, g])
@@ -132,6 +133,8 @@ CASES = [
     (2, 1, 128, 32, [2500], [2]),                                  # one head: the keys over many blocks
     (4, 1, 128, 16, [150, 400, 33], [150, 131, 1]),                # prompts and chunks: tiles of 128 rows
     (2, 2, 64, 8, [333, 140], [333, 29]),
+    (16, 2, 128, 8, [200, 77], [9, 30]),                           # 64 rows of 8-position blocks
+    (8, 2, 128, 32, [300, 1500], [20, 41]),
 ]
 
 
@@ -155,6 +158,101 @@ def test_scaled_attend_equals_the_oracle(Hq, Hkv, D, B, ctxs, news, mask, cap, a
     out = p.run(torch.bfloat16 if alibi else torch.float32, status=st)
     assert st.item() == 0
     p.check(out)
+
+
+def _dense(p, take):
+    """Rows `take` of p's outputs in float64 on the GPU, and sums of a |v| beside them, by the definition."""
+    f64 = (lambda c, s: Q.dequantize_scaled(c, s)) if p.ks is not None else (lambda c, s: A.bf16_to_f64(c))
+    K, V = (torch.from_numpy(f64(c, s)).cuda() for c, s in ((p.kc, p.ks), (p.vc, p.vs)))
+    G, out, size = p.Hq // p.Hkv, [], []
+    for r in take:
+        s = int(np.searchsorted(p.start, r, side="right")) - 1
+        C, pos = int(p.ctx[s]), int(p.ctx[s]) - int(p.start[s + 1]) + r
+        lo, hi = (0, pos + 1) if p.visible is None else (max(0, int(p.visible[r][0])), min(C, int(p.visible[r][1])))
+        ids = torch.from_numpy(p.tables[s][:-(-C // p.B)]).long().cuda()
+        k, v = (x[ids].transpose(0, 1).reshape(p.Hkv, -1, p.D)[:, lo:max(hi, lo)] for x in (K, V))
+        x = torch.einsum("hgd,hjd->hgj", p.q[r].double().cuda().view(p.Hkv, G, p.D), k) * p.scale
+        if p.cap:
+            x = p.cap * torch.tanh(x / p.cap)
+        if p.slopes is not None:
+            far = (torch.arange(lo, max(hi, lo), device="cuda") - pos).abs()
+            x = x - torch.from_numpy(p.slopes).double().cuda().view(p.Hkv, G, 1) * far
+        w = x.softmax(-1)
+        out.append(torch.einsum("hgj,hjd->hgd", w, v).reshape(p.Hq, p.D))
+        size.append(torch.einsum("hgj,hjd->hgd", w, v.abs()).reshape(p.Hq, p.D))
+    return torch.stack(out), torch.stack(size)
+
+
+PROMPTS = [
+    # Hq, Hkv, D, B, sequences, the longest context, the most new tokens: enough of them for the prefill kernel's items
+    (32, 8, 128, 16, 24, 300, 131),
+    (16, 16, 64, 8, 12, 700, 700),
+    (8, 8, 128, 32, 20, 900, 300),
+    (64, 8, 128, 8, 16, 260, 100),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B,S,longest,most", PROMPTS)
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("cap,alibi,scaled", [(0.0, False, False), (3.0, False, False), (20.0, True, False), (0.0, True, True),
+                                              (30.0, False, True), (0.0, False, True)])
+def test_prompts_equal_the_definition(Hq, Hkv, D, B, S, longest, most, mask, cap, alibi, scaled):
+    """Tolerances as Problem.check's, with the largest |q| . |k| bounded by the products of the rows' sums and largest elements."""
+    if scaled and D != 128:
+        pytest.skip("E4M3 caches have heads of 128")
+    rng = np.random.default_rng(S + most)
+    ctxs = [int(c) for c in rng.integers(1, longest + 1, S)]
+    ctxs[0], ctxs[1] = longest, 1
+    news = [min(c, int(n)) for c, n in zip(ctxs, rng.integers(1, most + 1, S))]
+    news[0] = most
+    p = Problem(Hq + S, Hq, Hkv, D, B, ctxs, news, mask, scaled=scaled, gap=1, cap=cap, alibi=alibi)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = p.run(status=st)
+    assert st.item() == 0
+    assert torch.isnan(out[0]).all() and torch.isnan(out[-1]).all()
+    take = sorted({1, 2, int(p.start[1]) - 1, int(p.start[1]), int(p.start[-1]) - 1} | set(rng.integers(1, int(p.start[-1]), 60).tolist()))
+    want, weight = _dense(p, take)
+    kd, vd = (Q.dequantize_scaled(c, s) if scaled else A.bf16_to_f64(c) for c, s in ((p.kc, p.ks), (p.vc, p.vs)))
+    qa = p.q[take].double().cuda().abs()
+    size = (qa.sum(-1) * float(np.nanmax(np.abs(kd))) * p.scale)[..., None]
+    bias = 0.0 if p.slopes is None else torch.from_numpy(p.slopes).double().cuda()[:, None] * longest
+    off = ((2.0 ** -11 if scaled else 0.0) + 128 * 2.0 ** -24) * size + 2.0 ** -20 * size.clamp(max=cap) + 2.0 ** -21 * cap + \
+        2.0 ** -20 * bias + 2.0 ** -22 * size
+    tol = 2 * (off + 2.0 ** -11) * weight * 2 + 2.0 ** -24 * float(np.nanmax(np.abs(vd)))
+    got = out[take].double()
+    assert ((got - want).abs() <= tol).all(), (got - want).abs().max()
+    # and far within it on the whole: weights' roundings are as often up as down
+    assert (got - want).norm() <= 2.0 ** -9 * weight.norm()
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_values_that_are_not_finite_in_prompts(scaled, out_dtype):
+    S, n = 24, 131
+    p = Problem(1, 32, 8, 128, 16, [300] * S, [n] * S, "window", scaled=scaled)
+    p.visible[:, 0], p.visible[:, 1] = 100, 200
+    clean = p.run(out_dtype)
+    bad = 0x7F if scaled else 0xFF80                               # NaN, or an infinity
+    for j in list(range(0, 100, 9)) + [99, 200, 201, 255, 299]:
+        for c in (p.kc, p.vc):
+            c[p.tables[:, j // 16], :, j % 16] = bad
+    assert torch.equal(p.run(out_dtype), clean)
+    p = Problem(1, 32, 8, 128, 16, [300] * S, [n] * S, "window", scaled=scaled)
+    p.visible[:, 0], p.visible[:, 1] = 100, 200
+    p.visible[::2, 1] = 250
+    before = p.run(out_dtype)
+    p.vc[p.tables[3, 220 // 16], 1, 220 % 16, 5] = bad             # seen by the even tokens of one sequence, in one KV head
+    after = p.run(out_dtype)
+    got, want = ~torch.isfinite(after), torch.zeros(after.shape, dtype=torch.bool, device="cuda")
+    rows = torch.arange(3 * n, 4 * n, device="cuda")
+    want[rows[rows % 2 == 0], 4:8, 5] = True
+    assert torch.equal(got, want) and torch.equal(after[~got], before[~got])
+    if not scaled:                                                 # and values past fp16's range beside it
+        p.vc[p.tables[3, 150 // 16], 1, 150 % 16, 7] = 0x4880      # 2^18
+        wide = p.run(out_dtype)
+        assert torch.equal(~torch.isfinite(wide), want)
+        off = (wide[3 * n:4 * n, 4:8, 8:].float() - before[3 * n:4 * n, 4:8, 8:].float()).abs().max()
+        assert off <= 2 * 2.0 ** -10 * 5 + 2.0 ** -7 * before.abs().max() * (out_dtype == torch.bfloat16)   # (weights in two terms instead of f16)
 
 
 @pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
