@@ -149,14 +149,17 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
         !pa_host::cache_view(&mv, v_cache, cache_rows, d_head, f8 ? 1 : 2, box))
         return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const ShapedArgs& shaped = a;
+    const auto launch = [&](const auto& args) {
+        if (f8 && all_rows <= 8) return launch_multi<128, true, true>(split.warps, mk, mv, args, split.grid, st);
+        return f8              ? launch_multi<128, true>(split.warps, mk, mv, args, split.grid, st)
+               : d_head == 128 ? launch_multi<128, false>(split.warps, mk, mv, args, split.grid, st)
+                               : launch_multi<64, false>(split.warps, mk, mv, args, split.grid, st);
+    };
     int rc;
     if (wide)
         rc = launch_shaped_wide(unit, d_head, f8, q, block_size, mk, mv, a, split.grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     else
-        rc = f8 ? launch_multi<128, true>(split.warps, mk, mv, shaped, split.grid, st)
-             : d_head == 128 ? launch_multi<128, false>(split.warps, mk, mv, shaped, split.grid, st)
-                             : launch_multi<64, false>(split.warps, mk, mv, shaped, split.grid, st);
+        rc = a.cap_inv != 0.f || a.slopes ? launch(a) : launch(static_cast<const ShapedArgs&>(a));
     if (rc != PA_OK || split.direct) return rc;
     return launch_merge(a, unit, d_head, split.units, split.grid, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -102,11 +102,16 @@ struct State {
 // into the warp's state.  qr: the rows of q as A operands; c[h]: score factor
 // of rows g + 8 h.  scales (shaped, E4M3): the scale bytes of K and V of the
 // tile's first 8 positions, then of the others.
-template <int D, bool F8, class Args>
+// kEight: no unit has more than 8 rows, so rows 8 .. 15 of the matrix instructions stay empty and
+// their softmax is left out.  Only block-scaled caches have this form, whose decodes the instructions
+// issued bound (64 decodes over mixed lengths 68.2 -> 63.1 us, 64 x 4096 105.7 -> 97.7); of bf16
+// caches the reads bound them.
+template <int D, bool F8, class Args, bool kEight>
 __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const Args& a,
                                           const typename Args::Unit& u, int lane, const uint32_t (&qr)[D / 16][4],
                                           const Shape* shape, uint32_t scales, bool masked) {
     constexpr bool kShaped = Args::kShaped;
+    constexpr int kH = kEight ? 1 : 2;
     constexpr int kSlabBytes = kTile * 128, kSteps = D / 16;
     const int g = lane >> 2, t4 = lane & 3;
     // ldmatrix addresses.  K as B operand: keys (lane & 7) + 8 (lane >> 4), chunk + (lane >> 3 & 1);
@@ -144,27 +149,28 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) f[n][h] = kShaped && F8 ? fmaxf(c[h] * scale_of(scales >> (16 * n) & 0xff), 1e-37f) : c[h];   // never 0: masked scores stay -inf
+        for (int h = 0; h < kH; ++h) f[n][h] = kShaped && F8 ? fmaxf(c[h] * scale_of(scales >> (16 * n) & 0xff), 1e-37f) : c[h];   // never 0: masked scores stay -inf
     if constexpr (kShaped) {
-        if (a.cap_inv != 0.f || a.slopes) {            // scores in units of log2 from here on
+        if constexpr (Args::kCurved) {                 // scores in units of log2 from here on
             const float slope[2] = {shape[g].slope, shape[g + 8].slope};
             const int at[2] = {shape[g].pos, shape[g + 8].pos};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2 * kH; ++e) {
                     s[n][e] *= f[n][e >> 1];
                     if (a.cap_inv != 0.f) s[n][e] = pa::capped(s[n][e], a.cap_log2, a.cap_inv);
                     if (a.slopes) s[n][e] -= slope[e >> 1] * (float)abs(at[e >> 1] - (t0 + 8 * n + 2 * t4 + (e & 1)));
                 }
-            f[0][0] = f[0][1] = f[1][0] = f[1][1] = 1.f;
+#pragma unroll
+            for (int h = 0; h < kH; ++h) f[0][h] = f[1][h] = 1.f;
         }
         if (masked) {
             const int lo[2] = {shape[g].lo, shape[g + 8].lo}, hi[2] = {shape[g].hi, shape[g + 8].hi};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2 * kH; ++e) {
                     const int pos = t0 + 8 * n + 2 * t4 + (e & 1);
                     if (pos < lo[e >> 1] || pos >= hi[e >> 1]) s[n][e] = -INFINITY;
                 }
@@ -180,7 +186,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
 #pragma unroll
                 for (int d = 0; d < D / 8; ++d)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st.acc[d][e] *= less;
+                    for (int e = 0; e < 2 * kH; ++e) st.acc[d][e] *= less;
             }
             by[0] *= st.inv;
             by[1] *= st.inv;
@@ -195,7 +201,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
     // how far the tile's scores rise above the running maxima
     float over = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kH; ++h) {
         if constexpr (kShaped && F8) {
             over = fmaxf(over, fmaxf(fmaf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), f[0][h], -st.m[h]),
                                      fmaf(fmaxf(s[1][2 * h], s[1][2 * h + 1]), f[1][h], -st.m[h])));
@@ -206,7 +212,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
     }
     if (__any_sync(0xffffffffu, over > kRaise)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kH; ++h) {
             float top = kShaped && F8 ? fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]) * f[0][h], fmaxf(s[1][2 * h], s[1][2 * h + 1]) * f[1][h])
                                       : fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -223,9 +229,9 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
         }
     }
     // weights as the A operand: bf16 in two terms (a relative 2^-16), f16 times 2^7 (2^-11)
-    uint32_t ph[4], pl[4];
+    uint32_t ph[4] = {0, 0, 0, 0}, pl[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kH; ++h)
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const float p0 = pa::exp2_approx(fmaf(s[n][2 * h], f[n][h], -st.m[h]));
@@ -286,7 +292,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
     }
 }
 
-template <int D, bool F8, int kWarps, class Args>
+template <int D, bool F8, int kWarps, class Args, bool kEight>
 __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
     multi_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a) {
     using G = Geo<D, F8, kWarps>;
@@ -498,6 +504,11 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
         bool landed = true;
 #pragma unroll 1
         for (int k = 0; k < len; ++k) {
+            uint32_t tile_scales = 0;
+            if constexpr (kScaled) {
+                if (k && (k & 31) == 0) scales = scales_next;
+                tile_scales = __shfl_sync(0xffffffffu, scales, k & 31);
+            }
             const int at = used + k, stage = at % kStages;
             if (!__all_sync(0xffffffffu, pa::mbar_wait_bounded(&wfull[stage], (at / kStages) & 1, kMaxProbes))) {
                 // give up: nothing more is issued, and the copies in flight are waited for, each within the limit
@@ -510,11 +521,6 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
                 break;
             }
             const int t0 = base + k * kStep;
-            uint32_t tile_scales = 0;
-            if constexpr (kScaled) {
-                if (k && (k & 31) == 0) scales = scales_next;
-                tile_scales = __shfl_sync(0xffffffffu, scales, k & 31);
-            }
             if (t0 < ctx) {
                 const uint32_t ks = stage_at(stage);
                 const bool some = kShaped ? t0 < seen_lo || t0 + kTile > seen_hi : t0 + kTile > u.first;
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
                         unfinite[nth & 1] = 1;
                     __syncwarp();
                 }
-                fold_tile<D, F8>(st, ks, ks + G::kTileBytes, c, t0, a, u, lane, qr, shape, tile_scales, some || blind);
+                fold_tile<D, F8, Args, kEight>(st, ks, ks + G::kTileBytes, c, t0, a, u, lane, qr, shape, tile_scales, some || blind);
             }
             __syncwarp();
             if (k + kStages < len) issue(u, k + kStages);
@@ -712,20 +718,20 @@ inline Split split_work(bool f8, bool wide, long long all_rows, int num_seqs, in
     return s;
 }
 
-template <int D, bool F8, int kWarps, class Args>
+template <int D, bool F8, int kWarps, bool kEight, class Args>
 int launch_multi(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int grid, cudaStream_t st) {
     static int attr[64] = {0};
     constexpr int kSmem = Geo<D, F8, kWarps>::kSmem;
-    if (pa_host::ensure_smem_attr(multi_kernel<D, F8, kWarps, Args>, kSmem, attr) != cudaSuccess) return PA_ERR_CUDA;
-    return pa_host::launch_dependent(multi_kernel<D, F8, kWarps, Args>, dim3(grid), dim3(32 * kWarps), kSmem, st, mk, mv, a) ==
+    if (pa_host::ensure_smem_attr(multi_kernel<D, F8, kWarps, Args, kEight>, kSmem, attr) != cudaSuccess) return PA_ERR_CUDA;
+    return pa_host::launch_dependent(multi_kernel<D, F8, kWarps, Args, kEight>, dim3(grid), dim3(32 * kWarps), kSmem, st, mk, mv, a) ==
                    cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
 
-template <int D, bool F8, class Args>
+template <int D, bool F8, bool kEight = false, class Args>
 int launch_multi(int warps, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int grid, cudaStream_t st) {
-    return warps == 12 ? launch_multi<D, F8, 12>(mk, mv, a, grid, st) : launch_multi<D, F8, 4>(mk, mv, a, grid, st);
+    return warps == 12 ? launch_multi<D, F8, 12, kEight>(mk, mv, a, grid, st) : launch_multi<D, F8, 4, kEight>(mk, mv, a, grid, st);
 }
 
 }  // namespace
