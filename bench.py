@@ -53,7 +53,7 @@ COMMON_HEADER = os.path.join(ROOT, "paged_kv_cache_124_gb300", "csrc", "pa_commo
 PREFILL_PROFILE = os.path.join(ROOT, "profiles", "prefill_kernel_prefill_prompts_8b.md")
 CACHE_OPS_PROFILE = os.path.join(ROOT, "profiles", "copy_blocks_kernel_cache_ops_8b.md")
 CACHE_OPS_SOURCE = os.path.join(ROOT, "paged_kv_cache_124_gb300", "csrc", "pa_cache_ops.cu")
-PREFILL_SOURCE = os.path.join(ROOT, "paged_kv_cache_124_gb300", "csrc", "pa_prefill.cu")
+PREFILL_SOURCE = os.path.join(ROOT, "paged_kv_cache_124_gb300", "csrc", "pa_prefill.cuh")
 
 # NVTX range around each arm's K timed steps (an ncu launch list can be
 # limited to it with --nvtx --nvtx-include "timed_steps/")
