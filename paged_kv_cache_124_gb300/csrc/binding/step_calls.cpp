@@ -111,20 +111,23 @@ class Call {
 
     // A sequence of at most 64 small integers (bytes serve), its length in `n`.
     void small_ints(int i, const char* name, int8_t (&to)[64], int& n) const {
-        PyObject* fast = PySequence_Fast(args_[i], "");
-        if (!fast) {
+        PyObject* all = PySequence_Tuple(args_[i]);
+        if (!all) {
             PyErr_Clear();
             refuse(PyExc_TypeError, name, "must be a sequence of integers");
         }
-        const Py_ssize_t size = PySequence_Fast_GET_SIZE(fast);
-        bool fits = size <= 64;
-        for (Py_ssize_t k = 0; fits && k < size; ++k) {
-            const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(fast, k));
-            fits = !(v == -1 && PyErr_Occurred()) && v >= -128 && v < 128;
-            if (fits) to[k] = static_cast<int8_t>(v);
+        const Py_ssize_t size = PyTuple_GET_SIZE(all);
+        bool whole = true, fits = size <= 64;
+        for (Py_ssize_t k = 0; whole && fits && k < size; ++k) {
+            int overflow = 0;
+            const long v = PyLong_AsLongAndOverflow(PyTuple_GET_ITEM(all, k), &overflow);
+            whole = !PyErr_Occurred();
+            fits = overflow == 0 && v >= -128 && v < 128;
+            if (whole && fits) to[k] = static_cast<int8_t>(v);
         }
-        Py_DECREF(fast);
+        Py_DECREF(all);
         PyErr_Clear();
+        if (!whole) refuse(PyExc_TypeError, name, "must be a sequence of integers");
         if (!fits) refuse(PyExc_ValueError, name, "must be at most 64 small integers");
         n = static_cast<int>(size);
     }

@@ -487,3 +487,87 @@ def test_a_step_planned_written_and_attended():
         want = A.paged_shaped(to_bits(q_out.cpu()), kd, vd, h(bt), h(start), h(ctx), D ** -0.5, B, h(vis), 30.0)
         # norm-1 rows times sqrt(D): |q| |k| scale <= sqrt(D); q to f16, weights to f16, both sides of the quotient
         assert np.abs(out_to_f64(out) - want).max() <= 4 * (2.0 ** -11 * (D ** 0.5 + 1)) * np.nanmax(np.abs(vd))
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("most", [1, 20, 300])
+def test_two_calls_at_once(scaled, most):
+    """Two graphs of their own workspaces, replayed side by side on two streams."""
+    problems = [Problem(11 + i, 8, 2, 128, 16, [900 + i, 400], [most, max(1, most // 3)], "window", scaled=scaled, cap=5.0 * i)
+                for i in range(2)]
+    want = [p.run() for p in problems]
+    dev = lambda a: None if a is None else torch.from_numpy(a).cuda()  # noqa: E731
+    graphs, outs, held = [], [], []
+    for p, w in zip(problems, want):
+        p.check(w)
+        put = dev if scaled else from_bits
+        args = [p.q.cuda(), put(p.kc), put(p.vc), dev(p.tables), dev(p.start), dev(p.ctx), p.most, 16, p.scale, 8, 2, 128, 901]
+        kw = dict(visible=dev(p.visible), softcap=p.cap, k_scales=dev(p.ks), v_scales=dev(p.vs),
+                  workspace=api.attend_workspace(2, p.most, p.tables.shape[1], 16, 8, 2, 128, scaled))
+        out = torch.full_like(w, float("nan"))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            api.pa_attend(out, *args, **kw)
+        graphs.append(g)
+        outs.append(out)
+        held.append((args, kw))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)
+
+
+def test_tensors_of_wrong_type_shape_place_or_layout_are_refused():
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    b = lambda *s: z(*s, dt=torch.bfloat16)  # noqa: E731
+    u = lambda *s: z(*s, dt=torch.uint8)  # noqa: E731
+    f = lambda *s: z(*s, dt=torch.float32)  # noqa: E731
+    attend = dict(out=b(3, 4, 64), q=b(3, 4, 64), k_cache=b(2, 2, 16, 64), v_cache=b(2, 2, 16, 64), block_tables=z(1, 2),
+                  query_start=z(2), context_lens=z(1), max_query_len=3, block_size=16, scale=0.125, n_q_heads=4,
+                  n_kv_heads=2, d_head=64, max_context_len=32)
+    scaled = dict(attend, out=b(3, 4, 128), q=b(3, 4, 128), k_cache=u(2, 2, 16, 128), v_cache=u(2, 2, 16, 128), d_head=128,
+                  k_scales=u(2, 2), v_scales=u(2, 2))
+    mrope = dict(q_out=b(3, 4, 64), k_cache=b(2, 2, 16, 64), v_cache=b(2, 2, 16, 64), q=b(3, 4, 64), k=b(3, 2, 64),
+                 v=b(3, 2, 64), positions=z(2, 3), axes=[0, 1] * 16, slot_mapping=z(3).long() - 1, cos_sin=f(9, 64))
+    codes = dict(k_cache=u(2, 2, 16, 64), v_cache=u(2, 2, 16, 64), k_scales=u(2, 2), v_scales=u(2, 2))
+    rope = dict(mrope, **codes)
+    append = dict(codes, k=b(3, 2, 64), v=b(3, 2, 64), slot_mapping=z(3).long() - 1)
+    for fn, good, cases in (
+            (api.pa_attend, attend, [
+                (dict(out=z(3, 4, 64)), TypeError, "out must be bfloat16"), (dict(q=b(3, 2, 64)), ValueError, "q must be"),
+                (dict(q=b(3, 64, 4).transpose(1, 2)), ValueError, "q must be contiguous"),
+                (dict(visible=z(3)), ValueError, "visible must be"), (dict(visible=z(3, 2).long()), TypeError, "visible must be"),
+                (dict(visible=z(2, 3).t()), ValueError, "visible must be contiguous"),
+                (dict(slopes=f(2)), ValueError, "slopes must be"), (dict(slopes=b(4)), TypeError, "slopes must be"),
+                (dict(slopes=f(4).cpu()), ValueError, "slopes must be a CUDA tensor"), (dict(softcap="x"), TypeError, None),
+                (dict(k_scales=u(2, 2)), ValueError, "go together"),
+                (dict(k_scales=u(2, 2), v_scales=u(2, 2)), TypeError, "k_cache must be torch.uint8"),
+                (dict(workspace=z(16)), TypeError, "workspace must be torch.uint8"),
+                (dict(workspace=u(16)), api.PAError, None)]),
+            (api.pa_attend, scaled, [
+                (dict(k_cache=b(2, 2, 16, 128)), TypeError, "k_cache must be torch.uint8"),
+                (dict(k_scales=u(2)), ValueError, "k_scales must be"), (dict(v_scales=f(2, 2)), TypeError, "v_scales must be"),
+                (dict(v_scales=u(2, 4)[:, ::2]), ValueError, "v_scales must be contiguous")]),
+            (api.pa_qk_norm_mrope_cache, mrope, [
+                (dict(positions=z(3)), ValueError, "positions must"), (dict(positions=z(2, 4)), ValueError, "positions must be"),
+                (dict(axes=[0] * 31), ValueError, "axes must have"), (dict(axes=[0, 300] * 16), ValueError, None),
+                (dict(axes="x" * 32), TypeError, None), (dict(axes=[2, 1] * 16), api.PAError, None),
+                (dict(axes=None), TypeError, "axes must be"), (dict(k_scale=0.1), ValueError, "go together")]),
+            (api.pa_qk_norm_rope_cache_scaled, rope, [
+                (dict(k_cache=b(2, 2, 16, 64)), TypeError, "k_cache must be torch.uint8"),
+                (dict(axes=None), ValueError, "positions must"), (dict(v_scales=u(1, 2)), ValueError, "v_scales must be"),
+                (dict(v_scales=None), TypeError, "v_scales must be")]),
+            (api.pa_reshape_and_cache_scaled, append, [
+                (dict(k=b(3, 4, 64)), ValueError, "k must be"), (dict(v=b(4, 2, 64)), ValueError, "v must be"),
+                (dict(slot_mapping=z(3)), TypeError, "slot_mapping must be"), (dict(k_scales=None), TypeError, "k_scales must be"),
+                (dict(v_cache=u(2, 2, 64, 16).transpose(2, 3)), ValueError, "v_cache must be contiguous")])):
+        assert fn(**good) == api.PA_OK
+        for change, error, text in cases:
+            with pytest.raises(error, match=text):
+                fn(**dict(good, **change))
+    torch.cuda.synchronize()
