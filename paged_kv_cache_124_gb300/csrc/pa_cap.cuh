@@ -18,40 +18,68 @@ __device__ __forceinline__ float capped(float x, float cap_log2, float cap_inv) 
     return cap_log2 * (fabsf(u) < 0.3f ? u * p : fmaf(-2.f, r, 1.f));
 }
 
-// n scores s (times c2; cap_inv is 1 / cap_log2).  Where all of a warp's are
+// Two floats in a register pair: both of x; a b; a b + c.
+__device__ __forceinline__ uint64_t pair_of(float x) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// The largest magnitude of s (of NaN none).
+template <int n>
+__device__ __forceinline__ float largest(const float (&s)[n]) {
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < n; i += 2)
+        asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %1;\n\tabs.f32 y, %2;\n\tmax.f32 %0, %0, x, y;\n\t}"
+            : "+f"(top[i / 2 & 3])
+            : "f"(s[i]), "f"(s[i + 1]));
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+// The cap within a quarter of it, cap tanh(c2 s / cap) = s p(s^2): tanh(u) / u
+// fitted on [0, 0.25] with even ripple (relative 4e-7) by a polynomial in u^2,
+// the scales of u folded into its coefficients.
+struct NearCap {
+    float q0, q1, q2;
+    __device__ __forceinline__ NearCap(float c2, float cap_inv) {
+        const float by = c2 * cap_inv, w = by * by;
+        q0 = c2 * 0.999999604f;
+        q1 = c2 * w * -0.333219082f;
+        q2 = c2 * w * w * 0.128416134f;
+    }
+    __device__ __forceinline__ float operator()(float s) const {
+        const float v = s * s;
+        return s * fmaf(fmaf(q2, v, q1), v, q0);
+    }
+};
+
+// n scores s (times c2; cap_inv is 1 / cap_log2), the largest of which is top.  Where all of a warp's are
 // within half of the cap, as nearly always, by a polynomial in s^2 alone, in
 // packed pairs: tanh(u) / u fitted on [0, 0.5] with even ripple (relative
 // 6e-7), the scales of u folded into its coefficients.
 template <int n>
-__device__ __forceinline__ void cap_scores(float (&s)[n], float c2, float cap_log2, float cap_inv) {
-    float top[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < n; i += 2) asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %1;\n\tabs.f32 y, %2;\n\tmax.f32 %0, %0, x, y;\n\t}" : "+f"(top[i / 2 & 3]) : "f"(s[i]), "f"(s[i + 1]));
+__device__ __forceinline__ void cap_scores(float (&s)[n], float top, float c2, float cap_log2, float cap_inv) {
     const float by = c2 * cap_inv, w = by * by;
-    const bool far = !(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(by) < 0.5f);
+    const bool far = !(top * fabsf(by) < 0.5f);
     if (!__any_sync(0xffffffffu, far)) {
-        const auto both = [](float x) {
-            uint64_t r;
-            asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
-            return r;
-        };
-        const auto mul = [](uint64_t a, uint64_t b) {
-            uint64_t d;
-            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-            return d;
-        };
-        const auto fma = [](uint64_t a, uint64_t b, uint64_t c) {
-            uint64_t d;
-            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-            return d;
-        };
-        const uint64_t q0 = both(c2 * 0.999999456f), q1 = both(c2 * w * -0.3332632f), q2 = both(c2 * w * w * 0.131903234f),
-                       q3 = both(c2 * w * w * w * -0.0444030606f);
+        const uint64_t q0 = pair_of(c2 * 0.999999456f), q1 = pair_of(c2 * w * -0.3332632f), q2 = pair_of(c2 * w * w * 0.131903234f),
+                       q3 = pair_of(c2 * w * w * w * -0.0444030606f);
 #pragma unroll
         for (int i = 0; i < n; i += 2) {
             uint64_t x;
             asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(s[i]), "f"(s[i + 1]));
-            const uint64_t v = mul(x, x), y = mul(x, fma(fma(fma(q3, v, q2), v, q1), v, q0));
+            const uint64_t v = pair_mul(x, x), y = pair_mul(x, pair_fma(pair_fma(pair_fma(q3, v, q2), v, q1), v, q0));
             asm("mov.b64 {%0, %1}, %2;" : "=f"(s[i]), "=f"(s[i + 1]) : "l"(y));
         }
         return;

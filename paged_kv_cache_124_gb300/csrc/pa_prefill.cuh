@@ -342,6 +342,30 @@ __device__ __forceinline__ void write_weights(float (&s)[kHalfCols], uint64_t c2
     }
 }
 
+// The same as fp16 weights for scores near zero beside their cap, which go
+// through it here: p = 2^(cap(s) + neg).
+template <int kHalfCols>
+__device__ __forceinline__ void write_capped_weights(const float (&s)[kHalfCols], const pa::NearCap& cap, uint64_t negx2,
+                                                     uint64_t (&lp)[2], uint32_t t_p) {
+    const uint64_t q0 = f32x2(cap.q0, cap.q0), q1 = f32x2(cap.q1, cap.q1), q2 = f32x2(cap.q2, cap.q2);
+#pragma unroll
+    for (int h2 = 0; h2 < 2; ++h2) {
+        uint32_t w[kHalfCols / 4];
+#pragma unroll
+        for (int qq = 0; qq < kHalfCols / 4; ++qq) {
+            const int q = h2 * (kHalfCols / 4) + qq;
+            const uint64_t x = f32x2(s[2 * q], s[2 * q + 1]), v = mul_f32x2(x, x);
+            float x0, x1;
+            f32x2_split(fma_f32x2(x, fma_f32x2(fma_f32x2(q2, v, q1), v, q0), negx2), x0, x1);
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+            lp[q & 1] = add_f32x2(lp[q & 1], f32x2(x0, x1));
+            w[qq] = pack_f16_rn(x0, x1);
+        }
+        tmem_st16u(t_p + h2 * (kHalfCols / 4), w);
+    }
+}
+
 // --- bounded waits -------------------------------------------------------------
 
 // One thread.  Gives up when another role has aborted or after kMaxProbes
@@ -935,10 +959,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         const int lim = row_lim[x] - j * kKv - hc * kHalfCols;     // valid columns of this half
                         float c2 = c2x[x];
+                        bool near = false;                    // the cap is taken with the weights
                         if constexpr (Args::kCurved) {
                             if (a.cap_inv != 0.f) {
-                                pa::cap_scores<kHalfCols>(s, c2, a.cap_log2, a.cap_inv);
-                                c2 = 1.f;
+                                const float top = pa::largest(s);
+                                near = __all_sync(0xffffffffu, top * fabsf(c2 * a.cap_inv) < 0.25f && lim >= kHalfCols &&
+                                                                   row_lo[x] <= j * kKv + hc * kHalfCols) &&
+                                       !a.slopes && !wide;
+                                if (!near) {
+                                    pa::cap_scores<kHalfCols>(s, top, c2, a.cap_log2, a.cap_inv);
+                                    c2 = 1.f;
+                                }
                             }
                             if (a.slopes) {
                                 // the token's distance to the half's first column
@@ -984,6 +1015,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float mt = fmaxf(max3(mp[0], mp[1], mp[2]),
                                          fmaxf(max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+                        if constexpr (Args::kCurved) {
+                            if (near) {                       // (the cap grows with the score: the largest stays the largest)
+                                mt = pa::NearCap(c2, a.cap_inv)(mt);
+                                c2 = 1.f;
+                            }
+                        }
                         mt = fmaxf(mt, exchange(x, mt, ok));
                         if (!ok) break;
                         const float mts = mt * c2;            // scale > 0: the maximum commutes with it
@@ -1022,7 +1059,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the other 64 columns.
                         const uint64_t c2x2 = f32x2(c2, c2), negx2 = f32x2(neg, neg);
                         uint64_t lp[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};   // independent partial sums
-                        if (!wide)
+                        if constexpr (Args::kCurved)
+                            if (near)
+                                write_capped_weights<kHalfCols>(s, pa::NearCap(c2x[x], a.cap_inv), negx2, lp,
+                                                                t_s + hc * (kHalfCols / 2));
+                        if (near) {
+                        } else if (!wide)
                             write_weights<kHalfCols, false>(s, c2x2, negx2, lp, t_s + hc * (kHalfCols / 2));
                         else
                             write_weights<kHalfCols, true>(s, c2x2, negx2, lp, t_s + hc * (kHalfCols / 2));

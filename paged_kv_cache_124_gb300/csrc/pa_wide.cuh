@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float all = kScaled ? 1.f : c;
                         if (a.cap_inv != 0.f) {
-                            pa::cap_scores<kCols>(s, all, a.cap_log2, a.cap_inv);
+                            pa::cap_scores<kCols>(s, pa::largest(s), all, a.cap_log2, a.cap_inv);
                             all = 1.f;
                         }
                         if (a.slopes) {
