@@ -896,8 +896,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kOCols = D / 2;                     // output columns per thread
         int ns[2] = {0, 0}, nred[2] = {0, 0}, nod[2] = {0, 0};
         // Post this half's value for row r of tile x and read the other half's.
-        auto exchange = [&](int x, float v, bool& ok_) {
-            const int phase = nred[x]++;
+        auto exchange = [&](int x, float v, int& done, bool& ok_) {
+            const int phase = done++;
             float* slot = red + (((x * 2 + (phase & 1)) * 2) * kRows);
             slot[hc * kRows + r] = v;
             pa::mbar_arrive(&bars->red[x]);
@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&bars->item_empty[slot]);
             if (it.seq < 0) break;
-            const int nt[2] = {it.nt0, it.nt1};
+            int nt[2] = {it.nt0, it.nt1};
             // shaped: finite before a row has seen anything, as whole tiles may be masked
             constexpr float kNothing = kShaped ? -3.0e38f : -INFINITY;
             float m_used[2] = {kNothing, kNothing}, l[2] = {0.f, 0.f};
@@ -940,15 +940,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* fmt = a.v_fmt + (size_t)(it.h * a.num_seqs + it.seq) * a.t_slot + (kShaped ? it.base / kKv : 0);
             // The item's tiles, in one of two forms: all V tiles fp16 (the
             // common case, with no per-tile format check) or some bf16.
+            // The turns of the two row tiles are one loop, in which the tile whose
+            // turn it is stands first: as two copies of its body the forms with a
+            // cap or a bias miss the instruction cache (EEE).
+            constexpr int kUnrolled = 1;
+            const auto swap = [](auto& two) {
+                const auto first = two[0];
+                two[0] = two[1];
+                two[1] = first;
+            };
             auto run_tiles = [&](auto may_be_wide) {
                 constexpr bool kMayBeWide = decltype(may_be_wide)::value;
-                for (int j = 0; ok && j < it.n_tiles; ++j) {
+#pragma unroll (kUnrolled)
+                for (int turn = 0; ok && turn < 2 * it.n_tiles; ++turn) {
+                    const int j = turn >> 1, x = turn & 1;
                     const int wide = kMayBeWide ? (kShaped ? fmt[j] & 1 : fmt[j]) : 0;   // V tile j staged as fp16 (0) or bf16 (1)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (j >= nt[x]) continue;
-                        ok = wait_warp(&bars->s_full[x], ns[x] & 1, bars, a.status);
-                        ++ns[x];
+                    if (j < nt[0]) {
+                        ok = wait_warp(&bars->s_full[x], ns[0] & 1, bars, a.status);
+                        ++ns[0];
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t t_s = t_lane + kTmemS0 + x * 128;
@@ -957,14 +966,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int cc = 0; cc < kHalfCols / 32; ++cc)
                             tmem_ld32(t_s + hc * kHalfCols + cc * 32, s + cc * 32);
                         tmem_wait_ld();
-                        const int lim = row_lim[x] - j * kKv - hc * kHalfCols;     // valid columns of this half
-                        float c2 = c2x[x];
+                        const int lim = row_lim[0] - j * kKv - hc * kHalfCols;     // valid columns of this half
+                        float c2 = c2x[0];
                         bool near = false;                    // the cap is taken with the weights
                         if constexpr (Args::kCurved) {
                             if (a.cap_inv != 0.f) {
                                 const float top = pa::largest(s);
                                 near = __all_sync(0xffffffffu, top * fabsf(c2 * a.cap_inv) < 0.25f && lim >= kHalfCols &&
-                                                                   row_lo[x] <= j * kKv + hc * kHalfCols) &&
+                                                                   row_lo[0] <= j * kKv + hc * kHalfCols) &&
                                        !a.slopes && !wide;
                                 if (!near) {
                                     pa::cap_scores<kHalfCols>(s, top, c2, a.cap_log2, a.cap_inv);
@@ -993,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         if constexpr (kShaped) {
-                            const int from = row_lo[x] - j * kKv - hc * kHalfCols;
+                            const int from = row_lo[0] - j * kKv - hc * kHalfCols;
                             if (from > 0 || lim < kHalfCols) {
 #pragma unroll
                                 for (int cc = 0; cc < kHalfCols; ++cc) s[cc] = cc >= from && cc < lim ? s[cc] : -INFINITY;
@@ -1021,12 +1030,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 c2 = 1.f;
                             }
                         }
-                        mt = fmaxf(mt, exchange(x, mt, ok));
+                        mt = fmaxf(mt, exchange(x, mt, nred[0], ok));
                         if (!ok) break;
                         const float mts = mt * c2;            // scale > 0: the maximum commutes with it
-                        const bool rescale = mts > m_used[x] + kRescaleThreshold;
-                        const float m_new = rescale ? mts : m_used[x];
-                        const float alpha = rescale ? fast_exp2(m_used[x] - m_new) : 1.f;   // exp2(-inf) = 0 at first
+                        const bool rescale = mts > m_used[0] + kRescaleThreshold;
+                        const float m_new = rescale ? mts : m_used[0];
+                        const float alpha = rescale ? fast_exp2(m_used[0] - m_new) : 1.f;   // exp2(-inf) = 0 at first
                         if (j >= 1 && __any_sync(0xffffffffu, rescale)) {
                             // O holds the products of tiles < j (complete: this tile's
                             // scores were issued after them) and not yet this tile's
@@ -1040,13 +1049,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st32(t_o + cc * 32, o);
                             }
                         }
-                        l[x] *= alpha;
-                        m_used[x] = m_new;
+                        l[0] *= alpha;
+                        m_used[0] = m_new;
                         // Weights are p = 2^(s * c2 - m_used + 7): the 2^7 (the sums
                         // carry it too, so it cancels) puts them in [0, 2^15], where
                         // fp16 rounds every weight above 2^-21 of the row maximum to
                         // a relative 2^-11.
-                        const float neg = kWeightShift - m_used[x];
+                        const float neg = kWeightShift - m_used[0];
                         // Column pairs in packed f32x2 arithmetic: one FMA and one
                         // add per two weights.  The weights go to the tensor cores
                         // as fp16, written over the first 64 columns of S.  For a
@@ -1061,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint64_t lp[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};   // independent partial sums
                         if constexpr (Args::kCurved)
                             if (near)
-                                write_capped_weights<kHalfCols>(s, pa::NearCap(c2x[x], a.cap_inv), negx2, lp,
+                                write_capped_weights<kHalfCols>(s, pa::NearCap(c2x[0], a.cap_inv), negx2, lp,
                                                                 t_s + hc * (kHalfCols / 2));
                         if (near) {
                         } else if (!wide)
@@ -1074,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float l0, l1, l2, l3;
                         f32x2_split(lp[0], l0, l1);
                         f32x2_split(lp[1], l2, l3);
-                        l[x] += (l0 + l1) + (l2 + l3);
+                        l[0] += (l0 + l1) + (l2 + l3);
                         if (wide) {
 #pragma unroll
                             for (int h2 = 0; h2 < 2; ++h2) {
@@ -1097,6 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pa::mbar_arrive(&bars->plo_full[x]);
                         }
                     }
+                    swap(nt), swap(ns), swap(nred), swap(m_used), swap(l), swap(row_lim), swap(row_lo);
                 }
             };
             if (!kNeverWide && (kShaped ? it.wide & 1 : it.wide))
@@ -1106,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 2 && ok; ++x) {
                 if (nt[x] == 0) continue;
-                const float l_all = l[x] + exchange(x, l[x], ok);
+                const float l_all = l[x] + exchange(x, l[x], nred[x], ok);
                 if (ok) ok = wait_warp(&bars->o_done[x], nod[x] & 1, bars, a.status);
                 ++nod[x];
                 if (!ok) break;
