@@ -941,9 +941,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The item's tiles, in one of two forms: all V tiles fp16 (the
             // common case, with no per-tile format check) or some bf16.
             // The turns of the two row tiles are one loop, in which the tile whose
-            // turn it is stands first: as two copies of its body the forms with a
-            // cap or a bias miss the instruction cache (EEE).
-            constexpr int kUnrolled = 1;
+            // turn it is stands first: two copies of its body missed the
+            // instruction cache (8 prompts of 2,003 tokens, 32 query heads over
+            // 8: causal 276 us instead of 285, with a cap 380 instead of 413).
             const auto swap = [](auto& two) {
                 const auto first = two[0];
                 two[0] = two[1];
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto run_tiles = [&](auto may_be_wide) {
                 constexpr bool kMayBeWide = decltype(may_be_wide)::value;
-#pragma unroll (kUnrolled)
+#pragma unroll 1
                 for (int turn = 0; ok && turn < 2 * it.n_tiles; ++turn) {
                     const int j = turn >> 1, x = turn & 1;
                     const int wide = kMayBeWide ? (kShaped ? fmt[j] & 1 : fmt[j]) : 0;   // V tile j staged as fp16 (0) or bf16 (1)
