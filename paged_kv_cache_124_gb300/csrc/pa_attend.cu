@@ -13,9 +13,10 @@
 //
 // What the shape costs beside the plain kernels: with few rows, arithmetic
 // that the cache's bytes hide (64 decodes of 4096 positions, capped, 169 us,
-// 0.94 of the measured copy rate; block-scaled 107, where a weight and a score
-// take a factor more).  With many, the softmax's instructions bind: 8 prompts
-// of 2003 tokens 300 us causal (285 plain), 373 with a bias, 418 with a cap.
+// 0.94 of the measured copy rate; block-scaled 98, 0.81, against 92 with one
+// scale: a score and a weight take a factor more).  With many, the softmax's
+// instructions bind: 8 prompts of 2003 tokens 291 us causal (275 plain), 372
+// with a bias, 380 with a cap.
 
 #include "pa_attend.cuh"
 #include "pa_multi_rows.cuh"

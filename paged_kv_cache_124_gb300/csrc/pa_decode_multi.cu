@@ -9,9 +9,9 @@
 // "PagedAttention in vLLM: scattered memory, exact attention", sections 10
 // and 11: translation, the online softmax, the exact merge).
 //
-// This file serves up to 16 rows a KV head (and any number with a scale that
-// is not positive, or over a few contexts of one tile); pa_decode_wide.cu
-// takes more.
+// The kernel of pa_multi_rows.cuh serves up to 16 rows a KV head (and any number
+// with a scale that is not positive, or over a few contexts of one tile);
+// pa_decode_wide.cu takes more.
 //
 // What bounds it: each K/V byte is read once for n * G rows, 4 * n * G
 // operations per two bytes, so the cache's bytes bound it.  64 sequences of

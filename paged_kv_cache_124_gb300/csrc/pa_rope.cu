@@ -21,6 +21,12 @@
 // IEEE division for each of their elements, in 145 us, 0.74 for 724 MB.  With
 // few, every head has threads of its own: 4 tokens in 2.0 us, 250 of 256 (E4M3)
 // in 3.5 us.
+//
+// By several axes (pa_qk_norm_mrope_cache): each pair's angle is that of the
+// position on its axis, so a thread's angles come from up to three rows of the
+// table for a token instead of one, chosen by constants of the call.  5,003
+// tokens of 32 + 2 x 4 heads of 128 take 21.6 us, 0.72 of the measured copy
+// rate for 105 MB; 6 tokens 2.3 us.
 
 #include "pa_rope.cuh"
 

@@ -571,3 +571,10 @@ def test_tensors_of_wrong_type_shape_place_or_layout_are_refused():
             with pytest.raises(error, match=text):
                 fn(**dict(good, **change))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("scaled,lengths", [(False, range(1000, 1100)), (True, range(1100, 1200)), (False, [1500] * 99 + [3])])
+def test_one_unit_for_most_blocks(scaled, lengths):
+    """400 units of nearly one length, too long for a rule by length; and one that is much shorter."""
+    p = Problem(21, 4, 4, 128, 16, list(lengths), [1] * 100, scaled=scaled, cap=20.0)
+    p.check(p.run())
