@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restri
     if (!tile_there(a, s, j, ctx)) return;
     const int32_t* table = a.block_tables + (size_t)s * a.max_blocks;
     const size_t row0 = ((size_t)(h * a.num_seqs + s) * a.l_slot + (size_t)j * kKv) * D;
+    const int log2_block = __ffs(a.block_size) - 1;
     uint4 code[2][kPer];
     float scale[2][kPer];
     uint32_t bad = 0;
@@ -124,9 +125,10 @@ __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restri
         code[0][i] = code[1][i] = make_uint4(0, 0, 0, 0);
         scale[0][i] = scale[1][i] = 0.f;
         if (pos < ctx) {
-            const int blk = __ldg(table + pos / a.block_size);
+            const int blk = __ldg(table + (pos >> log2_block));
             if (blk >= 0 && blk < a.num_blocks) {
-                const size_t at = (((size_t)blk * a.n_kv_heads + h) * a.block_size + pos % a.block_size) * kChunksPerRow + c % kChunksPerRow;
+                const size_t at = ((((size_t)blk * a.n_kv_heads + h) << log2_block) + (pos & (a.block_size - 1))) * kChunksPerRow +
+                                  c % kChunksPerRow;
                 code[0][i] = __ldg(k_cache + at);
                 code[1][i] = __ldg(v_cache + at);
                 const int ke = a.k_scales[(size_t)blk * a.n_kv_heads + h], ve = a.v_scales[(size_t)blk * a.n_kv_heads + h];
@@ -159,9 +161,7 @@ __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restri
                 const float lo = x.x * scale[kv][i], hi = x.y * scale[kv][i];
                 f[e] = as_bf16 ? pack_bf16_rn(lo, hi) : pack_f16_rn(lo, hi);
             }
-            const int c = threadIdx.x + 256 * i;
-            dst[2 * c] = make_uint4(f[0], f[1], f[2], f[3]);
-            dst[2 * c + 1] = make_uint4(f[4], f[5], f[6], f[7]);
+            st_global_v8(dst + 2 * (threadIdx.x + 256 * i), f);   // (whole sectors; the workspace is 256-byte aligned)
         }
     }
     if (threadIdx.x == 0) a.v_fmt[(size_t)(h * a.num_seqs + s) * a.t_slot + j] = (wide ? 1 : 0) | (some ? 2 : 0);
