@@ -103,68 +103,70 @@ __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __rest
     if (threadIdx.x == 0) a.v_fmt[(size_t)(h * a.num_seqs + s) * a.t_slot + j] = (wide ? 1 : 0) | (some ? 2 : 0);
 }
 
-// A block-scaled cache's tile: K as bf16, V as fp16 where the blocks' scales are 2^-15 .. 2^7 (the values are
-// multiples of 2^-24 below 2^16 then), else as bf16; all exact.
+// A block-scaled cache's tile: K as bf16 (even blocks of z), V (odd ones) as fp16 where the blocks' scales are 2^-15 ..
+// 2^7 (the values are multiples of 2^-24 below 2^16 then), else as bf16; all exact.
 template <int D>
 __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restrict__ k_cache, const uint4* __restrict__ v_cache,
                                                            uint16_t* k_stage, const ShapedStageArgs a) {
     constexpr int kChunksPerRow = D / 16, kPer = kKv * kChunksPerRow / 256;
-    const int j = blockIdx.x, s = blockIdx.y, h = blockIdx.z;
+    const int j = blockIdx.x, s = blockIdx.y, h = blockIdx.z >> 1;
+    const bool is_v = blockIdx.z & 1;
     int ctx;
     if (!tile_there(a, s, j, ctx)) return;
     const int32_t* table = a.block_tables + (size_t)s * a.max_blocks;
-    const size_t row0 = ((size_t)(h * a.num_seqs + s) * a.l_slot + (size_t)j * kKv) * D;
+    const uint4* cache = is_v ? v_cache : k_cache;
+    const uint8_t* scales = is_v ? a.v_scales : a.k_scales;
     const int log2_block = __ffs(a.block_size) - 1;
-    uint4 code[2][kPer];
-    float scale[2][kPer];
-    uint32_t bad = 0;
+    uint4 code[kPer];
+    float scale[kPer];
     bool narrow = true;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int c = threadIdx.x + 256 * i, pos = j * kKv + c / kChunksPerRow;
-        code[0][i] = code[1][i] = make_uint4(0, 0, 0, 0);
-        scale[0][i] = scale[1][i] = 0.f;
+        code[i] = make_uint4(0, 0, 0, 0);
+        scale[i] = 0.f;
         if (pos < ctx) {
             const int blk = __ldg(table + (pos >> log2_block));
             if (blk >= 0 && blk < a.num_blocks) {
-                const size_t at = ((((size_t)blk * a.n_kv_heads + h) << log2_block) + (pos & (a.block_size - 1))) * kChunksPerRow +
-                                  c % kChunksPerRow;
-                code[0][i] = __ldg(k_cache + at);
-                code[1][i] = __ldg(v_cache + at);
-                const int ke = a.k_scales[(size_t)blk * a.n_kv_heads + h], ve = a.v_scales[(size_t)blk * a.n_kv_heads + h];
-                scale[0][i] = __int_as_float(ke ? ke << 23 : 0x00400000);
-                scale[1][i] = __int_as_float(ve ? ve << 23 : 0x00400000);
-                if (ve && (ve < 112 || ve > 134)) narrow = false;   // (what 2^-127 scales is nothing to any sum)
-            } else {
+                const size_t block = (size_t)blk * a.n_kv_heads + h;
+                code[i] = __ldg(cache + ((block << log2_block) + (pos & (a.block_size - 1))) * kChunksPerRow + c % kChunksPerRow);
+                const int e = scales[block];
+                scale[i] = __int_as_float(e ? e << 23 : 0x00400000);
+                if (e && (e < 112 || e > 134)) narrow = false;   // (what 2^-127 scales is nothing to any sum)
+            } else if (!is_v) {
                 pa::set_status(a.status, PA_DEV_BAD_BLOCK_ID);
             }
         }
-        uint4& v = code[1][i];                                   // NaN, E4M3's only one that is not finite
-        auto nan4 = [](uint32_t w) { return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu; };
-        const uint4 m = make_uint4(nan4(v.x), nan4(v.y), nan4(v.z), nan4(v.w));
-        bad |= m.x | m.y | m.z | m.w;
-        v = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
     }
-    const bool wide = __syncthreads_or(!narrow) != 0, some = __syncthreads_or(bad != 0) != 0;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        uint4* dst = reinterpret_cast<uint4*>((kv ? a.v_stage : k_stage) + row0);
-        const bool as_bf16 = kv == 0 || wide;
+    bool wide = true;
+    if (is_v) {
+        uint32_t bad = 0;
+        auto nan4 = [](uint32_t w) { return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu; };
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const uint32_t w[4] = {code[kv][i].x, code[kv][i].y, code[kv][i].z, code[kv][i].w};
-            uint32_t f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                const float lo = x.x * scale[kv][i], hi = x.y * scale[kv][i];
-                f[e] = as_bf16 ? pack_bf16_rn(lo, hi) : pack_f16_rn(lo, hi);
-            }
-            st_global_v8(dst + 2 * (threadIdx.x + 256 * i), f);   // (whole sectors; the workspace is 256-byte aligned)
+            uint4& v = code[i];                                  // NaN, E4M3's only one that is not finite
+            const uint4 m = make_uint4(nan4(v.x), nan4(v.y), nan4(v.z), nan4(v.w));
+            bad |= m.x | m.y | m.z | m.w;
+            v = make_uint4(v.x & ~m.x, v.y & ~m.y, v.z & ~m.z, v.w & ~m.w);
         }
+        wide = __syncthreads_or(!narrow) != 0;
+        const bool some = __syncthreads_or(bad != 0) != 0;
+        if (threadIdx.x == 0) a.v_fmt[(size_t)(h * a.num_seqs + s) * a.t_slot + j] = (wide ? 1 : 0) | (some ? 2 : 0);
     }
-    if (threadIdx.x == 0) a.v_fmt[(size_t)(h * a.num_seqs + s) * a.t_slot + j] = (wide ? 1 : 0) | (some ? 2 : 0);
+    uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_stage : k_stage) + ((size_t)(h * a.num_seqs + s) * a.l_slot + (size_t)j * kKv) * D);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+        uint32_t f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            const float lo = x.x * scale[i], hi = x.y * scale[i];
+            f[e] = wide ? pack_bf16_rn(lo, hi) : pack_f16_rn(lo, hi);
+        }
+        st_global_v8(dst + 2 * (threadIdx.x + 256 * i), f);      // (whole sectors; the workspace is 256-byte aligned)
+    }
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -177,7 +179,7 @@ int launch_shaped(const Args& a, const ShapedStageArgs& sa, const pa_attend_call
     const auto kernel = prefill_kernel<D, kScaled, Args>;
     if (pa_host::ensure_smem_attr(kernel, PGeo<D>::kSmem, g_smem_done<D, kScaled, Args>) != cudaSuccess)
         return PA_ERR_CUDA;
-    const dim3 sgrid((unsigned)sa.t_slot, (unsigned)sa.num_seqs, (unsigned)sa.n_kv_heads);
+    const dim3 sgrid((unsigned)sa.t_slot, (unsigned)sa.num_seqs, (unsigned)(kScaled ? 2 * sa.n_kv_heads : sa.n_kv_heads));
     cudaError_t e;
     if constexpr (kScaled)
         e = pa_host::launch_dependent(stage_scaled_kernel<D>, sgrid, dim3(256), 0, c.stream, static_cast<const uint4*>(c.k_cache),
@@ -199,7 +201,7 @@ size_t prompt_workspace(int num_seqs, int max_query_len, int max_blocks, int blo
     const int group = n_q_heads / n_kv_heads;
     const double tiles = ((double)max_query_len * group + 2 * kRows - 1) / (2 * kRows);
     const double slots = ((double)max_blocks * block_size + kKv) * num_seqs * n_kv_heads;
-    if (num_seqs > 65535 || n_kv_heads > 65535 || group > kRows || slots > INT_MAX - kKv ||
+    if (num_seqs > 65535 || n_kv_heads > (scaled ? 32767 : 65535) || group > kRows || slots > INT_MAX - kKv ||
         tiles * num_seqs * n_kv_heads > INT_MAX - 4096.0)
         return 0;
     return workspace_layout(num_seqs, max_blocks, block_size, n_kv_heads, d_head, scaled).total + 256;
