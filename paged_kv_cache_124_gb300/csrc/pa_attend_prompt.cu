@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __rest
     int ctx;
     if (!tile_there(a, s, j, ctx)) return;
     const int32_t* table = a.block_tables + (size_t)s * a.max_blocks;
+    const int log2_block = __ffs(a.block_size) - 1;
     uint4 v[kPer];
     uint32_t amax = 0, bad = 0;
 #pragma unroll
@@ -80,12 +81,15 @@ __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __rest
         const int c = threadIdx.x + 256 * i, pos = j * kKv + c / kChunksPerRow;
         v[i] = make_uint4(0, 0, 0, 0);
         if (pos < ctx) {
-            const int blk = __ldg(table + pos / a.block_size);
+            const int blk = __ldg(table + (pos >> log2_block));
             if (blk >= 0 && blk < a.num_blocks)
-                v[i] = __ldg(v_cache + (((size_t)blk * a.n_kv_heads + h) * a.block_size + pos % a.block_size) * kChunksPerRow +
+                v[i] = __ldg(v_cache + ((((size_t)blk * a.n_kv_heads + h) << log2_block) + (pos & (a.block_size - 1))) * kChunksPerRow +
                              c % kChunksPerRow);
             // a bad entry reads zeros; the prefill kernel's K loads flag it
         }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
         const uint4 m = make_uint4(unfinite2(v[i].x), unfinite2(v[i].y), unfinite2(v[i].z), unfinite2(v[i].w));
         bad |= m.x | m.y | m.z | m.w;
         v[i] = make_uint4(v[i].x & ~m.x, v[i].y & ~m.y, v[i].z & ~m.z, v[i].w & ~m.w);
