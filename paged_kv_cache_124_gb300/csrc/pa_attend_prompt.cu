@@ -218,7 +218,7 @@ int launch_prompt(const Call& c) {
     int* sched = reinterpret_cast<int*>(w8 + ws.total);
     const int group = c.n_q_heads / c.n_kv_heads, tq = kRows / group;
     const long long tiles = ((long long)c.max_query_len + 2 * tq - 1) / (2 * tq), items = tiles * c.num_seqs * c.n_kv_heads;
-    CurvedPrefillArgs a{};
+    ShapedPrefillArgs a{};
     a.out = c.out;
     a.out_f32 = c.out_f32;
     a.out_al32 = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;
@@ -273,11 +273,16 @@ int launch_prompt(const Call& c) {
     sa.num_tokens = c.num_tokens;
     sa.sched = sched;
     sa.ctx_cap = c.ctx_cap;
+    const auto with = [&](auto form) {
+        static_cast<ShapedPrefillArgs&>(form) = a;
+        return form;
+    };
     const auto launch = [&](const auto& args) {
         if (scaled) return launch_shaped<128, true>(args, sa, c, reinterpret_cast<uint16_t*>(w8 + ws.k_off), grid);
         return c.d_head == 128 ? launch_shaped<128, false>(args, sa, c, nullptr, grid) : launch_shaped<64, false>(args, sa, c, nullptr, grid);
     };
-    return c.softcap > 0.f || c.slopes ? launch(a) : launch(static_cast<const ShapedPrefillArgs&>(a));
+    if (c.slopes) return launch(with(BiasedPrefillArgs{}));
+    return c.softcap > 0.f ? launch(with(CappedPrefillArgs{})) : launch(a);
 }
 
 }  // namespace pa_attend_calls

@@ -51,7 +51,7 @@ struct PGeo {
 };
 
 struct PrefillArgs {
-    static constexpr bool kShaped = false, kCurved = false;
+    static constexpr bool kShaped = false, kCapped = false, kBiased = false;
     void* out;
     int out_f32;
     int out_al32;         // out is 32-byte aligned: 256-bit stores
@@ -83,16 +83,20 @@ struct PrefillArgs {
 // Scores s become cap tanh(s / cap), less slope |p - j|, over an interval of
 // positions per token (pa_attend).
 struct ShapedPrefillArgs : PrefillArgs {
-    static constexpr bool kShaped = true, kCurved = false;
+    static constexpr bool kShaped = true, kCapped = false, kBiased = false;
     const int2* visible;  // [tokens] positions x .. y - 1 are seen; null: causal
     const float* slopes;  // [query heads], or null
     float cap_log2, cap_inv;   // cap * log2(e) and 1 over it; 0: none
     const void* v_cache;  // for values that are not finite
     int ctx_cap, max_query_len;
 };
-// With a cap or a bias (forms of their own: their code beside the masks' alone cost 15 %).
-struct CurvedPrefillArgs : ShapedPrefillArgs {
-    static constexpr bool kCurved = true;
+// With a cap, and with a bias (and perhaps a cap): forms of their own, since code that a call does not use costs the
+// others instruction fetches (a cap's and a bias's beside the masks' alone 15 %).
+struct CappedPrefillArgs : ShapedPrefillArgs {
+    static constexpr bool kCapped = true;
+};
+struct BiasedPrefillArgs : ShapedPrefillArgs {
+    static constexpr bool kBiased = true;
 };
 
 // One work item: query rows [t0, t0 + 2 tq) of sequence seq's n new tokens
@@ -919,8 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_used[2] = {kNothing, kNothing}, l[2] = {0.f, 0.f};
             int row_lim[2], row_lo[2] = {0, 0};
             float slope = 0.f;                            // times log2(e)
-            if constexpr (Args::kCurved)
-                if (a.slopes) slope = 1.4426950408889634f * a.slopes[it.h * a.group + gq];
+            if constexpr (Args::kBiased) slope = 1.4426950408889634f * a.slopes[it.h * a.group + gq];
             bool valid_row[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -969,37 +972,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int lim = row_lim[0] - j * kKv - hc * kHalfCols;     // valid columns of this half
                         float c2 = c2x[0];
                         bool near = false;                    // the cap is taken with the weights
-                        if constexpr (Args::kCurved) {
-                            if (a.cap_inv != 0.f) {
-                                const float top = pa::largest(s);
-                                near = __all_sync(0xffffffffu, top * fabsf(c2 * a.cap_inv) < 0.25f && lim >= kHalfCols &&
-                                                                   row_lo[0] <= j * kKv + hc * kHalfCols) &&
-                                       !a.slopes && !wide;
-                                if (!near) {
-                                    pa::cap_scores<kHalfCols>(s, top, c2, a.cap_log2, a.cap_inv);
-                                    c2 = 1.f;
-                                }
-                            }
-                            if (a.slopes) {
-                                // the token's distance to the half's first column
-                                const float d0 = (float)(it.ctx - it.n + it.t0 + x * a.tq + t - it.base - j * kKv - hc * kHalfCols);
-                                if (__all_sync(0xffffffffu, (float)lim <= d0 + 1.f)) {   // no row sees ahead: distances without their sign
-                                    uint64_t bias[4];
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) bias[k] = f32x2(slope * (2 * k - d0), slope * (2 * k + 1 - d0));
-                                    const uint64_t c = f32x2(c2, c2), step = f32x2(8.f * slope, 8.f * slope);
-#pragma unroll
-                                    for (int cc = 0; cc < kHalfCols; cc += 2) {
-                                        uint64_t& b = bias[cc / 2 & 3];
-                                        f32x2_split(fma_f32x2(f32x2(s[cc], s[cc + 1]), c, b), s[cc], s[cc + 1]);
-                                        b = add_f32x2(b, step);
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int cc = 0; cc < kHalfCols; ++cc) s[cc] = fmaf(-slope, fabsf(d0 - (float)cc), s[cc] * c2);
-                                }
+                        if constexpr (Args::kCapped) {
+                            const float top = pa::largest(s);
+                            near = __all_sync(0xffffffffu, top * fabsf(c2 * a.cap_inv) < 0.25f && lim >= kHalfCols &&
+                                                               row_lo[0] <= j * kKv + hc * kHalfCols) && !wide;
+                            if (!near) {
+                                pa::cap_scores<kHalfCols>(s, top, c2, a.cap_log2, a.cap_inv);
                                 c2 = 1.f;
                             }
+                        }
+                        if constexpr (Args::kBiased) {
+                            if (a.cap_inv != 0.f) {
+                                pa::cap_scores<kHalfCols>(s, pa::largest(s), c2, a.cap_log2, a.cap_inv);
+                                c2 = 1.f;
+                            }
+                            // the token's distance to the half's first column
+                            const float d0 = (float)(it.ctx - it.n + it.t0 + x * a.tq + t - it.base - j * kKv - hc * kHalfCols);
+                            if (__all_sync(0xffffffffu, (float)lim <= d0 + 1.f)) {   // no row sees ahead: distances without their sign
+                                uint64_t bias[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) bias[k] = f32x2(slope * (2 * k - d0), slope * (2 * k + 1 - d0));
+                                const uint64_t c = f32x2(c2, c2), step = f32x2(8.f * slope, 8.f * slope);
+#pragma unroll
+                                for (int cc = 0; cc < kHalfCols; cc += 2) {
+                                    uint64_t& b = bias[cc / 2 & 3];
+                                    f32x2_split(fma_f32x2(f32x2(s[cc], s[cc + 1]), c, b), s[cc], s[cc + 1]);
+                                    b = add_f32x2(b, step);
+                                }
+                            } else {
+#pragma unroll
+                                for (int cc = 0; cc < kHalfCols; ++cc) s[cc] = fmaf(-slope, fabsf(d0 - (float)cc), s[cc] * c2);
+                            }
+                            c2 = 1.f;
                         }
                         if constexpr (kShaped) {
                             const int from = row_lo[0] - j * kKv - hc * kHalfCols;
@@ -1030,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float mt = fmaxf(max3(mp[0], mp[1], mp[2]),
                                          fmaxf(max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])));
-                        if constexpr (Args::kCurved) {
+                        if constexpr (Args::kCapped) {
                             if (near) {                       // (the cap grows with the score: the largest stays the largest)
                                 mt = pa::NearCap(c2, a.cap_inv)(mt);
                                 c2 = 1.f;
@@ -1074,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the other 64 columns.
                         const uint64_t c2x2 = f32x2(c2, c2), negx2 = f32x2(neg, neg);
                         uint64_t lp[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};   // independent partial sums
-                        if constexpr (Args::kCurved)
+                        if constexpr (Args::kCapped)
                             if (near)
                                 write_capped_weights<kHalfCols>(s, pa::NearCap(c2x[0], a.cap_inv), negx2, lp,
                                                                 t_s + hc * (kHalfCols / 2));
