@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         const int lim = row_lim[0] - j * kKv - hc * kHalfCols;     // valid columns of this half
                         float c2 = c2x[0];
-                        bool near = false;                    // the cap is taken with the weights
+                        bool near = false, raises = true;     // the cap is taken with the weights
                         if constexpr (Args::kCapped) {
                             const float top = pa::largest(s);
                             near = __all_sync(0xffffffffu, top * fabsf(c2 * a.cap_inv) < 0.25f && lim >= kHalfCols &&
@@ -979,6 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!near) {
                                 pa::cap_scores<kHalfCols>(s, top, c2, a.cap_log2, a.cap_inv);
                                 c2 = 1.f;
+                            } else {
+                                raises = __any_sync(0xffffffffu, pa::NearCap(c2, a.cap_inv)(top) > m_used[0] + kRescaleThreshold);
                             }
                         }
                         if constexpr (Args::kBiased) {
@@ -1021,25 +1023,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int cc = 0; cc < kHalfCols; ++cc) s[cc] = cc < lim ? s[cc] : -INFINITY;
                         }
-                        float mp[8];
+                        // (no score is above the largest magnitude, at hand for the cap: where
+                        // that raises no row's maximum, none is looked for; 408 -> 384 us for
+                        // 8 prompts of 2,003 tokens with spans)
+                        float mt = -INFINITY;
+                        if (!near || raises) {
+                            float mp[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) mp[k] = max3(s[k], s[8 + k], s[16 + k]);
+                            for (int k = 0; k < 8; ++k) mp[k] = max3(s[k], s[8 + k], s[16 + k]);
 #pragma unroll
-                        for (int cc = 24; cc + 16 <= kHalfCols; cc += 16)
+                            for (int cc = 24; cc + 16 <= kHalfCols; cc += 16)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) mp[k] = max3(mp[k], s[cc + k], s[cc + 8 + k]);
-                        if ((kHalfCols - 24) % 16 == 8) {
+                                for (int k = 0; k < 8; ++k) mp[k] = max3(mp[k], s[cc + k], s[cc + 8 + k]);
+                            if ((kHalfCols - 24) % 16 == 8) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) mp[k] = fmaxf(mp[k], s[kHalfCols - 8 + k]);
-                        }
-                        float mt = fmaxf(max3(mp[0], mp[1], mp[2]),
-                                         fmaxf(max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])));
-                        if constexpr (Args::kCapped) {
-                            if (near) {                       // (the cap grows with the score: the largest stays the largest)
-                                mt = pa::NearCap(c2, a.cap_inv)(mt);
-                                c2 = 1.f;
+                                for (int k = 0; k < 8; ++k) mp[k] = fmaxf(mp[k], s[kHalfCols - 8 + k]);
                             }
+                            mt = fmaxf(max3(mp[0], mp[1], mp[2]), fmaxf(max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+                            if constexpr (Args::kCapped)
+                                if (near) mt = pa::NearCap(c2, a.cap_inv)(mt);   // (it grows with the score: the largest stays so)
                         }
+                        if constexpr (Args::kCapped)
+                            if (near) c2 = 1.f;
                         mt = fmaxf(mt, exchange(x, mt, nred[0], ok));
                         if (!ok) break;
                         const float mts = mt * c2;            // scale > 0: the maximum commutes with it
