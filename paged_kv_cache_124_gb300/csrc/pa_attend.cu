@@ -19,6 +19,7 @@
 // with a bias, 380 with a cap.
 
 #include "pa_attend.cuh"
+#include "pa_cap.cuh"
 #include "pa_multi_rows.cuh"
 
 namespace {
@@ -143,7 +144,7 @@ int attend(void* out, int out_dtype, const void* q, const void* k_cache, const v
     a.k_scales = k_scales;
     a.v_scales = v_scales;
     a.cap_log2 = softcap * kLog2e;
-    a.cap_inv = softcap > 0.f ? 1.f / a.cap_log2 : 0.f;
+    a.cap_inv = softcap > 0.f ? fminf(1.f / a.cap_log2, pa::kMostCapInv) : 0.f;
     const int box = wide || block_size < kTile ? block_size : kTile;
     CUtensorMap mk, mv;
     if (!pa_host::cache_view(&mk, k_cache, cache_rows, d_head, f8 ? 1 : 2, box) ||

@@ -246,7 +246,7 @@ int launch_prompt(const Call& c) {
     a.visible = reinterpret_cast<const int2*>(c.visible);
     a.slopes = c.slopes;
     a.cap_log2 = c.softcap * kLog2e;
-    a.cap_inv = c.softcap > 0.f ? 1.f / a.cap_log2 : 0.f;
+    a.cap_inv = c.softcap > 0.f ? fminf(1.f / a.cap_log2, pa::kMostCapInv) : 0.f;
     a.v_cache = c.v_cache;
     a.ctx_cap = c.ctx_cap;
     a.max_query_len = c.max_query_len;

@@ -9,6 +9,11 @@
 
 namespace pa {
 
+// Caps below 1e-30 (in units of log2) are taken for it: the inverse has to be finite for scores of 0.
+constexpr float kMostCapInv = 1e30f;
+// Scores u = s by beyond these are not taken for near zero, as the polynomials' coefficients would not be finite.
+constexpr float kMostNearBy = 1e6f;
+
 __device__ __forceinline__ float capped(float x, float cap_log2, float cap_inv) {
     const float u = x * cap_inv, v = u * u;
     const float p = fmaf(fmaf(fmaf(fmaf(v, 62.f / 2835.f, -17.f / 315.f), v, 2.f / 15.f), v, -1.f / 3.f), v, 1.f);
@@ -71,7 +76,7 @@ struct NearCap {
 template <int n>
 __device__ __forceinline__ void cap_scores(float (&s)[n], float top, float c2, float cap_log2, float cap_inv) {
     const float by = c2 * cap_inv, w = by * by;
-    const bool far = !(top * fabsf(by) < 0.5f);
+    const bool far = !(top * fabsf(by) < 0.5f && fabsf(by) < kMostNearBy);
     if (!__any_sync(0xffffffffu, far)) {
         const uint64_t q0 = pair_of(c2 * 0.999999456f), q1 = pair_of(c2 * w * -0.3332632f), q2 = pair_of(c2 * w * w * 0.131903234f),
                        q3 = pair_of(c2 * w * w * w * -0.0444030606f);

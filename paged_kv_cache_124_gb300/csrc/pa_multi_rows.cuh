@@ -80,8 +80,8 @@ __device__ __forceinline__ Shape shape_of(const ShapedArgs& a, const ShapedUnit&
     s.hi = real ? min(s.pos + 1, u.ctx) : u.ctx;                 // a row that is not there: any finite result will do
     if (a.visible && real) {
         const int2 v = a.visible[u.q0 + i];
-        s.lo = v.x;
-        s.hi = min(v.y, u.ctx);
+        s.lo = max(v.x, 0);
+        s.hi = max(min(v.y, u.ctx), 0);
     }
     s.slope = a.slopes ? kLog2e * a.slopes[(u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))] : 0.f;
     return s;

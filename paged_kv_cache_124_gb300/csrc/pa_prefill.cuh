@@ -896,6 +896,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // score scale (log2 domain; FP8: times the K scale)
         const float c2s = kF8 && !kShaped ? a.scale_log2 * a.k_scale : a.scale_log2;
         const float c2x[2] = {c2s, c2s};
+        float near_top = 0.f;                             // scores below are near zero beside the cap
+        if constexpr (Args::kCapped) near_top = c2s * a.cap_inv < pa::kMostNearBy ? 0.25f / (c2s * a.cap_inv) : 0.f;
         constexpr int kHalfCols = kKv / 2;                // score columns per thread
         constexpr int kOCols = D / 2;                     // output columns per thread
         int ns[2] = {0, 0}, nred[2] = {0, 0}, nod[2] = {0, 0};
@@ -934,8 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kShaped) {                  // keys [row_lo, row_lim), counted from the item's first
                     if (a.visible && valid_row[x]) {
                         const int2 v = a.visible[it.q0 + tok];
-                        row_lo[x] = max(v.x - it.base, 0);
-                        row_lim[x] = min(v.y, it.ctx);
+                        row_lo[x] = max(max(v.x, 0) - it.base, 0);
+                        row_lim[x] = max(min(v.y, it.ctx), 0);
                     }
                     row_lim[x] -= it.base;
                 }
@@ -974,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bool near = false, raises = true;     // the cap is taken with the weights
                         if constexpr (Args::kCapped) {
                             const float top = pa::largest(s);
-                            near = __all_sync(0xffffffffu, top * fabsf(c2 * a.cap_inv) < 0.25f && lim >= kHalfCols &&
+                            near = __all_sync(0xffffffffu, top < near_top && lim >= kHalfCols &&
                                                                row_lo[0] <= j * kKv + hc * kHalfCols) && !wide;
                             if (!near) {
                                 pa::cap_scores<kHalfCols>(s, top, c2, a.cap_log2, a.cap_inv);

@@ -648,8 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kShaped) {
                 if (a.visible && real) {
                     const int2 v = a.visible[u->q0 + i];
-                    from = v.x;
-                    lim = v.y;
+                    from = max(v.x, 0);
+                    lim = max(v.y, 0);
                 }
                 lim = min(lim, u->ctx);
                 if (Args::kCurved && a.slopes) slope = kLog2e * a.slopes[(u->kvh << a.log2_group) + ((u->row0 + r) & ((1 << a.log2_group) - 1))];

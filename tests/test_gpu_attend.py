@@ -578,3 +578,34 @@ def test_one_unit_for_most_blocks(scaled, lengths):
     """400 units of nearly one length, too long for a rule by length; and one that is much shorter."""
     p = Problem(21, 4, 4, 128, 16, list(lengths), [1] * 100, scaled=scaled, cap=20.0)
     p.check(p.run())
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("news", [[4, 1], [6, 30], [70, 12], [300, 40]])
+def test_intervals_at_the_ends_of_32_bits(scaled, news):
+    p = Problem(31, 8, 2, 128, 16, [n + 230 for n in news], news, "window", scaled=scaled)
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    ends = [(lo, None), (0, hi), (lo, lo), (hi, lo), (hi, hi), (lo, hi), (100, hi), (lo, 7), (lo + 1, 0)]
+    for t in range(len(p.visible)):
+        a, b = ends[t % len(ends)]
+        p.visible[t] = a, p.visible[t, 1] if b is None else b
+    p.check(p.run())
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-20, 1e-7, 1e-3, 1e5, 1e30, 3e38])
+@pytest.mark.parametrize("news", [[3], [30], [300]])
+def test_caps_of_any_size(cap, news):
+    """Among them rows of q, and keys, that are zeros: scores of 0."""
+    p = Problem(32, 8, 2, 128, 16, [n + 230 for n in news], news, cap=cap)
+    q = to_bits(p.q).copy()
+    q[::2] = 0
+    p.q = from_bits(q).cpu()
+    p.check(p.run())
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-7, 1.0])
+@pytest.mark.parametrize("news", [[3], [30], [300]])
+def test_scores_of_zero_under_a_cap(cap, news):
+    p = Problem(33, 8, 2, 128, 16, [n + 230 for n in news], news, cap=cap)
+    p.q = torch.zeros_like(p.q)
+    p.check(p.run())
