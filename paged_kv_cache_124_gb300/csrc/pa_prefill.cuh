@@ -1009,21 +1009,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             c2 = 1.f;
                         }
-                        if constexpr (kShaped) {
-                            const int from = row_lo[0] - j * kKv - hc * kHalfCols;
-                            if (from > 0 || lim < kHalfCols) {
-                                // the columns seen as bits (two comparisons a column cost twice as much)
-                                const auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+                        const int from = kShaped ? row_lo[0] - j * kKv - hc * kHalfCols : 0;
+                        if (from > 0 || lim < kHalfCols) {
+                            // the columns seen as bits (two comparisons a column cost twice as much)
+                            const auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                                for (int x0 = 0; x0 < kHalfCols; x0 += 32) {
-                                    const uint32_t seen = below(lim - x0) & ~below(from - x0);
+                            for (int x0 = 0; x0 < kHalfCols; x0 += 32) {
+                                const uint32_t seen = below(lim - x0) & ~below(from - x0);
 #pragma unroll
-                                    for (int cc = 0; cc < 32; ++cc) s[x0 + cc] = seen & (1u << cc) ? s[x0 + cc] : -INFINITY;
-                                }
+                                for (int cc = 0; cc < 32; ++cc) s[x0 + cc] = seen & (1u << cc) ? s[x0 + cc] : -INFINITY;
                             }
-                        } else if (lim < kHalfCols) {
-#pragma unroll
-                            for (int cc = 0; cc < kHalfCols; ++cc) s[cc] = cc < lim ? s[cc] : -INFINITY;
                         }
                         // (no score is above the largest magnitude, at hand for the cap: where
                         // that raises no row's maximum, none is looked for; 408 -> 384 us for
