@@ -15,8 +15,8 @@
 // that the cache's bytes hide (64 decodes of 4096 positions, capped, 169 us,
 // 0.94 of the measured copy rate; block-scaled 98, 0.81, against 92 with one
 // scale: a score and a weight take a factor more).  With many, the softmax's
-// instructions bind: 8 prompts of 2003 tokens 291 us causal (275 plain), 372
-// with a bias, 380 with a cap.
+// instructions bind: 8 prompts of 2003 tokens 273 us causal (275 plain), 341
+// with a bias, 353 with a cap.
 
 #include "pa_attend.cuh"
 #include "pa_cap.cuh"
@@ -34,19 +34,21 @@ constexpr long long kPromptRows = 192;
 // block-scaled, of up to 256 positions with up to 32 rows: units of 16 rows.  More rows:
 // units of 64 or 128 (wide), whose contexts are split over the device, or the
 // prefill kernel, whose items of 256 rows read their keys once, up to their
-// own last one.  The estimates (us, on 152 SMs) count wide units, at 1.75 us
-// of an SM a tile of 128 positions (block-scaled, 64 rows: 1.25) and 6 (4.5)
-// to begin and end, and items, at 2.6 a tile of two and 6.5.  32 query and 8
-// KV heads, us of wide / prefill:
+// own last one.  The estimates (us, on 152 SMs) count wide units, at 1.55 us
+// of an SM a tile of 128 positions (block-scaled, 64 rows: 1.25) and 5 (4.5)
+// to begin and end, and items, at 1.9 a tile of two and 5.5, most of the last
+// wave waited for, behind their staging.  32 query and 8 KV heads, us of wide /
+// prefill:
 //   contexts x new tokens   bf16        block-scaled
-//   8 x 8192, 64            105 / 178   144 / 219
-//   8 x 8192, 128           183 / 181   266 / 221
-//   8 x 1024, 128            51 / 38     63 / 44
-//   64 x 2048, 64           196 / 253   311 / 319
-//   64 x 512, 128           190 / 124   241 / 146
-//   1 x 16384, 512          170 / 252   261 / 266
-//   8 x 64, 64               12 / 16     18 / 16
-//   64 x 64, 64              52 / 46     87 / 51
+//   8 x 8192, 64            106 / 159   143 / 185
+//   8 x 8192, 128           184 / 161   264 / 187
+//   8 x 4096, 192           150 / 142   218 / 158
+//   8 x 1024, 128            52 / 33     63 / 35
+//   64 x 2048, 64           198 / 219   312 / 259
+//   64 x 512, 64             88 / 74    139 / 83
+//   1 x 16384, 512          172 / 240   259 / 253
+//   3 x 700, 64              16 / 23     16 / 24
+//   64 x 64, 64              53 / 36     87 / 37
 // and of units of 16 rows / wide: 512 x 60, 8 tokens 99 / 99 and 118 / 144; 512 x 300 217 / 144 and 212 / 217.
 Route route_of(long long rows, float scale, bool f8, int num_seqs, int n_kv_heads, int group, int ctx) {
     const double heads = (double)num_seqs * n_kv_heads;
@@ -54,9 +56,10 @@ Route route_of(long long rows, float scale, bool f8, int num_seqs, int n_kv_head
     if (f8 && rows <= 32 && ctx <= 256 && heads >= 1024) return kUnits16;
     if (rows < kPromptRows) return kWide;
     const double units = heads * (double)((rows + (f8 ? 63 : 127)) / (f8 ? 64 : 128)), tiles = (ctx + 127) / 128;
-    const double wide = 5 + units * tiles * (f8 ? 1.25 : 1.75) / 152 + ceil(units / 152) * (f8 ? 4.5 : 6) + (units > 152 ? 4 : 0);
+    const double wide = 5 + units * tiles * (f8 ? 1.25 : 1.55) / 152 + ceil(units / 152) * (f8 ? 4.5 : 5) + (units > 152 ? 4 : 0);
     const double items = heads * (double)((rows + 255) / 256), seen = (ctx - 0.5 * (double)(rows / group)) / 128 + 0.5;
-    const double prompt = 8 + fmax(1.0, items / 152) * (2.6 * seen + 6.5) + heads * ctx * (f8 ? 0.9e-4 : 0.7e-4);
+    const double waves = items <= 152 ? 1 : 0.15 * items / 152 + 0.85 * ceil(items / 152);
+    const double prompt = 8 + waves * (1.9 * seen + 5.5) + heads * ctx * (f8 ? 0.9e-4 : 0.6e-4);
     return wide <= prompt ? kWide : kPrompt;
 }
 

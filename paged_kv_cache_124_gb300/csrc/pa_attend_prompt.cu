@@ -11,13 +11,13 @@
 // blocks' scales are outside fp16's range keeps bf16 values, as pa_prefill's
 // do).
 //
-// 8 prompts of 2,003 tokens with spans and a cap: 416 us, 681 TFLOP/s of what
-// is seen; without the cap 317 us, 894.  The softmax's instructions bound it
-// (a cap adds three packed products to a pair's eight instructions), not the
-// products: sixteen softmax warps (466 us), four for each row tile by itself
-// (489) and eight for each (474) were slower.  8 chunks of 512 tokens over
-// block-scaled prefixes of 2,048 to 8,192: 381 us, 857 TFLOP/s, staging
-// included.
+// 8 prompts of 2,003 tokens with spans and a cap: 384 us, 738 TFLOP/s of what
+// is seen; without the cap 295 us, 961.  The softmax's instructions bound it
+// (a cap adds two packed products and a comparison to a pair's eight
+// instructions), not the products: when it took 415, sixteen softmax warps
+// took 466, four for each row tile by itself 489 and eight for each 474.  8
+// chunks of 512 tokens over block-scaled prefixes of 2,048 to 8,192: 353 us,
+// 924 TFLOP/s, of which the staging is some 30 us.
 
 #include "pa_attend.cuh"
 #include "pa_prefill.cuh"

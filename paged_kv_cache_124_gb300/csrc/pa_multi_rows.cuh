@@ -10,7 +10,7 @@
 // the largest so far, so that a weight fits f16.  64 decodes of 512 to 4,096
 // positions, 32 query heads over 8 of 128: capped over bf16 99 us, 0.90 of the
 // measured copy rate, block-scaled 63 us, 0.71 (there the instructions issued
-// bound it); 96 through windows of 1,024 of 100 to 8,000 positions 40 us, 0.70
+// bound it); 96 through windows of 1,024 of 100 to 8,000 positions 37 us, 0.76
 // (a short call: starting, the first tiles and the joins are a part of it).
 #pragma once
 
