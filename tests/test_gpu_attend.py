@@ -105,9 +105,9 @@ class Problem:
         E, W = (2.0 ** -11 if self.ks is not None else 0.0), 2.0 ** -11
         got, qa = out_to_f64(out), np.abs(A.bf16_to_f64(to_bits(self.q)))
         covered = np.zeros(self.q.shape[0], dtype=bool)
-        G = self.Hq // self.Hkv
+        G, ka, va = self.Hq // self.Hkv, np.abs(f64(kd)), np.abs(f64(vd))
         for s in range(len(self.ctx)):
-            K, V = A.gather_kv(np.abs(f64(kd)), np.abs(f64(vd)), self.tables[s], int(self.ctx[s]), self.B)
+            K, V = A.gather_kv(ka, va, self.tables[s], int(self.ctx[s]), self.B)
             for r in range(self.start[s], self.start[s + 1]):
                 covered[r] = True
                 for g in range(self.Hq):
@@ -609,3 +609,23 @@ def test_scores_of_zero_under_a_cap(cap, news):
     p = Problem(33, 8, 2, 128, 16, [n + 230 for n in news], news, cap=cap)
     p.q = torch.zeros_like(p.q)
     p.check(p.run())
+
+
+def test_the_readmes_prompt_with_an_image():
+    """Within the roundings of check(), a score's size bounded by the largest norms."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    with open(path) as f:
+        (code,) = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    x = {}
+    exec(compile(code, "README.md", "exec"), x)
+    torch.cuda.synchronize()
+    n, nb = x["n"], -(-x["n"] // x["B"])
+    k, v = (Q.dequantize_scaled(x[c][:nb].cpu().numpy(), x[s][:nb].cpu().numpy()) for c, s in (("codes", "scales"), ("v_codes", "v_scales")))
+    q = to_bits(x["q_turned"])
+    args = (x["table"].cpu().numpy(), [0, n], [n], x["scale"], x["B"], x["visible"].cpu().numpy(), 50.0)
+    want, weight = A.paged_shaped(q, k, v, *args), A.paged_shaped(q, k, np.abs(v), *args)
+    size = x["scale"] * np.linalg.norm(A.bf16_to_f64(q), axis=-1).max() * np.linalg.norm(k, axis=-1).max()
+    off = (2.0 ** -11 + 128 * 2.0 ** -24 + 2.0 ** -20) * size + 2.0 ** -21 * 50 + 2.0 ** -11
+    assert (np.abs(out_to_f64(x["seen"]) - want) <= 4 * off * weight + 2.0 ** -8 * np.abs(want)).all()
