@@ -282,7 +282,8 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Ctl* ct
     return false;
 }
 
-template <int D, bool kHalf, bool F8, class Args>
+// kRuns: how many scales 32 positions of a block-scaled cache have (blocks of 32, 16, 8: 1, 2, 4).
+template <int D, bool kHalf, bool F8, class Args, int kRuns>
 __global__ void __launch_bounds__(kThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const Args a, int oob_row) {
@@ -726,16 +727,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 wait_ld<kCols>(s);
                 const int t0 = start + j * kKv;
-                float cs[4] = {c, c, c, c};                      // the scores' factors, of 8 positions each (all the same but where block-scaled)
-                float by[4] = {0.f, 0.f, 0.f, 0.f};              // block-scaled values: log2 of the weights' factors
+                float cs[kRuns], by[kRuns];                      // the scores' factors; block-scaled values: log2 of the weights'
+#pragma unroll
+                for (int x = 0; x < kRuns; ++x) cs[x] = c;
                 bool grows = false;                              // and whether V's largest scale does
                 float v_new = v_top;
                 if constexpr (kShaped) {
                     if constexpr (kScaled) {
                         int most = 0;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int e = __shfl_sync(0xffffffffu, scales, (32 * half + 8 * x) >> a.log2_block);
+                        for (int x = 0; x < kRuns; ++x) {
+                            const int e = __shfl_sync(0xffffffffu, scales, half * kRuns + x);
                             cs[x] = fmaxf(c * scale_of(e & 0xff), 1e-37f);   // never 0: masked scores stay -inf
                             by[x] = (float)(e >> 8);
                             most = max(most, e >> 8);
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (Args::kCurved) {                         // scores in units of log2 from here on
                         if constexpr (kScaled) {
 #pragma unroll
-                            for (int k = 0; k < kCols; k += 2) split(mul2(pair(s[k], s[k + 1]), pair(cs[k >> 3], cs[k >> 3])), s[k], s[k + 1]);
+                            for (int k = 0; k < kCols; k += 2) split(mul2(pair(s[k], s[k + 1]), pair(cs[k * kRuns / 32], cs[k * kRuns / 32])), s[k], s[k + 1]);
                         }
                         float all = kScaled ? 1.f : c;
                         if (a.cap_inv != 0.f) {
@@ -760,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < kCols; ++k) s[k] = fmaf(-slope, fabsf(d0 - (float)k), s[k] * all);
                         }
-                        cs[0] = cs[1] = cs[2] = cs[3] = 1.f;
+#pragma unroll
+                        for (int x = 0; x < kRuns; ++x) cs[x] = 1.f;
                     }
                 }
                 if (kShaped ? t0 < from || t0 + kCols > lim : t0 + kCols > first) {   // some row (shaped: this one) may not see some position
@@ -777,9 +780,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const float* v = s + 8 * x;
-                        p[x] = cs[x] * fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+                        p[x] = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
                     }
-                    top = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+                    if constexpr (kRuns == 4)
+                        top = fmaxf(fmaxf(cs[0] * p[0], cs[1] * p[1]), fmaxf(cs[2] * p[2], cs[3] * p[3]));
+                    else
+                        top = fmaxf(cs[0] * fmaxf(p[0], p[1]), cs[kRuns - 1] * fmaxf(p[2], p[3]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 } else {
                     float p[8];
@@ -819,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kScaled) {
                     v_top = v_new;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) by[x] = fmaxf(by[x] - v_top, -60.f);   // (weights of less are nothing)
+                    for (int x = 0; x < kRuns; ++x) by[x] = fmaxf(by[x] - v_top, -60.f);   // (weights of less are nothing)
                 }
                 uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
                 // two columns' weights, summed
@@ -831,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum[k & 1] = add2(sum[k & 1], p);
                     return p;
                 };
-                // the like of block x, times 2^by[x]
+                // the like of run x, times 2^by[x]
                 auto scaled_weights = [&](float x0, float x1, int x) {
                     const float n = kUp - m + by[x];
                     float y0, y1;
@@ -853,8 +859,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float p0, p1;
                             uint64_t p;
                             if constexpr (kScaled) {
-                                p = scaled_weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], k >> 1);
-                                block = (k & 1) + e == 0 ? p : add2(block, p);
+                                p = scaled_weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], k * kRuns / 8);
+                                block = k % (8 / kRuns) + e == 0 ? p : add2(block, p);
                             } else {
                                 p = weights(s[4 * k + 2 * e], s[4 * k + 2 * e + 1], e);
                             }
@@ -862,8 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             h[e] = pa::pack_f16x2(p0, p1);
                         }
                         if constexpr (kScaled)
-                            if (k & 1) {                         // a block's sum, without its factor
-                                const float back = pa::exp2_approx(-by[k >> 1]);
+                            if (k % (8 / kRuns) == 8 / kRuns - 1) {   // a run's sum, without its factor
+                                const float back = pa::exp2_approx(-by[k * kRuns / 8]);
                                 sum[0] = fma2(block, pair(back, back), sum[0]);
                             }
 #pragma unroll
@@ -1094,14 +1100,14 @@ inline bool q_view(CUtensorMap* map, const void* q, int num_tokens, int n_q_head
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kHalf, bool F8, class Args>
+template <int D, bool kHalf, bool F8, int kRuns = 1, class Args>
 cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int oob_row,
                    int grid, cudaStream_t st) {
     static int attr[64] = {0};
     constexpr int kSmem = Wide<D, kHalf, F8>::kSmem;
-    const cudaError_t e = pa_host::ensure_smem_attr(wide_kernel<D, kHalf, F8, Args>, kSmem, attr);
+    const cudaError_t e = pa_host::ensure_smem_attr(wide_kernel<D, kHalf, F8, Args, kRuns>, kSmem, attr);
     if (e != cudaSuccess) return e;
-    return pa_host::launch_dependent(wide_kernel<D, kHalf, F8, Args>, dim3(grid), dim3(kThreads), kSmem, st, mq, mk, mv, a,
+    return pa_host::launch_dependent(wide_kernel<D, kHalf, F8, Args, kRuns>, dim3(grid), dim3(kThreads), kSmem, st, mq, mk, mv, a,
                                      oob_row);
 }
 
@@ -1109,7 +1115,13 @@ template <class Args>
 cudaError_t launch_units(int rows, int d_head, bool f8, const void* q, int block_size, const CUtensorMap& mk,
                          const CUtensorMap& mv, const Args& a, int grid, cudaStream_t st) {
     const int oob = a.num_blocks * a.n_kv_heads * block_size;    // one past the view's last row
-    if (f8) return launch<128, true, true>(mk, mk, mv, a, oob, grid, st);   // (its q is not copied as it is)
+    if (f8) {                                                    // (its q is not copied as it is)
+        if constexpr (Args::kShaped) {
+            if (block_size == 8) return launch<128, true, true, 4>(mk, mk, mv, a, oob, grid, st);
+            if (block_size == 16) return launch<128, true, true, 2>(mk, mk, mv, a, oob, grid, st);
+        }
+        return launch<128, true, true>(mk, mk, mv, a, oob, grid, st);
+    }
     CUtensorMap mq;
     if (!q_view(&mq, q, a.num_tokens, a.n_q_heads, d_head, 1 << a.log2_group)) return cudaErrorInvalidValue;
     return d_head == 128 ? (rows == 64 ? launch<128, true, false>(mq, mk, mv, a, oob, grid, st)
