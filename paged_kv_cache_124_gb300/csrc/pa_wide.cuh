@@ -678,17 +678,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // asked for a tile ahead and their table entries two.
             float v_top = 0.f;                                   // the largest of V so far, 2^(this - 127), which O is in units of
             int entry = -1;
-            uint32_t scales = 0, scales_next = 0;
+            uint32_t k_next = 0, v_next = 0;                      // (put together when their turn comes: nothing waits for them before)
             auto entry_of = [&](int j) {
                 const int pos = start - 32 * half + j * kKv + lane * B;
                 return kScaled && lane * B < kHalfKv && j < len && pos < end ? table[pos >> a.log2_block] : -1;
             };
-            auto scales_of = [&](int blk) {
-                uint32_t e = 0;                                  // (zeros are in place of what is not there)
+            auto ask = [&](int blk) {
+                k_next = v_next = 0;                             // (zeros are in place of what is not there)
                 if constexpr (kScaled)
-                    if (blk >= 0 && blk < a.num_blocks)
-                        e = a.k_scales[(size_t)blk * a.n_kv_heads + kvh] | (uint32_t)a.v_scales[(size_t)blk * a.n_kv_heads + kvh] << 8;
-                return e;
+                    if (blk >= 0 && blk < a.num_blocks) {
+                        k_next = a.k_scales[(size_t)blk * a.n_kv_heads + kvh];
+                        v_next = a.v_scales[(size_t)blk * a.n_kv_heads + kvh];
+                    }
             };
             float m = kNone, l = 0.f, c = a.scale_log2;
             if constexpr (F8) {
@@ -696,15 +697,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 c = factors[(nth & 1) * 64 + r];
             }
             if constexpr (kScaled) {
-                scales = scales_of(entry_of(0));
+                ask(entry_of(0));
                 entry = entry_of(1);
             }
 #pragma unroll 1
             for (int j = 0; j < len; ++j, ++at) {
                 const int b = at & 1;
                 const uint32_t t_s = t_lane + b * 128 + w * kHalfKv;
+                uint32_t scales = 0;
                 if constexpr (kScaled) {
-                    scales_next = scales_of(entry);
+                    scales = k_next | v_next << 8;
+                    ask(entry);
                     entry = entry_of(j + 2);
                 }
                 if (!(ok = wait_for(&ctl->s_full[b], (at >> 1) & 1, ctl, a.status))) break;
@@ -745,7 +748,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
                         v_new = fmaxf((float)most, v_top);
                         grows = v_new > v_top;
-                        scales = scales_next;
                     }
                     if (Args::kCurved) {                         // scores in units of log2 from here on
                         if constexpr (kScaled) {
