@@ -8,7 +8,7 @@
 // multiply the scores, V's the weights, relative to the largest so far.
 //
 // 8 sequences of 32,000 positions and more, 8 new tokens of 32 query heads
-// over 8 (32 rows), block-scaled: 126 us, 0.63 of the measured copy rate for
+// over 8 (32 rows), block-scaled: 121 us, 0.65 of the measured copy rate for
 // 532 MB (issue 51 %, ALU 42 %: a tile's chain of scores, softmax
 // and the four terms of a weight bounds it, as with one scale).
 

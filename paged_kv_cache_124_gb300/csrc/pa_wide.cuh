@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = first + i;
             float slope = 0.f;                                   // times log2(e)
             const int32_t* table = nullptr;
-            size_t kvh = 0;
+            uint32_t kvh = 0;
             int end = 0;
             if constexpr (kShaped) {
                 if (a.visible && real) {
@@ -687,8 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 k_next = v_next = 0;                             // (zeros are in place of what is not there)
                 if constexpr (kScaled)
                     if (blk >= 0 && blk < a.num_blocks) {
-                        k_next = a.k_scales[(size_t)blk * a.n_kv_heads + kvh];
-                        v_next = a.v_scales[(size_t)blk * a.n_kv_heads + kvh];
+                        const uint32_t at = (uint32_t)blk * a.n_kv_heads + kvh;   // (a cache has less than 2^31 rows)
+                        k_next = a.k_scales[at];
+                        v_next = a.v_scales[at];
                     }
             };
             float m = kNone, l = 0.f, c = a.scale_log2;
