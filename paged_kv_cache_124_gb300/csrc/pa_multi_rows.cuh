@@ -356,27 +356,29 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
 
     // A warp's tile k of a unit holds positions (st0 + k) * kStep + 16 warp on (from base).  Its
     // table entries come 32 tiles at a time, one per lane, the next 32 ahead.
+    // (A tile of one block has it in both entries: no other block's scale is taken for that of a half without positions.)
     auto fetch = [&](const Unit& u, int k, int& e0, int& e1) {
-        e0 = e1 = 0;
+        e0 = e1 = -1;
         const int t0 = base_of(u) + (u.st0 + k) * kStep + warp * kTile;
         if (k < u.len && t0 < u.ctx) {
             const int32_t* table = table_of(a, u);
-            e0 = table[t0 >> a.log2_block];
+            e0 = e1 = table[t0 >> a.log2_block];
             if (B < kTile && t0 + B < u.ctx) e1 = table[(t0 >> a.log2_block) + 1];
         }
     };
-    // Block-scaled: the scale bytes that go with the entries, asked for when those have come and before their tiles.
+    // Block-scaled: the scale bytes that go with the entries, asked for when those have come and before their tiles.  Zeros
+    // for a block that is not there.
     auto scales_of = [&](const Unit& u, int b0, int b1) {
         uint32_t r = 0;
         if constexpr (kScaled) {
-            const size_t i0 = (size_t)(b0 >= 0 && b0 < a.num_blocks ? b0 : 0) * heads + u.kvh;
-            const size_t i1 = (size_t)(B >= kTile ? (b0 >= 0 && b0 < a.num_blocks ? b0 : 0) : b1 >= 0 && b1 < a.num_blocks ? b1 : 0) * heads + u.kvh;
-            r = a.k_scales[i0] | (uint32_t)a.v_scales[i0] << 8 | (uint32_t)a.k_scales[i1] << 16 | (uint32_t)a.v_scales[i1] << 24;
+            const size_t i0 = (size_t)b0 * heads + u.kvh, i1 = (size_t)b1 * heads + u.kvh;
+            if (b0 >= 0 && b0 < a.num_blocks) r = a.k_scales[i0] | (uint32_t)a.v_scales[i0] << 8;
+            if (b1 >= 0 && b1 < a.num_blocks) r |= (uint32_t)a.k_scales[i1] << 16 | (uint32_t)a.v_scales[i1] << 24;
         }
         return r;
     };
     uint32_t scales = 0, scales_next = 0;                         // of this lane's tile of the 32 in work, and of the next 32
-    int e0 = 0, e1 = 0, f0 = 0, f1 = 0;
+    int e0 = -1, e1 = -1, f0 = -1, f1 = -1;
     int used = 0;                                                 // tiles of the ring before the current unit's
     auto issue = [&](const Unit& u, int k) {                      // whole warp
         if (k && (k & 31) == 0) {
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
 #pragma unroll 1
         for (int k = G::kAhead; k < kStages; ++k)
             if (k < len) issue(u, k);
-        int n0 = 0, n1 = 0;
+        int n0 = -1, n1 = -1;
         if (more) fetch(next, lane, n0, n1);
         if (threadIdx.x == 0) {
             next_unit<kRows, kStep, kUnitCost>(walk, units[(nth + 2) & 3], a);

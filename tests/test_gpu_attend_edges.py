@@ -1,0 +1,118 @@
+"""pa_attend and pa_attend_scaled where something outside of what a row sees
+could reach it: scales, table entries and values of blocks that are not its
+own, and magnitudes at the ends of what the kernels' types hold."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as A
+from oracle import quant as Q
+from _gpu_util import from_bits, out_to_f64, to_bits
+from test_gpu_attend import Problem
+
+pytestmark = pytest.mark.gpu
+
+api = pytest.importorskip("paged_kv_cache_124_gb300.api")
+
+
+def _rows(p):
+    """(row, sequence, position, first seen, end of the seen) of p's new tokens."""
+    for s, C in enumerate(p.ctx.tolist()):
+        for r in range(p.start[s], p.start[s + 1]):
+            pos = C - int(p.start[s + 1]) + r
+            lo, hi = (0, pos + 1) if p.visible is None else (max(0, int(p.visible[r][0])), min(C, int(p.visible[r][1])))
+            yield r, s, pos, lo, max(hi, lo)
+
+
+def _want(p, r, s, pos, lo, hi):
+    """Row r by the definition in float64, [Hq, D]; sums of a |v| beside it; the largest sum of |q| |k| and |v| that it sees."""
+    G, at = p.Hq // p.Hkv, np.arange(lo, hi)
+    blk, off = p.tables[s][at // p.B], at % p.B
+    f64 = lambda c, s: A.bf16_to_f64(c[blk, :, off]) if s is None else \
+        Q.e4m3_to_f64(c[blk, :, off]) * 2.0 ** (s[blk].astype(float) - 127)[..., None]  # noqa: E731
+    k, v = f64(p.kc, p.ks), f64(p.vc, p.vs)                         # [hi - lo, Hkv, D]
+    q = A.bf16_to_f64(to_bits(p.q[r:r + 1]))[0].reshape(p.Hkv, G, p.D)
+    x = np.einsum("hgd,jhd->hgj", q, k) * p.scale
+    size = np.einsum("hgd,jhd->hgj", np.abs(q), np.abs(k)).max(-1) * abs(p.scale)
+    if p.cap:
+        x = p.cap * np.tanh(x / p.cap)
+    if p.slopes is not None:
+        x = x - p.slopes.astype(float).reshape(p.Hkv, G, 1) * np.abs(pos - at)
+    w = np.exp(x - x.max(-1, keepdims=True))
+    w /= w.sum(-1, keepdims=True)
+    out, weight = (np.einsum("hgj,jhd->hgd", w, y).reshape(p.Hq, p.D) for y in (v, np.abs(v)))
+    return out, weight, size.reshape(p.Hq, 1), np.abs(v).max((0, 2)).repeat(G)[:, None]
+
+
+def _check(p, out, least=2.0 ** -24, smallest=0.0, take=lambda rows: rows):
+    """Problem.check's tolerances, with magnitudes of what a row sees alone:
+    weights below f16's steps, `least` of the largest |v|; what is below
+    `smallest` may be lost.  Returns the norms of all errors and all sums of
+    a |v|."""
+    got, off, all_ = out_to_f64(out), 0.0, 0.0
+    E = 2.0 ** -11 if p.ks is not None else 0.0                    # codes' q to f16
+    for r, s, pos, lo, hi in take(list(_rows(p))):
+        if lo == hi:
+            assert (got[r] == 0).all()
+            continue
+        want, weight, size, top = _want(p, r, s, pos, lo, hi)
+        bias = 0.0 if p.slopes is None else np.abs(p.slopes[:, None].astype(float)) * (hi - lo)
+        s_off = (E + 128 * 2.0 ** -24 + 2.0 ** -22) * size + 2.0 ** -20 * np.minimum(size, p.cap) + 2.0 ** -21 * p.cap + 2.0 ** -20 * bias
+        tol = 2 * (s_off + 2.0 ** -11) * weight * 2 + least * top + smallest
+        if out.dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -8 * np.abs(want)
+        bad = np.abs(got[r] - want)
+        assert (bad <= tol).all(), (r, s, bad.max(), (bad / tol).max())
+        off, all_ = off + (bad ** 2).sum(), all_ + (weight ** 2).sum()
+    return off ** 0.5, all_ ** 0.5
+
+
+def _few(n):
+    rng = np.random.default_rng(0)
+    return lambda rows: [rows[i] for i in sorted(rng.choice(len(rows), min(n, len(rows)), replace=False))]
+
+
+def _to_other_place(p, block, to):
+    """Swap two blocks of the pool."""
+    for c in (p.kc, p.vc, p.ks, p.vs):
+        if c is not None:
+            c[[block, to]] = c[[to, block]]
+    a, b = p.tables == block, p.tables == to
+    p.tables[a], p.tables[b] = to, block
+
+
+def _unused(p):
+    return np.setdiff1d(np.arange(len(p.kc)), p.tables[p.tables >= 0])
+
+
+@pytest.mark.parametrize("Hq,new", [(4, 1), (4, 2), (16, 1), (4, 8)])
+@pytest.mark.parametrize("mask,cap", [("causal", 0.0), ("window", 0.0), ("causal", 5.0)])
+@pytest.mark.parametrize("byte", [255, 200])
+@pytest.mark.parametrize("B", [8, 16, 32])
+def test_scales_of_blocks_that_are_not_its_own(Hq, new, mask, cap, byte, B):
+    """Contexts that end in either half of a tile of 16 positions; block 0 and all others of no sequence hold no scale, or a large one."""
+    for ctx in (1, 5, 8, 9, 17, 24, 45, 52):
+        p = Problem(3, Hq, 1, 128, B, [ctx], [min(new, ctx)], mask, scaled=True, cap=cap)
+        _to_other_place(p, 0, _unused(p)[0])
+        p.ks[_unused(p)] = p.vs[_unused(p)] = byte
+        _check(p, p.run())
+
+
+@pytest.mark.parametrize("B", [8, 16, 32])
+def test_a_sequence_as_its_tokens_come(B):
+    """Appended and attended token by token, then four by four, in a pool whose unwritten scales are none."""
+    Hq, Hkv, D, n = 8, 2, 128, 70
+    g = torch.Generator(device="cuda").manual_seed(B)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda").mul_(2).bfloat16()  # noqa: E731
+    NB = n // B + 3
+    kc, vc = (torch.full((NB, Hkv, B, D), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((NB, Hkv), 255, dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = (NB - 1 - torch.arange(NB - 1, device="cuda")).int()[None].contiguous()   # (block 0 is of no sequence)
+    done = 0
+    for new in [1] * 34 + [4] * 9:
+        at = torch.arange(done, done + new, device="cuda")
+        api.pa_reshape_and_cache_scaled(kc, vc, ks, vs, draw(new, Hkv, D), draw(new, Hkv, D), table[0].long()[at // B] * B + at % B)
+        done += new
+        p = Problem(1, Hq, Hkv, D, B, [done], [new], scaled=True)
+        p.kc, p.vc, p.ks, p.vs, p.tables, p.q = (*(t.cpu().numpy() for t in (kc, vc, ks, vs, table)), draw(new, Hq, D).cpu())
+        _check(p, p.run())
