@@ -29,16 +29,19 @@ struct ShapedStageArgs : StageArgs {
     const uint8_t* v_scales;
     const int32_t* query_start;
     const int2* visible;
-    int num_tokens, ctx_cap;
+    int num_tokens, ctx_cap, max_query_len;
     int* sched;           // zeroed for the prefill kernel's claims
 };
 
-// Whether tile j of the sequence is seen by some row (by a whole block).
+// Whether tile j of the sequence is seen by some row (by a whole block).  Of a
+// sequence without new tokens, or one that the prefill kernel flags and leaves
+// out (by the same conditions), none is: nothing of it is read.
 __device__ __forceinline__ bool tile_is_seen(const ShapedStageArgs& a, int s, int j, int ctx) {
+    const int q0 = a.query_start[s], q1 = a.query_start[s + 1];
+    if (q0 < 0 || q1 <= q0 || q1 > a.num_tokens || q1 - q0 > ctx || q1 - q0 > a.max_query_len) return false;
     if (!a.visible) return true;
-    const int q0 = a.query_start[s], q1 = min(a.query_start[s + 1], a.num_tokens);   // (of a flagged sequence, anything)
     int lo = INT_MAX, hi = 0;
-    for (int t = max(q0, 0) + threadIdx.x; t < q1; t += 256) {
+    for (int t = q0 + threadIdx.x; t < q1; t += 256) {
         const int2 v = a.visible[t];
         const int from = max(v.x, 0), to = min(v.y, ctx);
         if (from < to) {
@@ -271,6 +274,7 @@ int launch_prompt(const Call& c) {
     sa.query_start = c.query_start;
     sa.visible = a.visible;
     sa.num_tokens = c.num_tokens;
+    sa.max_query_len = c.max_query_len;
     sa.sched = sched;
     sa.ctx_cap = c.ctx_cap;
     const auto with = [&](auto form) {

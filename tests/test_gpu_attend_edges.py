@@ -116,3 +116,20 @@ def test_a_sequence_as_its_tokens_come(B):
         p = Problem(1, Hq, Hkv, D, B, [done], [new], scaled=True)
         p.kc, p.vc, p.ks, p.vs, p.tables, p.q = (*(t.cpu().numpy() for t in (kc, vc, ks, vs, table)), draw(new, Hq, D).cpu())
         _check(p, p.run())
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("mask", ["causal", "window"])
+def test_sequences_without_new_tokens_cost_and_flag_nothing(scaled, mask):
+    """Beside prompts: one without new tokens whose table is not there, and one that is flagged for more of them than positions."""
+    news = [131, 0, 131, 40] + [131] * 20
+    p = Problem(6, 32, 8, 128, 16, [300] * 24, news, mask, scaled=scaled)
+    clean = p.run()
+    p.tables[1] = -1
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert torch.equal(p.run(status=st), clean) and st.item() == 0
+    p.ctx[3], p.tables[3] = 39, -1
+    out = p.run(status=st)
+    rest = torch.ones(len(out), dtype=torch.bool, device="cuda")
+    rest[p.start[3]:p.start[4]] = False
+    assert st.item() == api.PA_DEV_BAD_CONTEXT and torch.equal(out[rest], clean[rest]) and torch.isnan(out[~rest]).all()
