@@ -507,7 +507,9 @@ size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads,
  * document it belongs to (begin, p + 1), a prefix or an image whose positions
  * see one another (.., end); it is clipped to [0, C).  A token whose interval
  * is empty gets zeros.  Positions outside it do not reach the token's row,
- * whatever they hold.  Sums and statistics are fp32 (a capped score is within
+ * whatever they hold; blocks with none of the positions from the first to the
+ * last that the sequence's tokens see are not read, nor their table entries
+ * (a cache may free the blocks behind its window).  Sums and statistics are fp32 (a capped score is within
  * 2^-20 of itself and 2^-21 of the cap), outputs rounded once.
  *   visible       device int32 [num_tokens][2], 8-byte aligned, or NULL.
  *   slopes        device f32 [n_q_heads], finite, or NULL.

@@ -33,13 +33,15 @@ struct ShapedStageArgs : StageArgs {
     int* sched;           // zeroed for the prefill kernel's claims
 };
 
-// Whether tile j of the sequence is seen by some row (by a whole block).  Of a
-// sequence without new tokens, or one that the prefill kernel flags and leaves
-// out (by the same conditions), none is: nothing of it is read.
-__device__ __forceinline__ bool tile_is_seen(const ShapedStageArgs& a, int s, int j, int ctx) {
+// The positions from the first to the last that some token of the sequence
+// sees (x .. y - 1), found by a whole block; what lies outside is not read.  Of
+// a sequence without new tokens, or one that the prefill kernel flags and
+// leaves out (by the same conditions), none.
+__device__ __forceinline__ int2 seen_of(const ShapedStageArgs& a, int s, int ctx) {
     const int q0 = a.query_start[s], q1 = a.query_start[s + 1];
-    if (q0 < 0 || q1 <= q0 || q1 > a.num_tokens || q1 - q0 > ctx || q1 - q0 > a.max_query_len) return false;
-    if (!a.visible) return true;
+    if (q0 < 0 || q1 <= q0 || q1 > a.num_tokens || q1 - q0 > ctx || q1 - q0 > a.max_query_len) return make_int2(0, 0);
+    if (!a.visible) return make_int2(0, ctx);
+    __shared__ int2 part[8];
     int lo = INT_MAX, hi = 0;
     for (int t = q0 + threadIdx.x; t < q1; t += 256) {
         const int2 v = a.visible[t];
@@ -49,18 +51,33 @@ __device__ __forceinline__ bool tile_is_seen(const ShapedStageArgs& a, int s, in
             hi = max(hi, to);
         }
     }
-    // (ranges that only together reach over the tile count as seen: every tile between the first and the last is read)
-    const int before = __syncthreads_or(lo < (j + 1) * kKv), behind = __syncthreads_or(hi > j * kKv);
-    return before && behind;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_int2(lo, hi);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        lo = min(lo, part[w].x);
+        hi = max(hi, part[w].y);
+    }
+    return make_int2(lo, hi);
 }
 
-__device__ __forceinline__ bool tile_there(const ShapedStageArgs& a, int s, int j, int& ctx) {
+// Whether tile j has such positions; which, in `seen`.
+__device__ __forceinline__ bool tile_there(const ShapedStageArgs& a, int s, int j, int2& seen) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x < 2 && blockIdx.x + blockIdx.y + blockIdx.z == 0) a.sched[threadIdx.x] = 0;
-    ctx = a.context_lens[s];
+    int ctx = a.context_lens[s];
     ctx = min(max(ctx, 0), a.ctx_cap);                           // the prefill kernel flags and clamps the same
-    return j * kKv < ctx && tile_is_seen(a, s, j, ctx);
+    if (j * kKv >= ctx) return false;
+    seen = seen_of(a, s, ctx);
+    return seen.x < (j + 1) * kKv && seen.y > j * kKv;
+}
+
+// Whether a position's block holds any of them.
+__device__ __forceinline__ bool block_there(int pos, int2 seen, int block_size) {
+    return pos < seen.y && (pos | (block_size - 1)) >= seen.x;
 }
 
 // Two bf16 that are not finite, as a mask.
@@ -73,8 +90,8 @@ template <int D>
 __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __restrict__ v_cache, const ShapedStageArgs a) {
     constexpr int kChunksPerRow = D / 8, kPer = kKv * kChunksPerRow / 256;
     const int j = blockIdx.x, s = blockIdx.y, h = blockIdx.z;
-    int ctx;
-    if (!tile_there(a, s, j, ctx)) return;
+    int2 seen;
+    if (!tile_there(a, s, j, seen)) return;
     const int32_t* table = a.block_tables + (size_t)s * a.max_blocks;
     const int log2_block = __ffs(a.block_size) - 1;
     uint4 v[kPer];
@@ -83,7 +100,7 @@ __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __rest
     for (int i = 0; i < kPer; ++i) {
         const int c = threadIdx.x + 256 * i, pos = j * kKv + c / kChunksPerRow;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (pos < ctx) {
+        if (block_there(pos, seen, a.block_size)) {
             const int blk = __ldg(table + (pos >> log2_block));
             if (blk >= 0 && blk < a.num_blocks)
                 v[i] = __ldg(v_cache + ((((size_t)blk * a.n_kv_heads + h) << log2_block) + (pos & (a.block_size - 1))) * kChunksPerRow +
@@ -118,8 +135,8 @@ __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restri
     constexpr int kChunksPerRow = D / 16, kPer = kKv * kChunksPerRow / 256;
     const int j = blockIdx.x, s = blockIdx.y, h = blockIdx.z >> 1;
     const bool is_v = blockIdx.z & 1;
-    int ctx;
-    if (!tile_there(a, s, j, ctx)) return;
+    int2 seen;
+    if (!tile_there(a, s, j, seen)) return;
     const int32_t* table = a.block_tables + (size_t)s * a.max_blocks;
     const uint4* cache = is_v ? v_cache : k_cache;
     const uint8_t* scales = is_v ? a.v_scales : a.k_scales;
@@ -132,7 +149,7 @@ __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restri
         const int c = threadIdx.x + 256 * i, pos = j * kKv + c / kChunksPerRow;
         code[i] = make_uint4(0, 0, 0, 0);
         scale[i] = 0.f;
-        if (pos < ctx) {
+        if (block_there(pos, seen, a.block_size)) {
             const int blk = __ldg(table + (pos >> log2_block));
             if (blk >= 0 && blk < a.num_blocks) {
                 const size_t block = (size_t)blk * a.n_kv_heads + h;

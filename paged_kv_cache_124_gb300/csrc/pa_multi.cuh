@@ -38,14 +38,15 @@ struct Unit {
 };
 
 // The like where each token sees an interval of positions: ctx is the end of
-// the positions that some token of the sequence sees, base (a multiple of 16,
-// or of 32) their begin, where step 0 starts; all tokens that see any see
-// seen_lo .. seen_hi - 1.
+// the positions that some token of the sequence sees, lo their begin, and base
+// (lo down to a multiple of 16, or of 32) where step 0 starts; blocks wholly in
+// front of lo are not read, nor their table entries.  All tokens that see any
+// see seen_lo .. seen_hi - 1.
 struct ShapedSeq : Seq {
-    int base, first, seen_lo, seen_hi, blind;                     // blind: some token sees nothing
+    int lo, base, first, seen_lo, seen_hi, blind;                 // blind: some token sees nothing
 };
 struct ShapedUnit : Unit {
-    int base, seen_lo, seen_hi, blind;
+    int lo, base, seen_lo, seen_hi, blind;
 };
 
 struct MultiArgs {
@@ -141,6 +142,7 @@ __device__ __forceinline__ typename Args::Seq read_seq(const Args& a, int s, boo
             }
             if (lo >= hi) lo = hi = 0;                  // nothing is seen: a step of no positions, and zeros
         }
+        r.lo = lo;
         r.base = lo & ~(kRows == 16 ? 15 : 31);             // (a tile of the wide kernel begins with a block)
         r.ctx = hi;
         r.steps = max(1, (hi - r.base + kStep - 1) / kStep);
@@ -201,6 +203,7 @@ __device__ __noinline__ void next_unit(WalkOf<typename Args::Seq>& w, typename A
         u.ctx = w.sq.ctx;
         if constexpr (Args::kShaped) {
             u.first = w.sq.first;
+            u.lo = w.sq.lo;
             u.base = w.sq.base;
             u.seen_lo = w.sq.seen_lo;
             u.seen_hi = w.sq.seen_hi;

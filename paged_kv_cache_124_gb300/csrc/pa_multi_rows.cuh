@@ -352,18 +352,24 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
         if constexpr (kShaped) return u.base;
         else return 0;
     };
+    auto lo_of = [](const Unit& u) {
+        if constexpr (kShaped) return u.lo;
+        else return 0;
+    };
     auto stage_at = [&](int stage) { return ring0 + stage * (kWarps * G::kStageBytes); };
 
     // A warp's tile k of a unit holds positions (st0 + k) * kStep + 16 warp on (from base).  Its
     // table entries come 32 tiles at a time, one per lane, the next 32 ahead.
-    // (A tile of one block has it in both entries: no other block's scale is taken for that of a half without positions.)
+    // (A tile of which one block alone is seen has it in both entries: no block that the unit does not see is read.)
     auto fetch = [&](const Unit& u, int k, int& e0, int& e1) {
         e0 = e1 = -1;
         const int t0 = base_of(u) + (u.st0 + k) * kStep + warp * kTile;
         if (k < u.len && t0 < u.ctx) {
             const int32_t* table = table_of(a, u);
-            e0 = e1 = table[t0 >> a.log2_block];
-            if (B < kTile && t0 + B < u.ctx) e1 = table[(t0 >> a.log2_block) + 1];
+            const bool second = B < kTile && t0 + B < u.ctx, first = !second || t0 + B > lo_of(u);
+            if (first) e0 = e1 = table[t0 >> a.log2_block];
+            if (second) e1 = table[(t0 >> a.log2_block) + 1];
+            if (!first) e0 = e1;
         }
     };
     // Block-scaled: the scale bytes that go with the entries, asked for when those have come and before their tiles.  Zeros

@@ -108,6 +108,7 @@ struct Item {
     int kv_end0, kv_end1, nt0, nt1, n_tiles, has_b;
     int wide;             // some V tile of the item is staged as bf16 (shaped: bit 0; bit 1: some value is not finite)
     int base;             // position of the item's first tile (0 but where shaped), which its tiles count from
+    int lo;               // shaped: the first position that a row of the item sees; blocks in front of it are not read
 };
 
 struct Bars {
@@ -454,7 +455,7 @@ __device__ __forceinline__ bool decode_item(int i, const Args& a, Item& it, bool
     it.has_b = it.t0 + a.tq < it.n ? 1 : 0;
     it.kv_end0 = it.ctx - it.n + min(it.n, it.t0 + a.tq);
     it.kv_end1 = it.ctx - it.n + min(it.n, it.t0 + 2 * a.tq);
-    it.base = 0;
+    it.base = it.lo = 0;
     if constexpr (Args::kShaped) {
         // Each Q tile's positions end with the last that a row of it sees; both begin with the first that one of either
         // does.  A tile of rows that see nothing has a position all the same, and its rows become zeros.
@@ -471,6 +472,7 @@ __device__ __forceinline__ bool decode_item(int i, const Args& a, Item& it, bool
                     }
                 }
             lo = __reduce_min_sync(0xffffffffu, lo);
+            it.lo = lo;                                   // (nothing is seen: behind all blocks)
             it.base = lo == INT_MAX ? 0 : lo & ~(kKv - 1);
             it.kv_end0 = max(__reduce_max_sync(0xffffffffu, hi[0]), it.base + 1);
             it.kv_end1 = max(__reduce_max_sync(0xffffffffu, hi[1]), it.base + 1);
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool gather = is_k && !kF8;              // FP8: K is staged like V
             auto fetch = [&](int j) {
                 const int pos = base_pos + j * kKv + lane * a.block_size;
-                return (gather && lane < bpt && pos < kv_all) ? __ldg(table + pos / a.block_size) : kNoBlock;
+                return (gather && lane < bpt && pos < kv_all && (!kShaped || pos + a.block_size > it.lo)) ? __ldg(table + pos / a.block_size) : kNoBlock;
             };
             auto to_row = [&](int blk) {
                 if (blk == kNoBlock) return a.oob_row;

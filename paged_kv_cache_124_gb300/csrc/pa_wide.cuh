@@ -354,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ producers
         // Lanes i * blocks on copy the blocks of tile i of the `per` tiles
         // that one load of table entries serves, the next load's in flight
-        // meanwhile; blocks past the context, and bad ids, are read from
-        // outside the tensor, which fills zeros.
+        // meanwhile; blocks past the context or in front of what is seen, and
+        // bad ids, are read from outside the tensor, which fills zeros.
         const bool is_k = warp == kKWarp;
         const int log2_blocks = 7 - a.log2_block, blocks = 1 << log2_blocks, per = 32 >> log2_blocks;
         static_assert(kKv == 128, "log2_blocks");
@@ -367,12 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kNoBlock = -2147483647 - 1;
         // A unit, and the table entries of its first tiles on their way.
         struct Next {
-            int valid, len, ctx, st0, kvh, token, first, base;
+            int valid, len, ctx, st0, kvh, token, first, base, lo;
             const int32_t* table;
         };
         auto fetch = [&](const Next& x, int j) {                 // tiles j .. j + per - 1
             const int pos = x.base + (x.st0 + j + sub) * kKv + place;
-            return (j + sub < x.len && pos < x.ctx) ? x.table[pos >> a.log2_block] : kNoBlock;
+            return (j + sub < x.len && pos < x.ctx && pos + B > x.lo) ? x.table[pos >> a.log2_block] : kNoBlock;
         };
         auto take = [&](int nth, Next& x) {                      // K's warp posts it, V's waits for it
             const int slot = nth % kUnits;
@@ -393,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.ctx = u->ctx;
             x.st0 = u->st0;
             x.base = u->valid ? base_of(*u) : 0;
+            x.lo = 0;
+            if constexpr (kShaped) x.lo = u->valid ? u->lo : 0;
             x.kvh = u->kvh;
             x.table = table_of(a, *u);
             x.token = u->q0 + (u->row0 >> a.log2_group);
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float slope = 0.f;                                   // times log2(e)
             const int32_t* table = nullptr;
             uint32_t kvh = 0;
-            int end = 0;
+            int end = 0, begin = 0;                              // the unit's positions
             if constexpr (kShaped) {
                 if (a.visible && real) {
                     const int2 v = a.visible[u->q0 + i];
@@ -657,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 table = table_of(a, *u);
                 kvh = u->kvh;
                 end = u->ctx;
+                begin = u->lo;
             }
             __syncwarp();
             if (lane == 0) pa::mbar_arrive(&ctl->unit_empty[slot]);
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t k_next = 0, v_next = 0;                      // (put together when their turn comes: nothing waits for them before)
             auto entry_of = [&](int j) {
                 const int pos = start - 32 * half + j * kKv + lane * B;
-                return kScaled && lane * B < kHalfKv && j < len && pos < end ? table[pos >> a.log2_block] : -1;
+                return kScaled && lane * B < kHalfKv && j < len && pos < end && pos + B > begin ? table[pos >> a.log2_block] : -1;
             };
             auto ask = [&](int blk) {
                 k_next = v_next = 0;                             // (zeros are in place of what is not there)

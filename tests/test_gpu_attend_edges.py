@@ -133,3 +133,44 @@ def test_sequences_without_new_tokens_cost_and_flag_nothing(scaled, mask):
     rest = torch.ones(len(out), dtype=torch.bool, device="cuda")
     rest[p.start[3]:p.start[4]] = False
     assert st.item() == api.PA_DEV_BAD_CONTEXT and torch.equal(out[rest], clean[rest]) and torch.isnan(out[~rest]).all()
+
+
+def _unseen_blocks(p, low, high):
+    """Of the first sequence: blocks that hold none of the positions low .. high - 1."""
+    n = -(-int(p.ctx[0]) // p.B)
+    return [j for j in range(n) if (j + 1) * p.B <= low or j * p.B >= high]
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("B", [8, 16, 32])
+@pytest.mark.parametrize("S,new", [(1, 2), (1, 7), (1, 60), (24, 131)])
+def test_blocks_that_no_token_sees_need_not_be_there(scaled, B, S, new):
+    """A cache that frees blocks behind its window, and ones in front of what is seen: entries of -1 or past the pool, codes
+    and scales of whoever has the block now.  Nothing is flagged, and not a bit changes."""
+    for low, high in ((100, 200), (139, 141), (8, 299), (127, 129), (256, 300), (0, 3)):
+        p = Problem(5, 8, 2, 128, B, [300] * S, [new] * S, "window", scaled=scaled)
+        p.visible[:] = [low, high]
+        p.visible[::3, 0] = min(low + 1, high - 1)
+        clean = p.run()
+        _check(p, clean, take=_few(12))
+        gone = _unseen_blocks(p, low, high)
+        for s in range(S):
+            ids = p.tables[s][gone]
+            p.kc[ids] = p.vc[ids] = 0x7F if scaled else 0x7FC0
+            if scaled:
+                p.ks[ids] = p.vs[ids] = 255
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert torch.equal(p.run(status=st), clean) and st.item() == 0
+        for s in range(S):
+            p.tables[s][gone] = [-1 if j % 2 else len(p.kc) + j for j in gone]
+        assert torch.equal(p.run(status=st), clean) and st.item() == 0
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("S,new", [(2, 2), (2, 60), (24, 131)])
+def test_a_table_that_no_token_looks_at(scaled, S, new):
+    p = Problem(5, 8, 2, 128, 16, [300] * S, [new] * S, "window", scaled=scaled)
+    p.visible[p.start[1]:p.start[2]] = [200, 200]
+    clean, st = p.run(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    p.tables[1] = -1
+    assert torch.equal(p.run(status=st), clean) and st.item() == 0 and (clean[p.start[1]:p.start[2]] == 0).all()
