@@ -7,7 +7,7 @@
 // of its work, and only those at its ends, or in units with a row that sees
 // nothing, take a mask.  Block-scaled: a stage's scales are a lane's own load,
 // passed on by shuffles; K's multiply the scores, V's the weights, relative to
-// the largest so far, so that a weight fits f16.  64 decodes of 512 to 4,096
+// the largest that the row has seen so far, so that a weight fits f16.  64 decodes of 512 to 4,096
 // positions, 32 query heads over 8 of 128: capped over bf16 99 us, 0.90 of the
 // measured copy rate, block-scaled 63 us, 0.71 (there the instructions issued
 // bound it); 96 through windows of 1,024 of 100 to 8,000 positions 37 us, 0.76
@@ -28,7 +28,8 @@ using namespace pa_multi;
 constexpr int kTile = 16;                  // positions per warp and step
 constexpr int kRows = 16;                  // rows of a unit
 constexpr int kWarpsPerSm = 12;
-constexpr float kWeightScale = 128.f;      // FP8: weights enter f16 products times 2^7 (at most 2^15)
+constexpr int kLog2WeightScale = 7;        // FP8: weights enter f16 products times 2^7 (at most 2^15)
+constexpr float kWeightScale = 1 << kLog2WeightScale;
 // A block's kWarps (4 or 12) warps split a step's positions, 16 each.  What
 // its shares are counted in:
 __host__ __device__ constexpr int step_of(int warps) { return warps * kTile; }
@@ -98,10 +99,10 @@ __device__ __forceinline__ bool visible(const MultiArgs& a, const Unit& u, int r
 template <int D>
 struct State {
     float m[2], l[2];
-    float top, inv;                        // block-scaled values: the largest scale so far, which acc is in units of, and kWeightScale over it
+    int top[2];                            // block-scaled values: the largest scale's byte that the row has seen, 2^(byte - 127) being acc's unit
     float acc[D / 8][4];
     __device__ __forceinline__ void reset() {
-        top = inv = 0.f;
+        top[0] = top[1] = 0;
         m[0] = m[1] = kNone;
         l[0] = l[1] = 0.f;
 #pragma unroll
@@ -155,7 +156,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
             score(kk, r[0], r[1], r[2], r[3]);
         }
     }
-    float by[2] = {1.f, 1.f};                          // block-scaled values: factors of the weights, of 8 positions each
+    float by[2][2];                                    // block-scaled values: factors of the weights, of 8 positions each, by row
     float f[2][2];                                     // factors of the scores: of positions 8 n on, and row g + 8 h
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -187,20 +188,29 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
                 }
         }
         if constexpr (F8) {
-            by[0] = scale_of(scales >> 8 & 0xff);
-            by[1] = scale_of(scales >> 24);
-            const float top = fmaxf(by[0], by[1]);
-            if (top > st.top) {                        // (the whole warp)
-                const float less = st.top / top;       // (powers of two: exact)
-                st.top = top;
-                st.inv = kWeightScale / top;
+            // (A scale of positions that a row does not see is none of its own: its weights there are zeros, and the
+            // unit of the others stays.  All factors are powers of two, put together from their exponents.)
+            const int v0 = scales >> 8 & 0xff, v1 = scales >> 24;
 #pragma unroll
-                for (int d = 0; d < D / 8; ++d)
+            for (int h = 0; h < kH; ++h) {
+                int top = max(v0, v1);
+                if (masked) {
+                    const int lo = shape[g + 8 * h].lo, hi = shape[g + 8 * h].hi;
+                    top = max(lo < t0 + 8 && hi > t0 ? v0 : 0, lo < t0 + kTile && hi > t0 + 8 ? v1 : 0);
+                }
+                if (top > st.top[h]) {
+                    const float less = scale_of(max(127 + st.top[h] - top, 0));
+                    st.top[h] = top;
 #pragma unroll
-                    for (int e = 0; e < 2 * kH; ++e) st.acc[d][e] *= less;
+                    for (int d = 0; d < D / 8; ++d) {
+                        st.acc[d][2 * h] *= less;
+                        st.acc[d][2 * h + 1] *= less;
+                    }
+                }
+                const int unit = 127 + kLog2WeightScale - st.top[h];
+                by[0][h] = scale_of(max(min(unit + v0, 127 + kLog2WeightScale), 0));
+                by[1][h] = scale_of(max(min(unit + v1, 127 + kLog2WeightScale), 0));
             }
-            by[0] *= st.inv;
-            by[1] *= st.inv;
         }
     } else if (t0 + kTile > u.first) {                 // some row may not see some position
 #pragma unroll
@@ -249,7 +259,7 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
             const float p1 = pa::exp2_approx(fmaf(s[n][2 * h + 1], f[n][h], -st.m[h]));
             st.l[h] += p0 + p1;
             if constexpr (F8) {
-                ph[2 * n + h] = kShaped ? pa::pack_f16x2(p0 * by[n], p1 * by[n]) : pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale);
+                ph[2 * n + h] = kShaped ? pa::pack_f16x2(p0 * by[n][h], p1 * by[n][h]) : pa::pack_f16x2(p0 * kWeightScale, p1 * kWeightScale);
             } else {
                 const uint32_t w = pa::pack_bf16x2(p0, p1);
                 const float2 hi = pa::bf16x2_to_float2(w);
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
 #pragma unroll
             for (int d = 0; d < D / 8; ++d)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) st.acc[d][e] *= st.top;
+                for (int e = 0; e < 4; ++e) st.acc[d][e] *= scale_of(st.top[e >> 1]);
         const int g = lane >> 2, t4 = lane & 3;
         auto join_row = [&](int w, int r) {                       // fp32 row r of key warp w
             const int rows = kRows / G::kJoinStages, stage = (used + G::kAhead + r / rows) % kStages;

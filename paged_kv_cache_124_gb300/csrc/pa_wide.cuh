@@ -39,7 +39,7 @@ struct Wide {
     static constexpr int kStages = F8 || D == 64 ? 6 : 3;
     static constexpr int kK0 = kQBuffers * kQBytes;
     static constexpr int kV0 = kK0 + kStages * kTileBytes;
-    static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][row] maximum and sum; F8: then row factors
+    static constexpr int kStats = kV0 + kStages * kTileBytes;    // [group][row] maximum and sum; F8: then row factors and units
     static constexpr int kCtl = kStats + 2 * 128 * 8;
     static constexpr int kSmem = kCtl + 1024;
     static constexpr int kStepKeys = F8 ? 32 : 16;               // positions of one value product
@@ -66,7 +66,6 @@ struct CtlOf {
     uint32_t tmem;
     int abort;
     int unfinite[2];                       // per unit parity: some new value is not finite
-    float tops[2];                         // block-scaled values: per group, the scale that its accumulator is in units of
 };
 static_assert(sizeof(CtlOf<MultiArgs>) <= 1024 && sizeof(CtlOf<ShapedArgs>) <= 1024, "control block overflows its space");
 
@@ -622,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kCols = kHalf ? 32 : 64;                   // columns per thread
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16), t_o = t_lane + kTmemO + w * 128;
         const float* factors = reinterpret_cast<const float*>(stats + 128);   // F8: [unit parity][row]
+        float* tops = reinterpret_cast<float*>(stats + 192);      // block-scaled values: [group][row] the unit of the row's O
         constexpr float kSlack = F8 ? 0.5f : kRaise;             // F8: weights of at most 2^15.5 in E5M2's 57344
         constexpr float kHeadroom = F8 ? 3.f : 0.f;              // F8: a raise leaves room for the next ones (a raise
                                                                  // at every growth cost 560 cycles in half the tiles)
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // Block-scaled: the scales of the group's 64 positions of a tile, lane i's of block i (K's byte, and V's above it),
             // asked for a tile ahead and their table entries two.
-            float v_top = 0.f;                                   // the largest of V so far, 2^(this - 127), which O is in units of
+            float v_top = 0.f;                                   // the largest of V that the row has seen, 2^(this - 127) being its O's unit
             int entry = -1;
             uint32_t k_next = 0, v_next = 0;                      // (put together when their turn comes: nothing waits for them before)
             auto entry_of = [&](int j) {
@@ -741,13 +741,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float v_new = v_top;
                 if constexpr (kShaped) {
                     if constexpr (kScaled) {
+                        // (a scale of positions that the row does not see is none of its own: its weights there are zeros)
                         int most = 0;
+                        const uint32_t some = t0 < from || t0 + kCols > lim ? seen(t0) : ~0u;
 #pragma unroll
                         for (int x = 0; x < kRuns; ++x) {
                             const int e = __shfl_sync(0xffffffffu, scales, half * kRuns + x);
                             cs[x] = fmaxf(c * scale_of(e & 0xff), 1e-37f);   // never 0: masked scores stay -inf
                             by[x] = (float)(e >> 8);
-                            most = max(most, e >> 8);
+                            most = max(most, some & (~0u >> (32 - 32 / kRuns) << (x * (32 / kRuns))) ? e >> 8 : 0);
                         }
                         most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
                         v_new = fmaxf((float)most, v_top);
@@ -831,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kScaled) {
                     v_top = v_new;
 #pragma unroll
-                    for (int x = 0; x < kRuns; ++x) by[x] = fmaxf(by[x] - v_top, -60.f);   // (weights of less are nothing)
+                    for (int x = 0; x < kRuns; ++x) by[x] = fminf(fmaxf(by[x] - v_top, -60.f), 0.f);   // (weights of less are nothing)
                 }
                 uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
                 // two columns' weights, summed
@@ -927,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nth >= 1 && !wait_for(&ctl->stats_free, (nth - 1) & 1, ctl, a.status)) break;
             if (kHalf) l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (!half) stats[w * kRows + r] = make_float2(m, l);
-            if (kScaled && quarter == 0 && lane == 0) ctl->tops[w] = __int_as_float((int)v_top << 23);
+            if (kScaled && !half) tops[w * kRows + r] = scale_of((int)v_top);
             pa::mbar_arrive(&ctl->stats_full);
         }
     } else {
@@ -1024,15 +1026,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool unfinite = ctl->unfinite[nth & 1];
             float top0 = 1.f, top1 = 1.f;
             if constexpr (kScaled) {
-                top0 = ctl->tops[0];
-                top1 = ctl->tops[1];
+                const float* tops = reinterpret_cast<const float*>(stats + 192);
+                top0 = tops[r];
+                top1 = tops[kRows + r];
             }
             pa::mbar_arrive(&ctl->stats_free);
             const float M = fmaxf(e.x, o.x), Z0 = pa::exp2_approx(e.x - M), Z1 = pa::exp2_approx(o.x - M);
             const float Z = Z0 * e.y + Z1 * o.y;
             const float by = whole ? (Z == 0.f ? 0.f : a.v_scale / Z) : 1.f;
             const bool none = kShaped && Z == 0.f;               // a row that sees nothing (and perhaps had no products)
-            const float fe = Z0 * by * top0, fo = Z1 * by * top1;
+            const float fe = Z0 * by, fo = Z1 * by;
             const size_t at = (size_t)(2 * blockIdx.x + (st0 == 0 ? 1 : 0)) * kRows + r;
             if (!wait_for(&ctl->o_done, nth & 1, ctl, a.status)) break;
             fence_after();
@@ -1048,7 +1051,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pa::mbar_arrive(&ctl->o_free);
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = none ? 0.f : fe * v[k] + (both ? fo * v1[k] : 0.f);
+                for (int k = 0; k < 32; ++k)
+                    v[k] = none ? 0.f
+                         : kScaled ? fe * v[k] * top0 + (both ? fo * v1[k] * top1 : 0.f)   // (small scales last: their products are)
+                                   : fe * v[k] + (both ? fo * v1[k] : 0.f);
                 float f[kHalf ? 16 : 32];                         // of a row's two lanes, each writes half
                 if constexpr (kHalf) {
 #pragma unroll

@@ -174,3 +174,34 @@ def test_a_table_that_no_token_looks_at(scaled, S, new):
     clean, st = p.run(), torch.zeros(1, dtype=torch.int32, device="cuda")
     p.tables[1] = -1
     assert torch.equal(p.run(status=st), clean) and st.item() == 0 and (clean[p.start[1]:p.start[2]] == 0).all()
+
+
+@pytest.mark.parametrize("B", [8, 16, 32])
+@pytest.mark.parametrize("S,new", [(1, 2), (1, 4), (1, 40), (24, 131)])
+@pytest.mark.parametrize("apart", [20, 40, 90])
+def test_documents_whose_scales_are_far_apart(B, S, new, apart):
+    """Two documents in a sequence, the values of one 2^apart of the other's: each as exact as by itself, whichever comes first."""
+    for first in (False, True):
+        p = Problem(7, 4, 1, 128, B, [300] * S, [new] * S, "window", scaled=True)
+        cut = 160
+        for s in range(S):
+            p.vs[p.tables[s][:cut // B]] = 115 if first else 115 - apart
+            p.vs[p.tables[s][cut // B:-(-300 // B)]] = 115 - apart if first else 115
+        p.visible[::2], p.visible[1::2] = [0, cut], [cut, 300]
+        p.visible[::4, 0], p.visible[::4, 1] = 150, 160            # (a few positions beside the other document's)
+        _check(p, p.run(), take=_few(12))
+    for s in range(S):                                             # beside the largest scale that there is
+        p.vs[p.tables[s][:cut // B]], p.vs[p.tables[s][cut // B:-(-300 // B)]] = 115, 254
+    _check(p, p.run(), take=lambda rows: _few(12)([r for r in rows if r[4] <= cut]))
+
+
+@pytest.mark.parametrize("S,new", [(1, 2), (1, 4), (1, 40), (24, 131)])
+@pytest.mark.parametrize("byte", [1, 2, 6, 7, 20])
+def test_values_of_the_smallest_scales(S, new, byte):
+    """Elements below fp32's smallest normal number, 2^-126, may be taken for zeros."""
+    p = Problem(8, 4, 1, 128, 8, [300] * S, [new] * S, "window", scaled=True)
+    p.vs[:] = byte
+    _check(p, p.run(), smallest=2.0 ** -126, take=_few(12))
+    p.vs[p.tables[0][:20]] = 0                                     # beside blocks of the least
+    p.visible[:] = [100, 300]
+    _check(p, p.run(), smallest=2.0 ** -126 + 448 * 2.0 ** -127, take=_few(12))
