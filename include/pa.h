@@ -509,8 +509,11 @@ size_t pa_decode_multi_workspace_size(int max_query_len, int n_q_heads,
  * is empty gets zeros.  Positions outside it do not reach the token's row,
  * whatever they hold; blocks with none of the positions from the first to the
  * last that the sequence's tokens see are not read, nor their table entries
- * (a cache may free the blocks behind its window).  Sums and statistics are fp32 (a capped score is within
- * 2^-20 of itself and 2^-21 of the cap), outputs rounded once.
+ * (a cache may free the blocks behind its window).  Sums and statistics are
+ * fp32 (a capped score is within 2^-20 of itself and 2^-21 of the cap), weights
+ * of few tokens in two bf16 terms, of prompts and long chunks f16 (a relative
+ * 2^-11), whose values are f16 too where that is exact or within 2^-25, 2^-15 of
+ * the largest |v| of their position; outputs are rounded once.
  *   visible       device int32 [num_tokens][2], 8-byte aligned, or NULL.
  *   slopes        device f32 [n_q_heads], finite, or NULL.
  *   softcap       finite, >= 0; scale finite (PA_ERR_INVALID_ARG otherwise).

@@ -85,7 +85,10 @@ __device__ __forceinline__ uint32_t unfinite2(uint32_t w) {
     return ((((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu;
 }
 
-// stage_v_kernel without the values that are not finite (format bit 1: there are some).
+// stage_v_kernel without the values that are not finite (format bit 1: there are some), and whose tiles stay bf16 also
+// where some position's values are all small: fp16 rounds them to steps of 2^-24 below 2^-14, and a row may see no others.
+// So a value is off by at most 2^-25, 2^-15 of the largest of its position.  (Zeros are exact.)
+constexpr uint32_t kF16Small = 0x3A80;                           // 2^-10
 template <int D>
 __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __restrict__ v_cache, const ShapedStageArgs a) {
     constexpr int kChunksPerRow = D / 8, kPer = kKv * kChunksPerRow / 256;
@@ -116,7 +119,17 @@ __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __rest
         amax = max_u16x2(amax, max_u16x2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
         amax = max_u16x2(amax, max_u16x2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
     }
-    const bool wide = __syncthreads_or((amax & 0xffffu) >= kF16Wide || (amax >> 16) >= kF16Wide) != 0;
+    bool small = false;                                          // a position's chunks lie in neighbouring lanes
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t m = max_u16x2(max_u16x2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                     max_u16x2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+        const uint32_t mine = (kChunksPerRow == 16 ? 0xffffu : 0xffu) << (threadIdx.x & 31 & -kChunksPerRow);
+        const bool large = (m & 0xffffu) >= kF16Small || (m >> 16) >= kF16Small;
+        const uint32_t filled = __ballot_sync(0xffffffffu, m != 0) & mine, larges = __ballot_sync(0xffffffffu, large) & mine;
+        small |= filled != 0 && larges == 0;
+    }
+    const bool wide = __syncthreads_or(small || (amax & 0xffffu) >= kF16Wide || (amax >> 16) >= kF16Wide) != 0;
     const bool some = __syncthreads_or(bad != 0) != 0;
     uint4* dst = reinterpret_cast<uint4*>(a.v_stage + ((size_t)(h * a.num_seqs + s) * a.l_slot + (size_t)j * kKv) * D);
 #pragma unroll

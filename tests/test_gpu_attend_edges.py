@@ -205,3 +205,24 @@ def test_values_of_the_smallest_scales(S, new, byte):
     p.vs[p.tables[0][:20]] = 0                                     # beside blocks of the least
     p.visible[:] = [100, 300]
     _check(p, p.run(), smallest=2.0 ** -126 + 448 * 2.0 ** -127, take=_few(12))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B,S,new", [(32, 8, 128, 16, 24, 131), (16, 16, 64, 8, 24, 260), (4, 2, 128, 16, 2, 3), (16, 2, 128, 32, 2, 20)])
+@pytest.mark.parametrize("shift", [8, 18, 30])
+@pytest.mark.parametrize("rows", ["all", "some", "mixed"])
+def test_small_values(Hq, Hkv, D, B, S, new, shift, rows):
+    """Values 2^-shift of a normal deviate's, at all positions, at every fifth, or the second half of each head: relative to the
+    largest of the positions that are seen, as any others (below 2^-14 f16 has steps of 2^-24, half of which is 2^-15 of
+    2^-10, from where on a position's are taken for f16)."""
+    p = Problem(9, Hq, Hkv, D, B, [300] * S, [new] * S, "spans")
+    v = from_bits(p.vc, "cpu").float()
+    if rows == "all":
+        v *= 2.0 ** -shift
+    elif rows == "some":
+        v[:, :, ::5] *= 2.0 ** -shift
+    else:
+        v[..., D // 2:] *= 2.0 ** -shift
+    p.vc = to_bits(v.bfloat16())
+    if rows == "some":                                             # rows that see one such position alone
+        p.visible[::2, 0] = p.visible[::2, 1] - 1
+    _check(p, p.run(), least=2.0 ** -15, take=_few(16))
