@@ -69,15 +69,16 @@ struct NearCap {
     }
 };
 
-// n scores s (times c2; cap_inv is 1 / cap_log2), the largest of which is top.  Where all of a warp's are
-// within half of the cap, as nearly always, by a polynomial in s^2 alone, in
-// packed pairs: tanh(u) / u fitted on [0, 0.5] with even ripple (relative
-// 6e-7), the scales of u folded into its coefficients.
+// n scores s (times c2; cap_inv is 1 / cap_log2), the largest of which is top.  Where all of this thread's are
+// within half of the cap, by a polynomial in s^2 alone, in packed pairs:
+// tanh(u) / u fitted on [0, 0.5] with even ripple (relative 6e-7), the scales
+// of u folded into its coefficients.  (By thread, not by warp, so that a row's
+// form is its own; scores that a row does not see come as zeros, for the same.)
 template <int n>
 __device__ __forceinline__ void cap_scores(float (&s)[n], float top, float c2, float cap_log2, float cap_inv) {
     const float by = c2 * cap_inv, w = by * by;
     const bool far = !(top * fabsf(by) < 0.5f && fabsf(by) < kMostNearBy);
-    if (!__any_sync(0xffffffffu, far)) {
+    if (!far) {
         const uint64_t q0 = pair_of(c2 * 0.999999456f), q1 = pair_of(c2 * w * -0.3332632f), q2 = pair_of(c2 * w * w * 0.131903234f),
                        q3 = pair_of(c2 * w * w * w * -0.0444030606f);
 #pragma unroll

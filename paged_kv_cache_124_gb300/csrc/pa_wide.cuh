@@ -739,11 +739,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < kRuns; ++x) cs[x] = c;
                 bool grows = false;                              // and whether V's largest scale does
                 float v_new = v_top;
+                // some row (shaped: this one) may not see some position
+                const bool part = kShaped ? t0 < from || t0 + kCols > lim : t0 + kCols > first;
+                auto where_unseen = [&](float to) {
+#pragma unroll
+                    for (int x = 0; x < kCols; x += 32) {
+                        const uint32_t v = seen(t0 + x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[x + k] = (v & (1u << k)) ? s[x + k] : to;
+                    }
+                };
                 if constexpr (kShaped) {
                     if constexpr (kScaled) {
                         // (a scale of positions that the row does not see is none of its own: its weights there are zeros)
                         int most = 0;
-                        const uint32_t some = t0 < from || t0 + kCols > lim ? seen(t0) : ~0u;
+                        const uint32_t some = part ? seen(t0) : ~0u;
 #pragma unroll
                         for (int x = 0; x < kRuns; ++x) {
                             const int e = __shfl_sync(0xffffffffu, scales, half * kRuns + x);
@@ -762,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float all = kScaled ? 1.f : c;
                         if (a.cap_inv != 0.f) {
+                            if (part) where_unseen(0.f);
                             pa::cap_scores<kCols>(s, pa::largest(s), all, a.cap_log2, a.cap_inv);
                             all = 1.f;
                         }
@@ -774,14 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < kRuns; ++x) cs[x] = 1.f;
                     }
                 }
-                if (kShaped ? t0 < from || t0 + kCols > lim : t0 + kCols > first) {   // some row (shaped: this one) may not see some position
-#pragma unroll
-                    for (int x = 0; x < kCols; x += 32) {
-                        const uint32_t v = seen(t0 + x);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) s[x + k] = (v & (1u << k)) ? s[x + k] : -INFINITY;
-                    }
-                }
+                if (part) where_unseen(-INFINITY);
                 float top;
                 if constexpr (kScaled) {
                     float p[4];

@@ -226,3 +226,37 @@ def test_small_values(Hq, Hkv, D, B, S, new, shift, rows):
     if rows == "some":                                             # rows that see one such position alone
         p.visible[::2, 0] = p.visible[::2, 1] - 1
     _check(p, p.run(), least=2.0 ** -15, take=_few(16))
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("S,new", [(1, 2), (1, 7), (1, 90), (24, 131)])
+@pytest.mark.parametrize("cap,alibi", [(3.0, False), (20.0, True), (50.0, False)])
+def test_unseen_keys_do_not_change_how_a_cap_is_taken(scaled, S, new, cap, alibi):
+    """Keys that no token sees, made large, not finite or zeros: not a bit of the rows changes."""
+    p = Problem(10, 8, 2, 128, 16, [300] * S, [new] * S, "window", scaled=scaled, cap=cap, alibi=alibi)
+    p.visible[:] = [103, 197]
+    clean = p.run()
+    _check(p, clean, take=_few(12))
+    hidden = [j for j in range(300) if not 103 <= j < 197]
+    for bits in ([0x7E, 0xFE], [0x7F, 0x7F], [0, 0]) if scaled else ([0x4780, 0xC780], [0x7F80, 0x7FC0], [0, 0]):   # 2^16; inf, NaN
+        for s in range(S):
+            for n, j in enumerate(hidden):
+                p.kc[p.tables[s][j // 16], :, j % 16] = bits[n % 2]
+        assert torch.equal(p.run(), clean)
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("S,new", [(1, 40), (24, 131)])
+@pytest.mark.parametrize("alibi", [False, True])
+def test_keys_that_others_see_do_not_change_how_a_cap_is_taken(scaled, S, new, alibi):
+    """The even tokens see keys that the odd ones do not: large, they are far beyond the cap; the odd ones' rows keep every bit."""
+    p = Problem(13, 8, 2, 128, 16, [300] * S, [new] * S, "window", scaled=scaled, cap=30.0, alibi=alibi)
+    p.visible[:] = [0, 150]
+    p.visible[::2] = [0, 300]
+    clean = p.run()
+    for s in range(S):
+        for j in range(150, 300, 7):
+            p.kc[p.tables[s][j // 16], :, j % 16] = 0x7E if scaled else 0x4380      # 448, 2^8
+    out = p.run()
+    assert torch.equal(out[1::2], clean[1::2])
+    _check(p, out, take=_few(12))
