@@ -140,7 +140,12 @@ __global__ void __launch_bounds__(256) stage_shaped_v_kernel(const uint4* __rest
     if (threadIdx.x == 0) a.v_fmt[(size_t)(h * a.num_seqs + s) * a.t_slot + j] = (wide ? 1 : 0) | (some ? 2 : 0);
 }
 
-constexpr float kMostBf16 = 0x1.fep127f;
+// Two bf16, the largest for what is beyond it (infinite, it would reach rows that do not see it).
+__device__ __forceinline__ uint32_t pack_bf16_finite(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 
 // A block-scaled cache's tile: K as bf16 (even blocks of z), V (odd ones) as fp16 where the blocks' scales are 2^-15 ..
 // 2^7 (the values are multiples of 2^-24 below 2^16 then), else as bf16; all exact but for values beyond bf16's
@@ -203,10 +208,7 @@ __global__ void __launch_bounds__(256) stage_scaled_kernel(const uint4* __restri
             const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
             const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
             const float lo = x.x * scale[i], hi = x.y * scale[i];
-            if (is_v && wide)                                    // (2^128 and beyond would be infinite, and reach rows that do not see it)
-                f[e] = pack_bf16_rn(fminf(fmaxf(lo, -kMostBf16), kMostBf16), fminf(fmaxf(hi, -kMostBf16), kMostBf16));
-            else
-                f[e] = wide ? pack_bf16_rn(lo, hi) : pack_f16_rn(lo, hi);
+            f[e] = wide ? pack_bf16_finite(lo, hi) : pack_f16_rn(lo, hi);
         }
         st_global_v8(dst + 2 * (threadIdx.x + 256 * i), f);      // (whole sectors; the workspace is 256-byte aligned)
     }

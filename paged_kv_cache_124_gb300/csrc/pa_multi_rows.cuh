@@ -193,11 +193,13 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
             const int v0 = scales >> 8 & 0xff, v1 = scales >> 24;
 #pragma unroll
             for (int h = 0; h < kH; ++h) {
-                int top = max(v0, v1);
+                int u0 = v0, u1 = v1;
                 if (masked) {
                     const int lo = shape[g + 8 * h].lo, hi = shape[g + 8 * h].hi;
-                    top = max(lo < t0 + 8 && hi > t0 ? v0 : 0, lo < t0 + kTile && hi > t0 + 8 ? v1 : 0);
+                    if (lo >= t0 + 8 || hi <= t0) u0 = 0;
+                    if (lo >= t0 + kTile || hi <= t0 + 8) u1 = 0;
                 }
+                const int top = max(u0, u1);
                 if (top > st.top[h]) {
                     const float less = scale_of(max(127 + st.top[h] - top, 0));
                     st.top[h] = top;
@@ -208,8 +210,8 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
                     }
                 }
                 const int unit = 127 + kLog2WeightScale - st.top[h];
-                by[0][h] = scale_of(max(min(unit + v0, 127 + kLog2WeightScale), 0));
-                by[1][h] = scale_of(max(min(unit + v1, 127 + kLog2WeightScale), 0));
+                by[0][h] = scale_of(max(unit + u0, 0));
+                by[1][h] = scale_of(max(unit + u1, 0));
             }
         }
     } else if (t0 + kTile > u.first) {                 // some row may not see some position

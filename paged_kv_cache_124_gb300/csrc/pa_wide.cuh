@@ -752,14 +752,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kShaped) {
                     if constexpr (kScaled) {
                         // (a scale of positions that the row does not see is none of its own: its weights there are zeros)
-                        int most = 0;
-                        const uint32_t some = part ? seen(t0) : ~0u;
+                        int most = 0, v_of[kRuns];
 #pragma unroll
                         for (int x = 0; x < kRuns; ++x) {
                             const int e = __shfl_sync(0xffffffffu, scales, half * kRuns + x);
                             cs[x] = fmaxf(c * scale_of(e & 0xff), 1e-37f);   // never 0: masked scores stay -inf
-                            by[x] = (float)(e >> 8);
-                            most = max(most, some & (~0u >> (32 - 32 / kRuns) << (x * (32 / kRuns))) ? e >> 8 : 0);
+                            v_of[x] = e >> 8;
+                        }
+                        if (part) {
+                            const uint32_t some = seen(t0);
+#pragma unroll
+                            for (int x = 0; x < kRuns; ++x)
+                                if (!(some & (~0u >> (32 - 32 / kRuns) << (x * (32 / kRuns))))) v_of[x] = 0;
+                        }
+#pragma unroll
+                        for (int x = 0; x < kRuns; ++x) {
+                            by[x] = (float)v_of[x];
+                            most = max(most, v_of[x]);
                         }
                         most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
                         v_new = fmaxf((float)most, v_top);
@@ -837,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kScaled) {
                     v_top = v_new;
 #pragma unroll
-                    for (int x = 0; x < kRuns; ++x) by[x] = fminf(fmaxf(by[x] - v_top, -60.f), 0.f);   // (weights of less are nothing)
+                    for (int x = 0; x < kRuns; ++x) by[x] = fmaxf(by[x] - v_top, -60.f);   // (weights of less are nothing)
                 }
                 uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
                 // two columns' weights, summed
