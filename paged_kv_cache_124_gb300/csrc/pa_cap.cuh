@@ -9,6 +9,15 @@
 
 namespace pa {
 
+// A bias by distance, in units of log2, for a row that sees positions lo .. hi - 1: the distance to the nearest of them is
+// the same in all its scores and leaves its softmax alone, so it is left out: slope |p - j| less slope |p - p'| is
+// slope |p' - j| for the seen position p' nearest to p.  (Far from what it sees, a row's scores would lose as many bits as
+// the distance has.)
+__device__ __forceinline__ int bias_from(int pos, int lo, int hi) { return min(max(pos, lo), hi - 1); }
+// Beyond this one position, the nearest or the farthest, has all of the weight; times 2^31 it is finite.
+constexpr float kMostSlope = 1e28f;
+__device__ __forceinline__ float bias_slope(float slope) { return fminf(fmaxf(1.4426950408889634f * slope, -kMostSlope), kMostSlope); }
+
 // Caps below 1e-30 (in units of log2) are taken for it: the inverse has to be finite for scores of 0.
 constexpr float kMostCapInv = 1e30f;
 // Scores u = s by beyond these are not taken for near zero, as the polynomials' coefficients would not be finite.

@@ -66,8 +66,8 @@ struct Geo {
     static_assert(kJoinStages * kStageBytes == 4 * kRows * D, "a unit's states fill the join stages");
 };
 
-// Shaped units: what a row sees, its position, and its bias' slope times
-// log2(e).  In shared memory: few tiles need it, and registers are short.
+// Shaped units: what a row sees, the position that its bias counts from, and
+// the bias' slope times log2(e).  In shared memory: few tiles need it, and registers are short.
 struct Shape {
     int lo, hi, pos;
     float slope;
@@ -84,7 +84,8 @@ __device__ __forceinline__ Shape shape_of(const ShapedArgs& a, const ShapedUnit&
         s.lo = max(v.x, 0);
         s.hi = max(min(v.y, u.ctx), 0);
     }
-    s.slope = a.slopes ? kLog2e * a.slopes[(u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))] : 0.f;
+    s.pos = pa::bias_from(s.pos, s.lo, s.hi);
+    s.slope = a.slopes ? pa::bias_slope(a.slopes[(u.kvh << a.log2_group) + (row & ((1 << a.log2_group) - 1))]) : 0.f;
     return s;
 }
 

@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_used[2] = {kNothing, kNothing}, l[2] = {0.f, 0.f};
             int row_lim[2], row_lo[2] = {0, 0};
             float slope = 0.f;                            // times log2(e)
-            if constexpr (Args::kBiased) slope = 1.4426950408889634f * a.slopes[it.h * a.group + gq];
+            if constexpr (Args::kBiased) slope = pa::bias_slope(a.slopes[it.h * a.group + gq]);
             bool valid_row[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -1005,8 +1005,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pa::cap_scores<kHalfCols>(s, pa::largest(s), c2, a.cap_log2, a.cap_inv);
                                 c2 = 1.f;
                             }
-                            // the token's distance to the half's first column
-                            const float d0 = (float)(it.ctx - it.n + it.t0 + x * a.tq + t - it.base - j * kKv - hc * kHalfCols);
+                            // the distance to the half's first column, from where the row's bias counts
+                            const int at = pa::bias_from(it.ctx - it.n + it.t0 + x * a.tq + t - it.base, row_lo[0], row_lim[0]);
+                            const float d0 = (float)(at - j * kKv - hc * kHalfCols);
                             if (__all_sync(0xffffffffu, (float)lim <= d0 + 1.f)) {   // no row sees ahead: distances without their sign
                                 uint64_t bias[4];
 #pragma unroll

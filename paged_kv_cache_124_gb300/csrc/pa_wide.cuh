@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned long long word = tree && real ? words_of(a, *u)[i] : ~0ull;
             if (u->n < 64) word &= (1ull << u->n) - 1;
             int lim = (tree || !real) ? u->ctx : first + i + 1, from = 0;
-            const int pos = first + i;
+            int pos = first + i;                                 // which a bias counts from
             float slope = 0.f;                                   // times log2(e)
             const int32_t* table = nullptr;
             uint32_t kvh = 0;
@@ -655,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     lim = max(v.y, 0);
                 }
                 lim = min(lim, u->ctx);
-                if (Args::kCurved && a.slopes) slope = kLog2e * a.slopes[(u->kvh << a.log2_group) + ((u->row0 + r) & ((1 << a.log2_group) - 1))];
+                if (Args::kCurved && a.slopes) slope = pa::bias_slope(a.slopes[(u->kvh << a.log2_group) + ((u->row0 + r) & ((1 << a.log2_group) - 1))]);
+                pos = pa::bias_from(pos, from, lim);
                 table = table_of(a, *u);
                 kvh = u->kvh;
                 end = u->ctx;

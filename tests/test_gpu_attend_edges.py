@@ -260,3 +260,43 @@ def test_keys_that_others_see_do_not_change_how_a_cap_is_taken(scaled, S, new, a
     out = p.run()
     assert torch.equal(out[1::2], clean[1::2])
     _check(p, out, take=_few(12))
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("S,new,ctx", [(1, 2, 1 << 20), (1, 4, 1 << 20), (1, 40, 1 << 20), (64, 128, 1 << 18)])
+@pytest.mark.parametrize("slope", [0.5, 0.0625])
+def test_a_bias_over_positions_far_from_the_token(scaled, S, new, ctx, slope):
+    """A token that sees a short interval far behind it, or ahead of it: the distance to all of the interval is no weight's
+    concern, and takes no bits of the rest."""
+    B, n = 16, 8
+    p = Problem(11, 4, 1, 128, B, [n * B] * S, [1] * S, scaled=scaled)
+    p.tables = np.ascontiguousarray(np.tile(p.tables[:, :n], (1, ctx // (n * B))))   # the same blocks again and again
+    p.ctx[:] = ctx
+    p.start = (np.arange(S + 1) * new).astype(np.int32)
+    p.q = torch.randn(S * new, 4, 128, generator=torch.Generator().manual_seed(1)).bfloat16()
+    p.most, p.slopes = new, np.full(4, slope, dtype=np.float32)
+    p.visible = np.tile(np.array([[5, 60]], dtype=np.int32), (S * new, 1))
+    p.visible[1::2] = [37, 131]
+    out = p.run()
+    off, weight = _check(p, out, take=_few(16))
+    assert off <= 2.0 ** -10 * weight                              # weights' roundings, 2^-11 at the most, as often up as down
+    p.visible[:] = [ctx - 60, ctx]                                 # ahead of some, about others
+    off, weight = _check(p, p.run(), take=_few(16))
+    assert off <= 2.0 ** -10 * weight
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("S,new", [(1, 4), (1, 90), (24, 131)])
+@pytest.mark.parametrize("slope", [3e37, 1e30, -0.01])
+def test_slopes_of_any_size(scaled, S, new, slope):
+    """The nearest position alone where a slope is large; the farther the more where it is negative."""
+    p = Problem(12, 4, 1, 128, 16, [300] * S, [new] * S, "window", scaled=scaled)
+    p.slopes = np.full(4, slope, dtype=np.float32)
+    p.visible[:] = [20, 100]
+    out = p.run()
+    if slope < 0:
+        _check(p, out, take=_few(12))
+    else:
+        for r, s, pos, lo, hi in _few(12)(list(_rows(p))):
+            want = _want(p, r, s, pos, hi - 1, hi)[0]
+            assert (np.abs(out_to_f64(out[r]) - want) <= 2.0 ** -10 * np.abs(want)).all()
