@@ -538,10 +538,18 @@ int append(void* q_out, void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t
     a.block_size = block_size;
     a.log2_block = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     const bool many = n_q_heads >= 8 && (long long)num_tokens * (n_q_heads + 2 * n_kv_heads) * d_head >= 12000000;
-    // 32 + 2 x 8 heads of 128, us of kFew / kSome / kMany: prompts of 300 tokens 10.6 / 11.5 / 13.7, 700 13.9 / 12.1 / 14.4, 2003
-    // 19.4 / 17.4 / 19.5, 4006 31.5 / 26.5 / 23.0, 8012 58.6 / 47.9 / 41.5; a token each of 256 requests 5.0 / 8.2 / 9.7, 1024
-    // 12.8 / 13.7 / 16.4, 4096 36.5 / 28.6 / 27.1
-    const int mode = num_tokens < 600 ? kFew : num_tokens < 3000 ? kSome : kMany;
+    // Calls of up to 600 tokens are taken for decode batches, a token a block, larger ones for prompts (the slots are on the
+    // device).  kMany where its tiles of eight heads are three quarters full or more, and 180 blocks of them, of heads of 128,
+    // are there.  32 + 2 x 8 heads of 128, us of kFew / kSome / kMany: prompts of 300 tokens 10.6 / 11.5 / 13.7, 700 13.9 /
+    // 12.1 / 14.4, 2003 19.4 / 17.4 / 19.5, 4006 31.5 / 26.5 / 23.0, 8012 58.6 / 47.9 / 41.5; a token each of 256 requests 5.0 /
+    // 8.2 / 9.7, 1024 12.8 / 13.7 / 16.4, 4096 36.5 / 28.6 / 27.1.  Other heads (inputs in L2): 2 + 2 x 1 of 128, prompts of 300
+    // 8.2 / 5.0 / 6.0, 4006 11.9 / 7.4 / 9.3, 16,000 32.4 / 19.0 / 26.7, 256 requests 3.8 / 6.0 / 7.9, 1024 4.4 / 6.0 / 8.1;
+    // 16 + 2 x 2 of 64, 8012 18.9 / 17.0 / 23.2; 32 + 2 x 8 of 64, 3000 16.3 / 11.5 / 13.5, 4006 20.5 / 16.3 / 15.0, 8012 31.9 /
+    // 26.4 / 23.8; 32 + 2 x 32 of 128, 700 15.6 / 10.6 / 11.1, 1024 24.1 / 16.9 / 14.5; the append alone, 8 heads of 128, 3000
+    // 12.7 / 6.7 / 7.4, 4006 15.8 / 9.7 / 7.6.
+    const long long tiles = (n_kv_heads + 7) / 8, blocks = ((long long)num_tokens + kRuns - 1) / kRuns * tiles;
+    const bool full = n_kv_heads >= 6 * tiles;
+    const int mode = num_tokens < 600 ? kFew : full && blocks * d_head >= 180 * 128 ? kMany : kSome;
     a.q_heads_per = many ? (n_q_heads + 1) / 2 : 1;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e =

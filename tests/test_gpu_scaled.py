@@ -276,6 +276,11 @@ def test_many_tokens_are_the_same_in_calls_of_few(T, Hkv, D, B):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,Hkv,D,B", [(5003, 8, 128, 16), (3003, 15, 128, 32), (6003, 7, 64, 8), (16003, 2, 128, 16)])
+def test_many_tokens_of_heads_that_fill_their_tiles_or_do_not(T, Hkv, D, B):
+    test_many_tokens_are_the_same_in_calls_of_few(T, Hkv, D, B)
+
+
 def test_padding_bad_positions_and_bad_slots_of_the_append():
     T, Hq, Hkv, D, B, NB = 9, 4, 2, 128, 16, 4
     q, k, v = _qkv(T, Hq, Hkv, D, 3)
