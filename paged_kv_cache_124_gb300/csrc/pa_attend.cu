@@ -30,15 +30,18 @@ enum Route { kUnits16, kWide, kPrompt };
 constexpr long long kPromptRows = 192;
 
 // Which kernel takes a call.  Up to 16 rows a KV head, with a scale that is
-// not positive, and over few short contexts (in_small_tiles), or many that are
-// block-scaled, of up to 256 positions with up to 32 rows: units of 16 rows.  More rows:
-// units of 64 or 128 (wide), whose contexts are split over the device, or the
-// prefill kernel, whose items of 256 rows read their keys once, up to their
-// own last one.  The estimates (us, on 152 SMs) count wide units, at 1.55 us
-// of an SM a tile of 128 positions (block-scaled, 64 rows: 1.25) and 5 (4.5)
-// to begin and end, and items, at 1.9 a tile of two and 5.5, most of the last
-// wave waited for, behind their staging.  32 query and 8 KV heads, us of wide /
-// prefill:
+// not positive, and over few short contexts (in_small_tiles): units of 16 rows.
+// More rows: units of 64 or 128 (wide), whose contexts are split over the
+// device, or the prefill kernel, whose items of 256 rows read their keys once,
+// up to their own last one.  Block-scaled calls of up to 32 rows, half of what
+// a wide unit holds, stay with units of 16 also where the context is one tile
+// of a wide unit and there are three units of it an SM or more, so that its
+// chain of a tile from beginning to end is what they wait for.
+//
+// The estimates (us) count wide units, at 1.55 us of an SM a tile of 128
+// positions (block-scaled, 64 rows: 1.25) and 5 (4.5) to begin and end, and
+// items, at 1.9 a tile of two and 5.5, most of the last wave waited for,
+// behind their staging.  32 query and 8 KV heads, us of wide / prefill:
 //   contexts x new tokens   bf16        block-scaled
 //   8 x 8192, 64            106 / 159   143 / 185
 //   8 x 8192, 128           184 / 161   264 / 187
@@ -49,16 +52,25 @@ constexpr long long kPromptRows = 192;
 //   1 x 16384, 512          172 / 240   259 / 253
 //   3 x 700, 64              16 / 23     16 / 24
 //   64 x 64, 64              53 / 36     87 / 37
-// and of units of 16 rows / wide: 512 x 60, 8 tokens 99 / 99 and 118 / 144; 512 x 300 217 / 144 and 212 / 217.
+// and of units of 16 rows / wide, 8 tokens (32 rows), contexts of
+//                           60            128           256           512
+//   block-scaled, 32      17 / 17       20 / 17       23 / 21       29 / 26
+//                 64      22 / 26       27 / 27       36 / 32       48 / 46
+//                 256     60 / 76       73 / 84       98 / 101     145 / 136
+//                 1024   227 / 305     278 / 318     370 / 388     558 / 443
+//   bf16,         64      21 / 22       26 / 22       32 / 27       49 / 34
+//                 1024   190 / 195     230 / 202     355 / 253     690 / 362
+// (12 tokens, 48 rows, block-scaled: 64 x 60 30 / 26, 1024 x 60 337 / 331; 5 tokens, 20 rows: 110 / 141 for 512 x 60).
 Route route_of(long long rows, float scale, bool f8, int num_seqs, int n_kv_heads, int group, int ctx) {
     const double heads = (double)num_seqs * n_kv_heads;
     if (rows <= kRows || !(scale > 0.f) || in_small_tiles(f8, rows, heads, ctx)) return kUnits16;
-    if (f8 && rows <= 32 && ctx <= 256 && heads >= 1024) return kUnits16;
+    const double sm = std::max(1, sms());
+    if (f8 && rows <= 32 && ctx <= kWideStep && heads >= 3 * sm) return kUnits16;
     if (rows < kPromptRows) return kWide;
     const double units = heads * (double)((rows + (f8 ? 63 : 127)) / (f8 ? 64 : 128)), tiles = (ctx + 127) / 128;
-    const double wide = 5 + units * tiles * (f8 ? 1.25 : 1.55) / 152 + ceil(units / 152) * (f8 ? 4.5 : 5) + (units > 152 ? 4 : 0);
+    const double wide = 5 + units * tiles * (f8 ? 1.25 : 1.55) / sm + ceil(units / sm) * (f8 ? 4.5 : 5) + (units > sm ? 4 : 0);
     const double items = heads * (double)((rows + 255) / 256), seen = (ctx - 0.5 * (double)(rows / group)) / 128 + 0.5;
-    const double waves = items <= 152 ? 1 : 0.15 * items / 152 + 0.85 * ceil(items / 152);
+    const double waves = items <= sm ? 1 : 0.15 * items / sm + 0.85 * ceil(items / sm);
     const double prompt = 8 + waves * (1.9 * seen + 5.5) + heads * ctx * (f8 ? 0.9e-4 : 0.6e-4);
     return wide <= prompt ? kWide : kPrompt;
 }

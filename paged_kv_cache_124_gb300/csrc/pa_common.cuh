@@ -112,6 +112,18 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool supported_block_size(int b) { return b == 8 || b == 16 || b == 32; }
 inline bool supported_d_head(int d) { return d == 64 || d == 128; }
 
+// SMs of the current device; 0 where there is none.
+inline int sm_count() {
+    static int cached[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && cached[dev]) return cached[dev];
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) cached[dev] = n;
+    return n;
+}
+
 // Opt a kernel into more than 48 KiB of dynamic shared memory, once per
 // device and kernel.
 template <typename K>

@@ -672,16 +672,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarpsPerSm / kWarps)
 // host side
 // ---------------------------------------------------------------------------
 
-inline int sms() {
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev < 64 && cached[dev]) return cached[dev];
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev < 64) cached[dev] = n;
-    return n;
-}
+inline int sms() { return pa_host::sm_count(); }
 
 // Rows of a unit: on the wide kernel 64, and 128 for bf16 where a KV head has more.
 inline int unit_rows(long long rows, bool f8, bool wide) { return !wide ? kRows : f8 || rows <= 64 ? 64 : 128; }

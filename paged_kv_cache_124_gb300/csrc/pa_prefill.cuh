@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <climits>
 #include <type_traits>
 #include <mutex>
@@ -1404,16 +1405,7 @@ inline bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_
 template <int D, bool kF8, class Args>
 int g_smem_done[64];   // per kernel instantiation: bytes opted in, by device
 
-inline int num_sms() {
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    if (dev < 64 && cached[dev]) return cached[dev];
-    int n = 1;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 1;
-    if (dev < 64) cached[dev] = n;
-    return n;
-}
+inline int num_sms() { return std::max(1, pa_host::sm_count()); }
 
 // The tensor maps of a call: q from the caller; K from the caller's cache
 // (bf16) or from the staging (k_stage); V from the staging (the maps only move

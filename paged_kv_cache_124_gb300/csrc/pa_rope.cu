@@ -28,6 +28,8 @@
 // tokens of 32 + 2 x 4 heads of 128 take 21.6 us, 0.72 of the measured copy
 // rate for 105 MB; 6 tokens 2.3 us.
 
+#include <algorithm>
+
 #include "pa_rope.cuh"
 
 namespace {
@@ -225,12 +227,6 @@ __global__ void __launch_bounds__(kRopeThreads, 2) tokens_kernel(const RopeArgs 
     }
 }
 
-// Which kernel: the one per token is faster from about 12 million elements
-// on (32 + 2 x 8 heads of 128: 1000 tokens 10.0 against 6.5 us, 2000 13.1 /
-// 13.6, 4000 18.3 / 24.2, 32,048 122.9 / 168; E4M3 1000 13.9 / 7.0, 2000 16.8 /
-// 14.6, 4000 21.8 / 25.7, 32,048 144 / 180; 16 + 2 x 2 of 64: 5000 tokens 7.6 /
-// 5.7, 10,000 12.5 / 12.9, 40,000 36.2 / 42.5), if a token has heads enough to
-// share its angles (2 + 2 x 1: 40,000 tokens 38.5 / 21.9).
 template <int D, bool F8, bool kInterleaved, bool kAxes, int kSide>
 cudaError_t launch_tokens(const RopeArgs& a, cudaStream_t st) {
     const int per = kRopeThreads / (D / 16 * kSide);
@@ -238,6 +234,13 @@ cudaError_t launch_tokens(const RopeArgs& a, cudaStream_t st) {
                                      dim3((unsigned)(((long long)a.num_tokens + per - 1) / per)), dim3(kRopeThreads), 0, st, a);
 }
 
+// Which kernel: the one per token is faster from about 12 million elements
+// on (32 + 2 x 8 heads of 128: 1000 tokens 10.0 against 6.5 us, 2000 13.1 /
+// 13.6, 4000 18.3 / 24.2, 32,048 122.9 / 168; E4M3 1000 13.9 / 7.0, 2000 16.8 /
+// 14.6, 4000 21.8 / 25.7, 32,048 144 / 180; 16 + 2 x 2 of 64: 5000 tokens 7.6 /
+// 5.7, 10,000 12.5 / 12.9, 40,000 36.2 / 42.5), if a token has heads enough to
+// share its angles (2 + 2 x 1: 40,000 tokens 38.5 / 21.9).
+//
 // Several axes: the kernel per token with four heads side by side, in blocks
 // of half the time, where its waves of resident blocks (two an SM) are at most
 // 1.5 times those of two heads.  32 + 2 x 4 heads of 128, us by head / four /
@@ -250,7 +253,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
     const int heads = a.n_q_heads + 2 * a.n_kv_heads;
     const long long rows = (long long)a.num_tokens * heads;
     if constexpr (kAxes) {
-        const long long resident = 2 * 152, four = kRopeThreads / (4 * kLanes), two = kRopeThreads / (2 * kLanes);
+        const long long resident = 2LL * std::max(1, pa_host::sm_count()), four = kRopeThreads / (4 * kLanes), two = kRopeThreads / (2 * kLanes);
         const auto waves = [&](long long tokens) { return (a.num_tokens + tokens * resident - 1) / (tokens * resident); };
         if (heads >= 16 && rows * D >= 3000000 && 2 * waves(four) <= 3 * waves(two))
             return launch_tokens<D, F8, kInterleaved, kAxes, 4>(a, st);
