@@ -132,10 +132,11 @@ class Call {
         n = static_cast<int>(size);
     }
 
-  private:
     [[noreturn]] void refuse(PyObject* type, const char* name, const std::string& why) const {
         throw Refused{type, std::string(where_) + ": " + name + " " + why};
     }
+
+  private:
     const at::Tensor& placed(int i, const char* name, at::ScalarType dtype, const std::initializer_list<int64_t>* shape) const {
         const at::Tensor& t = tensor(i, name);
         if (t.scalar_type() != dtype)
@@ -330,15 +331,16 @@ struct Axes {
         positions = c.at_(at, "positions", at::kInt, {num, T});
         int pairs;
         c.small_ints(axes_at, "axes", of_pair, pairs);
-        if (2 * pairs != rot) throw Refused{PyExc_ValueError, "axes must have one entry for each pair that cos_sin turns"};
-        if (num == 0) throw Refused{PyExc_ValueError, "positions must have an axis"};
+        if (2 * pairs != rot) c.refuse(PyExc_ValueError, "axes", "must have one entry for each pair that cos_sin turns");
+        if (num == 0) c.refuse(PyExc_ValueError, "positions", "must have an axis");
     }
 };
 
 // (q_out, k_cache, v_cache, q, k, v, positions, axes, slot_mapping, cos_sin, q_weight, k_weight, eps, interleaved, status,
 //  k_scale, v_scale, k_scales, v_scales, device, stream)
 PyObject* qk_norm_mrope_cache(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    return guarded("pa_qk_norm_mrope_cache", args, n, 21, [](const Call& c) {
+    const bool to_scaled = n == 21 && args[17] != Py_None;
+    return guarded(to_scaled ? "pa_qk_norm_rope_cache_scaled" : "pa_qk_norm_mrope_cache", args, n, 21, [](const Call& c) {
         const at::Tensor& queries = c.tensor(3, "q", 3);
         const at::Tensor& cache = c.tensor(1, "k_cache", 4);
         const int64_t T = queries.size(0), Hq = queries.size(1), D = queries.size(2);

@@ -194,6 +194,19 @@ def test_binding_refuses_tensors_before_any_call(monkeypatch):
                                         z(1, dt=torch.int64), stream=0)
 
 
+def test_refusals_name_the_call_that_was_made(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    z = lambda *s, dt=torch.uint8: torch.zeros(s, dtype=dt)  # noqa: E731
+    b = lambda *s: z(*s, dt=torch.bfloat16)  # noqa: E731
+    rope = (b(1, 4, 64), b(1, 2, 64), b(1, 2, 64), z(2, 1, dt=torch.int32))
+    with pytest.raises(ValueError, match="^pa_qk_norm_rope_cache_scaled: "):
+        api.pa_qk_norm_rope_cache_scaled(b(1, 4, 64), z(2, 2, 16, 64), z(2, 2, 16, 64), z(2, 2), z(2, 2), *rope,
+                                         z(1, dt=torch.int64), z(9, 64, dt=torch.float32), axes=[0] * 32, stream=0)
+    with pytest.raises(ValueError, match="^pa_qk_norm_mrope_cache: "):
+        api.pa_qk_norm_mrope_cache(b(1, 4, 64), b(2, 2, 16, 64), b(2, 2, 16, 64), *rope, [0] * 32, z(1, dt=torch.int64),
+                                   z(9, 64, dt=torch.float32), stream=0)
+
+
 class _Handle:
     def __init__(self, cuda_stream):
         self.cuda_stream = cuda_stream
