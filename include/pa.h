@@ -779,8 +779,10 @@ int pa_qk_norm_mrope_cache_fp8(void* q_out, void* k_cache, void* v_cache,
  * that the call takes up twice, the scale is that of one of the two, and codes
  * may be of the other).
  *   k_scales, v_scales  device uint8 [num_blocks][n_kv_heads]; those of blocks
- *                 not begun yet are not read.  A block's copy takes its two
- *                 rows of them along. */
+ *                 not begun yet are not read.
+ * pa_copy_blocks_fp8 and pa_swap_blocks_fp8 move a block's codes; whoever
+ * copies or swaps it moves its row of k_scales and of v_scales with them, on
+ * the same stream.  (d_head 64 or 128; pa_attend_scaled reads 128.) */
 int pa_qk_norm_rope_cache_scaled(void* q_out, void* k_cache, void* v_cache,
                                  uint8_t* k_scales, uint8_t* v_scales,
                                  const void* q, const void* k, const void* v,

@@ -300,3 +300,41 @@ def test_slopes_of_any_size(scaled, S, new, slope):
         for r, s, pos, lo, hi in _few(12)(list(_rows(p))):
             want = _want(p, r, s, pos, hi - 1, hi)[0]
             assert (np.abs(out_to_f64(out[r]) - want) <= 2.0 ** -10 * np.abs(want)).all()
+
+
+def test_a_forked_and_swapped_block_scaled_cache():
+    """A partly filled tail block copied for a second writer, its rows of scales beside its codes, and swapped out and in."""
+    Hq, Hkv, D, B, n, NB = 8, 2, 128, 16, 37, 12
+    g = torch.Generator(device="cuda").manual_seed(2)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    kc, vc = (torch.full((NB, Hkv, B, D), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((NB, Hkv), 255, dtype=torch.uint8, device="cuda") for _ in range(2))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, at = i32(7, 2, 9), torch.arange(n, device="cuda")
+    api.pa_reshape_and_cache_scaled(kc, vc, ks, vs, draw(n, Hkv, D), draw(n, Hkv, D), table.long()[at // B] * B + at % B)
+    api.pa_copy_blocks([kc], [vc], i32(9, 4).view(1, 2))           # the tail, for the second sample
+    ks[4], vs[4] = ks[9], vs[9]
+    both = torch.stack([table, i32(7, 2, 4)])
+    x = draw(2, Hkv, D) * torch.tensor([1.0, 32.0], device="cuda").view(2, 1, 1)   # (the second's grows its block's scale)
+    api.pa_reshape_and_cache_scaled(kc, vc, ks, vs, x.bfloat16(), x.bfloat16(), both[:, n // B].long() * B + n % B)
+
+    def check(tables):
+        p = Problem(1, Hq, Hkv, D, B, [n + 1] * 2, [1, 1], scaled=True)
+        p.kc, p.vc, p.ks, p.vs, p.tables, p.q = (*(t.cpu().numpy() for t in (kc, vc, ks, vs, tables)), q)
+        out = p.run()
+        _check(p, out)
+        return out
+
+    q = torch.randn(2, Hq, D, generator=torch.Generator().manual_seed(3)).bfloat16()
+    first = check(both)
+    assert (ks[4] > ks[9]).all() and (vs[4] > vs[9]).all()
+    out_k, out_v = (torch.empty(3, Hkv, B, D, dtype=torch.uint8).pin_memory() for _ in range(2))
+    there, back = [[7, 0], [2, 1], [4, 2]], [[0, 1], [1, 3], [2, 5]]
+    pairs = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    api.pa_swap_blocks([out_k], [out_v], [kc], [vc], pairs(there))
+    held = [s[[7, 2, 4]].cpu() for s in (ks, vs)]
+    kc[[2, 4]], vc[[2, 4]], ks[[2, 4]], vs[[2, 4]] = 0x7F, 0x7F, 255, 255
+    api.pa_swap_blocks([kc], [vc], [out_k], [out_v], pairs(back))
+    ks[[1, 3, 5]], vs[[1, 3, 5]] = (h.cuda() for h in held)
+    both[1], both[0, 1] = i32(1, 3, 5), 3
+    assert torch.equal(check(both), first)
