@@ -241,7 +241,8 @@ __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs
                                       : fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float m = fmaxf(st.m[h], kShaped && F8 ? top : top * f[0][h]);
+            float m = fmaxf(st.m[h], kShaped && F8 ? top : top * f[0][h]);
+            if (kShaped && !(m > st.m[h] + kRaise)) m = st.m[h];   // (a row's own scores alone raise its maximum)
             const float less = pa::exp2_approx(st.m[h] - m);
             st.m[h] = m;
             st.l[h] *= less;

@@ -338,3 +338,23 @@ def test_a_forked_and_swapped_block_scaled_cache():
     ks[[1, 3, 5]], vs[[1, 3, 5]] = (h.cuda() for h in held)
     both[1], both[0, 1] = i32(1, 3, 5), 3
     assert torch.equal(check(both), first)
+
+
+@pytest.mark.parametrize("scaled", [False, True], ids=["bf16", "scaled"])
+@pytest.mark.parametrize("S,new", [(1, 2), (1, 4), (1, 7), (1, 40), (24, 131)])
+def test_keys_that_others_see_change_no_bit(scaled, S, new):
+    """The even tokens' scores rise far above all before, at positions that the odd ones do not see."""
+    p = Problem(14, 4, 1, 128, 16, [900] * S, [new] * S, "window", scaled=scaled)
+    p.visible[:] = [0, 758]
+    p.visible[::2] = [0, 900]
+    if scaled:                                                     # (and theirs a little, in the tile of both)
+        p.ks[p.tables[:, 752 // 16]] += 1
+    else:
+        p.kc[p.tables[:, 752 // 16], :, :6] += 0x80                # twice the values
+    clean = p.run()
+    for s in range(S):
+        for j in range(758, 900, 7):
+            p.kc[p.tables[s][j // 16], :, j % 16] = 0x7E if scaled else 0x4280      # 448, 2^6
+    out = p.run()
+    assert torch.equal(out[1::2], clean[1::2]) and not torch.equal(out[::2], clean[::2])
+    _check(p, out, take=_few(12))
