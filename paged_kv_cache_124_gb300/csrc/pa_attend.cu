@@ -12,11 +12,12 @@
 // window costs its own bytes.
 //
 // What the shape costs beside the plain kernels: with few rows, arithmetic
-// that the cache's bytes hide (64 decodes of 4096 positions, capped, 169 us,
-// 0.94 of the measured copy rate; block-scaled 98, 0.81, against 92 with one
-// scale: a score and a weight take a factor more).  With many, the softmax's
-// instructions bind: 8 prompts of 2003 tokens 273 us causal (275 plain), 341
-// with a bias, 353 with a cap.
+// that the cache's bytes hide (64 decodes of 4096 positions, capped, 170 us,
+// 0.93 of the measured copy rate; block-scaled 100, 0.80, and 113 with blocks
+// of 8, against 92 with one scale: a score and a weight take a factor more).
+// With many, the softmax of a tile is the longer: 8 prompts of 2003 tokens 273
+// us causal (272 plain), 346 with a bias, 358 with a cap beside which scores
+// are small, 433 and 612 where they are not (pa_attend_prompt.cu).
 
 #include "pa_attend.cuh"
 #include "pa_cap.cuh"

@@ -4,20 +4,29 @@
 // What the shape changes: an item's tiles run from the first position that
 // one of its rows sees to the last, rather than from 0 to its own; scores are
 // capped and biased in registers before the softmax; rows mask by an interval.
-// The staging leaves out values that are not finite, since the weights of
-// rows that do not see them are zeros and 0 * inf is not; the rows that see
-// them add them when they are written.  From a block-scaled cache it makes
+// The staging leaves out blocks that no token sees, and values that are not
+// finite, since the weights of rows that do not see them are zeros and 0 * inf
+// is not; the rows that see them add them when they are written.  From a block-scaled cache it makes
 // bf16 keys and fp16 values that hold every element exactly (a tile whose
 // blocks' scales are outside fp16's range keeps bf16 values, as pa_prefill's
 // do).
 //
-// 8 prompts of 2,003 tokens with spans and a cap: 384 us, 738 TFLOP/s of what
-// is seen; without the cap 295 us, 961.  The softmax's instructions bound it
-// (a cap adds two packed products and a comparison to a pair's eight
-// instructions), not the products: when it took 415, sixteen softmax warps
-// took 466, four for each row tile by itself 489 and eight for each 474.  8
-// chunks of 512 tokens over block-scaled prefixes of 2,048 to 8,192: 353 us,
-// 924 TFLOP/s, of which the staging is some 30 us.
+// 8 prompts of 2,003 tokens with spans: 296 us, 957 TFLOP/s of what is seen.
+// With a cap: 393 us, 721 TFLOP/s, where all scores of a warp's half tile are
+// within a quarter of it (scores of deviation 2 under a cap of 50: the cap is
+// taken with the weights); 463 where they are within half of it (deviation 4:
+// a longer polynomial before the maximum), 667 where they go beyond (deviation
+// 10: two special functions a score).  Nothing is full (issue 41 %, ALU 25 %,
+// tensor 34 %): both halves of a row tile wait for each other's maximum at
+// every tile before they write a weight, with two warps a scheduler, and the
+// code is long for the instruction cache (0.8 of a stall in each issue).  When
+// it took 415, sixteen softmax warps took 466, four for each row tile by itself
+// 489 and eight for each 474.  Keeping what is not seen out of the cap's form
+// costs 2 % (in one loop with the mask behind it 10 %, only where scores are
+// large, which is more code, 4 %).  8 chunks of 512 tokens over block-scaled
+// prefixes of 2,048 to 8,192: 353 us, 925 TFLOP/s, of which the staging is some
+// 30 us.  Tiles of small values (stage_shaped_v_kernel) take two-term weights:
+// 8 causal prompts all of whose values are below 2^-10 401 us against 273.
 
 #include "pa_attend.cuh"
 #include "pa_prefill.cuh"

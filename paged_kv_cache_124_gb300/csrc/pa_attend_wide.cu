@@ -5,12 +5,17 @@
 // are capped, biased and masked before the maximum.  Block-scaled caches: a
 // tile's 64 positions of a group have 2 to 8 blocks, whose scales its warps
 // fetch themselves, a tile ahead (their table entries two), a lane each; K's
-// multiply the scores, V's the weights, relative to the largest so far.
+// multiply the scores, V's the weights, relative to the largest that the row
+// has seen so far.
 //
 // 8 sequences of 32,000 positions and more, 8 new tokens of 32 query heads
-// over 8 (32 rows), block-scaled: 121 us, 0.65 of the measured copy rate for
-// 532 MB (issue 51 %, ALU 42 %: a tile's chain of scores, softmax
-// and the four terms of a weight bounds it, as with one scale).
+// over 8 (32 rows), block-scaled: 123 us, 0.64 of the measured copy rate for
+// 532 MB (issue 52 %, ALU 41 %: a tile's chain of scores, softmax
+// and the four terms of a weight bounds it, as with one scale); capped 158 us,
+// and 183 where scores go beyond half of the cap.  bf16, 8 of 8,192 positions,
+// 64 new tokens: 104 us for 268 MB (40 us): a unit has 128 of a KV head's 256
+// rows, so the cache is read twice, and the softmax of 256 rows a position is
+// what there is to do (capped 118).
 
 #include "pa_wide.cuh"
 

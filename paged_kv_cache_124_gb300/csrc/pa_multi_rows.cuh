@@ -9,9 +9,11 @@
 // passed on by shuffles; K's multiply the scores, V's the weights, relative to
 // the largest that the row has seen so far, so that a weight fits f16.  64 decodes of 512 to 4,096
 // positions, 32 query heads over 8 of 128: capped over bf16 99 us, 0.90 of the
-// measured copy rate, block-scaled 63 us, 0.71 (there the instructions issued
-// bound it); 96 through windows of 1,024 of 100 to 8,000 positions 37 us, 0.76
-// (a short call: starting, the first tiles and the joins are a part of it).
+// measured copy rate, block-scaled 64 us, 0.70 (nothing is full there, issue 44
+// %, ALU 42 %, DRAM 58 %: with twelve warps an SM a tile's chain of codes to
+// f16, scores, softmax and products is what they wait for); 96 through windows
+// of 1,024 of 100 to 8,000 positions 38 us, 0.75 (a short call: starting, the
+// first tiles and the joins are a part of it).
 #pragma once
 
 #include <math.h>
@@ -116,9 +118,9 @@ struct State {
 // of rows g + 8 h.  scales (shaped, E4M3): the scale bytes of K and V of the
 // tile's first 8 positions, then of the others.
 // kEight: no unit has more than 8 rows, so rows 8 .. 15 of the matrix instructions stay empty and
-// their softmax is left out.  Only block-scaled caches have this form, whose decodes the instructions
-// issued bound (64 decodes over mixed lengths 68.2 -> 63.1 us, 64 x 4096 105.7 -> 97.7); of bf16
-// caches the reads bound them.
+// their softmax is left out.  Only block-scaled caches have this form, whose tiles' chains are the
+// longest (64 decodes over mixed lengths 68.2 -> 63.1 us, 64 x 4096 105.7 -> 97.7 when it came); of
+// bf16 caches the reads bound them.
 template <int D, bool F8, class Args, bool kEight>
 __device__ __forceinline__ void fold_tile(State<D>& st, uint32_t ks, uint32_t vs, const float (&c)[2], int t0, const Args& a,
                                           const typename Args::Unit& u, int lane, const uint32_t (&qr)[D / 16][4],
