@@ -536,10 +536,11 @@ int pa_attend(void* out, int out_dtype, const void* q, const void* k_cache,
  *   code * 2^(k_scales[block][h] - 127)            (v_scales for values)
  * as pa_qk_norm_rope_cache_scaled and pa_reshape_and_cache_scaled write them
  * (bytes 0 .. 254; 255 is no scale).  Elements below 2^-126, and those of a
- * block whose byte is 0, all below 2^-118, may be taken for zeros.  q and a weight are taken as by pa_decode_multi_fp8 (a weight within
- * 2^-11, or 2^-28 of the row's largest), the weight times its value scale over
- * the largest value scale that its row sees: scales of other positions cost a
- * row nothing.  d_head 128.
+ * block whose byte is 0, all below 2^-118, may be taken for zeros.  q and a
+ * weight are taken as by pa_decode_multi_fp8 (a weight within 2^-11, or 2^-28 of
+ * the row's largest), the weight times its value scale over the largest value
+ * scale that its row sees: scales of other positions cost a row nothing.
+ * d_head 128.
  *   k_scales, v_scales  device uint8 [num_blocks][n_kv_heads]. */
 int pa_attend_scaled(void* out, int out_dtype, const void* q,
                      const void* k_cache, const void* v_cache,
